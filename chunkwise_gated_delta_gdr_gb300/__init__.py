@@ -10,6 +10,12 @@ Main entry points (same names as the C ABI):
   chunk_fwd(q, k, v, g, beta, initial_state=None, ...) -> (o, final_state)
   chunk_fwd_host(...)      the same on host (pinned) tensors, copies inside
   chunk_fwd_workspace_size(...), chunk_fwd_path(...), stream_status(...)
+
+The other layers of a decoder (``layers.py``):
+  linear_scan_fwd, linear_scan_bwd, linear_scan_checkpoints   gated linear recurrence
+  qk_norm_rope, qk_norm_rope_bwd    RMS norm of q and k heads with the position rotation
+  qk_norm_rope_append               the same for serving, into a paged key-value cache
+  paged_decode_attn, paged_decode_attn_workspace_size   one new token against that cache
 """
 from __future__ import annotations
 
@@ -35,6 +41,15 @@ EXPORTED = (
     "gdr_ssd_chunk_fwd", "gdr_ssd_chunk_fwd_workspace_size", "gdr_chunk_fwd_segmented",
     "gdr_chunk_fwd_segmented_workspace_size", "gdr_noalloc_stream_status",
     "gdr_set_flag_wait_limit",
+    "gdr_linear_scan_fwd", "gdr_linear_scan_bwd", "gdr_linear_scan_checkpoints_size",
+    "gdr_qk_norm_rope", "gdr_qk_norm_rope_bwd", "gdr_qk_norm_rope_bwd_workspace_size",
+    "gdr_qk_norm_rope_append", "gdr_paged_decode_attn", "gdr_paged_decode_attn_workspace_size",
+)
+# Entry points of layers.py, reached as attributes of the package.
+LAYERS = (
+    "linear_scan_fwd", "linear_scan_bwd", "linear_scan_checkpoints", "qk_norm_rope",
+    "qk_norm_rope_bwd", "qk_norm_rope_append", "paged_decode_attn",
+    "paged_decode_attn_workspace_size",
 )
 # Size of the library-owned scratch used by gdr_chunk_fwd_noalloc (per device).
 GDR_NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024
@@ -393,3 +408,13 @@ def noalloc_stream_status(stream=None) -> int:
 def stream_status(stream=None, workspace=None) -> int:
     """Synchronise the stream and return its gdr_status (see gdr.h)."""
     return int(load_library().gdr_stream_status(_stream_handle(stream), _ptr(workspace)))
+
+
+def __getattr__(name):
+    """The entry points of layers.py, imported (with torch) at their first use."""
+    if name in LAYERS:
+        from . import layers
+        for n in LAYERS:
+            globals()[n] = getattr(layers, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -1,0 +1,133 @@
+// gdr_ops.cuh -- what the scan, norm-and-rotation and paged attention kernels share:
+// typed loads and stores of a few consecutive elements, and host-side checks.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <math.h>
+#include <string.h>
+#include <stdint.h>
+
+#include "gdr_internal.cuh"
+
+namespace gdr {
+namespace ops {
+
+typedef __nv_bfloat16 bf16;
+
+// ------------------------------------------------------------------ device
+// V consecutive elements as raw bits, the widest aligned access the count allows.
+template <typename T, int V>
+struct Raw {
+  T v[V];
+};
+template <>
+struct Raw<float, 2> {
+  float2 v;
+};
+template <>
+struct Raw<float, 4> {
+  float4 v;
+};
+template <>
+struct Raw<bf16, 2> {
+  uint32_t v;
+};
+template <>
+struct Raw<bf16, 4> {
+  uint2 v;
+};
+
+template <typename T, int V>
+__device__ __forceinline__ Raw<T, V> load_raw(const T* p) {
+  Raw<T, V> r;
+  if constexpr (V == 1)
+    r.v[0] = *p;
+  else
+    r.v = *reinterpret_cast<const decltype(r.v)*>(p);
+  return r;
+}
+template <typename T, int V>
+__device__ __forceinline__ Raw<T, V> zero_raw() {
+  Raw<T, V> r;
+  memset(&r, 0, sizeof r);
+  return r;
+}
+
+__device__ __forceinline__ float2 unpack2(uint32_t b) {
+  return make_float2(__uint_as_float(b << 16), __uint_as_float(b & 0xffff0000u));
+}
+__device__ __forceinline__ uint32_t pack2(float x, float y) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void to_float(const Raw<T, V>& r, float* f) {
+  if constexpr (V == 1) {
+    f[0] = static_cast<float>(r.v[0]);
+  } else if constexpr (sizeof(T) == 2) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&r.v);
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      const float2 p = unpack2(w[i]);
+      f[2 * i] = p.x;
+      f[2 * i + 1] = p.y;
+    }
+  } else {
+    const float* w = reinterpret_cast<const float*>(&r.v);
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = w[i];
+  }
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void load_f(const T* p, float* f) {
+  to_float<T, V>(load_raw<T, V>(p), f);
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void store_f(T* p, const float* f) {
+  if constexpr (V == 1) {
+    if constexpr (sizeof(T) == 2)
+      *p = __float2bfloat16_rn(f[0]);
+    else
+      *p = f[0];
+  } else {
+    Raw<T, V> r;
+    if constexpr (sizeof(T) == 2) {
+      uint32_t* w = reinterpret_cast<uint32_t*>(&r.v);
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) w[i] = pack2(f[2 * i], f[2 * i + 1]);
+    } else {
+      float* w = reinterpret_cast<float*>(&r.v);
+#pragma unroll
+      for (int i = 0; i < V; ++i) w[i] = f[i];
+    }
+    *reinterpret_cast<decltype(r.v)*>(p) = r.v;
+  }
+}
+
+// ------------------------------------------------------------------ host
+inline bool is_aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+inline bool is_dtype(int d) { return d == GDR_F32 || d == GDR_BF16; }
+inline size_t dtype_size(int d) { return d == GDR_BF16 ? 2 : 4; }
+inline gdr_status launched() { return cudaGetLastError() == cudaSuccess ? GDR_OK : GDR_ERR_CUDA; }
+
+// Calls f with a null pointer of the element type that `dtype` names.
+template <typename F>
+auto with_dtype(int dtype, F f) {
+  return dtype == GDR_BF16 ? f(static_cast<bf16*>(nullptr)) : f(static_cast<float*>(nullptr));
+}
+
+// The sizes of a paged cache. Zero pages or table columns are an empty cache.
+inline gdr_status check_cache(const gdr_paged_cache* c) {
+  if (!c) return GDR_ERR_INVALID_ARG;
+  if (c->num_pages < 0 || c->page_size <= 0 || c->HK <= 0 || c->D <= 0 || c->max_pages < 0 ||
+      !is_dtype(c->dtype) || c->page_stride < 0 || c->token_stride < 0 || c->head_stride < 0)
+    return GDR_ERR_INVALID_ARG;
+  if (c->D > 256 || c->HK > (1 << 20)) return GDR_ERR_UNSUPPORTED;
+  return GDR_OK;
+}
+
+}  // namespace ops
+}  // namespace gdr

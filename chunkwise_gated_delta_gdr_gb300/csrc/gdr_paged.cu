@@ -1,0 +1,445 @@
+// gdr_paged.cu -- attention of one new token per sequence over a paged key-value cache.
+//
+//   o = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q . k_j - m),  lse = m + log sum_j p_j
+//
+// over the keys lo <= j < len, lo = max(0, len - window). The running maximum m and the
+// sums are kept per stretch of keys; two stretches join as
+//   m = max(m1, m2),  l = l1 e^{m1 - m} + l2 e^{m2 - m},  o likewise.
+// All of it runs in base 2: scores carry a factor log2(e).
+//
+// Partition. An item is one (sequence, key-value head, group of query heads); its keys are
+// cut into tiles of TILE keys. All tiles of the call, item after item, form one line that
+// the blocks share out equally, whatever the lengths are: block c takes the tiles
+// [c per, (c + 1) per), per = ceil(total / blocks). The lengths are read on the device, so
+// the host needs none of them. A block that holds a whole item writes its result; an item
+// cut by a block boundary leaves partial results, at most two per block (slot 0: the item
+// began in an earlier block, slot 1: it began here), which paged_join_kernel joins in order.
+#include <type_traits>
+
+#include "gdr_ops.cuh"
+
+namespace gdr {
+namespace ops {
+namespace {
+
+constexpr int TILE = 64;          // keys per tile
+constexpr int WARPS = 4;          // per block
+constexpr int GMAX = 16;          // query heads of an item at most
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+
+struct AttnArgs {
+  const void *q, *kc, *vc;
+  const int32_t *table, *lens;
+  void* out;
+  float* lse;                     // may be null
+  float *part_o, *part_ml;        // [blocks][2][GMAX][D], [blocks][2][GMAX][2]
+  int B, HQ, HK, D, G, GH, groups;  // G = HQ / HK; GH query heads per item, groups per kv head
+  int page, num_pages, max_pages, window, whole, blocks, out_bf16, q_bf16;
+  float scale2;                   // scale log2(e)
+  int64_t qb, qh, pp, pt, ph;
+  long long cap;                  // max_pages * page
+};
+
+// Keys of sequence b: [lo, n), and whether its length is valid.
+struct Span {
+  int lo, n;
+  bool ok;
+  __device__ int tiles() const { return (n - lo + TILE - 1) / TILE; }
+};
+__device__ __forceinline__ Span span_of(const AttnArgs& a, int b) {
+  const int n = a.lens[b];
+  Span s;
+  s.ok = n >= 0 && n <= a.cap;
+  s.n = s.ok ? n : 0;
+  s.lo = a.window > 0 && s.n > a.window ? s.n - a.window : 0;
+  return s;
+}
+
+// A place on the line of tiles.
+struct Place {
+  int b, item, tile;   // sequence, (kv head, group), tile of it
+  Span s;
+};
+
+// All lanes of a warp: tiles of the whole call.
+__device__ __forceinline__ long long total_tiles(const AttnArgs& a, int lane) {
+  long long t = 0;
+  for (int b = lane; b < a.B; b += 32) t += span_of(a, b).tiles();
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(~0u, t, o);
+  return t * a.HK * a.groups;
+}
+
+// All lanes of a warp: the place of tile w < total of the line.
+__device__ __forceinline__ Place locate(const AttnArgs& a, long long w, int lane) {
+  const int per_b = a.HK * a.groups;
+  long long base = 0;
+  for (int b0 = 0;; b0 += 32) {
+    const long long t = b0 + lane < a.B ? (long long)span_of(a, b0 + lane).tiles() * per_b : 0;
+    long long inc = t;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long u = __shfl_up_sync(~0u, inc, o);
+      if (lane >= o) inc += u;
+    }
+    const unsigned hit = __ballot_sync(~0u, base + inc > w);
+    if (hit || b0 + 32 >= a.B) {
+      const int src = hit ? __ffs(hit) - 1 : 0;
+      const long long first = __shfl_sync(~0u, base + inc - t, src);
+      Place p;
+      p.b = min(b0 + src, a.B - 1);
+      p.s = span_of(a, p.b);
+      const int tiles = max(1, p.s.tiles());
+      p.item = (int)((w - first) / tiles);
+      p.tile = (int)((w - first) - (long long)p.item * tiles);
+      return p;
+    }
+    base += __shfl_sync(~0u, inc, 31);
+  }
+}
+
+// The first item after p that has tiles (there has to be one).
+__device__ __forceinline__ void next_item(const AttnArgs& a, Place& p) {
+  p.tile = 0;
+  if (++p.item < a.HK * a.groups) return;
+  p.item = 0;
+  do {
+    p.s = span_of(a, ++p.b);
+  } while (p.s.tiles() == 0 && p.b + 1 < a.B);
+}
+
+__device__ __forceinline__ void put(void* out, size_t i, float v, int is_bf16) {
+  if (is_bf16)
+    static_cast<bf16*>(out)[i] = __float2bfloat16_rn(v);
+  else
+    static_cast<float*>(out)[i] = v;
+}
+
+// Result of head `hq` of sequence b, channel d, from the sums (m in base 2).
+__device__ __forceinline__ void finish(const AttnArgs& a, int b, int hq, int d, float m, float l,
+                                       float o) {
+  const size_t row = (size_t)b * a.HQ + hq;
+  put(a.out, row * a.D + d, l == 0.f ? 0.f : o / l, a.out_bf16);
+  if (d == 0 && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
+}
+
+// Sequences without tiles: zeros and -inf (no keys), NaN (an invalid length).
+__device__ __forceinline__ void empty_rows(const AttnArgs& a) {
+  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+    const Span s = span_of(a, b);
+    if (s.tiles()) continue;
+    const float o = s.ok ? 0.f : NAN;
+    for (int i = threadIdx.x; i < a.HQ * a.D; i += blockDim.x)
+      put(a.out, (size_t)b * a.HQ * a.D + i, o, a.out_bf16);
+    if (a.lse)
+      for (int i = threadIdx.x; i < a.HQ; i += blockDim.x)
+        a.lse[(size_t)b * a.HQ + i] = s.ok ? -INFINITY : NAN;
+  }
+}
+
+// This block's stretch of the line: its first place and its number of tiles (0: none).
+__device__ __forceinline__ long long stretch(const AttnArgs& a, int lane, Place* p) {
+  if (a.whole) {                   // one block per item
+    p->b = blockIdx.x / (a.HK * a.groups);
+    p->item = blockIdx.x - p->b * (a.HK * a.groups);
+    p->tile = 0;
+    p->s = span_of(a, p->b);
+    return p->s.tiles();
+  }
+  const long long total = total_tiles(a, lane), per = (total + a.blocks - 1) / a.blocks;
+  const long long first = blockIdx.x * per, last = min(total, first + per);
+  if (first >= last) return 0;
+  *p = locate(a, first, lane);
+  return last - first;
+}
+
+// Element offset of key j of sequence b (kv head 0), or -1 for a bad table entry.
+__device__ __forceinline__ int64_t key_row(const AttnArgs& a, int b, int j) {
+  const int pj = j / a.page;
+  const int32_t pg = a.table[(size_t)b * a.max_pages + pj];
+  if (pg < 0 || pg >= a.num_pages) return -1;
+  return pg * a.pp + (j - pj * a.page) * a.pt;
+}
+
+// ------------------------------------------------------------ fp32 arithmetic, any type
+// Eight lanes per key: lane c of an octet holds the channels 4 (c + 8 i) .. + 3, i < NC,
+// so a warp works on four keys at a time and a row is read in 16-byte pieces (8-byte for
+// bf16). Each octet keeps its own maximum and sums for the item's GH heads.
+template <typename T>
+__device__ __forceinline__ void load4(const T* row, int ch, int D, bool vec, float* f) {
+  if (vec) {
+    if (ch < D)
+      load_f<T, 4>(row + ch, f);
+    else
+      f[0] = f[1] = f[2] = f[3] = 0.f;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = ch + e < D ? static_cast<float>(row[ch + e]) : 0.f;
+  }
+}
+
+template <typename T, int NC, int GH>
+__global__ void __launch_bounds__(WARPS * 32) paged_any_kernel(AttnArgs a, int vec) {
+  constexpr int DP = NC * 32;
+  __shared__ float so[WARPS][GH][DP], sml[WARPS][GH][2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane & 7, oct = lane >> 3;
+  empty_rows(a);
+  Place p;
+  long long left = stretch(a, lane, &p);
+  while (left > 0) {
+    const int tiles = p.s.tiles();
+    const int t1 = (int)min((long long)tiles, p.tile + left);
+    const int hk = p.item / a.groups, g0 = (p.item - hk * a.groups) * GH;
+    const int heads = min(GH, a.G - g0), hq0 = hk * a.G + g0;
+    float q[GH][NC * 4], o[GH][NC * 4], m[GH], l[GH];
+#pragma unroll
+    for (int g = 0; g < GH; ++g) {
+      m[g] = -INFINITY;
+      l[g] = 0.f;
+#pragma unroll
+      for (int i = 0; i < NC * 4; ++i) {
+        const int ch = 4 * (c + 8 * (i >> 2)) + (i & 3);
+        o[g][i] = 0.f;
+        q[g][i] = 0.f;
+        if (g < heads && ch < a.D) {
+          const int64_t at = p.b * a.qb + (hq0 + g) * a.qh + ch;
+          q[g][i] = a.scale2 * (a.q_bf16 ? __bfloat162float(static_cast<const bf16*>(a.q)[at])
+                                         : static_cast<const float*>(a.q)[at]);
+        }
+      }
+    }
+    const int end = min(p.s.n, p.s.lo + t1 * TILE);
+    for (int j0 = p.s.lo + p.tile * TILE + warp * 4; j0 < end; j0 += WARPS * 4) {
+      const int j = j0 + oct;
+      const bool live = j < end;
+      const int64_t row = live ? key_row(a, p.b, j) : -1;
+      float s[GH], vv[NC * 4];
+#pragma unroll
+      for (int g = 0; g < GH; ++g) s[g] = 0.f;
+      if (row >= 0) {
+        const T* kr = static_cast<const T*>(a.kc) + row + hk * a.ph;
+        const T* vr = static_cast<const T*>(a.vc) + row + hk * a.ph;
+        float kv[NC * 4];
+#pragma unroll
+        for (int i = 0; i < NC; ++i) load4<T>(kr, 4 * (c + 8 * i), a.D, vec, kv + 4 * i);
+#pragma unroll
+        for (int i = 0; i < NC; ++i) load4<T>(vr, 4 * (c + 8 * i), a.D, vec, vv + 4 * i);
+#pragma unroll
+        for (int g = 0; g < GH; ++g)
+#pragma unroll
+          for (int i = 0; i < NC * 4; ++i) s[g] = fmaf(q[g][i], kv[i], s[g]);
+      }
+#pragma unroll
+      for (int g = 0; g < GH; ++g) {
+#pragma unroll
+        for (int x = 4; x > 0; x >>= 1) s[g] += __shfl_xor_sync(~0u, s[g], x);
+      }
+      if (!live) continue;                       // whole octets, after the shuffles
+      if (row < 0) {                             // a bad page poisons the item
+#pragma unroll
+        for (int g = 0; g < GH; ++g) l[g] = NAN;
+        continue;
+      }
+#pragma unroll
+      for (int g = 0; g < GH; ++g) {
+        if (s[g] > m[g]) {
+          const float f = exp2f(m[g] - s[g]);    // 0 from -inf
+          m[g] = s[g];
+          l[g] *= f;
+#pragma unroll
+          for (int i = 0; i < NC * 4; ++i) o[g][i] *= f;
+        }
+        const float w = exp2f(s[g] - (m[g] == -INFINITY ? 0.f : m[g]));
+        l[g] += w;
+#pragma unroll
+        for (int i = 0; i < NC * 4; ++i) o[g][i] = fmaf(w, vv[i], o[g][i]);
+      }
+    }
+    __syncwarp();
+    // Octets, then warps.
+#pragma unroll
+    for (int g = 0; g < GH; ++g) {
+      float mm = m[g];
+#pragma unroll
+      for (int x = 8; x < 32; x <<= 1) mm = fmaxf(mm, __shfl_xor_sync(~0u, mm, x));
+      const float f = m[g] == -INFINITY ? (l[g] == 0.f ? 0.f : 1.f) : exp2f(m[g] - mm);
+      l[g] *= f;
+#pragma unroll
+      for (int x = 8; x < 32; x <<= 1) l[g] += __shfl_xor_sync(~0u, l[g], x);
+#pragma unroll
+      for (int i = 0; i < NC * 4; ++i) {
+        o[g][i] *= f;
+#pragma unroll
+        for (int x = 8; x < 32; x <<= 1) o[g][i] += __shfl_xor_sync(~0u, o[g][i], x);
+        if (oct == 0) so[warp][g][4 * (c + 8 * (i >> 2)) + (i & 3)] = o[g][i];
+      }
+      if (lane == 0) {
+        sml[warp][g][0] = mm;
+        sml[warp][g][1] = l[g];
+      }
+    }
+    __syncthreads();
+    const bool done = p.tile == 0 && t1 == tiles;
+    const size_t slot = (size_t)blockIdx.x * 2 + (p.tile == 0 ? 1 : 0);
+    for (int e = threadIdx.x; e < heads * a.D; e += WARPS * 32) {
+      const int g = e / a.D, d = e - g * a.D;
+      float mm = -INFINITY, ll = 0.f, oo = 0.f;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) mm = fmaxf(mm, sml[w][g][0]);
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) {
+        const float f = sml[w][g][0] == -INFINITY ? 1.f : exp2f(sml[w][g][0] - mm);
+        ll += f * sml[w][g][1];
+        oo += f * so[w][g][d];
+      }
+      if (done) {
+        finish(a, p.b, hq0 + g, d, mm, ll, oo);
+      } else {
+        a.part_o[(slot * GMAX + g) * a.D + d] = oo;
+        if (d == 0) {
+          a.part_ml[(slot * GMAX + g) * 2] = mm;
+          a.part_ml[(slot * GMAX + g) * 2 + 1] = ll;
+        }
+      }
+    }
+    __syncthreads();
+    left -= t1 - p.tile;
+    if (left > 0) next_item(a, p);
+  }
+}
+
+// ------------------------------------------------------------ items cut by block boundaries
+// Block c: the item that the boundary after stretch c cuts, if that is the item's first one.
+__global__ void __launch_bounds__(128) paged_join_kernel(AttnArgs a) {
+  const int lane = threadIdx.x & 31;
+  const long long total = total_tiles(a, lane), per = (total + a.blocks - 1) / a.blocks;
+  const long long at = (blockIdx.x + 1) * per;
+  if (at >= total) return;
+  const Place p = locate(a, at, lane);
+  const long long first = at - p.tile;
+  if (p.tile == 0 || first / per != blockIdx.x) return;
+  const int c1 = (int)((first + p.s.tiles() - 1) / per);
+  const int hk = p.item / a.groups, g0 = (p.item - hk * a.groups) * a.GH;
+  const int heads = min(a.GH, a.G - g0);
+  for (int e = threadIdx.x; e < heads * a.D; e += 128) {
+    const int g = e / a.D, d = e - g * a.D;
+    float m = -INFINITY, l = 0.f, o = 0.f;
+    for (int c = blockIdx.x; c <= c1; ++c) {
+      const size_t s = ((size_t)c * 2 + (c == (int)blockIdx.x)) * GMAX + g;
+      const float m1 = a.part_ml[s * 2], l1 = a.part_ml[s * 2 + 1], o1 = a.part_o[s * a.D + d];
+      const float mm = fmaxf(m, m1);
+      const float f = m == -INFINITY ? 1.f : exp2f(m - mm);
+      const float f1 = m1 == -INFINITY ? 1.f : exp2f(m1 - mm);
+      l = l * f + l1 * f1;
+      o = o * f + o1 * f1;
+      m = mm;
+    }
+    finish(a, p.b, g0 + hk * a.G + g, d, m, l, o);
+  }
+}
+
+// ------------------------------------------------------------ host
+// Blocks of the shared line: enough for several per SM.
+constexpr int kBlocks = 152 * 4;
+constexpr long long kMaxKeys = (1LL << 31) - 1024;   // tile ends stay within an int
+constexpr int kWholeTiles = 4;    // capacity up to which one block takes a whole item
+
+struct Plan {
+  int GH, groups, whole, blocks;
+  size_t o_bytes, ml_bytes;
+};
+
+Plan make_plan(const gdr_attn_dims* d, const gdr_paged_cache* c) {
+  Plan p;
+  const int G = d->HQ / c->HK;
+  p.GH = c->D <= 128 ? 4 : 2;
+  p.groups = (G + p.GH - 1) / p.GH;
+  long long keys = (long long)c->max_pages * c->page_size;
+  if (d->window > 0 && keys > d->window) keys = d->window;
+  const long long items = (long long)d->B * c->HK * p.groups;
+  p.whole = keys <= kWholeTiles * TILE && items < (1LL << 31);
+  p.blocks = p.whole ? (int)items : kBlocks;
+  p.o_bytes = p.whole ? 0 : align_up((size_t)p.blocks * 2 * GMAX * c->D * sizeof(float));
+  p.ml_bytes = p.whole ? 0 : align_up((size_t)p.blocks * 2 * GMAX * 2 * sizeof(float));
+  return p;
+}
+
+gdr_status check(const gdr_attn_dims* d, const gdr_paged_cache* c) {
+  if (!d) return GDR_ERR_INVALID_ARG;
+  const gdr_status st = check_cache(c);
+  if (st != GDR_OK) return st;
+  if (d->B < 0 || d->HQ <= 0 || d->HQ % c->HK != 0 || !is_dtype(d->q_dtype) ||
+      !is_dtype(d->out_dtype) || d->window < 0 || d->q_stride_b < 0 || d->q_stride_h < 0 ||
+      !(isfinite(d->scale) && d->scale > 0.f))
+    return GDR_ERR_INVALID_ARG;
+  if (d->HQ > (1 << 20)) return GDR_ERR_UNSUPPORTED;
+  return GDR_OK;
+}
+
+}  // namespace
+}  // namespace ops
+}  // namespace gdr
+
+using namespace gdr;
+using namespace gdr::ops;
+
+extern "C" {
+
+size_t gdr_paged_decode_attn_workspace_size(const gdr_attn_dims* dims,
+                                            const gdr_paged_cache* cache) {
+  if (check(dims, cache) != GDR_OK) return 0;
+  const Plan p = make_plan(dims, cache);
+  return kAlign + p.o_bytes + p.ml_bytes;
+}
+
+gdr_status gdr_paged_decode_attn(const void* q, const void* k_cache, const void* v_cache,
+                                 const int32_t* page_table, const int32_t* lens, void* out,
+                                 float* lse, const gdr_attn_dims* dims,
+                                 const gdr_paged_cache* cache, void* workspace,
+                                 size_t workspace_bytes, gdr_stream_t stream) {
+  const gdr_status st = check(dims, cache);
+  if (st != GDR_OK) return st;
+  if (!is_aligned(q, dtype_size(dims->q_dtype)) || !is_aligned(k_cache, 16) ||
+      !is_aligned(v_cache, 16) || !is_aligned(page_table, 4) || !is_aligned(lens, 4) ||
+      !is_aligned(out, 16) || !is_aligned(lse, 16))
+    return GDR_ERR_ALIGNMENT;
+  if (dims->B == 0) return GDR_OK;
+  if (!q || !k_cache || !v_cache || !page_table || !lens || !out) return GDR_ERR_INVALID_ARG;
+  const Plan p = make_plan(dims, cache);
+  if (!workspace || workspace_bytes < kAlign + p.o_bytes + p.ml_bytes) return GDR_ERR_WORKSPACE;
+  if (!is_aligned(workspace, kAlign)) return GDR_ERR_ALIGNMENT;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  AttnArgs a = {};
+  a.q = q; a.kc = k_cache; a.vc = v_cache; a.table = page_table; a.lens = lens;
+  a.out = out; a.lse = lse;
+  a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + kAlign);
+  a.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + kAlign + p.o_bytes);
+  a.B = dims->B; a.HQ = dims->HQ; a.HK = cache->HK; a.D = cache->D;
+  a.G = dims->HQ / cache->HK; a.GH = p.GH; a.groups = p.groups;
+  a.page = cache->page_size; a.num_pages = cache->num_pages; a.max_pages = cache->max_pages;
+  a.window = dims->window; a.whole = p.whole; a.blocks = p.blocks;
+  a.out_bf16 = dims->out_dtype == GDR_BF16; a.q_bf16 = dims->q_dtype == GDR_BF16;
+  a.scale2 = dims->scale * LOG2E;
+  a.qb = dims->q_stride_b; a.qh = dims->q_stride_h;
+  a.pp = cache->page_stride; a.pt = cache->token_stride; a.ph = cache->head_stride;
+  if (a.B == 1) a.qb = 0;                        // never stepped along
+  if (a.HQ == 1) a.qh = 0;
+  a.cap = (long long)cache->max_pages * cache->page_size;
+  if (a.cap > kMaxKeys) a.cap = kMaxKeys;
+  const int vec = a.D % 4 == 0 && a.pp % 4 == 0 && a.pt % 4 == 0 && a.ph % 4 == 0;
+  const gdr_status run = with_dtype(cache->dtype, [&](auto* t) {
+    using T = std::remove_pointer_t<decltype(t)>;
+    if (a.D <= 64)
+      paged_any_kernel<T, 2, 4><<<p.blocks, WARPS * 32, 0, s>>>(a, vec);
+    else if (a.D <= 128)
+      paged_any_kernel<T, 4, 4><<<p.blocks, WARPS * 32, 0, s>>>(a, vec);
+    else
+      paged_any_kernel<T, 8, 2><<<p.blocks, WARPS * 32, 0, s>>>(a, vec);
+    return launched();
+  });
+  if (run != GDR_OK || p.whole) return run;
+  paged_join_kernel<<<p.blocks - 1, 128, 0, s>>>(a);
+  return launched();
+}
+
+}  // extern "C"

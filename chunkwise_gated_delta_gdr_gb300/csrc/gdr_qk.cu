@@ -1,0 +1,359 @@
+// gdr_qk.cu -- RMS norm of query and key heads with the position rotation, its
+// gradients, and the form that writes keys and values into a paged cache.
+//
+//   r = 1 / sqrt(mean(x^2) + eps),  u = r x,  y = turn(u w)
+//   d = turn^-1(dy),  dw = sum d u,  dx = r (d w - u mean(d w u))
+#include <type_traits>
+
+#include "gdr_ops.cuh"
+
+namespace gdr {
+namespace ops {
+namespace {
+
+enum Mode { kFwd = 0, kBwd = 1, kAppend = 2 };
+
+struct QkArgs {
+  const void *q, *k, *v;
+  const float *wq, *wk, *cos, *sin;
+  const void* pos;
+  void *qo, *ko;              // forward outputs; backward: the gradients of q and k
+  const void *dqo, *dko;      // backward: upstream gradients
+  float* part;                // backward: [gridDim.x][2][D] sums for the weights, or null
+  void *kc, *vc;              // append: the caches
+  const int32_t* table;
+  int B, T, HQ, HK, D, R, interleaved, pos64, rows;
+  int num_pages, page, max_pages, cache_bf16;
+  float eps;
+  int64_t qb, qt, qh, kb, kt, kh, vb, vt, vh, pp, pt, ph;
+  long long tokens;
+};
+
+__device__ __forceinline__ long long position(const QkArgs& a, long long tok) {
+  if (!a.pos) return 0;
+  return a.pos64 ? static_cast<const long long*>(a.pos)[tok] : static_cast<const int*>(a.pos)[tok];
+}
+
+// Offset of a token's row 0 in the caches, or -1 where it has no page.
+__device__ __forceinline__ int64_t cache_row(const QkArgs& a, long long b, long long p) {
+  if (p < 0 || p >= (long long)a.max_pages * a.page) return -1;
+  const int j = (int)(p / a.page);
+  const int32_t pg = a.table[b * a.max_pages + j];
+  if (pg < 0 || pg >= a.num_pages) return -1;
+  return pg * a.pp + (p - (long long)j * a.page) * a.pt;
+}
+
+__device__ __forceinline__ void store_cache(void* c, int64_t i, float v, int is_bf16) {
+  if (is_bf16)
+    static_cast<bf16*>(c)[i] = __float2bfloat16_rn(v);
+  else
+    static_cast<float*>(c)[i] = v;
+}
+
+// ------------------------------------------------------------ any size and stride
+// One warp per head row, channel i at lane i % 32; the pairs of the rotation meet in
+// shared memory. Covers what the vector kernel's alignment rules leave out.
+constexpr int GW = 8;                            // warps per block
+template <typename I, typename O, int MODE>
+__global__ void __launch_bounds__(GW * 32) qk_any_kernel(QkArgs a) {
+  constexpr int J = 8;                           // channels per lane: D <= 256
+  __shared__ float row[GW][256];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = a.R >> 1;
+  const int per = a.HQ + a.HK + (MODE == kAppend ? a.HK : 0);
+  float* y = row[warp];
+  float acc[2][J];
+#pragma unroll
+  for (int j = 0; j < J; ++j) acc[0][j] = acc[1][j] = 0.f;
+  const long long total = a.tokens * per;
+  for (long long r = (long long)blockIdx.x * GW + warp; r < total; r += (long long)gridDim.x * GW) {
+    const long long tok = r / per, b = tok / a.T, t = tok - b * a.T;
+    const int head = (int)(r - tok * per);
+    const int kind = head < a.HQ ? 0 : head < a.HQ + a.HK ? 1 : 2;
+    const int h = kind == 0 ? head : kind == 1 ? head - a.HQ : head - a.HQ - a.HK;
+    const long long p = position(a, tok);
+    bool bad = a.R > 0 && (p < 0 || p >= a.rows);
+    int64_t at = 0;
+    if (MODE == kAppend) {
+      at = cache_row(a, b, p);
+      bad = bad || at < 0;
+      at += h * a.ph;
+    }
+    const I* src = kind == 0   ? static_cast<const I*>(a.q) + b * a.qb + t * a.qt + h * a.qh
+                   : kind == 1 ? static_cast<const I*>(a.k) + b * a.kb + t * a.kt + h * a.kh
+                               : static_cast<const I*>(a.v) + b * a.vb + t * a.vt + h * a.vh;
+    if (MODE == kAppend && kind == 2) {
+      if (!bad)
+        for (int i = lane; i < a.D; i += 32)
+          store_cache(a.vc, at + i, static_cast<float>(src[i]), a.cache_bf16);
+      continue;
+    }
+    const float* w = kind == 0 ? a.wq : a.wk;
+    float x[J], ss = 0.f;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int i = lane + 32 * j;
+      x[j] = i < a.D ? static_cast<float>(src[i]) : 0.f;
+      ss = fmaf(x[j], x[j], ss);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o);
+    const float rs = rsqrtf(ss / a.D + a.eps);
+    const int64_t dense = (tok * (kind == 0 ? a.HQ : a.HK) + h) * a.D;
+    const O* dy = nullptr;
+    if (MODE == kBwd) dy = static_cast<const O*>(kind == 0 ? a.dqo : a.dko) + dense;
+    // Forward: the weighted unit row; backward: the upstream row.
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int i = lane + 32 * j;
+      if (i < a.D) y[i] = MODE == kBwd ? static_cast<float>(dy[i]) : x[j] * rs * (w ? w[i] : 1.f);
+    }
+    __syncwarp();
+    float z[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int i = lane + 32 * j;
+      z[j] = 0.f;
+      if (i >= a.D) continue;
+      z[j] = y[i];
+      if (i < a.R && !bad) {
+        const int pr = a.interleaved ? i >> 1 : (i < half ? i : i - half);
+        const bool first = a.interleaved ? (i & 1) == 0 : i < half;
+        const int mate = a.interleaved ? i ^ 1 : (first ? i + half : i - half);
+        const float c = a.cos[p * half + pr], s0 = a.sin[p * half + pr];
+        const float s = (MODE == kBwd) == first ? s0 : -s0;
+        z[j] = fmaf(y[mate], s, y[i] * c);
+      }
+      if (bad) z[j] = NAN;
+    }
+    __syncwarp();
+    if (MODE == kBwd) {
+      float m = 0.f;
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const int i = lane + 32 * j;
+        if (i >= a.D) continue;
+        const float u = x[j] * rs;
+        if (kind == 0)
+          acc[0][j] = fmaf(z[j], u, acc[0][j]);
+        else
+          acc[1][j] = fmaf(z[j], u, acc[1][j]);
+        z[j] *= w ? w[i] : 1.f;
+        m = fmaf(z[j], u, m);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(~0u, m, o);
+      m /= a.D;
+      I* dst = static_cast<I*>(kind == 0 ? a.qo : a.ko) + dense;
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const int i = lane + 32 * j;
+        if (i < a.D) dst[i] = static_cast<I>(rs * (z[j] - x[j] * rs * m));
+      }
+    } else if (MODE == kAppend && kind == 1) {
+      if (!bad)
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+          if (lane + 32 * j < a.D) store_cache(a.kc, at + lane + 32 * j, z[j], a.cache_bf16);
+    } else {
+      O* dst = static_cast<O*>(kind == 0 ? a.qo : a.ko) + dense;
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+        if (lane + 32 * j < a.D) dst[lane + 32 * j] = static_cast<O>(z[j]);
+    }
+  }
+  if (MODE == kBwd && a.part) {
+    for (int n = 0; n < 2; ++n) {
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < J; ++j) row[warp][lane + 32 * j] = acc[n][j];
+      __syncthreads();
+      for (int i = threadIdx.x; i < a.D; i += GW * 32) {
+        float s = 0.f;
+#pragma unroll
+        for (int v = 0; v < GW; ++v) s += row[v][i];
+        a.part[((size_t)blockIdx.x * 2 + n) * a.D + i] = s;
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------ the weights' gradients
+// One warp per (q or k, channel): the blocks' sums in order, 32 strands then a tree.
+__global__ void __launch_bounds__(256) qk_weight_kernel(const float* part, int blocks, int D,
+                                                        float* dwq, float* dwk) {
+  const int col = (blockIdx.x * 256 + threadIdx.x) >> 5, lane = threadIdx.x & 31;
+  if (col >= 2 * D) return;
+  float s = 0.f;
+  for (int i = lane; i < blocks; i += 32) s += part[(size_t)i * 2 * D + col];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
+  float* out = col < D ? dwq : dwk;
+  if (lane == 0 && out) out[col < D ? col : col - D] = s;
+}
+
+// ------------------------------------------------------------ host
+constexpr int kMaxBlocks = 1024;                 // of the backward: rows of the partial sums
+
+gdr_status check(const gdr_qk_dims* d) {
+  if (!d) return GDR_ERR_INVALID_ARG;
+  if (d->B < 0 || d->T < 0 || d->HQ <= 0 || d->HK <= 0 || d->D <= 0) return GDR_ERR_INVALID_ARG;
+  if (d->R < 0 || d->R > d->D || d->R % 2 != 0 || d->table_rows < 0) return GDR_ERR_INVALID_ARG;
+  if (!is_dtype(d->in_dtype) || !is_dtype(d->out_dtype)) return GDR_ERR_INVALID_ARG;
+  if (d->position_bits != 32 && d->position_bits != 64) return GDR_ERR_INVALID_ARG;
+  if (!(isfinite(d->eps) && d->eps > 0.f)) return GDR_ERR_INVALID_ARG;
+  const int64_t st[] = {d->q_stride_b, d->q_stride_t, d->q_stride_h, d->k_stride_b, d->k_stride_t,
+                        d->k_stride_h, d->v_stride_b, d->v_stride_t, d->v_stride_h};
+  for (int64_t s : st)
+    if (s < 0) return GDR_ERR_INVALID_ARG;
+  if (d->D > 256 || d->HQ > (1 << 20) || d->HK > (1 << 20)) return GDR_ERR_UNSUPPORTED;
+  return GDR_OK;
+}
+
+QkArgs make_args(const gdr_qk_dims* d, const float* wq, const float* wk, const float* cos,
+                 const float* sin, const void* pos) {
+  QkArgs a = {};
+  a.wq = wq; a.wk = wk; a.cos = cos; a.sin = sin; a.pos = pos;
+  a.B = d->B; a.T = d->T; a.HQ = d->HQ; a.HK = d->HK; a.D = d->D; a.R = d->R;
+  a.interleaved = d->interleaved != 0;
+  a.pos64 = d->position_bits == 64;
+  a.rows = d->table_rows;
+  a.eps = d->eps;
+  a.qb = d->q_stride_b; a.qt = d->q_stride_t; a.qh = d->q_stride_h;
+  a.kb = d->k_stride_b; a.kt = d->k_stride_t; a.kh = d->k_stride_h;
+  a.vb = d->v_stride_b; a.vt = d->v_stride_t; a.vh = d->v_stride_h;
+  a.tokens = (long long)d->B * d->T;
+  if (a.B == 1) a.qb = a.kb = a.vb = 0;          // never stepped along
+  if (a.T == 1) a.qt = a.kt = a.vt = 0;
+  if (a.HQ == 1) a.qh = 0;
+  if (a.HK == 1) a.kh = a.vh = 0;
+  return a;
+}
+
+// The arguments every form shares: null pointers and alignment of the dense ones.
+gdr_status check_shared(const gdr_qk_dims* d, const void* q, const void* k, const float* wq,
+                        const float* wk, const float* cos, const float* sin, const void* pos,
+                        bool need_pos) {
+  if (d->B > 0 && d->T > 0) {
+    if (!q || !k) return GDR_ERR_INVALID_ARG;
+    if (d->R > 0 && (!cos || !sin)) return GDR_ERR_INVALID_ARG;
+    if ((d->R > 0 || need_pos) && !pos) return GDR_ERR_INVALID_ARG;
+  }
+  const size_t e = dtype_size(d->in_dtype);
+  if (!is_aligned(q, e) || !is_aligned(k, e) || !is_aligned(wq, 16) || !is_aligned(wk, 16) ||
+      !is_aligned(cos, 16) || !is_aligned(sin, 16) || !is_aligned(pos, d->position_bits / 8))
+    return GDR_ERR_ALIGNMENT;
+  return GDR_OK;
+}
+
+int any_blocks(const QkArgs& a, int per, int most) {
+  const long long want = (a.tokens * per + GW - 1) / GW;
+  return (int)(want < most ? want : most);
+}
+
+template <int MODE>
+gdr_status launch(const gdr_qk_dims* d, const QkArgs& a, int blocks, cudaStream_t s) {
+  return with_dtype(d->in_dtype, [&](auto* i) {
+    return with_dtype(d->out_dtype, [&](auto* o) {
+      using I = std::remove_pointer_t<decltype(i)>;
+      using O = std::remove_pointer_t<decltype(o)>;
+      qk_any_kernel<I, O, MODE><<<blocks, GW * 32, 0, s>>>(a);
+      return launched();
+    });
+  });
+}
+
+}  // namespace
+}  // namespace ops
+}  // namespace gdr
+
+using namespace gdr;
+using namespace gdr::ops;
+
+extern "C" {
+
+gdr_status gdr_qk_norm_rope(const void* q, const void* k, const float* q_weight,
+                            const float* k_weight, const float* cos, const float* sin,
+                            const void* positions, void* q_out, void* k_out,
+                            const gdr_qk_dims* dims, gdr_stream_t stream) {
+  gdr_status st = check(dims);
+  if (st != GDR_OK) return st;
+  st = check_shared(dims, q, k, q_weight, k_weight, cos, sin, positions, false);
+  if (st != GDR_OK) return st;
+  if (!is_aligned(q_out, 16) || !is_aligned(k_out, 16)) return GDR_ERR_ALIGNMENT;
+  if (dims->B == 0 || dims->T == 0) return GDR_OK;
+  if (!q_out || !k_out) return GDR_ERR_INVALID_ARG;
+  QkArgs a = make_args(dims, q_weight, k_weight, cos, sin, positions);
+  a.q = q; a.k = k; a.qo = q_out; a.ko = k_out;
+  return launch<kFwd>(dims, a, any_blocks(a, a.HQ + a.HK, 1 << 20),
+                      reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t gdr_qk_norm_rope_bwd_workspace_size(const gdr_qk_dims* dims) {
+  if (check(dims) != GDR_OK) return 0;
+  return align_up((size_t)kMaxBlocks * 2 * dims->D * sizeof(float));
+}
+
+gdr_status gdr_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q,
+                                const void* k, const float* q_weight, const float* k_weight,
+                                const float* cos, const float* sin, const void* positions,
+                                void* dq, void* dk, float* dq_weight, float* dk_weight,
+                                const gdr_qk_dims* dims, void* workspace, size_t workspace_bytes,
+                                gdr_stream_t stream) {
+  gdr_status st = check(dims);
+  if (st != GDR_OK) return st;
+  st = check_shared(dims, q, k, q_weight, k_weight, cos, sin, positions, false);
+  if (st != GDR_OK) return st;
+  if (!is_aligned(dq_out, 16) || !is_aligned(dk_out, 16) || !is_aligned(dq, 16) ||
+      !is_aligned(dk, 16) || !is_aligned(dq_weight, 16) || !is_aligned(dk_weight, 16))
+    return GDR_ERR_ALIGNMENT;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (dims->B == 0 || dims->T == 0) {            // no tokens: the sums are zero
+    for (float* w : {dq_weight, dk_weight})
+      if (w && cudaMemsetAsync(w, 0, dims->D * sizeof(float), s) != cudaSuccess)
+        return GDR_ERR_CUDA;
+    return GDR_OK;
+  }
+  if (!dq_out || !dk_out || !dq || !dk) return GDR_ERR_INVALID_ARG;
+  QkArgs a = make_args(dims, q_weight, k_weight, cos, sin, positions);
+  a.q = q; a.k = k; a.dqo = dq_out; a.dko = dk_out; a.qo = dq; a.ko = dk;
+  if (dq_weight || dk_weight) {
+    if (!workspace || workspace_bytes < gdr_qk_norm_rope_bwd_workspace_size(dims))
+      return GDR_ERR_WORKSPACE;
+    if (!is_aligned(workspace, kAlign)) return GDR_ERR_ALIGNMENT;
+    a.part = static_cast<float*>(workspace);
+  }
+  const int blocks = any_blocks(a, a.HQ + a.HK, kMaxBlocks);
+  st = launch<kBwd>(dims, a, blocks, s);
+  if (st != GDR_OK || !a.part) return st;
+  qk_weight_kernel<<<(2 * a.D + 7) / 8, 256, 0, s>>>(a.part, blocks, a.D, dq_weight, dk_weight);
+  return launched();
+}
+
+gdr_status gdr_qk_norm_rope_append(const void* q, const void* k, const void* v,
+                                   const float* q_weight, const float* k_weight, const float* cos,
+                                   const float* sin, const void* positions, void* q_out,
+                                   void* k_cache, void* v_cache, const int32_t* page_table,
+                                   const gdr_qk_dims* dims, const gdr_paged_cache* cache,
+                                   gdr_stream_t stream) {
+  gdr_status st = check(dims);
+  if (st != GDR_OK) return st;
+  st = check_cache(cache);
+  if (st != GDR_OK) return st;
+  if (cache->HK != dims->HK || cache->D != dims->D) return GDR_ERR_INVALID_ARG;
+  st = check_shared(dims, q, k, q_weight, k_weight, cos, sin, positions, true);
+  if (st != GDR_OK) return st;
+  if (!is_aligned(v, dtype_size(dims->in_dtype)) || !is_aligned(q_out, 16) ||
+      !is_aligned(k_cache, 16) || !is_aligned(v_cache, 16) || !is_aligned(page_table, 4))
+    return GDR_ERR_ALIGNMENT;
+  if (dims->B == 0 || dims->T == 0) return GDR_OK;
+  if (!v || !q_out || !k_cache || !v_cache || !page_table) return GDR_ERR_INVALID_ARG;
+  QkArgs a = make_args(dims, q_weight, k_weight, cos, sin, positions);
+  a.q = q; a.k = k; a.v = v; a.qo = q_out; a.kc = k_cache; a.vc = v_cache; a.table = page_table;
+  a.num_pages = cache->num_pages; a.page = cache->page_size; a.max_pages = cache->max_pages;
+  a.cache_bf16 = cache->dtype == GDR_BF16;
+  a.pp = cache->page_stride; a.pt = cache->token_stride; a.ph = cache->head_stride;
+  return launch<kAppend>(dims, a, any_blocks(a, a.HQ + 2 * a.HK, 1 << 20),
+                         reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

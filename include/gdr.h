@@ -329,6 +329,218 @@ gdr_status gdr_chunk_fwd_segmented(const void* q, const void* k, const void* v, 
 size_t gdr_chunk_fwd_segmented_workspace_size(const gdr_dims* dims, int chunk_size,
                                               int gate_mode, int segments);
 
+/* ==========================================================================
+ * The other layers of a decoder built on the recurrences above: a gated linear
+ * recurrence with a vector state (forward and backward), the per-head norm and
+ * position rotation of an attention layer's queries and keys (forward, backward,
+ * and the serving form that fills a paged key-value cache), and the attention
+ * of one new token over that cache. These entry points take views: inputs
+ * described with strides (in elements, >= 0) may start at any element and skip
+ * freely between tokens and heads; only the last dimension is dense. Tensors
+ * without strides stay dense, with 16-byte aligned bases (positions, page_table
+ * and lens: their element's alignment). No output may overlap an input unless
+ * the entry says so. The method's pages have no counterpart of these operators.
+ */
+
+/*
+ * gdr_linear_scan_fwd -- gated linear recurrence, one state per channel:
+ *     h_t = exp(g_t) h_{t-1} + u_t,   t = 0 .. T-1,   h_{-1} = initial_state (or 0)
+ * with u_t = x_t, or u_t = (1 - exp(g_t)) x_t when gated_input is set (an
+ * exponential average). States and sums are fp32.
+ *
+ *   x               (device) [B, T, D] x_dtype, strides x_stride_b, x_stride_t
+ *   g               (device) [B, T, D] g_dtype, natural-log decay, strides g_stride_*;
+ *                   any sign, but the sum of g over any span of tokens must stay below
+ *                   ~80; -inf restarts the channel (exp(g) = 0)
+ *   initial_state   (device) fp32 [B, D] or NULL (zeros)
+ *   h               (device) [B, T, D] h_dtype
+ *   final_state     (device) fp32 [B, D] or NULL; may alias initial_state
+ *   checkpoints     (device) fp32 [B, ceil(T / GDR_SCAN_CHECKPOINT), D] or NULL: the state
+ *                   before every GDR_SCAN_CHECKPOINT-th token, for gdr_linear_scan_bwd
+ *
+ * T = 1 is the decode step (initial_state and final_state the same buffer).
+ * T == 0 writes final_state = initial_state (or zeros) and nothing else.
+ */
+#define GDR_SCAN_CHECKPOINT 64
+
+typedef struct {
+  int B, T, D;
+  int x_dtype;      /* gdr_dtype of x and dx */
+  int g_dtype;      /* gdr_dtype of g and dg */
+  int h_dtype;      /* gdr_dtype of h and dh */
+  int gated_input;  /* 0: u = x; nonzero: u = (1 - exp(g)) x */
+  int64_t x_stride_b, x_stride_t;    /* elements */
+  int64_t g_stride_b, g_stride_t;
+  int64_t dh_stride_b, dh_stride_t;  /* backward only */
+} gdr_scan_dims;
+
+gdr_status gdr_linear_scan_fwd(const void* x, const void* g, const float* initial_state, void* h,
+                               float* final_state, float* checkpoints, const gdr_scan_dims* dims,
+                               gdr_stream_t stream);
+
+/* Bytes of the checkpoints of these sizes (0 if the arguments are invalid). */
+size_t gdr_linear_scan_checkpoints_size(const gdr_scan_dims* dims);
+
+/*
+ * gdr_linear_scan_bwd -- gradients of gdr_linear_scan_fwd. With
+ *     l_t = dh_t + exp(g_{t+1}) l_{t+1},   l_{T-1} = dh_{T-1} + d_final_state
+ * it writes dx_t = l_t (times 1 - exp(g_t) with gated_input),
+ * dg_t = l_t exp(g_t) (h_{t-1}, minus x_t with gated_input) and
+ * d_initial_state = exp(g_0) l_0. The states h are rebuilt in fp32 from x, g
+ * and the checkpoints of the forward call, never from its rounded output.
+ *
+ *   dh               (device) [B, T, D] h_dtype, strides dh_stride_*
+ *   x, g             as in the forward call (the same values)
+ *   checkpoints      (device) as the forward call wrote them
+ *   d_final_state    (device) fp32 [B, D] or NULL (zeros)
+ *   dx, dg           (device) [B, T, D] x_dtype and g_dtype, dense
+ *   d_initial_state  (device) fp32 [B, D] or NULL; may alias d_final_state
+ *
+ * T == 0 writes d_initial_state = d_final_state (or zeros) and nothing else.
+ * The results do not depend on the order in which blocks run.
+ */
+gdr_status gdr_linear_scan_bwd(const void* dh, const void* x, const void* g,
+                               const float* checkpoints, const float* d_final_state, void* dx,
+                               void* dg, float* d_initial_state, const gdr_scan_dims* dims,
+                               gdr_stream_t stream);
+
+/*
+ * gdr_qk_norm_rope -- RMS norm of every query and key head, then the position
+ * rotation, in one pass. For each head row x of D channels
+ *     y = x / sqrt(mean(x^2) + eps) * weight
+ * and the first R channels of y are turned pair by pair by the token's angle:
+ *     (y_i, y_j) <- (y_i c - y_j s, y_j c + y_i s),   c, s = cos, sin[position][p]
+ * with the pair p = 0 .. R/2-1 at i = p, j = p + R/2, or at i = 2p, j = 2p + 1
+ * when interleaved is set. All of it is fp32, rounded once to out_dtype.
+ *
+ *   q, k       (device) [B, T, HQ, D], [B, T, HK, D] in_dtype, strides below
+ *   q_weight, k_weight  (device) fp32 [D], or NULL (ones)
+ *   cos, sin   (device) fp32 [table_rows, R / 2]; NULL with R == 0
+ *   positions  (device) [B, T] int32 or int64 (position_bits); NULL with R == 0
+ *   q_out, k_out  (device) [B, T, HQ, D], [B, T, HK, D] out_dtype, dense
+ *
+ * D <= 256; R even, 0 <= R <= D. A token whose position is outside
+ * [0, table_rows) gets NaN in all its output rows (no address outside the
+ * tables is formed).
+ */
+typedef struct {
+  int B, T, HQ, HK, D, R;
+  int in_dtype;       /* gdr_dtype of q, k (and v, dq, dk) */
+  int out_dtype;      /* gdr_dtype of q_out, k_out (and dq_out, dk_out) */
+  int interleaved;
+  int position_bits;  /* 32 or 64 */
+  int table_rows;
+  float eps;          /* finite, > 0 */
+  int64_t q_stride_b, q_stride_t, q_stride_h;  /* elements */
+  int64_t k_stride_b, k_stride_t, k_stride_h;
+  int64_t v_stride_b, v_stride_t, v_stride_h;  /* gdr_qk_norm_rope_append only */
+} gdr_qk_dims;
+
+gdr_status gdr_qk_norm_rope(const void* q, const void* k, const float* q_weight,
+                            const float* k_weight, const float* cos, const float* sin,
+                            const void* positions, void* q_out, void* k_out,
+                            const gdr_qk_dims* dims, gdr_stream_t stream);
+
+/*
+ * gdr_qk_norm_rope_bwd -- gradients of gdr_qk_norm_rope. With d the upstream
+ * gradient turned back by the angle and u = x / sqrt(mean(x^2) + eps):
+ *     d_weight = sum over tokens and heads of d u
+ *     dx = (d weight - u mean(d weight u)) / sqrt(mean(x^2) + eps)
+ *
+ *   dq_out, dk_out  (device) [B, T, HQ, D], [B, T, HK, D] out_dtype, dense
+ *   dq, dk          (device) the same shapes, in_dtype, dense
+ *   dq_weight, dk_weight  (device) fp32 [D], or NULL (not computed)
+ *   workspace       (device) gdr_qk_norm_rope_bwd_workspace_size() bytes, 256-byte aligned;
+ *                   not needed (NULL, 0) when both weight gradients are NULL
+ *
+ * The weight gradients are summed in an order that depends on the sizes and
+ * the device alone. A token whose position is outside the tables gives NaN.
+ */
+gdr_status gdr_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q,
+                                const void* k, const float* q_weight, const float* k_weight,
+                                const float* cos, const float* sin, const void* positions,
+                                void* dq, void* dk, float* dq_weight, float* dk_weight,
+                                const gdr_qk_dims* dims, void* workspace, size_t workspace_bytes,
+                                gdr_stream_t stream);
+size_t gdr_qk_norm_rope_bwd_workspace_size(const gdr_qk_dims* dims);
+
+/*
+ * A paged key-value cache: pages of page_size tokens, each HK heads of D
+ * channels, for keys and for values (two arrays of the same layout). Element
+ * (page, token, head, channel) is at page page_stride + token token_stride +
+ * head head_stride + channel. page_table [B, max_pages] int32 (dense) names the
+ * pages of each sequence in order; entries beyond a sequence's length are not
+ * read.
+ */
+typedef struct {
+  int num_pages, page_size, HK, D;
+  int dtype;      /* gdr_dtype of both caches */
+  int max_pages;  /* columns of page_table */
+  int64_t page_stride, token_stride, head_stride;  /* elements */
+} gdr_paged_cache;
+
+/*
+ * gdr_qk_norm_rope_append -- gdr_qk_norm_rope for serving: the normed and
+ * rotated keys and the values (unchanged) go straight into their pages.
+ *
+ * q, k, v and the norm's arguments as above (v [B, T, HK, D] in_dtype). Token t
+ * of sequence b is stored at index positions[b][t] of its sequence: page
+ * page_table[b][position / page_size], token position % page_size. q_out
+ * [B, T, HQ, D] out_dtype; out_dtype may differ from the caches' dtype.
+ * positions is needed even with R == 0. No two tokens may share a position of
+ * one sequence, and no page may be shared between the sequences of a call.
+ * A position outside the rotation's tables (with R > 0) or the page table, or
+ * a table entry outside [0, num_pages), stores nothing and gives NaN in the
+ * token's q_out rows.
+ */
+gdr_status gdr_qk_norm_rope_append(const void* q, const void* k, const void* v,
+                                   const float* q_weight, const float* k_weight, const float* cos,
+                                   const float* sin, const void* positions, void* q_out,
+                                   void* k_cache, void* v_cache, const int32_t* page_table,
+                                   const gdr_qk_dims* dims, const gdr_paged_cache* cache,
+                                   gdr_stream_t stream);
+
+/*
+ * gdr_paged_decode_attn -- attention of one new token per sequence over its
+ * paged cache. Query head hq reads key-value head hq / (HQ / HK). Over the keys
+ * j of sequence b with max(0, len - window) <= j < len (window 0: no limit)
+ *     o = sum_j softmax_j(scale q . k_j) v_j,   lse = log sum_j exp(scale q . k_j)
+ * The keys of a sequence are shared out over the whole device in equal parts
+ * and the parts joined, so one long row runs as fast as many short ones.
+ *
+ *   q           (device) [B, HQ, D] q_dtype, strides q_stride_b, q_stride_h
+ *   k_cache, v_cache, page_table  (device) the cache
+ *   lens        (device) int32 [B]: keys of each sequence (the new token's included)
+ *   out         (device) [B, HQ, D] out_dtype
+ *   lse         (device) fp32 [B, HQ], or NULL
+ *   workspace   (device) gdr_paged_decode_attn_workspace_size() bytes, 256-byte aligned;
+ *               contents on entry do not matter
+ *
+ * D <= 256. bf16 q and caches with D in {64, 80, 96, 128, 192, 256} and 16-byte
+ * aligned rows run on the tensor cores (products of bf16 values, sums and the
+ * softmax in fp32, its weights rounded to bf16 for the product with V); the
+ * others in fp32. Keys outside the range are not read, whatever they hold. A
+ * row without keys gives o = 0 and lse = -inf. A length outside
+ * [0, max_pages page_size] or a table entry outside [0, num_pages) gives NaN
+ * for that sequence. The result does not depend on the order in which blocks
+ * run.
+ */
+typedef struct {
+  int B, HQ;
+  int q_dtype, out_dtype;
+  int window;  /* >= 0; 0: every key */
+  float scale; /* finite, > 0 */
+  int64_t q_stride_b, q_stride_h;  /* elements */
+} gdr_attn_dims;
+
+gdr_status gdr_paged_decode_attn(const void* q, const void* k_cache, const void* v_cache,
+                                 const int32_t* page_table, const int32_t* lens, void* out,
+                                 float* lse, const gdr_attn_dims* dims,
+                                 const gdr_paged_cache* cache, void* workspace,
+                                 size_t workspace_bytes, gdr_stream_t stream);
+size_t gdr_paged_decode_attn_workspace_size(const gdr_attn_dims* dims,
+                                            const gdr_paged_cache* cache);
+
 /* Static, human-readable name of a status code. */
 const char* gdr_status_string(gdr_status s);
 
