@@ -46,6 +46,16 @@ __device__ __forceinline__ Raw<T, V> load_raw(const T* p) {
     r.v = *reinterpret_cast<const decltype(r.v)*>(p);
   return r;
 }
+// The same, for data that is read once.
+template <typename T, int V>
+__device__ __forceinline__ Raw<T, V> load_once(const T* p) {
+  Raw<T, V> r;
+  if constexpr (V == 1)
+    r.v[0] = __ldcs(p);
+  else
+    r.v = __ldcs(reinterpret_cast<const decltype(r.v)*>(p));
+  return r;
+}
 template <typename T, int V>
 __device__ __forceinline__ Raw<T, V> zero_raw() {
   Raw<T, V> r;
