@@ -2,10 +2,12 @@
 //
 //   h_t = a_t h_{t-1} + u_t,  a = exp(g),  u = x or (1 - a) x
 //   l_t = dh_t + a_{t+1} l_{t+1};  dx = l (1 - a, gated),  dg = l a (h_{t-1} - x, gated)
+#include <atomic>
 #include <type_traits>
 
 #include "gdr_ops.cuh"
 #include "gdr_ptx.cuh"
+#include "gdr_tmap.cuh"
 
 namespace gdr {
 namespace ops {
@@ -59,31 +61,38 @@ __global__ void __launch_bounds__(128) scan_serial_kernel(ScanArgs a) {
 
 // ------------------------------------------------------------ split along the sequence
 // A cluster of S blocks walks the tokens of one column block (32 V channels) in steps of S
-// tiles of TILE tokens, a tile per block, R tokens of it per warp. A stretch of tokens acts
-// on the state as h -> A h + H (A the product of its a), and two stretches compose as
-// (A2 A1, A2 H1 + H2). Per step each warp forms the pair of its tokens from registers, the
-// warps' pairs meet in shared memory, the blocks' pairs in every block's shared memory
-// (written remotely), and one cluster barrier later each warp knows the state before its
-// first token and runs its tokens again, now with it, from the same registers. The next
-// step's tokens load meanwhile. All orders are fixed.
-constexpr int W = 8, R = 8, TILE = W * R, MAXS = 16;
-static_assert(TILE == CK, "a tile starts at a checkpoint");
+// tiles, a tile of W R tokens per block, R of them per warp. A stretch of tokens acts on the
+// state as h -> A h + P (A the product of its a), and two stretches compose as
+// (A2 A1, A2 P1 + P2). Per step each warp forms the pair of its tokens from registers, the
+// warps' pairs meet in shared memory, the blocks' pairs in every block's shared memory, sent
+// there with their bytes counted on a barrier of the receiver (one way, where a cluster
+// barrier takes a round trip). Then each warp knows the state before its first token and
+// runs its tokens again from the same registers, now with it. All orders are fixed.
+constexpr int W = 8, MAXS = 8;
+constexpr long kWaitLimit = 1L << 24;
 
-// Pairs (or triples) of the warps, double-buffered by step: one barrier per step suffices,
-// as a buffer is written again only after the barrier of the step between.
-template <int V>
+// Tokens per warp: as many as leave two blocks on an SM, registers and shared memory both.
+template <typename X, typename G, int V>
+constexpr int kRows = V == 1 || sizeof(X) + sizeof(G) <= 6 ? 16 : 8;
+
+// Pairs (or triples) of the warps and pairs of the blocks, double-buffered by step: a buffer
+// is written again only after the block barrier of the step between, and after every block
+// has sent that step's pair, which it does once it has read this one.
+template <int V, int K>
 struct alignas(16) ScanShared {
-  float warp[2][W][3][32 * V];
-  float block[2][MAXS][2][32 * V];
+  float warp[2][W][32][K * V];
+  float block[2][MAXS][32][2 * V];
+  uint64_t full[4];                  // ring stages (tensor copies)
+  uint64_t met[2];                   // the blocks' pairs
 };
 
-template <int V>
+template <int N>
 __device__ __forceinline__ void put_v(float* p, const float* v) {
-  store_f<float, V>(p, v);
+  store_f<float, N>(p, v);
 }
-template <int V>
+template <int N>
 __device__ __forceinline__ void get_v(const float* p, float* v) {
-  load_f<float, V>(p, v);
+  load_f<float, N>(p, v);
 }
 template <int V>
 __device__ __forceinline__ void copy_v(float* p, const float* v) {
@@ -91,149 +100,265 @@ __device__ __forceinline__ void copy_v(float* p, const float* v) {
   for (int i = 0; i < V; ++i) p[i] = v[i];
 }
 
-// Writes v to the same shared location in block `rank` of the cluster.
-template <int V>
-__device__ __forceinline__ void put_remote(float* p, uint32_t rank, const float* v) {
-  const uint32_t at = ptx::mapa(ptx::smem_u32(p), rank);
-#pragma unroll
-  for (int i = 0; i < V; ++i)
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at + 4 * i), "f"(v[i]) : "memory");
+// A wait that gave up makes every later result of the block NaN.
+__device__ __forceinline__ void wait_or_poison(uint64_t* bar, uint32_t parity, float* carry, int V) {
+  if (!ptx::mbar_wait(bar, parity, kWaitLimit))
+    for (int i = 0; i < V; ++i) carry[i] = NAN;
 }
 
-// The cluster's pairs applied to `carry`: in, the state before this step; returns the state
-// before this block's tile, and leaves the state after the step in carry. tA, tH: this
-// block's pair. Includes the step's barrier.
-template <int V>
-__device__ __forceinline__ void cluster_carry(ScanShared<V>& sm, int par, int S, int rank,
+// Bounded wait for the pairs of a step, acquiring what other blocks of the cluster sent.
+__device__ __forceinline__ bool met_wait(uint64_t* bar, uint32_t parity) {
+  for (long i = 0; i < kWaitLimit; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n"
+        " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(ptx::smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (ok) return true;
+  }
+  return false;
+}
+
+// The blocks' pairs of a step applied to `carry` (the state before the step): `mine` becomes
+// the state before this block's tile, carry the state after the step.
+template <int V, int K>
+__device__ __forceinline__ void cluster_carry(ScanShared<V, K>& sm, int step, int S, int rank,
                                               int warp, int lane, const float* tA,
-                                              const float* tH, float* carry, float* mine) {
+                                              const float* tP, float* carry, float* mine) {
   if (S == 1) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       mine[i] = carry[i];
-      carry[i] = fmaf(tA[i], carry[i], tH[i]);
+      carry[i] = fmaf(tA[i], carry[i], tP[i]);
     }
     return;
   }
-  for (int q = warp; q < S; q += W) {
-    put_remote<V>(&sm.block[par][rank][0][lane * V], q, tA);
-    put_remote<V>(&sm.block[par][rank][1][lane * V], q, tH);
+  const int par = step & 1;
+  if (threadIdx.x == 0) ptx::mbar_expect_tx(&sm.met[par], S * 32 * 2 * V * 4);
+  if (warp < S) {
+    const uint32_t dst = ptx::mapa(ptx::smem_u32(sm.block[par][rank][lane]), warp);
+    const uint32_t bar = ptx::mapa(ptx::smem_u32(&sm.met[par]), warp);
+    if constexpr (V == 2)
+      asm volatile(
+          "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, "
+          "[%5];" ::"r"(dst), "f"(tA[0]), "f"(tA[1]), "f"(tP[0]), "f"(tP[1]), "r"(bar)
+          : "memory");
+    else
+      asm volatile(
+          "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(
+              dst), "f"(tA[0]), "f"(tP[0]), "r"(bar)
+          : "memory");
   }
-  ptx::cluster_sync();
-#pragma unroll 4
-  for (int q = 0; q < S; ++q) {
-    float qA[V], qH[V];
-    get_v<V>(&sm.block[par][q][0][lane * V], qA);
-    get_v<V>(&sm.block[par][q][1][lane * V], qH);
-    if (q == rank) copy_v<V>(mine, carry);
+  if (!met_wait(&sm.met[par], (step >> 1) & 1)) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) carry[i] = fmaf(qA[i], carry[i], qH[i]);
+    for (int i = 0; i < V; ++i) carry[i] = NAN;
+  }
+#pragma unroll
+  for (int q = 0; q < MAXS; ++q) {
+    if (q == rank) copy_v<V>(mine, carry);
+    if (q < S) {
+      float m[2 * V];
+      get_v<2 * V>(sm.block[par][q][lane], m);
+#pragma unroll
+      for (int i = 0; i < V; ++i) carry[i] = fmaf(m[i], carry[i], m[V + i]);
+    }
   }
 }
 
-template <typename X, typename G, typename H, int V>
-__global__ void __launch_bounds__(W * 32, 3) scan_kernel(ScanArgs a, int S) {
-  __shared__ ScanShared<V> sm;
+// One tensor's tiles on their way into a ring in shared memory, token-major. kTensor: a
+// thread copies whole tiles, out-of-range tokens and channels arriving as zeros (so that
+// a = exp(0) = 1 and u = 0 there: tokens that change nothing). Otherwise each thread copies
+// its own channel's tokens, fp32 asynchronously, bf16 (too small for such a copy) through
+// registers; it reads only those, so it waits for itself alone.
+template <typename T, int V, int R, bool kTensor>
+struct Feed {
+  static constexpr bool kRing = kTensor || sizeof(T) == 4;
+  static constexpr int kBytes = kRing ? W * R * 32 * V * (int)sizeof(T) : 0;    // of a stage
+  Raw<T, V> reg[kRing ? 1 : R];
+  char* base;
+  __device__ __forceinline__ Feed(char* ring, int warp, int lane)
+      : base(ring + (warp * R * 32 + lane) * V * (int)sizeof(T)) {}
+  __device__ __forceinline__ void fetch(int offset, int r, const T* p) {
+    static_assert(kTensor || V == 1, "");
+    if constexpr (kRing)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
+                       ptx::smem_u32(base + offset + r * (32 * V * (int)sizeof(T)))),
+                   "l"(p)
+                   : "memory");
+    else
+      reg[r] = load_once<T, V>(p);
+  }
+  __device__ __forceinline__ void take(int offset, int r, float* f) const {
+    if constexpr (kRing)
+      load_f<T, V>(
+          reinterpret_cast<const T*>(base + offset + r * (32 * V * (int)sizeof(T))), f);
+    else
+      to_float<T, V>(reg[r], f);
+  }
+};
+
+// Tiles under way. Without a ring for every tensor: the one the registers hold.
+template <typename X, typename G, typename H, bool kTensor>
+constexpr int kStages = kTensor || (sizeof(X) == 4 && sizeof(G) == 4 && sizeof(H) == 4) ? 2 : 1;
+
+struct ScanMaps {
+  CUtensorMap x, g, dh;
+};
+
+template <typename X, typename G, typename H, int V, bool kTensor>
+struct Fwd {
+  static constexpr int R = kRows<X, G, V>, TILE = W * R, ST = kStages<X, G, float, kTensor>;
+  static constexpr int XB = Feed<X, V, R, kTensor>::kBytes, GB = Feed<G, V, R, kTensor>::kBytes;
+  static constexpr int SB = XB + GB, SMEM = ST * SB;
+};
+
+template <typename X, typename G, typename H, int V, bool kTensor>
+__global__ void __launch_bounds__(W * 32, 2)
+    scan_kernel(const __grid_constant__ ScanMaps maps, ScanArgs a, int S) {
+  using F = Fwd<X, G, H, V, kTensor>;
+  constexpr int R = F::R, TILE = F::TILE, ST = F::ST, SB = F::SB;
+  extern __shared__ __align__(128) char ring[];
+  __shared__ ScanShared<V, 2> sm;
   const int rank = blockIdx.x % S, col = blockIdx.x / S, b = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int d = (col * 32 + lane) * V;
   const bool on = d < a.D;
   const X* x = static_cast<const X*>(a.x) + b * a.xb + d;
   const G* g = static_cast<const G*>(a.g) + b * a.gb + d;
-  H* h = static_cast<H*>(a.h) + (size_t)b * a.T * a.D + d;
   float carry[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) carry[i] = on && a.s0 ? a.s0[(size_t)b * a.D + d + i] : 0.f;
 
-  Raw<X, V> xr[R];
-  Raw<G, V> gr[R];
-  auto load = [&](int t0) {
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      if (on && t0 + r < a.T) {
-        xr[r] = load_once<X, V>(x + (t0 + r) * a.xt);
-        gr[r] = load_once<G, V>(g + (t0 + r) * a.gt);
+  Feed<X, V, R, kTensor> xf(ring, warp, lane);
+  Feed<G, V, R, kTensor> gf(ring + F::XB, warp, lane);
+  // Tile `n` into `stage`: all threads (their own tokens), or thread 0 (the whole tile).
+  auto load = [&](int stage, int n) {
+    if constexpr (kTensor) {
+      if (threadIdx.x == 0 && n * TILE < a.T) {
+        ptx::mbar_expect_tx(&sm.full[stage], SB);
+        const uint32_t dst = ptx::smem_u32(ring + stage * SB);
+        ptx::tma_load3(dst, &maps.x, col * 32 * V, n * TILE, b, &sm.full[stage]);
+        ptx::tma_load3(dst + F::XB, &maps.g, col * 32 * V, n * TILE, b, &sm.full[stage]);
       }
+    } else {
+      const int t0 = n * TILE + warp * R;
+      if (on) {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+          if (t0 + r < a.T) {
+            xf.fetch(stage * SB, r, x + (t0 + r) * a.xt);
+            gf.fetch(stage * SB, r, g + (t0 + r) * a.gt);
+          }
+      }
+      ptx::cp_async_commit();
     }
   };
-  const int steps = (a.N + S - 1) / S;
-  int t0 = rank * TILE + warp * R;
-  load(t0);
-  for (int step = 0; step < steps; ++step, t0 += S * TILE) {
-    const int par = step & 1;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < ST; ++i) ptx::mbar_init(&sm.full[i], 1);
+    for (int i = 0; i < 2; ++i) ptx::mbar_init(&sm.met[i], 1);
+    ptx::mbar_fence_init();
+  }
+  if (S > 1)
+    ptx::cluster_sync();
+  else
+    __syncthreads();
+  int n = rank;
+#pragma unroll
+  for (int i = 0; i < ST; ++i) load(i, n + i * S);
+  H* h = static_cast<H*>(a.h) + ((size_t)b * a.T + n * TILE + warp * R) * a.D + d;
+  const size_t hop = (size_t)S * TILE * a.D;
+  const int tiles = (a.T + TILE - 1) / TILE, steps = (tiles + S - 1) / S;
+  const float gm = a.gated ? -1.f : 0.f;
+  for (int step = 0; step < steps; ++step, n += S, h += hop) {
+    const int par = step & 1, stage = step % ST, t0 = n * TILE + warp * R;
+    const int rows = min(R, a.T - t0);           // of this warp; may be negative
     float e[R][V], u[R][V], A[V], P[V];
+    if constexpr (kTensor) {
+      if (n * TILE < a.T) wait_or_poison(&sm.full[stage], (step / ST) & 1, carry, V);
+    } else {
+      ptx::cp_async_wait<ST - 1>();
+    }
 #pragma unroll
     for (int i = 0; i < V; ++i) A[i] = 1.f, P[i] = 0.f;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      if (on && t0 + r < a.T) {
-        to_float<X, V>(xr[r], u[r]);
-        to_float<G, V>(gr[r], e[r]);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          e[r][i] = expf(e[r][i]);
-          if (a.gated) u[r][i] *= 1.f - e[r][i];
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) e[r][i] = 1.f, u[r][i] = 0.f;
+      for (int i = 0; i < V; ++i) e[r][i] = u[r][i] = 0.f;
+      if (kTensor ? n * TILE < a.T : on && r < rows) {
+        xf.take(stage * SB, r, u[r]);
+        gf.take(stage * SB, r, e[r]);
       }
-    }
-    load(t0 + S * TILE);
-#pragma unroll
-    for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int i = 0; i < V; ++i) {
+        e[r][i] = expf(e[r][i]);
+        u[r][i] *= fmaf(gm, e[r][i], 1.f);       // 1 or 1 - a
         P[i] = fmaf(e[r][i], P[i], u[r][i]);
         A[i] *= e[r][i];
       }
-    put_v<V>(&sm.warp[par][warp][0][lane * V], A);
-    put_v<V>(&sm.warp[par][warp][1][lane * V], P);
+    }
+    if constexpr (!kTensor) load(stage, n + ST * S);
+    float w[2 * V];
+    copy_v<V>(w, A);
+    copy_v<V>(w + V, P);
+    put_v<2 * V>(sm.warp[par][warp][lane], w);
     __syncthreads();
-    float pA[V], pH[V], tA[V], tH[V], s[V];      // before this warp; of the whole tile
+    if constexpr (kTensor) load(stage, n + ST * S);
+    float pA[V], pP[V], tA[V], tP[V], s[V];      // before this warp; of the whole tile
 #pragma unroll
-    for (int i = 0; i < V; ++i) tA[i] = 1.f, tH[i] = 0.f;
+    for (int i = 0; i < V; ++i) tA[i] = 1.f, tP[i] = 0.f;
 #pragma unroll
-    for (int w = 0; w < W; ++w) {
-      if (w == warp) {
+    for (int v = 0; v < W; ++v) {
+      if (v == warp) {
         copy_v<V>(pA, tA);
-        copy_v<V>(pH, tH);
+        copy_v<V>(pP, tP);
       }
-      float wA[V], wH[V];
-      get_v<V>(&sm.warp[par][w][0][lane * V], wA);
-      get_v<V>(&sm.warp[par][w][1][lane * V], wH);
+      get_v<2 * V>(sm.warp[par][v][lane], w);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        tH[i] = fmaf(wA[i], tH[i], wH[i]);
-        tA[i] *= wA[i];
+        tP[i] = fmaf(w[i], tP[i], w[V + i]);
+        tA[i] *= w[i];
       }
     }
-    cluster_carry<V>(sm, par, S, rank, warp, lane, tA, tH, carry, s);
-    if (a.ck && warp == 0 && on && t0 < a.T) {
+    cluster_carry<V, 2>(sm, step, S, rank, warp, lane, tA, tP, carry, s);
 #pragma unroll
-      for (int i = 0; i < V; ++i) a.ck[((size_t)b * a.N + t0 / CK) * a.D + d + i] = s[i];
-    }
+    for (int i = 0; i < V; ++i) s[i] = fmaf(pA[i], s[i], pP[i]);
+    if (a.ck && warp * R % CK == 0 && on && rows > 0)
+      put_v<V>(a.ck + ((size_t)b * a.N + t0 / CK) * a.D + d, s);
+    if (on) {
+      H* row = h;
 #pragma unroll
-    for (int i = 0; i < V; ++i) s[i] = fmaf(pA[i], s[i], pH[i]);
+      for (int r = 0; r < R; ++r, row += a.D) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) s[i] = fmaf(e[r][i], s[i], u[r][i]);
-      if (on && t0 + r < a.T) store_f<H, V>(h + (size_t)(t0 + r) * a.D, s);
+        for (int i = 0; i < V; ++i) s[i] = fmaf(e[r][i], s[i], u[r][i]);
+        if (r < rows) store_f<H, V>(row, s);
+      }
     }
   }
-  if (a.sT && rank == 0 && warp == 0 && on) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) a.sT[(size_t)b * a.D + d + i] = carry[i];
-  }
+  if (a.sT && rank == 0 && warp == 0 && on) put_v<V>(a.sT + (size_t)b * a.D + d, carry);
+  if (S > 1) ptx::cluster_sync();                // no block leaves while another may send to it
 }
 
 // The same walk from the last tile back. What travels is mu_t = a_t l_t, the gradient that
 // reaches h_{t-1}: a stretch maps the mu after it to A mu + M, with the same A. The states
 // inside a tile come from its checkpoint and the warps' forward pairs.
-template <typename X, typename G, typename H, int V>
-__global__ void __launch_bounds__(W * 32, 2) scan_bwd_kernel(ScanArgs a, int S) {
-  __shared__ ScanShared<V> sm;
+template <typename X, typename G, typename H, int V, bool kTensor>
+struct Bwd {
+  static constexpr int R = CK / W, TILE = CK, ST = kStages<X, G, H, kTensor>;
+  static constexpr int XB = Feed<X, V, R, kTensor>::kBytes, GB = Feed<G, V, R, kTensor>::kBytes;
+  static constexpr int DB = Feed<H, V, R, kTensor>::kBytes;
+  static constexpr int SB = XB + GB + DB, SMEM = ST * SB;
+};
+
+template <typename X, typename G, typename H, int V, bool kTensor>
+__global__ void __launch_bounds__(W * 32, 2)
+    scan_bwd_kernel(const __grid_constant__ ScanMaps maps, ScanArgs a, int S) {
+  using F = Bwd<X, G, H, V, kTensor>;
+  constexpr int R = F::R, TILE = F::TILE, ST = F::ST, SB = F::SB;
+  extern __shared__ __align__(128) char ring[];
+  __shared__ ScanShared<V, 4> sm;                // A, P, M of each warp (and a gap)
   const int rank = blockIdx.x % S, col = blockIdx.x / S, b = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int d = (col * 32 + lane) * V;
@@ -242,79 +367,109 @@ __global__ void __launch_bounds__(W * 32, 2) scan_bwd_kernel(ScanArgs a, int S) 
   const G* g = static_cast<const G*>(a.g) + b * a.gb + d;
   const H* dh = static_cast<const H*>(a.dh) + b * a.db + d;
   const float* ck = a.ck + (size_t)b * a.N * a.D + d;
-  X* dx = static_cast<X*>(a.dx) + (size_t)b * a.T * a.D + d;
-  G* dg = static_cast<G*>(a.dg) + (size_t)b * a.T * a.D + d;
-  float carry[V];
+  float carry[V], cr[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) carry[i] = on && a.s0 ? a.s0[(size_t)b * a.D + d + i] : 0.f;
 
-  Raw<X, V> xr[R];
-  Raw<G, V> gr[R];
-  Raw<H, V> dr[R];
-  float cr[V];
-  auto load = [&](int n) {
-    if (!on || n < 0) return;
-#pragma unroll
-    for (int i = 0; i < V; ++i) cr[i] = ck[(size_t)n * a.D + i];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int t = n * TILE + warp * R + r;
-      if (t < a.T) {
-        xr[r] = load_once<X, V>(x + t * a.xt);
-        gr[r] = load_once<G, V>(g + t * a.gt);
-        dr[r] = load_once<H, V>(dh + t * a.dt);
+  Feed<X, V, R, kTensor> xf(ring, warp, lane);
+  Feed<G, V, R, kTensor> gf(ring + F::XB, warp, lane);
+  Feed<H, V, R, kTensor> df(ring + F::XB + F::GB, warp, lane);
+  auto load = [&](int stage, int n) {
+    if constexpr (kTensor) {
+      if (threadIdx.x == 0 && n >= 0) {
+        ptx::mbar_expect_tx(&sm.full[stage], SB);
+        const uint32_t dst = ptx::smem_u32(ring + stage * SB);
+        ptx::tma_load3(dst, &maps.x, col * 32 * V, n * TILE, b, &sm.full[stage]);
+        ptx::tma_load3(dst + F::XB, &maps.g, col * 32 * V, n * TILE, b, &sm.full[stage]);
+        ptx::tma_load3(dst + F::XB + F::GB, &maps.dh, col * 32 * V, n * TILE, b, &sm.full[stage]);
       }
+    } else {
+      const int t0 = n * TILE + warp * R;
+      if (on && n >= 0) {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+          if (t0 + r < a.T) {
+            xf.fetch(stage * SB, r, x + (t0 + r) * a.xt);
+            gf.fetch(stage * SB, r, g + (t0 + r) * a.gt);
+            df.fetch(stage * SB, r, dh + (t0 + r) * a.dt);
+          }
+      }
+      ptx::cp_async_commit();
     }
   };
-  const int steps = (a.N + S - 1) / S;
-  int n = a.N - 1 - rank;
-  load(n);
-  for (int step = 0; step < steps; ++step, n -= S) {
-    const int par = step & 1, t0 = n * TILE + warp * R;
-    float e[R][V], u[R][V], l[R][V], hs[V], A[V], P[V], M[V];
+  auto load_ck = [&](int n) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) A[i] = 1.f, P[i] = M[i] = 0.f, hs[i] = cr[i];
+    for (int i = 0; i < V; ++i) cr[i] = 0.f;
+    if (on && n >= 0) load_f<float, V>(ck + (size_t)n * a.D, cr);
+  };
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < ST; ++i) ptx::mbar_init(&sm.full[i], 1);
+    for (int i = 0; i < 2; ++i) ptx::mbar_init(&sm.met[i], 1);
+    ptx::mbar_fence_init();
+  }
+  if (S > 1)
+    ptx::cluster_sync();
+  else
+    __syncthreads();
+  int n = a.N - 1 - rank;
+#pragma unroll
+  for (int i = 0; i < ST; ++i) load(i, n - i * S);
+  load_ck(n);
+  const int steps = (a.N + S - 1) / S;
+  const float gm = a.gated ? -1.f : 0.f;
+  for (int step = 0; step < steps; ++step, n -= S) {
+    const int par = step & 1, stage = step % ST, t0 = n * TILE + warp * R;
+    const int rows = n < 0 ? 0 : min(R, a.T - t0);
+    float e[R][V], u[R][V], l[R][V], hs[V], A[V], P[V], M[V];
+    if constexpr (kTensor) {
+      if (n >= 0) wait_or_poison(&sm.full[stage], (step / ST) & 1, carry, V);
+    } else {
+      ptx::cp_async_wait<ST - 1>();
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) A[i] = 1.f, P[i] = M[i] = 0.f;
+    copy_v<V>(hs, cr);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      if (on && n >= 0 && t0 + r < a.T) {
-        to_float<X, V>(xr[r], u[r]);
-        to_float<G, V>(gr[r], e[r]);
-        to_float<H, V>(dr[r], l[r]);
 #pragma unroll
-        for (int i = 0; i < V; ++i) e[r][i] = expf(e[r][i]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) e[r][i] = 1.f, u[r][i] = l[r][i] = 0.f;
+      for (int i = 0; i < V; ++i) e[r][i] = u[r][i] = l[r][i] = 0.f;
+      if (kTensor ? n >= 0 : on && r < rows) {
+        xf.take(stage * SB, r, u[r]);
+        gf.take(stage * SB, r, e[r]);
+        df.take(stage * SB, r, l[r]);
       }
-    }
-    load(n - S);
-#pragma unroll
-    for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        P[i] = fmaf(e[r][i], P[i], a.gated ? (1.f - e[r][i]) * u[r][i] : u[r][i]);
+        e[r][i] = expf(e[r][i]);
+        P[i] = fmaf(e[r][i], P[i], u[r][i] * fmaf(gm, e[r][i], 1.f));
         A[i] *= e[r][i];
       }
+    }
+    if constexpr (!kTensor) load(stage, n - ST * S);
+    load_ck(n - S);
 #pragma unroll
     for (int r = R - 1; r >= 0; --r)
 #pragma unroll
       for (int i = 0; i < V; ++i) M[i] = e[r][i] * (l[r][i] + M[i]);
-    put_v<V>(&sm.warp[par][warp][0][lane * V], A);
-    put_v<V>(&sm.warp[par][warp][1][lane * V], P);
-    put_v<V>(&sm.warp[par][warp][2][lane * V], M);
+    float w[2 * V];
+    copy_v<V>(w, A);
+    copy_v<V>(w + V, P);
+    put_v<2 * V>(sm.warp[par][warp][lane], w);
+    put_v<V>(sm.warp[par][warp][lane] + 2 * V, M);
     __syncthreads();
+    if constexpr (kTensor) load(stage, n - ST * S);
     float pA[V], pM[V], tA[V], tM[V], mu[V];     // after this warp; of the whole tile
 #pragma unroll
     for (int i = 0; i < V; ++i) tA[i] = 1.f, tM[i] = 0.f;
 #pragma unroll
-    for (int w = W - 1; w >= 0; --w) {
-      if (w == warp) {
+    for (int v = W - 1; v >= 0; --v) {
+      if (v == warp) {
         copy_v<V>(pA, tA);
         copy_v<V>(pM, tM);
       }
       float wA[V], wM[V];
-      get_v<V>(&sm.warp[par][w][0][lane * V], wA);
-      get_v<V>(&sm.warp[par][w][2][lane * V], wM);
+      get_v<V>(sm.warp[par][v][lane], wA);
+      get_v<V>(sm.warp[par][v][lane] + 2 * V, wM);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         tM[i] = fmaf(wA[i], tM[i], wM[i]);
@@ -322,15 +477,13 @@ __global__ void __launch_bounds__(W * 32, 2) scan_bwd_kernel(ScanArgs a, int S) 
       }
     }
 #pragma unroll
-    for (int w = 0; w < W - 1; ++w)
-      if (w < warp) {
-        float wA[V], wH[V];
-        get_v<V>(&sm.warp[par][w][0][lane * V], wA);
-        get_v<V>(&sm.warp[par][w][1][lane * V], wH);
+    for (int v = 0; v < W - 1; ++v)
+      if (v < warp) {
+        get_v<2 * V>(sm.warp[par][v][lane], w);
 #pragma unroll
-        for (int i = 0; i < V; ++i) hs[i] = fmaf(wA[i], hs[i], wH[i]);
+        for (int i = 0; i < V; ++i) hs[i] = fmaf(w[i], hs[i], w[V + i]);
       }
-    cluster_carry<V>(sm, par, S, rank, warp, lane, tA, tM, carry, mu);
+    cluster_carry<V, 4>(sm, step, S, rank, warp, lane, tA, tM, carry, mu);
 #pragma unroll
     for (int i = 0; i < V; ++i) mu[i] = fmaf(pA[i], mu[i], pM[i]);
     // u becomes what dg multiplies: h_{t-1}, minus x_t when gated.
@@ -339,29 +492,28 @@ __global__ void __launch_bounds__(W * 32, 2) scan_bwd_kernel(ScanArgs a, int S) 
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const float past = a.gated ? hs[i] - u[r][i] : hs[i];
-        hs[i] = fmaf(e[r][i], hs[i], a.gated ? (1.f - e[r][i]) * u[r][i] : u[r][i]);
+        hs[i] = fmaf(e[r][i], hs[i], u[r][i] * fmaf(gm, e[r][i], 1.f));
         u[r][i] = past;
       }
+    const size_t row0 = ((size_t)b * a.T + max(t0, 0)) * a.D + d;
 #pragma unroll
     for (int r = R - 1; r >= 0; --r) {
       float ox[V], og[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const float lr = l[r][i] + mu[i];
-        ox[i] = a.gated ? lr * (1.f - e[r][i]) : lr;
+        ox[i] = lr * fmaf(gm, e[r][i], 1.f);
         mu[i] = e[r][i] * lr;
         og[i] = mu[i] * u[r][i];
       }
-      if (on && n >= 0 && t0 + r < a.T) {
-        store_f<X, V>(dx + (size_t)(t0 + r) * a.D, ox);
-        store_f<G, V>(dg + (size_t)(t0 + r) * a.D, og);
+      if (on && r < rows) {
+        store_f<X, V>(static_cast<X*>(a.dx) + row0 + (size_t)r * a.D, ox);
+        store_f<G, V>(static_cast<G*>(a.dg) + row0 + (size_t)r * a.D, og);
       }
     }
   }
-  if (a.sT && rank == 0 && warp == 0 && on) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) a.sT[(size_t)b * a.D + d + i] = carry[i];
-  }
+  if (a.sT && rank == 0 && warp == 0 && on) put_v<V>(a.sT + (size_t)b * a.D + d, carry);
+  if (S > 1) ptx::cluster_sync();                // no block leaves while another may send to it
 }
 
 gdr_status check(const gdr_scan_dims* d) {
@@ -407,18 +559,115 @@ gdr_status copy_state(float* out, const float* in, size_t n, cudaStream_t s) {
 // Tokens up to which one thread runs a channel's tokens by itself.
 constexpr int kSerial = 8;
 
-// Blocks along the sequence for a kernel: as many as keep every cluster resident at once.
-int cluster_size(const void* fn, int resident, const ScanArgs& a, int V) {
-  const long long cols = (a.D + 32 * V - 1) / (32 * V) * (long long)a.B;
-  long long s = 152LL * resident / (cols > 0 ? cols : 1);
-  if (s > MAXS) s = MAXS;
-  if (s > a.N) s = a.N;
-  (void)fn;
-  return s < 1 ? 1 : (int)s;
+// A view [B, T, D] as a tensor map with boxes of `rows` tokens x `cols` channels.
+bool tmap_view(CUtensorMap* m, const void* p, int dtype, const ScanArgs& a, int64_t sb, int64_t st,
+               int cols, int rows) {
+  const int es = (int)dtype_size(dtype);
+  const cuuint64_t row = (cuuint64_t)a.D * es;   // of a dimension that is never stepped along
+  const cuuint64_t dims[3] = {(cuuint64_t)a.D, (cuuint64_t)a.T, (cuuint64_t)a.B};
+  const cuuint64_t strides[2] = {a.T == 1 ? row : (cuuint64_t)st * es,
+                                 a.B == 1 ? row : (cuuint64_t)sb * es};
+  const cuuint32_t box[3] = {(cuuint32_t)cols, (cuuint32_t)rows, 1};
+  return fast::tmap_encode(
+      m, dtype == GDR_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3,
+      p, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
-template <bool kBwd, int V>
-gdr_status launch(const gdr_scan_dims* d, const ScanArgs& a, cudaStream_t s) {
+// Whether a view can be copied by tensor maps: 16-byte aligned rows that differ.
+bool tensor_ok(const void* p, int dtype, const ScanArgs& a, int64_t sb, int64_t st) {
+  const int64_t es = (int64_t)dtype_size(dtype);
+  return a.D * es % 16 == 0 && is_aligned(p, 16) &&
+         (a.T == 1 || (st * es % 16 == 0 && st > 0)) && (a.B == 1 || (sb * es % 16 == 0 && sb > 0));
+}
+
+// Clusters of s blocks that the device holds at once, s = 1 .. MAXS, into `active`; asked of
+// the runtime once per kernel (F names it) and device. False on a CUDA error.
+template <typename F, typename Fn>
+bool residency(Fn fn, int* active) {
+  constexpr int kDevices = 16;
+  static std::atomic<int> table[kDevices][MAXS + 1];   // [0]: filled
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= kDevices) return false;
+  std::atomic<int>* row = table[dev];
+  if (!row[0].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, F::SMEM) !=
+        cudaSuccess) {
+      (void)cudaGetLastError();
+      return false;
+    }
+    for (int s = 1; s <= MAXS; ++s) {
+      cudaLaunchAttribute at[1];
+      at[0].id = cudaLaunchAttributeClusterDimension;
+      at[0].val.clusterDim.x = s;
+      at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(s);
+      cfg.blockDim = dim3(W * 32);
+      cfg.dynamicSmemBytes = F::SMEM;
+      cfg.attrs = at;
+      cfg.numAttrs = 1;
+      int n = 0;
+      if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess) {
+        (void)cudaGetLastError();
+        n = 0;
+      }
+      row[s].store(n, std::memory_order_relaxed);
+    }
+    row[0].store(1, std::memory_order_release);
+  }
+  for (int s = 1; s <= MAXS; ++s) active[s] = row[s].load(std::memory_order_relaxed);
+  return active[1] > 0;
+}
+
+// Blocks per cluster: the fewest steps in all, over the waves that the clusters take.
+int cluster_size(const int* active, long long clusters, int tiles) {
+  int best = 1;
+  long long least = -1;
+  for (int s = 1; s <= MAXS && s <= tiles; ++s) {
+    if (active[s] <= 0) continue;
+    const long long cost = (clusters + active[s] - 1) / active[s] * ((tiles + s - 1) / s);
+    if (least < 0 || cost < least) least = cost, best = s;
+  }
+  return best;
+}
+
+template <typename X, typename G, typename H, int V, bool kTensor, bool kBwd>
+gdr_status launch_walk(const gdr_scan_dims* d, const ScanArgs& a, cudaStream_t s) {
+  using F = std::conditional_t<kBwd, Bwd<X, G, H, V, kTensor>, Fwd<X, G, H, V, kTensor>>;
+  auto fn = kBwd ? scan_bwd_kernel<X, G, H, V, kTensor> : scan_kernel<X, G, H, V, kTensor>;
+  int active[MAXS + 1];
+  if (!residency<F>(fn, active)) return GDR_ERR_CUDA;
+  const long long cols = (a.D + 32LL * V - 1) / (32 * V);
+  const int S = cluster_size(active, cols * a.B, (a.T + F::TILE - 1) / F::TILE);
+  ScanMaps m;
+  if constexpr (kTensor) {
+    if (!tmap_view(&m.x, a.x, d->x_dtype, a, a.xb, a.xt, 32 * V, F::TILE) ||
+        !tmap_view(&m.g, a.g, d->g_dtype, a, a.gb, a.gt, 32 * V, F::TILE) ||
+        (kBwd && !tmap_view(&m.dh, a.dh, d->h_dtype, a, a.db, a.dt, 32 * V, F::TILE)))
+      return GDR_ERR_CUDA;
+  }
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = S;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(cols * S), a.B);
+  cfg.blockDim = dim3(W * 32);
+  cfg.dynamicSmemBytes = F::SMEM;
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, fn, m, a, S) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return GDR_ERR_CUDA;
+  }
+  return GDR_OK;
+}
+
+enum Path { kPlain, kPairs, kTensorMaps };       // one channel; two; tiles by tensor maps
+
+template <bool kBwd>
+gdr_status launch(const gdr_scan_dims* d, const ScanArgs& a, Path path, cudaStream_t s) {
   return with_dtype(d->x_dtype, [&](auto* x) {
     return with_dtype(d->g_dtype, [&](auto* g) {
       return with_dtype(d->h_dtype, [&](auto* h) {
@@ -427,37 +676,30 @@ gdr_status launch(const gdr_scan_dims* d, const ScanArgs& a, cudaStream_t s) {
         using H = std::remove_pointer_t<decltype(h)>;
         if constexpr (!kBwd) {
           if (a.T <= kSerial) {
+            const int V = path == kPlain ? 1 : 2;
             const dim3 grid((a.D + 128 * V - 1) / (128 * V), a.B);
-            scan_serial_kernel<X, G, H, V><<<grid, 128, 0, s>>>(a);
+            if (V == 1)
+              scan_serial_kernel<X, G, H, 1><<<grid, 128, 0, s>>>(a);
+            else
+              scan_serial_kernel<X, G, H, 2><<<grid, 128, 0, s>>>(a);
             return launched();
           }
         }
-        auto fn = kBwd ? scan_bwd_kernel<X, G, H, V> : scan_kernel<X, G, H, V>;
-        const int S = cluster_size((const void*)fn, kBwd ? 2 : 3, a, V);
-        cudaLaunchAttribute at[1];
-        at[0].id = cudaLaunchAttributeClusterDimension;
-        at[0].val.clusterDim.x = S;
-        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((a.D + 32 * V - 1) / (32 * V) * S, a.B);
-        cfg.blockDim = dim3(W * 32);
-        cfg.stream = s;
-        cfg.attrs = at;
-        cfg.numAttrs = 1;
-        if (S > 8 && cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
-                         cudaSuccess) {
-          (void)cudaGetLastError();
-          return GDR_ERR_CUDA;
-        }
-        const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, a, S);
-        if (e != cudaSuccess) {
-          (void)cudaGetLastError();
-          return GDR_ERR_CUDA;
-        }
-        return GDR_OK;
+        return path == kTensorMaps ? launch_walk<X, G, H, 2, true, kBwd>(d, a, s)
+                                   : launch_walk<X, G, H, 1, false, kBwd>(d, a, s);
       });
     });
   });
+}
+
+Path choose(const gdr_scan_dims* d, const ScanArgs& a) {
+  if (tensor_ok(a.x, d->x_dtype, a, a.xb, a.xt) && tensor_ok(a.g, d->g_dtype, a, a.gb, a.gt) &&
+      (!a.dh || tensor_ok(a.dh, d->h_dtype, a, a.db, a.dt)))
+    return kTensorMaps;
+  return a.D % 2 == 0 && vec_ok(a.x, d->x_dtype, a.xb, a.xt, 2) &&
+                 vec_ok(a.g, d->g_dtype, a.gb, a.gt, 2)
+             ? kPairs
+             : kPlain;
 }
 
 }  // namespace
@@ -489,9 +731,7 @@ gdr_status gdr_linear_scan_fwd(const void* x, const void* g, const float* initia
   if (!work) return copy_state(final_state, initial_state, (size_t)dims->B * dims->D, s);
   ScanArgs a = make_args(dims);
   a.x = x; a.g = g; a.s0 = initial_state; a.h = h; a.sT = final_state; a.ck = checkpoints;
-  const bool vec = dims->D % 2 == 0 && vec_ok(x, dims->x_dtype, a.xb, a.xt, 2) &&
-                   vec_ok(g, dims->g_dtype, a.gb, a.gt, 2);
-  return vec ? launch<false, 2>(dims, a, s) : launch<false, 1>(dims, a, s);
+  return launch<false>(dims, a, choose(dims, a), s);
 }
 
 gdr_status gdr_linear_scan_bwd(const void* dh, const void* x, const void* g,
@@ -512,10 +752,7 @@ gdr_status gdr_linear_scan_bwd(const void* dh, const void* x, const void* g,
   ScanArgs a = make_args(dims);
   a.x = x; a.g = g; a.dh = dh; a.s0 = d_final_state; a.sT = d_initial_state;
   a.dx = dx; a.dg = dg; a.ck = const_cast<float*>(checkpoints);
-  const bool vec = dims->D % 2 == 0 && vec_ok(x, dims->x_dtype, a.xb, a.xt, 2) &&
-                   vec_ok(g, dims->g_dtype, a.gb, a.gt, 2) &&
-                   vec_ok(dh, dims->h_dtype, a.db, a.dt, 2);
-  return vec ? launch<true, 2>(dims, a, s) : launch<true, 1>(dims, a, s);
+  return launch<true>(dims, a, choose(dims, a), s);
 }
 
 }  // extern "C"
