@@ -78,9 +78,10 @@ constexpr int kRows = V == 1 || sizeof(X) + sizeof(G) <= 6 ? 16 : 8;
 // Pairs (or triples) of the warps and pairs of the blocks, double-buffered by step: a buffer
 // is written again only after the block barrier of the step between, and after every block
 // has sent that step's pair, which it does once it has read this one.
-template <int V, int K>
+template <int V, bool kBwd>
 struct alignas(16) ScanShared {
-  float warp[2][W][32][K * V];
+  float warp[2][W][32][2 * V];
+  float back[kBwd ? 2 : 1][kBwd ? W : 1][32][V];
   float block[2][MAXS][32][2 * V];
   uint64_t full[4];                  // ring stages (tensor copies)
   uint64_t met[2];                   // the blocks' pairs
@@ -124,8 +125,8 @@ __device__ __forceinline__ bool met_wait(uint64_t* bar, uint32_t parity) {
 
 // The blocks' pairs of a step applied to `carry` (the state before the step): `mine` becomes
 // the state before this block's tile, carry the state after the step.
-template <int V, int K>
-__device__ __forceinline__ void cluster_carry(ScanShared<V, K>& sm, int step, int S, int rank,
+template <int V, bool kBwd>
+__device__ __forceinline__ void cluster_carry(ScanShared<V, kBwd>& sm, int step, int S, int rank,
                                               int warp, int lane, const float* tA,
                                               const float* tP, float* carry, float* mine) {
   if (S == 1) {
@@ -156,15 +157,13 @@ __device__ __forceinline__ void cluster_carry(ScanShared<V, K>& sm, int step, in
 #pragma unroll
     for (int i = 0; i < V; ++i) carry[i] = NAN;
   }
-#pragma unroll
-  for (int q = 0; q < MAXS; ++q) {
+#pragma unroll 2
+  for (int q = 0; q < S; ++q) {
     if (q == rank) copy_v<V>(mine, carry);
-    if (q < S) {
-      float m[2 * V];
-      get_v<2 * V>(sm.block[par][q][lane], m);
+    float m[2 * V];
+    get_v<2 * V>(sm.block[par][q][lane], m);
 #pragma unroll
-      for (int i = 0; i < V; ++i) carry[i] = fmaf(m[i], carry[i], m[V + i]);
-    }
+    for (int i = 0; i < V; ++i) carry[i] = fmaf(m[i], carry[i], m[V + i]);
   }
 }
 
@@ -221,7 +220,7 @@ __global__ void __launch_bounds__(W * 32, 2)
   using F = Fwd<X, G, H, V, kTensor>;
   constexpr int R = F::R, TILE = F::TILE, ST = F::ST, SB = F::SB;
   extern __shared__ __align__(128) char ring[];
-  __shared__ ScanShared<V, 2> sm;
+  __shared__ ScanShared<V, false> sm;
   const int rank = blockIdx.x % S, col = blockIdx.x / S, b = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int d = (col * 32 + lane) * V;
@@ -322,7 +321,7 @@ __global__ void __launch_bounds__(W * 32, 2)
         tA[i] *= w[i];
       }
     }
-    cluster_carry<V, 2>(sm, step, S, rank, warp, lane, tA, tP, carry, s);
+    cluster_carry<V, false>(sm, step, S, rank, warp, lane, tA, tP, carry, s);
 #pragma unroll
     for (int i = 0; i < V; ++i) s[i] = fmaf(pA[i], s[i], pP[i]);
     if (a.ck && warp * R % CK == 0 && on && rows > 0)
@@ -358,7 +357,7 @@ __global__ void __launch_bounds__(W * 32, 2)
   using F = Bwd<X, G, H, V, kTensor>;
   constexpr int R = F::R, TILE = F::TILE, ST = F::ST, SB = F::SB;
   extern __shared__ __align__(128) char ring[];
-  __shared__ ScanShared<V, 4> sm;                // A, P, M of each warp (and a gap)
+  __shared__ ScanShared<V, true> sm;
   const int rank = blockIdx.x % S, col = blockIdx.x / S, b = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int d = (col * 32 + lane) * V;
@@ -455,7 +454,7 @@ __global__ void __launch_bounds__(W * 32, 2)
     copy_v<V>(w, A);
     copy_v<V>(w + V, P);
     put_v<2 * V>(sm.warp[par][warp][lane], w);
-    put_v<V>(sm.warp[par][warp][lane] + 2 * V, M);
+    put_v<V>(sm.back[par][warp][lane], M);
     __syncthreads();
     if constexpr (kTensor) load(stage, n - ST * S);
     float pA[V], pM[V], tA[V], tM[V], mu[V];     // after this warp; of the whole tile
@@ -469,7 +468,7 @@ __global__ void __launch_bounds__(W * 32, 2)
       }
       float wA[V], wM[V];
       get_v<V>(sm.warp[par][v][lane], wA);
-      get_v<V>(sm.warp[par][v][lane] + 2 * V, wM);
+      get_v<V>(sm.back[par][v][lane], wM);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         tM[i] = fmaf(wA[i], tM[i], wM[i]);
@@ -483,7 +482,7 @@ __global__ void __launch_bounds__(W * 32, 2)
 #pragma unroll
         for (int i = 0; i < V; ++i) hs[i] = fmaf(w[i], hs[i], w[V + i]);
       }
-    cluster_carry<V, 4>(sm, step, S, rank, warp, lane, tA, tM, carry, mu);
+    cluster_carry<V, true>(sm, step, S, rank, warp, lane, tA, tM, carry, mu);
 #pragma unroll
     for (int i = 0; i < V; ++i) mu[i] = fmaf(pA[i], mu[i], pM[i]);
     // u becomes what dg multiplies: h_{t-1}, minus x_t when gated.
