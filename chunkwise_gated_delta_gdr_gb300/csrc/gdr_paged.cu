@@ -17,6 +17,7 @@
 #include <type_traits>
 
 #include "gdr_ops.cuh"
+#include "gdr_ptx.cuh"
 
 namespace gdr {
 namespace ops {
@@ -33,8 +34,10 @@ struct AttnArgs {
   void* out;
   float* lse;                     // may be null
   float *part_o, *part_ml;        // [blocks][2][GMAX][D], [blocks][2][GMAX][2]
+  int4* cut;                      // [blocks]: the item that block c began and left unfinished
   int B, HQ, HK, D, G, GH, groups;  // G = HQ / HK; GH query heads per item, groups per kv head
-  int page, num_pages, max_pages, window, whole, blocks, out_bf16, q_bf16;
+  int page, shift;                // shift: log2(page) if page is a power of two, else -1
+  int num_pages, max_pages, window, whole, blocks, out_bf16, q_bf16;
   float scale2;                   // scale log2(e)
   int64_t qb, qh, pp, pt, ph;
   long long cap;                  // max_pages * page
@@ -137,8 +140,10 @@ __device__ __forceinline__ void empty_rows(const AttnArgs& a) {
   }
 }
 
-// This block's stretch of the line: its first place and its number of tiles (0: none).
-__device__ __forceinline__ long long stretch(const AttnArgs& a, int lane, Place* p) {
+// This block's stretch of the line: its first place and its number of tiles (0: none);
+// *per: tiles per block.
+__device__ __forceinline__ long long stretch(const AttnArgs& a, int lane, Place* p,
+                                             long long* per_block) {
   if (a.whole) {                   // one block per item
     p->b = blockIdx.x / (a.HK * a.groups);
     p->item = blockIdx.x - p->b * (a.HK * a.groups);
@@ -146,16 +151,25 @@ __device__ __forceinline__ long long stretch(const AttnArgs& a, int lane, Place*
     p->s = span_of(a, p->b);
     return p->s.tiles();
   }
+  if (threadIdx.x == 0) a.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
   const long long total = total_tiles(a, lane), per = (total + a.blocks - 1) / a.blocks;
   const long long first = blockIdx.x * per, last = min(total, first + per);
   if (first >= last) return 0;
+  *per_block = per;
   *p = locate(a, first, lane);
   return last - first;
 }
 
+// Thread 0 of a block that leaves an item it began: `rest` of its tiles go to later blocks.
+__device__ __forceinline__ void leave_cut(const AttnArgs& a, const Place& p, int rest,
+                                          long long per) {
+  if (threadIdx.x == 0)
+    a.cut[blockIdx.x] = make_int4(p.b, p.item, 1 + (int)((rest + per - 1) / per), 0);
+}
+
 // Element offset of key j of sequence b (kv head 0), or -1 for a bad table entry.
 __device__ __forceinline__ int64_t key_row(const AttnArgs& a, int b, int j) {
-  const int pj = j / a.page;
+  const int pj = a.shift >= 0 ? j >> a.shift : j / a.page;
   const int32_t pg = a.table[(size_t)b * a.max_pages + pj];
   if (pg < 0 || pg >= a.num_pages) return -1;
   return pg * a.pp + (j - pj * a.page) * a.pt;
@@ -182,10 +196,11 @@ template <typename T, int NC, int GH>
 __global__ void __launch_bounds__(WARPS * 32) paged_any_kernel(AttnArgs a, int vec) {
   constexpr int DP = NC * 32;
   __shared__ float so[WARPS][GH][DP], sml[WARPS][GH][2];
+  asm volatile("griddepcontrol.launch_dependents;");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane & 7, oct = lane >> 3;
   empty_rows(a);
   Place p;
-  long long left = stretch(a, lane, &p);
+  long long per = 1, left = stretch(a, lane, &p, &per);
   while (left > 0) {
     const int tiles = p.s.tiles();
     const int t1 = (int)min((long long)tiles, p.tile + left);
@@ -281,6 +296,7 @@ __global__ void __launch_bounds__(WARPS * 32) paged_any_kernel(AttnArgs a, int v
     __syncthreads();
     const bool done = p.tile == 0 && t1 == tiles;
     const size_t slot = (size_t)blockIdx.x * 2 + (p.tile == 0 ? 1 : 0);
+    if (!done && p.tile == 0) leave_cut(a, p, tiles - t1, per);
     for (int e = threadIdx.x; e < heads * a.D; e += WARPS * 32) {
       const int g = e / a.D, d = e - g * a.D;
       float mm = -INFINITY, ll = 0.f, oo = 0.f;
@@ -308,60 +324,325 @@ __global__ void __launch_bounds__(WARPS * 32) paged_any_kernel(AttnArgs a, int v
   }
 }
 
-// ------------------------------------------------------------ items cut by block boundaries
-// Block c: the item that the boundary after stretch c cuts, if that is the item's first one.
-__global__ void __launch_bounds__(128) paged_join_kernel(AttnArgs a) {
-  const int lane = threadIdx.x & 31;
-  const long long total = total_tiles(a, lane), per = (total + a.blocks - 1) / a.blocks;
-  const long long at = (blockIdx.x + 1) * per;
-  if (at >= total) return;
-  const Place p = locate(a, at, lane);
-  const long long first = at - p.tile;
-  if (p.tile == 0 || first / per != blockIdx.x) return;
-  const int c1 = (int)((first + p.s.tiles() - 1) / per);
-  const int hk = p.item / a.groups, g0 = (p.item - hk * a.groups) * a.GH;
-  const int heads = min(a.GH, a.G - g0);
-  for (int e = threadIdx.x; e < heads * a.D; e += 128) {
-    const int g = e / a.D, d = e - g * a.D;
-    float m = -INFINITY, l = 0.f, o = 0.f;
-    for (int c = blockIdx.x; c <= c1; ++c) {
-      const size_t s = ((size_t)c * 2 + (c == (int)blockIdx.x)) * GMAX + g;
-      const float m1 = a.part_ml[s * 2], l1 = a.part_ml[s * 2 + 1], o1 = a.part_o[s * a.D + d];
-      const float mm = fmaxf(m, m1);
-      const float f = m == -INFINITY ? 1.f : exp2f(m - mm);
-      const float f1 = m1 == -INFINITY ? 1.f : exp2f(m1 - mm);
-      l = l * f + l1 * f1;
-      o = o * f + o1 * f1;
-      m = mm;
+// ------------------------------------------------------------ bf16 on the tensor cores
+// The 16 rows of an m16n8k16 product are the query heads that share a kv head. A warp takes
+// 16 keys of a tile at a time and needs nobody else for them: it copies its own K and V rows
+// (16-byte pieces, gathered by page) into its own ring of ST slots, forms S = Q K^T, the
+// softmax weights and O += P V from there with its own running maximum and sums, and the
+// four warps meet once per item. K and V pass through shared memory once; rows are padded
+// to an odd number of 16-byte pieces, which keeps the matrix loads free of bank conflicts
+// for every D.
+template <int D>
+struct Mma {
+  static constexpr int C = D / 8, RS = (C | 1) * 16;     // pieces per row, bytes per padded row
+  static constexpr int SLOT = 2 * 16 * RS, ST = 3, KS = D / 16;
+  static constexpr int SMEM = WARPS * ST * SLOT;
+  static constexpr int OCC = D <= 64 ? 4 : D <= 128 ? 2 : 1;
+  static constexpr int OS = D + 8;                       // floats per row of a merged slot
+  static_assert(16 * OS * 4 <= SLOT, "a slot holds a warp's sums");
+};
+
+template <int D>
+__global__ void __launch_bounds__(WARPS * 32, Mma<D>::OCC) paged_mma_kernel(AttnArgs a) {
+  using M = Mma<D>;
+  constexpr int C = M::C, RS = M::RS, ST = M::ST, KS = M::KS;
+  extern __shared__ __align__(16) char ring[];
+  __shared__ float sml[WARPS][16][2];
+  __shared__ int sbad[WARPS][ST];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = lane >> 2, quad = lane & 3;
+  asm volatile("griddepcontrol.launch_dependents;");
+  empty_rows(a);
+  Place pc;                                      // the tile being computed
+  long long per = 1, left = stretch(a, lane, &pc, &per);
+  if (left <= 0) return;
+  Place pi = pc;                                 // the tile being copied
+  long long to_copy = left;
+  char* slots = ring + warp * ST * M::SLOT;
+  const uint32_t slots_u = ptx::smem_u32(slots);
+  const bf16* kc = static_cast<const bf16*>(a.kc);
+  const bf16* vc = static_cast<const bf16*>(a.vc);
+
+  // Where this lane's key of the tile at pi starts (-1: bad page, -2: no such key).
+  auto find = [&]() -> int64_t {
+    const int j = pi.s.lo + pi.tile * TILE + warp * 16 + (lane & 15);
+    if (j >= pi.s.n) return -2;
+    const int64_t r = key_row(a, pi.b, j);
+    return r < 0 ? -1 : r + (pi.item / a.groups) * a.ph;
+  };
+  int64_t off = find();
+  auto copy = [&](int slot) {
+    if (to_copy > 0) {
+      const unsigned bad = __ballot_sync(~0u, off == -1);
+      if (lane == 0) sbad[warp][slot] = bad != 0;
+      const uint32_t kd = slots_u + slot * M::SLOT, vd = kd + 16 * RS;
+#pragma unroll
+      for (int i = 0; i < C / 2; ++i) {
+        const int e = lane + 32 * i, r = e / C, ch = e - r * C;
+        const int64_t o = __shfl_sync(~0u, off, r);
+        const int64_t at = o < 0 ? 0 : o + ch * 8;
+        ptx::cp_async16(kd + r * RS + ch * 16, kc + at, o < 0 ? 0 : 16);
+        ptx::cp_async16(vd + r * RS + ch * 16, vc + at, o < 0 ? 0 : 16);
+      }
+      if (--to_copy > 0) {                       // the next tile's rows, looked up meanwhile
+        if (++pi.tile == pi.s.tiles()) next_item(a, pi);
+        off = find();
+      }
     }
-    finish(a, p.b, g0 + hk * a.G + g, d, m, l, o);
+    ptx::cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < ST; ++i) copy(i);
+
+  uint32_t q[KS][4];
+  float o[D / 8][4], m[2], l[2];
+  int hq0 = 0, heads = 0, tile0 = 0;
+  auto begin = [&]() {
+    const int hk = pc.item / a.groups, g0 = (pc.item - hk * a.groups) * GMAX;
+    hq0 = hk * a.G + g0;
+    heads = min(GMAX, a.G - g0);
+    tile0 = pc.tile;
+    const bf16* qp = static_cast<const bf16*>(a.q) + pc.b * a.qb + (hq0 + row) * a.qh + 2 * quad;
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+#pragma unroll
+      for (int h = 0; h < 4; ++h)                // rows row, row + 8; channels +0, +8
+        q[k][h] = row + 8 * (h & 1) < heads
+                      ? *reinterpret_cast<const uint32_t*>(qp + 8 * (h & 1) * a.qh + 16 * k +
+                                                           8 * (h >> 1))
+                      : 0u;
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+      for (int h = 0; h < 4; ++h) o[i][h] = 0.f;
+    m[0] = m[1] = -INFINITY;
+    l[0] = l[1] = 0.f;
+  };
+  begin();
+
+  const int mrow = (lane & 7) + (lane >> 4) * 8, mch = (lane >> 3) & 1;   // K: key, piece
+  const int vrow = (lane & 7) + ((lane >> 3) & 1) * 8, vch = lane >> 4;   // V: key, piece
+  for (int slot = 0;; slot = slot + 1 == ST ? 0 : slot + 1) {
+    ptx::cp_async_wait<ST - 1>();
+    __syncwarp();
+    const int live = pc.s.n - (pc.s.lo + pc.tile * TILE + warp * 16);    // keys of this warp
+    const uint32_t kd = slots_u + slot * M::SLOT, vd = kd + 16 * RS;
+    if (live > 0) {
+      float s[2][4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int h = 0; h < 4; ++h) s[n][h] = 0.f;
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        uint32_t f[4];
+        ptx::ldsm_x4(f, kd + mrow * RS + (2 * k + mch) * 16);
+        ptx::mma_bf16_16816(s[0], q[k], f[0], f[1]);
+        ptx::mma_bf16_16816(s[1], q[k], f[2], f[3]);
+      }
+      float top[2] = {m[0], m[1]};
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          s[n][h] *= a.scale2;
+          if (n * 8 + 2 * quad + (h & 1) >= live) s[n][h] = -INFINITY;
+          top[h >> 1] = fmaxf(top[h >> 1], s[n][h]);
+        }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 1));
+        top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 2));
+      }
+      if (__any_sync(~0u, top[0] > m[0] || top[1] > m[1])) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float f = top[r] > m[r] ? exp2f(m[r] - top[r]) : 1.f;    // 0 from -inf
+          m[r] = top[r];
+          l[r] *= f;
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            o[i][2 * r] *= f;
+            o[i][2 * r + 1] *= f;
+          }
+        }
+      }
+      const float base[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          s[n][h] = exp2f(s[n][h] - base[h >> 1]);
+          l[h >> 1] += s[n][h];                  // unrounded; lanes' sums meet at the end
+        }
+      if (sbad[warp][slot]) l[0] = l[1] = NAN;
+      const uint32_t p[4] = {pack2(s[0][0], s[0][1]), pack2(s[0][2], s[0][3]),
+                             pack2(s[1][0], s[1][1]), pack2(s[1][2], s[1][3])};
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        uint32_t f[4];
+        ptx::ldsm_x4_t(f, vd + vrow * RS + (2 * i + vch) * 16);
+        ptx::mma_bf16_16816(o[2 * i], p, f[0], f[1]);
+        ptx::mma_bf16_16816(o[2 * i + 1], p, f[2], f[3]);
+      }
+    }
+    const int tiles = pc.s.tiles();
+    --left;
+    if (pc.tile + 1 == tiles || left == 0) {     // the item's end, or this block's
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        l[r] += __shfl_xor_sync(~0u, l[r], 1);
+        l[r] += __shfl_xor_sync(~0u, l[r], 2);
+        if (quad == 0) {
+          sml[warp][row + 8 * r][0] = m[r];
+          sml[warp][row + 8 * r][1] = l[r];
+        }
+      }
+      __syncwarp();                              // the slot's last readers are done
+      float* so = reinterpret_cast<float*>(slots + slot * M::SLOT);
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+          *reinterpret_cast<float2*>(so + (row + 8 * r) * M::OS + 8 * i + 2 * quad) =
+              make_float2(o[i][2 * r], o[i][2 * r + 1]);
+      __syncthreads();
+      const bool done = tile0 == 0 && pc.tile + 1 == tiles;
+      const size_t part = (size_t)blockIdx.x * 2 + (tile0 == 0 ? 1 : 0);
+      if (!done && tile0 == 0) leave_cut(a, pc, tiles - pc.tile - 1, per);
+      for (int e = threadIdx.x; e < heads * D; e += WARPS * 32) {
+        const int g = e / D, d = e - g * D;
+        float mm = -INFINITY, ll = 0.f, oo = 0.f;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) mm = fmaxf(mm, sml[w][g][0]);
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+          const float f = sml[w][g][0] == -INFINITY ? 1.f : exp2f(sml[w][g][0] - mm);
+          ll = fmaf(f, sml[w][g][1], ll);
+          oo = fmaf(f, *reinterpret_cast<const float*>(ring + (w * ST + slot) * M::SLOT +
+                                                       (g * M::OS + d) * 4), oo);
+        }
+        if (done) {
+          finish(a, pc.b, hq0 + g, d, mm, ll, oo);
+        } else {
+          a.part_o[(part * GMAX + g) * D + d] = oo;
+          if (d == 0) {
+            a.part_ml[(part * GMAX + g) * 2] = mm;
+            a.part_ml[(part * GMAX + g) * 2 + 1] = ll;
+          }
+        }
+      }
+      __syncthreads();
+      if (left == 0) break;
+      next_item(a, pc);
+      begin();
+    } else {
+      ++pc.tile;
+    }
+    __syncwarp();
+    copy(slot);
   }
 }
 
+// ------------------------------------------------------------ items cut by block boundaries
+// Block (c, g): head g of the item that block c began and later blocks went on with, if
+// there is one. The parts' weights first, then their sums, JOIN / D parts at a time.
+constexpr int JOIN = 512;
+__global__ void __launch_bounds__(JOIN) paged_join_kernel(AttnArgs a) {
+  __shared__ float weight[JOIN], red[JOIN], top[JOIN / 32], sum[JOIN / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = blockIdx.y;
+  asm volatile("griddepcontrol.wait;" ::: "memory");       // the parts are written
+  const int4 cut = a.cut[blockIdx.x];
+  const int c0 = blockIdx.x, parts = cut.z, hk = cut.y / a.groups;
+  const int g0 = (cut.y - hk * a.groups) * a.GH;
+  if (parts < 2 || g >= min(a.GH, a.G - g0)) return;
+  auto slot = [&](int c) { return ((size_t)(c0 + c) * 2 + (c == 0)) * GMAX + g; };
+  float m = -INFINITY;
+  for (int c = threadIdx.x; c < parts; c += JOIN) m = fmaxf(m, a.part_ml[slot(c) * 2]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+  if (lane == 0) top[warp] = m;
+  __syncthreads();
+  m = -INFINITY;
+  for (int w = 0; w < JOIN / 32; ++w) m = fmaxf(m, top[w]);
+  const int G = JOIN / a.D, d = threadIdx.x % a.D, grp = threadIdx.x / a.D;
+  float l = 0.f, o = 0.f;
+  for (int b0 = 0; b0 < parts; b0 += JOIN) {
+    const int n = min(JOIN, parts - b0);
+    if (threadIdx.x < n) {
+      const size_t s = slot(b0 + threadIdx.x);
+      const float mc = a.part_ml[s * 2], f = mc == -INFINITY ? 1.f : exp2f(mc - m);
+      weight[threadIdx.x] = f;
+      l = fmaf(f, a.part_ml[s * 2 + 1], l);
+    }
+    __syncthreads();
+    if (grp < G) {
+#pragma unroll 8
+      for (int c = grp; c < n; c += G) o = fmaf(weight[c], a.part_o[slot(b0 + c) * a.D + d], o);
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(~0u, l, x);
+  if (lane == 0) sum[warp] = l;
+  red[threadIdx.x] = o;
+  __syncthreads();
+  if (threadIdx.x >= a.D) return;
+  l = o = 0.f;
+  for (int w = 0; w < JOIN / 32; ++w) l += sum[w];
+  for (int k = 0; k < G; ++k) o += red[k * a.D + d];
+  finish(a, cut.x, hk * a.G + g0 + g, d, m, l, o);
+}
+
 // ------------------------------------------------------------ host
-// Blocks of the shared line: enough for several per SM.
-constexpr int kBlocks = 152 * 4;
+constexpr int kSms = 152;
 constexpr long long kMaxKeys = (1LL << 31) - 1024;   // tile ends stay within an int
 constexpr int kWholeTiles = 4;    // capacity up to which one block takes a whole item
 
 struct Plan {
-  int GH, groups, whole, blocks;
-  size_t o_bytes, ml_bytes;
+  int mma, GH, groups, whole, blocks;
+  size_t o_bytes, ml_bytes, cut_bytes;
 };
 
-Plan make_plan(const gdr_attn_dims* d, const gdr_paged_cache* c) {
+// Whether sizes, types and strides allow the tensor-core kernel (16-byte pieces of every
+// cache row; their bases are 16-byte aligned by contract).
+bool mma_sizes(const gdr_attn_dims* d, const gdr_paged_cache* c) {
+  const int D = c->D;
+  return d->q_dtype == GDR_BF16 && c->dtype == GDR_BF16 &&
+         (D == 64 || D == 80 || D == 96 || D == 128 || D == 192 || D == 256) &&
+         c->page_stride % 8 == 0 && c->token_stride % 8 == 0 && c->head_stride % 8 == 0 &&
+         (d->q_stride_b % 2 == 0 || d->B == 1) && (d->q_stride_h % 2 == 0 || d->HQ == 1);
+}
+
+Plan make_plan(const gdr_attn_dims* d, const gdr_paged_cache* c, bool mma) {
   Plan p;
   const int G = d->HQ / c->HK;
-  p.GH = c->D <= 128 ? 4 : 2;
+  p.mma = mma;
+  p.GH = mma ? GMAX : c->D <= 128 ? 4 : 2;
   p.groups = (G + p.GH - 1) / p.GH;
   long long keys = (long long)c->max_pages * c->page_size;
   if (d->window > 0 && keys > d->window) keys = d->window;
   const long long items = (long long)d->B * c->HK * p.groups;
   p.whole = keys <= kWholeTiles * TILE && items < (1LL << 31);
-  p.blocks = p.whole ? (int)items : kBlocks;
+  p.blocks = p.whole ? (int)items
+             : mma   ? kSms * (c->D <= 64 ? 4 : c->D <= 128 ? 2 : 1)
+                     : kSms * (c->D <= 64 ? 4 : 2);
   p.o_bytes = p.whole ? 0 : align_up((size_t)p.blocks * 2 * GMAX * c->D * sizeof(float));
   p.ml_bytes = p.whole ? 0 : align_up((size_t)p.blocks * 2 * GMAX * 2 * sizeof(float));
+  p.cut_bytes = p.whole ? 0 : align_up((size_t)p.blocks * sizeof(int4));
   return p;
+}
+
+size_t plan_bytes(const Plan& p) { return kAlign + p.o_bytes + p.ml_bytes + p.cut_bytes; }
+
+template <int D>
+gdr_status launch_mma(const AttnArgs& a, cudaStream_t s) {
+  if (cudaFuncSetAttribute(paged_mma_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           Mma<D>::SMEM) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return GDR_ERR_CUDA;
+  }
+  paged_mma_kernel<D><<<a.blocks, WARPS * 32, Mma<D>::SMEM, s>>>(a);
+  return launched();
 }
 
 gdr_status check(const gdr_attn_dims* d, const gdr_paged_cache* c) {
@@ -388,8 +669,10 @@ extern "C" {
 size_t gdr_paged_decode_attn_workspace_size(const gdr_attn_dims* dims,
                                             const gdr_paged_cache* cache) {
   if (check(dims, cache) != GDR_OK) return 0;
-  const Plan p = make_plan(dims, cache);
-  return kAlign + p.o_bytes + p.ml_bytes;
+  // q's alignment is not known here: room for either kernel.
+  const size_t any = plan_bytes(make_plan(dims, cache, false));
+  const size_t mma = mma_sizes(dims, cache) ? plan_bytes(make_plan(dims, cache, true)) : 0;
+  return any > mma ? any : mma;
 }
 
 gdr_status gdr_paged_decode_attn(const void* q, const void* k_cache, const void* v_cache,
@@ -405,18 +688,22 @@ gdr_status gdr_paged_decode_attn(const void* q, const void* k_cache, const void*
     return GDR_ERR_ALIGNMENT;
   if (dims->B == 0) return GDR_OK;
   if (!q || !k_cache || !v_cache || !page_table || !lens || !out) return GDR_ERR_INVALID_ARG;
-  const Plan p = make_plan(dims, cache);
-  if (!workspace || workspace_bytes < kAlign + p.o_bytes + p.ml_bytes) return GDR_ERR_WORKSPACE;
+  if (!workspace || workspace_bytes < gdr_paged_decode_attn_workspace_size(dims, cache))
+    return GDR_ERR_WORKSPACE;
   if (!is_aligned(workspace, kAlign)) return GDR_ERR_ALIGNMENT;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const Plan p = make_plan(dims, cache, mma_sizes(dims, cache) && is_aligned(q, 4));
   AttnArgs a = {};
   a.q = q; a.kc = k_cache; a.vc = v_cache; a.table = page_table; a.lens = lens;
   a.out = out; a.lse = lse;
   a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + kAlign);
   a.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + kAlign + p.o_bytes);
+  a.cut = reinterpret_cast<int4*>(static_cast<char*>(workspace) + kAlign + p.o_bytes + p.ml_bytes);
   a.B = dims->B; a.HQ = dims->HQ; a.HK = cache->HK; a.D = cache->D;
   a.G = dims->HQ / cache->HK; a.GH = p.GH; a.groups = p.groups;
-  a.page = cache->page_size; a.num_pages = cache->num_pages; a.max_pages = cache->max_pages;
+  a.page = cache->page_size;
+  a.shift = (a.page & (a.page - 1)) == 0 ? __builtin_ctz(a.page) : -1;
+  a.num_pages = cache->num_pages; a.max_pages = cache->max_pages;
   a.window = dims->window; a.whole = p.whole; a.blocks = p.blocks;
   a.out_bf16 = dims->out_dtype == GDR_BF16; a.q_bf16 = dims->q_dtype == GDR_BF16;
   a.scale2 = dims->scale * LOG2E;
@@ -426,20 +713,43 @@ gdr_status gdr_paged_decode_attn(const void* q, const void* k_cache, const void*
   if (a.HQ == 1) a.qh = 0;
   a.cap = (long long)cache->max_pages * cache->page_size;
   if (a.cap > kMaxKeys) a.cap = kMaxKeys;
-  const int vec = a.D % 4 == 0 && a.pp % 4 == 0 && a.pt % 4 == 0 && a.ph % 4 == 0;
-  const gdr_status run = with_dtype(cache->dtype, [&](auto* t) {
-    using T = std::remove_pointer_t<decltype(t)>;
-    if (a.D <= 64)
-      paged_any_kernel<T, 2, 4><<<p.blocks, WARPS * 32, 0, s>>>(a, vec);
-    else if (a.D <= 128)
-      paged_any_kernel<T, 4, 4><<<p.blocks, WARPS * 32, 0, s>>>(a, vec);
-    else
-      paged_any_kernel<T, 8, 2><<<p.blocks, WARPS * 32, 0, s>>>(a, vec);
-    return launched();
-  });
+  gdr_status run = GDR_OK;
+  if (p.mma) {
+    run = a.D == 64    ? launch_mma<64>(a, s)
+          : a.D == 80  ? launch_mma<80>(a, s)
+          : a.D == 96  ? launch_mma<96>(a, s)
+          : a.D == 128 ? launch_mma<128>(a, s)
+          : a.D == 192 ? launch_mma<192>(a, s)
+                       : launch_mma<256>(a, s);
+  } else {
+    const int vec = a.D % 4 == 0 && a.pp % 4 == 0 && a.pt % 4 == 0 && a.ph % 4 == 0;
+    run = with_dtype(cache->dtype, [&](auto* t) {
+      using T = std::remove_pointer_t<decltype(t)>;
+      if (a.D <= 64)
+        paged_any_kernel<T, 2, 4><<<p.blocks, WARPS * 32, 0, s>>>(a, vec);
+      else if (a.D <= 128)
+        paged_any_kernel<T, 4, 4><<<p.blocks, WARPS * 32, 0, s>>>(a, vec);
+      else
+        paged_any_kernel<T, 8, 2><<<p.blocks, WARPS * 32, 0, s>>>(a, vec);
+      return launched();
+    });
+  }
   if (run != GDR_OK || p.whole) return run;
-  paged_join_kernel<<<p.blocks - 1, 128, 0, s>>>(a);
-  return launched();
+  // The join may start while the last parts are being written; it waits for them itself.
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.blocks - 1, a.G < p.GH ? a.G : p.GH);
+  cfg.blockDim = dim3(JOIN);
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, paged_join_kernel, a) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return GDR_ERR_CUDA;
+  }
+  return GDR_OK;
 }
 
 }  // extern "C"
