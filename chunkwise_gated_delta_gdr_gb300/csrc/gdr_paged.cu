@@ -545,10 +545,10 @@ __global__ void __launch_bounds__(WARPS * 32, Mma<D>::OCC) paged_mma_kernel(Attn
 
 // ------------------------------------------------------------ items cut by block boundaries
 // Block (c, g): head g of the item that block c began and later blocks went on with, if
-// there is one. The parts' weights first, then their sums, JOIN / D parts at a time.
-constexpr int JOIN = 512;
-__global__ void __launch_bounds__(JOIN) paged_join_kernel(AttnArgs a) {
-  __shared__ float weight[JOIN], red[JOIN], top[JOIN / 32], sum[JOIN / 32];
+// there is one. Four warps take every fourth part, a lane the channels lane, lane + 32, ...
+constexpr int JW = 4;
+__global__ void __launch_bounds__(JW * 32) paged_join_kernel(AttnArgs a) {
+  __shared__ float red[JW][256], sum[JW];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = blockIdx.y;
   asm volatile("griddepcontrol.wait;" ::: "memory");       // the parts are written
   const int4 cut = a.cut[blockIdx.x];
@@ -557,40 +557,35 @@ __global__ void __launch_bounds__(JOIN) paged_join_kernel(AttnArgs a) {
   if (parts < 2 || g >= min(a.GH, a.G - g0)) return;
   auto slot = [&](int c) { return ((size_t)(c0 + c) * 2 + (c == 0)) * GMAX + g; };
   float m = -INFINITY;
-  for (int c = threadIdx.x; c < parts; c += JOIN) m = fmaxf(m, a.part_ml[slot(c) * 2]);
+  for (int c = lane; c < parts; c += 32) m = fmaxf(m, a.part_ml[slot(c) * 2]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-  if (lane == 0) top[warp] = m;
-  __syncthreads();
-  m = -INFINITY;
-  for (int w = 0; w < JOIN / 32; ++w) m = fmaxf(m, top[w]);
-  const int G = JOIN / a.D, d = threadIdx.x % a.D, grp = threadIdx.x / a.D;
-  float l = 0.f, o = 0.f;
-  for (int b0 = 0; b0 < parts; b0 += JOIN) {
-    const int n = min(JOIN, parts - b0);
-    if (threadIdx.x < n) {
-      const size_t s = slot(b0 + threadIdx.x);
-      const float mc = a.part_ml[s * 2], f = mc == -INFINITY ? 1.f : exp2f(mc - m);
-      weight[threadIdx.x] = f;
-      l = fmaf(f, a.part_ml[s * 2 + 1], l);
-    }
-    __syncthreads();
-    if (grp < G) {
-#pragma unroll 8
-      for (int c = grp; c < n; c += G) o = fmaf(weight[c], a.part_o[slot(b0 + c) * a.D + d], o);
-    }
-    __syncthreads();
+  float l = 0.f, o[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o[i] = 0.f;
+#pragma unroll 4
+  for (int c = warp; c < parts; c += JW) {
+    const size_t s = slot(c);
+    const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + s * 2);
+    const float f = ml.x == -INFINITY ? 1.f : exp2f(ml.x - m);
+    l = fmaf(f, ml.y, l);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (lane + 32 * i < a.D) o[i] = fmaf(f, a.part_o[s * a.D + lane + 32 * i], o[i]);
   }
 #pragma unroll
-  for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(~0u, l, x);
+  for (int i = 0; i < 8; ++i) red[warp][lane + 32 * i] = o[i];
   if (lane == 0) sum[warp] = l;
-  red[threadIdx.x] = o;
   __syncthreads();
-  if (threadIdx.x >= a.D) return;
-  l = o = 0.f;
-  for (int w = 0; w < JOIN / 32; ++w) l += sum[w];
-  for (int k = 0; k < G; ++k) o += red[k * a.D + d];
-  finish(a, cut.x, hk * a.G + g0 + g, d, m, l, o);
+  l = 0.f;
+#pragma unroll
+  for (int w = 0; w < JW; ++w) l += sum[w];
+  for (int d = threadIdx.x; d < a.D; d += JW * 32) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < JW; ++w) v += red[w][d];
+    finish(a, cut.x, hk * a.G + g0 + g, d, m, l, v);
+  }
 }
 
 // ------------------------------------------------------------ host
@@ -741,7 +736,7 @@ gdr_status gdr_paged_decode_attn(const void* q, const void* k_cache, const void*
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.blocks - 1, a.G < p.GH ? a.G : p.GH);
-  cfg.blockDim = dim3(JOIN);
+  cfg.blockDim = dim3(JW * 32);
   cfg.stream = s;
   cfg.attrs = at;
   cfg.numAttrs = 1;
