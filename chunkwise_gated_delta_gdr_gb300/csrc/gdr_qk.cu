@@ -177,6 +177,198 @@ __global__ void __launch_bounds__(GW * 32) qk_any_kernel(QkArgs a) {
   }
 }
 
+// ------------------------------------------------------------ rows of 8 channels a lane
+// A group of GL lanes (D / 8, rounded up to a power of two, at least 8) takes a head row; a lane holds
+// two runs of four channels, chosen so that the members of its four pairs are its own: the
+// runs at 4 j and 4 j + R / 2 (2 x 4 neighbouring channels when pairs are neighbours, and
+// beyond R). So the rotation needs no exchange, the norm one tree of shuffles. A group stays
+// with one token for `rows` of its head rows and loads the token's cos and sin once for all
+// of them; U rows are in flight per lane.
+constexpr int VT = 256;                          // threads per block
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, int o0, int o1, float* f) {
+  load_f<T, 4>(p + o0, f);
+  load_f<T, 4>(p + o1, f + 4);
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, int o0, int o1, const float* f) {
+  store_f<T, 4>(p + o0, f);
+  store_f<T, 4>(p + o1, f + 4);
+}
+
+// Turns the lane's four pairs by the angles (c, s).
+template <bool kNeighbours>
+__device__ __forceinline__ void turn(float* y, const float* c, const float* s) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float& p = kNeighbours ? y[2 * i] : y[i];
+    float& q = kNeighbours ? y[2 * i + 1] : y[i + 4];
+    const float x = p;
+    p = fmaf(-q, s[i], x * c[i]);
+    q = fmaf(x, s[i], q * c[i]);
+  }
+}
+
+struct VecPlan {
+  int GL, rows, chunks;                          // lanes per row, head rows per unit, units per token
+  unsigned units;
+};
+
+template <typename I, typename O, int MODE, bool kNeighbours>
+__global__ void __launch_bounds__(VT, MODE == kBwd ? 2 : 3) qk_vec_kernel(QkArgs a, VecPlan v) {
+  constexpr int U = MODE == kBwd ? 2 : 4;
+  const int GL = v.GL, lane = threadIdx.x & (GL - 1), half = a.R >> 1, rot = a.R >> 3;
+  const bool on = lane * 8 < a.D, turned = lane < rot;
+  const bool split = !kNeighbours && turned;
+  const int o0 = split ? 4 * lane : 8 * lane, o1 = split ? 4 * lane + half : 8 * lane + 4;
+  const int per = a.HQ + a.HK + (MODE == kAppend ? a.HK : 0);
+  const float inv = 1.f / a.D;
+  // Groups of one warp may stand at different units: each exchanges among its own lanes.
+  const unsigned mask = GL == 32 ? ~0u : ((1u << GL) - 1) << (threadIdx.x & 31 & ~(GL - 1));
+  float w[2][8], acc[2][8];
+#pragma unroll
+  for (int n = 0; n < 2; ++n) {
+    const float* p = n ? a.wk : a.wq;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[n][i] = 1.f, acc[n][i] = 0.f;
+    if (p && on) load8<float>(p, o0, o1, w[n]);
+  }
+  const unsigned groups = gridDim.x * (VT / GL);
+  for (unsigned unit = blockIdx.x * (VT / GL) + threadIdx.x / GL; unit < v.units; unit += groups) {
+    const unsigned tok = unit / v.chunks, b = tok / a.T, t = tok - b * a.T;
+    const int r0 = (int)(unit - tok * v.chunks) * v.rows, r1 = min(per, r0 + v.rows);
+    const long long pos = position(a, tok);
+    bool bad = a.R > 0 && (pos < 0 || pos >= a.rows);
+    int64_t at = 0;
+    if (MODE == kAppend) {
+      at = cache_row(a, b, pos);
+      bad = bad || at < 0;
+    }
+    float c[4], s[4];
+    if (turned && on && !bad) {
+      load_f<float, 4>(a.cos + pos * half + 4 * lane, c);
+      load_f<float, 4>(a.sin + pos * half + 4 * lane, s);
+      if (MODE == kBwd) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] = -s[i];
+      }
+    }
+    const I* qr = static_cast<const I*>(a.q) + b * a.qb + t * a.qt;
+    const I* kr = static_cast<const I*>(a.k) + b * a.kb + t * a.kt;
+    const I* vr = static_cast<const I*>(a.v) + b * a.vb + t * a.vt;
+    for (int r = r0; r < r1; r += U) {
+      float x[U][8], dy[MODE == kBwd ? U : 1][8], ss[U], dot[U];
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int h = r + k;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[k][i] = 0.f;
+        if (MODE == kBwd) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dy[k][i] = 0.f;
+        }
+        if (on && h < r1) {
+          load8<I>(h < a.HQ           ? qr + h * a.qh
+                   : h < a.HQ + a.HK  ? kr + (h - a.HQ) * a.kh
+                                      : vr + (h - a.HQ - a.HK) * a.vh,
+                   o0, o1, x[k]);
+          if (MODE == kBwd)
+            load8<O>(h < a.HQ ? static_cast<const O*>(a.dqo) + ((size_t)tok * a.HQ + h) * a.D
+                              : static_cast<const O*>(a.dko) +
+                                    ((size_t)tok * a.HK + h - a.HQ) * a.D,
+                     o0, o1, dy[k]);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int n = r + k >= a.HQ;
+        ss[k] = dot[k] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss[k] = fmaf(x[k][i], x[k][i], ss[k]);
+        if (MODE == kBwd) {
+          if (turned) turn<kNeighbours>(dy[k], c, s);
+          if (bad) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dy[k][i] = NAN;
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dot[k] = fmaf(dy[k][i] * w[n][i], x[k][i], dot[k]);
+        }
+      }
+      for (int o = GL >> 1; o > 0; o >>= 1) {
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+          ss[k] += __shfl_xor_sync(mask, ss[k], o);
+          if (MODE == kBwd) dot[k] += __shfl_xor_sync(mask, dot[k], o);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int h = r + k, n = h >= a.HQ;
+        const bool value = MODE == kAppend && h >= a.HQ + a.HK;
+        const float rs = value ? 1.f : rsqrtf(fmaf(ss[k], inv, a.eps));
+        float y[8];
+        if (MODE == kBwd) {
+          // dx = rs (d w - u mean(d w u)), u = rs x
+          const float m = dot[k] * inv * rs * rs;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            acc[n][i] = h < r1 ? fmaf(dy[k][i], x[k][i] * rs, acc[n][i]) : acc[n][i];
+            y[i] = rs * fmaf(-x[k][i], m, dy[k][i] * w[n][i]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] = value ? x[k][i] : x[k][i] * rs * w[n][i];
+          if (turned && !value) turn<kNeighbours>(y, c, s);
+          if (bad) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = NAN;
+          }
+        }
+        if (!on || h >= r1) continue;
+        if (MODE == kBwd) {
+          store8<I>(n ? static_cast<I*>(a.ko) + ((size_t)tok * a.HK + h - a.HQ) * a.D
+                      : static_cast<I*>(a.qo) + ((size_t)tok * a.HQ + h) * a.D,
+                    o0, o1, y);
+        } else if (MODE == kFwd || !n) {
+          store8<O>(n ? static_cast<O*>(a.ko) + ((size_t)tok * a.HK + h - a.HQ) * a.D
+                      : static_cast<O*>(a.qo) + ((size_t)tok * a.HQ + h) * a.D,
+                    o0, o1, y);
+        } else if (!bad) {
+          const int64_t to = at + (int64_t)(value ? h - a.HQ - a.HK : h - a.HQ) * a.ph;
+          void* cache = value ? a.vc : a.kc;
+          if (a.cache_bf16)
+            store8<bf16>(static_cast<bf16*>(cache) + to, o0, o1, y);
+          else
+            store8<float>(static_cast<float*>(cache) + to, o0, o1, y);
+        }
+      }
+    }
+  }
+  if (MODE == kBwd && a.part) {                  // the block's groups, in order
+    __shared__ float red[VT / 8][8 * 8 + 4];     // groups x channels of a pass
+    for (int n = 0; n < 2; ++n)
+      for (int l0 = 0; l0 < a.D / 8; l0 += 8) {  // eight lanes' channels at a time
+        __syncthreads();
+        const int g = threadIdx.x / GL;
+        if (lane >= l0 && lane < l0 + 8) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) red[g][(lane - l0) * 8 + i] = n ? acc[1][i] : acc[0][i];
+        }
+        __syncthreads();
+        const int src = l0 + (threadIdx.x >> 3), i = threadIdx.x & 7;
+        if (threadIdx.x < 64 && src * 8 < a.D) {
+          float sum = 0.f;
+          for (int k = 0; k < VT / GL; ++k) sum += red[k][threadIdx.x];
+          const bool sp = !kNeighbours && src < rot;
+          const int ch = i < 4 ? (sp ? 4 * src : 8 * src) + i
+                               : (sp ? 4 * src + half : 8 * src + 4) + i - 4;
+          a.part[((size_t)blockIdx.x * 2 + n) * a.D + ch] = sum;
+        }
+      }
+  }
+}
+
 // ------------------------------------------------------------ the weights' gradients
 // One warp per (q or k, channel): the blocks' sums in order, 32 strands then a tree.
 __global__ void __launch_bounds__(256) qk_weight_kernel(const float* part, int blocks, int D,
@@ -192,7 +384,7 @@ __global__ void __launch_bounds__(256) qk_weight_kernel(const float* part, int b
 }
 
 // ------------------------------------------------------------ host
-constexpr int kMaxBlocks = 1024;                 // of the backward: rows of the partial sums
+constexpr int kMaxBlocks = 152 * 2;              // of the backward: rows of the partial sums
 
 gdr_status check(const gdr_qk_dims* d) {
   if (!d) return GDR_ERR_INVALID_ARG;
@@ -245,18 +437,57 @@ gdr_status check_shared(const gdr_qk_dims* d, const void* q, const void* k, cons
   return GDR_OK;
 }
 
-int any_blocks(const QkArgs& a, int per, int most) {
-  const long long want = (a.tokens * per + GW - 1) / GW;
-  return (int)(want < most ? want : most);
+// Whether the vector kernel takes these sizes, strides and bases: whole runs of four
+// channels, aligned.
+bool vec_ok(const gdr_qk_dims* d, const QkArgs& a, int mode, const gdr_paged_cache* c) {
+  if (d->D % 8 != 0 || d->R % 8 != 0) return false;
+  const size_t run = 4 * dtype_size(d->in_dtype);
+  const int64_t s[] = {a.qb, a.qt, a.qh, a.kb, a.kt, a.kh,
+                       mode == kAppend ? a.vb : 0, mode == kAppend ? a.vt : 0,
+                       mode == kAppend ? a.vh : 0};
+  for (int64_t x : s)
+    if (x % 4 != 0) return false;
+  if (!is_aligned(a.q, run) || !is_aligned(a.k, run)) return false;
+  if (mode == kAppend && (!is_aligned(a.v, run) || c->page_stride % 4 != 0 ||
+                          c->token_stride % 4 != 0 || c->head_stride % 4 != 0))
+    return false;
+  return a.tokens * (a.HQ + 2LL * a.HK) < (1LL << 31);
 }
 
+VecPlan vec_plan(const QkArgs& a, int per) {
+  VecPlan v;
+  v.GL = 8;
+  while (v.GL * 8 < a.D) v.GL *= 2;
+  // At most 16 head rows of a token per group, fewer where that leaves the device empty.
+  const long long share = a.tokens * per / (152LL * (1024 / v.GL));
+  const int most = (int)(share < 1 ? 1 : share > 16 ? 16 : share);
+  v.chunks = (per + most - 1) / most;
+  v.rows = (per + v.chunks - 1) / v.chunks;
+  v.chunks = (per + v.rows - 1) / v.rows;
+  v.units = (unsigned)(a.tokens * v.chunks);
+  return v;
+}
+
+// Launches with at most `most` blocks; returns how many through *blocks.
 template <int MODE>
-gdr_status launch(const gdr_qk_dims* d, const QkArgs& a, int blocks, cudaStream_t s) {
+gdr_status launch(const gdr_qk_dims* d, const QkArgs& a, const gdr_paged_cache* c, int most,
+                  int* blocks, cudaStream_t s) {
+  const int per = a.HQ + a.HK + (MODE == kAppend ? a.HK : 0);
+  const bool vec = vec_ok(d, a, MODE, c);
+  const VecPlan v = vec ? vec_plan(a, per) : VecPlan();
+  const long long want = vec ? ((long long)v.units * v.GL + VT - 1) / VT
+                             : (a.tokens * per + GW - 1) / GW;
+  *blocks = (int)(want < most ? want : most);
   return with_dtype(d->in_dtype, [&](auto* i) {
     return with_dtype(d->out_dtype, [&](auto* o) {
       using I = std::remove_pointer_t<decltype(i)>;
       using O = std::remove_pointer_t<decltype(o)>;
-      qk_any_kernel<I, O, MODE><<<blocks, GW * 32, 0, s>>>(a);
+      if (!vec)
+        qk_any_kernel<I, O, MODE><<<*blocks, GW * 32, 0, s>>>(a);
+      else if (a.interleaved)
+        qk_vec_kernel<I, O, MODE, true><<<*blocks, VT, 0, s>>>(a, v);
+      else
+        qk_vec_kernel<I, O, MODE, false><<<*blocks, VT, 0, s>>>(a, v);
       return launched();
     });
   });
@@ -284,8 +515,8 @@ gdr_status gdr_qk_norm_rope(const void* q, const void* k, const float* q_weight,
   if (!q_out || !k_out) return GDR_ERR_INVALID_ARG;
   QkArgs a = make_args(dims, q_weight, k_weight, cos, sin, positions);
   a.q = q; a.k = k; a.qo = q_out; a.ko = k_out;
-  return launch<kFwd>(dims, a, any_blocks(a, a.HQ + a.HK, 1 << 20),
-                      reinterpret_cast<cudaStream_t>(stream));
+  int blocks;
+  return launch<kFwd>(dims, a, nullptr, 1 << 30, &blocks, reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t gdr_qk_norm_rope_bwd_workspace_size(const gdr_qk_dims* dims) {
@@ -322,8 +553,8 @@ gdr_status gdr_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const vo
     if (!is_aligned(workspace, kAlign)) return GDR_ERR_ALIGNMENT;
     a.part = static_cast<float*>(workspace);
   }
-  const int blocks = any_blocks(a, a.HQ + a.HK, kMaxBlocks);
-  st = launch<kBwd>(dims, a, blocks, s);
+  int blocks;
+  st = launch<kBwd>(dims, a, nullptr, kMaxBlocks, &blocks, s);
   if (st != GDR_OK || !a.part) return st;
   qk_weight_kernel<<<(2 * a.D + 7) / 8, 256, 0, s>>>(a.part, blocks, a.D, dq_weight, dk_weight);
   return launched();
@@ -352,7 +583,8 @@ gdr_status gdr_qk_norm_rope_append(const void* q, const void* k, const void* v,
   a.num_pages = cache->num_pages; a.page = cache->page_size; a.max_pages = cache->max_pages;
   a.cache_bf16 = cache->dtype == GDR_BF16;
   a.pp = cache->page_stride; a.pt = cache->token_stride; a.ph = cache->head_stride;
-  return launch<kAppend>(dims, a, any_blocks(a, a.HQ + 2 * a.HK, 1 << 20),
+  int blocks;
+  return launch<kAppend>(dims, a, cache, 1 << 30, &blocks,
                          reinterpret_cast<cudaStream_t>(stream));
 }
 
