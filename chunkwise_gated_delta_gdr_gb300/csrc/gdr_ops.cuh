@@ -90,6 +90,41 @@ __device__ __forceinline__ void to_float(const Raw<T, V>& r, float* f) {
   }
 }
 
+// Two fp32 operations per instruction, on pairs of registers.
+__device__ __forceinline__ unsigned long long bits2(float2 a) {
+  return *reinterpret_cast<unsigned long long*>(&a);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  unsigned long long d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+  return *reinterpret_cast<float2*>(&d);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  unsigned long long d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits2(a)), "l"(bits2(b)));
+  return *reinterpret_cast<float2*>(&d);
+}
+// Four consecutive elements as two pairs.
+__device__ __forceinline__ void load_pairs(const float* p, float2* f) {
+  const float4 v = *reinterpret_cast<const float4*>(p);
+  f[0] = make_float2(v.x, v.y);
+  f[1] = make_float2(v.z, v.w);
+}
+__device__ __forceinline__ void to_pairs(const Raw<float, 4>& r, float2* f) {
+  f[0] = make_float2(r.v.x, r.v.y);
+  f[1] = make_float2(r.v.z, r.v.w);
+}
+__device__ __forceinline__ void to_pairs(const Raw<bf16, 4>& r, float2* f) {
+  f[0] = unpack2(r.v.x);
+  f[1] = unpack2(r.v.y);
+}
+__device__ __forceinline__ void store_pairs(float* p, const float2* f) {
+  *reinterpret_cast<float4*>(p) = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+}
+__device__ __forceinline__ void store_pairs(bf16* p, const float2* f) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack2(f[0].x, f[0].y), pack2(f[1].x, f[1].y));
+}
+
 template <typename T, int V>
 __device__ __forceinline__ void load_f(const T* p, float* f) {
   to_float<T, V>(load_raw<T, V>(p), f);

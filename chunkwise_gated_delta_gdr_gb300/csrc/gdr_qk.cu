@@ -178,194 +178,265 @@ __global__ void __launch_bounds__(GW * 32) qk_any_kernel(QkArgs a) {
 }
 
 // ------------------------------------------------------------ rows of 8 channels a lane
-// A group of GL lanes (D / 8, rounded up to a power of two, at least 8) takes a head row; a lane holds
-// two runs of four channels, chosen so that the members of its four pairs are its own: the
-// runs at 4 j and 4 j + R / 2 (2 x 4 neighbouring channels when pairs are neighbours, and
-// beyond R). So the rotation needs no exchange, the norm one tree of shuffles. A group stays
-// with one token for `rows` of its head rows and loads the token's cos and sin once for all
-// of them; U rows are in flight per lane.
-constexpr int VT = 256;                          // threads per block
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, int o0, int o1, float* f) {
-  load_f<T, 4>(p + o0, f);
-  load_f<T, 4>(p + o1, f + 4);
-}
-template <typename T>
-__device__ __forceinline__ void store8(T* p, int o0, int o1, const float* f) {
-  store_f<T, 4>(p + o0, f);
-  store_f<T, 4>(p + o1, f + 4);
-}
+// A group of GL lanes (D / 8, rounded up to a power of two, at least 8) takes a head row; a
+// lane holds two runs of four channels, chosen so that the members of its four rotation
+// pairs are its own: the runs at 4 j and 4 j + R / 2 (2 x 4 neighbouring channels when pairs
+// are neighbours, and beyond R). So the rotation needs no exchange, the norm one tree of
+// shuffles. What bounds this kernel beside the bytes is the number of instructions per row:
+// a group stays with one token for up to 16 of its rows, so that addresses, angles and
+// weights are set up once for them, the weight is folded into the angles
+//   y[j] = rs (M[j] x[j] + N[j] z[j]),   z[j] the other members of the pairs x[j],
+// and fp32 goes two operations an instruction. The next U rows are under way, as raw bits,
+// while U rows are worked on.
+constexpr int VT = 128;                          // threads per block
 
-// Turns the lane's four pairs by the angles (c, s).
-template <bool kNeighbours>
-__device__ __forceinline__ void turn(float* y, const float* c, const float* s) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float& p = kNeighbours ? y[2 * i] : y[i];
-    float& q = kNeighbours ? y[2 * i + 1] : y[i + 4];
-    const float x = p;
-    p = fmaf(-q, s[i], x * c[i]);
-    q = fmaf(x, s[i], q * c[i]);
-  }
-}
-
+// A unit: `rows` head rows of one token, all of q, of k, or (append) of v. Units are numbered
+// section by section.
 struct VecPlan {
-  int GL, rows, chunks;                          // lanes per row, head rows per unit, units per token
-  unsigned units;
+  int GL;                                        // lanes per row
+  int rows[3], chunks[3];                        // per section: rows per unit, units per token
+  unsigned units[3];
 };
 
-template <typename I, typename O, int MODE, bool kNeighbours>
-__global__ void __launch_bounds__(VT, MODE == kBwd ? 2 : 3) qk_vec_kernel(QkArgs a, VecPlan v) {
-  constexpr int U = MODE == kBwd ? 2 : 4;
-  const int GL = v.GL, lane = threadIdx.x & (GL - 1), half = a.R >> 1, rot = a.R >> 3;
+// The pairs that turn with x[0..3]: the other run's, or each pair swapped.
+template <bool kNeighbours>
+__device__ __forceinline__ float2 mate(const float2* x, int j) {
+  return kNeighbours ? make_float2(x[j].y, x[j].x) : x[j ^ 2];
+}
+
+template <typename I, typename O, int MODE, bool kNeighbours, int GL>
+__global__ void __launch_bounds__(VT, MODE == kBwd ? 4 : 6) qk_vec_kernel(QkArgs a, VecPlan v) {
+  constexpr bool bwd = MODE == kBwd;
+  constexpr int U = 2, K = bwd ? 1 : 2;       // rows under way; at work at a time
+  const int lane = threadIdx.x & (GL - 1), half = a.R >> 1, rot = a.R >> 3;
   const bool on = lane * 8 < a.D, turned = lane < rot;
   const bool split = !kNeighbours && turned;
   const int o0 = split ? 4 * lane : 8 * lane, o1 = split ? 4 * lane + half : 8 * lane + 4;
-  const int per = a.HQ + a.HK + (MODE == kAppend ? a.HK : 0);
+  const int run = o1 - o0;                       // from one run to the other
   const float inv = 1.f / a.D;
   // Groups of one warp may stand at different units: each exchanges among its own lanes.
   const unsigned mask = GL == 32 ? ~0u : ((1u << GL) - 1) << (threadIdx.x & 31 & ~(GL - 1));
-  float w[2][8], acc[2][8];
-#pragma unroll
-  for (int n = 0; n < 2; ++n) {
-    const float* p = n ? a.wk : a.wq;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[n][i] = 1.f, acc[n][i] = 0.f;
-    if (p && on) load8<float>(p, o0, o1, w[n]);
-  }
   const unsigned groups = gridDim.x * (VT / GL);
-  for (unsigned unit = blockIdx.x * (VT / GL) + threadIdx.x / GL; unit < v.units; unit += groups) {
-    const unsigned tok = unit / v.chunks, b = tok / a.T, t = tok - b * a.T;
-    const int r0 = (int)(unit - tok * v.chunks) * v.rows, r1 = min(per, r0 + v.rows);
-    const long long pos = position(a, tok);
-    bool bad = a.R > 0 && (pos < 0 || pos >= a.rows);
-    int64_t at = 0;
-    if (MODE == kAppend) {
-      at = cache_row(a, b, pos);
-      bad = bad || at < 0;
+  unsigned unit = blockIdx.x * (VT / GL) + threadIdx.x / GL;
+#pragma unroll 1
+  for (int n = 0; n < (MODE == kAppend ? 3 : 2); ++n) {     // q, k, v
+    const bool value = MODE == kAppend && n == 2;
+    const int H = n == 0 ? a.HQ : a.HK;
+    const float* wp = n == 0 ? a.wq : n == 1 ? a.wk : nullptr;
+    float2 w[4], acc[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = make_float2(1.f, 1.f), acc[j] = make_float2(0.f, 0.f);
+    if (wp && on && unit < v.units[n]) {
+      load_pairs(wp + o0, w);
+      load_pairs(wp + o1, w + 2);
     }
-    float c[4], s[4];
-    if (turned && on && !bad) {
-      load_f<float, 4>(a.cos + pos * half + 4 * lane, c);
-      load_f<float, 4>(a.sin + pos * half + 4 * lane, s);
-      if (MODE == kBwd) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[i] = -s[i];
-      }
-    }
-    const I* qr = static_cast<const I*>(a.q) + b * a.qb + t * a.qt;
-    const I* kr = static_cast<const I*>(a.k) + b * a.kb + t * a.kt;
-    const I* vr = static_cast<const I*>(a.v) + b * a.vb + t * a.vt;
-    for (int r = r0; r < r1; r += U) {
-      float x[U][8], dy[MODE == kBwd ? U : 1][8], ss[U], dot[U];
-#pragma unroll
-      for (int k = 0; k < U; ++k) {
-        const int h = r + k;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[k][i] = 0.f;
-        if (MODE == kBwd) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) dy[k][i] = 0.f;
-        }
-        if (on && h < r1) {
-          load8<I>(h < a.HQ           ? qr + h * a.qh
-                   : h < a.HQ + a.HK  ? kr + (h - a.HQ) * a.kh
-                                      : vr + (h - a.HQ - a.HK) * a.vh,
-                   o0, o1, x[k]);
-          if (MODE == kBwd)
-            load8<O>(h < a.HQ ? static_cast<const O*>(a.dqo) + ((size_t)tok * a.HQ + h) * a.D
-                              : static_cast<const O*>(a.dko) +
-                                    ((size_t)tok * a.HK + h - a.HQ) * a.D,
-                     o0, o1, dy[k]);
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < U; ++k) {
-        const int n = r + k >= a.HQ;
-        ss[k] = dot[k] = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss[k] = fmaf(x[k][i], x[k][i], ss[k]);
-        if (MODE == kBwd) {
-          if (turned) turn<kNeighbours>(dy[k], c, s);
-          if (bad) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) dy[k][i] = NAN;
+    const I* src = static_cast<const I*>(n == 0 ? a.q : n == 1 ? a.k : a.v);
+    const int64_t sb = n == 0 ? a.qb : n == 1 ? a.kb : a.vb;
+    const int64_t st = n == 0 ? a.qt : n == 1 ? a.kt : a.vt;
+    const int64_t sh = n == 0 ? a.qh : n == 1 ? a.kh : a.vh;
+#pragma unroll 1
+    for (; unit < v.units[n]; unit += groups) {
+      const unsigned tok = unit / v.chunks[n], b = tok / a.T, t = tok - b * a.T;
+      const int r0 = (int)(unit - tok * v.chunks[n]) * v.rows[n], rows = min(H - r0, v.rows[n]);
+      const int64_t dense = ((int64_t)tok * H + r0) * a.D + o0;
+      const I* xp = src + b * sb + t * st + r0 * sh + o0;
+      const O* dp = static_cast<const O*>(n == 0 ? a.dqo : a.dko) + dense;
+      const long long pos = position(a, tok);
+      struct Rows {                              // U rows as raw bits
+        Raw<I, 4> x[U][2];
+        Raw<O, 4> d[bwd ? U : 1][2];
+      };
+      auto fetch = [&](Rows& f, int r) {         // the U rows from r; zeros beyond the unit
+        auto row = [&](int k) {
+          f.x[k][0] = load_raw<I, 4>(xp);
+          f.x[k][1] = load_raw<I, 4>(xp + run);
+          xp += sh;
+          if constexpr (bwd) {
+            f.d[k][0] = load_raw<O, 4>(dp);
+            f.d[k][1] = load_raw<O, 4>(dp + run);
+            dp += a.D;
           }
+        };
+        if (on && r + U <= rows) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) dot[k] = fmaf(dy[k][i] * w[n][i], x[k][i], dot[k]);
-        }
-      }
-      for (int o = GL >> 1; o > 0; o >>= 1) {
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-          ss[k] += __shfl_xor_sync(mask, ss[k], o);
-          if (MODE == kBwd) dot[k] += __shfl_xor_sync(mask, dot[k], o);
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < U; ++k) {
-        const int h = r + k, n = h >= a.HQ;
-        const bool value = MODE == kAppend && h >= a.HQ + a.HK;
-        const float rs = value ? 1.f : rsqrtf(fmaf(ss[k], inv, a.eps));
-        float y[8];
-        if (MODE == kBwd) {
-          // dx = rs (d w - u mean(d w u)), u = rs x
-          const float m = dot[k] * inv * rs * rs;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            acc[n][i] = h < r1 ? fmaf(dy[k][i], x[k][i] * rs, acc[n][i]) : acc[n][i];
-            y[i] = rs * fmaf(-x[k][i], m, dy[k][i] * w[n][i]);
-          }
+          for (int k = 0; k < U; ++k) row(k);
         } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = value ? x[k][i] : x[k][i] * rs * w[n][i];
-          if (turned && !value) turn<kNeighbours>(y, c, s);
-          if (bad) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = NAN;
+          for (int k = 0; k < U; ++k) {
+            f.x[k][0] = f.x[k][1] = zero_raw<I, 4>();
+            if constexpr (bwd) f.d[k][0] = f.d[k][1] = zero_raw<O, 4>();
+            if (on && r + k < rows) row(k);
           }
         }
-        if (!on || h >= r1) continue;
-        if (MODE == kBwd) {
-          store8<I>(n ? static_cast<I*>(a.ko) + ((size_t)tok * a.HK + h - a.HQ) * a.D
-                      : static_cast<I*>(a.qo) + ((size_t)tok * a.HQ + h) * a.D,
-                    o0, o1, y);
-        } else if (MODE == kFwd || !n) {
-          store8<O>(n ? static_cast<O*>(a.ko) + ((size_t)tok * a.HK + h - a.HQ) * a.D
-                      : static_cast<O*>(a.qo) + ((size_t)tok * a.HQ + h) * a.D,
-                    o0, o1, y);
-        } else if (!bad) {
-          const int64_t to = at + (int64_t)(value ? h - a.HQ - a.HK : h - a.HQ) * a.ph;
-          void* cache = value ? a.vc : a.kc;
-          if (a.cache_bf16)
-            store8<bf16>(static_cast<bf16*>(cache) + to, o0, o1, y);
-          else
-            store8<float>(static_cast<float*>(cache) + to, o0, o1, y);
+      };
+      Rows f0, f1;
+      fetch(f0, 0);
+      bool bad = a.R > 0 && (pos < 0 || pos >= a.rows);
+      char* to;                                  // this lane's place in the first result row
+      int64_t step;
+      bool to_bf16;
+      if (MODE == kAppend && n > 0) {
+        const int64_t at = cache_row(a, b, pos);
+        bad = bad || at < 0;
+        to_bf16 = a.cache_bf16;
+        const int es = to_bf16 ? 2 : 4;
+        to = static_cast<char*>(value ? a.vc : a.kc) + (at + r0 * a.ph + o0) * es;
+        step = a.ph * es;
+      } else {
+        if (MODE == kAppend) bad = bad || cache_row(a, b, pos) < 0;
+        to_bf16 = sizeof(O) == 2;
+        if constexpr (bwd) to_bf16 = sizeof(I) == 2;
+        const int es = to_bf16 ? 2 : 4;
+        to = static_cast<char*>(n == 0 ? a.qo : a.ko) + dense * es;
+        step = (int64_t)a.D * es;
+      }
+      const bool keep = on && !(MODE == kAppend && n > 0 && bad);
+      // c and s of the lane's pairs, laid out like them; sg turns forward.
+      float2 c[4], sg[4];
+      if (turned && !bad && !value) {
+        const float4 cv = *reinterpret_cast<const float4*>(a.cos + pos * half + 4 * lane);
+        const float4 sv = *reinterpret_cast<const float4*>(a.sin + pos * half + 4 * lane);
+        if (kNeighbours) {
+          c[0] = make_float2(cv.x, cv.x), c[1] = make_float2(cv.y, cv.y);
+          c[2] = make_float2(cv.z, cv.z), c[3] = make_float2(cv.w, cv.w);
+          sg[0] = make_float2(-sv.x, sv.x), sg[1] = make_float2(-sv.y, sv.y);
+          sg[2] = make_float2(-sv.z, sv.z), sg[3] = make_float2(-sv.w, sv.w);
+        } else {
+          c[0] = c[2] = make_float2(cv.x, cv.y), c[1] = c[3] = make_float2(cv.z, cv.w);
+          sg[2] = make_float2(sv.x, sv.y), sg[3] = make_float2(sv.z, sv.w);
+          sg[0] = make_float2(-sv.x, -sv.y), sg[1] = make_float2(-sv.z, -sv.w);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c[j] = make_float2(1.f, 1.f), sg[j] = make_float2(0.f, 0.f);
+      }
+      if constexpr (bwd) {                       // back by the angle
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sg[j] = make_float2(-sg[j].x, -sg[j].y);
+      } else {
+        float2 m[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m[j] = mate<kNeighbours>(w, j);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          c[j] = mul2(c[j], w[j]);               // M
+          sg[j] = mul2(sg[j], m[j]);             // N
         }
       }
+      auto work = [&](const Rows& f, int r) {
+#pragma unroll
+        for (int k0 = 0; k0 < U; k0 += K) {
+          float2 x[K][4], d[K][4];
+          float ss[K], dot[K];
+#pragma unroll
+          for (int k = 0; k < K; ++k) {
+            to_pairs(f.x[k0 + k][0], x[k]);
+            to_pairs(f.x[k0 + k][1], x[k] + 2);
+            float2 q = mul2(x[k][0], x[k][0]);
+#pragma unroll
+            for (int j = 1; j < 4; ++j) q = fma2(x[k][j], x[k][j], q);
+            ss[k] = q.x + q.y;
+            if constexpr (bwd) {
+              float2 z[4];
+              to_pairs(f.d[k0 + k][0], z);
+              to_pairs(f.d[k0 + k][1], z + 2);
+              if (turned) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  d[k][j] = fma2(sg[j], mate<kNeighbours>(z, j), mul2(c[j], z[j]));
+              } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) d[k][j] = z[j];
+              }
+              q = make_float2(0.f, 0.f);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) q = fma2(mul2(d[k][j], w[j]), x[k][j], q);
+              dot[k] = q.x + q.y;
+            }
+          }
+          if (!value) {
+#pragma unroll
+            for (int o = GL / 2; o > 0; o >>= 1) {
+#pragma unroll
+              for (int k = 0; k < K; ++k) {
+                ss[k] += __shfl_xor_sync(mask, ss[k], o);
+                if constexpr (bwd) dot[k] += __shfl_xor_sync(mask, dot[k], o);
+              }
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < K; ++k) {
+            // A bad position makes the whole row NaN (and stores nothing into the caches).
+            const float rs = bad ? NAN : value ? 1.f : rsqrtf(fmaf(ss[k], inv, a.eps));
+            const float2 rs2 = make_float2(rs, rs);
+            float2 y[4];
+            if constexpr (bwd) {
+              // dx = rs (d w - u mean(d w u)), u = rs x
+              const float m = -dot[k] * inv * rs;
+              const float2 m2 = make_float2(m, m);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float2 u = mul2(x[k][j], rs2);
+                acc[j] = fma2(d[k][j], u, acc[j]);   // rows beyond the unit are zeros
+                y[j] = mul2(rs2, fma2(u, m2, mul2(d[k][j], w[j])));
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) y[j] = mul2(c[j], x[k][j]);
+              if (turned) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) y[j] = fma2(sg[j], mate<kNeighbours>(x[k], j), y[j]);
+              }
+#pragma unroll
+              for (int j = 0; j < 4; ++j) y[j] = mul2(y[j], rs2);
+            }
+            if (keep && r + k0 + k < rows) {
+              if (to_bf16) {
+                store_pairs(reinterpret_cast<bf16*>(to), y);
+                store_pairs(reinterpret_cast<bf16*>(to) + run, y + 2);
+              } else {
+                store_pairs(reinterpret_cast<float*>(to), y);
+                store_pairs(reinterpret_cast<float*>(to) + run, y + 2);
+              }
+            }
+            to += step;
+          }
+        }
+      };
+#pragma unroll 1
+      for (int r = 0;;) {                        // one batch at work, the next under way
+        fetch(f1, r + U);
+        work(f0, r);
+        if ((r += U) >= rows) break;
+        fetch(f0, r + U);
+        work(f1, r);
+        if ((r += U) >= rows) break;
+      }
     }
-  }
-  if (MODE == kBwd && a.part) {                  // the block's groups, in order
-    __shared__ float red[VT / 8][8 * 8 + 4];     // groups x channels of a pass
-    for (int n = 0; n < 2; ++n)
-      for (int l0 = 0; l0 < a.D / 8; l0 += 8) {  // eight lanes' channels at a time
+    unit -= v.units[n];
+    if (bwd && a.part) {                         // the block's groups, in order
+      __shared__ float red[VT / 8][8 * 8 + 4];   // groups x channels of eight lanes
+      for (int l0 = 0; l0 < a.D / 8; l0 += 8) {
         __syncthreads();
-        const int g = threadIdx.x / GL;
         if (lane >= l0 && lane < l0 + 8) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) red[g][(lane - l0) * 8 + i] = n ? acc[1][i] : acc[0][i];
+          for (int j = 0; j < 4; ++j) {
+            red[threadIdx.x / GL][(lane - l0) * 8 + 2 * j] = acc[j].x;
+            red[threadIdx.x / GL][(lane - l0) * 8 + 2 * j + 1] = acc[j].y;
+          }
         }
         __syncthreads();
-        const int src = l0 + (threadIdx.x >> 3), i = threadIdx.x & 7;
-        if (threadIdx.x < 64 && src * 8 < a.D) {
+        const int of = l0 + (threadIdx.x >> 3), i = threadIdx.x & 7;
+        if (threadIdx.x < 64 && of * 8 < a.D) {
           float sum = 0.f;
           for (int k = 0; k < VT / GL; ++k) sum += red[k][threadIdx.x];
-          const bool sp = !kNeighbours && src < rot;
-          const int ch = i < 4 ? (sp ? 4 * src : 8 * src) + i
-                               : (sp ? 4 * src + half : 8 * src + 4) + i - 4;
+          const bool sp = !kNeighbours && of < rot;
+          const int ch = i < 4 ? (sp ? 4 * of : 8 * of) + i
+                               : (sp ? 4 * of + half : 8 * of + 4) + i - 4;
           a.part[((size_t)blockIdx.x * 2 + n) * a.D + ch] = sum;
         }
       }
+    }
   }
 }
 
@@ -384,7 +455,7 @@ __global__ void __launch_bounds__(256) qk_weight_kernel(const float* part, int b
 }
 
 // ------------------------------------------------------------ host
-constexpr int kMaxBlocks = 152 * 2;              // of the backward: rows of the partial sums
+constexpr int kMaxBlocks = 152 * 4;              // of the backward: rows of the partial sums
 
 gdr_status check(const gdr_qk_dims* d) {
   if (!d) return GDR_ERR_INVALID_ARG;
@@ -454,18 +525,33 @@ bool vec_ok(const gdr_qk_dims* d, const QkArgs& a, int mode, const gdr_paged_cac
   return a.tokens * (a.HQ + 2LL * a.HK) < (1LL << 31);
 }
 
-VecPlan vec_plan(const QkArgs& a, int per) {
-  VecPlan v;
+VecPlan vec_plan(const QkArgs& a, int mode) {
+  VecPlan v = {};
   v.GL = 8;
   while (v.GL * 8 < a.D) v.GL *= 2;
+  const int heads[3] = {a.HQ, a.HK, mode == kAppend ? a.HK : 0};
   // At most 16 head rows of a token per group, fewer where that leaves the device empty.
-  const long long share = a.tokens * per / (152LL * (1024 / v.GL));
+  const long long share =
+      a.tokens * (heads[0] + heads[1] + heads[2]) / (152LL * (1024 / v.GL));
   const int most = (int)(share < 1 ? 1 : share > 16 ? 16 : share);
-  v.chunks = (per + most - 1) / most;
-  v.rows = (per + v.chunks - 1) / v.chunks;
-  v.chunks = (per + v.rows - 1) / v.rows;
-  v.units = (unsigned)(a.tokens * v.chunks);
+  for (int n = 0; n < 3; ++n) {
+    if (!heads[n]) continue;
+    const int chunks = (heads[n] + most - 1) / most;
+    v.rows[n] = (heads[n] + chunks - 1) / chunks;
+    v.chunks[n] = (heads[n] + v.rows[n] - 1) / v.rows[n];
+    v.units[n] = (unsigned)(a.tokens * v.chunks[n]);
+  }
   return v;
+}
+
+template <typename I, typename O, int MODE, bool kNeighbours>
+void launch_vec(const QkArgs& a, const VecPlan& v, int blocks, cudaStream_t s) {
+  if (v.GL == 8)
+    qk_vec_kernel<I, O, MODE, kNeighbours, 8><<<blocks, VT, 0, s>>>(a, v);
+  else if (v.GL == 16)
+    qk_vec_kernel<I, O, MODE, kNeighbours, 16><<<blocks, VT, 0, s>>>(a, v);
+  else
+    qk_vec_kernel<I, O, MODE, kNeighbours, 32><<<blocks, VT, 0, s>>>(a, v);
 }
 
 // Launches with at most `most` blocks; returns how many through *blocks.
@@ -474,8 +560,9 @@ gdr_status launch(const gdr_qk_dims* d, const QkArgs& a, const gdr_paged_cache* 
                   int* blocks, cudaStream_t s) {
   const int per = a.HQ + a.HK + (MODE == kAppend ? a.HK : 0);
   const bool vec = vec_ok(d, a, MODE, c);
-  const VecPlan v = vec ? vec_plan(a, per) : VecPlan();
-  const long long want = vec ? ((long long)v.units * v.GL + VT - 1) / VT
+  const VecPlan v = vec ? vec_plan(a, MODE) : VecPlan();
+  const long long units = (long long)v.units[0] + v.units[1] + v.units[2];
+  const long long want = vec ? (units * v.GL + VT - 1) / VT
                              : (a.tokens * per + GW - 1) / GW;
   *blocks = (int)(want < most ? want : most);
   return with_dtype(d->in_dtype, [&](auto* i) {
@@ -485,9 +572,9 @@ gdr_status launch(const gdr_qk_dims* d, const QkArgs& a, const gdr_paged_cache* 
       if (!vec)
         qk_any_kernel<I, O, MODE><<<*blocks, GW * 32, 0, s>>>(a);
       else if (a.interleaved)
-        qk_vec_kernel<I, O, MODE, true><<<*blocks, VT, 0, s>>>(a, v);
+        launch_vec<I, O, MODE, true>(a, v, *blocks, s);
       else
-        qk_vec_kernel<I, O, MODE, false><<<*blocks, VT, 0, s>>>(a, v);
+        launch_vec<I, O, MODE, false>(a, v, *blocks, s);
       return launched();
     });
   });

@@ -269,6 +269,11 @@ QK_SHAPES = [  # B, T, HQ, HK, D, R, interleaved, dtype
     (1, 5, 2, 2, 72, 0, False, BF), (2, 40, 16, 4, 64, 32, False, F32),
     (1, 3, 40, 8, 128, 20, False, BF), (70, 1, 16, 4, 128, 128, True, BF),
     (1, 2, 1, 1, 2, 2, False, F32), (1, 2, 1, 1, 1, 0, False, F32),
+    # enough tokens for the ring of whole tokens: several tiles a block, ragged ends
+    (1, 1301, 3, 1, 128, 128, False, BF), (2, 999, 4, 4, 64, 32, True, BF),
+    (3, 1001, 2, 1, 80, 40, False, BF), (1, 701, 5, 2, 96, 96, False, F32),
+    (1, 613, 9, 3, 256, 64, False, BF), (2, 2503, 1, 1, 128, 0, False, BF),
+    (1, 9001, 1, 1, 64, 64, False, BF), (1, 350, 33, 3, 128, 128, True, F32),
 ]
 
 
@@ -336,17 +341,17 @@ def test_qk_long_positions_and_no_weights():
     check(n[0], ref, 4e-6, row_scale(ref))
 
 
-@pytest.mark.parametrize("D", [128, 30])
-def test_qk_zero_rows_and_extremes(D):
+@pytest.mark.parametrize("D,T", [(128, 4), (30, 4), (128, 2000)])
+def test_qk_zero_rows_and_extremes(D, T):
     """A zero row stays zero (1/sqrt(eps) times 0); a row of infinities gives NaN in it alone."""
-    q, k, _, wq, wk, cos, sin, pos = qk_inputs(1, 4, 2, 1, D, D, F32, 24)
+    q, k, _, wq, wk, cos, sin, pos = qk_inputs(1, T, 2, 1, D, D, F32, 24)
     q, k = q.clone(), k.clone()
     q[0, 1, 0] = 0
     q[0, 2, 1] = math.inf
     qo, ko = gdr.qk_norm_rope(q, k, wq, wk, cos, sin, pos)
     assert not qo[0, 1, 0].any()
     assert torch.isnan(qo[0, 2, 1]).all()
-    keep = torch.ones(4, 2, dtype=torch.bool)
+    keep = torch.ones(T, 2, dtype=torch.bool)
     keep[2, 1] = False
     assert torch.isfinite(qo[0][keep]).all() and torch.isfinite(ko).all()
     dq = gdr.qk_norm_rope_bwd(torch.ones_like(qo[:, :2]), torch.ones_like(ko[:, :2]), q[:, :2],
@@ -355,9 +360,9 @@ def test_qk_zero_rows_and_extremes(D):
 
 
 @pytest.mark.parametrize("bits", [torch.int32, torch.int64])
-@pytest.mark.parametrize("D", [128, 30])
-def test_qk_positions_out_of_range(D, bits):
-    q, k, _, wq, wk, cos, sin, pos = qk_inputs(2, 6, 4, 2, D, D, BF, 25)
+@pytest.mark.parametrize("D,T", [(128, 6), (30, 6), (128, 1500)])
+def test_qk_positions_out_of_range(D, T, bits):
+    q, k, _, wq, wk, cos, sin, pos = qk_inputs(2, T, 4, 2, D, D, BF, 25)
     pos = pos.to(bits)
     good = gdr.qk_norm_rope(q, k, wq, wk, cos, sin, pos)
     bad = pos.clone()
