@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cuda_bf16.h>
+#include <atomic>
 #include <math.h>
 #include <string.h>
 #include <stdint.h>
@@ -157,6 +158,41 @@ inline bool is_aligned(const void* p, size_t a) { return (reinterpret_cast<uintp
 inline bool is_dtype(int d) { return d == GDR_F32 || d == GDR_BF16; }
 inline size_t dtype_size(int d) { return d == GDR_BF16 ? 2 : 4; }
 inline gdr_status launched() { return cudaGetLastError() == cudaSuccess ? GDR_OK : GDR_ERR_CUDA; }
+
+// Lets `fn` use `bytes` of dynamic shared memory; asked of the runtime once per kernel (Tag
+// names it) and device.
+template <typename Tag, typename Fn>
+bool allow_smem(Fn fn, int bytes) {
+  static std::atomic<unsigned> done;             // a bit per device
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const unsigned bit = dev < 32 ? 1u << dev : 0u;
+  if (done.load(std::memory_order_relaxed) & bit) return true;
+  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return false;
+  }
+  done.fetch_or(bit, std::memory_order_relaxed);
+  return true;
+}
+
+// A launch that may begin while the kernel before it in the stream still runs; the launched
+// kernel waits for that one's results itself (griddepcontrol.wait, in every block).
+template <typename Fn, typename... Args>
+gdr_status launch_behind(Fn fn, dim3 grid, int threads, cudaStream_t s, Args... args) {
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, fn, args...) == cudaSuccess) return GDR_OK;
+  (void)cudaGetLastError();
+  return GDR_ERR_CUDA;
+}
 
 // Calls f with a null pointer of the element type that `dtype` names.
 template <typename F>

@@ -631,11 +631,7 @@ size_t plan_bytes(const Plan& p) { return kAlign + p.o_bytes + p.ml_bytes + p.cu
 
 template <int D>
 gdr_status launch_mma(const AttnArgs& a, cudaStream_t s) {
-  if (cudaFuncSetAttribute(paged_mma_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           Mma<D>::SMEM) != cudaSuccess) {
-    (void)cudaGetLastError();
-    return GDR_ERR_CUDA;
-  }
+  if (!allow_smem<Mma<D>>(paged_mma_kernel<D>, Mma<D>::SMEM)) return GDR_ERR_CUDA;
   paged_mma_kernel<D><<<a.blocks, WARPS * 32, Mma<D>::SMEM, s>>>(a);
   return launched();
 }
@@ -731,20 +727,8 @@ gdr_status gdr_paged_decode_attn(const void* q, const void* k_cache, const void*
   }
   if (run != GDR_OK || p.whole) return run;
   // The join may start while the last parts are being written; it waits for them itself.
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.blocks - 1, a.G < p.GH ? a.G : p.GH);
-  cfg.blockDim = dim3(JW * 32);
-  cfg.stream = s;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, paged_join_kernel, a) != cudaSuccess) {
-    (void)cudaGetLastError();
-    return GDR_ERR_CUDA;
-  }
-  return GDR_OK;
+  return launch_behind(paged_join_kernel, dim3(p.blocks - 1, a.G < p.GH ? a.G : p.GH), JW * 32, s,
+                       a);
 }
 
 }  // extern "C"

@@ -57,6 +57,7 @@ constexpr int GW = 8;                            // warps per block
 template <typename I, typename O, int MODE>
 __global__ void __launch_bounds__(GW * 32) qk_any_kernel(QkArgs a) {
   constexpr int J = 8;                           // channels per lane: D <= 256
+  if (MODE == kBwd) asm volatile("griddepcontrol.launch_dependents;");
   __shared__ float row[GW][256];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = a.R >> 1;
   const int per = a.HQ + a.HK + (MODE == kAppend ? a.HK : 0);
@@ -207,6 +208,7 @@ __device__ __forceinline__ float2 mate(const float2* x, int j) {
 template <typename I, typename O, int MODE, bool kNeighbours, int GL>
 __global__ void __launch_bounds__(VT, MODE == kBwd ? 4 : 6) qk_vec_kernel(QkArgs a, VecPlan v) {
   constexpr bool bwd = MODE == kBwd;
+  if (bwd) asm volatile("griddepcontrol.launch_dependents;");
   constexpr int U = 2, K = bwd ? 1 : 2;       // rows under way; at work at a time
   const int lane = threadIdx.x & (GL - 1), half = a.R >> 1, rot = a.R >> 3;
   const bool on = lane * 8 < a.D, turned = lane < rot;
@@ -441,17 +443,27 @@ __global__ void __launch_bounds__(VT, MODE == kBwd ? 4 : 6) qk_vec_kernel(QkArgs
 }
 
 // ------------------------------------------------------------ the weights' gradients
-// One warp per (q or k, channel): the blocks' sums in order, 32 strands then a tree.
-__global__ void __launch_bounds__(256) qk_weight_kernel(const float* part, int blocks, int D,
-                                                        float* dwq, float* dwk) {
-  const int col = (blockIdx.x * 256 + threadIdx.x) >> 5, lane = threadIdx.x & 31;
-  if (col >= 2 * D) return;
+// 32 columns (channels of dq_weight, then dk_weight) a block; row y of its threads adds every
+// SR-th block's sums, then the rows are added in order.
+constexpr int SR = 32;
+__global__ void __launch_bounds__(32 * SR) qk_weight_kernel(const float* part, int blocks, int D,
+                                                            float* dwq, float* dwk) {
+  __shared__ float red[SR][33];
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5, col = blockIdx.x * 32 + x;
+  asm volatile("griddepcontrol.wait;" ::: "memory");       // the sums are written
   float s = 0.f;
-  for (int i = lane; i < blocks; i += 32) s += part[(size_t)i * 2 * D + col];
+  if (col < 2 * D) {
+#pragma unroll 8
+    for (int i = y; i < blocks; i += SR) s += part[(size_t)i * 2 * D + col];
+  }
+  red[y][x] = s;
+  __syncthreads();
+  if (y || col >= 2 * D) return;
+  s = 0.f;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
+  for (int i = 0; i < SR; ++i) s += red[i][x];
   float* out = col < D ? dwq : dwk;
-  if (lane == 0 && out) out[col < D ? col : col - D] = s;
+  if (out) out[col < D ? col : col - D] = s;
 }
 
 // ------------------------------------------------------------ host
@@ -643,8 +655,8 @@ gdr_status gdr_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const vo
   int blocks;
   st = launch<kBwd>(dims, a, nullptr, kMaxBlocks, &blocks, s);
   if (st != GDR_OK || !a.part) return st;
-  qk_weight_kernel<<<(2 * a.D + 7) / 8, 256, 0, s>>>(a.part, blocks, a.D, dq_weight, dk_weight);
-  return launched();
+  return launch_behind(qk_weight_kernel, dim3((2 * a.D + 31) / 32), 32 * SR, s,
+                       (const float*)a.part, blocks, a.D, dq_weight, dk_weight);
 }
 
 gdr_status gdr_qk_norm_rope_append(const void* q, const void* k, const void* v,

@@ -2,7 +2,6 @@
 //
 //   h_t = a_t h_{t-1} + u_t,  a = exp(g),  u = x or (1 - a) x
 //   l_t = dh_t + a_{t+1} l_{t+1};  dx = l (1 - a, gated),  dg = l a (h_{t-1} - x, gated)
-#include <atomic>
 #include <type_traits>
 
 #include "gdr_ops.cuh"
@@ -589,11 +588,7 @@ bool residency(Fn fn, int* active) {
   if (cudaGetDevice(&dev) != cudaSuccess || dev >= kDevices) return false;
   std::atomic<int>* row = table[dev];
   if (!row[0].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, F::SMEM) !=
-        cudaSuccess) {
-      (void)cudaGetLastError();
-      return false;
-    }
+    if (!allow_smem<F>(fn, F::SMEM)) return false;
     for (int s = 1; s <= MAXS; ++s) {
       cudaLaunchAttribute at[1];
       at[0].id = cudaLaunchAttributeClusterDimension;

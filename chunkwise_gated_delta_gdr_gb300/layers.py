@@ -80,6 +80,25 @@ def _lib():
 
 
 # ------------------------------------------------------------------ shared checks
+# A step of a decoder makes a few such calls per layer, each a few microseconds of GPU work:
+# what they cost on the host counts. So the checks below take one pass over a tensor's
+# attributes and work out what is wrong only once something is.
+F32 = torch.float32
+_structs = {}
+
+
+def _struct(cls, *values):
+    """cls(*values), one object per set of values (sizes, strides and flags; the library
+    only reads it)."""
+    key = (cls, values)
+    s = _structs.get(key)
+    if s is None:
+        if len(_structs) >= 4096:
+            _structs.clear()
+        s = _structs[key] = cls(*values)
+    return s
+
+
 def _code(name, t):
     code = _DTYPE.get(t.dtype)
     if code is None:
@@ -89,30 +108,31 @@ def _code(name, t):
 
 def _view(name, t, shape, device):
     """t: a CUDA tensor of this shape on `device`, its last dimension dense."""
+    if t.shape == shape and t.device == device and (t.stride(-1) == 1 or shape[-1] == 1):
+        return
     if t.device != device:
         raise ValueError(f"{name} must be on {device}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    if t.stride(-1) != 1 and shape[-1] != 1:
-        raise ValueError(f"{name} must be dense in its last dimension")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must be dense in its last dimension")
 
 
-def _dense(name, t, shape, device, dtype=torch.float32):
-    """t: None, or a contiguous CUDA tensor of this shape and dtype on `device`."""
+def _dense(name, t, shape, device, dtype=F32):
+    """The address of t: None, or a contiguous CUDA tensor of this shape and dtype on `device`."""
     if t is None:
         return None
+    if t.shape == shape and t.dtype is dtype and t.device == device and t.is_contiguous():
+        return t.data_ptr()
     if t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous tensor on {device}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    return t.data_ptr()
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
 
 
 def _stream(device, stream):
     """Raw handle of `stream` (default: torch's current stream of `device`)."""
-    if device.type != "cuda" or device.index != torch.cuda.current_device():
+    if device.type != "cuda" or device.index != torch._C._cuda_getDevice():
         raise ValueError(f"tensors must be on the current CUDA device, got {device}")
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(device.index)
@@ -152,12 +172,14 @@ def linear_scan_fwd(x, g, initial_state=None, *, gated_input: bool = False,
     Returns (h [B,T,D] of out_dtype, default x's; final_state fp32 [B,D] or None).
     Asynchronous on ``stream`` (default: torch's current stream).
     """
-    shape, device = tuple(x.shape), x.device
+    shape, device = x.shape, x.device
     if len(shape) != 3:
         raise ValueError("x must be [B, T, D]")
     B, T, D = shape
     raw = _stream(device, stream)
-    _view("x", x, shape, device)
+    xs, gs = x.stride(), g.stride()
+    if xs[2] != 1 and D != 1:
+        raise ValueError("x must be dense in its last dimension")
     _view("g", g, shape, device)
     if out is None:
         out = torch.empty(shape, dtype=out_dtype or x.dtype, device=device)
@@ -167,9 +189,8 @@ def linear_scan_fwd(x, g, initial_state=None, *, gated_input: bool = False,
     if final_state is None and output_final_state:
         final_state = torch.empty(B, D, dtype=torch.float32, device=device)
         _hold(stream, final_state)
-    xs, gs = x.stride(), g.stride()
-    dims = gdr_scan_dims(B, T, D, _code("x", x), _code("g", g), _code("out", out),
-                         bool(gated_input), xs[0], xs[1], gs[0], gs[1], 0, 0)
+    dims = _struct(gdr_scan_dims, B, T, D, _code("x", x), _code("g", g), _code("out", out),
+                   bool(gated_input), xs[0], xs[1], gs[0], gs[1], 0, 0)
     state = (B, D)
     st = _lib().gdr_linear_scan_fwd(
         x.data_ptr(), g.data_ptr(), _dense("initial_state", initial_state, state, device),
@@ -188,7 +209,7 @@ def linear_scan_bwd(dh, x, g, checkpoints, d_final_state=None, *, gated_input: b
     in the forward call, ``checkpoints`` as it filled them, d_final_state fp32 [B,D] or
     None. Returns (dx of x's dtype, dg of g's dtype, d_initial_state fp32 [B,D] or None).
     """
-    shape, device = tuple(x.shape), x.device
+    shape, device = x.shape, x.device
     if len(shape) != 3:
         raise ValueError("x must be [B, T, D]")
     B, T, D = shape
@@ -207,8 +228,8 @@ def linear_scan_bwd(dh, x, g, checkpoints, d_final_state=None, *, gated_input: b
         d_initial_state = torch.empty(B, D, dtype=torch.float32, device=device)
         _hold(stream, d_initial_state)
     xs, gs, ds = x.stride(), g.stride(), dh.stride()
-    dims = gdr_scan_dims(B, T, D, _code("x", x), _code("g", g), _code("dh", dh),
-                         bool(gated_input), xs[0], xs[1], gs[0], gs[1], ds[0], ds[1])
+    dims = _struct(gdr_scan_dims, B, T, D, _code("x", x), _code("g", g), _code("dh", dh),
+                   bool(gated_input), xs[0], xs[1], gs[0], gs[1], ds[0], ds[1])
     state = (B, D)
     st = _lib().gdr_linear_scan_bwd(
         dh.data_ptr(), x.data_ptr(), g.data_ptr(),
@@ -255,12 +276,12 @@ def _qk_dims(q, k, v, cos, sin, positions, eps, interleaved, out_code):
             raise TypeError("q, k and v must have one dtype")
         vs = v.stride()
     qs, ks = q.stride(), k.stride()
-    return gdr_qk_dims(B, T, HQ, HK, D, R, _code("q", q), out_code, bool(interleaved), bits, rows,
-                       eps, qs[0], qs[1], qs[2], ks[0], ks[1], ks[2], vs[0], vs[1], vs[2])
+    return _struct(gdr_qk_dims, B, T, HQ, HK, D, R, _code("q", q), out_code, bool(interleaved), bits,
+                   rows, eps, qs[0], qs[1], qs[2], ks[0], ks[1], ks[2], vs[0], vs[1], vs[2])
 
 
 def _qk_shared(q_weight, k_weight, cos, sin, positions, D, device):
-    half = None if cos is None else tuple(cos.shape)
+    half = None if cos is None else cos.shape
     return (_dense("q_weight", q_weight, (D,), device), _dense("k_weight", k_weight, (D,), device),
             _dense("cos", cos, half, device), _dense("sin", sin, half, device),
             None if positions is None else positions.data_ptr())
@@ -341,15 +362,16 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, cos=Non
 def _cache_dims(k_cache, v_cache, page_table, B, device):
     if k_cache.dim() != 4 or page_table.dim() != 2:
         raise ValueError("caches must be [pages, page_size, heads, D], page_table [B, max_pages]")
-    shape = tuple(k_cache.shape)
-    _view("k_cache", k_cache, shape, device)
-    _view("v_cache", v_cache, shape, device)
-    if v_cache.dtype != k_cache.dtype or v_cache.stride() != k_cache.stride():
+    shape, ps = k_cache.shape, k_cache.stride()
+    if k_cache.device != device or (ps[3] != 1 and shape[3] != 1):
+        _view("k_cache", k_cache, shape, device)
+    if v_cache is not k_cache and (v_cache.shape != shape or v_cache.device != device):
+        _view("v_cache", v_cache, shape, device)
+    if v_cache.dtype != k_cache.dtype or v_cache.stride() != ps:
         raise ValueError("k_cache and v_cache must have one dtype and one layout")
     _dense("page_table", page_table, (B, page_table.shape[1]), device, torch.int32)
-    ps = k_cache.stride()
-    return gdr_paged_cache(shape[0], shape[1], shape[2], shape[3], _code("k_cache", k_cache),
-                           page_table.shape[1], ps[0], ps[1], ps[2])
+    return _struct(gdr_paged_cache, shape[0], shape[1], shape[2], shape[3],
+                   _code("k_cache", k_cache), page_table.shape[1], ps[0], ps[1], ps[2])
 
 
 def qk_norm_rope_append(q, k, v, q_weight, k_weight, cos, sin, positions, k_cache, v_cache,
@@ -394,7 +416,8 @@ def _attn_dims(q, k_cache, v_cache, page_table, scale, window, out_code):
     _view("q", q, (B, HQ, cache.D), q.device)
     qs = q.stride()
     scale = 1.0 / math.sqrt(D) if scale is None else scale
-    return gdr_attn_dims(B, HQ, _code("q", q), out_code, window, scale, qs[0], qs[1]), cache
+    return _struct(gdr_attn_dims, B, HQ, _code("q", q), out_code, window, scale, qs[0],
+                   qs[1]), cache
 
 
 def paged_decode_attn_workspace_size(q, k_cache, page_table) -> int:
@@ -419,7 +442,7 @@ def paged_decode_attn(q, k_cache, v_cache, page_table, lens, *, scale: Optional[
     [B,HQ]). A sequence without keys gives zeros and -inf; a length or a page out of
     range gives NaN.
     """
-    shape, device = tuple(q.shape), q.device
+    shape, device = q.shape, q.device
     raw = _stream(device, stream)
     if out is None:
         out = torch.empty(shape, dtype=out_dtype or q.dtype, device=device)
