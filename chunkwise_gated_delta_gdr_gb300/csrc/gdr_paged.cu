@@ -34,7 +34,8 @@ struct AttnArgs {
   void* out;
   float* lse;                     // may be null
   float *part_o, *part_ml;        // [blocks][2][GMAX][D], [blocks][2][GMAX][2]
-  int4* cut;                      // [blocks]: the item that block c began and left unfinished
+  int4* cut;                      // notes of the items left unfinished (see note_of)
+  int by_item, hb;                // how notes are numbered; heads per join block
   int B, HQ, HK, D, G, GH, groups;  // G = HQ / HK; GH query heads per item, groups per kv head
   int page, shift;                // shift: log2(page) if page is a power of two, else -1
   int num_pages, max_pages, window, whole, blocks, out_bf16, q_bf16;
@@ -131,6 +132,9 @@ __device__ __forceinline__ void empty_rows(const AttnArgs& a) {
   for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
     const Span s = span_of(a, b);
     if (s.tiles()) continue;
+    if (a.by_item)
+      for (int i = threadIdx.x; i < a.HK * a.groups; i += blockDim.x)
+        a.cut[b * (a.HK * a.groups) + i] = make_int4(0, 0, 0, 0);
     const float o = s.ok ? 0.f : NAN;
     for (int i = threadIdx.x; i < a.HQ * a.D; i += blockDim.x)
       put(a.out, (size_t)b * a.HQ * a.D + i, o, a.out_bf16);
@@ -151,7 +155,7 @@ __device__ __forceinline__ long long stretch(const AttnArgs& a, int lane, Place*
     p->s = span_of(a, p->b);
     return p->s.tiles();
   }
-  if (threadIdx.x == 0) a.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
+  if (threadIdx.x == 0 && !a.by_item) a.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
   const long long total = total_tiles(a, lane), per = (total + a.blocks - 1) / a.blocks;
   const long long first = blockIdx.x * per, last = min(total, first + per);
   if (first >= last) return 0;
@@ -160,11 +164,17 @@ __device__ __forceinline__ long long stretch(const AttnArgs& a, int lane, Place*
   return last - first;
 }
 
-// Thread 0 of a block that leaves an item it began: `rest` of its tiles go to later blocks.
-__device__ __forceinline__ void leave_cut(const AttnArgs& a, const Place& p, int rest,
-                                          long long per) {
-  if (threadIdx.x == 0)
-    a.cut[blockIdx.x] = make_int4(p.b, p.item, 1 + (int)((rest + per - 1) / per), 0);
+// The note of an item cut by a block boundary: {sequence, item, parts, first block}. Few
+// items: one note per item, written by the block that begins it; many: one per block, of the
+// one item it may begin and leave. parts < 2: nothing to join.
+__device__ __forceinline__ int4* note_of(const AttnArgs& a, const Place& p) {
+  return a.cut + (a.by_item ? p.b * (a.HK * a.groups) + p.item : (int)blockIdx.x);
+}
+// Thread 0 of a block that ends its work on an item it began, `rest` tiles before its end.
+__device__ __forceinline__ void write_note(const AttnArgs& a, const Place& p, int rest,
+                                           long long per) {
+  if (threadIdx.x == 0 && !a.whole && (a.by_item || rest > 0))
+    *note_of(a, p) = make_int4(p.b, p.item, 1 + (int)((rest + per - 1) / per), blockIdx.x);
 }
 
 // Element offset of key j of sequence b (kv head 0), or -1 for a bad table entry.
@@ -194,7 +204,7 @@ __device__ __forceinline__ void load4(const T* row, int ch, int D, bool vec, flo
 
 template <typename T, int NC, int GH>
 __global__ void __launch_bounds__(WARPS * 32) paged_any_kernel(AttnArgs a, int vec) {
-  constexpr int DP = NC * 32;
+  constexpr int DP = NC * 32, KU = NC == 2 ? 4 : NC == 4 ? 2 : 1;   // keys in flight per octet
   __shared__ float so[WARPS][GH][DP], sml[WARPS][GH][2];
   asm volatile("griddepcontrol.launch_dependents;");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane & 7, oct = lane >> 3;
@@ -224,50 +234,69 @@ __global__ void __launch_bounds__(WARPS * 32) paged_any_kernel(AttnArgs a, int v
       }
     }
     const int end = min(p.s.n, p.s.lo + t1 * TILE);
-    for (int j0 = p.s.lo + p.tile * TILE + warp * 4; j0 < end; j0 += WARPS * 4) {
-      const int j = j0 + oct;
-      const bool live = j < end;
-      const int64_t row = live ? key_row(a, p.b, j) : -1;
-      float s[GH], vv[NC * 4];
+    const T* kc = static_cast<const T*>(a.kc) + hk * a.ph;
+    const T* vc = static_cast<const T*>(a.vc) + hk * a.ph;
+    // KU keys per octet at a time; the next ones' pages are looked up meanwhile.
+    int j0 = p.s.lo + p.tile * TILE + warp * 4 + oct;
+    int64_t row[KU];
+    auto find = [&](int j) {
 #pragma unroll
-      for (int g = 0; g < GH; ++g) s[g] = 0.f;
-      if (row >= 0) {
-        const T* kr = static_cast<const T*>(a.kc) + row + hk * a.ph;
-        const T* vr = static_cast<const T*>(a.vc) + row + hk * a.ph;
+      for (int u = 0; u < KU; ++u)               // -1: bad page, -2: no such key
+        row[u] = j + 16 * u < end ? key_row(a, p.b, j + 16 * u) : -2;
+    };
+    find(j0);
+    for (int jw = j0 - oct; jw < end; jw += 16 * KU, j0 += 16 * KU) {
+      float s[KU][GH], vv[KU][NC * 4];
+      int64_t at[KU];
+#pragma unroll
+      for (int u = 0; u < KU; ++u) at[u] = row[u];
+#pragma unroll
+      for (int u = 0; u < KU; ++u) {
         float kv[NC * 4];
 #pragma unroll
-        for (int i = 0; i < NC; ++i) load4<T>(kr, 4 * (c + 8 * i), a.D, vec, kv + 4 * i);
+        for (int i = 0; i < NC * 4; ++i) kv[i] = vv[u][i] = 0.f;
+        if (at[u] >= 0) {
 #pragma unroll
-        for (int i = 0; i < NC; ++i) load4<T>(vr, 4 * (c + 8 * i), a.D, vec, vv + 4 * i);
+          for (int i = 0; i < NC; ++i) load4<T>(kc + at[u], 4 * (c + 8 * i), a.D, vec, kv + 4 * i);
 #pragma unroll
-        for (int g = 0; g < GH; ++g)
+          for (int i = 0; i < NC; ++i)
+            load4<T>(vc + at[u], 4 * (c + 8 * i), a.D, vec, vv[u] + 4 * i);
+        }
 #pragma unroll
-          for (int i = 0; i < NC * 4; ++i) s[g] = fmaf(q[g][i], kv[i], s[g]);
+        for (int g = 0; g < GH; ++g) {
+          s[u][g] = 0.f;
+#pragma unroll
+          for (int i = 0; i < NC * 4; ++i) s[u][g] = fmaf(q[g][i], kv[i], s[u][g]);
+        }
       }
+      find(j0 + 16 * KU);
+#pragma unroll
+      for (int x = 4; x > 0; x >>= 1)
+#pragma unroll
+        for (int u = 0; u < KU; ++u)
+#pragma unroll
+          for (int g = 0; g < GH; ++g) s[u][g] += __shfl_xor_sync(~0u, s[u][g], x);
 #pragma unroll
       for (int g = 0; g < GH; ++g) {
+        float top = m[g];
 #pragma unroll
-        for (int x = 4; x > 0; x >>= 1) s[g] += __shfl_xor_sync(~0u, s[g], x);
-      }
-      if (!live) continue;                       // whole octets, after the shuffles
-      if (row < 0) {                             // a bad page poisons the item
-#pragma unroll
-        for (int g = 0; g < GH; ++g) l[g] = NAN;
-        continue;
-      }
-#pragma unroll
-      for (int g = 0; g < GH; ++g) {
-        if (s[g] > m[g]) {
-          const float f = exp2f(m[g] - s[g]);    // 0 from -inf
-          m[g] = s[g];
+        for (int u = 0; u < KU; ++u) top = fmaxf(top, at[u] == -2 ? -INFINITY : s[u][g]);
+        if (top > m[g]) {
+          const float f = exp2f(m[g] - top);     // 0 from -inf
+          m[g] = top;
           l[g] *= f;
 #pragma unroll
           for (int i = 0; i < NC * 4; ++i) o[g][i] *= f;
         }
-        const float w = exp2f(s[g] - (m[g] == -INFINITY ? 0.f : m[g]));
-        l[g] += w;
+        const float base = m[g] == -INFINITY ? 0.f : m[g];
 #pragma unroll
-        for (int i = 0; i < NC * 4; ++i) o[g][i] = fmaf(w, vv[i], o[g][i]);
+        for (int u = 0; u < KU; ++u) {
+          // A bad page poisons the item.
+          const float w = at[u] == -2 ? 0.f : at[u] == -1 ? NAN : exp2f(s[u][g] - base);
+          l[g] += w;
+#pragma unroll
+          for (int i = 0; i < NC * 4; ++i) o[g][i] = fmaf(w, vv[u][i], o[g][i]);
+        }
       }
     }
     __syncwarp();
@@ -296,7 +325,7 @@ __global__ void __launch_bounds__(WARPS * 32) paged_any_kernel(AttnArgs a, int v
     __syncthreads();
     const bool done = p.tile == 0 && t1 == tiles;
     const size_t slot = (size_t)blockIdx.x * 2 + (p.tile == 0 ? 1 : 0);
-    if (!done && p.tile == 0) leave_cut(a, p, tiles - t1, per);
+    if (p.tile == 0) write_note(a, p, tiles - t1, per);
     for (int e = threadIdx.x; e < heads * a.D; e += WARPS * 32) {
       const int g = e / a.D, d = e - g * a.D;
       float mm = -INFINITY, ll = 0.f, oo = 0.f;
@@ -508,7 +537,7 @@ __global__ void __launch_bounds__(WARPS * 32, Mma<D>::OCC) paged_mma_kernel(Attn
       __syncthreads();
       const bool done = tile0 == 0 && pc.tile + 1 == tiles;
       const size_t part = (size_t)blockIdx.x * 2 + (tile0 == 0 ? 1 : 0);
-      if (!done && tile0 == 0) leave_cut(a, pc, tiles - pc.tile - 1, per);
+      if (tile0 == 0) write_note(a, pc, tiles - pc.tile - 1, per);
       for (int e = threadIdx.x; e < heads * D; e += WARPS * 32) {
         const int g = e / D, d = e - g * D;
         float mm = -INFINITY, ll = 0.f, oo = 0.f;
@@ -544,47 +573,55 @@ __global__ void __launch_bounds__(WARPS * 32, Mma<D>::OCC) paged_mma_kernel(Attn
 }
 
 // ------------------------------------------------------------ items cut by block boundaries
-// Block (c, g): head g of the item that block c began and later blocks went on with, if
-// there is one. Four warps take every fourth part, a lane the channels lane, lane + 32, ...
-constexpr int JW = 4;
+// Block (x, y): heads y hb .. y hb + hb - 1 of note x's item. JW / hb warps share a head,
+// each takes every so manieth part, a lane the channels lane, lane + 32, ...
+constexpr int JW = 8;
 __global__ void __launch_bounds__(JW * 32) paged_join_kernel(AttnArgs a) {
-  __shared__ float red[JW][256], sum[JW];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = blockIdx.y;
+  __shared__ float red[JW][256], sum[JW], top[JW];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, pw = JW / a.hb;
+  const int hl = warp / pw, w0 = warp - hl * pw, g = blockIdx.y * a.hb + hl;
   asm volatile("griddepcontrol.wait;" ::: "memory");       // the parts are written
   const int4 cut = a.cut[blockIdx.x];
-  const int c0 = blockIdx.x, parts = cut.z, hk = cut.y / a.groups;
-  const int g0 = (cut.y - hk * a.groups) * a.GH;
-  if (parts < 2 || g >= min(a.GH, a.G - g0)) return;
+  const int parts = cut.z, c0 = cut.w, hk = cut.y / a.groups;
+  const int g0 = (cut.y - hk * a.groups) * a.GH, heads = min(a.GH, a.G - g0);
+  if (parts < 2) return;
   auto slot = [&](int c) { return ((size_t)(c0 + c) * 2 + (c == 0)) * GMAX + g; };
-  float m = -INFINITY;
-  for (int c = lane; c < parts; c += 32) m = fmaxf(m, a.part_ml[slot(c) * 2]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-  float l = 0.f, o[8];
+  auto ml_of = [&](int c) { return *reinterpret_cast<const float2*>(a.part_ml + slot(c) * 2); };
+  float m = -INFINITY, l = 0.f, o[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) o[i] = 0.f;
-#pragma unroll 4
-  for (int c = warp; c < parts; c += JW) {
-    const size_t s = slot(c);
-    const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + s * 2);
-    const float f = ml.x == -INFINITY ? 1.f : exp2f(ml.x - m);
-    l = fmaf(f, ml.y, l);
+  if (g < heads) {
+    for (int c = lane; c < parts; c += 32) m = fmaxf(m, ml_of(c).x);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (lane + 32 * i < a.D) o[i] = fmaf(f, a.part_o[s * a.D + lane + 32 * i], o[i]);
+    for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, x));
+#pragma unroll 4
+    for (int c = w0; c < parts; c += pw) {
+      const size_t s = slot(c);
+      const float2 ml = ml_of(c);
+      const float f = ml.x == -INFINITY ? 1.f : exp2f(ml.x - m);
+      l = fmaf(f, ml.y, l);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (lane + 32 * i < a.D) o[i] = fmaf(f, a.part_o[s * a.D + lane + 32 * i], o[i]);
+    }
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) red[warp][lane + 32 * i] = o[i];
-  if (lane == 0) sum[warp] = l;
+  if (lane == 0) {
+    sum[warp] = l;
+    top[warp] = m;
+  }
   __syncthreads();
-  l = 0.f;
-#pragma unroll
-  for (int w = 0; w < JW; ++w) l += sum[w];
-  for (int d = threadIdx.x; d < a.D; d += JW * 32) {
+  for (int e = threadIdx.x; e < a.hb * a.D; e += JW * 32) {
+    const int h = e / a.D, d = e - h * a.D;
+    if (blockIdx.y * a.hb + h >= heads) break;
     float v = 0.f;
-#pragma unroll
-    for (int w = 0; w < JW; ++w) v += red[w][d];
-    finish(a, cut.x, hk * a.G + g0 + g, d, m, l, v);
+    l = 0.f;
+    for (int w = h * pw; w < (h + 1) * pw; ++w) {
+      l += sum[w];
+      v += red[w][d];
+    }
+    finish(a, cut.x, hk * a.G + g0 + blockIdx.y * a.hb + h, d, top[h * pw], l, v);
   }
 }
 
@@ -594,7 +631,7 @@ constexpr long long kMaxKeys = (1LL << 31) - 1024;   // tile ends stay within an
 constexpr int kWholeTiles = 4;    // capacity up to which one block takes a whole item
 
 struct Plan {
-  int mma, GH, groups, whole, blocks;
+  int mma, GH, groups, whole, blocks, by_item, notes, hb;
   size_t o_bytes, ml_bytes, cut_bytes;
 };
 
@@ -623,6 +660,13 @@ Plan make_plan(const gdr_attn_dims* d, const gdr_paged_cache* c, bool mma) {
                      : kSms * (c->D <= 64 ? 4 : 2);
   p.o_bytes = p.whole ? 0 : align_up((size_t)p.blocks * 2 * GMAX * c->D * sizeof(float));
   p.ml_bytes = p.whole ? 0 : align_up((size_t)p.blocks * 2 * GMAX * 2 * sizeof(float));
+  // Notes per item where that makes fewer of them; then as many join blocks as keep a few
+  // parts per warp.
+  p.by_item = !p.whole && items <= p.blocks;
+  p.notes = p.by_item ? (int)items : p.blocks;
+  const int heads = G < p.GH ? G : p.GH;
+  p.hb = 8;
+  while (p.hb > 1 && (p.hb >= 2 * heads || (long long)p.notes * heads / p.hb < 2 * kSms)) p.hb /= 2;
   p.cut_bytes = p.whole ? 0 : align_up((size_t)p.blocks * sizeof(int4));
   return p;
 }
@@ -697,6 +741,7 @@ gdr_status gdr_paged_decode_attn(const void* q, const void* k_cache, const void*
   a.num_pages = cache->num_pages; a.max_pages = cache->max_pages;
   a.window = dims->window; a.whole = p.whole; a.blocks = p.blocks;
   a.out_bf16 = dims->out_dtype == GDR_BF16; a.q_bf16 = dims->q_dtype == GDR_BF16;
+  a.by_item = p.by_item; a.hb = p.hb;
   a.scale2 = dims->scale * LOG2E;
   a.qb = dims->q_stride_b; a.qh = dims->q_stride_h;
   a.pp = cache->page_stride; a.pt = cache->token_stride; a.ph = cache->head_stride;
@@ -727,8 +772,8 @@ gdr_status gdr_paged_decode_attn(const void* q, const void* k_cache, const void*
   }
   if (run != GDR_OK || p.whole) return run;
   // The join may start while the last parts are being written; it waits for them itself.
-  return launch_behind(paged_join_kernel, dim3(p.blocks - 1, a.G < p.GH ? a.G : p.GH), JW * 32, s,
-                       a);
+  const int heads = a.G < p.GH ? a.G : p.GH;
+  return launch_behind(paged_join_kernel, dim3(p.notes, (heads + p.hb - 1) / p.hb), JW * 32, s, a);
 }
 
 }  // extern "C"
