@@ -358,24 +358,27 @@ __global__ void __launch_bounds__(WARPS * 32) paged_any_kernel(AttnArgs a, int v
 // 16 keys of a tile at a time and needs nobody else for them: it copies its own K and V rows
 // (16-byte pieces, gathered by page) into its own ring of ST slots, forms S = Q K^T, the
 // softmax weights and O += P V from there with its own running maximum and sums, and the
-// four warps meet once per item. K and V pass through shared memory once; rows are padded
-// to an odd number of 16-byte pieces, which keeps the matrix loads free of bank conflicts
-// for every D.
+// four warps meet once per item. K and V pass through shared memory once; the pieces of a
+// row are swizzled by the row's number in rows of a multiple of 128 bytes, so that neither
+// the matrix loads conflict nor the copies split (rows padded to an odd number of pieces
+// cost 1.5 times the L2 reads).
 template <int D>
 struct Mma {
-  static constexpr int C = D / 8, RS = (C | 1) * 16;     // pieces per row, bytes per padded row
+  static constexpr int C = D / 8, RS = (C + 7) / 8 * 128;   // pieces per row, bytes per row
   static constexpr int SLOT = 2 * 16 * RS, ST = 3, KS = D / 16;
   static constexpr int SMEM = WARPS * ST * SLOT;
   static constexpr int OCC = D <= 64 ? 4 : D <= 128 ? 2 : 1;
-  static constexpr int OS = D + 8;                       // floats per row of a merged slot
-  static_assert(16 * OS * 4 <= SLOT, "a slot holds a warp's sums");
+  static constexpr int OS = RS / 2;                      // floats per row of a warp's sums,
+  static_assert(16 * OS * 4 == SLOT, "which fill its slot");
+  // Where channel d of row g of the sums lies (swizzled likewise).
+  __device__ static int sum_at(int g, int d) { return g * OS + (d ^ ((g & 7) << 3)); }
 };
 
 template <int D>
 __global__ void __launch_bounds__(WARPS * 32, Mma<D>::OCC) paged_mma_kernel(AttnArgs a) {
   using M = Mma<D>;
   constexpr int C = M::C, RS = M::RS, ST = M::ST, KS = M::KS;
-  extern __shared__ __align__(16) char ring[];
+  extern __shared__ __align__(128) char ring[];
   __shared__ float sml[WARPS][16][2];
   __shared__ int sbad[WARPS][ST];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = lane >> 2, quad = lane & 3;
@@ -409,8 +412,9 @@ __global__ void __launch_bounds__(WARPS * 32, Mma<D>::OCC) paged_mma_kernel(Attn
         const int e = lane + 32 * i, r = e / C, ch = e - r * C;
         const int64_t o = __shfl_sync(~0u, off, r);
         const int64_t at = o < 0 ? 0 : o + ch * 8;
-        ptx::cp_async16(kd + r * RS + ch * 16, kc + at, o < 0 ? 0 : 16);
-        ptx::cp_async16(vd + r * RS + ch * 16, vc + at, o < 0 ? 0 : 16);
+        const uint32_t to = r * RS + ((ch ^ (r & 7)) << 4);
+        ptx::cp_async16(kd + to, kc + at, o < 0 ? 0 : 16);
+        ptx::cp_async16(vd + to, vc + at, o < 0 ? 0 : 16);
       }
       if (--to_copy > 0) {                       // the next tile's rows, looked up meanwhile
         if (++pi.tile == pi.s.tiles()) next_item(a, pi);
@@ -448,8 +452,10 @@ __global__ void __launch_bounds__(WARPS * 32, Mma<D>::OCC) paged_mma_kernel(Attn
   };
   begin();
 
-  const int mrow = (lane & 7) + (lane >> 4) * 8, mch = (lane >> 3) & 1;   // K: key, piece
-  const int vrow = (lane & 7) + ((lane >> 3) & 1) * 8, vch = lane >> 4;   // V: key, piece
+  // Row and first piece (swizzled, as a byte offset) of this lane's matrix rows in K and V.
+  const int krow = ((lane & 7) + (lane >> 4) * 8) * RS;
+  const int vrow = ((lane & 7) + ((lane >> 3) & 1) * 8) * RS;
+  const int kpc = (((lane >> 3) & 1) ^ (lane & 7)) << 4, vpc = ((lane >> 4) ^ (lane & 7)) << 4;
   for (int slot = 0;; slot = slot + 1 == ST ? 0 : slot + 1) {
     ptx::cp_async_wait<ST - 1>();
     __syncwarp();
@@ -464,7 +470,7 @@ __global__ void __launch_bounds__(WARPS * 32, Mma<D>::OCC) paged_mma_kernel(Attn
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
         uint32_t f[4];
-        ptx::ldsm_x4(f, kd + mrow * RS + (2 * k + mch) * 16);
+        ptx::ldsm_x4(f, kd + krow + (kpc ^ (32 * k)));
         ptx::mma_bf16_16816(s[0], q[k], f[0], f[1]);
         ptx::mma_bf16_16816(s[1], q[k], f[2], f[3]);
       }
@@ -509,7 +515,7 @@ __global__ void __launch_bounds__(WARPS * 32, Mma<D>::OCC) paged_mma_kernel(Attn
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
         uint32_t f[4];
-        ptx::ldsm_x4_t(f, vd + vrow * RS + (2 * i + vch) * 16);
+        ptx::ldsm_x4_t(f, vd + vrow + (vpc ^ (32 * i)));
         ptx::mma_bf16_16816(o[2 * i], p, f[0], f[1]);
         ptx::mma_bf16_16816(o[2 * i + 1], p, f[2], f[3]);
       }
@@ -532,7 +538,7 @@ __global__ void __launch_bounds__(WARPS * 32, Mma<D>::OCC) paged_mma_kernel(Attn
       for (int i = 0; i < D / 8; ++i)
 #pragma unroll
         for (int r = 0; r < 2; ++r)
-          *reinterpret_cast<float2*>(so + (row + 8 * r) * M::OS + 8 * i + 2 * quad) =
+          *reinterpret_cast<float2*>(so + M::sum_at(row + 8 * r, 8 * i + 2 * quad)) =
               make_float2(o[i][2 * r], o[i][2 * r + 1]);
       __syncthreads();
       const bool done = tile0 == 0 && pc.tile + 1 == tiles;
@@ -548,7 +554,7 @@ __global__ void __launch_bounds__(WARPS * 32, Mma<D>::OCC) paged_mma_kernel(Attn
           const float f = sml[w][g][0] == -INFINITY ? 1.f : exp2f(sml[w][g][0] - mm);
           ll = fmaf(f, sml[w][g][1], ll);
           oo = fmaf(f, *reinterpret_cast<const float*>(ring + (w * ST + slot) * M::SLOT +
-                                                       (g * M::OS + d) * 4), oo);
+                                                       M::sum_at(g, d) * 4), oo);
         }
         if (done) {
           finish(a, pc.b, hq0 + g, d, mm, ll, oo);
