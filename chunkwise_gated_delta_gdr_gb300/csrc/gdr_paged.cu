@@ -353,88 +353,39 @@ __global__ void __launch_bounds__(WARPS * 32) paged_any_kernel(AttnArgs a, int v
   }
 }
 
-// ------------------------------------------------------------ bf16 on the tensor cores
-// The 16 rows of an m16n8k16 product are the query heads that share a kv head. A warp takes
-// 16 keys of a tile at a time and needs nobody else for them: it copies its own K and V rows
-// (16-byte pieces, gathered by page) into its own ring of ST slots, forms S = Q K^T, the
-// softmax weights and O += P V from there with its own running maximum and sums, and the
-// four warps meet once per item. K and V pass through shared memory once; the pieces of a
-// row are swizzled by the row's number in rows of a multiple of 128 bytes, so that neither
-// the matrix loads conflict nor the copies split (rows padded to an odd number of pieces
-// cost 1.5 times the L2 reads).
+// ------------------------------------------------------------ rings of gathered rows
+// A warp takes KEYS keys of a tile at a time (SUB such steps, so that NW warps cover the
+// tile) and needs nobody else for them: it copies its own K and V rows (16-byte pieces,
+// gathered by page) into its own ring of ST slots, and keeps a running maximum and sums of
+// its own; the warps meet once per item, each leaving its sums in the slot it has just used
+// up. The pieces of a row are swizzled by the row's number in rows of a multiple of 128
+// bytes, so that neither the reads conflict nor the copies split (rows padded to an odd
+// number of pieces cost 1.5 times the L2 reads). A Core is the arithmetic on a slot.
+
+// bf16 on the tensor cores. The 16 rows of an m16n8k16 product are the query heads that
+// share a kv head: S = Q K^T, the softmax in registers, O += P V. The work is bound by the
+// bytes of the cache, not by the products (a few % of the tensor rate at 8 heads), so what
+// matters is that a row passes through shared memory once and that 100 KB or more of copies
+// are under way per SM.
 template <int D>
-struct Mma {
-  static constexpr int C = D / 8, RS = (C + 7) / 8 * 128;   // pieces per row, bytes per row
-  static constexpr int SLOT = 2 * 16 * RS, ST = 3, KS = D / 16;
-  static constexpr int SMEM = WARPS * ST * SLOT;
+struct MmaCore {
+  typedef bf16 T;
+  static constexpr int DIM = D, NW = 4, KEYS = 16, SUB = 1, ST = 3, HEADS = GMAX, KS = D / 16;
+  static constexpr int C = D / 8, RS = (C + 7) / 8 * 128, SLOT = 2 * KEYS * RS;
   static constexpr int OCC = D <= 64 ? 4 : D <= 128 ? 2 : 1;
-  static constexpr int OS = RS / 2;                      // floats per row of a warp's sums,
+  static constexpr int QS = 0;                   // floats of shared memory for q
+  static constexpr int OS = RS / 2;              // floats per row of a warp's sums,
   static_assert(16 * OS * 4 == SLOT, "which fill its slot");
-  // Where channel d of row g of the sums lies (swizzled likewise).
+  __device__ static int piece(int r, int ch) { return (ch ^ (r & 7)) << 4; }
+  // Where channel d of head g of the sums lies (swizzled likewise).
   __device__ static int sum_at(int g, int d) { return g * OS + (d ^ ((g & 7) << 3)); }
-};
-
-template <int D>
-__global__ void __launch_bounds__(WARPS * 32, Mma<D>::OCC) paged_mma_kernel(AttnArgs a) {
-  using M = Mma<D>;
-  constexpr int C = M::C, RS = M::RS, ST = M::ST, KS = M::KS;
-  extern __shared__ __align__(128) char ring[];
-  __shared__ float sml[WARPS][16][2];
-  __shared__ int sbad[WARPS][ST];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = lane >> 2, quad = lane & 3;
-  asm volatile("griddepcontrol.launch_dependents;");
-  empty_rows(a);
-  Place pc;                                      // the tile being computed
-  long long per = 1, left = stretch(a, lane, &pc, &per);
-  if (left <= 0) return;
-  Place pi = pc;                                 // the tile being copied
-  long long to_copy = left;
-  char* slots = ring + warp * ST * M::SLOT;
-  const uint32_t slots_u = ptx::smem_u32(slots);
-  const bf16* kc = static_cast<const bf16*>(a.kc);
-  const bf16* vc = static_cast<const bf16*>(a.vc);
-
-  // Where this lane's key of the tile at pi starts (-1: bad page, -2: no such key).
-  auto find = [&]() -> int64_t {
-    const int j = pi.s.lo + pi.tile * TILE + warp * 16 + (lane & 15);
-    if (j >= pi.s.n) return -2;
-    const int64_t r = key_row(a, pi.b, j);
-    return r < 0 ? -1 : r + (pi.item / a.groups) * a.ph;
-  };
-  int64_t off = find();
-  auto copy = [&](int slot) {
-    if (to_copy > 0) {
-      const unsigned bad = __ballot_sync(~0u, off == -1);
-      if (lane == 0) sbad[warp][slot] = bad != 0;
-      const uint32_t kd = slots_u + slot * M::SLOT, vd = kd + 16 * RS;
-#pragma unroll
-      for (int i = 0; i < C / 2; ++i) {
-        const int e = lane + 32 * i, r = e / C, ch = e - r * C;
-        const int64_t o = __shfl_sync(~0u, off, r);
-        const int64_t at = o < 0 ? 0 : o + ch * 8;
-        const uint32_t to = r * RS + ((ch ^ (r & 7)) << 4);
-        ptx::cp_async16(kd + to, kc + at, o < 0 ? 0 : 16);
-        ptx::cp_async16(vd + to, vc + at, o < 0 ? 0 : 16);
-      }
-      if (--to_copy > 0) {                       // the next tile's rows, looked up meanwhile
-        if (++pi.tile == pi.s.tiles()) next_item(a, pi);
-        off = find();
-      }
-    }
-    ptx::cp_async_commit();
-  };
-#pragma unroll
-  for (int i = 0; i < ST; ++i) copy(i);
 
   uint32_t q[KS][4];
   float o[D / 8][4], m[2], l[2];
-  int hq0 = 0, heads = 0, tile0 = 0;
-  auto begin = [&]() {
-    const int hk = pc.item / a.groups, g0 = (pc.item - hk * a.groups) * GMAX;
-    hq0 = hk * a.G + g0;
-    heads = min(GMAX, a.G - g0);
-    tile0 = pc.tile;
-    const bf16* qp = static_cast<const bf16*>(a.q) + pc.b * a.qb + (hq0 + row) * a.qh + 2 * quad;
+
+  __device__ __forceinline__ void begin(const AttnArgs& a, int b, int hq0, int heads, float*) {
+    const int lane = threadIdx.x & 31, row = lane >> 2, quad = lane & 3;
+    const bf16* qp = static_cast<const bf16*>(a.q) + b * a.qb + (hq0 + row) * a.qh + 2 * quad;
 #pragma unroll
     for (int k = 0; k < KS; ++k)
 #pragma unroll
@@ -449,112 +400,336 @@ __global__ void __launch_bounds__(WARPS * 32, Mma<D>::OCC) paged_mma_kernel(Attn
       for (int h = 0; h < 4; ++h) o[i][h] = 0.f;
     m[0] = m[1] = -INFINITY;
     l[0] = l[1] = 0.f;
+  }
+
+  __device__ __forceinline__ void step(const AttnArgs& a, char* slot, int live, bool bad,
+                                       const float*, float*) {
+    const int lane = threadIdx.x & 31, quad = lane & 3;
+    const uint32_t kd = ptx::smem_u32(slot), vd = kd + KEYS * RS;
+    // Row and first piece (swizzled, as a byte offset) of this lane's matrix rows in K and V.
+    const int krow = ((lane & 7) + (lane >> 4) * 8) * RS;
+    const int vrow = ((lane & 7) + ((lane >> 3) & 1) * 8) * RS;
+    const int kpc = (((lane >> 3) & 1) ^ (lane & 7)) << 4, vpc = ((lane >> 4) ^ (lane & 7)) << 4;
+    float s[2][4];
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int h = 0; h < 4; ++h) s[n][h] = 0.f;
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      uint32_t f[4];
+      ptx::ldsm_x4(f, kd + krow + (kpc ^ (32 * k)));
+      ptx::mma_bf16_16816(s[0], q[k], f[0], f[1]);
+      ptx::mma_bf16_16816(s[1], q[k], f[2], f[3]);
+    }
+    float top[2] = {m[0], m[1]};
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        s[n][h] *= a.scale2;
+        if (n * 8 + 2 * quad + (h & 1) >= live) s[n][h] = -INFINITY;
+        top[h >> 1] = fmaxf(top[h >> 1], s[n][h]);
+      }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 1));
+      top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 2));
+    }
+    if (__any_sync(~0u, top[0] > m[0] || top[1] > m[1])) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float f = top[r] > m[r] ? exp2f(m[r] - top[r]) : 1.f;    // 0 from -inf
+        m[r] = top[r];
+        l[r] *= f;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          o[i][2 * r] *= f;
+          o[i][2 * r + 1] *= f;
+        }
+      }
+    }
+    const float base[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        s[n][h] = exp2f(s[n][h] - base[h >> 1]);
+        l[h >> 1] += s[n][h];                    // unrounded; the lanes' sums meet at the end
+      }
+    if (bad) l[0] = l[1] = NAN;
+    // The weights are rounded to bf16 for the product with V: u = 2^-8 of each, as V itself.
+    const uint32_t p[4] = {pack2(s[0][0], s[0][1]), pack2(s[0][2], s[0][3]),
+                           pack2(s[1][0], s[1][1]), pack2(s[1][2], s[1][3])};
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+      uint32_t f[4];
+      ptx::ldsm_x4_t(f, vd + vrow + (vpc ^ (32 * i)));
+      ptx::mma_bf16_16816(o[2 * i], p, f[0], f[1]);
+      ptx::mma_bf16_16816(o[2 * i + 1], p, f[2], f[3]);
+    }
+  }
+
+  // The warp's sums into its slot, maxima and weights into sml[head][2].
+  __device__ __forceinline__ void leave(float* so, float (*sml)[2]) {
+    const int lane = threadIdx.x & 31, row = lane >> 2, quad = lane & 3;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      l[r] += __shfl_xor_sync(~0u, l[r], 1);
+      l[r] += __shfl_xor_sync(~0u, l[r], 2);
+      if (quad == 0) {
+        sml[row + 8 * r][0] = m[r];
+        sml[row + 8 * r][1] = l[r];
+      }
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i)
+        *reinterpret_cast<float2*>(so + sum_at(row + 8 * r, 8 * i + 2 * quad)) =
+            make_float2(o[i][2 * r], o[i][2 * r + 1]);
+    }
+  }
+};
+
+// fp32 throughout, for GH query heads of a kv head. Eight keys a step: four lanes per key
+// take a quarter of its channels for the scores of all heads (q from shared memory), then
+// each of the four goes on with every fourth head's softmax; the weights pass through shared
+// memory and a lane sums the channels 4 lane .. + 3 (and + 128) of V for all heads.
+template <int D, int GH_>
+struct F32Core {
+  typedef float T;
+  static constexpr int DIM = D, GH = GH_, HEADS = GH_, KEYS = 8, NW = D <= 128 ? 8 : 4;
+  static constexpr int SUB = TILE / (NW * KEYS), ST = 3, OCC = D <= 64 ? 2 : 1;
+  static constexpr int C = D / 4, RS = (C + 7) / 8 * 128, SLOT = 2 * KEYS * RS;
+  static constexpr int QS = GH * D;              // q of the item
+  static constexpr int NH = GH < 4 ? 1 : GH / 4; // heads of a lane's softmax
+  static constexpr int NV = (D + 127) / 128;     // runs of four channels of a lane
+  static_assert(GH * D * 4 <= SLOT, "a slot holds a warp's sums");
+  __device__ static int piece(int r, int ch) { return (ch ^ ((r & 1) << 2)) << 4; }
+  __device__ static int sum_at(int g, int d) { return g * D + d; }
+
+  float4 o[GH][NV];
+  float m[NH], l[NH];                            // of heads (lane & 3) + 4 i
+
+  __device__ __forceinline__ void begin(const AttnArgs& a, int b, int hq0, int heads, float* sq) {
+    for (int e = threadIdx.x; e < GH * D; e += NW * 32) {
+      const int g = e / D;
+      float v = 0.f;
+      if (g < heads) {
+        const int64_t at = b * a.qb + (hq0 + g) * a.qh + (e - g * D);
+        v = a.scale2 * (a.q_bf16 ? __bfloat162float(static_cast<const bf16*>(a.q)[at])
+                                 : static_cast<const float*>(a.q)[at]);
+      }
+      sq[e] = v;
+    }
+#pragma unroll
+    for (int g = 0; g < GH; ++g)
+#pragma unroll
+      for (int i = 0; i < NV; ++i) o[g][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < NH; ++i) m[i] = -INFINITY, l[i] = 0.f;
+  }
+
+  // sw: [KEYS + 1][GH] floats of this warp: the weights of a step, and factors for o.
+  __device__ __forceinline__ void step(const AttnArgs& a, char* slot, int live, bool bad,
+                                       const float* sq, float* sw) {
+    const int lane = threadIdx.x & 31, key = lane >> 2, part = lane & 3;
+    float2 acc[GH];
+#pragma unroll
+    for (int g = 0; g < GH; ++g) acc[g] = make_float2(0.f, 0.f);
+#pragma unroll 4
+    for (int i = 0; i < C / 4; ++i) {
+      const int ch = 4 * i + part;
+      const float4 k = *reinterpret_cast<const float4*>(slot + key * RS + piece(key, ch));
+#pragma unroll
+      for (int g = 0; g < GH; ++g) {
+        const float4 q = *reinterpret_cast<const float4*>(sq + g * D + 4 * ch);
+        acc[g] = fma2(make_float2(k.x, k.y), make_float2(q.x, q.y), acc[g]);
+        acc[g] = fma2(make_float2(k.z, k.w), make_float2(q.z, q.w), acc[g]);
+      }
+    }
+    float s[GH];
+#pragma unroll
+    for (int g = 0; g < GH; ++g) {
+      s[g] = acc[g].x + acc[g].y;
+      s[g] += __shfl_xor_sync(~0u, s[g], 1);
+      s[g] += __shfl_xor_sync(~0u, s[g], 2);
+    }
+    bool moved = false;
+#pragma unroll
+    for (int i = 0; i < NH; ++i) {
+      float v = s[4 * i];                        // this lane's head, part + 4 i
+#pragma unroll
+      for (int g = 1; g < 4; ++g)
+        if (4 * i + g < GH && part == g) v = s[4 * i + g];
+      if (key >= live) v = -INFINITY;
+      float top = fmaxf(m[i], v);
+      top = fmaxf(top, __shfl_xor_sync(~0u, top, 4));
+      top = fmaxf(top, __shfl_xor_sync(~0u, top, 8));
+      top = fmaxf(top, __shfl_xor_sync(~0u, top, 16));
+      const float f = top > m[i] ? exp2f(m[i] - top) : 1.f;            // 0 from -inf
+      moved = moved || top > m[i];
+      m[i] = top;
+      const float w = exp2f(v - (top == -INFINITY ? 0.f : top));
+      l[i] = fmaf(l[i], f, w);                   // of this key's lanes; they meet at the end
+      if (bad) l[i] = NAN;
+      if (part + 4 * i < GH) {
+        sw[key * GH + part + 4 * i] = w;
+        if (key == 0) sw[KEYS * GH + part + 4 * i] = f;
+      }
+    }
+    moved = __any_sync(~0u, moved);
+    __syncwarp();
+    if (moved) {
+#pragma unroll
+      for (int g = 0; g < GH; ++g) {
+        const float f = sw[KEYS * GH + g];
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+          o[g][i] = make_float4(o[g][i].x * f, o[g][i].y * f, o[g][i].z * f, o[g][i].w * f);
+      }
+    }
+    const char* vs = slot + KEYS * RS;
+#pragma unroll
+    for (int k = 0; k < KEYS; ++k) {
+      float4 v[NV];
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        v[i] = lane + 32 * i < C
+                   ? *reinterpret_cast<const float4*>(vs + k * RS + piece(k, lane + 32 * i))
+                   : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int g = 0; g < GH; ++g) {
+        const float w = sw[k * GH + g];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          float2* oo = reinterpret_cast<float2*>(&o[g][i]);
+          oo[0] = fma2(make_float2(w, w), make_float2(v[i].x, v[i].y), oo[0]);
+          oo[1] = fma2(make_float2(w, w), make_float2(v[i].z, v[i].w), oo[1]);
+        }
+      }
+    }
+    __syncwarp();                                // sw is written again by the next step
+  }
+
+  __device__ __forceinline__ void leave(float* so, float (*sml)[2]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < NH; ++i) {
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) l[i] += __shfl_xor_sync(~0u, l[i], x);
+      if (lane < 4 && lane + 4 * i < GH) {
+        sml[lane + 4 * i][0] = m[i];
+        sml[lane + 4 * i][1] = l[i];
+      }
+    }
+#pragma unroll
+    for (int g = 0; g < GH; ++g)
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (lane + 32 * i < C)
+          *reinterpret_cast<float4*>(so + sum_at(g, 4 * lane + 128 * i)) = o[g][i];
+  }
+};
+
+template <class Core>
+__global__ void __launch_bounds__(Core::NW * 32, Core::OCC) paged_ring_kernel(AttnArgs a) {
+  typedef typename Core::T T;
+  constexpr int D = Core::DIM, NW = Core::NW, ST = Core::ST, C = Core::C, RS = Core::RS;
+  constexpr int KEYS = Core::KEYS, SUB = Core::SUB, SLOT = Core::SLOT, PER = 16 / sizeof(T);
+  static_assert(NW * KEYS * SUB == TILE && KEYS * C % 32 == 0, "");
+  extern __shared__ __align__(128) char ring[];
+  __shared__ float sml[NW][Core::HEADS][2];
+  __shared__ int sbad[NW][ST];
+  __shared__ __align__(16) float sq[Core::QS ? Core::QS : 1];
+  __shared__ float sw[NW][Core::QS ? (KEYS + 1) * Core::HEADS : 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.launch_dependents;");
+  empty_rows(a);
+  Place pc;                                      // the tile being computed
+  long long per = 1, left = stretch(a, lane, &pc, &per);
+  if (left <= 0) return;
+  Place pi = pc;                                 // the tile being copied
+  long long to_copy = left;
+  int sub_copy = 0;
+  char* slots = ring + warp * ST * SLOT;
+  const T* kc = static_cast<const T*>(a.kc);
+  const T* vc = static_cast<const T*>(a.vc);
+
+  // Where this lane's key of the step at pi starts (-1: bad page, -2: no such key).
+  auto find = [&]() -> int64_t {
+    const int j = pi.s.lo + pi.tile * TILE + (sub_copy * NW + warp) * KEYS + (lane & (KEYS - 1));
+    if (j >= pi.s.n) return -2;
+    const int64_t r = key_row(a, pi.b, j);
+    return r < 0 ? -1 : r + (pi.item / a.groups) * a.ph;
+  };
+  int64_t off = find();
+  auto copy = [&](int slot) {
+    if (to_copy > 0) {
+      const unsigned bad = __ballot_sync(~0u, off == -1);
+      if (lane == 0) sbad[warp][slot] = bad != 0;
+      const uint32_t kd = ptx::smem_u32(slots + slot * SLOT), vd = kd + KEYS * RS;
+#pragma unroll
+      for (int i = 0; i < KEYS * C / 32; ++i) {
+        const int e = lane + 32 * i, r = e / C, ch = e - r * C;
+        const int64_t o = __shfl_sync(~0u, off, r);
+        const int64_t at = o < 0 ? 0 : o + ch * PER;
+        const uint32_t to = r * RS + Core::piece(r, ch);
+        ptx::cp_async16(kd + to, kc + at, o < 0 ? 0 : 16);
+        ptx::cp_async16(vd + to, vc + at, o < 0 ? 0 : 16);
+      }
+      if (++sub_copy == SUB) {
+        sub_copy = 0;
+        if (--to_copy > 0 && ++pi.tile == pi.s.tiles()) next_item(a, pi);
+      }
+      if (to_copy > 0) off = find();             // the next step's rows, looked up meanwhile
+    }
+    ptx::cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < ST; ++i) copy(i);
+
+  Core core;
+  int hq0 = 0, heads = 0, tile0 = 0, sub = 0;
+  auto begin = [&]() {
+    const int hk = pc.item / a.groups, g0 = (pc.item - hk * a.groups) * Core::HEADS;
+    hq0 = hk * a.G + g0;
+    heads = min(Core::HEADS, a.G - g0);
+    tile0 = pc.tile;
+    core.begin(a, pc.b, hq0, heads, sq);
   };
   begin();
+  if (Core::QS) __syncthreads();
 
-  // Row and first piece (swizzled, as a byte offset) of this lane's matrix rows in K and V.
-  const int krow = ((lane & 7) + (lane >> 4) * 8) * RS;
-  const int vrow = ((lane & 7) + ((lane >> 3) & 1) * 8) * RS;
-  const int kpc = (((lane >> 3) & 1) ^ (lane & 7)) << 4, vpc = ((lane >> 4) ^ (lane & 7)) << 4;
   for (int slot = 0;; slot = slot + 1 == ST ? 0 : slot + 1) {
     ptx::cp_async_wait<ST - 1>();
     __syncwarp();
-    const int live = pc.s.n - (pc.s.lo + pc.tile * TILE + warp * 16);    // keys of this warp
-    const uint32_t kd = slots_u + slot * M::SLOT, vd = kd + 16 * RS;
-    if (live > 0) {
-      float s[2][4];
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int h = 0; h < 4; ++h) s[n][h] = 0.f;
-#pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        uint32_t f[4];
-        ptx::ldsm_x4(f, kd + krow + (kpc ^ (32 * k)));
-        ptx::mma_bf16_16816(s[0], q[k], f[0], f[1]);
-        ptx::mma_bf16_16816(s[1], q[k], f[2], f[3]);
-      }
-      float top[2] = {m[0], m[1]};
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          s[n][h] *= a.scale2;
-          if (n * 8 + 2 * quad + (h & 1) >= live) s[n][h] = -INFINITY;
-          top[h >> 1] = fmaxf(top[h >> 1], s[n][h]);
-        }
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 1));
-        top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 2));
-      }
-      if (__any_sync(~0u, top[0] > m[0] || top[1] > m[1])) {
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const float f = top[r] > m[r] ? exp2f(m[r] - top[r]) : 1.f;    // 0 from -inf
-          m[r] = top[r];
-          l[r] *= f;
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            o[i][2 * r] *= f;
-            o[i][2 * r + 1] *= f;
-          }
-        }
-      }
-      const float base[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          s[n][h] = exp2f(s[n][h] - base[h >> 1]);
-          l[h >> 1] += s[n][h];                  // unrounded; lanes' sums meet at the end
-        }
-      if (sbad[warp][slot]) l[0] = l[1] = NAN;
-      const uint32_t p[4] = {pack2(s[0][0], s[0][1]), pack2(s[0][2], s[0][3]),
-                             pack2(s[1][0], s[1][1]), pack2(s[1][2], s[1][3])};
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        uint32_t f[4];
-        ptx::ldsm_x4_t(f, vd + vrow + (vpc ^ (32 * i)));
-        ptx::mma_bf16_16816(o[2 * i], p, f[0], f[1]);
-        ptx::mma_bf16_16816(o[2 * i + 1], p, f[2], f[3]);
-      }
-    }
+    const int live = pc.s.n - (pc.s.lo + pc.tile * TILE + (sub * NW + warp) * KEYS);
+    if (live > 0) core.step(a, slots + slot * SLOT, live, sbad[warp][slot] != 0, sq, sw[warp]);
     const int tiles = pc.s.tiles();
+    if (++sub < SUB) {
+      __syncwarp();
+      copy(slot);
+      continue;
+    }
+    sub = 0;
     --left;
     if (pc.tile + 1 == tiles || left == 0) {     // the item's end, or this block's
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        l[r] += __shfl_xor_sync(~0u, l[r], 1);
-        l[r] += __shfl_xor_sync(~0u, l[r], 2);
-        if (quad == 0) {
-          sml[warp][row + 8 * r][0] = m[r];
-          sml[warp][row + 8 * r][1] = l[r];
-        }
-      }
       __syncwarp();                              // the slot's last readers are done
-      float* so = reinterpret_cast<float*>(slots + slot * M::SLOT);
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-          *reinterpret_cast<float2*>(so + M::sum_at(row + 8 * r, 8 * i + 2 * quad)) =
-              make_float2(o[i][2 * r], o[i][2 * r + 1]);
+      core.leave(reinterpret_cast<float*>(slots + slot * SLOT), sml[warp]);
       __syncthreads();
       const bool done = tile0 == 0 && pc.tile + 1 == tiles;
       const size_t part = (size_t)blockIdx.x * 2 + (tile0 == 0 ? 1 : 0);
       if (tile0 == 0) write_note(a, pc, tiles - pc.tile - 1, per);
-      for (int e = threadIdx.x; e < heads * D; e += WARPS * 32) {
+      for (int e = threadIdx.x; e < heads * D; e += NW * 32) {
         const int g = e / D, d = e - g * D;
         float mm = -INFINITY, ll = 0.f, oo = 0.f;
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w) mm = fmaxf(mm, sml[w][g][0]);
+        for (int w = 0; w < NW; ++w) mm = fmaxf(mm, sml[w][g][0]);
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w) {
+        for (int w = 0; w < NW; ++w) {
           const float f = sml[w][g][0] == -INFINITY ? 1.f : exp2f(sml[w][g][0] - mm);
           ll = fmaf(f, sml[w][g][1], ll);
-          oo = fmaf(f, *reinterpret_cast<const float*>(ring + (w * ST + slot) * M::SLOT +
-                                                       M::sum_at(g, d) * 4), oo);
+          oo = fmaf(f, reinterpret_cast<const float*>(ring + (w * ST + slot) *
+                                                                 SLOT)[Core::sum_at(g, d)], oo);
         }
         if (done) {
           finish(a, pc.b, hq0 + g, d, mm, ll, oo);
@@ -566,10 +741,12 @@ __global__ void __launch_bounds__(WARPS * 32, Mma<D>::OCC) paged_mma_kernel(Attn
           }
         }
       }
+      if (left > 0) {
+        next_item(a, pc);
+        begin();
+      }
       __syncthreads();
       if (left == 0) break;
-      next_item(a, pc);
-      begin();
     } else {
       ++pc.tile;
     }
@@ -634,36 +811,68 @@ __global__ void __launch_bounds__(JW * 32) paged_join_kernel(AttnArgs a) {
 // ------------------------------------------------------------ host
 constexpr int kSms = 152;
 constexpr long long kMaxKeys = (1LL << 31) - 1024;   // tile ends stay within an int
-constexpr int kWholeTiles = 4;    // capacity up to which one block takes a whole item
+constexpr int kWholeTiles = 8;    // capacity up to which one block takes a whole item
+
+enum Kind { kAny, kMma, kF32 };                  // which kernel
 
 struct Plan {
-  int mma, GH, groups, whole, blocks, by_item, notes, hb;
+  Kind kind;
+  int GH, groups, whole, blocks, by_item, notes, hb;
   size_t o_bytes, ml_bytes, cut_bytes;
 };
 
-// Whether sizes, types and strides allow the tensor-core kernel (16-byte pieces of every
-// cache row; their bases are 16-byte aligned by contract).
-bool mma_sizes(const gdr_attn_dims* d, const gdr_paged_cache* c) {
-  const int D = c->D;
-  return d->q_dtype == GDR_BF16 && c->dtype == GDR_BF16 &&
-         (D == 64 || D == 80 || D == 96 || D == 128 || D == 192 || D == 256) &&
-         c->page_stride % 8 == 0 && c->token_stride % 8 == 0 && c->head_stride % 8 == 0 &&
-         (d->q_stride_b % 2 == 0 || d->B == 1) && (d->q_stride_h % 2 == 0 || d->HQ == 1);
+// Whether sizes, types and strides allow a ring kernel (16-byte pieces of every cache row;
+// their bases are 16-byte aligned by contract): on the tensor cores for bf16 q and caches,
+// in fp32 for fp32 caches.
+Kind kind_of(const gdr_attn_dims* d, const gdr_paged_cache* c) {
+  const int D = c->D, run = c->dtype == GDR_BF16 ? 8 : 4;
+  if (D != 64 && D != 80 && D != 96 && D != 128 && D != 192 && D != 256) return kAny;
+  if (c->page_stride % run != 0 || c->token_stride % run != 0 || c->head_stride % run != 0)
+    return kAny;
+  if (c->dtype == GDR_F32) return kF32;
+  return d->q_dtype == GDR_BF16 && (d->q_stride_b % 2 == 0 || d->B == 1) &&
+                 (d->q_stride_h % 2 == 0 || d->HQ == 1)
+             ? kMma
+             : kAny;
 }
 
-Plan make_plan(const gdr_attn_dims* d, const gdr_paged_cache* c, bool mma) {
+// f(null pointer of the Core) for a ring kernel of head dimension D.
+template <typename F>
+auto with_core(Kind kind, int D, int G, F f) {
+  auto pick = [&](auto dim) {
+    constexpr int N = decltype(dim)::value;
+    if (kind == kMma) return f(static_cast<MmaCore<N>*>(nullptr));
+    // Two heads or eight: a step's work in heads that are not there is not waited for, it is
+    // hidden behind the copies.
+    return G <= 2 ? f(static_cast<F32Core<N, 2>*>(nullptr)) : f(static_cast<F32Core<N, 8>*>(nullptr));
+  };
+  return D == 64    ? pick(std::integral_constant<int, 64>())
+         : D == 80  ? pick(std::integral_constant<int, 80>())
+         : D == 96  ? pick(std::integral_constant<int, 96>())
+         : D == 128 ? pick(std::integral_constant<int, 128>())
+         : D == 192 ? pick(std::integral_constant<int, 192>())
+                    : pick(std::integral_constant<int, 256>());
+}
+
+Plan make_plan(const gdr_attn_dims* d, const gdr_paged_cache* c, Kind kind) {
   Plan p;
   const int G = d->HQ / c->HK;
-  p.mma = mma;
-  p.GH = mma ? GMAX : c->D <= 128 ? 4 : 2;
+  p.kind = kind;
+  int resident = 2;                              // blocks per SM
+  p.GH = c->D <= 128 ? 4 : 2;
+  if (kind != kAny)
+    with_core(kind, c->D, G, [&](auto* core) {
+      using Core = std::remove_pointer_t<decltype(core)>;
+      p.GH = Core::HEADS;
+      resident = Core::OCC;
+      return 0;
+    });
   p.groups = (G + p.GH - 1) / p.GH;
   long long keys = (long long)c->max_pages * c->page_size;
   if (d->window > 0 && keys > d->window) keys = d->window;
   const long long items = (long long)d->B * c->HK * p.groups;
   p.whole = keys <= kWholeTiles * TILE && items < (1LL << 31);
-  p.blocks = p.whole ? (int)items
-             : mma   ? kSms * (c->D <= 64 ? 4 : c->D <= 128 ? 2 : 1)
-                     : kSms * (c->D <= 64 ? 4 : 2);
+  p.blocks = p.whole ? (int)items : kSms * resident;
   p.o_bytes = p.whole ? 0 : align_up((size_t)p.blocks * 2 * GMAX * c->D * sizeof(float));
   p.ml_bytes = p.whole ? 0 : align_up((size_t)p.blocks * 2 * GMAX * 2 * sizeof(float));
   // Notes per item where that makes fewer of them; then as many join blocks as keep a few
@@ -679,10 +888,11 @@ Plan make_plan(const gdr_attn_dims* d, const gdr_paged_cache* c, bool mma) {
 
 size_t plan_bytes(const Plan& p) { return kAlign + p.o_bytes + p.ml_bytes + p.cut_bytes; }
 
-template <int D>
-gdr_status launch_mma(const AttnArgs& a, cudaStream_t s) {
-  if (!allow_smem<Mma<D>>(paged_mma_kernel<D>, Mma<D>::SMEM)) return GDR_ERR_CUDA;
-  paged_mma_kernel<D><<<a.blocks, WARPS * 32, Mma<D>::SMEM, s>>>(a);
+template <class Core>
+gdr_status launch_ring(const AttnArgs& a, cudaStream_t s) {
+  constexpr int bytes = Core::NW * Core::ST * Core::SLOT;
+  if (!allow_smem<Core>(paged_ring_kernel<Core>, bytes)) return GDR_ERR_CUDA;
+  paged_ring_kernel<Core><<<a.blocks, Core::NW * 32, bytes, s>>>(a);
   return launched();
 }
 
@@ -711,9 +921,9 @@ size_t gdr_paged_decode_attn_workspace_size(const gdr_attn_dims* dims,
                                             const gdr_paged_cache* cache) {
   if (check(dims, cache) != GDR_OK) return 0;
   // q's alignment is not known here: room for either kernel.
-  const size_t any = plan_bytes(make_plan(dims, cache, false));
-  const size_t mma = mma_sizes(dims, cache) ? plan_bytes(make_plan(dims, cache, true)) : 0;
-  return any > mma ? any : mma;
+  const size_t any = plan_bytes(make_plan(dims, cache, kAny));
+  const size_t ring = plan_bytes(make_plan(dims, cache, kind_of(dims, cache)));
+  return any > ring ? any : ring;
 }
 
 gdr_status gdr_paged_decode_attn(const void* q, const void* k_cache, const void* v_cache,
@@ -733,7 +943,9 @@ gdr_status gdr_paged_decode_attn(const void* q, const void* k_cache, const void*
     return GDR_ERR_WORKSPACE;
   if (!is_aligned(workspace, kAlign)) return GDR_ERR_ALIGNMENT;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const Plan p = make_plan(dims, cache, mma_sizes(dims, cache) && is_aligned(q, 4));
+  Kind kind = kind_of(dims, cache);
+  if (kind == kMma && !is_aligned(q, 4)) kind = kAny;
+  const Plan p = make_plan(dims, cache, kind);
   AttnArgs a = {};
   a.q = q; a.kc = k_cache; a.vc = v_cache; a.table = page_table; a.lens = lens;
   a.out = out; a.lse = lse;
@@ -756,13 +968,10 @@ gdr_status gdr_paged_decode_attn(const void* q, const void* k_cache, const void*
   a.cap = (long long)cache->max_pages * cache->page_size;
   if (a.cap > kMaxKeys) a.cap = kMaxKeys;
   gdr_status run = GDR_OK;
-  if (p.mma) {
-    run = a.D == 64    ? launch_mma<64>(a, s)
-          : a.D == 80  ? launch_mma<80>(a, s)
-          : a.D == 96  ? launch_mma<96>(a, s)
-          : a.D == 128 ? launch_mma<128>(a, s)
-          : a.D == 192 ? launch_mma<192>(a, s)
-                       : launch_mma<256>(a, s);
+  if (p.kind != kAny) {
+    run = with_core(p.kind, a.D, a.G, [&](auto* core) {
+      return launch_ring<std::remove_pointer_t<decltype(core)>>(a, s);
+    });
   } else {
     const int vec = a.D % 4 == 0 && a.pp % 4 == 0 && a.pt % 4 == 0 && a.ph % 4 == 0;
     run = with_dtype(cache->dtype, [&](auto* t) {
