@@ -9,12 +9,14 @@ dimension dense); outputs are dense.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import math
+import os
 from typing import Optional
 
 import torch
 
-from . import (GDR_BF16, GDR_ERR_INVALID_ARG, GDR_F32, GDR_OK, GdrError, load_library)
+from . import (GDR_BF16, GDR_ERR_INVALID_ARG, GDR_F32, GDR_OK, LIB_PATH, GdrError, load_library)
 
 SCAN_CHECKPOINT = 64        # GDR_SCAN_CHECKPOINT
 _DTYPE = {torch.bfloat16: GDR_BF16, torch.float32: GDR_F32}
@@ -79,10 +81,32 @@ def _lib():
     return _bound
 
 
-# ------------------------------------------------------------------ shared checks
 # A step of a decoder makes a few such calls per layer, each a few microseconds of GPU work:
-# what they cost on the host counts. So the checks below take one pass over a tensor's
-# attributes and work out what is wrong only once something is.
+# what they cost on the host counts. csrc/layers_host.cpp makes the same checks and the same
+# C calls in one step for the ordinary case (torch's current stream, results of the default
+# dtype or passed in); it answers None to everything else, and the code below takes over,
+# with its messages. On a GB300's host a call of qk_norm_rope_append takes 13 us through the
+# Python code and 2.5 us compiled, the launch included.
+_host = None
+
+
+def _load_host():
+    global _host
+    path = os.path.join(os.path.dirname(LIB_PATH), "_layers_host.so")
+    if not os.path.exists(path):
+        raise RuntimeError(f"{path} not built; run chunkwise_gated_delta_gdr_gb300.build")
+    spec = importlib.util.spec_from_file_location("_layers_host", path)
+    _host = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(_host)
+
+
+if os.path.exists(LIB_PATH):
+    load_library()
+    _load_host()
+
+
+# ------------------------------------------------------------------ shared checks
+# One pass over a tensor's attributes; what is wrong is worked out only once something is.
 F32 = torch.float32
 _structs = {}
 
@@ -172,6 +196,11 @@ def linear_scan_fwd(x, g, initial_state=None, *, gated_input: bool = False,
     Returns (h [B,T,D] of out_dtype, default x's; final_state fp32 [B,D] or None).
     Asynchronous on ``stream`` (default: torch's current stream).
     """
+    if stream is None and out_dtype is None and _host is not None:
+        r = _host.linear_scan_fwd(x, g, initial_state, gated_input, output_final_state, out,
+                                  final_state, checkpoints)
+        if r is not None:
+            return r
     shape, device = x.shape, x.device
     if len(shape) != 3:
         raise ValueError("x must be [B, T, D]")
@@ -209,6 +238,11 @@ def linear_scan_bwd(dh, x, g, checkpoints, d_final_state=None, *, gated_input: b
     in the forward call, ``checkpoints`` as it filled them, d_final_state fp32 [B,D] or
     None. Returns (dx of x's dtype, dg of g's dtype, d_initial_state fp32 [B,D] or None).
     """
+    if stream is None and _host is not None:
+        r = _host.linear_scan_bwd(dh, x, g, checkpoints, d_final_state, gated_input,
+                                  output_initial_state_grad, dx, dg, d_initial_state)
+        if r is not None:
+            return r
     shape, device = x.shape, x.device
     if len(shape) != 3:
         raise ValueError("x must be [B, T, D]")
@@ -298,6 +332,11 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positio
     with ``interleaved``. Without cos and sin only the norm is taken. Returns
     (q_out, k_out) of out_dtype (default q's). A position outside the tables gives NaN.
     """
+    if stream is None and out_dtype is None and _host is not None:
+        r = _host.qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved,
+                               q_out, k_out)
+        if r is not None:
+            return r
     B, T, HQ, D = q.shape
     device, HK = q.device, k.shape[2]
     raw = _stream(device, stream)
@@ -325,6 +364,11 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, cos=Non
     """Gradients of qk_norm_rope: dq_out [B,T,HQ,D], dk_out [B,T,HK,D] (dense, one dtype),
     the rest as in the forward call. Returns (dq, dk, dq_weight, dk_weight): dense, of q's
     dtype, and fp32 [D] (None with output_weight_grads=False)."""
+    if stream is None and _host is not None:
+        r = _host.qk_norm_rope_bwd(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved,
+                                   dq_out, dk_out, dq, dk, output_weight_grads, workspace)
+        if r is not None:
+            return r
     B, T, HQ, D = q.shape
     device, HK = q.device, k.shape[2]
     raw = _stream(device, stream)
@@ -386,6 +430,11 @@ def qk_norm_rope_append(q, k, v, q_weight, k_weight, cos, sin, positions, k_cach
     (int32 [B, max_pages]). A position or page out of range stores nothing and gives NaN
     in the token's q_out.
     """
+    if stream is None and out_dtype is None and _host is not None:
+        r = _host.qk_norm_rope_append(q, k, q_weight, k_weight, cos, sin, positions, eps,
+                                      interleaved, v, k_cache, v_cache, page_table, q_out)
+        if r is not None:
+            return r
     B, T, HQ, D = q.shape
     device = q.device
     raw = _stream(device, stream)
@@ -442,6 +491,11 @@ def paged_decode_attn(q, k_cache, v_cache, page_table, lens, *, scale: Optional[
     [B,HQ]). A sequence without keys gives zeros and -inf; a length or a page out of
     range gives NaN.
     """
+    if stream is None and out_dtype is None and _host is not None:
+        r = _host.paged_decode_attn(q, k_cache, v_cache, page_table, lens, scale, window, out, lse,
+                                    workspace)
+        if r is not None:
+            return r
     shape, device = q.shape, q.device
     raw = _stream(device, stream)
     if out is None:

@@ -763,3 +763,85 @@ def test_capture_in_a_graph():
     a = g.double().exp()[:, 0]
     want = x[:, 0].double() * (1 + a + a * a)
     check(state, want, 2e-5)
+
+
+def test_compiled_calls_take_the_ordinary_case(monkeypatch):
+    """The compiled calls and the Python ones give the same bits; the ordinary case, results
+    passed in or not, never reaches the Python ones."""
+    from chunkwise_gated_delta_gdr_gb300 import layers
+    gen = gen_of(60)
+    x, g, h0, dh, dfinal = scan_inputs(2, 300, 128, BF, F32, 61)
+    q, k, v, wq, wk, cos, sin, pos = qk_inputs(3, 1, 4, 2, 128, 64, BF, 62)
+    lens = torch.tensor([40, 3000, 7])
+    table, total = make_pages(lens + 1, 16, gen)
+    kc, vc = make_cache(gen, total, 16, 2, 128, BF)
+    table, ln = table.to(DEV), lens.int().to(DEV)
+    at = lens[:, None].int().to(DEV)
+    cos2, sin2 = tables(4000, 64)
+    dq = rnd(gen, *q.shape, dtype=BF), rnd(gen, *k.shape, dtype=BF)
+    outs = [torch.empty(2, 300, 128, dtype=BF, device=DEV), torch.empty(2, 128, device=DEV),
+            torch.empty(3, 1, 4, 128, dtype=BF, device=DEV)]
+
+    def calls():
+        ck = gdr.linear_scan_checkpoints(x)
+        r = [*gdr.linear_scan_fwd(x, g, h0, checkpoints=ck),
+             *gdr.linear_scan_fwd(x, g, h0, gated_input=True, out=outs[0], final_state=outs[1]),
+             *gdr.linear_scan_fwd(x, g, output_final_state=False),
+             *gdr.linear_scan_bwd(dh, x, g, ck, dfinal),
+             *gdr.qk_norm_rope(q, k, wq, wk, cos, sin, pos), *gdr.qk_norm_rope(q, k),
+             *gdr.qk_norm_rope(q, k, wq, None, cos, sin, pos.long(), eps=1e-3, interleaved=True),
+             *gdr.qk_norm_rope_bwd(*dq, q, k, wq, wk, cos, sin, pos),
+             *gdr.qk_norm_rope_bwd(*dq, q, k, output_weight_grads=False),
+             gdr.qk_norm_rope_append(q, k, v, wq, wk, cos2, sin2, at, kc, vc, table, q_out=outs[2]),
+             kc, vc, *gdr.paged_decode_attn(q[:, 0], kc, vc, table, ln + 1),
+             *gdr.paged_decode_attn(q[:, 0], kc, vc, table, ln + 1, scale=0.2, window=50)]
+        return [t if t is None else t.clone() for t in r]
+
+    with monkeypatch.context() as m:
+        m.setattr(layers, "_lib", None)                  # the Python calls cannot run
+        fast = calls()
+    monkeypatch.setattr(layers, "_host", None)
+    slow = calls()
+    assert len(fast) == len(slow)
+    for a, b in zip(fast, slow):
+        assert (a is None and b is None) or torch.equal(a, b)
+
+
+@pytest.mark.parametrize("compiled", [True, False])
+def test_refusals_on_the_gpu(compiled, monkeypatch):
+    from chunkwise_gated_delta_gdr_gb300 import layers
+    if not compiled:
+        monkeypatch.setattr(layers, "_host", None)
+    x = torch.zeros(2, 8, 16, device=DEV)
+    q, k = torch.zeros(2, 3, 4, 64, device=DEV), torch.zeros(2, 3, 2, 64, device=DEV)
+    kc = torch.zeros(5, 16, 2, 64, device=DEV)
+    table, lens = torch.zeros(2, 2, dtype=torch.int32, device=DEV), torch.ones(2, device=DEV).int()
+    bad = [
+        (lambda: gdr.linear_scan_fwd(x, x[:, :4]), ValueError),
+        (lambda: gdr.linear_scan_fwd(x, x.cpu()), ValueError),
+        (lambda: gdr.linear_scan_fwd(x, x.double()), TypeError),
+        (lambda: gdr.linear_scan_fwd(x.transpose(1, 2), x.transpose(1, 2)), ValueError),
+        (lambda: gdr.linear_scan_fwd(x, x, torch.zeros(2, 15, device=DEV)), ValueError),
+        (lambda: gdr.linear_scan_fwd(x, x, torch.zeros(2, 16, device=DEV).bfloat16()), TypeError),
+        (lambda: gdr.linear_scan_fwd(x, x, out=x.bfloat16(), out_dtype=F32), TypeError),
+        (lambda: gdr.linear_scan_bwd(x, x, x, None), ValueError),
+        (lambda: gdr.linear_scan_bwd(x, x, x, torch.zeros(2, 2, 16, device=DEV)), ValueError),
+        (lambda: gdr.qk_norm_rope(q, k[:, :2]), ValueError),
+        (lambda: gdr.qk_norm_rope(q, k.bfloat16()), TypeError),
+        (lambda: gdr.qk_norm_rope(q, k, eps=0.0), gdr.GdrError),
+        (lambda: gdr.qk_norm_rope(q, k, torch.ones(63, device=DEV)), ValueError),
+        (lambda: gdr.qk_norm_rope(q, k, None, None, x[0], x[0]), ValueError),
+        (lambda: gdr.paged_decode_attn(q[:, 0], kc, kc, table.long(), lens), TypeError),
+        (lambda: gdr.paged_decode_attn(q[:, 0], kc, kc, table, lens.long()), TypeError),
+        (lambda: gdr.paged_decode_attn(q[:, 0], kc, kc[:, :, :1], table, lens), ValueError),
+        (lambda: gdr.paged_decode_attn(q[:, 0, :3], kc, kc, table, lens), gdr.GdrError),
+        (lambda: gdr.paged_decode_attn(q[:, 0], kc, kc, table, lens, scale=-1.0), gdr.GdrError),
+        (lambda: gdr.paged_decode_attn(q[:, 0], kc, kc, table, lens, window=-1), gdr.GdrError),
+        (lambda: gdr.paged_decode_attn(q[:, 0], kc, kc, table, lens,
+                                       workspace=torch.zeros(64, dtype=torch.uint8, device=DEV)),
+         gdr.GdrError),
+    ]
+    for i, (call, error) in enumerate(bad):
+        with pytest.raises(error):
+            call()
+            pytest.fail(f"refusal {i} did not come")
