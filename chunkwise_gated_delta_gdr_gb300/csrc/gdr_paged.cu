@@ -119,12 +119,15 @@ __device__ __forceinline__ void put(void* out, size_t i, float v, int is_bf16) {
     static_cast<float*>(out)[i] = v;
 }
 
-// Result of head `hq` of sequence b, channel d, from the sums (m in base 2).
+// Results of head `hq` of sequence b (channel d) from the sums, m in base 2.
+__device__ __forceinline__ void finish_lse(const AttnArgs& a, int b, int hq, float m, float l) {
+  if (a.lse) a.lse[(size_t)b * a.HQ + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
+}
 __device__ __forceinline__ void finish(const AttnArgs& a, int b, int hq, int d, float m, float l,
                                        float o) {
   const size_t row = (size_t)b * a.HQ + hq;
   put(a.out, row * a.D + d, l == 0.f ? 0.f : o / l, a.out_bf16);
-  if (d == 0 && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
+  if (d == 0) finish_lse(a, b, hq, m, l);
 }
 
 // Sequences without tiles: zeros and -inf (no keys), NaN (an invalid length).
@@ -719,22 +722,33 @@ __global__ void __launch_bounds__(Core::NW * 32, Core::OCC) paged_ring_kernel(At
       const bool done = tile0 == 0 && pc.tile + 1 == tiles;
       const size_t part = (size_t)blockIdx.x * 2 + (tile0 == 0 ? 1 : 0);
       if (tile0 == 0) write_note(a, pc, tiles - pc.tile - 1, per);
-      for (int e = threadIdx.x; e < heads * D; e += NW * 32) {
-        const int g = e / D, d = e - g * D;
-        float mm = -INFINITY, ll = 0.f, oo = 0.f;
+      for (int e = threadIdx.x; e < heads * (D / 4); e += NW * 32) {   // four channels each
+        const int g = e / (D / 4), d = 4 * (e - g * (D / 4));
+        float mm = -INFINITY, ll = 0.f;
+        float2 oo[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
         for (int w = 0; w < NW; ++w) mm = fmaxf(mm, sml[w][g][0]);
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
           const float f = sml[w][g][0] == -INFINITY ? 1.f : exp2f(sml[w][g][0] - mm);
+          const float4 v = *reinterpret_cast<const float4*>(
+              ring + (w * ST + slot) * SLOT + 4 * Core::sum_at(g, d));
           ll = fmaf(f, sml[w][g][1], ll);
-          oo = fmaf(f, reinterpret_cast<const float*>(ring + (w * ST + slot) *
-                                                                 SLOT)[Core::sum_at(g, d)], oo);
+          oo[0] = fma2(make_float2(f, f), make_float2(v.x, v.y), oo[0]);
+          oo[1] = fma2(make_float2(f, f), make_float2(v.z, v.w), oo[1]);
         }
         if (done) {
-          finish(a, pc.b, hq0 + g, d, mm, ll, oo);
+          const size_t at = ((size_t)pc.b * a.HQ + hq0 + g) * D + d;
+          const float r = ll == 0.f ? 0.f : 1.f / ll;    // no weight: zeros
+          oo[0] = ll == 0.f ? make_float2(0.f, 0.f) : mul2(oo[0], make_float2(r, r));
+          oo[1] = ll == 0.f ? make_float2(0.f, 0.f) : mul2(oo[1], make_float2(r, r));
+          if (a.out_bf16)
+            store_pairs(static_cast<bf16*>(a.out) + at, oo);
+          else
+            store_pairs(static_cast<float*>(a.out) + at, oo);
+          if (d == 0) finish_lse(a, pc.b, hq0 + g, mm, ll);
         } else {
-          a.part_o[(part * GMAX + g) * D + d] = oo;
+          store_pairs(a.part_o + (part * GMAX + g) * D + d, oo);
           if (d == 0) {
             a.part_ml[(part * GMAX + g) * 2] = mm;
             a.part_ml[(part * GMAX + g) * 2 + 1] = ll;

@@ -36,7 +36,7 @@ __global__ void __launch_bounds__(128) scan_serial_kernel(ScanArgs a) {
   float s[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) s[i] = a.s0 ? a.s0[(size_t)b * a.D + d + i] : 0.f;
-#pragma unroll 4
+#pragma unroll 8
   for (int t = 0; t < a.T; ++t) {
     float xv[V], gv[V];
     load_f<X, V>(x + t * a.xt, xv);
@@ -554,8 +554,14 @@ gdr_status copy_state(float* out, const float* in, size_t n, cudaStream_t s) {
   return e == cudaSuccess ? GDR_OK : GDR_ERR_CUDA;
 }
 
-// Tokens up to which one thread runs a channel's tokens by itself.
-constexpr int kSerial = 8;
+constexpr int kSms = 152;
+// Tokens up to which one thread runs its channels' tokens by itself: a few always; more where
+// there are channels for more blocks than the walk keeps resident, whose tile of 128 tokens
+// would be mostly empty (64 x 16 x 2048: 25 us by the walk, 6.4 so; 64 x 64 x 2048: 31, 41).
+constexpr int kSerial = 8, kSerialWide = 32;
+bool serial(const ScanArgs& a) {
+  return a.T <= kSerial || (a.T <= kSerialWide && (long long)a.B * a.D >= 64LL * 2 * kSms);
+}
 
 // A view [B, T, D] as a tensor map with boxes of `rows` tokens x `cols` channels.
 bool tmap_view(CUtensorMap* m, const void* p, int dtype, const ScanArgs& a, int64_t sb, int64_t st,
@@ -578,84 +584,127 @@ bool tensor_ok(const void* p, int dtype, const ScanArgs& a, int64_t sb, int64_t 
          (a.T == 1 || (st * es % 16 == 0 && st > 0)) && (a.B == 1 || (sb * es % 16 == 0 && sb > 0));
 }
 
-// Clusters of s blocks that the device holds at once, s = 1 .. MAXS, into `active`; asked of
-// the runtime once per kernel (F names it) and device. False on a CUDA error.
+// Clusters of s blocks, s = 1 .. MAXS, that the device holds at once: with one block per SM
+// (alone) and with as many as fit (packed). Asked of the runtime once per kernel (F names it)
+// and device; false on a CUDA error.
+struct Residency {
+  int alone[MAXS + 1], packed[MAXS + 1];
+};
 template <typename F, typename Fn>
-bool residency(Fn fn, int* active) {
-  constexpr int kDevices = 16;
-  static std::atomic<int> table[kDevices][MAXS + 1];   // [0]: filled
+bool residency(Fn fn, Residency* r) {
+  constexpr int kDevices = 16, kAlone = 120 * 1024;    // more than half an SM's shared memory
+  static std::atomic<int> table[kDevices][2][MAXS + 1];   // [0][0]: filled
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev >= kDevices) return false;
-  std::atomic<int>* row = table[dev];
-  if (!row[0].load(std::memory_order_acquire)) {
-    if (!allow_smem<F>(fn, F::SMEM)) return false;
-    for (int s = 1; s <= MAXS; ++s) {
-      cudaLaunchAttribute at[1];
-      at[0].id = cudaLaunchAttributeClusterDimension;
-      at[0].val.clusterDim.x = s;
-      at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-      cudaLaunchConfig_t cfg = {};
-      cfg.gridDim = dim3(s);
-      cfg.blockDim = dim3(W * 32);
-      cfg.dynamicSmemBytes = F::SMEM;
-      cfg.attrs = at;
-      cfg.numAttrs = 1;
-      int n = 0;
-      if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess) {
-        (void)cudaGetLastError();
-        n = 0;
+  auto& row = table[dev];
+  if (!row[0][0].load(std::memory_order_acquire)) {
+    if (!allow_smem<F>(fn, F::SMEM > kAlone ? F::SMEM : kAlone)) return false;
+    for (int k = 0; k < 2; ++k)
+      for (int s = 1; s <= MAXS; ++s) {
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = s;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(s);
+        cfg.blockDim = dim3(W * 32);
+        cfg.dynamicSmemBytes = k == 0 && F::SMEM < kAlone ? kAlone : F::SMEM;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess) {
+          (void)cudaGetLastError();
+          n = 0;
+        }
+        row[k][s].store(n, std::memory_order_relaxed);
       }
-      row[s].store(n, std::memory_order_relaxed);
-    }
-    row[0].store(1, std::memory_order_release);
+    row[0][0].store(1, std::memory_order_release);
   }
-  for (int s = 1; s <= MAXS; ++s) active[s] = row[s].load(std::memory_order_relaxed);
-  return active[1] > 0;
+  for (int s = 1; s <= MAXS; ++s) {
+    r->alone[s] = row[0][s].load(std::memory_order_relaxed);
+    r->packed[s] = row[1][s].load(std::memory_order_relaxed);
+  }
+  return r->packed[1] > 0;
 }
 
-// Blocks per cluster: the fewest steps in all, over the waves that the clusters take.
-int cluster_size(const int* active, long long clusters, int tiles) {
-  int best = 1;
+// Blocks per cluster (*best) with the least time for `clusters` of them over `tiles` tiles;
+// returns that time in tenths of a step of a block that has its SM for itself. Two blocks
+// that share an SM take 1.7 times as long for a step (measured: 1.6 and 2.7 us for forward
+// steps at 1 x 16384 x 1024, S = 6 and 8; 1.7 and 2.6 us backward), three 2.5 times.
+long long cluster_size(const Residency& r, long long clusters, int tiles, int* best) {
   long long least = -1;
+  *best = 1;
   for (int s = 1; s <= MAXS && s <= tiles; ++s) {
-    if (active[s] <= 0) continue;
-    const long long cost = (clusters + active[s] - 1) / active[s] * ((tiles + s - 1) / s);
-    if (least < 0 || cost < least) least = cost, best = s;
+    if (r.packed[s] <= 0) continue;
+    const long long waves = (clusters + r.packed[s] - 1) / r.packed[s];
+    const int share = clusters <= r.alone[s] ? 10 : clusters * s <= 2 * kSms ? 17 : 25;
+    const long long cost = waves * ((tiles + s - 1) / s) * share;
+    if (least < 0 || cost < least) least = cost, *best = s;
   }
-  return best;
+  return least;
 }
 
 template <typename X, typename G, typename H, int V, bool kTensor, bool kBwd>
-gdr_status launch_walk(const gdr_scan_dims* d, const ScanArgs& a, cudaStream_t s) {
+struct Walk {
   using F = std::conditional_t<kBwd, Bwd<X, G, H, V, kTensor>, Fwd<X, G, H, V, kTensor>>;
-  auto fn = kBwd ? scan_bwd_kernel<X, G, H, V, kTensor> : scan_kernel<X, G, H, V, kTensor>;
-  int active[MAXS + 1];
-  if (!residency<F>(fn, active)) return GDR_ERR_CUDA;
-  const long long cols = (a.D + 32LL * V - 1) / (32 * V);
-  const int S = cluster_size(active, cols * a.B, (a.T + F::TILE - 1) / F::TILE);
-  ScanMaps m;
-  if constexpr (kTensor) {
-    if (!tmap_view(&m.x, a.x, d->x_dtype, a, a.xb, a.xt, 32 * V, F::TILE) ||
-        !tmap_view(&m.g, a.g, d->g_dtype, a, a.gb, a.gt, 32 * V, F::TILE) ||
-        (kBwd && !tmap_view(&m.dh, a.dh, d->h_dtype, a, a.db, a.dt, 32 * V, F::TILE)))
+  static auto kernel() {
+    if constexpr (kBwd)
+      return scan_bwd_kernel<X, G, H, V, kTensor>;
+    else
+      return scan_kernel<X, G, H, V, kTensor>;
+  }
+  // The time of this walk by the rule above, and its blocks per cluster; -1: a CUDA error.
+  static long long plan(const ScanArgs& a, int* S) {
+    Residency r;
+    if (!residency<F>(kernel(), &r)) return -1;
+    const long long cols = (a.D + 32LL * V - 1) / (32 * V);
+    return cluster_size(r, cols * a.B, (a.T + F::TILE - 1) / F::TILE, S);
+  }
+  static gdr_status launch(const gdr_scan_dims* d, const ScanArgs& a, int S, cudaStream_t s) {
+    ScanMaps m;
+    if constexpr (kTensor) {
+      if (!tmap_view(&m.x, a.x, d->x_dtype, a, a.xb, a.xt, 32 * V, F::TILE) ||
+          !tmap_view(&m.g, a.g, d->g_dtype, a, a.gb, a.gt, 32 * V, F::TILE) ||
+          (kBwd && !tmap_view(&m.dh, a.dh, d->h_dtype, a, a.db, a.dt, 32 * V, F::TILE)))
+        return GDR_ERR_CUDA;
+    }
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = S;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((a.D + 32LL * V - 1) / (32 * V) * S), a.B);
+    cfg.blockDim = dim3(W * 32);
+    cfg.dynamicSmemBytes = F::SMEM;
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kernel(), m, a, S) != cudaSuccess) {
+      (void)cudaGetLastError();
       return GDR_ERR_CUDA;
+    }
+    return GDR_OK;
   }
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = S;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(cols * S), a.B);
-  cfg.blockDim = dim3(W * 32);
-  cfg.dynamicSmemBytes = F::SMEM;
-  cfg.stream = s;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, fn, m, a, S) != cudaSuccess) {
-    (void)cudaGetLastError();
-    return GDR_ERR_CUDA;
-  }
-  return GDR_OK;
+};
+
+// Two channels a lane or one. One halves a block's work for the same number of steps: a
+// step takes 0.7 of the time (319 and 221 us at 1 x 16384 x 1024, S = 1, backward), and
+// narrow problems get twice the blocks.
+template <typename X, typename G, typename H, bool kBwd>
+gdr_status launch_tensor(const gdr_scan_dims* d, const ScanArgs& a, cudaStream_t s) {
+  int S2 = 1, S1 = 1;
+  const long long two = Walk<X, G, H, 2, true, kBwd>::plan(a, &S2);
+  const long long one = Walk<X, G, H, 1, true, kBwd>::plan(a, &S1);
+  if (two < 0 || one < 0) return GDR_ERR_CUDA;
+  return one * 7 < two * 10 ? Walk<X, G, H, 1, true, kBwd>::launch(d, a, S1, s)
+                            : Walk<X, G, H, 2, true, kBwd>::launch(d, a, S2, s);
+}
+
+template <typename X, typename G, typename H, bool kBwd>
+gdr_status launch_plain(const gdr_scan_dims* d, const ScanArgs& a, cudaStream_t s) {
+  int S = 1;
+  if (Walk<X, G, H, 1, false, kBwd>::plan(a, &S) < 0) return GDR_ERR_CUDA;
+  return Walk<X, G, H, 1, false, kBwd>::launch(d, a, S, s);
 }
 
 enum Path { kPlain, kPairs, kTensorMaps };       // one channel; two; tiles by tensor maps
@@ -669,7 +718,7 @@ gdr_status launch(const gdr_scan_dims* d, const ScanArgs& a, Path path, cudaStre
         using G = std::remove_pointer_t<decltype(g)>;
         using H = std::remove_pointer_t<decltype(h)>;
         if constexpr (!kBwd) {
-          if (a.T <= kSerial) {
+          if (serial(a)) {
             const int V = path == kPlain ? 1 : 2;
             const dim3 grid((a.D + 128 * V - 1) / (128 * V), a.B);
             if (V == 1)
@@ -679,8 +728,8 @@ gdr_status launch(const gdr_scan_dims* d, const ScanArgs& a, Path path, cudaStre
             return launched();
           }
         }
-        return path == kTensorMaps ? launch_walk<X, G, H, 2, true, kBwd>(d, a, s)
-                                   : launch_walk<X, G, H, 1, false, kBwd>(d, a, s);
+        return path == kTensorMaps ? launch_tensor<X, G, H, kBwd>(d, a, s)
+                                   : launch_plain<X, G, H, kBwd>(d, a, s);
       });
     });
   });
