@@ -6,6 +6,7 @@
 #include <type_traits>
 
 #include "gdr_ops.cuh"
+#include "gdr_ptx.cuh"
 
 namespace gdr {
 namespace ops {
@@ -187,8 +188,9 @@ __global__ void __launch_bounds__(GW * 32) qk_any_kernel(QkArgs a) {
 // a group stays with one token for up to 16 of its rows, so that addresses, angles and
 // weights are set up once for them, the weight is folded into the angles
 //   y[j] = rs (M[j] x[j] + N[j] z[j]),   z[j] the other members of the pairs x[j],
-// and fp32 goes two operations an instruction. The next U rows are under way, as raw bits,
-// while U rows are worked on.
+// and fp32 goes two operations an instruction. A lane copies its own runs of the next rows
+// asynchronously into its own places in shared memory (prefetching into registers held two
+// rows and spilled), so it waits for itself alone.
 constexpr int VT = 128;                          // threads per block
 
 // A unit: `rows` head rows of one token, all of q, of k, or (append) of v. Units are numbered
@@ -205,11 +207,26 @@ __device__ __forceinline__ float2 mate(const float2* x, int j) {
   return kNeighbours ? make_float2(x[j].y, x[j].x) : x[j ^ 2];
 }
 
+// Four elements, asynchronously into this thread's own place.
+template <typename T>
+__device__ __forceinline__ void copy_run(T* dst, const T* src) {
+  if constexpr (sizeof(T) == 2)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(ptx::smem_u32(dst)), "l"(src)
+                 : "memory");
+  else
+    ptx::cp_async16(ptx::smem_u32(dst), src, 16);
+}
+
 template <typename I, typename O, int MODE, bool kNeighbours, int GL>
 __global__ void __launch_bounds__(VT, MODE == kBwd ? 4 : 6) qk_vec_kernel(QkArgs a, VecPlan v) {
   constexpr bool bwd = MODE == kBwd;
   if (bwd) asm volatile("griddepcontrol.launch_dependents;");
-  constexpr int U = 2, K = bwd ? 1 : 2;       // rows under way; at work at a time
+  constexpr int K = bwd ? 1 : 2, DEPTH = 4;      // rows at work; steps of as many under way
+  constexpr int XROW = 2 * VT * 4, DROW = bwd ? 2 * VT * 4 : 0;   // elements of a row of the block
+  __shared__ __align__(16) I stage_x[DEPTH * K * XROW];
+  __shared__ __align__(16) O stage_d[bwd ? DEPTH * K * DROW : 1];
+  I* xs = stage_x + threadIdx.x * 4;
+  O* ds = stage_d + (bwd ? threadIdx.x * 4 : 0);
   const int lane = threadIdx.x & (GL - 1), half = a.R >> 1, rot = a.R >> 3;
   const bool on = lane * 8 < a.D, turned = lane < rot;
   const bool split = !kNeighbours && turned;
@@ -218,6 +235,13 @@ __global__ void __launch_bounds__(VT, MODE == kBwd ? 4 : 6) qk_vec_kernel(QkArgs
   const float inv = 1.f / a.D;
   // Groups of one warp may stand at different units: each exchanges among its own lanes.
   const unsigned mask = GL == 32 ? ~0u : ((1u << GL) - 1) << (threadIdx.x & 31 & ~(GL - 1));
+  if (!on) {                                     // channels that are not there: zeros
+    for (int s = 0; s < DEPTH * K * 2; ++s) {
+      const float z[4] = {0.f, 0.f, 0.f, 0.f};
+      store_f<I, 4>(xs + s * (XROW / 2), z);
+      if constexpr (bwd) store_f<O, 4>(ds + s * (DROW / 2), z);
+    }
+  }
   const unsigned groups = gridDim.x * (VT / GL);
   unsigned unit = blockIdx.x * (VT / GL) + threadIdx.x / GL;
 #pragma unroll 1
@@ -244,35 +268,26 @@ __global__ void __launch_bounds__(VT, MODE == kBwd ? 4 : 6) qk_vec_kernel(QkArgs
       const I* xp = src + b * sb + t * st + r0 * sh + o0;
       const O* dp = static_cast<const O*>(n == 0 ? a.dqo : a.dko) + dense;
       const long long pos = position(a, tok);
-      struct Rows {                              // U rows as raw bits
-        Raw<I, 4> x[U][2];
-        Raw<O, 4> d[bwd ? U : 1][2];
-      };
-      auto fetch = [&](Rows& f, int r) {         // the U rows from r; zeros beyond the unit
-        auto row = [&](int k) {
-          f.x[k][0] = load_raw<I, 4>(xp);
-          f.x[k][1] = load_raw<I, 4>(xp + run);
+      // Step i: the K rows from i K, on their way into slot i % DEPTH of this lane.
+      auto fetch = [&](int i) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          if (on && i * K + k < rows) {
+            const int slot = (i % DEPTH) * K + k;
+            copy_run<I>(xs + slot * XROW, xp);
+            copy_run<I>(xs + slot * XROW + XROW / 2, xp + run);
+            if constexpr (bwd) {
+              copy_run<O>(ds + slot * DROW, dp);
+              copy_run<O>(ds + slot * DROW + DROW / 2, dp + run);
+            }
+          }
           xp += sh;
-          if constexpr (bwd) {
-            f.d[k][0] = load_raw<O, 4>(dp);
-            f.d[k][1] = load_raw<O, 4>(dp + run);
-            dp += a.D;
-          }
-        };
-        if (on && r + U <= rows) {
-#pragma unroll
-          for (int k = 0; k < U; ++k) row(k);
-        } else {
-#pragma unroll
-          for (int k = 0; k < U; ++k) {
-            f.x[k][0] = f.x[k][1] = zero_raw<I, 4>();
-            if constexpr (bwd) f.d[k][0] = f.d[k][1] = zero_raw<O, 4>();
-            if (on && r + k < rows) row(k);
-          }
+          dp += a.D;
         }
+        ptx::cp_async_commit();
       };
-      Rows f0, f1;
-      fetch(f0, 0);
+#pragma unroll
+      for (int i = 0; i < DEPTH; ++i) fetch(i);
       bool bad = a.R > 0 && (pos < 0 || pos >= a.rows);
       char* to;                                  // this lane's place in the first result row
       int64_t step;
@@ -325,23 +340,25 @@ __global__ void __launch_bounds__(VT, MODE == kBwd ? 4 : 6) qk_vec_kernel(QkArgs
           sg[j] = mul2(sg[j], m[j]);             // N
         }
       }
-      auto work = [&](const Rows& f, int r) {
-#pragma unroll
-        for (int k0 = 0; k0 < U; k0 += K) {
+#pragma unroll 1
+      for (int r = 0, i = 0; r < rows; r += K, ++i) {
+        ptx::cp_async_wait<DEPTH - 1>();
+        {
           float2 x[K][4], d[K][4];
           float ss[K], dot[K];
 #pragma unroll
           for (int k = 0; k < K; ++k) {
-            to_pairs(f.x[k0 + k][0], x[k]);
-            to_pairs(f.x[k0 + k][1], x[k] + 2);
+            const int slot = (i % DEPTH) * K + k;
+            to_pairs(load_raw<I, 4>(xs + slot * XROW), x[k]);
+            to_pairs(load_raw<I, 4>(xs + slot * XROW + XROW / 2), x[k] + 2);
             float2 q = mul2(x[k][0], x[k][0]);
 #pragma unroll
             for (int j = 1; j < 4; ++j) q = fma2(x[k][j], x[k][j], q);
             ss[k] = q.x + q.y;
             if constexpr (bwd) {
               float2 z[4];
-              to_pairs(f.d[k0 + k][0], z);
-              to_pairs(f.d[k0 + k][1], z + 2);
+              to_pairs(load_raw<O, 4>(ds + slot * DROW), z);
+              to_pairs(load_raw<O, 4>(ds + slot * DROW + DROW / 2), z + 2);
               if (turned) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
@@ -356,6 +373,7 @@ __global__ void __launch_bounds__(VT, MODE == kBwd ? 4 : 6) qk_vec_kernel(QkArgs
               dot[k] = q.x + q.y;
             }
           }
+          fetch(i + DEPTH);
           if (!value) {
 #pragma unroll
             for (int o = GL / 2; o > 0; o >>= 1) {
@@ -392,7 +410,7 @@ __global__ void __launch_bounds__(VT, MODE == kBwd ? 4 : 6) qk_vec_kernel(QkArgs
 #pragma unroll
               for (int j = 0; j < 4; ++j) y[j] = mul2(y[j], rs2);
             }
-            if (keep && r + k0 + k < rows) {
+            if (keep && r + k < rows) {
               if (to_bf16) {
                 store_pairs(reinterpret_cast<bf16*>(to), y);
                 store_pairs(reinterpret_cast<bf16*>(to) + run, y + 2);
@@ -404,15 +422,6 @@ __global__ void __launch_bounds__(VT, MODE == kBwd ? 4 : 6) qk_vec_kernel(QkArgs
             to += step;
           }
         }
-      };
-#pragma unroll 1
-      for (int r = 0;;) {                        // one batch at work, the next under way
-        fetch(f1, r + U);
-        work(f0, r);
-        if ((r += U) >= rows) break;
-        fetch(f0, r + U);
-        work(f1, r);
-        if ((r += U) >= rows) break;
       }
     }
     unit -= v.units[n];
