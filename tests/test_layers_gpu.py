@@ -10,8 +10,8 @@ result has to be the rounding of a value within the fp32 tolerance of the refere
   the row's largest value; 4e-6 is used. Weight gradients sum n rows of such terms: 4e-6 of
   the sum of the terms' magnitudes.
 - Attention: fp32 scores of |s| < 40 are within 40 * 16 e < 4e-5 of themselves, and so is
-  every weight; on the tensor cores a weight is also rounded to bf16 (u):
-  (4e-5 [+ u]) sum p |v| / sum p.
+  every weight; on the tensor cores a weight is also rounded to bf16 (u), or where the
+  result is fp32 to two of them (u^2): (4e-5 [+ u or u^2]) sum p |v| / sum p.
 """
 import math
 
@@ -512,7 +512,9 @@ def attn_check(q, kc, vc, table, lens, window=0, out_dtype=None, scale=None):
     o, lse = gdr.paged_decode_attn(q, kc, vc, table, lens, window=window, out_dtype=out_dtype,
                                    scale=scale)
     ro, rl, size = attn_ref(q, kc, vc, table, lens, scale or 1 / math.sqrt(D), window)
-    tol = 4e-5 + (U if q.dtype == BF and kc.dtype == BF else 0)
+    tol = 4e-5
+    if q.dtype == BF and kc.dtype == BF:
+        tol += U if o.dtype == BF else U * U
     check(o, ro, tol, size)
     dead = torch.isinf(rl)
     assert torch.equal(lse[dead], rl[dead].float())
