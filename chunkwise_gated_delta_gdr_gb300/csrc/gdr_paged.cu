@@ -34,8 +34,7 @@ struct AttnArgs {
   void* out;
   float* lse;                     // may be null
   float *part_o, *part_ml;        // [blocks][2][GMAX][D], [blocks][2][GMAX][2]
-  int4* cut;                      // notes of the items left unfinished (see note_of)
-  int by_item, hb;                // how notes are numbered; heads per join block
+  int by_item, hb;                // of the join: a block per item, or per boundary; heads per block
   int B, HQ, HK, D, G, GH, groups;  // G = HQ / HK; GH query heads per item, groups per kv head
   int page, shift;                // shift: log2(page) if page is a power of two, else -1
   int num_pages, max_pages, window, whole, blocks, out_bf16, q_bf16;
@@ -135,9 +134,6 @@ __device__ __forceinline__ void empty_rows(const AttnArgs& a) {
   for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
     const Span s = span_of(a, b);
     if (s.tiles()) continue;
-    if (a.by_item)
-      for (int i = threadIdx.x; i < a.HK * a.groups; i += blockDim.x)
-        a.cut[b * (a.HK * a.groups) + i] = make_int4(0, 0, 0, 0);
     const float o = s.ok ? 0.f : NAN;
     for (int i = threadIdx.x; i < a.HQ * a.D; i += blockDim.x)
       put(a.out, (size_t)b * a.HQ * a.D + i, o, a.out_bf16);
@@ -147,10 +143,8 @@ __device__ __forceinline__ void empty_rows(const AttnArgs& a) {
   }
 }
 
-// This block's stretch of the line: its first place and its number of tiles (0: none);
-// *per: tiles per block.
-__device__ __forceinline__ long long stretch(const AttnArgs& a, int lane, Place* p,
-                                             long long* per_block) {
+// This block's stretch of the line: its first place and its number of tiles (0: none).
+__device__ __forceinline__ long long stretch(const AttnArgs& a, int lane, Place* p) {
   if (a.whole) {                   // one block per item
     p->b = blockIdx.x / (a.HK * a.groups);
     p->item = blockIdx.x - p->b * (a.HK * a.groups);
@@ -158,26 +152,11 @@ __device__ __forceinline__ long long stretch(const AttnArgs& a, int lane, Place*
     p->s = span_of(a, p->b);
     return p->s.tiles();
   }
-  if (threadIdx.x == 0 && !a.by_item) a.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
   const long long total = total_tiles(a, lane), per = (total + a.blocks - 1) / a.blocks;
   const long long first = blockIdx.x * per, last = min(total, first + per);
   if (first >= last) return 0;
-  *per_block = per;
   *p = locate(a, first, lane);
   return last - first;
-}
-
-// The note of an item cut by a block boundary: {sequence, item, parts, first block}. Few
-// items: one note per item, written by the block that begins it; many: one per block, of the
-// one item it may begin and leave. parts < 2: nothing to join.
-__device__ __forceinline__ int4* note_of(const AttnArgs& a, const Place& p) {
-  return a.cut + (a.by_item ? p.b * (a.HK * a.groups) + p.item : (int)blockIdx.x);
-}
-// Thread 0 of a block that ends its work on an item it began, `rest` tiles before its end.
-__device__ __forceinline__ void write_note(const AttnArgs& a, const Place& p, int rest,
-                                           long long per) {
-  if (threadIdx.x == 0 && !a.whole && (a.by_item || rest > 0))
-    *note_of(a, p) = make_int4(p.b, p.item, 1 + (int)((rest + per - 1) / per), blockIdx.x);
 }
 
 // Element offset of key j of sequence b (kv head 0), or -1 for a bad table entry.
@@ -213,7 +192,7 @@ __global__ void __launch_bounds__(WARPS * 32) paged_any_kernel(AttnArgs a, int v
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane & 7, oct = lane >> 3;
   empty_rows(a);
   Place p;
-  long long per = 1, left = stretch(a, lane, &p, &per);
+  long long left = stretch(a, lane, &p);
   while (left > 0) {
     const int tiles = p.s.tiles();
     const int t1 = (int)min((long long)tiles, p.tile + left);
@@ -328,7 +307,6 @@ __global__ void __launch_bounds__(WARPS * 32) paged_any_kernel(AttnArgs a, int v
     __syncthreads();
     const bool done = p.tile == 0 && t1 == tiles;
     const size_t slot = (size_t)blockIdx.x * 2 + (p.tile == 0 ? 1 : 0);
-    if (p.tile == 0) write_note(a, p, tiles - t1, per);
     for (int e = threadIdx.x; e < heads * a.D; e += WARPS * 32) {
       const int g = e / a.D, d = e - g * a.D;
       float mm = -INFINITY, ll = 0.f, oo = 0.f;
@@ -662,7 +640,7 @@ __global__ void __launch_bounds__(Core::NW * 32, Core::OCC) paged_ring_kernel(At
   asm volatile("griddepcontrol.launch_dependents;");
   empty_rows(a);
   Place pc;                                      // the tile being computed
-  long long per = 1, left = stretch(a, lane, &pc, &per);
+  long long left = stretch(a, lane, &pc);
   if (left <= 0) return;
   Place pi = pc;                                 // the tile being copied
   long long to_copy = left;
@@ -735,7 +713,6 @@ __global__ void __launch_bounds__(Core::NW * 32, Core::OCC) paged_ring_kernel(At
       __syncthreads();
       const bool done = tile0 == 0 && pc.tile + 1 == tiles;
       const size_t part = (size_t)blockIdx.x * 2 + (tile0 == 0 ? 1 : 0);
-      if (tile0 == 0) write_note(a, pc, tiles - pc.tile - 1, per);
       for (int e = threadIdx.x; e < heads * (D / 4); e += NW * 32) {   // four channels each
         const int g = e / (D / 4), d = 4 * (e - g * (D / 4));
         float mm = -INFINITY, ll = 0.f;
@@ -784,55 +761,102 @@ __global__ void __launch_bounds__(Core::NW * 32, Core::OCC) paged_ring_kernel(At
 }
 
 // ------------------------------------------------------------ items cut by block boundaries
-// Block (x, y): heads y hb .. y hb + hb - 1 of note x's item. JW / hb warps share a head,
-// each takes every so manieth part, a lane the channels lane, lane + 32, ...
-constexpr int JW = 8;
+// Launched behind the kernel above, with small blocks that fit beside its own: each finds its
+// item while that kernel still runs, so that all that is left after it is one round of
+// loads. Block (x, y): heads y hb .. of item x, or, with more items than blocks, of the item
+// that the boundary after stretch x is the first to cut. The JW warps share a head's parts
+// (hb < JW) or take every JW-th head; a lane has V channels in a row at a time.
+constexpr int JW = 4;
+template <int V>
 __global__ void __launch_bounds__(JW * 32) paged_join_kernel(AttnArgs a) {
-  __shared__ float red[JW][256], sum[JW], top[JW];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, pw = JW / a.hb;
-  const int hl = warp / pw, w0 = warp - hl * pw, g = blockIdx.y * a.hb + hl;
-  asm volatile("griddepcontrol.wait;" ::: "memory");       // the parts are written
-  const int4 cut = a.cut[blockIdx.x];
-  const int parts = cut.z, c0 = cut.w, hk = cut.y / a.groups;
-  const int g0 = (cut.y - hk * a.groups) * a.GH, heads = min(a.GH, a.G - g0);
-  if (parts < 2) return;
-  auto slot = [&](int c) { return ((size_t)(c0 + c) * 2 + (c == 0)) * GMAX + g; };
-  auto ml_of = [&](int c) { return *reinterpret_cast<const float2*>(a.part_ml + slot(c) * 2); };
-  float m = -INFINITY, l = 0.f, o[8];
+  constexpr int N = 256 / (32 * V);              // runs of V channels of a lane
+  __shared__ float red[JW][256], sum[JW];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int per_b = a.HK * a.groups;
+  const long long total = total_tiles(a, lane), per = (total + a.blocks - 1) / a.blocks;
+  Place p = {};
+  long long first = 0;
+  bool mine = total > 0;
+  if (a.by_item) {
+    p.b = blockIdx.x / per_b;
+    p.item = blockIdx.x - p.b * per_b;
+    p.s = span_of(a, p.b);
+    long long before = 0;
+    for (int b = lane; b < p.b; b += 32) before += span_of(a, b).tiles();
 #pragma unroll
-  for (int i = 0; i < 8; ++i) o[i] = 0.f;
-  if (g < heads) {
+    for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(~0u, before, o);
+    first = before * per_b + (long long)p.item * p.s.tiles();
+    mine = mine && p.s.tiles() > 0;
+  } else {
+    const long long at = (blockIdx.x + 1) * per;
+    mine = mine && at < total;
+    if (mine) {
+      p = locate(a, at, lane);
+      first = at - p.tile;
+      mine = p.tile > 0 && first / per == blockIdx.x;
+    }
+  }
+  const long long c0 = mine ? first / per : 0;
+  const int parts = mine ? (int)((first + p.s.tiles() - 1) / per - c0) + 1 : 0;
+  const int hk = p.item / a.groups, g0 = (p.item - hk * a.groups) * a.GH;
+  const int heads = min(a.GH, a.G - g0), h0 = blockIdx.y * a.hb, h1 = min(heads, h0 + a.hb);
+  asm volatile("griddepcontrol.wait;" ::: "memory");       // the parts are written
+  if (parts < 2) return;
+  const int share = a.hb < JW ? JW / a.hb : 1;             // warps per head
+  const int w0 = warp % share;
+  for (int g = h0 + warp / share; g < h1; g += JW / share) {
+    auto slot = [&](int c) { return ((size_t)(c0 + c) * 2 + (c == 0)) * GMAX + g; };
+    auto ml_of = [&](int c) { return *reinterpret_cast<const float2*>(a.part_ml + slot(c) * 2); };
+    float m = -INFINITY, l = 0.f, o[N][V];
     for (int c = lane; c < parts; c += 32) m = fmaxf(m, ml_of(c).x);
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, x));
-#pragma unroll 4
-    for (int c = w0; c < parts; c += pw) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int v = 0; v < V; ++v) o[i][v] = 0.f;
+#pragma unroll 8
+    for (int c = w0; c < parts; c += share) {
       const size_t s = slot(c);
       const float2 ml = ml_of(c);
       const float f = ml.x == -INFINITY ? 1.f : exp2f(ml.x - m);
       l = fmaf(f, ml.y, l);
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (lane + 32 * i < a.D) o[i] = fmaf(f, a.part_o[s * a.D + lane + 32 * i], o[i]);
-    }
-  }
+      for (int i = 0; i < N; ++i) {
+        const int ch = (lane + 32 * i) * V;
+        if (ch < a.D) {
+          float v[V];
+          load_f<float, V>(a.part_o + s * a.D + ch, v);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) red[warp][lane + 32 * i] = o[i];
-  if (lane == 0) {
-    sum[warp] = l;
-    top[warp] = m;
-  }
-  __syncthreads();
-  for (int e = threadIdx.x; e < a.hb * a.D; e += JW * 32) {
-    const int h = e / a.D, d = e - h * a.D;
-    if (blockIdx.y * a.hb + h >= heads) break;
-    float v = 0.f;
-    l = 0.f;
-    for (int w = h * pw; w < (h + 1) * pw; ++w) {
-      l += sum[w];
-      v += red[w][d];
+          for (int k = 0; k < V; ++k) o[i][k] = fmaf(f, v[k], o[i][k]);
+        }
+      }
     }
-    finish(a, cut.x, hk * a.G + g0 + blockIdx.y * a.hb + h, d, top[h * pw], l, v);
+    const int hq = hk * a.G + g0 + g;
+    if (share == 1) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const int ch = (lane + 32 * i) * V + v;
+          if (ch < a.D) finish(a, p.b, hq, ch, m, l, o[i][v]);
+        }
+    } else {                                     // once: hb < JW heads a block
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int v = 0; v < V; ++v) red[warp][(lane + 32 * i) * V + v] = o[i][v];
+      if (lane == 0) sum[warp] = l;
+      __threadfence_block();
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / share), "r"(share * 32) : "memory");
+      l = 0.f;
+      for (int w = warp - w0; w < warp - w0 + share; ++w) l += sum[w];
+      for (int d = w0 * 32 + lane; d < a.D; d += share * 32) {
+        float v = 0.f;
+        for (int w = warp - w0; w < warp - w0 + share; ++w) v += red[w][d];
+        finish(a, p.b, hq, d, m, l, v);
+      }
+    }
   }
 }
 
@@ -845,8 +869,8 @@ enum Kind { kAny, kMma, kF32 };                  // which kernel
 
 struct Plan {
   Kind kind;
-  int GH, groups, whole, blocks, by_item, notes, hb;
-  size_t o_bytes, ml_bytes, cut_bytes;
+  int GH, groups, whole, blocks, by_item, joins, hb;
+  size_t o_bytes, ml_bytes;
 };
 
 // Whether sizes, types and strides allow a ring kernel (16-byte pieces of every cache row;
@@ -903,18 +927,16 @@ Plan make_plan(const gdr_attn_dims* d, const gdr_paged_cache* c, Kind kind) {
   p.blocks = p.whole ? (int)items : kSms * resident;
   p.o_bytes = p.whole ? 0 : align_up((size_t)p.blocks * 2 * GMAX * c->D * sizeof(float));
   p.ml_bytes = p.whole ? 0 : align_up((size_t)p.blocks * 2 * GMAX * 2 * sizeof(float));
-  // Notes per item where that makes fewer of them; then as many join blocks as keep a few
-  // parts per warp.
+  // The join's blocks: as few heads each as leave two of them per SM.
   p.by_item = !p.whole && items <= p.blocks;
-  p.notes = p.by_item ? (int)items : p.blocks;
+  p.joins = p.by_item ? (int)items : p.blocks - 1;
   const int heads = G < p.GH ? G : p.GH;
-  p.hb = 8;
-  while (p.hb > 1 && (p.hb >= 2 * heads || (long long)p.notes * heads / p.hb < 2 * kSms)) p.hb /= 2;
-  p.cut_bytes = p.whole ? 0 : align_up((size_t)p.blocks * sizeof(int4));
+  p.hb = 1;
+  while (p.hb < heads && (long long)p.joins * ((heads + p.hb - 1) / p.hb) > 2 * kSms) p.hb *= 2;
   return p;
 }
 
-size_t plan_bytes(const Plan& p) { return kAlign + p.o_bytes + p.ml_bytes + p.cut_bytes; }
+size_t plan_bytes(const Plan& p) { return kAlign + p.o_bytes + p.ml_bytes; }
 
 template <class Core>
 gdr_status launch_ring(const AttnArgs& a, cudaStream_t s) {
@@ -979,7 +1001,6 @@ gdr_status gdr_paged_decode_attn(const void* q, const void* k_cache, const void*
   a.out = out; a.lse = lse;
   a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + kAlign);
   a.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + kAlign + p.o_bytes);
-  a.cut = reinterpret_cast<int4*>(static_cast<char*>(workspace) + kAlign + p.o_bytes + p.ml_bytes);
   a.B = dims->B; a.HQ = dims->HQ; a.HK = cache->HK; a.D = cache->D;
   a.G = dims->HQ / cache->HK; a.GH = p.GH; a.groups = p.groups;
   a.page = cache->page_size;
@@ -1016,7 +1037,8 @@ gdr_status gdr_paged_decode_attn(const void* q, const void* k_cache, const void*
   if (run != GDR_OK || p.whole) return run;
   // The join may start while the last parts are being written; it waits for them itself.
   const int heads = a.G < p.GH ? a.G : p.GH;
-  return launch_behind(paged_join_kernel, dim3(p.notes, (heads + p.hb - 1) / p.hb), JW * 32, s, a);
+  return launch_behind(a.D % 4 == 0 ? paged_join_kernel<4> : paged_join_kernel<1>,
+                       dim3(p.joins, (heads + p.hb - 1) / p.hb), JW * 32, s, a);
 }
 
 }  // extern "C"
