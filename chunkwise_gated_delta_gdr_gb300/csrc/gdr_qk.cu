@@ -452,24 +452,25 @@ __global__ void __launch_bounds__(VT, MODE == kBwd ? 4 : 6) qk_vec_kernel(QkArgs
 }
 
 // ------------------------------------------------------------ the weights' gradients
-// 32 columns (channels of dq_weight, then dk_weight) a block; row y of its threads adds every
-// SR-th block's sums, then the rows are added in order.
-constexpr int SR = 32;
-__global__ void __launch_bounds__(32 * SR) qk_weight_kernel(const float* part, int blocks, int D,
+// Eight columns (channels of dq_weight, then dk_weight) a block, so that the loads are a few
+// per thread and spread over many SMs: row y of its threads adds every SR-th block's sums,
+// then the rows are added in order.
+constexpr int SX = 8, SR = 64;
+__global__ void __launch_bounds__(SX * SR) qk_weight_kernel(const float* part, int blocks, int D,
                                                             float* dwq, float* dwk) {
-  __shared__ float red[SR][33];
-  const int x = threadIdx.x & 31, y = threadIdx.x >> 5, col = blockIdx.x * 32 + x;
+  __shared__ float red[SR][SX];
+  const int x = threadIdx.x % SX, y = threadIdx.x / SX, col = blockIdx.x * SX + x;
   asm volatile("griddepcontrol.wait;" ::: "memory");       // the sums are written
   float s = 0.f;
   if (col < 2 * D) {
-#pragma unroll 8
+#pragma unroll 10
     for (int i = y; i < blocks; i += SR) s += part[(size_t)i * 2 * D + col];
   }
   red[y][x] = s;
   __syncthreads();
   if (y || col >= 2 * D) return;
   s = 0.f;
-#pragma unroll
+#pragma unroll 16
   for (int i = 0; i < SR; ++i) s += red[i][x];
   float* out = col < D ? dwq : dwk;
   if (out) out[col < D ? col : col - D] = s;
@@ -664,7 +665,7 @@ gdr_status gdr_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const vo
   int blocks;
   st = launch<kBwd>(dims, a, nullptr, kMaxBlocks, &blocks, s);
   if (st != GDR_OK || !a.part) return st;
-  return launch_behind(qk_weight_kernel, dim3((2 * a.D + 31) / 32), 32 * SR, s,
+  return launch_behind(qk_weight_kernel, dim3((2 * a.D + SX - 1) / SX), SX * SR, s,
                        (const float*)a.part, blocks, a.D, dq_weight, dk_weight);
 }
 

@@ -244,11 +244,13 @@ __global__ void __launch_bounds__(W * 32, 2)
     } else {
       const int t0 = n * TILE + warp * R;
       if (on) {
+        const X* xp = x + t0 * a.xt;
+        const G* gp = g + t0 * a.gt;
 #pragma unroll
-        for (int r = 0; r < R; ++r)
+        for (int r = 0; r < R; ++r, xp += a.xt, gp += a.gt)
           if (t0 + r < a.T) {
-            xf.fetch(stage * SB, r, x + (t0 + r) * a.xt);
-            gf.fetch(stage * SB, r, g + (t0 + r) * a.gt);
+            xf.fetch(stage * SB, r, xp);
+            gf.fetch(stage * SB, r, gp);
           }
       }
       ptx::cp_async_commit();
@@ -384,12 +386,15 @@ __global__ void __launch_bounds__(W * 32, 2)
     } else {
       const int t0 = n * TILE + warp * R;
       if (on && n >= 0) {
+        const X* xp = x + t0 * a.xt;
+        const G* gp = g + t0 * a.gt;
+        const H* dp = dh + t0 * a.dt;
 #pragma unroll
-        for (int r = 0; r < R; ++r)
+        for (int r = 0; r < R; ++r, xp += a.xt, gp += a.gt, dp += a.dt)
           if (t0 + r < a.T) {
-            xf.fetch(stage * SB, r, x + (t0 + r) * a.xt);
-            gf.fetch(stage * SB, r, g + (t0 + r) * a.gt);
-            df.fetch(stage * SB, r, dh + (t0 + r) * a.dt);
+            xf.fetch(stage * SB, r, xp);
+            gf.fetch(stage * SB, r, gp);
+            df.fetch(stage * SB, r, dp);
           }
       }
       ptx::cp_async_commit();
