@@ -3,6 +3,14 @@
 //
 //   r = 1 / sqrt(mean(x^2) + eps),  u = r x,  y = turn(u w)
 //   d = turn^-1(dy),  dw = sum d u,  dx = r (d w - u mean(d w u))
+//
+// Each head row is read once and written once (two reads in the backward): bound by HBM, and
+// close behind it by the instructions per row. Measured on one GB300, bf16, heads of 128:
+//   2 x 8192 x (32 + 4) heads, half of each turned: forward 55 us, 5.5 TB/s (a plain copy:
+//   6.78 TB/s); backward 84 us, 5.4 TB/s
+//   1 x 4096 x (12 + 12) heads: forward 15.5 us, backward 20.5 and the weights' sums 3 us
+//   64 decode tokens x (16 + 4 + 4) heads into their pages: 6.1 us a call, bound by the chain
+//   position - page and angles - row of one token
 #include <type_traits>
 
 #include "gdr_ops.cuh"

@@ -2,6 +2,17 @@
 //
 //   h_t = a_t h_{t-1} + u_t,  a = exp(g),  u = x or (1 - a) x
 //   l_t = dh_t + a_{t+1} l_{t+1};  dx = l (1 - a, gated),  dg = l a (h_{t-1} - x, gated)
+//
+// About 4 operations per element forward and 14 with the backward, against 8 and 14 bytes
+// (bf16 x, fp32 g): bound by HBM where there are channels or sequences enough, by the
+// latency of a step (see below) where there are not. Every element is read once and written
+// once: the sequence is split without a second pass. (1 - a is taken from the rounded a, so
+// that the two weights of the average add up to one; its error is a's own.)
+//
+// Measured on one GB300, bf16 x and fp32 g, us and TB/s (a plain copy: 6.78 TB/s):
+//   forward   1 x 65000 x 4096  311  6.8     2 x 8192 x 4096   84  6.4    1 x 4096 x 1536  16.5  3.0
+//   backward  1 x 65000 x 4096  596  6.3     2 x 8192 x 4096  153  6.1    1 x 4096 x 1536  26.8  3.3
+//   fp32, 3 x 1021 x 777 (rows that no tensor copy can read): 11.2 and 17.4 us, 2.6 and 2.7 TB/s
 #include <type_traits>
 
 #include "gdr_ops.cuh"
@@ -25,7 +36,8 @@ struct ScanArgs {
   int64_t xb, xt, gb, gt, db, dt;   // strides in elements
 };
 
-// One thread per V channels, tokens in order.
+// One thread per V channels, tokens in order: decode steps and short prompts, bound by the
+// launch (64 x 1 x 2048: 4.1 us a call, 3 us of it the kernel).
 template <typename X, typename G, typename H, int V>
 __global__ void __launch_bounds__(128) scan_serial_kernel(ScanArgs a) {
   const int d = (blockIdx.x * 128 + threadIdx.x) * V, b = blockIdx.y;
@@ -67,6 +79,9 @@ __global__ void __launch_bounds__(128) scan_serial_kernel(ScanArgs a) {
 // there with their bytes counted on a barrier of the receiver (one way, where a cluster
 // barrier takes a round trip). Then each warp knows the state before its first token and
 // runs its tokens again from the same registers, now with it. All orders are fixed.
+// A step of a block alone on its SM takes about 1.6 us, 0.5 of them the exchange; with more
+// warps and fewer rows each it took longer (16 warps of 8 rows: 1.54 instead of 1.15 us
+// without the exchange).
 constexpr int W = 8, MAXS = 8;
 constexpr long kWaitLimit = 1L << 24;
 

@@ -360,6 +360,8 @@ size_t gdr_chunk_fwd_segmented_workspace_size(const gdr_dims* dims, int chunk_si
  *
  * T = 1 is the decode step (initial_state and final_state the same buffer).
  * T == 0 writes final_state = initial_state (or zeros) and nothing else.
+ * B <= 65535. No workspace; waits between the blocks of a cluster are bounded, and one that
+ * gave up (a second or so) makes the block's results NaN.
  */
 #define GDR_SCAN_CHECKPOINT 64
 
