@@ -79,7 +79,7 @@ def _link_host(obj: str) -> None:
     libs = os.path.join(_torch_dir(), "lib")
     tmp = HOST + f".tmp{os.getpid()}"
     _run(["g++", "-shared", "-o", tmp, obj, "-L" + libs, "-ltorch_python", "-ltorch", "-ltorch_cpu",
-          "-lc10", "-lc10_cuda", "-L" + OUT_DIR, "-lgdr", "-Wl,-rpath," + libs,
+          "-ltorch_cuda", "-lc10", "-lc10_cuda", "-L" + OUT_DIR, "-lgdr", "-Wl,-rpath," + libs,
           "-Wl,-rpath,$ORIGIN"], "link of " + HOST)
     os.replace(tmp, HOST)
 

@@ -184,22 +184,21 @@ __device__ __forceinline__ void cluster_carry(ScanShared<V, kBwd>& sm, int step,
 // One tensor's tiles on their way into a ring in shared memory, token-major. kTensor: a
 // thread copies whole tiles, out-of-range tokens and channels arriving as zeros (so that
 // a = exp(0) = 1 and u = 0 there: tokens that change nothing). Otherwise each thread copies
-// its own channel's tokens, fp32 asynchronously, bf16 (too small for such a copy) through
-// registers; it reads only those, so it waits for itself alone.
+// its own channels' tokens, 4 or 8 bytes asynchronously, a single bf16 (too small for such a
+// copy) through registers; it reads only those, so it waits for itself alone.
 template <typename T, int V, int R, bool kTensor>
 struct Feed {
-  static constexpr bool kRing = kTensor || sizeof(T) == 4;
+  static constexpr bool kRing = kTensor || sizeof(T) * V >= 4;
   static constexpr int kBytes = kRing ? W * R * 32 * V * (int)sizeof(T) : 0;    // of a stage
   Raw<T, V> reg[kRing ? 1 : R];
   char* base;
   __device__ __forceinline__ Feed(char* ring, int warp, int lane)
       : base(ring + (warp * R * 32 + lane) * V * (int)sizeof(T)) {}
   __device__ __forceinline__ void fetch(int offset, int r, const T* p) {
-    static_assert(kTensor || V == 1, "");
     if constexpr (kRing)
-      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
+      asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(
                        ptx::smem_u32(base + offset + r * (32 * V * (int)sizeof(T)))),
-                   "l"(p)
+                   "l"(p), "n"(V * (int)sizeof(T))
                    : "memory");
     else
       reg[r] = load_once<T, V>(p);
@@ -214,8 +213,9 @@ struct Feed {
 };
 
 // Tiles under way. Without a ring for every tensor: the one the registers hold.
-template <typename X, typename G, typename H, bool kTensor>
-constexpr int kStages = kTensor || (sizeof(X) == 4 && sizeof(G) == 4 && sizeof(H) == 4) ? 2 : 1;
+template <typename X, typename G, typename H, int V, bool kTensor>
+constexpr int kStages =
+    kTensor || (sizeof(X) * V >= 4 && sizeof(G) * V >= 4 && sizeof(H) * V >= 4) ? 2 : 1;
 
 struct ScanMaps {
   CUtensorMap x, g, dh;
@@ -223,7 +223,7 @@ struct ScanMaps {
 
 template <typename X, typename G, typename H, int V, bool kTensor>
 struct Fwd {
-  static constexpr int R = kRows<X, G, V>, TILE = W * R, ST = kStages<X, G, float, kTensor>;
+  static constexpr int R = kRows<X, G, V>, TILE = W * R, ST = kStages<X, G, float, V, kTensor>;
   static constexpr int XB = Feed<X, V, R, kTensor>::kBytes, GB = Feed<G, V, R, kTensor>::kBytes;
   static constexpr int SB = XB + GB, SMEM = ST * SB;
 };
@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(W * 32, 2)
 // inside a tile come from its checkpoint and the warps' forward pairs.
 template <typename X, typename G, typename H, int V, bool kTensor>
 struct Bwd {
-  static constexpr int R = CK / W, TILE = CK, ST = kStages<X, G, H, kTensor>;
+  static constexpr int R = CK / W, TILE = CK, ST = kStages<X, G, H, V, kTensor>;
   static constexpr int XB = Feed<X, V, R, kTensor>::kBytes, GB = Feed<G, V, R, kTensor>::kBytes;
   static constexpr int DB = Feed<H, V, R, kTensor>::kBytes;
   static constexpr int SB = XB + GB + DB, SMEM = ST * SB;
@@ -720,11 +720,11 @@ gdr_status launch_tensor(const gdr_scan_dims* d, const ScanArgs& a, cudaStream_t
                             : Walk<X, G, H, 2, true, kBwd>::launch(d, a, S2, s);
 }
 
-template <typename X, typename G, typename H, bool kBwd>
+template <typename X, typename G, typename H, int V, bool kBwd>
 gdr_status launch_plain(const gdr_scan_dims* d, const ScanArgs& a, cudaStream_t s) {
   int S = 1;
-  if (Walk<X, G, H, 1, false, kBwd>::plan(a, &S) < 0) return GDR_ERR_CUDA;
-  return Walk<X, G, H, 1, false, kBwd>::launch(d, a, S, s);
+  if (Walk<X, G, H, V, false, kBwd>::plan(a, &S) < 0) return GDR_ERR_CUDA;
+  return Walk<X, G, H, V, false, kBwd>::launch(d, a, S, s);
 }
 
 enum Path { kPlain, kPairs, kTensorMaps };       // one channel; two; tiles by tensor maps
@@ -749,7 +749,8 @@ gdr_status launch(const gdr_scan_dims* d, const ScanArgs& a, Path path, cudaStre
           }
         }
         return path == kTensorMaps ? launch_tensor<X, G, H, kBwd>(d, a, s)
-                                   : launch_plain<X, G, H, kBwd>(d, a, s);
+               : path == kPairs    ? launch_plain<X, G, H, 2, kBwd>(d, a, s)
+                                   : launch_plain<X, G, H, 1, kBwd>(d, a, s);
       });
     });
   });
@@ -760,7 +761,8 @@ Path choose(const gdr_scan_dims* d, const ScanArgs& a) {
       (!a.dh || tensor_ok(a.dh, d->h_dtype, a, a.db, a.dt)))
     return kTensorMaps;
   return a.D % 2 == 0 && vec_ok(a.x, d->x_dtype, a.xb, a.xt, 2) &&
-                 vec_ok(a.g, d->g_dtype, a.gb, a.gt, 2)
+                 vec_ok(a.g, d->g_dtype, a.gb, a.gt, 2) &&
+                 (!a.dh || vec_ok(a.dh, d->h_dtype, a.db, a.dt, 2))
              ? kPairs
              : kPlain;
 }

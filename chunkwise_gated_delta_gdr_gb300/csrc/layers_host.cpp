@@ -9,13 +9,14 @@
 // than GDR_OK) it returns None, and layers.py goes its own way, with its messages.
 #include <Python.h>
 
-#include <ATen/Functions.h>
 #include <ATen/core/Tensor.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
+#include <optional>
 
 #include "gdr.h"
 
@@ -78,7 +79,7 @@ struct Call {
     return reinterpret_cast<gdr_stream_t>(c10::cuda::getCurrentCUDAStream(device).stream());
   }
   Tensor empty(at::IntArrayRef shape, at::ScalarType type) const {
-    return at::empty(shape, at::TensorOptions().dtype(type).device(at::kCUDA, device));
+    return at::detail::empty_cuda(shape, type, at::Device(at::kCUDA, device), std::nullopt);
   }
 };
 

@@ -110,7 +110,7 @@ def test_scan_shapes(shape, gated):
 
 
 @pytest.mark.parametrize("xd,gd", [(BF, F32), (BF, BF), (F32, BF)])
-@pytest.mark.parametrize("shape", [(2, 1, 34), (1, 777, 33), (2, 1300, 128)])
+@pytest.mark.parametrize("shape", [(2, 1, 34), (1, 777, 33), (2, 1300, 128), (1, 900, 130)])
 def test_scan_types(shape, xd, gd):
     scan_check(*scan_inputs(*shape, xd, gd, 2), True)
     scan_check(*scan_inputs(*shape, xd, gd, 3), False)
