@@ -6,9 +6,9 @@
 //
 // Each head row is read once and written once (two reads in the backward): bound by HBM, and
 // close behind it by the instructions per row. Measured on one GB300, bf16, heads of 128:
-//   2 x 8192 x (32 + 4) heads, half of each turned: forward 55 us, 5.5 TB/s (a plain copy:
+//   2 x 8192 x (32 + 4) heads, half of each turned: forward 53 us, 5.7 TB/s (a plain copy:
 //   6.78 TB/s); backward 84 us, 5.4 TB/s
-//   1 x 4096 x (12 + 12) heads: forward 15.5 us, backward 20.5 and the weights' sums 3 us
+//   1 x 4096 x (12 + 12) heads: forward 15 us, backward 20 and the weights' sums 3 us
 //   64 decode tokens x (16 + 4 + 4) heads into their pages: 6.1 us a call, bound by the chain
 //   position - page and angles - row of one token
 #include <type_traits>
@@ -225,8 +225,12 @@ __device__ __forceinline__ void copy_run(T* dst, const T* src) {
     ptx::cp_async16(ptx::smem_u32(dst), src, 16);
 }
 
+// Blocks an SM holds. Seven forward, with spills, changed no time by more than 4 % (1 x 4096
+// tokens: 12 + 12 heads 14.4 us against 14.9, 32 + 8 heads 20.5 against 18.7).
+constexpr int resident(int mode) { return mode == kBwd ? 4 : 6; }
+
 template <typename I, typename O, int MODE, bool kNeighbours, int GL>
-__global__ void __launch_bounds__(VT, MODE == kBwd ? 4 : 6) qk_vec_kernel(QkArgs a, VecPlan v) {
+__global__ void __launch_bounds__(VT, resident(MODE)) qk_vec_kernel(QkArgs a, VecPlan v) {
   constexpr bool bwd = MODE == kBwd;
   if (bwd) asm volatile("griddepcontrol.launch_dependents;");
   constexpr int K = bwd ? 1 : 2, DEPTH = 4;      // rows at work; steps of as many under way
@@ -555,22 +559,33 @@ bool vec_ok(const gdr_qk_dims* d, const QkArgs& a, int mode, const gdr_paged_cac
   return a.tokens * (a.HQ + 2LL * a.HK) < (1LL << 31);
 }
 
-VecPlan vec_plan(const QkArgs& a, int mode) {
-  VecPlan v = {};
-  v.GL = 8;
-  while (v.GL * 8 < a.D) v.GL *= 2;
+// The split of a token's heads into rows of at most `most` per group; returns the blocks.
+long long vec_split(const QkArgs& a, int mode, int most, VecPlan& v) {
   const int heads[3] = {a.HQ, a.HK, mode == kAppend ? a.HK : 0};
-  // At most 16 head rows of a token per group, fewer where that leaves the device empty.
-  const long long share =
-      a.tokens * (heads[0] + heads[1] + heads[2]) / (152LL * (1024 / v.GL));
-  const int most = (int)(share < 1 ? 1 : share > 16 ? 16 : share);
+  long long units = 0;
   for (int n = 0; n < 3; ++n) {
     if (!heads[n]) continue;
     const int chunks = (heads[n] + most - 1) / most;
     v.rows[n] = (heads[n] + chunks - 1) / chunks;
     v.chunks[n] = (heads[n] + v.rows[n] - 1) / v.rows[n];
     v.units[n] = (unsigned)(a.tokens * v.chunks[n]);
+    units += v.units[n];
   }
+  return (units * v.GL + VT - 1) / VT;
+}
+
+// More rows per group spread a token's angles and addresses over more work, until some SMs
+// have none: the fewest of 1, 2, 4 .. 16 rows whose blocks are resident at once, else 16
+// (2 x 512 x (32 + 8) heads forward: 4 rows 10.2 us, 8 rows 8.3, 32 rows 10.3); forward 32
+// where that leaves four rounds (2 x 8192 x (32 + 4) heads: 53.4 us against 55.4; with their
+// values into pages 67.6 against 71.1; backward 84.0 against 82.4, so not there).
+VecPlan vec_plan(const QkArgs& a, int mode) {
+  VecPlan v = {};
+  v.GL = 8;
+  while (v.GL * 8 < a.D) v.GL *= 2;
+  const long long round = 152LL * resident(mode);
+  if (mode != kBwd && vec_split(a, mode, 32, v) >= 4 * round) return v;
+  for (int most = 1; vec_split(a, mode, most, v) > round && most < 16;) most *= 2;
   return v;
 }
 
