@@ -119,7 +119,11 @@ def _struct(cls, *values):
     if s is None:
         if len(_structs) >= 4096:
             _structs.clear()
-        s = _structs[key] = cls(*values)
+        s = cls(*values)
+        for (name, _), v in zip(cls._fields_, values):
+            if isinstance(v, int) and getattr(s, name) != v:
+                raise ValueError(f"{name} = {v} is out of range")
+        _structs[key] = s
     return s
 
 
@@ -160,15 +164,21 @@ def _stream(device, stream):
         raise ValueError(f"tensors must be on the current CUDA device, got {device}")
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(device.index)
+    if stream.device != device:
+        raise ValueError(f"stream must be on {device}, got {stream.device}")
     return stream.cuda_stream
 
 
-def _hold(stream, *tensors):
-    """Tensors allocated here and used on another stream than torch's current one."""
-    if stream is not None:
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+def _empty(shape, dtype, device, stream):
+    """A result or scratch. For a stream that is not torch's current one it comes from that
+    stream's pool, so that nothing queued elsewhere still uses its memory when the kernel
+    writes it, and it goes back there only after the current stream's work, too."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
 
 
 def _raise(status, where):
@@ -211,13 +221,11 @@ def linear_scan_fwd(x, g, initial_state=None, *, gated_input: bool = False,
         raise ValueError("x must be dense in its last dimension")
     _view("g", g, shape, device)
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype or x.dtype, device=device)
-        _hold(stream, out)
+        out = _empty(shape, out_dtype or x.dtype, device, stream)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise TypeError(f"out must be {out_dtype}, got {out.dtype}")
     if final_state is None and output_final_state:
-        final_state = torch.empty(B, D, dtype=torch.float32, device=device)
-        _hold(stream, final_state)
+        final_state = _empty((B, D), torch.float32, device, stream)
     dims = _struct(gdr_scan_dims, B, T, D, _code("x", x), _code("g", g), _code("out", out),
                    bool(gated_input), xs[0], xs[1], gs[0], gs[1], 0, 0)
     state = (B, D)
@@ -253,14 +261,11 @@ def linear_scan_bwd(dh, x, g, checkpoints, d_final_state=None, *, gated_input: b
     if checkpoints is None:
         raise ValueError("checkpoints of the forward call are needed")
     if dx is None:
-        dx = torch.empty(shape, dtype=x.dtype, device=device)
-        _hold(stream, dx)
+        dx = _empty(shape, x.dtype, device, stream)
     if dg is None:
-        dg = torch.empty(shape, dtype=g.dtype, device=device)
-        _hold(stream, dg)
+        dg = _empty(shape, g.dtype, device, stream)
     if d_initial_state is None and output_initial_state_grad:
-        d_initial_state = torch.empty(B, D, dtype=torch.float32, device=device)
-        _hold(stream, d_initial_state)
+        d_initial_state = _empty((B, D), torch.float32, device, stream)
     xs, gs, ds = x.stride(), g.stride(), dh.stride()
     dims = _struct(gdr_scan_dims, B, T, D, _code("x", x), _code("g", g), _code("dh", dh),
                    bool(gated_input), xs[0], xs[1], gs[0], gs[1], ds[0], ds[1])
@@ -341,13 +346,11 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positio
     device, HK = q.device, k.shape[2]
     raw = _stream(device, stream)
     if q_out is None:
-        q_out = torch.empty(B, T, HQ, D, dtype=out_dtype or q.dtype, device=device)
-        _hold(stream, q_out)
+        q_out = _empty((B, T, HQ, D), out_dtype or q.dtype, device, stream)
     elif out_dtype is not None and q_out.dtype != out_dtype:
         raise TypeError(f"q_out must be {out_dtype}, got {q_out.dtype}")
     if k_out is None:
-        k_out = torch.empty(B, T, HK, D, dtype=q_out.dtype, device=device)
-        _hold(stream, k_out)
+        k_out = _empty((B, T, HK, D), q_out.dtype, device, stream)
     dims = _qk_dims(q, k, None, cos, sin, positions, eps, interleaved, _code("q_out", q_out))
     st = _lib().gdr_qk_norm_rope(
         q.data_ptr(), k.data_ptr(),
@@ -373,23 +376,19 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, cos=Non
     device, HK = q.device, k.shape[2]
     raw = _stream(device, stream)
     if dq is None:
-        dq = torch.empty(B, T, HQ, D, dtype=q.dtype, device=device)
-        _hold(stream, dq)
+        dq = _empty((B, T, HQ, D), q.dtype, device, stream)
     if dk is None:
-        dk = torch.empty(B, T, HK, D, dtype=q.dtype, device=device)
-        _hold(stream, dk)
+        dk = _empty((B, T, HK, D), q.dtype, device, stream)
     dims = _qk_dims(q, k, None, cos, sin, positions, eps, interleaved, _code("dq_out", dq_out))
     dwq = dwk = None
     ws_bytes = 0
     lib = _lib()
     if output_weight_grads:
-        dwq = torch.empty(D, dtype=torch.float32, device=device)
-        dwk = torch.empty(D, dtype=torch.float32, device=device)
+        dwq = _empty((D,), torch.float32, device, stream)
+        dwk = _empty((D,), torch.float32, device, stream)
         if workspace is None:
             size = lib.gdr_qk_norm_rope_bwd_workspace_size(dims)
-            workspace = torch.empty(max(size, 256), dtype=torch.uint8, device=device)
-            _hold(stream, workspace)
-        _hold(stream, dwq, dwk)
+            workspace = _empty((max(size, 256),), torch.uint8, device, stream)
         ws_bytes = workspace.numel()
     st = lib.gdr_qk_norm_rope_bwd(
         _dense("dq_out", dq_out, (B, T, HQ, D), device, dq_out.dtype),
@@ -439,8 +438,7 @@ def qk_norm_rope_append(q, k, v, q_weight, k_weight, cos, sin, positions, k_cach
     device = q.device
     raw = _stream(device, stream)
     if q_out is None:
-        q_out = torch.empty(B, T, HQ, D, dtype=out_dtype or q.dtype, device=device)
-        _hold(stream, q_out)
+        q_out = _empty((B, T, HQ, D), out_dtype or q.dtype, device, stream)
     elif out_dtype is not None and q_out.dtype != out_dtype:
         raise TypeError(f"q_out must be {out_dtype}, got {q_out.dtype}")
     if positions is None or v is None:
@@ -499,19 +497,16 @@ def paged_decode_attn(q, k_cache, v_cache, page_table, lens, *, scale: Optional[
     shape, device = q.shape, q.device
     raw = _stream(device, stream)
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype or q.dtype, device=device)
-        _hold(stream, out)
+        out = _empty(shape, out_dtype or q.dtype, device, stream)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise TypeError(f"out must be {out_dtype}, got {out.dtype}")
     dims, cache = _attn_dims(q, k_cache, v_cache, page_table, scale, window, _code("out", out))
     if lse is None:
-        lse = torch.empty(shape[:2], dtype=torch.float32, device=device)
-        _hold(stream, lse)
+        lse = _empty(shape[:2], torch.float32, device, stream)
     lib = _lib()
     if workspace is None:
         size = lib.gdr_paged_decode_attn_workspace_size(dims, cache)
-        workspace = torch.empty(max(size, 256), dtype=torch.uint8, device=device)
-        _hold(stream, workspace)
+        workspace = _empty((max(size, 256),), torch.uint8, device, stream)
     st = lib.gdr_paged_decode_attn(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(),
         _dense("lens", lens, shape[:1], device, torch.int32),

@@ -267,3 +267,12 @@ def test_binding_checks_of_the_rotation(layers):
         layers._qk_dims(q, k.double(), None, cos, cos, pos, 1e-6, False, 0)
     with pytest.raises(ValueError, match="shape"):
         layers._qk_dims(q, k[:, :2], None, cos, cos, pos, 1e-6, False, 0)
+
+
+def test_binding_refuses_sizes_past_32_bits(layers):
+    for v in (1 << 31, 1 << 32, -(1 << 31) - 1):
+        with pytest.raises(ValueError, match="out of range"):
+            layers._struct(layers.gdr_scan_dims, 1, v, 1, 0, 0, 0, False, 0, 0, 0, 0, 0, 0)
+    s = layers._struct(layers.gdr_scan_dims, 1, (1 << 31) - 1, 1, 0, 0, 0, True, 1 << 40, 0, 0, 0,
+                       0, 0)
+    assert s.T == (1 << 31) - 1 and s.gated_input == 1 and s.x_stride_b == 1 << 40

@@ -317,6 +317,28 @@ def test_qk_forward_and_backward(case, odd):
         check(dw, rw, 4e-6, mags)
 
 
+def test_qk_many_rows_per_group():
+    """Long inputs keep up to 32 heads of a token in one group: 33 + 3 heads, split 17 and 16."""
+    q, k, v, wq, wk, cos, sin, pos = qk_inputs(1, 20000, 33, 3, 64, 64, BF, 27)
+    qo, ko = gdr.qk_norm_rope(q, k, wq, wk, cos, sin, pos)
+    for x, w, y in ((q, wq, qo), (k, wk, ko)):
+        ref = qk_ref(x, w, cos, sin, pos, 1e-6, False)
+        check(y, ref, 4e-6, row_scale(ref))
+    table, total = make_pages(torch.tensor([20000]), 64, gen_of(28))
+    kc, vc = make_cache(gen_of(29), total, 64, 3, 64, BF)
+    at = torch.arange(20000, device=DEV)[None].int()
+    order = torch.arange(20000, device=DEV)
+    pages = table.to(DEV)[0].long()[order // 64]
+    plain = gdr.qk_norm_rope(q, k, wq, wk, cos[:1].expand_as(cos).contiguous(),
+                             sin[:1].expand_as(sin).contiguous(), pos)
+    same = gdr.qk_norm_rope_append(q, k, v, wq, wk, cos[:1].expand(20000, -1).contiguous(),
+                                   sin[:1].expand(20000, -1).contiguous(), at, kc, vc,
+                                   table.to(DEV))
+    assert torch.equal(same, plain[0])
+    assert torch.equal(kc[pages, order % 64], plain[1][0])
+    assert torch.equal(vc[pages, order % 64], v[0])
+
+
 @pytest.mark.parametrize("dt,out", [(BF, F32), (F32, BF)])
 @pytest.mark.parametrize("D", [128, 30])
 def test_qk_output_type(dt, out, D):
@@ -719,6 +741,31 @@ def test_another_stream():
     got = calls(side)
     side.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def test_memory_of_results_on_another_stream():
+    """Memory that the current stream still reads is not given to a call on another one."""
+    x, g, _, _, _ = scan_inputs(1, 4096, 1024, BF, F32, 57)
+    want = gdr.linear_scan_fwd(x, g)[0]
+    big, old, copy = torch.zeros(1 << 28, device=DEV), torch.full_like(want, 3), want.clone()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        big.mul_(1.0)
+    copy.copy_(old)
+    del old
+    got = gdr.linear_scan_fwd(x, g, stream=side)[0]
+    torch.cuda.synchronize()
+    assert (copy == 3).all() and torch.equal(got, want)
+
+
+def test_sizes_past_32_bits_are_refused():
+    x = torch.empty(1 << 32, 0, 4, dtype=BF, device=DEV)
+    with pytest.raises(ValueError, match="B = 4294967296"):
+        gdr.linear_scan_fwd(x, x, output_final_state=False)
+    q = torch.empty(1 << 32, 0, 1, 64, dtype=BF, device=DEV)
+    with pytest.raises(ValueError, match="B = 4294967296"):
+        gdr.qk_norm_rope(q, q)
 
 
 def test_capture_in_a_graph():
