@@ -771,10 +771,11 @@ __global__ void __launch_bounds__(Core::NW * 32, Core::OCC) paged_ring_kernel(At
 
 // ------------------------------------------------------------ items cut by block boundaries
 // Launched behind the kernel above; each block finds its item before it waits for that kernel,
-// so that what is left after it is two rounds of loads. It costs 4 us at 64 sequences and 6
-// at one of 65000 keys (54 parts), most of it the second kernel's start. Block (x, y): heads y hb .. of item x, or, with more items than blocks, of the item
-// that the boundary after stretch x is the first to cut. The JW warps share a head's parts
-// (hb < JW) or take every JW-th head; a lane has V channels in a row at a time.
+// so that what is left after it is two rounds of loads. It costs 4 us at 64 sequences and 6 at
+// one of 65000 keys (54 parts), most of it the second kernel's start. Block (x, y): heads y hb
+// and on of item x, or, with more items than blocks, of the item that the boundary after
+// stretch x is the first to cut. The JW warps share a head's parts (hb < JW) or take every
+// JW-th head; a lane has V channels in a row at a time.
 constexpr int JW = 4;
 template <int V>
 __global__ void __launch_bounds__(JW * 32) paged_join_kernel(AttnArgs a) {

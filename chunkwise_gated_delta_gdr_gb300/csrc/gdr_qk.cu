@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(GW * 32) qk_any_kernel(QkArgs a) {
 // pairs are its own: the runs at 4 j and 4 j + R / 2 (2 x 4 neighbouring channels when pairs
 // are neighbours, and beyond R). So the rotation needs no exchange, the norm one tree of
 // shuffles. What bounds this kernel beside the bytes is the number of instructions per row:
-// a group stays with one token for up to 16 of its rows, so that addresses, angles and
+// a group stays with one token for up to 32 of its rows, so that addresses, angles and
 // weights are set up once for them, the weight is folded into the angles
 //   y[j] = rs (M[j] x[j] + N[j] z[j]),   z[j] the other members of the pairs x[j],
 // and fp32 goes two operations an instruction. A lane copies its own runs of the next rows
