@@ -448,29 +448,30 @@ struct MmaCore {
         l[h >> 1] += s[n][h];                    // unrounded; the lanes' sums meet at the end
       }
     if (bad) l[0] = l[1] = NAN;
-    // The weights are rounded to bf16 for the product with V, which puts as much error into
-    // the result as rounding it to bf16 does. Where the result is fp32, a second product adds
-    // what the rounding left over: 16 bits of a weight then, for 2 % of the time at D = 128.
-    auto times_v = [&](const uint32_t* p) {
+    // A weight goes into the product with V as two bf16: its upper bits as they are, then what
+    // they leave over, rounded; 2^-15 of it is lost at most (one bf16 alone would put as much
+    // error into a bf16 result as rounding that does). Neither part is negative, and the second
+    // is never 0 beside a first that is not, so that an infinite v gives what w v gives.
+    uint32_t hi[4], lo[4];
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        uint32_t f[4];
-        ptx::ldsm_x4_t(f, vd + vrow + (vpc ^ (32 * i)));
-        ptx::mma_bf16_16816(o[2 * i], p, f[0], f[1]);
-        ptx::mma_bf16_16816(o[2 * i + 1], p, f[2], f[3]);
-      }
-    };
-    uint32_t p[4];
+    for (int i = 0; i < 4; ++i) {
+      const float *w = &s[i >> 1][2 * (i & 1)];
+      float rest[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = pack2(s[i >> 1][2 * (i & 1)], s[i >> 1][2 * (i & 1) + 1]);
-    times_v(p);
-    if (!a.out_bf16) {
+      for (int e = 0; e < 2; ++e)
+        rest[e] = fmaxf(w[e] - __uint_as_float(__float_as_uint(w[e]) & 0xffff0000u),
+                        fminf(w[e], 0x1p-126f));
+      hi[i] = __byte_perm(__float_as_uint(w[0]), __float_as_uint(w[1]), 0x7632);
+      lo[i] = pack2(rest[0], rest[1]);
+    }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 h = unpack2(p[i]);
-        p[i] = pack2(s[i >> 1][2 * (i & 1)] - h.x, s[i >> 1][2 * (i & 1) + 1] - h.y);
-      }
-      times_v(p);
+    for (int i = 0; i < D / 16; ++i) {
+      uint32_t f[4];
+      ptx::ldsm_x4_t(f, vd + vrow + (vpc ^ (32 * i)));
+      ptx::mma_bf16_16816(o[2 * i], hi, f[0], f[1]);
+      ptx::mma_bf16_16816(o[2 * i + 1], hi, f[2], f[3]);
+      ptx::mma_bf16_16816(o[2 * i], lo, f[0], f[1]);
+      ptx::mma_bf16_16816(o[2 * i + 1], lo, f[2], f[3]);
     }
   }
 

@@ -520,12 +520,12 @@ gdr_status gdr_qk_norm_rope_append(const void* q, const void* k, const void* v,
  *
  * D <= 256. bf16 q and caches with D in {64, 80, 96, 128, 192, 256} and 16-byte
  * aligned rows run on the tensor cores (products of bf16 values, sums and the
- * softmax in fp32, its weights rounded to bf16 for the product with V, or to two
- * bf16 where the result is fp32); the others in fp32. Keys outside the range are not read, whatever they hold. A
- * row without keys, or with scores of -inf alone, gives o = 0 and lse = -inf. A length outside
- * [0, max_pages page_size] or a table entry outside [0, num_pages) gives NaN
- * for that sequence. The result does not depend on the order in which blocks
- * run.
+ * softmax in fp32, each of its weights split into two bf16 for the product with
+ * V, which loses 2^-15 of it at most); the others in fp32. Keys outside the range
+ * are not read, whatever they hold. A row without keys, or with scores of -inf
+ * alone, gives o = 0 and lse = -inf. A length outside [0, max_pages page_size] or
+ * a table entry outside [0, num_pages) gives NaN for that sequence. The result
+ * does not depend on the order in which blocks run.
  */
 typedef struct {
   int B, HQ;

@@ -1,0 +1,56 @@
+"""The layers' operators where values, sizes and arguments are out of the ordinary, against
+the 64-bit implementations of test_layers_gpu.py; tolerances as derived there, or beside the
+test."""
+import math
+
+import pytest
+import torch
+
+import chunkwise_gated_delta_gdr_gb300 as gdr
+from test_layers_gpu import BF, DEV, EDGE, F32, attn_ref, check, gen_of, make_cache, make_pages, rnd
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ weights of the attention
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("D", [64, 80, 96, 128, 192, 256])
+def test_attn_weights_keep_two_parts(D, out):
+    """bf16 caches, results of either type: a weight loses at most 2^-15 of itself on the tensor
+    cores, beside the 4e-5 of every form; whole rows and rows cut into parts and joined."""
+    gen = gen_of(70)
+    for lens in (torch.tensor(EDGE + [2, 3, 300]), torch.tensor([5, 5000, 0, 700])):
+        table, total = make_pages(lens, 16, gen)
+        kc, vc = make_cache(gen, total, 16, 2, D, BF)
+        q = rnd(gen, len(lens), 6, D, dtype=BF)
+        table, lens = table.to(DEV), lens.int().to(DEV)
+        o, _ = gdr.paged_decode_attn(q, kc, vc, table, lens, out_dtype=out)
+        ref, _, size = attn_ref(q, kc, vc, table, lens, 1 / math.sqrt(D), 0)
+        check(o, ref, 4e-5 + 2.0 ** -15, size)
+
+
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("dt,D", [(BF, 128), (BF, 256), (F32, 64), (BF, 40)])
+@pytest.mark.parametrize("n", [90, 3000])
+def test_attn_infinite_values(dt, D, out, n):
+    """One infinite value makes its channel infinite for the heads that see it, two of opposite
+    signs (or a NaN) make it NaN; every other channel keeps its bits."""
+    gen = gen_of(71)
+    lens = torch.tensor([n, n])
+    table, total = make_pages(lens, 16, gen)
+    kc, vc = make_cache(gen, total, 16, 2, D, dt)
+    kc *= 0.25                               # weights of one size
+    q, lens = rnd(gen, 2, 4, D, dtype=dt), lens.int().to(DEV)
+    good, lse = gdr.paged_decode_attn(q, kc, vc, table.to(DEV), lens, out_dtype=out)
+
+    def put(j, ch, value):                   # sequence 0, kv head 1: query heads 2 and 3
+        vc[table[0, j // 16].item(), j % 16, 1, ch] = value
+
+    put(3, 0, math.inf), put(40, 9, -math.inf), put(n - 1, 2, math.inf)
+    put(17, 5, math.inf), put(70, 5, -math.inf), put(20, 7, math.nan)
+    o, lse2 = gdr.paged_decode_attn(q, kc, vc, table.to(DEV), lens, out_dtype=out)
+    want = good.clone()
+    want[0, 2:, [0, 2]], want[0, 2:, 9], want[0, 2:, [5, 7]] = math.inf, -math.inf, math.nan
+    assert torch.equal(lse, lse2)
+    assert torch.equal(torch.isnan(o), torch.isnan(want))
+    assert torch.equal(o.nan_to_num(1.5), want.nan_to_num(1.5))
