@@ -5,8 +5,8 @@
 #include <cuda_bf16.h>
 #include <atomic>
 #include <math.h>
-#include <string.h>
 #include <stdint.h>
+#include <type_traits>
 
 #include "gdr_internal.cuh"
 
@@ -58,10 +58,11 @@ __device__ __forceinline__ Raw<T, V> load_once(const T* p) {
   return r;
 }
 template <typename T, int V>
-__device__ __forceinline__ Raw<T, V> zero_raw() {
-  Raw<T, V> r;
-  memset(&r, 0, sizeof r);
-  return r;
+__device__ __forceinline__ void store_raw(T* p, const Raw<T, V>& r) {
+  if constexpr (V == 1)
+    *p = r.v[0];
+  else
+    *reinterpret_cast<std::remove_const_t<decltype(r.v)>*>(p) = r.v;
 }
 
 __device__ __forceinline__ float2 unpack2(uint32_t b) {

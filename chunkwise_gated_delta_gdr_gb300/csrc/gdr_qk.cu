@@ -92,9 +92,13 @@ __global__ void __launch_bounds__(GW * 32) qk_any_kernel(QkArgs a) {
                    : kind == 1 ? static_cast<const I*>(a.k) + b * a.kb + t * a.kt + h * a.kh
                                : static_cast<const I*>(a.v) + b * a.vb + t * a.vt + h * a.vh;
     if (MODE == kAppend && kind == 2) {
-      if (!bad)
-        for (int i = lane; i < a.D; i += 32)
-          store_cache(a.vc, at + i, static_cast<float>(src[i]), a.cache_bf16);
+      if (!bad)                                  // values as they are
+        for (int i = lane; i < a.D; i += 32) {
+          if (a.cache_bf16 == (sizeof(I) == 2))
+            static_cast<I*>(a.vc)[at + i] = src[i];
+          else
+            store_cache(a.vc, at + i, static_cast<float>(src[i]), a.cache_bf16);
+        }
       continue;
     }
     const float* w = kind == 0 ? a.wq : a.wk;
@@ -322,7 +326,7 @@ __global__ void __launch_bounds__(VT, resident(MODE)) qk_vec_kernel(QkArgs a, Ve
       const bool keep = on && !(MODE == kAppend && n > 0 && bad);
       // c and s of the lane's pairs, laid out like them; sg turns forward.
       float2 c[4], sg[4];
-      if (turned && !bad && !value) {
+      if (turned && !bad) {
         const float4 cv = *reinterpret_cast<const float4*>(a.cos + pos * half + 4 * lane);
         const float4 sv = *reinterpret_cast<const float4*>(a.sin + pos * half + 4 * lane);
         if (kNeighbours) {
@@ -355,7 +359,35 @@ __global__ void __launch_bounds__(VT, resident(MODE)) qk_vec_kernel(QkArgs a, Ve
 #pragma unroll 1
       for (int r = 0, i = 0; r < rows; r += K, ++i) {
         ptx::cp_async_wait<DEPTH - 1>();
-        {
+        if (value) {                             // as they are, their type's rounding apart
+          Raw<I, 4> x[K][2];
+#pragma unroll
+          for (int k = 0; k < K; ++k) {
+            const int slot = (i % DEPTH) * K + k;
+            x[k][0] = load_raw<I, 4>(xs + slot * XROW);
+            x[k][1] = load_raw<I, 4>(xs + slot * XROW + XROW / 2);
+          }
+          fetch(i + DEPTH);
+#pragma unroll
+          for (int k = 0; k < K; ++k, to += step) {
+            if (!keep || r + k >= rows) continue;
+            if (to_bf16 == (sizeof(I) == 2)) {
+              store_raw(reinterpret_cast<I*>(to), x[k][0]);
+              store_raw(reinterpret_cast<I*>(to) + run, x[k][1]);
+            } else {
+              float2 y[4];
+              to_pairs(x[k][0], y);
+              to_pairs(x[k][1], y + 2);
+              if (to_bf16) {
+                store_pairs(reinterpret_cast<bf16*>(to), y);
+                store_pairs(reinterpret_cast<bf16*>(to) + run, y + 2);
+              } else {
+                store_pairs(reinterpret_cast<float*>(to), y);
+                store_pairs(reinterpret_cast<float*>(to) + run, y + 2);
+              }
+            }
+          }
+        } else {
           float2 x[K][4], d[K][4];
           float ss[K], dot[K];
 #pragma unroll
@@ -386,20 +418,18 @@ __global__ void __launch_bounds__(VT, resident(MODE)) qk_vec_kernel(QkArgs a, Ve
             }
           }
           fetch(i + DEPTH);
-          if (!value) {
 #pragma unroll
-            for (int o = GL / 2; o > 0; o >>= 1) {
+          for (int o = GL / 2; o > 0; o >>= 1) {
 #pragma unroll
-              for (int k = 0; k < K; ++k) {
-                ss[k] += __shfl_xor_sync(mask, ss[k], o);
-                if constexpr (bwd) dot[k] += __shfl_xor_sync(mask, dot[k], o);
-              }
+            for (int k = 0; k < K; ++k) {
+              ss[k] += __shfl_xor_sync(mask, ss[k], o);
+              if constexpr (bwd) dot[k] += __shfl_xor_sync(mask, dot[k], o);
             }
           }
 #pragma unroll
           for (int k = 0; k < K; ++k) {
             // A bad position makes the whole row NaN (and stores nothing into the caches).
-            const float rs = bad ? NAN : value ? 1.f : rsqrtf(fmaf(ss[k], inv, a.eps));
+            const float rs = bad ? NAN : rsqrtf(fmaf(ss[k], inv, a.eps));
             const float2 rs2 = make_float2(rs, rs);
             float2 y[4];
             if constexpr (bwd) {

@@ -483,7 +483,8 @@ typedef struct {
 
 /*
  * gdr_qk_norm_rope_append -- gdr_qk_norm_rope for serving: the normed and
- * rotated keys and the values (unchanged) go straight into their pages.
+ * rotated keys and the values (bit for bit, or rounded to the caches' dtype) go
+ * straight into their pages.
  *
  * q, k, v and the norm's arguments as above (v [B, T, HK, D] in_dtype). Token t
  * of sequence b is stored at index positions[b][t] of its sequence: page

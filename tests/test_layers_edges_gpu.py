@@ -7,7 +7,8 @@ import pytest
 import torch
 
 import chunkwise_gated_delta_gdr_gb300 as gdr
-from test_layers_gpu import BF, DEV, EDGE, F32, attn_ref, check, gen_of, make_cache, make_pages, rnd
+from test_layers_gpu import (BF, DEV, EDGE, F32, attn_ref, check, gen_of, make_cache, make_pages,
+                             qk_inputs, rnd, tables)
 
 pytestmark = pytest.mark.gpu
 
@@ -54,3 +55,38 @@ def test_attn_infinite_values(dt, D, out, n):
     assert torch.equal(lse, lse2)
     assert torch.equal(torch.isnan(o), torch.isnan(want))
     assert torch.equal(o.nan_to_num(1.5), want.nan_to_num(1.5))
+
+
+# ------------------------------------------------------------------ values on their way to the cache
+def bits(t):
+    return t.contiguous().view(torch.int16 if t.dtype == BF else torch.int32)
+
+
+@pytest.mark.parametrize("dt,cdt", [(BF, BF), (F32, F32), (BF, F32), (F32, BF)])
+@pytest.mark.parametrize("odd", [False, True])
+@pytest.mark.parametrize("D,R", [(128, 128), (128, 64), (64, 0), (256, 256), (80, 40)])
+@pytest.mark.parametrize("T", [1, 9])
+def test_append_stores_values_unchanged(T, D, R, odd, dt, cdt):
+    """Infinities, NaN and -0 in turned and unturned channels of v: bit for bit where the types
+    agree (else v.to of the cache's type), by the kernel for aligned rows and the other."""
+    B, HQ, HK, page = 3, 4, 2, 16
+    q, k, v, wq, wk, cos, sin, _ = qk_inputs(B, T, HQ, HK, D, R, dt, 72, odd)
+    cos, sin = tables(60, R) if R else (None, None)
+    v = v.clone() if not odd else v          # the rows of `odd` start off every alignment
+    for h in range(HK):
+        for ch, x in ((0, math.inf), (1, -0.0), (D // 2 - 1, math.nan), (D // 2 + 3, -math.inf),
+                      (D - 1, math.nan), (D - 2, math.inf), (D // 4, -0.0)):
+            v[:, h % T, h, ch] = x
+    table, total = make_pages(torch.full((B,), 40), page, gen_of(73))
+    kc, vc = make_cache(gen_of(74), total, page, HK, D, cdt)
+    pos = (torch.tensor([[0], [13], [30]]) + torch.arange(T)).int().to(DEV)
+    table = table.to(DEV)
+    gdr.qk_norm_rope_append(q, k, v, wq, wk, cos, sin, pos, kc, vc, table)
+    got = vc[torch.gather(table.long(), 1, pos.long() // page), pos.long() % page]
+    want = v.to(cdt)
+    if dt == cdt:
+        assert torch.equal(bits(got), bits(want))
+    else:
+        nan = torch.isnan(want)
+        assert torch.equal(nan, torch.isnan(got))
+        assert torch.equal(bits(got)[~nan], bits(want)[~nan])
