@@ -158,6 +158,13 @@ def _dense(name, t, shape, device, dtype=F32):
     raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
 
 
+def _scratch(t, device):
+    """Address and bytes of a caller's workspace: a contiguous CUDA tensor on `device`."""
+    if t.device != device or not t.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
 def _stream(device, stream):
     """Raw handle of `stream` (default: torch's current stream of `device`)."""
     if device.type != "cuda" or device.index != torch._C._cuda_getDevice():
@@ -380,7 +387,7 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, cos=Non
     if dk is None:
         dk = _empty((B, T, HK, D), q.dtype, device, stream)
     dims = _qk_dims(q, k, None, cos, sin, positions, eps, interleaved, _code("dq_out", dq_out))
-    dwq = dwk = None
+    dwq = dwk = ws = None
     ws_bytes = 0
     lib = _lib()
     if output_weight_grads:
@@ -389,7 +396,7 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, cos=Non
         if workspace is None:
             size = lib.gdr_qk_norm_rope_bwd_workspace_size(dims)
             workspace = _empty((max(size, 256),), torch.uint8, device, stream)
-        ws_bytes = workspace.numel()
+        ws, ws_bytes = _scratch(workspace, device)
     st = lib.gdr_qk_norm_rope_bwd(
         _dense("dq_out", dq_out, (B, T, HQ, D), device, dq_out.dtype),
         _dense("dk_out", dk_out, (B, T, HK, D), device, dq_out.dtype), q.data_ptr(), k.data_ptr(),
@@ -397,7 +404,7 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, cos=Non
         _dense("dq", dq, (B, T, HQ, D), device, q.dtype),
         _dense("dk", dk, (B, T, HK, D), device, q.dtype),
         None if dwq is None else dwq.data_ptr(), None if dwk is None else dwk.data_ptr(), dims,
-        None if workspace is None else workspace.data_ptr(), ws_bytes, raw)
+        ws, ws_bytes, raw)
     _raise(st, "gdr_qk_norm_rope_bwd")
     return dq, dk, dwq, dwk
 
@@ -507,10 +514,11 @@ def paged_decode_attn(q, k_cache, v_cache, page_table, lens, *, scale: Optional[
     if workspace is None:
         size = lib.gdr_paged_decode_attn_workspace_size(dims, cache)
         workspace = _empty((max(size, 256),), torch.uint8, device, stream)
+    ws, ws_bytes = _scratch(workspace, device)
     st = lib.gdr_paged_decode_attn(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(),
         _dense("lens", lens, shape[:1], device, torch.int32),
         _dense("out", out, shape, device, out.dtype), _dense("lse", lse, shape[:2], device), dims,
-        cache, workspace.data_ptr(), workspace.numel(), raw)
+        cache, ws, ws_bytes, raw)
     _raise(st, "gdr_paged_decode_attn")
     return out, lse
