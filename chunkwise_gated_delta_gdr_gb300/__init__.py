@@ -394,8 +394,9 @@ def chunk_fwd_host(q, k, v, g, beta, initial_state=None, *, out, final_state=Non
 
 def set_flag_wait_limit(polls: int) -> int:
     """gdr_set_flag_wait_limit: bound (polls, about 64 ns apart) of the
-    one-launch forward's waits on chunk flags for later calls; polls < 0 leaves
-    it unchanged. Returns the previous bound."""
+    one-launch forward's waits on chunk flags, and of the linear recurrence's
+    waits, for later calls; polls < 0 leaves it unchanged. Returns the previous
+    bound."""
     return int(load_library().gdr_set_flag_wait_limit(int(polls)))
 
 

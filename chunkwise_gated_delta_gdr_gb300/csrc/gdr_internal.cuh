@@ -56,8 +56,8 @@ gdr_status launch_tc(const Problem& p, void* ws_body, unsigned int* error_word,
 // Whether gdr_chunk_fwd takes the one-launch form of the fast path (scalar
 // gate) for this problem on the current device.
 bool tc_one_launch(const Problem& p);
-// Bound (polls) of the one-launch forward's waits on chunk flags, for calls
-// enqueued from now on (polls < 0: unchanged); returns the previous bound.
+// Bound (polls) of the one-launch forward's waits on chunk flags and of the
+// linear recurrence's waits, for calls enqueued from now on (polls < 0: unchanged); returns the previous bound.
 long long set_wait_limit(long long polls);
 
 // Segmented scan helpers (gdr_segment.cu): n identity K x K states; the serial

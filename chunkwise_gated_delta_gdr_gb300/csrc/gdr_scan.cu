@@ -33,6 +33,7 @@ struct ScanArgs {
   float* ck;           // checkpoints; may be null in the forward
   int B, T, D, N;      // N = ceil(T / CK)
   int gated;
+  long polls;          // bound of a wait (gdr_set_flag_wait_limit)
   int64_t xb, xt, gb, gt, db, dt;   // strides in elements
 };
 
@@ -83,7 +84,6 @@ __global__ void __launch_bounds__(128) scan_serial_kernel(ScanArgs a) {
 // warps and fewer rows each it took longer (16 warps of 8 rows: 1.54 instead of 1.15 us
 // without the exchange).
 constexpr int W = 8, MAXS = 8;
-constexpr long kWaitLimit = 1L << 24;
 
 // Tokens per warp: as many as leave two blocks on an SM, registers and shared memory both.
 template <typename X, typename G, int V>
@@ -115,15 +115,16 @@ __device__ __forceinline__ void copy_v(float* p, const float* v) {
   for (int i = 0; i < V; ++i) p[i] = v[i];
 }
 
-// A wait that gave up makes every later result of the block NaN.
-__device__ __forceinline__ void wait_or_poison(uint64_t* bar, uint32_t parity, float* carry, int V) {
-  if (!ptx::mbar_wait(bar, parity, kWaitLimit))
-    for (int i = 0; i < V; ++i) carry[i] = NAN;
-}
+// Waits are bounded. Each thread holds `lost`, 0 until one of its waits gives up (then one more
+// than the number of tiles it has seen arrive). It then waits for nothing more, its channels'
+// rows are NaN from that tile on, and so are the pairs formed with its own: no wrong state goes
+// on as a finite number. It sends nothing more either, since pairs of two steps would be
+// counted as one, so that blocks that wait for it give up as well. Thread 0 starts no copies
+// then; see leave() for those under way.
 
 // Bounded wait for the pairs of a step, acquiring what other blocks of the cluster sent.
-__device__ __forceinline__ bool met_wait(uint64_t* bar, uint32_t parity) {
-  for (long i = 0; i < kWaitLimit; ++i) {
+__device__ __forceinline__ bool met_wait(uint64_t* bar, uint32_t parity, long polls) {
+  for (long i = 0; i <= polls; ++i) {
     uint32_t ok;
     asm volatile(
         "{\n .reg .pred p;\n"
@@ -141,8 +142,9 @@ __device__ __forceinline__ bool met_wait(uint64_t* bar, uint32_t parity) {
 // the state before this block's tile, carry the state after the step.
 template <int V, bool kBwd>
 __device__ __forceinline__ void cluster_carry(ScanShared<V, kBwd>& sm, int step, int S, int rank,
-                                              int warp, int lane, const float* tA,
-                                              const float* tP, float* carry, float* mine) {
+                                              int warp, int lane, long polls, const float* tA,
+                                              const float* tP, float* carry, float* mine,
+                                              int& lost) {
   if (S == 1) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -152,8 +154,8 @@ __device__ __forceinline__ void cluster_carry(ScanShared<V, kBwd>& sm, int step,
     return;
   }
   const int par = step & 1;
-  if (threadIdx.x == 0) ptx::mbar_expect_tx(&sm.met[par], S * 32 * 2 * V * 4);
-  if (warp < S) {
+  if (threadIdx.x == 0 && !lost) ptx::mbar_expect_tx(&sm.met[par], S * 32 * 2 * V * 4);
+  if (warp < S && !lost) {
     const uint32_t dst = ptx::mapa(ptx::smem_u32(sm.block[par][rank][lane]), warp);
     const uint32_t bar = ptx::mapa(ptx::smem_u32(&sm.met[par]), warp);
     if constexpr (V == 2)
@@ -167,7 +169,8 @@ __device__ __forceinline__ void cluster_carry(ScanShared<V, kBwd>& sm, int step,
               dst), "f"(tA[0]), "f"(tP[0]), "r"(bar)
           : "memory");
   }
-  if (!met_wait(&sm.met[par], (step >> 1) & 1)) {
+  if (!lost && !met_wait(&sm.met[par], (step >> 1) & 1, polls)) lost = step + 2;
+  if (lost) {
 #pragma unroll
     for (int i = 0; i < V; ++i) carry[i] = NAN;
   }
@@ -179,6 +182,25 @@ __device__ __forceinline__ void cluster_carry(ScanShared<V, kBwd>& sm, int step,
 #pragma unroll
     for (int i = 0; i < V; ++i) carry[i] = fmaf(m[i], carry[i], m[V + i]);
   }
+}
+
+// A block's last act. Copies that thread 0 started and did not see arrive (where there(step)) are
+// waited for, again with a bound. No block leaves while another may send to it; pairs sent
+// before that barrier that a block has not seen arrive need a microsecond more: it stays a
+// thousand.
+constexpr long kDrainPolls = 1L << 24;
+template <int ST, typename F>
+__device__ __forceinline__ void leave(uint64_t* full, int lost, int S, F there) {
+  if constexpr (ST > 0) {
+    if (lost && threadIdx.x == 0)
+      for (int j = lost - 1; j < lost - 1 + ST; ++j)
+        if (there(j)) (void)ptx::mbar_wait(&full[j % ST], (j / ST) & 1, kDrainPolls);
+  }
+  if (S == 1) return;
+  __syncwarp();
+  ptx::cluster_sync();
+  if (lost)
+    for (int i = 0; i < 1000; ++i) __nanosleep(1000);
 }
 
 // One tensor's tiles on their way into a ring in shared memory, token-major. kTensor: a
@@ -245,12 +267,13 @@ __global__ void __launch_bounds__(W * 32, 2)
 #pragma unroll
   for (int i = 0; i < V; ++i) carry[i] = on && a.s0 ? a.s0[(size_t)b * a.D + d + i] : 0.f;
 
+  int lost = 0;
   Feed<X, V, R, kTensor> xf(ring, warp, lane);
   Feed<G, V, R, kTensor> gf(ring + F::XB, warp, lane);
   // Tile `n` into `stage`: all threads (their own tokens), or thread 0 (the whole tile).
   auto load = [&](int stage, int n) {
     if constexpr (kTensor) {
-      if (threadIdx.x == 0 && n * TILE < a.T) {
+      if (threadIdx.x == 0 && !lost && n * TILE < a.T) {
         ptx::mbar_expect_tx(&sm.full[stage], SB);
         const uint32_t dst = ptx::smem_u32(ring + stage * SB);
         ptx::tma_load3(dst, &maps.x, col * 32 * V, n * TILE, b, &sm.full[stage]);
@@ -292,7 +315,8 @@ __global__ void __launch_bounds__(W * 32, 2)
     const int rows = min(R, a.T - t0);           // of this warp; may be negative
     float e[R][V], u[R][V], A[V], P[V];
     if constexpr (kTensor) {
-      if (n * TILE < a.T) wait_or_poison(&sm.full[stage], (step / ST) & 1, carry, V);
+      if (n * TILE < a.T && !lost && !ptx::mbar_wait(&sm.full[stage], (step / ST) & 1, a.polls))
+        lost = step + 1;
     } else {
       ptx::cp_async_wait<ST - 1>();
     }
@@ -313,6 +337,10 @@ __global__ void __launch_bounds__(W * 32, 2)
         P[i] = fmaf(e[r][i], P[i], u[r][i]);
         A[i] *= e[r][i];
       }
+    }
+    if (lost) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) P[i] = u[0][i] = NAN;
     }
     if constexpr (!kTensor) load(stage, n + ST * S);
     float w[2 * V];
@@ -337,7 +365,7 @@ __global__ void __launch_bounds__(W * 32, 2)
         tA[i] *= w[i];
       }
     }
-    cluster_carry<V, false>(sm, step, S, rank, warp, lane, tA, tP, carry, s);
+    cluster_carry<V, false>(sm, step, S, rank, warp, lane, a.polls, tA, tP, carry, s, lost);
 #pragma unroll
     for (int i = 0; i < V; ++i) s[i] = fmaf(pA[i], s[i], pP[i]);
     if (a.ck && warp * R % CK == 0 && on && rows > 0)
@@ -353,7 +381,8 @@ __global__ void __launch_bounds__(W * 32, 2)
     }
   }
   if (a.sT && rank == 0 && warp == 0 && on) put_v<V>(a.sT + (size_t)b * a.D + d, carry);
-  if (S > 1) ptx::cluster_sync();                // no block leaves while another may send to it
+  leave<kTensor ? ST : 0>(sm.full, lost, S,
+                          [&](int j) { return (long long)(rank + j * S) * TILE < a.T; });
 }
 
 // The same walk from the last tile back. What travels is mu_t = a_t l_t, the gradient that
@@ -386,12 +415,13 @@ __global__ void __launch_bounds__(W * 32, 2)
 #pragma unroll
   for (int i = 0; i < V; ++i) carry[i] = on && a.s0 ? a.s0[(size_t)b * a.D + d + i] : 0.f;
 
+  int lost = 0;
   Feed<X, V, R, kTensor> xf(ring, warp, lane);
   Feed<G, V, R, kTensor> gf(ring + F::XB, warp, lane);
   Feed<H, V, R, kTensor> df(ring + F::XB + F::GB, warp, lane);
   auto load = [&](int stage, int n) {
     if constexpr (kTensor) {
-      if (threadIdx.x == 0 && n >= 0) {
+      if (threadIdx.x == 0 && !lost && n >= 0) {
         ptx::mbar_expect_tx(&sm.full[stage], SB);
         const uint32_t dst = ptx::smem_u32(ring + stage * SB);
         ptx::tma_load3(dst, &maps.x, col * 32 * V, n * TILE, b, &sm.full[stage]);
@@ -440,7 +470,8 @@ __global__ void __launch_bounds__(W * 32, 2)
     const int rows = n < 0 ? 0 : min(R, a.T - t0);
     float e[R][V], u[R][V], l[R][V], hs[V], A[V], P[V], M[V];
     if constexpr (kTensor) {
-      if (n >= 0) wait_or_poison(&sm.full[stage], (step / ST) & 1, carry, V);
+      if (n >= 0 && !lost && !ptx::mbar_wait(&sm.full[stage], (step / ST) & 1, a.polls))
+        lost = step + 1;
     } else {
       ptx::cp_async_wait<ST - 1>();
     }
@@ -469,6 +500,10 @@ __global__ void __launch_bounds__(W * 32, 2)
     for (int r = R - 1; r >= 0; --r)
 #pragma unroll
       for (int i = 0; i < V; ++i) M[i] = e[r][i] * (l[r][i] + M[i]);
+    if (lost) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) P[i] = M[i] = l[R - 1][i] = NAN;
+    }
     float w[2 * V];
     copy_v<V>(w, A);
     copy_v<V>(w + V, P);
@@ -501,7 +536,7 @@ __global__ void __launch_bounds__(W * 32, 2)
 #pragma unroll
         for (int i = 0; i < V; ++i) hs[i] = fmaf(w[i], hs[i], w[V + i]);
       }
-    cluster_carry<V, true>(sm, step, S, rank, warp, lane, tA, tM, carry, mu);
+    cluster_carry<V, true>(sm, step, S, rank, warp, lane, a.polls, tA, tM, carry, mu, lost);
 #pragma unroll
     for (int i = 0; i < V; ++i) mu[i] = fmaf(pA[i], mu[i], pM[i]);
     // u becomes what dg multiplies: h_{t-1}, minus x_t when gated.
@@ -531,7 +566,7 @@ __global__ void __launch_bounds__(W * 32, 2)
     }
   }
   if (a.sT && rank == 0 && warp == 0 && on) put_v<V>(a.sT + (size_t)b * a.D + d, carry);
-  if (S > 1) ptx::cluster_sync();                // no block leaves while another may send to it
+  leave<kTensor ? ST : 0>(sm.full, lost, S, [&](int j) { return a.N - 1 - rank - j * S >= 0; });
 }
 
 gdr_status check(const gdr_scan_dims* d) {
@@ -552,6 +587,7 @@ ScanArgs make_args(const gdr_scan_dims* d) {
   a.B = d->B; a.T = d->T; a.D = d->D;
   a.N = (int)(((int64_t)d->T + CK - 1) / CK);
   a.gated = d->gated_input != 0;
+  a.polls = (long)set_wait_limit(-1);
   a.xb = d->x_stride_b; a.xt = d->x_stride_t;
   a.gb = d->g_stride_b; a.gt = d->g_stride_t;
   a.db = d->dh_stride_b; a.dt = d->dh_stride_t;

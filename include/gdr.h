@@ -191,7 +191,8 @@ gdr_status gdr_stream_status(gdr_stream_t stream, void* workspace);
  * (gdr_stream_status reports it) and runs to its end on whatever the
  * workspace holds: the call then finishes with wrong outputs instead of
  * hanging. The default, 2^24 polls (about a second), is far beyond any real
- * wait.
+ * wait. The waits of gdr_linear_scan_fwd and _bwd have the same bound; there a
+ * wait that gave up turns results into NaN.
  *
  *   polls   >= 0: the new bound, for calls enqueued from now on (all devices,
  *           all threads); < 0: leave the bound as it is.
@@ -360,8 +361,10 @@ size_t gdr_chunk_fwd_segmented_workspace_size(const gdr_dims* dims, int chunk_si
  *
  * T = 1 is the decode step (initial_state and final_state the same buffer).
  * T == 0 writes final_state = initial_state (or zeros) and nothing else.
- * B <= 65535. No workspace; waits between the blocks of a cluster are bounded, and one that
- * gave up (a second or so) makes the block's results NaN.
+ * B <= 65535. No workspace. Waits for copies and between the blocks of a cluster are bounded
+ * (gdr_set_flag_wait_limit). Where one gives up, its channels' rows from that tile on are NaN,
+ * and so is every later state that the missing tokens would have reached, in all outputs: what
+ * is finite is right.
  */
 #define GDR_SCAN_CHECKPOINT 64
 

@@ -8,7 +8,7 @@ import torch
 
 import chunkwise_gated_delta_gdr_gb300 as gdr
 from test_layers_gpu import (BF, DEV, EDGE, F32, attn_ref, check, gen_of, make_cache, make_pages,
-                             qk_inputs, rnd, tables)
+                             qk_inputs, rnd, scan_inputs, tables)
 
 pytestmark = pytest.mark.gpu
 
@@ -90,3 +90,39 @@ def test_append_stores_values_unchanged(T, D, R, odd, dt, cdt):
         nan = torch.isnan(want)
         assert torch.equal(nan, torch.isnan(got))
         assert torch.equal(bits(got)[~nan], bits(want)[~nan])
+
+
+# ------------------------------------------------------------------ waits of the scan that give up
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("B,T,D", [(1, 5000, 512), (3, 700, 1024), (1, 3000, 66), (2, 900, 33)])
+def test_scan_waits_that_give_up(B, T, D, dt):
+    """With few polls allowed, waits for tiles and for other blocks give up: every result is NaN
+    or has its right bits, the launch ends by itself, and calls with the usual bound are as ever."""
+    x, g, h0, dh, dfinal = scan_inputs(B, T, D, dt, F32, 75)
+    ck = gdr.linear_scan_checkpoints(x)
+
+    def calls():
+        outs = [torch.full_like(x, 7), torch.full_like(h0, 7), torch.full_like(ck, 7),
+                torch.full_like(x, 7), torch.full_like(g, 7), torch.full_like(h0, 7)]
+        gdr.linear_scan_fwd(x, g, h0, gated_input=True, out=outs[0], final_state=outs[1],
+                            checkpoints=outs[2])
+        gdr.linear_scan_bwd(dh, x, g, ck, dfinal, gated_input=True, dx=outs[3], dg=outs[4],
+                            d_initial_state=outs[5])
+        torch.cuda.synchronize()
+        return outs
+
+    gdr.linear_scan_fwd(x, g, h0, gated_input=True, checkpoints=ck)
+    want = calls()
+    old = gdr.set_flag_wait_limit(-1)
+    for polls in (0, 0, 1, 2, 8, 64):
+        gdr.set_flag_wait_limit(polls)
+        try:
+            got = calls()
+        finally:
+            gdr.set_flag_wait_limit(old)
+        for a, b in zip(got, want):
+            there = ~torch.isnan(a)
+            assert torch.equal(a[there], b[there]), polls
+        if polls == 0 and D * x.element_size() % 16 == 0:    # a tile needs a microsecond
+            assert torch.isnan(got[0]).any() and torch.isnan(got[3]).any()
+    assert all(torch.equal(a, b) for a, b in zip(calls(), want))
