@@ -5,8 +5,9 @@
 // reading a tensor's attributes one by one from Python costs more than that. Each function
 // here takes the arguments of its namesake in layers.py (without `stream`: torch's current
 // one), checks everything the namesake checks, allocates the results that were not passed
-// and makes the call. Where anything is out of the ordinary (a wrong argument, a status other
-// than GDR_OK) it returns None, and layers.py goes its own way, with its messages.
+// and makes the call. Where anything is out of the ordinary before that call (a wrong argument,
+// an allocation that fails) it returns None, and layers.py goes its own way, with its messages.
+// Once the call is made it is not made again: a status other than GDR_OK is returned, an int.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
@@ -136,14 +137,24 @@ PyObject* tuple_of(P*... items) {
   return t;
 }
 
+PyObject* none() {                               // layers.py takes over
+  if (PyErr_Occurred()) PyErr_Clear();
+  Py_RETURN_NONE;
+}
+// What a call answers: its results, made before the call was, or its status.
+PyObject* answer(PyObject* results, gdr_status status) {
+  if (status == GDR_OK) return results;
+  Py_XDECREF(results);
+  return PyLong_FromLong(status);
+}
+
 // C++ exceptions (of an allocation) become None: layers.py then meets the same one itself.
 template <typename F>
 PyObject* guarded(F f) {
   try {
     return f();
   } catch (...) {
-    if (PyErr_Occurred()) PyErr_Clear();
-    Py_RETURN_NONE;
+    return none();
   }
 }
 
@@ -176,11 +187,13 @@ PyObject* linear_scan_fwd(PyObject*, PyObject* const* arg, Py_ssize_t n) {
     Tensor made_out, made_fin;
     if (!out) out = &(made_out = c.empty({B, T, D}, x->scalar_type()));
     if (!fin && want) fin = &(made_fin = c.empty({B, D}, at::kFloat));
-    if (gdr_linear_scan_fwd(x->data_ptr(), g->data_ptr(), static_cast<const float*>(ps0),
-                            out->data_ptr(), fin ? fin->data_ptr<float>() : nullptr,
-                            static_cast<float*>(pck), &d, c.stream()) != GDR_OK)
-      Py_RETURN_NONE;
-    return tuple_of(result(arg[5], made_out), result(arg[6], made_fin));
+    PyObject* results = tuple_of(result(arg[5], made_out), result(arg[6], made_fin));
+    if (!results) return none();
+    return answer(results,
+                  gdr_linear_scan_fwd(x->data_ptr(), g->data_ptr(),
+                                      static_cast<const float*>(ps0), out->data_ptr(),
+                                      fin ? fin->data_ptr<float>() : nullptr,
+                                      static_cast<float*>(pck), &d, c.stream()));
   });
 }
 
@@ -216,12 +229,15 @@ PyObject* linear_scan_bwd(PyObject*, PyObject* const* arg, Py_ssize_t n) {
     if (!dx) dx = &(made_dx = c.empty({B, T, D}, x->scalar_type()));
     if (!dg) dg = &(made_dg = c.empty({B, T, D}, g->scalar_type()));
     if (!d0 && want) d0 = &(made_d0 = c.empty({B, D}, at::kFloat));
-    if (gdr_linear_scan_bwd(dh->data_ptr(), x->data_ptr(), g->data_ptr(),
-                            static_cast<const float*>(pck), static_cast<const float*>(pdf),
-                            dx->data_ptr(), dg->data_ptr(),
-                            d0 ? d0->data_ptr<float>() : nullptr, &d, c.stream()) != GDR_OK)
-      Py_RETURN_NONE;
-    return tuple_of(result(arg[7], made_dx), result(arg[8], made_dg), result(arg[9], made_d0));
+    PyObject* results =
+        tuple_of(result(arg[7], made_dx), result(arg[8], made_dg), result(arg[9], made_d0));
+    if (!results) return none();
+    return answer(results,
+                  gdr_linear_scan_bwd(dh->data_ptr(), x->data_ptr(), g->data_ptr(),
+                                      static_cast<const float*>(pck),
+                                      static_cast<const float*>(pdf), dx->data_ptr(),
+                                      dg->data_ptr(), d0 ? d0->data_ptr<float>() : nullptr, &d,
+                                      c.stream()));
   });
 }
 
@@ -291,10 +307,11 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* arg, Py_ssize_t n) {
     Tensor made_q, made_k;
     if (!qo) qo = &(made_q = c.empty({a.B, a.T, a.HQ, a.D}, type));
     if (!ko) ko = &(made_k = c.empty({a.B, a.T, a.HK, a.D}, type));
-    if (gdr_qk_norm_rope(a.q->data_ptr(), a.k->data_ptr(), a.wq, a.wk, a.cos, a.sin, a.pos,
-                         qo->data_ptr(), ko->data_ptr(), &a.d, c.stream()) != GDR_OK)
-      Py_RETURN_NONE;
-    return tuple_of(result(arg[9], made_q), result(arg[10], made_k));
+    PyObject* results = tuple_of(result(arg[9], made_q), result(arg[10], made_k));
+    if (!results) return none();
+    return answer(results,
+                  gdr_qk_norm_rope(a.q->data_ptr(), a.k->data_ptr(), a.wq, a.wk, a.cos, a.sin,
+                                   a.pos, qo->data_ptr(), ko->data_ptr(), &a.d, c.stream()));
   });
 }
 
@@ -330,15 +347,17 @@ PyObject* qk_norm_rope_bwd(PyObject*, PyObject* const* arg, Py_ssize_t n) {
         ws = &(made_ws = c.empty({(int64_t)size}, at::kByte));
       }
     }
-    if (gdr_qk_norm_rope_bwd(dqo->data_ptr(), dko->data_ptr(), a.q->data_ptr(), a.k->data_ptr(),
-                             a.wq, a.wk, a.cos, a.sin, a.pos, dq->data_ptr(), dk->data_ptr(),
-                             weights ? made_wq.data_ptr<float>() : nullptr,
-                             weights ? made_wk.data_ptr<float>() : nullptr, &a.d,
-                             ws ? ws->data_ptr() : nullptr, ws ? ws->numel() : 0,
-                             c.stream()) != GDR_OK)
-      Py_RETURN_NONE;
-    return tuple_of(result(arg[11], made_dq), result(arg[12], made_dk), result(Py_None, made_wq),
-                    result(Py_None, made_wk));
+    PyObject* results = tuple_of(result(arg[11], made_dq), result(arg[12], made_dk),
+                                 result(Py_None, made_wq), result(Py_None, made_wk));
+    if (!results) return none();
+    return answer(results,
+                  gdr_qk_norm_rope_bwd(dqo->data_ptr(), dko->data_ptr(), a.q->data_ptr(),
+                                       a.k->data_ptr(), a.wq, a.wk, a.cos, a.sin, a.pos,
+                                       dq->data_ptr(), dk->data_ptr(),
+                                       weights ? made_wq.data_ptr<float>() : nullptr,
+                                       weights ? made_wk.data_ptr<float>() : nullptr, &a.d,
+                                       ws ? ws->data_ptr() : nullptr, ws ? ws->numel() : 0,
+                                       c.stream()));
   });
 }
 
@@ -380,11 +399,13 @@ PyObject* qk_norm_rope_append(PyObject*, PyObject* const* arg, Py_ssize_t n) {
     if (!c.ready()) Py_RETURN_NONE;
     Tensor made;
     if (!qo) qo = &(made = c.empty({a.B, a.T, a.HQ, a.D}, type));
-    if (gdr_qk_norm_rope_append(a.q->data_ptr(), a.k->data_ptr(), v->data_ptr(), a.wq, a.wk, a.cos,
-                                a.sin, a.pos, qo->data_ptr(), kc->data_ptr(), vc->data_ptr(),
-                                pt->data_ptr<int32_t>(), &a.d, &p, c.stream()) != GDR_OK)
-      Py_RETURN_NONE;
-    return result(arg[13], made);
+    PyObject* results = result(arg[13], made);
+    if (!results) return none();
+    return answer(results,
+                  gdr_qk_norm_rope_append(a.q->data_ptr(), a.k->data_ptr(), v->data_ptr(), a.wq,
+                                          a.wk, a.cos, a.sin, a.pos, qo->data_ptr(),
+                                          kc->data_ptr(), vc->data_ptr(), pt->data_ptr<int32_t>(),
+                                          &a.d, &p, c.stream()));
   });
 }
 
@@ -422,12 +443,13 @@ PyObject* paged_decode_attn(PyObject*, PyObject* const* arg, Py_ssize_t n) {
       if (!size) Py_RETURN_NONE;
       ws = &(made_ws = c.empty({(int64_t)size}, at::kByte));
     }
-    if (gdr_paged_decode_attn(q->data_ptr(), kc->data_ptr(), vc->data_ptr(),
-                              pt->data_ptr<int32_t>(), lens->data_ptr<int32_t>(), out->data_ptr(),
-                              lse->data_ptr<float>(), &d, &p, ws->data_ptr(), ws->numel(),
-                              c.stream()) != GDR_OK)
-      Py_RETURN_NONE;
-    return tuple_of(result(arg[7], made_out), result(arg[8], made_lse));
+    PyObject* results = tuple_of(result(arg[7], made_out), result(arg[8], made_lse));
+    if (!results) return none();
+    return answer(results,
+                  gdr_paged_decode_attn(q->data_ptr(), kc->data_ptr(), vc->data_ptr(),
+                                        pt->data_ptr<int32_t>(), lens->data_ptr<int32_t>(),
+                                        out->data_ptr(), lse->data_ptr<float>(), &d, &p,
+                                        ws->data_ptr(), ws->numel(), c.stream()));
   });
 }
 

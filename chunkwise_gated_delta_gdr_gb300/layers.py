@@ -85,7 +85,8 @@ def _lib():
 # what they cost on the host counts. csrc/layers_host.cpp makes the same checks and the same
 # C calls in one step for the ordinary case (torch's current stream, results of the default
 # dtype or passed in); it answers None to everything else, and the code below takes over,
-# with its messages. On a GB300's host a call of qk_norm_rope_append takes 13 us through the
+# with its messages. A C call that was made is not made again: its status, if it is not OK, is
+# the answer. On a GB300's host a call of qk_norm_rope_append takes 13 us through the
 # Python code and 2.5 us compiled, the launch included.
 _host = None
 
@@ -217,6 +218,8 @@ def linear_scan_fwd(x, g, initial_state=None, *, gated_input: bool = False,
         r = _host.linear_scan_fwd(x, g, initial_state, gated_input, output_final_state, out,
                                   final_state, checkpoints)
         if r is not None:
+            if type(r) is int:
+                _raise(r, "gdr_linear_scan_fwd")
             return r
     shape, device = x.shape, x.device
     if len(shape) != 3:
@@ -257,6 +260,8 @@ def linear_scan_bwd(dh, x, g, checkpoints, d_final_state=None, *, gated_input: b
         r = _host.linear_scan_bwd(dh, x, g, checkpoints, d_final_state, gated_input,
                                   output_initial_state_grad, dx, dg, d_initial_state)
         if r is not None:
+            if type(r) is int:
+                _raise(r, "gdr_linear_scan_bwd")
             return r
     shape, device = x.shape, x.device
     if len(shape) != 3:
@@ -348,6 +353,8 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positio
         r = _host.qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved,
                                q_out, k_out)
         if r is not None:
+            if type(r) is int:
+                _raise(r, "gdr_qk_norm_rope")
             return r
     B, T, HQ, D = q.shape
     device, HK = q.device, k.shape[2]
@@ -378,6 +385,8 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, cos=Non
         r = _host.qk_norm_rope_bwd(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved,
                                    dq_out, dk_out, dq, dk, output_weight_grads, workspace)
         if r is not None:
+            if type(r) is int:
+                _raise(r, "gdr_qk_norm_rope_bwd")
             return r
     B, T, HQ, D = q.shape
     device, HK = q.device, k.shape[2]
@@ -440,6 +449,8 @@ def qk_norm_rope_append(q, k, v, q_weight, k_weight, cos, sin, positions, k_cach
         r = _host.qk_norm_rope_append(q, k, q_weight, k_weight, cos, sin, positions, eps,
                                       interleaved, v, k_cache, v_cache, page_table, q_out)
         if r is not None:
+            if type(r) is int:
+                _raise(r, "gdr_qk_norm_rope_append")
             return r
     B, T, HQ, D = q.shape
     device = q.device
@@ -500,6 +511,8 @@ def paged_decode_attn(q, k_cache, v_cache, page_table, lens, *, scale: Optional[
         r = _host.paged_decode_attn(q, k_cache, v_cache, page_table, lens, scale, window, out, lse,
                                     workspace)
         if r is not None:
+            if type(r) is int:
+                _raise(r, "gdr_paged_decode_attn")
             return r
     shape, device = q.shape, q.device
     raw = _stream(device, stream)

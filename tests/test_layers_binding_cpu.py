@@ -60,3 +60,47 @@ def test_workspaces_are_checked(layers, recorded):
         call(ws)
         name, args = recorded.calls.pop()
         assert ws.data_ptr() in args and ws.numel() * 4 in args, name
+
+
+# ------------------------------------------------------------------ the compiled calls' answers
+class Compiled:
+    """Stands in for the compiled module: every call answers `value`."""
+
+    def __init__(self, value):
+        self.value, self.count = value, 0
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.count += 1
+            return self.value
+        return call
+
+
+def every_call():
+    x, q = torch.zeros(1, 4, 8), torch.zeros(2, 3, 4, 64)
+    k = torch.zeros(5, 16, 4, 64)
+    pos, table = torch.zeros(2, 3, dtype=torch.int32), torch.zeros(2, 4, dtype=torch.int32)
+    return {"linear_scan_fwd": lambda: gdr.linear_scan_fwd(x, x),
+            "linear_scan_bwd": lambda: gdr.linear_scan_bwd(x, x, x, gdr.linear_scan_checkpoints(x)),
+            "qk_norm_rope": lambda: gdr.qk_norm_rope(q, q),
+            "qk_norm_rope_bwd": lambda: gdr.qk_norm_rope_bwd(q, q, q, q),
+            "qk_norm_rope_append": lambda: gdr.qk_norm_rope_append(
+                q, q, q, None, None, None, None, pos, k, k, table),
+            "paged_decode_attn": lambda: gdr.paged_decode_attn(*attn_args())}
+
+
+@pytest.mark.parametrize("name", list(every_call()))
+def test_a_call_that_was_made_is_not_made_again(layers, recorded, monkeypatch, name):
+    """The compiled call answers a status: an error, and no second call. It answers None:
+    the Python call is made, once."""
+    call = every_call()[name]
+    for status in (gdr.GDR_ERR_CUDA, gdr.GDR_ERR_INVALID_ARG):
+        host = Compiled(status)
+        monkeypatch.setattr(layers, "_host", host)
+        with pytest.raises(gdr.GdrError, match="gdr_" + name) as error:
+            call()
+        assert error.value.status == status
+        assert host.count == 1 and not recorded.calls
+    monkeypatch.setattr(layers, "_host", Compiled(None))
+    call()
+    assert [n for n, _ in recorded.calls if not n.endswith("_size")] == ["gdr_" + name]

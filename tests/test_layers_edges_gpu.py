@@ -126,3 +126,15 @@ def test_scan_waits_that_give_up(B, T, D, dt):
         if polls == 0 and D * x.element_size() % 16 == 0:    # a tile needs a microsecond
             assert torch.isnan(got[0]).any() and torch.isnan(got[3]).any()
     assert all(torch.equal(a, b) for a, b in zip(calls(), want))
+
+
+# ------------------------------------------------------------------ calls and their statuses
+def test_compiled_calls_answer_a_status(monkeypatch):
+    """A refusal of the C ABI comes back from the compiled call, and is not asked for twice."""
+    from chunkwise_gated_delta_gdr_gb300 import layers
+    q, k = torch.zeros(2, 3, 4, 64, device=DEV), torch.zeros(2, 3, 2, 64, device=DEV)
+    assert layers._host.qk_norm_rope(q, k, None, None, None, None, None, 0.0, False, None,
+                                     None) == gdr.GDR_ERR_INVALID_ARG
+    monkeypatch.setattr(layers, "_lib", None)            # the Python call cannot run
+    with pytest.raises(gdr.GdrError, match="gdr_qk_norm_rope"):
+        gdr.qk_norm_rope(q, k, eps=0.0)
