@@ -158,7 +158,23 @@ __device__ __forceinline__ void store_f(T* p, const float* f) {
 inline bool is_aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 inline bool is_dtype(int d) { return d == GDR_F32 || d == GDR_BF16; }
 inline size_t dtype_size(int d) { return d == GDR_BF16 ? 2 : 4; }
-inline gdr_status launched() { return cudaGetLastError() == cudaSuccess ? GDR_OK : GDR_ERR_CUDA; }
+// The status of a runtime call; leaves no error for a later one to report.
+inline gdr_status status_of(cudaError_t e) {
+  if (e == cudaSuccess) return GDR_OK;
+  (void)cudaGetLastError();
+  return GDR_ERR_CUDA;
+}
+
+// A launch; its own status, not the error that an earlier call left behind.
+template <typename Fn, typename... Args>
+gdr_status launch_kernel(Fn fn, dim3 grid, int threads, size_t smem, cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  return status_of(cudaLaunchKernelEx(&cfg, fn, args...));
+}
 
 // Lets `fn` use `bytes` of dynamic shared memory; asked of the runtime once per kernel (Tag
 // names it) and device.
@@ -190,9 +206,7 @@ gdr_status launch_behind(Fn fn, dim3 grid, int threads, cudaStream_t s, Args... 
   cfg.stream = s;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, fn, args...) == cudaSuccess) return GDR_OK;
-  (void)cudaGetLastError();
-  return GDR_ERR_CUDA;
+  return status_of(cudaLaunchKernelEx(&cfg, fn, args...));
 }
 
 // Calls f with a null pointer of the element type that `dtype` names.

@@ -953,8 +953,7 @@ template <class Core>
 gdr_status launch_ring(const AttnArgs& a, cudaStream_t s) {
   constexpr int bytes = Core::NW * Core::ST * Core::SLOT;
   if (!allow_smem<Core>(paged_ring_kernel<Core>, bytes)) return GDR_ERR_CUDA;
-  paged_ring_kernel<Core><<<a.blocks, Core::NW * 32, bytes, s>>>(a);
-  return launched();
+  return launch_kernel(paged_ring_kernel<Core>, dim3(a.blocks), Core::NW * 32, bytes, s, a);
 }
 
 gdr_status check(const gdr_attn_dims* d, const gdr_paged_cache* c) {
@@ -1036,13 +1035,10 @@ gdr_status gdr_paged_decode_attn(const void* q, const void* k_cache, const void*
     const int vec = a.D % 4 == 0 && a.pp % 4 == 0 && a.pt % 4 == 0 && a.ph % 4 == 0;
     run = with_dtype(cache->dtype, [&](auto* t) {
       using T = std::remove_pointer_t<decltype(t)>;
-      if (a.D <= 64)
-        paged_any_kernel<T, 2, 4><<<p.blocks, WARPS * 32, 0, s>>>(a, vec);
-      else if (a.D <= 128)
-        paged_any_kernel<T, 4, 4><<<p.blocks, WARPS * 32, 0, s>>>(a, vec);
-      else
-        paged_any_kernel<T, 8, 2><<<p.blocks, WARPS * 32, 0, s>>>(a, vec);
-      return launched();
+      return launch_kernel(a.D <= 64    ? paged_any_kernel<T, 2, 4>
+                           : a.D <= 128 ? paged_any_kernel<T, 4, 4>
+                                        : paged_any_kernel<T, 8, 2>,
+                           dim3(p.blocks), WARPS * 32, 0, s, a, vec);
     });
   }
   if (run != GDR_OK || p.whole) return run;

@@ -620,13 +620,11 @@ VecPlan vec_plan(const QkArgs& a, int mode) {
 }
 
 template <typename I, typename O, int MODE, bool kNeighbours>
-void launch_vec(const QkArgs& a, const VecPlan& v, int blocks, cudaStream_t s) {
-  if (v.GL == 8)
-    qk_vec_kernel<I, O, MODE, kNeighbours, 8><<<blocks, VT, 0, s>>>(a, v);
-  else if (v.GL == 16)
-    qk_vec_kernel<I, O, MODE, kNeighbours, 16><<<blocks, VT, 0, s>>>(a, v);
-  else
-    qk_vec_kernel<I, O, MODE, kNeighbours, 32><<<blocks, VT, 0, s>>>(a, v);
+gdr_status launch_vec(const QkArgs& a, const VecPlan& v, int blocks, cudaStream_t s) {
+  return launch_kernel(v.GL == 8    ? qk_vec_kernel<I, O, MODE, kNeighbours, 8>
+                       : v.GL == 16 ? qk_vec_kernel<I, O, MODE, kNeighbours, 16>
+                                    : qk_vec_kernel<I, O, MODE, kNeighbours, 32>,
+                       dim3(blocks), VT, 0, s, a, v);
 }
 
 // Launches with at most `most` blocks; returns how many through *blocks.
@@ -644,13 +642,9 @@ gdr_status launch(const gdr_qk_dims* d, const QkArgs& a, const gdr_paged_cache* 
     return with_dtype(d->out_dtype, [&](auto* o) {
       using I = std::remove_pointer_t<decltype(i)>;
       using O = std::remove_pointer_t<decltype(o)>;
-      if (!vec)
-        qk_any_kernel<I, O, MODE><<<*blocks, GW * 32, 0, s>>>(a);
-      else if (a.interleaved)
-        launch_vec<I, O, MODE, true>(a, v, *blocks, s);
-      else
-        launch_vec<I, O, MODE, false>(a, v, *blocks, s);
-      return launched();
+      return !vec ? launch_kernel(qk_any_kernel<I, O, MODE>, dim3(*blocks), GW * 32, 0, s, a)
+             : a.interleaved ? launch_vec<I, O, MODE, true>(a, v, *blocks, s)
+                             : launch_vec<I, O, MODE, false>(a, v, *blocks, s);
     });
   });
 }
@@ -702,9 +696,8 @@ gdr_status gdr_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const vo
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (dims->B == 0 || dims->T == 0) {            // no tokens: the sums are zero
     for (float* w : {dq_weight, dk_weight})
-      if (w && cudaMemsetAsync(w, 0, dims->D * sizeof(float), s) != cudaSuccess)
-        return GDR_ERR_CUDA;
-    return GDR_OK;
+      if (w && st == GDR_OK) st = status_of(cudaMemsetAsync(w, 0, dims->D * sizeof(float), s));
+    return st;
   }
   if (!dq_out || !dk_out || !dq || !dk) return GDR_ERR_INVALID_ARG;
   QkArgs a = make_args(dims, q_weight, k_weight, cos, sin, positions);

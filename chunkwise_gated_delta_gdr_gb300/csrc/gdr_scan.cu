@@ -605,9 +605,8 @@ bool vec_ok(const void* p, int dtype, int64_t sb, int64_t st, int V) {
 // T == 0: out = in (or zeros).
 gdr_status copy_state(float* out, const float* in, size_t n, cudaStream_t s) {
   if (!out || out == in || n == 0) return GDR_OK;
-  const cudaError_t e = in ? cudaMemcpyAsync(out, in, n * 4, cudaMemcpyDeviceToDevice, s)
-                           : cudaMemsetAsync(out, 0, n * 4, s);
-  return e == cudaSuccess ? GDR_OK : GDR_ERR_CUDA;
+  return status_of(in ? cudaMemcpyAsync(out, in, n * 4, cudaMemcpyDeviceToDevice, s)
+                      : cudaMemsetAsync(out, 0, n * 4, s));
 }
 
 constexpr int kSms = 152;
@@ -735,11 +734,7 @@ struct Walk {
     cfg.stream = s;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kernel(), m, a, S) != cudaSuccess) {
-      (void)cudaGetLastError();
-      return GDR_ERR_CUDA;
-    }
-    return GDR_OK;
+    return status_of(cudaLaunchKernelEx(&cfg, kernel(), m, a, S));
   }
 };
 
@@ -777,11 +772,9 @@ gdr_status launch(const gdr_scan_dims* d, const ScanArgs& a, Path path, cudaStre
           if (serial(a)) {
             const int V = path == kPlain ? 1 : 2;
             const dim3 grid((a.D + 128 * V - 1) / (128 * V), a.B);
-            if (V == 1)
-              scan_serial_kernel<X, G, H, 1><<<grid, 128, 0, s>>>(a);
-            else
-              scan_serial_kernel<X, G, H, 2><<<grid, 128, 0, s>>>(a);
-            return launched();
+            return launch_kernel(V == 1 ? scan_serial_kernel<X, G, H, 1>
+                                        : scan_serial_kernel<X, G, H, 2>,
+                                 grid, 128, 0, s, a);
           }
         }
         return path == kTensorMaps ? launch_tensor<X, G, H, kBwd>(d, a, s)

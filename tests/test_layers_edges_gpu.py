@@ -1,6 +1,7 @@
 """The layers' operators where values, sizes and arguments are out of the ordinary, against
 the 64-bit implementations of test_layers_gpu.py; tolerances as derived there, or beside the
 test."""
+import ctypes
 import math
 
 import pytest
@@ -138,3 +139,45 @@ def test_compiled_calls_answer_a_status(monkeypatch):
     monkeypatch.setattr(layers, "_lib", None)            # the Python call cannot run
     with pytest.raises(gdr.GdrError, match="gdr_qk_norm_rope"):
         gdr.qk_norm_rope(q, k, eps=0.0)
+
+
+def leave_an_error():
+    """A host-side error that the library does not clear: its stream status asked for while the
+    stream is being captured, which only ends the capture."""
+    paths = {line.split()[-1] for line in open("/proc/self/maps") if "/libcudart.so" in line}
+    rt = ctypes.CDLL(paths.pop())
+    stream = torch.cuda.Stream()
+    handle, graph = ctypes.c_void_p(stream.cuda_stream), ctypes.c_void_p()
+    assert rt.cudaStreamBeginCapture(handle, 2) == 0                 # relaxed
+    try:
+        assert gdr.stream_status(stream) == gdr.GDR_ERR_CUDA
+    finally:
+        assert rt.cudaStreamEndCapture(handle, ctypes.byref(graph)) != 0
+        rt.cudaGetLastError()
+
+
+@pytest.mark.parametrize("T", [1, 700])
+def test_scan_reports_its_own_status(T):
+    """An error that an earlier call left behind is not this call's, whose state moves once."""
+    x, g, h0, _, _ = scan_inputs(2, T, 64, BF, F32, 76)
+    want, state = gdr.linear_scan_fwd(x, g, h0)[1], h0.clone()
+    leave_an_error()
+    gdr.linear_scan_fwd(x, g, state, final_state=state)
+    assert torch.equal(state, want)
+
+
+@pytest.mark.parametrize("D", [64, 33])
+def test_norm_and_attention_report_their_own_status(D):
+    q, k, v, wq, wk, cos, sin, _ = qk_inputs(2, 1, 4, 2, D, 32, BF, 77)
+    table, total = make_pages(torch.tensor([9, 9]), 16, gen_of(78))
+    kc, vc = make_cache(gen_of(79), total, 16, 2, D, BF)
+    table, lens = table.to(DEV), torch.tensor([9, 9], dtype=torch.int32, device=DEV)
+    pos = (lens - 1)[:, None].contiguous()
+    d = torch.ones_like(q, memory_format=torch.contiguous_format)
+    for call in (lambda: gdr.qk_norm_rope(q, k, wq, wk, cos, sin, pos),
+                 lambda: gdr.qk_norm_rope_bwd(d, d[:, :, :2].contiguous(), q, k, wq, wk, cos, sin,
+                                              pos),
+                 lambda: gdr.qk_norm_rope_append(q, k, v, wq, wk, cos, sin, pos, kc, vc, table),
+                 lambda: gdr.paged_decode_attn(q[:, 0], kc, vc, table, lens)):
+        leave_an_error()
+        call()
