@@ -181,3 +181,41 @@ def test_norm_and_attention_report_their_own_status(D):
                  lambda: gdr.paged_decode_attn(q[:, 0], kc, vc, table, lens)):
         leave_an_error()
         call()
+
+
+# ------------------------------------------------------------------ slow gates
+@pytest.mark.parametrize("dt", [F32, BF])
+@pytest.mark.parametrize("B,T,D", [(2, 1, 64), (1, 20, 66), (1, 300, 64), (3, 260, 33), (40, 31, 514),
+                                   (2, 700, 258)])
+def test_scan_gated_input_of_slow_gates(B, T, D, dt):
+    """Gates of 1e-8 .. 1, of either sign: every state and gradient to its own size. The weight
+    -expm1(g) is within 3e-7 of itself; a step rounds exp(g), products and sums, 2.5e-7 of the
+    state in all, and x and dh are positive, so that nothing cancels."""
+    gen = gen_of(80)
+    x = (rnd(gen, B, T, D).abs() + 0.5).to(dt)
+    dh = (rnd(gen, B, T, D).abs() + 0.5).to(dt)
+    size = 10.0 ** (-8 * torch.rand(D, generator=gen, dtype=torch.float64))
+    sign = torch.where(torch.arange(D) % 5 == 4, 1.0, -1.0)
+    size[sign > 0] *= 1e-3                               # exp of the sum of these stays near 1
+    g = (size * sign).float().to(DEV).expand(B, T, D)
+    ck = gdr.linear_scan_checkpoints(x)
+    h, s = gdr.linear_scan_fwd(x, g, gated_input=True, out_dtype=F32, checkpoints=ck)
+    dx, dg, _ = gdr.linear_scan_bwd(dh, x, g, ck, gated_input=True)
+    a, m = g.double().exp(), -torch.expm1(g.double())
+    state, past, states = torch.zeros(B, D, dtype=torch.float64, device=DEV), [], []
+    for t in range(T):
+        past.append(state)
+        state = a[:, t] * state + m[:, t] * x[:, t].double()
+        states.append(state)
+    l, lx, lg = torch.zeros_like(state), [], []
+    for t in reversed(range(T)):
+        l = l + dh[:, t].double()
+        lx.insert(0, l * m[:, t])
+        lg.insert(0, l * a[:, t] * (past[t].abs() + x[:, t].double()))   # its terms' sizes
+        l = l * a[:, t]
+    tol = 5e-7 + 2.5e-7 * T
+    for got, ref in ((h, torch.stack(states, 1)), (s, state), (dx, torch.stack(lx, 1))):
+        check(got, ref, tol, ref.abs())
+    size = torch.stack(lg, 1)
+    ref = size / (torch.stack(past, 1).abs() + x.double()) * (torch.stack(past, 1) - x.double())
+    check(dg, ref, 2 * tol, size)
