@@ -195,12 +195,12 @@ def _raise(status, where):
 
 
 # ------------------------------------------------------------------ gated linear recurrence
-def linear_scan_checkpoints(x):
+def linear_scan_checkpoints(x, *, stream=None):
     """Buffer [B, ceil(T / 64), D] fp32 for linear_scan_fwd(checkpoints=...), which
-    linear_scan_bwd reads."""
+    linear_scan_bwd reads. ``stream``: the one those calls are given."""
     B, T, D = x.shape
-    return torch.empty(B, (T + SCAN_CHECKPOINT - 1) // SCAN_CHECKPOINT, D, dtype=torch.float32,
-                       device=x.device)
+    return _empty((B, (T + SCAN_CHECKPOINT - 1) // SCAN_CHECKPOINT, D), torch.float32, x.device,
+                  stream)
 
 
 def linear_scan_fwd(x, g, initial_state=None, *, gated_input: bool = False,

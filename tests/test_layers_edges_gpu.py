@@ -219,3 +219,26 @@ def test_scan_gated_input_of_slow_gates(B, T, D, dt):
     size = torch.stack(lg, 1)
     ref = size / (torch.stack(past, 1).abs() + x.double()) * (torch.stack(past, 1) - x.double())
     check(dg, ref, 2 * tol, size)
+
+
+def test_checkpoints_on_another_stream():
+    """Memory that the current stream still reads is not given to checkpoints that another one
+    fills."""
+    x, g, _, dh, _ = scan_inputs(1, 65536, 1024, BF, F32, 81)
+    ck = gdr.linear_scan_checkpoints(x)
+    gdr.linear_scan_fwd(x, g, checkpoints=ck)
+    want = gdr.linear_scan_bwd(dh, x, g, ck)
+    out = torch.empty_like(x)
+    old, copy = torch.full_like(ck, 3), torch.zeros_like(ck)
+    big, side = torch.zeros(1 << 28, device=DEV), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        big.mul_(1.0)
+    copy.copy_(old)
+    del old
+    ck = gdr.linear_scan_checkpoints(x, stream=side)
+    gdr.linear_scan_fwd(x, g, out=out, checkpoints=ck, stream=side)
+    got = gdr.linear_scan_bwd(dh, x, g, ck, stream=side)
+    torch.cuda.synchronize()
+    assert (copy == 3).all()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
