@@ -215,7 +215,8 @@ auto with_dtype(int dtype, F f) {
   return dtype == GDR_BF16 ? f(static_cast<bf16*>(nullptr)) : f(static_cast<float*>(nullptr));
 }
 
-// The sizes of a paged cache. Zero pages or table columns are an empty cache.
+// The sizes of a paged cache. Zero pages or table columns are an empty cache: its arrays may
+// be null, as those of empty tensors are.
 inline gdr_status check_cache(const gdr_paged_cache* c) {
   if (!c) return GDR_ERR_INVALID_ARG;
   if (c->num_pages < 0 || c->page_size <= 0 || c->HK <= 0 || c->D <= 0 || c->max_pages < 0 ||
@@ -223,6 +224,9 @@ inline gdr_status check_cache(const gdr_paged_cache* c) {
     return GDR_ERR_INVALID_ARG;
   if (c->D > 256 || c->HK > (1 << 20)) return GDR_ERR_UNSUPPORTED;
   return GDR_OK;
+}
+inline bool has_arrays(const gdr_paged_cache* c, const void* k, const void* v, const void* table) {
+  return (c->num_pages == 0 || (k && v)) && (c->max_pages == 0 || table);
 }
 
 }  // namespace ops

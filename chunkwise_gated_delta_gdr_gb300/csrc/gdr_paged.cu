@@ -998,7 +998,8 @@ gdr_status gdr_paged_decode_attn(const void* q, const void* k_cache, const void*
       !is_aligned(out, 16) || !is_aligned(lse, 16))
     return GDR_ERR_ALIGNMENT;
   if (dims->B == 0) return GDR_OK;
-  if (!q || !k_cache || !v_cache || !page_table || !lens || !out) return GDR_ERR_INVALID_ARG;
+  if (!q || !lens || !out || !has_arrays(cache, k_cache, v_cache, page_table))
+    return GDR_ERR_INVALID_ARG;
   if (!workspace || workspace_bytes < gdr_paged_decode_attn_workspace_size(dims, cache))
     return GDR_ERR_WORKSPACE;
   if (!is_aligned(workspace, kAlign)) return GDR_ERR_ALIGNMENT;
@@ -1007,7 +1008,10 @@ gdr_status gdr_paged_decode_attn(const void* q, const void* k_cache, const void*
   if (kind == kMma && !is_aligned(q, 4)) kind = kAny;
   const Plan p = make_plan(dims, cache, kind);
   AttnArgs a = {};
-  a.q = q; a.kc = k_cache; a.vc = v_cache; a.table = page_table; a.lens = lens;
+  // Copies of rows that are not there read nothing, from the address of row 0 all the same.
+  a.kc = k_cache ? k_cache : workspace;
+  a.vc = v_cache ? v_cache : workspace;
+  a.q = q; a.table = page_table; a.lens = lens;
   a.out = out; a.lse = lse;
   a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + kAlign);
   a.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + kAlign + p.o_bytes);

@@ -732,7 +732,7 @@ gdr_status gdr_qk_norm_rope_append(const void* q, const void* k, const void* v,
       !is_aligned(k_cache, 16) || !is_aligned(v_cache, 16) || !is_aligned(page_table, 4))
     return GDR_ERR_ALIGNMENT;
   if (dims->B == 0 || dims->T == 0) return GDR_OK;
-  if (!v || !q_out || !k_cache || !v_cache || !page_table) return GDR_ERR_INVALID_ARG;
+  if (!v || !q_out || !has_arrays(cache, k_cache, v_cache, page_table)) return GDR_ERR_INVALID_ARG;
   QkArgs a = make_args(dims, q_weight, k_weight, cos, sin, positions);
   a.q = q; a.k = k; a.v = v; a.qo = q_out; a.kc = k_cache; a.vc = v_cache; a.table = page_table;
   a.num_pages = cache->num_pages; a.page = cache->page_size; a.max_pages = cache->max_pages;

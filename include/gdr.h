@@ -475,7 +475,7 @@ size_t gdr_qk_norm_rope_bwd_workspace_size(const gdr_qk_dims* dims);
  * (page, token, head, channel) is at page page_stride + token token_stride +
  * head head_stride + channel. page_table [B, max_pages] int32 (dense) names the
  * pages of each sequence in order; entries beyond a sequence's length are not
- * read.
+ * read. Zero pages, or zero columns, are an empty cache: its arrays may be NULL.
  */
 typedef struct {
   int num_pages, page_size, HK, D;

@@ -242,3 +242,25 @@ def test_checkpoints_on_another_stream():
     torch.cuda.synchronize()
     assert (copy == 3).all()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+# ------------------------------------------------------------------ empty caches
+@pytest.mark.parametrize("dt,D", [(BF, 128), (F32, 64), (BF, 40)])
+@pytest.mark.parametrize("pages,columns", [(0, 0), (3, 0), (0, 2), (0, 100)])
+def test_empty_cache(pages, columns, dt, D):
+    """No pages, or a table without columns: rows without keys give zeros and -inf, a row that
+    says it has keys gives NaN, an append stores nothing and gives NaN."""
+    kc = torch.full((pages, 16, 2, D), 3.0, dtype=dt, device=DEV)
+    vc = kc.clone()
+    table = torch.zeros(3, columns, dtype=torch.int32, device=DEV)
+    q = rnd(gen_of(82), 3, 4, D, dtype=dt)
+    lens = torch.tensor([0, 5, 0], dtype=torch.int32, device=DEV)
+    o, lse = gdr.paged_decode_attn(q, kc, vc, table, lens)
+    assert not o[[0, 2]].any() and (lse[[0, 2]] == -math.inf).all()
+    assert torch.isnan(o[1]).all() and torch.isnan(lse[1]).all()
+    qkv = rnd(gen_of(83), 3, 1, 8, D, dtype=dt)
+    pos = torch.tensor([[0], [5], [1 << 30]], dtype=torch.int32, device=DEV)
+    qo = gdr.qk_norm_rope_append(qkv[:, :, :4], qkv[:, :, 4:6], qkv[:, :, 6:], None, None, None,
+                                 None, pos, kc, vc, table)
+    assert torch.isnan(qo).all()
+    assert (kc == 3).all() and (vc == 3).all()
