@@ -12,10 +12,12 @@ import ctypes
 import importlib.util
 import math
 import os
+import warnings
 from typing import Optional
 
 import torch
 
+from .build import host_path
 from . import (GDR_BF16, GDR_ERR_INVALID_ARG, GDR_F32, GDR_OK, LIB_PATH, GdrError, load_library)
 
 SCAN_CHECKPOINT = 64        # GDR_SCAN_CHECKPOINT
@@ -88,22 +90,27 @@ def _lib():
 # with its messages. A C call that was made is not made again: its status, if it is not OK, is
 # the answer. On a GB300's host a call of qk_norm_rope_append takes 13 us through the
 # Python code and 2.5 us compiled, the launch included.
-_host = None
-
-
-def _load_host():
-    global _host
-    path = os.path.join(os.path.dirname(LIB_PATH), "_layers_host.so")
+def _load_host(path):
+    """The compiled calls, or None (with a warning) where they were not built for this torch or
+    cannot be imported: every call then runs from Python."""
     if not os.path.exists(path):
-        raise RuntimeError(f"{path} not built; run chunkwise_gated_delta_gdr_gb300.build")
+        warnings.warn(f"{path} not built (chunkwise_gated_delta_gdr_gb300.build): the layers' "
+                      "calls run from Python, with some 10 us more host time each")
+        return None
     spec = importlib.util.spec_from_file_location("_layers_host", path)
-    _host = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(_host)
+    try:
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+    except ImportError as e:
+        warnings.warn(f"the layers' calls run from Python: {e}")
+        return None
+    return module
 
 
+_host = None
 if os.path.exists(LIB_PATH):
     load_library()
-    _load_host()
+    _host = _load_host(host_path(torch.__version__))
 
 
 # ------------------------------------------------------------------ shared checks

@@ -104,3 +104,40 @@ def test_a_call_that_was_made_is_not_made_again(layers, recorded, monkeypatch, n
     monkeypatch.setattr(layers, "_host", Compiled(None))
     call()
     assert [n for n, _ in recorded.calls if not n.endswith("_size")] == ["gdr_" + name]
+
+
+# ------------------------------------------------------------------ the compiled module and torch
+def test_compiled_module_is_named_after_its_torch(layers):
+    assert gbuild._host_target() == gbuild.host_path(torch.__version__)
+    assert gbuild.host_path("1.2.3") != gbuild.host_path("1.2.4")
+    assert layers._host is None or layers._host.__file__ == gbuild.host_path(torch.__version__)
+
+
+def test_another_torch_is_not_up_to_date(layers, monkeypatch, tmp_path):
+    (tmp_path / "version.py").write_text("__version__ = '0.0.1'\n")
+    monkeypatch.setattr(gbuild, "_torch_dir", lambda: str(tmp_path))
+    assert gbuild._host_target() == gbuild.host_path("0.0.1")
+    assert not gbuild.up_to_date()
+
+
+def test_module_that_is_missing_or_broken_leaves_the_python_calls(layers, tmp_path):
+    with pytest.warns(UserWarning, match="not built"):
+        assert layers._load_host(gbuild.host_path("0.0.1")) is None
+    broken = tmp_path / "_layers_host.so"
+    broken.write_bytes(b"no module")
+    with pytest.warns(UserWarning, match="from Python"):
+        assert layers._load_host(str(broken)) is None
+
+
+@pytest.mark.parametrize("error", [FileNotFoundError("g++"), RuntimeError("g++ failed")])
+def test_library_builds_without_the_compiled_module(layers, monkeypatch, tmp_path, error):
+    """No compiler for it, no torch headers: build() still gives the library."""
+    def fail():
+        raise error
+    monkeypatch.setattr(gbuild, "_compile_host", fail)
+    monkeypatch.setattr(gbuild, "_host_target", lambda: str(tmp_path / "none.so"))
+    with pytest.warns(UserWarning, match="no compiled calls"):
+        assert gbuild.build() == gbuild.LIB
+    monkeypatch.undo()
+    monkeypatch.setattr(gbuild, "_torch_dir", lambda: None)
+    assert gbuild._host_target() is None and gbuild.up_to_date()
