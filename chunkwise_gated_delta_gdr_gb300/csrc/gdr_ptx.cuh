@@ -352,33 +352,6 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n"
                "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// TMA tile loads with cluster multicast: the box lands at the same shared
-// offset in every CTA of `mask`, each counting the bytes on its own mbarrier
-// at `bar`'s offset.
-__device__ __forceinline__ void tma_load3_mc(uint32_t dst, const CUtensorMap* map, int c0, int c1,
-                                             int c2, uint64_t* bar, uint16_t mask) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster"
-      " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
-      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar)), "h"(mask)
-      : "memory");
-}
-__device__ __forceinline__ void tma_load4_mc(uint32_t dst, const CUtensorMap* map, int c0, int c1,
-                                             int c2, int c3, uint64_t* bar, uint16_t mask) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
-      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar)), "h"(mask)
-      : "memory");
-}
-// Arrival on the mbarrier at `bar`'s offset in every CTA of `mask` once all
-// tcgen05.mma issued so far by this thread are done.
-__device__ __forceinline__ void umma_commit_mc(uint64_t* bar, uint16_t mask) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-      " [%0], %1;" ::"r"(smem_u32(bar)), "h"(mask)
-      : "memory");
-}
 // Plain bulk copy shared -> global of `bytes` (multiple of 16, both ends
 // 16-byte aligned), tracked by this thread's bulk async-group.
 __device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
