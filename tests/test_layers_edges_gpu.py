@@ -9,7 +9,7 @@ import torch
 
 import chunkwise_gated_delta_gdr_gb300 as gdr
 from test_layers_gpu import (BF, DEV, EDGE, F32, attn_ref, check, gen_of, make_cache, make_pages,
-                             qk_inputs, rnd, scan_inputs, tables)
+                             qk_inputs, qk_ref, rnd, scan_check, scan_inputs, tables)
 
 pytestmark = pytest.mark.gpu
 
@@ -264,3 +264,33 @@ def test_empty_cache(pages, columns, dt, D):
                                  None, pos, kc, vc, table)
     assert torch.isnan(qo).all()
     assert (kc == 3).all() and (vc == 3).all()
+
+
+# ------------------------------------------------------------------ branches of the dispatch
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("dt", [F32, BF])
+@pytest.mark.parametrize("shape", [(64, 9, 512), (40, 31, 514), (33, 32, 777), (24, 33, 1024)])
+def test_scan_wide_and_short(shape, dt, gated):
+    """Channels for more blocks than the walk keeps resident, at the number of tokens (32) up to
+    which a thread takes its channels by itself, pairs and single channels."""
+    scan_check(*scan_inputs(*shape, dt, F32, 84), gated)
+
+
+@pytest.mark.parametrize("dt,out", [(BF, F32), (F32, BF)])
+@pytest.mark.parametrize("D,R,inter", [(128, 128, False), (96, 48, True), (30, 30, False), (33, 32, True)])
+def test_qk_backward_of_mixed_types(D, R, inter, dt, out):
+    """Upstream gradients of another type than q and k: all four gradients."""
+    B, T, HQ, HK = 2, 37, 4, 2
+    q, k, _, wq, wk, cos, sin, pos = qk_inputs(B, T, HQ, HK, D, R, dt, 85)
+    d = rnd(gen_of(86), B, T, HQ, D, dtype=out), rnd(gen_of(87), B, T, HK, D, dtype=out)
+    grads = gdr.qk_norm_rope_bwd(*d, q, k, wq, wk, cos, sin, pos, eps=1e-5, interleaved=inter)
+    for x, w, dy, dx, dw in ((q, wq, d[0], grads[0], grads[2]), (k, wk, d[1], grads[1], grads[3])):
+        xr, wr = x.double().requires_grad_(True), w.double().requires_grad_(True)
+        rx, rw = torch.autograd.grad(qk_ref(xr, wr, cos, sin, pos, 1e-5, inter), (xr, wr), dy.double())
+        unit = qk_ref(x, None, None, None, None, 1e-5, False)
+        inv = (unit / x.double()).abs().nan_to_num(0.0).amax(-1, keepdim=True)
+        terms = dy.double().abs().amax(-1, keepdim=True) * inv * 2
+        assert dx.dtype == dt and dw.dtype == F32
+        check(dx, rx, 4e-6 * max(1, D / 32), terms * unit.abs().amax(-1, keepdim=True).clamp_min(1))
+        mags = (dy.double().abs().amax(-1, keepdim=True) * 2 * unit.abs()).sum((0, 1, 2))
+        check(dw, rw, 4e-6, mags)
