@@ -947,7 +947,8 @@ Plan make_plan(const gdr_attn_dims* d, const gdr_paged_cache* c, Kind kind) {
   return p;
 }
 
-size_t plan_bytes(const Plan& p) { return kAlign + p.o_bytes + p.ml_bytes; }
+// Never 0, which stands for invalid arguments.
+size_t plan_bytes(const Plan& p) { return p.whole ? kAlign : p.o_bytes + p.ml_bytes; }
 
 template <class Core>
 gdr_status launch_ring(const AttnArgs& a, cudaStream_t s) {
@@ -1013,8 +1014,8 @@ gdr_status gdr_paged_decode_attn(const void* q, const void* k_cache, const void*
   a.vc = v_cache ? v_cache : workspace;
   a.q = q; a.table = page_table; a.lens = lens;
   a.out = out; a.lse = lse;
-  a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + kAlign);
-  a.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + kAlign + p.o_bytes);
+  a.part_o = static_cast<float*>(workspace);
+  a.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.o_bytes);
   a.B = dims->B; a.HQ = dims->HQ; a.HK = cache->HK; a.D = cache->D;
   a.G = dims->HQ / cache->HK; a.GH = p.GH; a.groups = p.groups;
   a.page = cache->page_size;
