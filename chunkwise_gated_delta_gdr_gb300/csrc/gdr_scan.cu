@@ -41,7 +41,7 @@ struct ScanArgs {
 // exp over [0, g], taken by the trapezoidal rule with the first Euler-Maclaurin correction,
 // 1 - d / 2 + g d / 12, whose next term is below 4e-7; beyond |g| = 0.13 the difference keeps
 // a's error, under 1e-6 of it. (Pairs go two operations an instruction. Against the difference
-// alone: 88 us instead of 82 forward, 164 instead of 153 backward, at 2 x 8192 x 4096.)
+// alone: 86 us instead of 83 forward, 161 instead of 153 backward, at 2 x 8192 x 4096.)
 template <int V>
 __device__ __forceinline__ void gate(float* g, float* m) {
   constexpr float kNear = 0.13f;
@@ -272,17 +272,17 @@ struct ScanMaps {
   CUtensorMap x, g, dh;
 };
 
-template <typename X, typename G, typename H, int V, bool kTensor>
+template <typename X, typename G, typename H, int V, bool kTensor, bool kGated>
 struct Fwd {
   static constexpr int R = kRows<X, G, V>, TILE = W * R, ST = kStages<X, G, float, V, kTensor>;
   static constexpr int XB = Feed<X, V, R, kTensor>::kBytes, GB = Feed<G, V, R, kTensor>::kBytes;
   static constexpr int SB = XB + GB, SMEM = ST * SB;
 };
 
-template <typename X, typename G, typename H, int V, bool kTensor>
+template <typename X, typename G, typename H, int V, bool kTensor, bool kGated>
 __global__ void __launch_bounds__(W * 32, 2)
     scan_kernel(const __grid_constant__ ScanMaps maps, ScanArgs a, int S) {
-  using F = Fwd<X, G, H, V, kTensor>;
+  using F = Fwd<X, G, H, V, kTensor, kGated>;
   constexpr int R = F::R, TILE = F::TILE, ST = F::ST, SB = F::SB;
   extern __shared__ __align__(128) char ring[];
   __shared__ ScanShared<V, false> sm;
@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(W * 32, 2)
         gf.take(stage * SB, r, e[r]);
       }
     }
-    if (a.gated) {
+    if constexpr (kGated) {
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         float m[V];
@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(W * 32, 2)
 // The same walk from the last tile back. What travels is mu_t = a_t l_t, the gradient that
 // reaches h_{t-1}: a stretch maps the mu after it to A mu + M, with the same A. The states
 // inside a tile come from its checkpoint and the warps' forward pairs.
-template <typename X, typename G, typename H, int V, bool kTensor>
+template <typename X, typename G, typename H, int V, bool kTensor, bool kGated>
 struct Bwd {
   static constexpr int R = CK / W, TILE = CK, ST = kStages<X, G, H, V, kTensor>;
   static constexpr int XB = Feed<X, V, R, kTensor>::kBytes, GB = Feed<G, V, R, kTensor>::kBytes;
@@ -442,14 +442,14 @@ struct Bwd {
   // leaves the blocks per SM as they are, else in registers.
   static constexpr int PARK = W * 32 * R * V * 4, SM = 228 * 1024;
   static constexpr int USED = ST * SB + (int)sizeof(ScanShared<V, true>) + 1024;
-  static constexpr bool kPark = 2 * USED > SM || 2 * (USED + PARK) <= SM;
+  static constexpr bool kPark = kGated && (2 * USED > SM || 2 * (USED + PARK) <= SM);
   static constexpr int SMEM = ST * SB + (kPark ? PARK : 0);
 };
 
-template <typename X, typename G, typename H, int V, bool kTensor>
+template <typename X, typename G, typename H, int V, bool kTensor, bool kGated>
 __global__ void __launch_bounds__(W * 32, 2)
     scan_bwd_kernel(const __grid_constant__ ScanMaps maps, ScanArgs a, int S) {
-  using F = Bwd<X, G, H, V, kTensor>;
+  using F = Bwd<X, G, H, V, kTensor, kGated>;
   constexpr int R = F::R, TILE = F::TILE, ST = F::ST, SB = F::SB;
   extern __shared__ __align__(128) char ring[];
   __shared__ ScanShared<V, true> sm;
@@ -469,9 +469,9 @@ __global__ void __launch_bounds__(W * 32, 2)
   Feed<X, V, R, kTensor> xf(ring, warp, lane);
   Feed<G, V, R, kTensor> gf(ring + F::XB, warp, lane);
   Feed<H, V, R, kTensor> df(ring + F::XB + F::GB, warp, lane);
-  auto load = [&](int stage, int n) {
+  auto load = [&](int stage, int n, bool go) {
     if constexpr (kTensor) {
-      if (threadIdx.x == 0 && !lost && n >= 0) {
+      if (threadIdx.x == 0 && go && n >= 0) {
         ptx::mbar_expect_tx(&sm.full[stage], SB);
         const uint32_t dst = ptx::smem_u32(ring + stage * SB);
         ptx::tma_load3(dst, &maps.x, col * 32 * V, n * TILE, b, &sm.full[stage]);
@@ -512,13 +512,13 @@ __global__ void __launch_bounds__(W * 32, 2)
     __syncthreads();
   int n = a.N - 1 - rank;
 #pragma unroll
-  for (int i = 0; i < ST; ++i) load(i, n - i * S);
+  for (int i = 0; i < ST; ++i) load(i, n - i * S, true);
   load_ck(n);
   const int steps = (a.N + S - 1) / S;
   for (int step = 0; step < steps; ++step, n -= S) {
     const int par = step & 1, stage = step % ST, t0 = n * TILE + warp * R;
     const int rows = n < 0 ? 0 : min(R, a.T - t0);
-    float e[R][V], m[F::kPark ? 1 : R][V], u[R][V], l[R][V], hs[V], A[V], P[V], M[V];
+    float e[R][V], m[kGated && !F::kPark ? R : 1][V], u[R][V], l[R][V], hs[V], A[V], P[V], M[V];
     if constexpr (kTensor) {
       if (n >= 0 && !lost && !ptx::mbar_wait(&sm.full[stage], (step / ST) & 1, a.polls))
         lost = step + 1;
@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(W * 32, 2)
     }
     // u becomes what dg multiplies (h_{t-1}, minus x_t when gated), but for what the state before
     // the warp adds to it.
-    if (a.gated) {
+    if constexpr (kGated) {
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         float weight[V];
@@ -569,7 +569,7 @@ __global__ void __launch_bounds__(W * 32, 2)
           A[i] *= e[r][i];
         }
     }
-    if constexpr (!kTensor) load(stage, n - ST * S);
+    if constexpr (!kTensor) load(stage, n - ST * S, true);
     load_ck(n - S);
 #pragma unroll
     for (int r = R - 1; r >= 0; --r)
@@ -585,7 +585,9 @@ __global__ void __launch_bounds__(W * 32, 2)
     put_v<2 * V>(sm.warp[par][warp][lane], w);
     put_v<V>(sm.back[par][warp][lane], M);
     __syncthreads();
-    if constexpr (kTensor) load(stage, n - ST * S);
+    // The stage is free. Its next tile is asked for here, or without gates, whose steps are
+    // shorter, behind the exchange (2 x 8192 x 4096: 148 us there, 165 here; gated 164 and 162).
+    if constexpr (kTensor && kGated) load(stage, n - ST * S, !lost);
     float pA[V], pM[V], tA[V], tM[V], mu[V];     // after this warp; of the whole tile
 #pragma unroll
     for (int i = 0; i < V; ++i) tA[i] = 1.f, tM[i] = 0.f;
@@ -621,11 +623,13 @@ __global__ void __launch_bounds__(W * 32, 2)
         u[r][i] += hs[i];
         hs[i] *= e[r][i];
       }
+    // (Also if the exchange of this very step gave up: leave() counts on it.)
+    if constexpr (kTensor && !kGated) load(stage, n - ST * S, !lost || lost == step + 2);
     const size_t row0 = ((size_t)b * a.T + max(t0, 0)) * a.D + d;
 #pragma unroll
     for (int r = R - 1; r >= 0; --r) {
       float ox[V], og[V], weight[V];
-      if (a.gated) {
+      if constexpr (kGated) {
         if constexpr (F::kPark)
           get_v<V>(park + r * (W * 32 * V), weight);
         else
@@ -781,14 +785,15 @@ long long cluster_size(const Residency& r, long long clusters, int tiles, int* b
   return least;
 }
 
-template <typename X, typename G, typename H, int V, bool kTensor, bool kBwd>
+template <typename X, typename G, typename H, int V, bool kTensor, bool kBwd, bool kGated>
 struct Walk {
-  using F = std::conditional_t<kBwd, Bwd<X, G, H, V, kTensor>, Fwd<X, G, H, V, kTensor>>;
+  using F = std::conditional_t<kBwd, Bwd<X, G, H, V, kTensor, kGated>,
+                               Fwd<X, G, H, V, kTensor, kGated>>;
   static auto kernel() {
     if constexpr (kBwd)
-      return scan_bwd_kernel<X, G, H, V, kTensor>;
+      return scan_bwd_kernel<X, G, H, V, kTensor, kGated>;
     else
-      return scan_kernel<X, G, H, V, kTensor>;
+      return scan_kernel<X, G, H, V, kTensor, kGated>;
   }
   // The time of this walk by the rule above, and its blocks per cluster; -1: a CUDA error.
   static long long plan(const ScanArgs& a, int* S) {
@@ -823,21 +828,21 @@ struct Walk {
 // Two channels a lane or one. One halves a block's work for the same number of steps: a
 // step takes 0.7 of the time (319 and 221 us at 1 x 16384 x 1024, S = 1, backward), and
 // narrow problems get twice the blocks.
-template <typename X, typename G, typename H, bool kBwd>
+template <typename X, typename G, typename H, bool kBwd, bool kGated>
 gdr_status launch_tensor(const gdr_scan_dims* d, const ScanArgs& a, cudaStream_t s) {
+  using One = Walk<X, G, H, 1, true, kBwd, kGated>;
+  using Two = Walk<X, G, H, 2, true, kBwd, kGated>;
   int S2 = 1, S1 = 1;
-  const long long two = Walk<X, G, H, 2, true, kBwd>::plan(a, &S2);
-  const long long one = Walk<X, G, H, 1, true, kBwd>::plan(a, &S1);
+  const long long two = Two::plan(a, &S2), one = One::plan(a, &S1);
   if (two < 0 || one < 0) return GDR_ERR_CUDA;
-  return one * 7 < two * 10 ? Walk<X, G, H, 1, true, kBwd>::launch(d, a, S1, s)
-                            : Walk<X, G, H, 2, true, kBwd>::launch(d, a, S2, s);
+  return one * 7 < two * 10 ? One::launch(d, a, S1, s) : Two::launch(d, a, S2, s);
 }
 
-template <typename X, typename G, typename H, int V, bool kBwd>
+template <typename X, typename G, typename H, int V, bool kBwd, bool kGated>
 gdr_status launch_plain(const gdr_scan_dims* d, const ScanArgs& a, cudaStream_t s) {
+  using Plain = Walk<X, G, H, V, false, kBwd, kGated>;
   int S = 1;
-  if (Walk<X, G, H, V, false, kBwd>::plan(a, &S) < 0) return GDR_ERR_CUDA;
-  return Walk<X, G, H, V, false, kBwd>::launch(d, a, S, s);
+  return Plain::plan(a, &S) < 0 ? GDR_ERR_CUDA : Plain::launch(d, a, S, s);
 }
 
 enum Path { kPlain, kPairs, kTensorMaps };       // one channel; two; tiles by tensor maps
@@ -859,9 +864,13 @@ gdr_status launch(const gdr_scan_dims* d, const ScanArgs& a, Path path, cudaStre
                                  grid, 128, 0, s, a);
           }
         }
-        return path == kTensorMaps ? launch_tensor<X, G, H, kBwd>(d, a, s)
-               : path == kPairs    ? launch_plain<X, G, H, 2, kBwd>(d, a, s)
-                                   : launch_plain<X, G, H, 1, kBwd>(d, a, s);
+        auto walk = [&](auto gated) {
+          constexpr bool kGated = decltype(gated)::value;
+          return path == kTensorMaps ? launch_tensor<X, G, H, kBwd, kGated>(d, a, s)
+                 : path == kPairs    ? launch_plain<X, G, H, 2, kBwd, kGated>(d, a, s)
+                                     : launch_plain<X, G, H, 1, kBwd, kGated>(d, a, s);
+        };
+        return a.gated ? walk(std::true_type()) : walk(std::false_type());
       });
     });
   });
