@@ -153,18 +153,24 @@ __device__ __forceinline__ void copy_v(float* p, const float* v) {
 
 // Bounded wait for the pairs of a step, acquiring what other blocks of the cluster sent.
 __device__ __forceinline__ bool met_wait(uint64_t* bar, uint32_t parity, long polls) {
-  for (long i = 0; i <= polls; ++i) {
-    uint32_t ok;
+  const uint32_t at = ptx::smem_u32(bar);
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n"
+      " mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(at), "r"(parity)
+      : "memory");
+  for (long i = 0; !ok && i < polls; ++i)
     asm volatile(
         "{\n .reg .pred p;\n"
         " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
         " selp.u32 %0, 1, 0, p;\n}\n"
         : "=r"(ok)
-        : "r"(ptx::smem_u32(bar)), "r"(parity)
+        : "r"(at), "r"(parity)
         : "memory");
-    if (ok) return true;
-  }
-  return false;
+  return ok != 0;
 }
 
 // The blocks' pairs of a step applied to `carry` (the state before the step): `mine` becomes

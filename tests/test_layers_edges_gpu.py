@@ -94,9 +94,10 @@ def test_append_stores_values_unchanged(T, D, R, odd, dt, cdt):
 
 
 # ------------------------------------------------------------------ waits of the scan that give up
+@pytest.mark.parametrize("gated", [True, False])
 @pytest.mark.parametrize("dt", [BF, F32])
 @pytest.mark.parametrize("B,T,D", [(1, 5000, 512), (3, 700, 1024), (1, 3000, 66), (2, 900, 33)])
-def test_scan_waits_that_give_up(B, T, D, dt):
+def test_scan_waits_that_give_up(B, T, D, dt, gated):
     """With few polls allowed, waits for tiles and for other blocks give up: every result is NaN
     or has its right bits, the launch ends by itself, and calls with the usual bound are as ever."""
     x, g, h0, dh, dfinal = scan_inputs(B, T, D, dt, F32, 75)
@@ -105,14 +106,14 @@ def test_scan_waits_that_give_up(B, T, D, dt):
     def calls():
         outs = [torch.full_like(x, 7), torch.full_like(h0, 7), torch.full_like(ck, 7),
                 torch.full_like(x, 7), torch.full_like(g, 7), torch.full_like(h0, 7)]
-        gdr.linear_scan_fwd(x, g, h0, gated_input=True, out=outs[0], final_state=outs[1],
+        gdr.linear_scan_fwd(x, g, h0, gated_input=gated, out=outs[0], final_state=outs[1],
                             checkpoints=outs[2])
-        gdr.linear_scan_bwd(dh, x, g, ck, dfinal, gated_input=True, dx=outs[3], dg=outs[4],
+        gdr.linear_scan_bwd(dh, x, g, ck, dfinal, gated_input=gated, dx=outs[3], dg=outs[4],
                             d_initial_state=outs[5])
         torch.cuda.synchronize()
         return outs
 
-    gdr.linear_scan_fwd(x, g, h0, gated_input=True, checkpoints=ck)
+    gdr.linear_scan_fwd(x, g, h0, gated_input=gated, checkpoints=ck)
     want = calls()
     old = gdr.set_flag_wait_limit(-1)
     for polls in (0, 0, 1, 2, 8, 64):
