@@ -18,11 +18,17 @@
 // The cache is read once: 2 len HK D elements, against 4 len HQ D operations, a few % of the
 // tensor rate at 8 queries a head. Bound by HBM from some 100 MB on, by the chain length -
 // page - row - sums below. Measured on one GB300, bf16, D = 128, kv heads of the cache HK:
-//   1 x 65000 keys, HK = 16, 2 queries a head: 89 us, 6.0 TB/s (a plain copy: 6.78 TB/s)
-//   64 sequences of 0 .. 8192 keys, HK = 4, 8 queries a head: 84 % of the copy rate
+//   1 x 65000 keys, HK = 16, 2 queries a head: 90-92 us, 5.8-6.0 TB/s (a plain copy: 6.78 TB/s)
+//   64 sequences of 0 .. 8192 keys, HK = 4, 8 queries a head: 97-101 us, 79-82 % of the copy rate
 //   4 x 200 keys, HK = 16: 8.2 us a call
-// fp32, 16 x 8000 keys, HK = 8: D = 256 308 us, 6.8 TB/s; D = 64 90 us, 5.8; D = 128 with 8
-// queries a head 242 us, 4.3 (bound by the fp32 products).
+// 16 x 8000 keys, HK = 8, D = 128: 4 queries a head 92 us, 5.7 TB/s; 16 97 us; 32 182 us, since the
+// cache is read once per group of 16.
+// fp32, 16 x 8000 keys, HK = 8: D = 256 309 us, 6.8 TB/s; D = 64 92 us, 5.7; D = 128 with 4
+// queries a head 174 us, 6.0; with 8 241 us, 4.3, bound by the reads of q from shared memory
+// (that pipe is 65 % busy, fp32 arithmetic 17 %).
+// The general kernel, same keys: fp32 D = 72, 2 queries a head 277 us, 2.1 TB/s; bf16, 4 queries,
+// D = 40 529 us and D = 136 858 us, 0.3 and 0.6 TB/s: its rows come through registers, a few keys
+// at a time, once per 4 query heads (2 beyond D = 128).
 #include <type_traits>
 
 #include "gdr_ops.cuh"
@@ -775,7 +781,7 @@ __global__ void __launch_bounds__(Core::NW * 32, Core::OCC) paged_ring_kernel(At
 // ------------------------------------------------------------ items cut by block boundaries
 // Launched behind the kernel above; each block finds its item before it waits for that kernel,
 // so that what is left after it is two rounds of loads. It costs 4 us at 64 sequences and 6 at
-// one of 65000 keys (54 parts), most of it the second kernel's start. Block (x, y): heads y hb
+// one of 65000 keys (16 items of 19 or 20 parts), most of it the second kernel's start. Block (x, y): heads y hb
 // and on of item x, or, with more items than blocks, of the item that the boundary after
 // stretch x is the first to cut. The JW warps share a head's parts (hb < JW) or take every
 // JW-th head; a lane has V channels in a row at a time.

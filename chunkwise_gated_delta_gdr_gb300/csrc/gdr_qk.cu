@@ -9,6 +9,8 @@
 //   2 x 8192 x (32 + 4) heads, half of each turned: forward 53 us, 5.7 TB/s (a plain copy:
 //   6.78 TB/s); backward 84 us, 5.4 TB/s
 //   1 x 4096 x (12 + 12) heads: forward 15 us, backward 20 and the weights' sums 3 us
+//   into pages: 66 us (5.1 TB/s) and 18.5 us
+//   fp32: forward 107 us, backward 181, into pages 121 (5.6, 5.0 and 5.5 TB/s); 23, 33 and 28 us
 //   64 decode tokens x (16 + 4 + 4) heads into their pages: 6.1 us a call, bound by the chain
 //   position - page and angles - row of one token
 #include <type_traits>
@@ -439,7 +441,7 @@ __global__ void __launch_bounds__(VT, resident(MODE)) qk_vec_kernel(QkArgs a, Ve
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 const float2 u = mul2(x[k][j], rs2);
-                acc[j] = fma2(d[k][j], u, acc[j]);   // rows beyond the unit are zeros
+                acc[j] = fma2(d[k][j], u, acc[j]);
                 y[j] = mul2(rs2, fma2(u, m2, mul2(d[k][j], w[j])));
               }
             } else {

@@ -8,10 +8,12 @@
 // latency of a step (see below) where there are not. Every element is read once and written
 // once: the sequence is split without a second pass.
 //
-// Measured on one GB300, bf16 x and fp32 g, us and TB/s (a plain copy: 6.78 TB/s):
-//   forward   1 x 65000 x 4096  311  6.8     2 x 8192 x 4096   84  6.4    1 x 4096 x 1536  16.5  3.0
-//   backward  1 x 65000 x 4096  596  6.3     2 x 8192 x 4096  153  6.1    1 x 4096 x 1536  26.8  3.3
-//   fp32, 3 x 1021 x 777 (rows that no tensor copy can read): 11.2 and 17.4 us, 2.6 and 2.7 TB/s
+// Measured on one GB300, fp32 g, us (TB/s; a plain copy: 6.78), forward and backward:
+//   bf16 x         1 x 65000 x 4096       2 x 8192 x 4096      1 x 4096 x 1536
+//     u = x        318 (6.7) 584 (6.4)    84 (6.4) 149 (6.3)   16.8 (3.0) 24.7 (3.6)
+//     (1 - a) x    324 (6.6) 629 (5.9)    86 (6.2) 161 (5.8)   18.5 (2.7) 26.7 (3.3)
+//   fp32 x, (1 - a) x                    139 (5.8) 201 (6.7)   19.4 (3.9) 28.8 (4.4)
+//   fp32, 3 x 1021 x 777 (rows that no tensor copy can read): 10.4 (2.7) 16.6 (2.9); gated 11.5, 18.6
 #include <type_traits>
 
 #include "gdr_ops.cuh"
