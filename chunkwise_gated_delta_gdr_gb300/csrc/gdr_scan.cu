@@ -34,7 +34,7 @@ struct ScanArgs {
   float* ck;           // checkpoints; may be null in the forward
   int B, T, D, N;      // N = ceil(T / CK)
   int gated;
-  long polls;          // bound of a wait (gdr_set_flag_wait_limit)
+  long polls;          // bound of a wait
   int64_t xb, xt, gb, gt, db, dt;   // strides in elements
 };
 
@@ -225,7 +225,7 @@ __device__ __forceinline__ void cluster_carry(ScanShared<V, kBwd>& sm, int step,
 // waited for, again with a bound. No block leaves while another may send to it; pairs sent
 // before that barrier that a block has not seen arrive need a microsecond more: it stays a
 // thousand.
-constexpr long kDrainPolls = 1L << 24;
+constexpr long kDrainPolls = 1L << 20;           // about a second
 template <int ST, typename F>
 __device__ __forceinline__ void leave(uint64_t* full, int lost, int S, F there) {
   if constexpr (ST > 0) {
@@ -681,7 +681,8 @@ ScanArgs make_args(const gdr_scan_dims* d) {
   a.B = d->B; a.T = d->T; a.D = d->D;
   a.N = (int)(((int64_t)d->T + CK - 1) / CK);
   a.gated = d->gated_input != 0;
-  a.polls = (long)set_wait_limit(-1);
+  // A poll here may be suspended for about 1 us (measured), as long as sixteen of a flag take.
+  a.polls = (long)(set_wait_limit(-1) / 16);
   a.xb = d->x_stride_b; a.xt = d->x_stride_t;
   a.gb = d->g_stride_b; a.gt = d->g_stride_t;
   a.db = d->dh_stride_b; a.dt = d->dh_stride_t;

@@ -191,8 +191,8 @@ gdr_status gdr_stream_status(gdr_stream_t stream, void* workspace);
  * (gdr_stream_status reports it) and runs to its end on whatever the
  * workspace holds: the call then finishes with wrong outputs instead of
  * hanging. The default, 2^24 polls (about a second), is far beyond any real
- * wait. The waits of gdr_linear_scan_fwd and _bwd have the same bound; there a
- * wait that gave up turns results into NaN.
+ * wait. The waits of gdr_linear_scan_fwd and _bwd have the same bound in time
+ * (polls / 16, each about 1 us); there a wait that gave up turns results into NaN.
  *
  *   polls   >= 0: the new bound, for calls enqueued from now on (all devices,
  *           all threads); < 0: leave the bound as it is.
