@@ -16,6 +16,9 @@ The other layers of a decoder (``layers.py``):
   qk_norm_rope, qk_norm_rope_bwd    RMS norm of q and k heads with the position rotation
   qk_norm_rope_append               the same for serving, into a paged key-value cache
   paged_decode_attn, paged_decode_attn_workspace_size   one new token against that cache
+  paged_prefix_attn, paged_prefix_attn_workspace_size   the same for a batch with a shared prompt
+  gated_norm, gated_norm_bwd        RMS norm of a layer's output heads with its output gate
+  residual_norm, residual_norm_bwd  add into the residual and norm for the next layer
 """
 from __future__ import annotations
 
@@ -44,12 +47,16 @@ EXPORTED = (
     "gdr_linear_scan_fwd", "gdr_linear_scan_bwd", "gdr_linear_scan_checkpoints_size",
     "gdr_qk_norm_rope", "gdr_qk_norm_rope_bwd", "gdr_qk_norm_rope_bwd_workspace_size",
     "gdr_qk_norm_rope_append", "gdr_paged_decode_attn", "gdr_paged_decode_attn_workspace_size",
+    "gdr_paged_prefix_attn", "gdr_paged_prefix_attn_workspace_size",
+    "gdr_gated_norm", "gdr_gated_norm_bwd", "gdr_gated_norm_bwd_workspace_size",
+    "gdr_residual_norm", "gdr_residual_norm_bwd", "gdr_residual_norm_bwd_workspace_size",
 )
 # Entry points of layers.py, reached as attributes of the package.
 LAYERS = (
     "linear_scan_fwd", "linear_scan_bwd", "linear_scan_checkpoints", "qk_norm_rope",
     "qk_norm_rope_bwd", "qk_norm_rope_append", "paged_decode_attn",
-    "paged_decode_attn_workspace_size",
+    "paged_decode_attn_workspace_size", "paged_prefix_attn", "paged_prefix_attn_workspace_size",
+    "gated_norm", "gated_norm_bwd", "residual_norm", "residual_norm_bwd",
 )
 # Size of the library-owned scratch used by gdr_chunk_fwd_noalloc (per device).
 GDR_NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024

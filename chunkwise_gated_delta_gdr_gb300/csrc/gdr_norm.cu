@@ -1,0 +1,865 @@
+// gdr_norm.cu -- the norms around a layer of a decoder, forward and backward.
+//
+// gated_norm, the norm of a layer's output heads with its output gate, a = act(z):
+//   y = u w a,  u = x r,  r = 1 / sqrt(mean(x^2) + eps)        (gate behind the norm)
+//   y = u w,    u = v r,  v = x a, r of v                      (gate before the norm)
+// and with d the gradient of y
+//   behind: dw = sum d a u,  c = d a w,  dx = r (c - u mean(c u)),  dz = d u w a'
+//   before: dw = sum d u,    c = d w,    dv = r (c - u mean(c u)),  dx = dv a,  dz = dv x a'
+//
+// residual_norm, between two layers: p = y or its norm uy wp, a = act(z) or 1, s a number or a
+// channel's weight:
+//   r' = r + s a p,  out = u w,  u = r' rho
+//   g = dr' + rho (c - u mean(c u)),  c = dout w,  dw = sum dout u,  dr = g,  ds = sum g a p
+//   dz = g s p a',  dp = g s a,  dy = dp, or behind a norm: dwp = sum dp uy,
+//   dy = ry (dp wp - uy mean(dp wp uy))
+//
+// Every tensor is read once and written once: bound by HBM where there is enough of it, by the
+// chain load - sum over the row - store of one row below.
+#include "gdr_norm.cuh"
+
+namespace gdr {
+namespace ops {
+namespace {
+
+constexpr int kMaxThreads = 512;
+
+struct GatedArgs {
+  View x, z, d;                  // d: the gradient of y (backward)
+  const float* w;                // [D] or [H][D], or null
+  void *y, *dx, *dz;             // dense
+  float* part;                   // weight gradient's parts, or null
+  int B, T, H, D, tokens, groups, per_head, kind, first;
+  int in_bf16, out_bf16;         // out: of y and d
+  int pieces, stages;
+  float eps, inv_d;
+};
+
+// Sum over the block's groups of each element's acc (LANES > 0), in the first group's registers.
+template <class S>
+__device__ __forceinline__ void sum_groups(float* acc, float* s, int tid) {
+  if constexpr (S::LANES > 0) {
+#pragma unroll
+    for (int o = S::LANES; o < 32; o <<= 1)
+#pragma unroll
+      for (int j = 0; j < S::N; ++j) acc[j] += __shfl_xor_sync(~0u, acc[j], o);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    if (lane < S::LANES)
+#pragma unroll
+      for (int j = 0; j < S::N; ++j) s[(warp * S::N + j) * S::LANES + tid] = acc[j];
+    __syncthreads();
+    if (threadIdx.x < S::LANES)
+      for (int k = 1; k < warps; ++k)
+#pragma unroll
+        for (int j = 0; j < S::N; ++j) acc[j] += s[(k * S::N + j) * S::LANES + tid];
+    __syncthreads();
+  }
+}
+
+template <class S, bool BWD>
+__global__ void __launch_bounds__(kMaxThreads) gated_kernel(GatedArgs a) {
+  constexpr int V = S::V, NV = S::NV, N = S::N, TENSORS = BWD ? 3 : 2;
+  extern __shared__ __align__(16) char places[];
+  __shared__ Red red;
+  __shared__ float sums[BWD && S::LANES ? 8 * 32 * N : 1];      // at most 8 warps in such a block
+  if (BWD) asm volatile("griddepcontrol.launch_dependents;");
+  const Walk w = walk_of<S::LANES>(a.tokens, a.H, a.groups);
+  const Ahead ahead = {places, a.pieces, a.stages};
+  const float* weight = a.w && a.per_head ? a.w + (size_t)w.head * a.D : a.w;
+  float acc[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) acc[j] = 0.f;
+
+  Row<S> row[TENSORS];
+  auto rows_of = [&](int it) {                   // false: no such row
+    const int tok = w.tok + it * w.step;
+    if (!w.on || tok >= a.tokens) return false;
+    const int b = tok / a.T, t = tok - b * a.T;
+    const int per = NV * (a.in_bf16 ? 1 : 2);
+    const size_t es = a.in_bf16 ? 2 : 4, os = a.out_bf16 ? 2 : 4;
+    row[0] = {static_cast<const char*>(a.x.p) + a.x.at(b, t, w.head) * es, a.in_bf16, 0};
+    row[1] = {static_cast<const char*>(a.z.p) + a.z.at(b, t, w.head) * es, a.in_bf16, per};
+    if (BWD)
+      row[TENSORS - 1] = {static_cast<const char*>(a.d.p) + a.d.at(b, t, w.head) * os, a.out_bf16,
+                          2 * per};
+    return true;
+  };
+  auto fetch = [&](int it, int stage) {
+    if constexpr (S::kAhead) {
+      if (it < w.iters && rows_of(it)) {
+#pragma unroll
+        for (int c = 0; c < NV; ++c) {
+          const int i = (c * w.threads + w.tid) * V;
+          if (i < a.D)
+#pragma unroll
+            for (int k = 0; k < TENSORS; ++k) row[k].fetch(ahead, stage, c, i);
+        }
+      }
+      ptx::cp_async_commit();
+    }
+  };
+  for (int i = 0; i + 1 < a.stages; ++i) fetch(i, i);
+  int turn = 0, stage = 0;
+  for (int it = 0; it < w.iters; ++it, stage = stage + 1 == a.stages ? 0 : stage + 1) {
+    fetch(it + a.stages - 1, stage == 0 ? a.stages - 1 : stage - 1);
+    if constexpr (S::kAhead) ahead.wait();
+    const bool on = rows_of(it);
+    const size_t dense = ((size_t)(w.tok + it * w.step) * a.H + w.head) * a.D;
+    float s[2] = {0.f, 0.f};
+    if (on)
+#pragma unroll
+      for (int c = 0; c < NV; ++c) {
+        const int i = (c * w.threads + w.tid) * V;
+        if (i >= a.D) continue;
+        float x[V], z[V], d[V], wt[V];
+        row[0].get(ahead, stage, c, i, x);
+        if (a.first || BWD) row[1].get(ahead, stage, c, i, z);
+        if (BWD) {
+          row[TENSORS - 1].get(ahead, stage, c, i, d);
+          if (weight) load_run<float, V>(weight + i, wt);
+        }
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const float g = a.first || BWD ? act(z[e], a.kind) : 1.f;
+          const float v = a.first ? x[e] * g : x[e];
+          s[0] = fmaf(v, v, s[0]);
+          if (BWD) {
+            const float dc = a.first ? d[e] : d[e] * g;
+            s[1] = fmaf(weight ? dc * wt[e] : dc, v, s[1]);
+          }
+        }
+      }
+    row_sum<S::LANES, BWD ? 2 : 1>(s, red, turn);
+    if (!on) continue;
+    const float r = rsqrtf(fmaf(s[0], a.inv_d, a.eps)), m = s[1] * a.inv_d * r;
+#pragma unroll
+    for (int c = 0; c < NV; ++c) {
+      const int i = (c * w.threads + w.tid) * V;
+      if (i >= a.D) continue;
+      float x[V], z[V], d[V], wt[V], o[V], oz[V];
+      row[0].get(ahead, stage, c, i, x);
+      row[1].get(ahead, stage, c, i, z);
+      if (BWD) row[TENSORS - 1].get(ahead, stage, c, i, d);
+      if (weight) {
+        load_run<float, V>(weight + i, wt);
+      } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) wt[e] = 1.f;
+      }
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        float slope;
+        const float g = act(z[e], a.kind, slope);
+        const float u = (a.first ? x[e] * g : x[e]) * r;
+        if (!BWD) {
+          o[e] = a.first ? u * wt[e] : u * wt[e] * g;
+        } else if (a.first) {
+          const float dv = r * fmaf(-u, m, d[e] * wt[e]);
+          acc[c * V + e] = fmaf(d[e], u, acc[c * V + e]);
+          o[e] = dv * g;
+          oz[e] = dv * x[e] * slope;
+        } else {
+          const float dg = d[e] * g;
+          acc[c * V + e] = fmaf(dg, u, acc[c * V + e]);
+          o[e] = r * fmaf(-u, m, dg * wt[e]);
+          oz[e] = d[e] * u * wt[e] * slope;
+        }
+      }
+      if (BWD) {
+        store_any<V>(a.dx, dense + i, a.in_bf16, o);
+        store_any<V>(a.dz, dense + i, a.in_bf16, oz);
+      } else {
+        store_any<V>(a.y, dense + i, a.out_bf16, o);
+      }
+    }
+  }
+  if (!BWD || !a.part) return;
+  // Shared weights: a row of parts per block; a head's own: one per group of that head.
+  if (!a.per_head) sum_groups<S>(acc, sums, w.tid);
+  if (a.per_head ? !w.on : (S::LANES && threadIdx.x >= S::LANES)) return;
+  float* to = a.part + (a.per_head ? ((size_t)w.tok * a.H + w.head) * a.D : (size_t)blockIdx.x * a.D);
+#pragma unroll
+  for (int c = 0; c < NV; ++c) {
+    const int i = (c * w.threads + w.tid) * V;
+    if (i < a.D) store_run<float, V>(to + i, acc + c * V);
+  }
+}
+
+// ------------------------------------------------------------------ residual
+struct ResArgs {
+  View r, y, z, d, dr;           // r: the residual, backward: r'; d, dr: gradients of out and r'
+  const float *w, *wp, *sv;      // [D] or null; sv: the scale per channel
+  void *out, *r_out;             // forward; r_out null without y
+  void *o_dr, *o_dy, *o_dz;      // backward, dense (o_dy, o_dz null without y, z)
+  float* part;                   // [3][blocks][D]: of w, wp, sv; null: none
+  int B, T, D, tokens, kind, post, want_p, want_s;
+  int r_bf16, y_bf16, out_bf16;  // y_bf16: of y and z; out_bf16: of out and d
+  int has_y, has_z, has_dr;
+  int pieces, stages;
+  float eps, inv_d, s;
+};
+
+template <class S>
+__global__ void __launch_bounds__(kMaxThreads) residual_fwd_kernel(ResArgs a) {
+  constexpr int V = S::V, NV = S::NV, N = S::N;
+  extern __shared__ __align__(16) char places[];
+  __shared__ Red red;
+  const Walk w = walk_of<0>(a.tokens, 1, gridDim.x);
+  const Ahead ahead = {places, a.pieces, a.stages};
+  Row<S> rr, ry, rz;
+  auto rows_of = [&](int it) {
+    const int tok = w.tok + it * w.step;
+    if (tok >= a.tokens) return false;
+    const int b = tok / a.T, t = tok - b * a.T;
+    const int rp = NV * (a.r_bf16 ? 1 : 2), yp = NV * (a.y_bf16 ? 1 : 2);
+    rr = {static_cast<const char*>(a.r.p) + a.r.at(b, t, 0) * (a.r_bf16 ? 2 : 4), a.r_bf16, 0};
+    ry = {static_cast<const char*>(a.y.p) + a.y.at(b, t, 0) * (a.y_bf16 ? 2 : 4), a.y_bf16, rp};
+    rz = {static_cast<const char*>(a.z.p) + a.z.at(b, t, 0) * (a.y_bf16 ? 2 : 4), a.y_bf16, rp + yp};
+    return true;
+  };
+  auto fetch = [&](int it, int stage) {
+    if constexpr (S::kAhead) {
+      if (it < w.iters && rows_of(it)) {
+#pragma unroll
+        for (int c = 0; c < NV; ++c) {
+          const int i = (c * w.threads + w.tid) * V;
+          if (i < a.D) {
+            rr.fetch(ahead, stage, c, i);
+            if (a.has_y) ry.fetch(ahead, stage, c, i);
+            if (a.has_z) rz.fetch(ahead, stage, c, i);
+          }
+        }
+      }
+      ptx::cp_async_commit();
+    }
+  };
+  for (int i = 0; i + 1 < a.stages; ++i) fetch(i, i);
+  int turn = 0, stage = 0;
+  for (int it = 0; it < w.iters; ++it, stage = stage + 1 == a.stages ? 0 : stage + 1) {
+    fetch(it + a.stages - 1, stage == 0 ? a.stages - 1 : stage - 1);
+    if constexpr (S::kAhead) ahead.wait();
+    if (!rows_of(it)) break;                     // the whole block
+    const size_t dense = (size_t)(w.tok + it * w.step) * a.D;
+    float py = 1.f, s[1];
+    if (a.post) {
+      s[0] = 0.f;
+#pragma unroll
+      for (int c = 0; c < NV; ++c) {
+        const int i = (c * w.threads + w.tid) * V;
+        if (i >= a.D) continue;
+        float y[V];
+        ry.get(ahead, stage, c, i, y);
+#pragma unroll
+        for (int e = 0; e < V; ++e) s[0] = fmaf(y[e], y[e], s[0]);
+      }
+      row_sum<0, 1>(s, red, turn);
+      py = rsqrtf(fmaf(s[0], a.inv_d, a.eps));
+    }
+    float r[N];
+    s[0] = 0.f;
+#pragma unroll
+    for (int c = 0; c < NV; ++c) {
+      const int i = (c * w.threads + w.tid) * V;
+      if (i >= a.D) continue;
+      float* x = r + c * V;
+      rr.get(ahead, stage, c, i, x);
+      if (a.has_y) {
+        float y[V], k[V];
+        ry.get(ahead, stage, c, i, y);
+#pragma unroll
+        for (int e = 0; e < V; ++e) y[e] *= py;
+        if (a.wp) {
+          load_run<float, V>(a.wp + i, k);
+#pragma unroll
+          for (int e = 0; e < V; ++e) y[e] *= k[e];
+        }
+        if (a.has_z) {
+          rz.get(ahead, stage, c, i, k);
+#pragma unroll
+          for (int e = 0; e < V; ++e) y[e] *= act(k[e], a.kind);
+        }
+        if (a.sv) {
+          load_run<float, V>(a.sv + i, k);
+#pragma unroll
+          for (int e = 0; e < V; ++e) x[e] = fmaf(k[e], y[e], x[e]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < V; ++e) x[e] = fmaf(a.s, y[e], x[e]);
+        }
+        store_any<V>(a.r_out, dense + i, a.r_bf16, x);
+      }
+#pragma unroll
+      for (int e = 0; e < V; ++e) s[0] = fmaf(x[e], x[e], s[0]);
+    }
+    row_sum<0, 1>(s, red, turn);
+    const float rho = rsqrtf(fmaf(s[0], a.inv_d, a.eps));
+#pragma unroll
+    for (int c = 0; c < NV; ++c) {
+      const int i = (c * w.threads + w.tid) * V;
+      if (i >= a.D) continue;
+      float o[V], k[V];
+#pragma unroll
+      for (int e = 0; e < V; ++e) o[e] = r[c * V + e] * rho;
+      if (a.w) {
+        load_run<float, V>(a.w + i, k);
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[e] *= k[e];
+      }
+      store_any<V>(a.out, dense + i, a.out_bf16, o);
+    }
+  }
+}
+
+// FULL: y goes through a norm, a gate or a scale per channel; without, dy = s g.
+template <class S, bool FULL>
+__global__ void __launch_bounds__(kMaxThreads) residual_bwd_kernel(ResArgs a) {
+  constexpr int V = S::V, NV = S::NV, N = S::N;
+  extern __shared__ __align__(16) char places[];
+  __shared__ Red red;
+  asm volatile("griddepcontrol.launch_dependents;");
+  const Walk w = walk_of<0>(a.tokens, 1, gridDim.x);
+  const Ahead ahead = {places, a.pieces, a.stages};
+  float acc[FULL ? 3 : 1][N];
+#pragma unroll
+  for (int k = 0; k < (FULL ? 3 : 1); ++k)
+#pragma unroll
+    for (int j = 0; j < N; ++j) acc[k][j] = 0.f;
+  Row<S> rr, rd, rg, ry, rz;
+  auto rows_of = [&](int it) {
+    const int tok = w.tok + it * w.step;
+    if (tok >= a.tokens) return false;
+    const int b = tok / a.T, t = tok - b * a.T;
+    const int rp = NV * (a.r_bf16 ? 1 : 2), op = NV * (a.out_bf16 ? 1 : 2);
+    const int yp = NV * (a.y_bf16 ? 1 : 2), re = a.r_bf16 ? 2 : 4, ye = a.y_bf16 ? 2 : 4;
+    rr = {static_cast<const char*>(a.r.p) + a.r.at(b, t, 0) * re, a.r_bf16, 0};
+    rd = {static_cast<const char*>(a.d.p) + a.d.at(b, t, 0) * (a.out_bf16 ? 2 : 4), a.out_bf16, rp};
+    rg = {static_cast<const char*>(a.dr.p) + a.dr.at(b, t, 0) * re, a.r_bf16, rp + op};
+    const int at = rp + op + (a.has_dr ? rp : 0);
+    ry = {static_cast<const char*>(a.y.p) + a.y.at(b, t, 0) * ye, a.y_bf16, at};
+    rz = {static_cast<const char*>(a.z.p) + a.z.at(b, t, 0) * ye, a.y_bf16, at + yp};
+    return true;
+  };
+  auto fetch = [&](int it, int stage) {
+    if constexpr (S::kAhead) {
+      if (it < w.iters && rows_of(it)) {
+#pragma unroll
+        for (int c = 0; c < NV; ++c) {
+          const int i = (c * w.threads + w.tid) * V;
+          if (i < a.D) {
+            rr.fetch(ahead, stage, c, i);
+            rd.fetch(ahead, stage, c, i);
+            if (a.has_dr) rg.fetch(ahead, stage, c, i);
+            if (FULL) {
+              ry.fetch(ahead, stage, c, i);
+              if (a.has_z) rz.fetch(ahead, stage, c, i);
+            }
+          }
+        }
+      }
+      ptx::cp_async_commit();
+    }
+  };
+  for (int i = 0; i + 1 < a.stages; ++i) fetch(i, i);
+  int turn = 0, stage = 0;
+  for (int it = 0; it < w.iters; ++it, stage = stage + 1 == a.stages ? 0 : stage + 1) {
+    fetch(it + a.stages - 1, stage == 0 ? a.stages - 1 : stage - 1);
+    if constexpr (S::kAhead) ahead.wait();
+    if (!rows_of(it)) break;                     // the whole block
+    const size_t dense = (size_t)(w.tok + it * w.step) * a.D;
+    float s[3] = {0.f, 0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < NV; ++c) {
+      const int i = (c * w.threads + w.tid) * V;
+      if (i >= a.D) continue;
+      float x[V], d[V], k[V];
+      rr.get(ahead, stage, c, i, x);
+      rd.get(ahead, stage, c, i, d);
+      if (a.w) {
+        load_run<float, V>(a.w + i, k);
+#pragma unroll
+        for (int e = 0; e < V; ++e) d[e] *= k[e];
+      }
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        s[0] = fmaf(x[e], x[e], s[0]);
+        s[1] = fmaf(d[e], x[e], s[1]);
+      }
+      if (FULL && a.post) {
+        ry.get(ahead, stage, c, i, x);
+#pragma unroll
+        for (int e = 0; e < V; ++e) s[2] = fmaf(x[e], x[e], s[2]);
+      }
+    }
+    row_sum<0, FULL ? 3 : 2>(s, red, turn);
+    const float rho = rsqrtf(fmaf(s[0], a.inv_d, a.eps)), m = s[1] * a.inv_d * rho;
+    const float py = FULL && a.post ? rsqrtf(fmaf(s[2], a.inv_d, a.eps)) : 1.f;
+    float dp[FULL ? N : 1], se[1] = {0.f};       // dp: dp wp behind a norm
+#pragma unroll
+    for (int c = 0; c < NV; ++c) {
+      const int i = (c * w.threads + w.tid) * V;
+      if (i >= a.D) continue;
+      float g[V], x[V], d[V], k[V];
+      rr.get(ahead, stage, c, i, x);
+      rd.get(ahead, stage, c, i, d);
+      if (a.has_dr) {
+        rg.get(ahead, stage, c, i, g);
+      } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) g[e] = 0.f;
+      }
+      if (a.w) {
+        load_run<float, V>(a.w + i, k);
+      } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) k[e] = 1.f;
+      }
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float u = x[e] * rho;
+        acc[0][c * V + e] = fmaf(d[e], u, acc[0][c * V + e]);
+        g[e] = fmaf(rho, fmaf(-u, m, d[e] * k[e]), g[e]);
+      }
+      store_any<V>(a.o_dr, dense + i, a.r_bf16, g);
+      if (!FULL) {
+        if (a.o_dy) {
+#pragma unroll
+          for (int e = 0; e < V; ++e) g[e] *= a.s;
+          store_any<V>(a.o_dy, dense + i, a.y_bf16, g);
+        }
+        continue;
+      }
+      if constexpr (FULL) {
+        float y[V], z[V], wp[V];
+        ry.get(ahead, stage, c, i, y);           // uy, where y is normed
+#pragma unroll
+        for (int e = 0; e < V; ++e) y[e] *= py;
+        if (a.wp) {
+          load_run<float, V>(a.wp + i, wp);
+        } else {
+#pragma unroll
+          for (int e = 0; e < V; ++e) wp[e] = 1.f;
+        }
+        if (a.has_z) rz.get(ahead, stage, c, i, z);
+        if (a.sv) load_run<float, V>(a.sv + i, k);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const int j = c * V + e;
+          float slope = 0.f;
+          const float av = a.has_z ? act(z[e], a.kind, slope) : 1.f;
+          const float p = y[e] * wp[e], gs = g[e] * (a.sv ? k[e] : a.s);
+          acc[2][j] = fmaf(g[e] * av, p, acc[2][j]);
+          z[e] = gs * p * slope;
+          const float q = gs * av;
+          acc[1][j] = fmaf(q, y[e], acc[1][j]);
+          dp[j] = q * wp[e];
+          se[0] = fmaf(dp[j], y[e], se[0]);
+        }
+        if (a.has_z) store_any<V>(a.o_dz, dense + i, a.y_bf16, z);
+        if (!a.post) store_any<V>(a.o_dy, dense + i, a.y_bf16, dp + c * V);
+      }
+    }
+    if constexpr (FULL) {
+      if (a.post) {
+        row_sum<0, 1>(se, red, turn);
+        const float my = se[0] * a.inv_d;
+#pragma unroll
+        for (int c = 0; c < NV; ++c) {
+          const int i = (c * w.threads + w.tid) * V;
+          if (i >= a.D) continue;
+          float y[V];
+          ry.get(ahead, stage, c, i, y);
+#pragma unroll
+          for (int e = 0; e < V; ++e) y[e] = py * fmaf(-y[e] * py, my, dp[c * V + e]);
+          store_any<V>(a.o_dy, dense + i, a.y_bf16, y);
+        }
+      }
+    }
+  }
+  if (!a.part) return;
+#pragma unroll
+  for (int k = 0; k < (FULL ? 3 : 1); ++k) {
+    if ((k == 1 && !a.want_p) || (k == 2 && !a.want_s)) continue;
+    float* to = a.part + ((size_t)k * gridDim.x + blockIdx.x) * a.D;
+#pragma unroll
+    for (int c = 0; c < NV; ++c) {
+      const int i = (c * w.threads + w.tid) * V;
+      if (i < a.D) store_run<float, V>(to + i, acc[k] + c * V);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ host
+constexpr int kSms = 152;
+constexpr int kWidest = 16384;                   // elements of a row at most
+constexpr int kSmemPerSm = 200 * 1024;         // of copies ahead, an SM and a block at most
+
+constexpr int kPlainSmem = 36 * 1024;            // fits beside the static part without being asked for
+
+// What a call's kernel looks like: threads of a block, groups and blocks, copies ahead.
+struct Plan {
+  int lanes, v, nv, threads, groups, blocks, rows;   // rows: of the parts, per weight
+  int pieces, stages, smem;
+};
+
+// f(Shape) for a plan.
+template <typename F>
+auto with_block(const Plan& p, F f) {
+  if (p.v == 8) return p.nv == 2 ? f(Shape<0, 8, 2>()) : f(Shape<0, 8, 4>());
+  return p.nv == 16 ? f(Shape<0, 1, 16>()) : f(Shape<0, 1, 32>());
+}
+template <typename F>
+auto with_shape(const Plan& p, F f) {
+  if (p.lanes == 0) return with_block(p, f);
+  if (p.v == 1) return f(Shape<32, 1, 8>());
+  return p.lanes == 8    ? f(Shape<8, 8, 1>())
+         : p.lanes == 16 ? f(Shape<16, 8, 1>())
+                         : f(Shape<32, 8, 1>());
+}
+
+// pieces: 16-byte pieces per run of 8, over all tensors of a row. vec: whether 16-byte accesses
+// fit. lanes_ok: whether a row may share a warp. per_sm: threads an SM is to hold.
+Plan make_plan(int tokens, int H, int D, int pieces, bool vec, bool lanes_ok, bool per_head,
+               int per_sm) {
+  Plan p = {};
+  p.v = vec ? 8 : 1;
+  p.lanes = !lanes_ok || D > 256 ? 0 : !vec || D > 128 ? 32 : D > 64 ? 16 : 8;
+  int per_block = 1;                             // groups of a block
+  if (p.lanes) {
+    p.nv = vec ? 1 : 8;
+    p.threads = 256;
+    per_block = p.threads / p.lanes;
+  } else {
+    const int two = vec ? 16 : 16;               // elements of a thread, but for the widest rows
+    p.nv = D <= kMaxThreads * two ? (vec ? 2 : 16) : (vec ? 4 : 32);
+    const int n = p.nv * p.v;
+    p.threads = ((D + n - 1) / n + 31) / 32 * 32;
+  }
+  const long long rows = (long long)tokens * H;
+  long long blocks = (rows + per_block - 1) / per_block;
+  const long long most = (long long)kSms * (per_sm / p.threads > 1 ? per_sm / p.threads : 1);
+  if (blocks > most) blocks = most;
+  const long long least = (H + per_block - 1) / per_block;     // a group per head
+  if (blocks < least) blocks = least;
+  p.blocks = (int)blocks;
+  p.groups = (int)(blocks * per_block / H * H);
+  p.rows = per_head ? p.groups / H : p.blocks;
+  p.pieces = pieces * p.nv;
+  p.stages = 1;
+  if (p.v == 8 && p.nv <= 2) {
+    const int stage = p.pieces * p.threads * 16;
+    const int resident = per_sm / p.threads > 1 ? per_sm / p.threads : 1;
+    p.stages = 3;
+    while (p.stages > 1 && (long long)p.stages * stage * resident > kSmemPerSm) --p.stages;
+    p.smem = p.stages * stage;
+  }
+  return p;
+}
+
+bool vec_view(const void* p, int dtype, int64_t b, int64_t t, int64_t h) {
+  return b % 8 == 0 && t % 8 == 0 && h % 8 == 0 && is_aligned(p, 16);
+}
+
+// Column sums of the parts, behind the kernel that writes them.
+gdr_status sum_parts(const float* part, float* o0, float* o1, float* o2, int rows, int cols,
+                     cudaStream_t s) {
+  return launch_behind(column_sum_kernel, dim3((cols + 31) / 32, o1 || o2 ? 3 : 1), 32 * kSumRows,
+                       s, part, o0, o1, o2, rows, cols);
+}
+gdr_status zero(float* p, size_t n, cudaStream_t s) {
+  return !p || n == 0 ? GDR_OK : status_of(cudaMemsetAsync(p, 0, n * sizeof(float), s));
+}
+
+bool bad_eps(float e) { return !(isfinite(e) && e > 0.f); }
+bool bad_act(int k) { return k != GDR_ACT_NONE && k != GDR_ACT_SIGMOID && k != GDR_ACT_SILU; }
+
+gdr_status check(const gdr_gated_dims* d) {
+  if (!d) return GDR_ERR_INVALID_ARG;
+  if (d->B < 0 || d->T < 0 || d->H <= 0 || d->D <= 0 || !is_dtype(d->in_dtype) ||
+      !is_dtype(d->out_dtype) || bad_act(d->activation) || bad_eps(d->eps))
+    return GDR_ERR_INVALID_ARG;
+  for (int64_t s : {d->x_stride_b, d->x_stride_t, d->x_stride_h, d->gate_stride_b,
+                    d->gate_stride_t, d->gate_stride_h})
+    if (s < 0) return GDR_ERR_INVALID_ARG;
+  if (d->D > kWidest || (long long)d->B * d->T > (1LL << 30) || d->H > (1 << 20))
+    return GDR_ERR_UNSUPPORTED;
+  return GDR_OK;
+}
+
+constexpr int kFwdPerSm = 1024, kBwdPerSm = 768;
+
+Plan gated_plan(const gdr_gated_dims* d, bool vec, bool bwd) {
+  const int in = d->in_dtype == GDR_BF16 ? 1 : 2, out = d->out_dtype == GDR_BF16 ? 1 : 2;
+  return make_plan(d->B * d->T, d->H, d->D, 2 * in + (bwd ? out : 0), vec, true,
+                   d->weight_per_head != 0, bwd ? kBwdPerSm : kFwdPerSm);
+}
+size_t gated_bytes(const gdr_gated_dims* d, const Plan& p) {
+  const size_t cols = (size_t)d->D * (d->weight_per_head ? d->H : 1);
+  return align_up((size_t)p.rows * cols * sizeof(float));
+}
+
+// Arguments that both directions share.
+gdr_status gated_args(GatedArgs& a, const gdr_gated_dims* d, const void* x, const void* gate,
+                      const float* w, bool* vec) {
+  if (!is_aligned(x, dtype_size(d->in_dtype)) || !is_aligned(gate, dtype_size(d->in_dtype)) ||
+      !is_aligned(w, 16))
+    return GDR_ERR_ALIGNMENT;
+  a.B = d->B; a.T = d->T; a.H = d->H; a.D = d->D; a.tokens = d->B * d->T;
+  // A dimension of one element is never stepped along.
+  const int64_t b = d->B > 1, t = d->T > 1, h = d->H > 1;
+  a.x = {x, b * d->x_stride_b, t * d->x_stride_t, h * d->x_stride_h};
+  a.z = {gate, b * d->gate_stride_b, t * d->gate_stride_t, h * d->gate_stride_h};
+  a.w = w;
+  a.per_head = d->weight_per_head != 0;
+  a.kind = d->activation;
+  a.first = d->gate_first != 0;
+  a.in_bf16 = d->in_dtype == GDR_BF16;
+  a.out_bf16 = d->out_dtype == GDR_BF16;
+  a.eps = d->eps;
+  a.inv_d = 1.f / d->D;
+  *vec = d->D % 8 == 0 && vec_view(x, d->in_dtype, a.x.b, a.x.t, a.x.h) &&
+         vec_view(gate, d->in_dtype, a.z.b, a.z.t, a.z.h);
+  return GDR_OK;
+}
+
+template <bool BWD>
+gdr_status launch_gated(GatedArgs& a, const Plan& p, cudaStream_t s) {
+  a.groups = p.groups;
+  a.pieces = p.pieces;
+  a.stages = p.stages;
+  return with_shape(p, [&](auto shape) {
+    using S = decltype(shape);
+    struct Tag;
+    if (p.smem > kPlainSmem && !allow_smem<Tag>(gated_kernel<S, BWD>, kSmemPerSm))
+      return GDR_ERR_CUDA;
+    return launch_kernel(gated_kernel<S, BWD>, dim3(p.blocks), p.threads, p.smem, s, a);
+  });
+}
+
+gdr_status check(const gdr_residual_dims* d) {
+  if (!d) return GDR_ERR_INVALID_ARG;
+  if (d->B < 0 || d->T < 0 || d->D <= 0 || !is_dtype(d->residual_dtype) || !is_dtype(d->y_dtype) ||
+      !is_dtype(d->out_dtype) || bad_act(d->activation) || bad_eps(d->eps) || !isfinite(d->scale))
+    return GDR_ERR_INVALID_ARG;
+  for (int64_t s : {d->residual_stride_b, d->residual_stride_t, d->y_stride_b, d->y_stride_t,
+                    d->gate_stride_b, d->gate_stride_t})
+    if (s < 0) return GDR_ERR_INVALID_ARG;
+  if (d->D > kWidest || (long long)d->B * d->T > (1LL << 30)) return GDR_ERR_UNSUPPORTED;
+  return GDR_OK;
+}
+
+// pieces: of all tensors of a row (see make_plan).
+Plan residual_plan(const gdr_residual_dims* d, bool vec, int pieces, bool bwd) {
+  return make_plan(d->B * d->T, 1, d->D, pieces, vec, false, false, bwd ? kBwdPerSm : kFwdPerSm);
+}
+
+gdr_status residual_args(ResArgs& a, const gdr_residual_dims* d, const void* r, const void* y,
+                         const void* z, const float* w, const float* wp, const float* sv,
+                         bool* vec) {
+  if (!is_aligned(r, dtype_size(d->residual_dtype)) || !is_aligned(y, dtype_size(d->y_dtype)) ||
+      !is_aligned(z, dtype_size(d->y_dtype)) || !is_aligned(w, 16) || !is_aligned(wp, 16) ||
+      !is_aligned(sv, 16))
+    return GDR_ERR_ALIGNMENT;
+  a.B = d->B; a.T = d->T; a.D = d->D; a.tokens = d->B * d->T;
+  const int64_t b = d->B > 1, t = d->T > 1;
+  a.r = {r, b * d->residual_stride_b, t * d->residual_stride_t, 0};
+  a.y = {y, b * d->y_stride_b, t * d->y_stride_t, 0};
+  a.z = {z, b * d->gate_stride_b, t * d->gate_stride_t, 0};
+  a.w = w; a.wp = wp; a.sv = sv;
+  a.has_y = y != nullptr;
+  a.has_z = z != nullptr;
+  a.post = d->post_norm != 0;
+  a.kind = d->activation;
+  a.r_bf16 = d->residual_dtype == GDR_BF16;
+  a.y_bf16 = d->y_dtype == GDR_BF16;
+  a.out_bf16 = d->out_dtype == GDR_BF16;
+  a.eps = d->eps;
+  a.inv_d = 1.f / d->D;
+  a.s = d->scale;
+  *vec = d->D % 8 == 0 && vec_view(r, d->residual_dtype, a.r.b, a.r.t, 0) &&
+         (!y || vec_view(y, d->y_dtype, a.y.b, a.y.t, 0)) &&
+         (!z || vec_view(z, d->y_dtype, a.z.b, a.z.t, 0));
+  return GDR_OK;
+}
+// A gate, a post norm or a scale per channel act on y.
+bool needs_y(const gdr_residual_dims* d, const void* z, const float* wp, const float* sv) {
+  return d->post_norm || z || wp || sv;
+}
+// wp belongs to the post norm.
+bool bad_branch(const gdr_residual_dims* d, const void* y, const void* z, const float* wp,
+                const float* sv) {
+  return (!y && needs_y(d, z, wp, sv)) || (wp && !d->post_norm);
+}
+
+}  // namespace
+}  // namespace ops
+}  // namespace gdr
+
+using namespace gdr;
+using namespace gdr::ops;
+
+extern "C" {
+
+gdr_status gdr_gated_norm(const void* x, const void* gate, const float* weight, void* y,
+                          const gdr_gated_dims* dims, gdr_stream_t stream) {
+  const gdr_status st = check(dims);
+  if (st != GDR_OK) return st;
+  GatedArgs a = {};
+  bool vec = false;
+  const gdr_status ok = gated_args(a, dims, x, gate, weight, &vec);
+  if (ok != GDR_OK) return ok;
+  if (!is_aligned(y, 16)) return GDR_ERR_ALIGNMENT;
+  if (a.tokens == 0) return GDR_OK;
+  if (!x || !gate || !y) return GDR_ERR_INVALID_ARG;
+  a.y = y;
+  return launch_gated<false>(a, gated_plan(dims, vec, false), reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t gdr_gated_norm_bwd_workspace_size(const gdr_gated_dims* dims) {
+  if (check(dims) != GDR_OK) return 0;
+  // The bases' alignment is not known here: room for either kernel.
+  const size_t v = gated_bytes(dims, gated_plan(dims, true, true));
+  const size_t o = gated_bytes(dims, gated_plan(dims, false, true));
+  const size_t most = v > o ? v : o;
+  return most ? most : kAlign;
+}
+
+gdr_status gdr_gated_norm_bwd(const void* d_y, const void* x, const void* gate, const float* weight,
+                              void* dx, void* d_gate, float* d_weight, const gdr_gated_dims* dims,
+                              void* workspace, size_t workspace_bytes, gdr_stream_t stream) {
+  const gdr_status st = check(dims);
+  if (st != GDR_OK) return st;
+  GatedArgs a = {};
+  bool vec = false;
+  const gdr_status ok = gated_args(a, dims, x, gate, weight, &vec);
+  if (ok != GDR_OK) return ok;
+  if (!is_aligned(d_y, 16) || !is_aligned(dx, 16) || !is_aligned(d_gate, 16) ||
+      !is_aligned(d_weight, 16))
+    return GDR_ERR_ALIGNMENT;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const int cols = dims->D * (a.per_head ? dims->H : 1);
+  if (a.tokens == 0) return zero(d_weight, cols, s);
+  if (!d_y || !x || !gate || !dx || !d_gate) return GDR_ERR_INVALID_ARG;
+  const Plan p = gated_plan(dims, vec, true);
+  if (d_weight) {
+    if (!workspace || workspace_bytes < gdr_gated_norm_bwd_workspace_size(dims))
+      return GDR_ERR_WORKSPACE;
+    if (!is_aligned(workspace, kAlign)) return GDR_ERR_ALIGNMENT;
+    a.part = static_cast<float*>(workspace);
+  }
+  const int64_t h = dims->D, t = h * dims->H;
+  a.d = {d_y, t * dims->T, t, h};
+  a.dx = dx;
+  a.dz = d_gate;
+  const gdr_status run = launch_gated<true>(a, p, s);
+  if (run != GDR_OK || !d_weight) return run;
+  return sum_parts(a.part, d_weight, nullptr, nullptr, p.rows, cols, s);
+}
+
+gdr_status gdr_residual_norm(const void* residual, const void* y, const void* gate,
+                             const float* weight, const float* post_weight, const float* scale,
+                             void* residual_out, void* out, const gdr_residual_dims* dims,
+                             gdr_stream_t stream) {
+  const gdr_status st = check(dims);
+  if (st != GDR_OK) return st;
+  ResArgs a = {};
+  bool vec = false;
+  const gdr_status ok =
+      residual_args(a, dims, residual, y, gate, weight, post_weight, scale, &vec);
+  if (ok != GDR_OK) return ok;
+  if (!is_aligned(residual_out, 16) || !is_aligned(out, 16)) return GDR_ERR_ALIGNMENT;
+  if (a.tokens == 0) return GDR_OK;
+  if (!residual || !out || bad_branch(dims, y, gate, post_weight, scale) || !y != !residual_out)
+    return GDR_ERR_INVALID_ARG;
+  a.out = out;
+  a.r_out = residual_out;
+  const int re = a.r_bf16 ? 1 : 2, ye = a.y_bf16 ? 1 : 2;
+  const Plan p = residual_plan(dims, vec, re + a.has_y * ye + a.has_z * ye, false);
+  a.pieces = p.pieces;
+  a.stages = p.stages;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return with_block(p, [&](auto shape) {
+    using S = decltype(shape);
+    struct Tag;
+    if (p.smem > kPlainSmem && !allow_smem<Tag>(residual_fwd_kernel<S>, kSmemPerSm))
+      return GDR_ERR_CUDA;
+    return launch_kernel(residual_fwd_kernel<S>, dim3(p.blocks), p.threads, p.smem, s, a);
+  });
+}
+
+size_t gdr_residual_norm_bwd_workspace_size(const gdr_residual_dims* dims) {
+  if (check(dims) != GDR_OK) return 0;
+  const Plan v = residual_plan(dims, true, 1, true), o = residual_plan(dims, false, 1, true);
+  const size_t rows = v.rows > o.rows ? v.rows : o.rows;
+  const size_t bytes = align_up(3 * rows * dims->D * sizeof(float));
+  return bytes ? bytes : kAlign;
+}
+
+gdr_status gdr_residual_norm_bwd(const void* d_out, const void* d_residual_out,
+                                 const void* residual_out, const void* y, const void* gate,
+                                 const float* weight, const float* post_weight, const float* scale,
+                                 void* d_residual, void* d_y, void* d_gate, float* d_weight,
+                                 float* d_post_weight, float* d_scale,
+                                 const gdr_residual_dims* dims, void* workspace,
+                                 size_t workspace_bytes, gdr_stream_t stream) {
+  const gdr_status st = check(dims);
+  if (st != GDR_OK) return st;
+  ResArgs a = {};
+  bool vec = false;
+  const gdr_status ok =
+      residual_args(a, dims, residual_out, y, gate, weight, post_weight, scale, &vec);
+  if (ok != GDR_OK) return ok;
+  for (const void* p : {d_out, d_residual_out, static_cast<const void*>(d_residual),
+                        static_cast<const void*>(d_y), static_cast<const void*>(d_gate),
+                        static_cast<const void*>(d_weight), static_cast<const void*>(d_post_weight),
+                        static_cast<const void*>(d_scale)})
+    if (!is_aligned(p, 16)) return GDR_ERR_ALIGNMENT;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (a.tokens == 0) {
+    for (float* p : {d_weight, d_post_weight, d_scale}) {
+      const gdr_status z = zero(p, dims->D, s);
+      if (z != GDR_OK) return z;
+    }
+    return GDR_OK;
+  }
+  const bool full = needs_y(dims, gate, post_weight, scale);
+  if (!d_out || !residual_out || !d_residual || (full && !y) || (post_weight && !dims->post_norm) ||
+      (full && !d_y) || !gate != !d_gate || (d_post_weight && !dims->post_norm) ||
+      (d_scale && !scale))
+    return GDR_ERR_INVALID_ARG;
+  a.has_dr = d_residual_out != nullptr;
+  const int re = a.r_bf16 ? 1 : 2, ye = a.y_bf16 ? 1 : 2, oe = a.out_bf16 ? 1 : 2;
+  const int pieces = re * (1 + a.has_dr) + oe + (full ? ye * (1 + a.has_z) : 0);
+  const Plan p = residual_plan(dims, vec, pieces, true);
+  if (d_weight || d_post_weight || d_scale) {
+    if (!workspace || workspace_bytes < gdr_residual_norm_bwd_workspace_size(dims))
+      return GDR_ERR_WORKSPACE;
+    if (!is_aligned(workspace, kAlign)) return GDR_ERR_ALIGNMENT;
+    a.part = static_cast<float*>(workspace);
+  }
+  a.want_p = d_post_weight != nullptr;
+  a.want_s = d_scale != nullptr;
+  const int64_t t = dims->D;
+  a.d = {d_out, t * dims->T, t, 0};
+  a.dr = {d_residual_out, t * dims->T, t, 0};
+  a.o_dr = d_residual;
+  a.o_dy = d_y;
+  a.o_dz = d_gate;
+  a.pieces = p.pieces;
+  a.stages = p.stages;
+  const gdr_status run = with_block(p, [&](auto shape) {
+    using S = decltype(shape);
+    auto go = [&](auto* fn, auto* tag) {
+      if (p.smem > kPlainSmem && !allow_smem<std::remove_pointer_t<decltype(tag)>>(fn, kSmemPerSm))
+        return GDR_ERR_CUDA;
+      return launch_kernel(fn, dim3(p.blocks), p.threads, p.smem, s, a);
+    };
+    struct Full;
+    struct Plain;
+    return full ? go(residual_bwd_kernel<S, true>, static_cast<Full*>(nullptr))
+                : go(residual_bwd_kernel<S, false>, static_cast<Plain*>(nullptr));
+  });
+  if (run != GDR_OK || !a.part) return run;
+  return sum_parts(a.part, d_weight, d_post_weight, d_scale, p.rows, dims->D, s);
+}
+
+}  // extern "C"

@@ -1,0 +1,260 @@
+// gdr_norm.cuh -- what the norm kernels around a layer share: rows of a norm held in the
+// registers of a group of lanes or of a block, their copies ahead of time, sums over a row,
+// gate activations, and the column sums of the weights' gradients.
+#pragma once
+
+#include "gdr_ops.cuh"
+#include "gdr_ptx.cuh"
+
+namespace gdr {
+namespace ops {
+namespace {
+
+// Who holds a row, and how. LANES > 0: that many lanes of a warp (8, 16 or 32), several rows
+// per warp. LANES == 0: a whole block, whose size follows the row's. A thread holds NV runs of
+// V consecutive elements; run c of thread i starts at element (c threads + i) V. V is 8 where
+// sizes, strides and bases allow 16-byte accesses, else 1.
+template <int LANES_, int V_, int NV_>
+struct Shape {
+  static constexpr int LANES = LANES_, V = V_, NV = NV_, N = V_ * NV_;
+  // Copies ahead of time go through shared memory, 16 bytes at a time. Rows past 8192 elements
+  // (NV beyond 2 runs of 8) are loaded when they are needed.
+  static constexpr bool kAhead = V_ == 8 && NV_ <= 2;
+};
+
+// V consecutive elements as raw words.
+template <typename T, int V>
+struct Run {
+  uint32_t w[V * sizeof(T) / 4];
+};
+template <>
+struct Run<bf16, 1> {
+  bf16 v;
+};
+
+template <typename T, int V>
+__device__ __forceinline__ void unpack(const Run<T, V>& r, float* f) {
+  if constexpr (V == 1) {
+    if constexpr (sizeof(T) == 2)
+      f[0] = __bfloat162float(r.v);
+    else
+      f[0] = __uint_as_float(r.w[0]);
+  } else if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      const float2 p = unpack2(r.w[i]);
+      f[2 * i] = p.x;
+      f[2 * i + 1] = p.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = __uint_as_float(r.w[i]);
+  }
+}
+template <typename T, int V>
+__device__ __forceinline__ void load_run(const T* p, float* f) {
+  Run<T, V> r;
+  if constexpr (V == 1 && sizeof(T) == 2) {
+    r.v = *p;
+  } else if constexpr (V == 1) {
+    r.w[0] = __float_as_uint(*p);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V * (int)sizeof(T) / 16; ++i) {
+      const uint4 u = reinterpret_cast<const uint4*>(p)[i];
+      r.w[4 * i] = u.x;
+      r.w[4 * i + 1] = u.y;
+      r.w[4 * i + 2] = u.z;
+      r.w[4 * i + 3] = u.w;
+    }
+  }
+  unpack<T, V>(r, f);
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_run(T* p, const float* f) {
+  if constexpr (V == 1) {
+    if constexpr (sizeof(T) == 2)
+      *p = __float2bfloat16_rn(f[0]);
+    else
+      *p = f[0];
+  } else if constexpr (sizeof(T) == 2) {
+    *reinterpret_cast<uint4*>(p) =
+        make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+  } else {
+    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+  }
+}
+// The same with the type known at run time only.
+template <int V>
+__device__ __forceinline__ void load_any(const void* p, int64_t i, int is_bf16, float* f) {
+  if (is_bf16)
+    load_run<bf16, V>(static_cast<const bf16*>(p) + i, f);
+  else
+    load_run<float, V>(static_cast<const float*>(p) + i, f);
+}
+template <int V>
+__device__ __forceinline__ void store_any(void* p, int64_t i, int is_bf16, const float* f) {
+  if (is_bf16)
+    store_run<bf16, V>(static_cast<bf16*>(p) + i, f);
+  else
+    store_run<float, V>(static_cast<float*>(p) + i, f);
+}
+
+// act(z) and its derivative.
+enum Act { kNone = GDR_ACT_NONE, kSigmoid = GDR_ACT_SIGMOID, kSilu = GDR_ACT_SILU };
+__device__ __forceinline__ float act(float z, int kind) {
+  if (kind == kNone) return z;
+  const float g = __fdividef(1.f, 1.f + __expf(-z));
+  return kind == kSigmoid ? g : z * g;
+}
+__device__ __forceinline__ float act(float z, int kind, float& slope) {
+  if (kind == kNone) {
+    slope = 1.f;
+    return z;
+  }
+  const float g = __fdividef(1.f, 1.f + __expf(-z)), h = 1.f - g;
+  slope = kind == kSigmoid ? g * h : fmaf(z * g, h, g);
+  return kind == kSigmoid ? g : z * g;
+}
+
+// Sums of K values over a row's threads, known to all of them. A block's sums meet in `red`
+// (two halves, taken in turn, so that one barrier per sum is enough).
+struct Red {
+  float v[2][3][32];
+};
+template <int LANES, int K>
+__device__ __forceinline__ void row_sum(float* s, Red& red, int& turn) {
+  constexpr int FIRST = LANES ? LANES / 2 : 16;
+#pragma unroll
+  for (int o = FIRST; o > 0; o >>= 1)
+#pragma unroll
+    for (int k = 0; k < K; ++k) s[k] += __shfl_xor_sync(~0u, s[k], o);
+  if constexpr (LANES == 0) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    if (warps > 1) {
+      if (lane < K) {
+        float mine = s[0];
+#pragma unroll
+        for (int k = 1; k < K; ++k) mine = lane == k ? s[k] : mine;
+        red.v[turn][lane][warp] = mine;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        s[k] = lane < warps ? red.v[turn][k][lane] : 0.f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s[k] += __shfl_xor_sync(~0u, s[k], o);
+      }
+      turn ^= 1;
+    }
+  }
+}
+
+// Which rows a group takes: rows are (token, head); a group keeps one head, so that the sums
+// for that head's weights stay in its registers, and takes every step-th token.
+struct Walk {
+  int head, tok, step, iters, tid, threads;      // tok: the first; tid of `threads` in the group
+  bool on;                                       // whether the group has a head at all
+};
+template <int LANES>
+__device__ __forceinline__ Walk walk_of(int tokens, int H, int groups) {
+  Walk w;
+  w.threads = LANES ? LANES : blockDim.x;
+  w.tid = LANES ? threadIdx.x % (LANES ? LANES : 1) : threadIdx.x;
+  const int gid = LANES ? blockIdx.x * (blockDim.x / (LANES ? LANES : 1)) + threadIdx.x / (LANES ? LANES : 1)
+                        : blockIdx.x;
+  w.on = gid < groups;                           // groups: a multiple of H
+  w.head = gid % H;
+  w.tok = gid / H;
+  w.step = groups / H;
+  w.iters = (tokens + w.step - 1) / w.step;      // of every group alike; rows past the end idle
+  return w;
+}
+
+// A strided view [B, T, H, D] or a dense one.
+struct View {
+  const void* p;
+  int64_t b, t, h;
+  __device__ int64_t at(int bi, int ti, int head) const { return bi * b + ti * t + head * h; }
+};
+
+// A group's copies ahead of time: every thread's own pieces of 16 bytes, in its own places of
+// shared memory, so that no barrier is needed between a copy and its use.
+struct Ahead {
+  char* base;                                    // [stages][pieces][threads of the block] x 16 bytes
+  int pieces, stages;
+  __device__ __forceinline__ char* place(int stage, int piece) const {
+    return base + ((size_t)(stage * pieces + piece) * blockDim.x + threadIdx.x) * 16;
+  }
+  __device__ __forceinline__ void wait() const {
+    if (stages == 3)
+      ptx::cp_async_wait<2>();
+    else if (stages == 2)
+      ptx::cp_async_wait<1>();
+    else
+      ptx::cp_async_wait<0>();
+  }
+};
+
+// One tensor of a row. With S::kAhead its runs come from the thread's places in shared memory,
+// from `first` on, where fetch() had them copied; without, from global memory.
+template <class S>
+struct Row {
+  const void* p;                                 // the row's first element
+  int is_bf16, first;                            // first: its first piece within a stage
+  __device__ __forceinline__ int per_run() const { return is_bf16 ? 1 : 2; }
+  __device__ __forceinline__ void fetch(const Ahead& a, int stage, int c, int i) const {
+    const char* src = static_cast<const char*>(p) + (size_t)i * (is_bf16 ? 2 : 4);
+    const int at = first + c * per_run();
+    ptx::cp_async16(ptx::smem_u32(a.place(stage, at)), src, 16);
+    if (!is_bf16) ptx::cp_async16(ptx::smem_u32(a.place(stage, at + 1)), src + 16, 16);
+  }
+  __device__ __forceinline__ void get(const Ahead& a, int stage, int c, int i, float* f) const {
+    if constexpr (S::kAhead) {
+      const int at = first + c * per_run();
+      const uint4 u = *reinterpret_cast<const uint4*>(a.place(stage, at));
+      if (is_bf16) {
+        const Run<bf16, 8> r = {{u.x, u.y, u.z, u.w}};
+        unpack<bf16, 8>(r, f);
+      } else {
+        const uint4 v = *reinterpret_cast<const uint4*>(a.place(stage, at + 1));
+        const Run<float, 8> r = {{u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w}};
+        unpack<float, 8>(r, f);
+      }
+    } else {
+      load_any<S::V>(p, i, is_bf16, f);
+    }
+  }
+};
+
+// Column sums of part [which][rows][cols] into out<which>.
+constexpr int kSumRows = 32;
+__global__ void __launch_bounds__(32 * kSumRows) column_sum_kernel(const float* part, float* out0,
+                                                                   float* out1, float* out2,
+                                                                   int rows, int cols) {
+  __shared__ float s[kSumRows][33];
+  asm volatile("griddepcontrol.wait;" ::: "memory");       // the parts are written
+  const int lane = threadIdx.x & 31, r0 = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane, which = blockIdx.y;
+  float* out = which == 0 ? out0 : which == 1 ? out1 : out2;
+  if (!out) return;
+  const float* p = part + (size_t)which * rows * cols;
+  float v = 0.f;
+  if (c < cols) {
+#pragma unroll 4
+    for (int r = r0; r < rows; r += kSumRows) v += p[(size_t)r * cols + c];
+  }
+  s[r0][lane] = v;
+  __syncthreads();
+  if (r0 == 0) {
+    v = 0.f;
+#pragma unroll
+    for (int r = 0; r < kSumRows; ++r) v += s[r][lane];
+    if (c < cols) out[c] = v;
+  }
+}
+
+}  // namespace
+}  // namespace ops
+}  // namespace gdr

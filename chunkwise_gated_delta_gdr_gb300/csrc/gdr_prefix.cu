@@ -1,0 +1,400 @@
+// gdr_prefix.cu -- attention of one new token per sequence, for a batch whose sequences share a
+// prompt: one softmax over the shared keys [0, P) and each sequence's own paged keys.
+//
+// The queries of all sequences that read one key-value head are the rows of a matrix product
+// with the shared keys, which are read once for all of them instead of once per sequence. Over a
+// stretch of keys, with a running maximum m per row (base 2: scores carry a factor log2(e)),
+//   s = scale q . k,  p = 2^(s - m),  l = sum p,  o = sum p v
+// and stretches join as  m = max m_i,  l = sum l_i 2^(m_i - m),  o likewise. A sequence's own
+// keys are one more stretch (paged_decode_attn's result and its lse).
+//
+// Partition. An item is one (key-value head, tile of rows); its keys are cut into tiles. All
+// tiles of the call, item after item, form one line that the blocks share out equally; each
+// block leaves one part per item of its stretch, and a last kernel joins the parts of a row.
+#include "gdr_prefix.cuh"
+
+namespace gdr {
+namespace ops {
+namespace {
+
+// ------------------------------------------------------------ fp32 arithmetic, any type
+// 64 rows x 64 keys a step: scores as 4 x 4 per thread from shared memory, then the rows'
+// softmax by four lanes each, then 4 rows x (D / 16) channels per thread of the product with V.
+constexpr int RM = 64, KT = 64, NT = 256;
+template <int NJ>                                // channels in runs of 64: D <= 64 NJ
+struct AnySmem {
+  static constexpr int DP = NJ * 64, LD = DP + 4, LS = KT + 4;
+  float q[RM * LD], k[KT * LD], v[KT * LD], s[RM * LS];
+  float factor[RM];
+  int bad;
+};
+
+template <typename T, int NJ>
+__global__ void __launch_bounds__(NT) prefix_any_kernel(PrefixArgs a, int vec) {
+  extern __shared__ __align__(16) char raw[];
+  typedef AnySmem<NJ> Smem;
+  constexpr int DP = Smem::DP, LD = Smem::LD, LS = Smem::LS;
+  Smem& sm = *reinterpret_cast<Smem*>(raw);
+  const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15, warp = tid >> 5, lane = tid & 31;
+  Stretch st = stretch_of(a, blockIdx.x);
+  if (tid == 0) sm.bad = 0;
+  while (st.left > 0) {
+    const int hk = st.item / a.row_tiles, r0 = (st.item - hk * a.row_tiles) * RM;
+    __syncthreads();                             // the last item's tiles are done with
+    for (int r = warp; r < RM; r += NT / 32) {
+      const int m = r0 + r;
+      const int64_t at = m < a.M ? q_row(a, hk, m) : 0;
+      for (int d = lane; d < DP; d += 32) {
+        float v = 0.f;
+        if (m < a.M && d < a.D)
+          v = a.scale2 * (a.q_bf16 ? __bfloat162float(static_cast<const bf16*>(a.q)[at + d])
+                                   : static_cast<const float*>(a.q)[at + d]);
+        sm.q[r * LD + d] = v;
+      }
+    }
+    float o[4][NJ * 4], m = -INFINITY, l = 0.f;  // m, l: of row tid / 4
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < NJ * 4; ++j) o[i][j] = 0.f;
+    const int last = min(a.tiles, st.tile + st.left);
+    const T* kc = static_cast<const T*>(a.kc) + hk * a.ph;
+    const T* vc = static_cast<const T*>(a.vc) + hk * a.ph;
+    for (int t = st.tile; t < last; ++t) {
+      for (int r = warp; r < KT; r += NT / 32) {
+        const int j = t * KT + r;
+        const int64_t row = j < a.P ? prefix_row(a, j) : 0;
+        const bool live = j < a.P && row >= 0;
+        if (j < a.P && row < 0) sm.bad = 1;
+        for (int d = 4 * lane; d < DP; d += 128) {
+          float kv[4], vv[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) kv[e] = vv[e] = 0.f;
+          if (live && vec) {
+            if (d < a.D) {
+              load_f<T, 4>(kc + row + d, kv);
+              load_f<T, 4>(vc + row + d, vv);
+            }
+          } else if (live) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (d + e < a.D) {
+                kv[e] = static_cast<float>(kc[row + d + e]);
+                vv[e] = static_cast<float>(vc[row + d + e]);
+              }
+          }
+          *reinterpret_cast<float4*>(&sm.k[r * LD + d]) = make_float4(kv[0], kv[1], kv[2], kv[3]);
+          *reinterpret_cast<float4*>(&sm.v[r * LD + d]) = make_float4(vv[0], vv[1], vv[2], vv[3]);
+        }
+      }
+      __syncthreads();
+      float2 acc[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = make_float2(0.f, 0.f);
+#pragma unroll 4
+      for (int d = 0; d < DP; d += 4) {
+        float4 qv[4], kv[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          qv[i] = *reinterpret_cast<const float4*>(&sm.q[(ty + 16 * i) * LD + d]);
+          kv[i] = *reinterpret_cast<const float4*>(&sm.k[(tx + 16 * i) * LD + d]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            acc[i][j] = fma2(make_float2(qv[i].x, qv[i].y), make_float2(kv[j].x, kv[j].y), acc[i][j]);
+            acc[i][j] = fma2(make_float2(qv[i].z, qv[i].w), make_float2(kv[j].z, kv[j].w), acc[i][j]);
+          }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          sm.s[(ty + 16 * i) * LS + tx + 16 * j] =
+              t * KT + tx + 16 * j < a.P ? acc[i][j].x + acc[i][j].y : -INFINITY;
+      __syncthreads();
+      {                                          // four lanes per row, every fourth key each
+        float* row = sm.s + (tid >> 2) * LS + (tid & 3);
+        float top = m;
+#pragma unroll
+        for (int j = 0; j < KT; j += 4) top = fmaxf(top, row[j]);
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+        const float f = top > m ? exp2f(m - top) : 1.f;    // 0 from -inf
+        const float base = top == -INFINITY ? 0.f : top;
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < KT; j += 4) {
+          const float w = exp2f(row[j] - base);
+          row[j] = w;
+          sum += w;
+        }
+        m = top;
+        l = fmaf(l, f, sum);                     // of this lane's keys; the four meet at the end
+        if ((tid & 3) == 0) sm.factor[tid >> 2] = f;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float f = sm.factor[ty + 16 * i];
+#pragma unroll
+        for (int j = 0; j < NJ * 4; ++j) o[i][j] *= f;
+      }
+#pragma unroll 2
+      for (int k = 0; k < KT; k += 4) {
+        float4 p[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          p[i] = *reinterpret_cast<const float4*>(&sm.s[(ty + 16 * i) * LS + k]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) {
+            const float4 v = *reinterpret_cast<const float4*>(&sm.v[(k + e) * LD + 64 * j + 4 * tx]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float w = e == 0 ? p[i].x : e == 1 ? p[i].y : e == 2 ? p[i].z : p[i].w;
+              float2* oo = reinterpret_cast<float2*>(&o[i][4 * j]);
+              oo[0] = fma2(make_float2(w, w), make_float2(v.x, v.y), oo[0]);
+              oo[1] = fma2(make_float2(w, w), make_float2(v.z, v.w), oo[1]);
+            }
+          }
+      }
+      __syncthreads();
+    }
+    l += __shfl_xor_sync(~0u, l, 1);
+    l += __shfl_xor_sync(~0u, l, 2);
+    const size_t part = part_of(a, st.item, blockIdx.x) * RM;
+    if ((tid & 3) == 0) {
+      a.part_ml[(part + (tid >> 2)) * 2] = m;
+      a.part_ml[(part + (tid >> 2)) * 2 + 1] = sm.bad ? NAN : l;   // a bad page poisons the row
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (r0 + ty + 16 * i < a.M)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int d = 64 * j + 4 * tx + e;
+            if (d < a.D) a.part_o[(part + ty + 16 * i) * a.D + d] = o[i][4 * j + e];
+          }
+    st.left -= last - st.tile;
+    st.tile = 0;
+    ++st.item;
+  }
+}
+
+// ------------------------------------------------------------ joining the stretches
+// A warp per query head of a sequence: the shared keys' parts in order, then its own keys.
+constexpr int JW = 4;
+template <int V>
+__global__ void __launch_bounds__(JW * 32) prefix_join_kernel(PrefixArgs a) {
+  constexpr int N = 256 / (32 * V);
+  const int lane = threadIdx.x & 31;
+  const long long row = (long long)blockIdx.x * JW + (threadIdx.x >> 5);
+  if (row >= (long long)a.B * a.HQ) return;
+  const int b = (int)(row / a.HQ), hq = (int)(row - (long long)b * a.HQ);
+  const int hk = hq / a.G, r = b * a.G + hq - hk * a.G;
+  const int item = hk * a.row_tiles + r / a.rows, in = r % a.rows;
+  const int parts = parts_of(a, item);
+  const size_t first = ((size_t)item * a.max_parts) * a.rows + in;
+  const float own = a.own_lse[row] * LOG2E;
+  float m = own;
+  for (int c = lane; c < parts; c += 32)
+    m = fmaxf(m, a.part_ml[(first + (size_t)c * a.rows) * 2]);
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, x));
+  const float base = m == -INFINITY ? 0.f : m;
+  float l = exp2f(own - base), o[N][V];          // 0 without keys, NaN where they are bad
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int ch = (lane + 32 * i) * V;
+    if (ch < a.D) {
+      load_f<float, V>(a.own_o + (size_t)row * a.D + ch, o[i]);
+#pragma unroll
+      for (int k = 0; k < V; ++k) o[i][k] *= l;
+    }
+  }
+#pragma unroll 4
+  for (int c = 0; c < parts; ++c) {
+    const size_t at = first + (size_t)c * a.rows;
+    const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + at * 2);
+    const float f = exp2f(ml.x - base);
+    l = fmaf(f, ml.y, l);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int ch = (lane + 32 * i) * V;
+      if (ch < a.D) {
+        float v[V];
+        load_f<float, V>(a.part_o + at * a.D + ch, v);
+#pragma unroll
+        for (int k = 0; k < V; ++k) o[i][k] = fmaf(f, v[k], o[i][k]);
+      }
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int ch = (lane + 32 * i) * V;
+    if (ch < a.D) {
+#pragma unroll
+      for (int k = 0; k < V; ++k) o[i][k] = l == 0.f ? 0.f : o[i][k] * inv;
+      if (a.out_bf16)
+        store_f<bf16, V>(static_cast<bf16*>(a.out) + (size_t)row * a.D + ch, o[i]);
+      else
+        store_f<float, V>(static_cast<float*>(a.out) + (size_t)row * a.D + ch, o[i]);
+    }
+  }
+  if (lane == 0 && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
+}
+
+// ------------------------------------------------------------ host
+constexpr int kSms = 152;
+
+// How the shared keys of a call are cut up.
+struct Plan {
+  int rows, keys;                                // of a tile
+  int row_tiles, tiles, blocks, per, max_parts;
+  size_t o_bytes, ml_bytes, own_bytes, lse_bytes, decode_bytes;
+  size_t bytes() const { return o_bytes + ml_bytes + own_bytes + lse_bytes + decode_bytes; }
+};
+
+Plan make_plan(const gdr_attn_dims* d, const gdr_paged_cache* c, int P) {
+  Plan p = {};
+  p.decode_bytes = gdr_paged_decode_attn_workspace_size(d, c);
+  if (P == 0) return p;                          // no shared keys: paged_decode_attn's own work
+  const int G = d->HQ / c->HK;
+  const long long M = (long long)d->B * G;
+  p.rows = RM;
+  p.keys = KT;
+  const int resident = c->D <= 64 ? 2 : 1;
+  p.row_tiles = (int)((M + p.rows - 1) / p.rows);
+  p.tiles = (P + p.keys - 1) / p.keys;
+  const long long total = (long long)p.row_tiles * c->HK * p.tiles;
+  const long long most = (long long)kSms * resident;
+  p.blocks = (int)(total < most ? total : most);
+  p.per = (int)((total + p.blocks - 1) / p.blocks);
+  p.blocks = (int)((total + p.per - 1) / p.per);
+  p.max_parts = (p.tiles - 1) / p.per + 2;
+  const size_t rows = (size_t)p.row_tiles * c->HK * p.max_parts * p.rows;
+  p.o_bytes = align_up(rows * c->D * sizeof(float));
+  p.ml_bytes = align_up(rows * 2 * sizeof(float));
+  p.own_bytes = align_up((size_t)d->B * d->HQ * c->D * sizeof(float));
+  p.lse_bytes = align_up((size_t)d->B * d->HQ * sizeof(float));
+  return p;
+}
+
+gdr_status check(const gdr_attn_dims* d, const gdr_paged_cache* c, int prefix_pages, int P) {
+  if (!d) return GDR_ERR_INVALID_ARG;
+  const gdr_status st = check_cache(c);
+  if (st != GDR_OK) return st;
+  if (d->B < 0 || d->HQ <= 0 || d->HQ % c->HK != 0 || !is_dtype(d->q_dtype) ||
+      !is_dtype(d->out_dtype) || d->window != 0 || d->q_stride_b < 0 || d->q_stride_h < 0 ||
+      !(isfinite(d->scale) && d->scale > 0.f) || prefix_pages < 0 || P < 0 ||
+      P > (long long)prefix_pages * c->page_size)
+    return GDR_ERR_INVALID_ARG;
+  if (d->HQ > (1 << 20) || (long long)d->B * d->HQ > (1LL << 30) || P > (1 << 30))
+    return GDR_ERR_UNSUPPORTED;
+  // Tiles of the line, of 64 rows and keys: counts of them stay within an int.
+  if (((double)d->B * d->HQ / 64 + c->HK) * ((double)P / 64 + 1) > (double)(1LL << 37))
+    return GDR_ERR_UNSUPPORTED;
+  return GDR_OK;
+}
+
+template <typename T, int NJ>
+gdr_status launch_any(const PrefixArgs& a, int vec, int blocks, cudaStream_t s) {
+  struct Tag;
+  if (!allow_smem<Tag>(prefix_any_kernel<T, NJ>, sizeof(AnySmem<NJ>))) return GDR_ERR_CUDA;
+  return launch_kernel(prefix_any_kernel<T, NJ>, dim3(blocks), NT, sizeof(AnySmem<NJ>), s, a, vec);
+}
+
+}  // namespace
+}  // namespace ops
+}  // namespace gdr
+
+using namespace gdr;
+using namespace gdr::ops;
+
+extern "C" {
+
+size_t gdr_paged_prefix_attn_workspace_size(const gdr_attn_dims* dims, const gdr_paged_cache* cache,
+                                            int prefix_pages, int prefix_len) {
+  if (check(dims, cache, prefix_pages, prefix_len) != GDR_OK) return 0;
+  return make_plan(dims, cache, prefix_len).bytes();
+}
+
+gdr_status gdr_paged_prefix_attn(const void* q, const void* k_cache, const void* v_cache,
+                                 const int32_t* prefix_table, int prefix_pages, int prefix_len,
+                                 const int32_t* page_table, const int32_t* lens, void* out,
+                                 float* lse, const gdr_attn_dims* dims,
+                                 const gdr_paged_cache* cache, void* workspace,
+                                 size_t workspace_bytes, gdr_stream_t stream) {
+  const gdr_status st = check(dims, cache, prefix_pages, prefix_len);
+  if (st != GDR_OK) return st;
+  if (!is_aligned(q, dtype_size(dims->q_dtype)) || !is_aligned(k_cache, 16) ||
+      !is_aligned(v_cache, 16) || !is_aligned(page_table, 4) || !is_aligned(prefix_table, 4) ||
+      !is_aligned(lens, 4) || !is_aligned(out, 16) || !is_aligned(lse, 16))
+    return GDR_ERR_ALIGNMENT;
+  if (dims->B == 0) return GDR_OK;
+  if (!q || !lens || !out || !has_arrays(cache, k_cache, v_cache, page_table) ||
+      (prefix_pages > 0 && !prefix_table))
+    return GDR_ERR_INVALID_ARG;
+  const Plan p = make_plan(dims, cache, prefix_len);
+  if (!workspace || workspace_bytes < p.bytes()) return GDR_ERR_WORKSPACE;
+  if (!is_aligned(workspace, kAlign)) return GDR_ERR_ALIGNMENT;
+  if (prefix_len == 0)
+    return gdr_paged_decode_attn(q, k_cache, v_cache, page_table, lens, out, lse, dims, cache,
+                                 workspace, workspace_bytes, stream);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  char* at = static_cast<char*>(workspace);
+  PrefixArgs a = {};
+  a.part_o = reinterpret_cast<float*>(at);
+  a.part_ml = reinterpret_cast<float*>(at += p.o_bytes);
+  a.own_o = reinterpret_cast<float*>(at += p.ml_bytes);
+  a.own_lse = reinterpret_cast<float*>(at += p.own_bytes);
+  void* decode_ws = at += p.lse_bytes;
+  a.q = q;
+  a.kc = k_cache ? k_cache : workspace;          // never read without pages
+  a.vc = v_cache ? v_cache : workspace;
+  a.table = prefix_table;
+  a.out = out;
+  a.lse = lse;
+  a.B = dims->B; a.HQ = dims->HQ; a.HK = cache->HK; a.D = cache->D;
+  a.G = dims->HQ / cache->HK;
+  a.M = dims->B * a.G;
+  a.P = prefix_len;
+  a.rows = p.rows; a.row_tiles = p.row_tiles; a.tiles = p.tiles; a.per = p.per;
+  a.blocks = p.blocks; a.max_parts = p.max_parts;
+  a.page = cache->page_size;
+  a.num_pages = cache->num_pages;
+  a.out_bf16 = dims->out_dtype == GDR_BF16;
+  a.q_bf16 = dims->q_dtype == GDR_BF16;
+  a.scale2 = dims->scale * LOG2E;
+  a.qb = a.B > 1 ? dims->q_stride_b : 0;
+  a.qh = a.HQ > 1 ? dims->q_stride_h : 0;
+  a.pp = cache->page_stride; a.pt = cache->token_stride; a.ph = cache->head_stride;
+
+  const int vec = a.D % 4 == 0 && a.pp % 4 == 0 && a.pt % 4 == 0 && a.ph % 4 == 0;
+  gdr_status run = with_dtype(cache->dtype, [&](auto* t) {
+    using T = std::remove_pointer_t<decltype(t)>;
+    return a.D <= 64    ? launch_any<T, 1>(a, vec, p.blocks, s)
+           : a.D <= 128 ? launch_any<T, 2>(a, vec, p.blocks, s)
+           : a.D <= 192 ? launch_any<T, 3>(a, vec, p.blocks, s)
+                        : launch_any<T, 4>(a, vec, p.blocks, s);
+  });
+  if (run != GDR_OK) return run;
+  gdr_attn_dims own = *dims;
+  own.out_dtype = GDR_F32;
+  run = gdr_paged_decode_attn(q, k_cache, v_cache, page_table, lens, a.own_o, a.own_lse, &own,
+                              cache, decode_ws, p.decode_bytes, stream);
+  if (run != GDR_OK) return run;
+  const long long rows = (long long)a.B * a.HQ;
+  return launch_kernel(a.D % 4 == 0 ? prefix_join_kernel<4> : prefix_join_kernel<1>,
+                       dim3((unsigned)((rows + JW - 1) / JW)), JW * 32, 0, s, a);
+}
+
+}  // extern "C"

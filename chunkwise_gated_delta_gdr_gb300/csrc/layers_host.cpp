@@ -453,10 +453,281 @@ PyObject* paged_decode_attn(PyObject*, PyObject* const* arg, Py_ssize_t n) {
   });
 }
 
+// (q, k_cache, v_cache, prefix_table, prefix_len, page_table, lens, scale or None, out, lse,
+//  workspace)
+PyObject* paged_prefix_attn(PyObject*, PyObject* const* arg, Py_ssize_t n) {
+  if (n != 11) Py_RETURN_NONE;
+  return guarded([&]() -> PyObject* {
+    Call c;
+    const Tensor *q = c.get(arg[0]), *kc = c.get(arg[1]), *vc = c.get(arg[2]), *px = c.get(arg[3]);
+    const Tensor *pt = c.get(arg[5]), *lens = c.get(arg[6]), *out = c.get(arg[8], true);
+    const Tensor *lse = c.get(arg[9], true), *ws = c.get(arg[10], true);
+    if (!c.ok || q->dim() != 3 || px->dim() != 1) Py_RETURN_NONE;
+    const int64_t B = q->size(0), HQ = q->size(1), D = q->size(2);
+    gdr_paged_cache p = {};
+    if (!read_cache(c, p, kc, vc, pt, B)) Py_RETURN_NONE;
+    c.view(q, {B, HQ, (int64_t)p.D});
+    c.dense(px, {px->size(0)}, at::kInt);
+    c.dense(lens, {B}, at::kInt);
+    const int pages = fit(px->size(0), c), prefix = integer(arg[4], c);
+    gdr_attn_dims d = {};
+    d.B = fit(B, c); d.HQ = fit(HQ, c);
+    d.q_dtype = c.float_code(q);
+    d.out_dtype = out ? c.float_code(out) : d.q_dtype;
+    d.scale = arg[7] == Py_None ? (float)(1.0 / std::sqrt((double)D)) : (float)number(arg[7], c);
+    const auto type = out ? out->scalar_type() : q->scalar_type();
+    c.dense(out, {B, HQ, D}, type);
+    c.dense(lse, {B, HQ});
+    if (ws) c.need(ws->scalar_type() == at::kByte && ws->is_contiguous());
+    if (!c.ready() || prefix < 0) Py_RETURN_NONE;
+    d.q_stride_b = q->stride(0); d.q_stride_h = q->stride(1);
+    Tensor made_out, made_lse, made_ws;
+    if (!out) out = &(made_out = c.empty({B, HQ, D}, type));
+    if (!lse) lse = &(made_lse = c.empty({B, HQ}, at::kFloat));
+    if (!ws) {
+      const size_t size = gdr_paged_prefix_attn_workspace_size(&d, &p, pages, prefix);
+      if (!size) Py_RETURN_NONE;
+      ws = &(made_ws = c.empty({(int64_t)size}, at::kByte));
+    }
+    PyObject* results = tuple_of(result(arg[8], made_out), result(arg[9], made_lse));
+    if (!results) return none();
+    return answer(results,
+                  gdr_paged_prefix_attn(q->data_ptr(), kc->data_ptr(), vc->data_ptr(),
+                                        px->data_ptr<int32_t>(), pages, prefix,
+                                        pt->data_ptr<int32_t>(), lens->data_ptr<int32_t>(),
+                                        out->data_ptr(), lse->data_ptr<float>(), &d, &p,
+                                        ws->data_ptr(), ws->numel(), c.stream()));
+  });
+}
+
+// x, gate, weight, activation, gate_first, eps of the two gated norm calls.
+struct Gated {
+  gdr_gated_dims d = {};
+  const Tensor *x, *z;
+  const float* w = nullptr;
+  int64_t B = 0, T = 0, H = 0, D = 0;
+  bool read(Call& c, PyObject* const* arg) {
+    x = c.get(arg[0]);
+    z = c.get(arg[1]);
+    const Tensor* tw = c.get(arg[2], true);
+    if (!c.ok || x->dim() != 4) return false;
+    B = x->size(0); T = x->size(1); H = x->size(2); D = x->size(3);
+    c.view(x, {B, T, H, D});
+    c.view(z, {B, T, H, D});
+    c.need(x->scalar_type() == z->scalar_type());
+    d.weight_per_head = tw && tw->dim() == 2;
+    w = static_cast<const float*>(d.weight_per_head ? c.dense(tw, {H, D}) : c.dense(tw, {D}));
+    d.B = fit(B, c); d.T = fit(T, c); d.H = fit(H, c); d.D = fit(D, c);
+    d.in_dtype = c.float_code(x);
+    d.activation = integer(arg[3], c);
+    d.gate_first = truth(arg[4], c);
+    d.eps = (float)number(arg[5], c);
+    if (!c.ok) return false;
+    d.x_stride_b = x->stride(0); d.x_stride_t = x->stride(1); d.x_stride_h = x->stride(2);
+    d.gate_stride_b = z->stride(0); d.gate_stride_t = z->stride(1); d.gate_stride_h = z->stride(2);
+    return true;
+  }
+};
+
+// (x, gate, weight, activation, gate_first, eps, out)
+PyObject* gated_norm(PyObject*, PyObject* const* arg, Py_ssize_t n) {
+  if (n != 7) Py_RETURN_NONE;
+  return guarded([&]() -> PyObject* {
+    Call c;
+    Gated a;
+    const Tensor* out = c.get(arg[6], true);
+    if (!a.read(c, arg)) Py_RETURN_NONE;
+    const auto type = out ? out->scalar_type() : a.x->scalar_type();
+    a.d.out_dtype = out ? c.float_code(out) : a.d.in_dtype;
+    c.dense(out, {a.B, a.T, a.H, a.D}, type);
+    if (!c.ready()) Py_RETURN_NONE;
+    Tensor made;
+    if (!out) out = &(made = c.empty({a.B, a.T, a.H, a.D}, type));
+    PyObject* results = result(arg[6], made);
+    if (!results) return none();
+    return answer(results, gdr_gated_norm(a.x->data_ptr(), a.z->data_ptr(), a.w, out->data_ptr(),
+                                          &a.d, c.stream()));
+  });
+}
+
+// (d_out, x, gate, weight, activation, gate_first, eps, dx, d_gate, output_weight_grad, workspace)
+PyObject* gated_norm_bwd(PyObject*, PyObject* const* arg, Py_ssize_t n) {
+  if (n != 11) Py_RETURN_NONE;
+  return guarded([&]() -> PyObject* {
+    Call c;
+    Gated a;
+    const Tensor *dy = c.get(arg[0]), *dx = c.get(arg[7], true), *dz = c.get(arg[8], true);
+    const Tensor* ws = c.get(arg[10], true);
+    if (!c.ok || !a.read(c, arg + 1)) Py_RETURN_NONE;
+    const bool want = truth(arg[9], c);
+    const at::IntArrayRef shape = a.x->sizes();
+    const auto type = a.x->scalar_type();
+    a.d.out_dtype = c.float_code(dy);
+    c.dense(dy, shape, dy->scalar_type());
+    c.dense(dx, shape, type);
+    c.dense(dz, shape, type);
+    if (ws) c.need(ws->scalar_type() == at::kByte && ws->is_contiguous());
+    if (!c.ready()) Py_RETURN_NONE;
+    Tensor made_dx, made_dz, made_dw, made_ws;
+    if (!dx) dx = &(made_dx = c.empty(shape, type));
+    if (!dz) dz = &(made_dz = c.empty(shape, type));
+    if (want) {
+      if (a.d.weight_per_head)
+        made_dw = c.empty({a.H, a.D}, at::kFloat);
+      else
+        made_dw = c.empty({a.D}, at::kFloat);
+      if (!ws) {
+        const size_t size = gdr_gated_norm_bwd_workspace_size(&a.d);
+        if (!size) Py_RETURN_NONE;
+        ws = &(made_ws = c.empty({(int64_t)size}, at::kByte));
+      }
+    }
+    PyObject* results = tuple_of(result(arg[7], made_dx), result(arg[8], made_dz),
+                                 result(Py_None, made_dw));
+    if (!results) return none();
+    return answer(results,
+                  gdr_gated_norm_bwd(dy->data_ptr(), a.x->data_ptr(), a.z->data_ptr(), a.w,
+                                     dx->data_ptr(), dz->data_ptr(),
+                                     want ? made_dw.data_ptr<float>() : nullptr, &a.d,
+                                     ws ? ws->data_ptr() : nullptr, ws ? ws->numel() : 0,
+                                     c.stream()));
+  });
+}
+
+// residual, y, weight, gate, activation, post_norm, post_weight, scale, eps of the two calls.
+struct Residual {
+  gdr_residual_dims d = {};
+  const Tensor *r, *y, *z;
+  const float *w = nullptr, *wp = nullptr, *s = nullptr;
+  int64_t B = 0, T = 0, D = 0;
+  bool read(Call& c, PyObject* const* arg) {
+    r = c.get(arg[0]);
+    y = c.get(arg[1], true);
+    z = c.get(arg[3], true);
+    const Tensor *tw = c.get(arg[2], true), *tp = c.get(arg[6], true), *ts = nullptr;
+    d.scale = 1.f;
+    if (THPVariable_Check(arg[7]))
+      ts = c.get(arg[7]);
+    else
+      d.scale = (float)number(arg[7], c);
+    d.activation = integer(arg[4], c);
+    d.post_norm = truth(arg[5], c);
+    d.eps = (float)number(arg[8], c);
+    if (!c.ok || r->dim() != 3) return false;
+    B = r->size(0); T = r->size(1); D = r->size(2);
+    c.view(r, {B, T, D});
+    d.residual_dtype = c.float_code(r);
+    d.y_dtype = GDR_F32;
+    if (y) {
+      c.view(y, {B, T, D});
+      d.y_dtype = c.float_code(y);
+      d.y_stride_b = y->stride(0);
+      d.y_stride_t = y->stride(1);
+    } else {
+      c.need(!z && !d.post_norm && !ts);
+    }
+    if (z && y) {
+      c.view(z, {B, T, D});
+      c.need(z->scalar_type() == y->scalar_type());
+      d.gate_stride_b = z->stride(0);
+      d.gate_stride_t = z->stride(1);
+    }
+    c.need(!tp || d.post_norm);
+    w = static_cast<const float*>(c.dense(tw, {D}));
+    wp = static_cast<const float*>(c.dense(tp, {D}));
+    s = static_cast<const float*>(c.dense(ts, {D}));
+    d.B = fit(B, c); d.T = fit(T, c); d.D = fit(D, c);
+    if (!c.ok) return false;
+    d.residual_stride_b = r->stride(0);
+    d.residual_stride_t = r->stride(1);
+    return true;
+  }
+};
+const void* address(const Tensor* t) { return t ? t->data_ptr() : nullptr; }
+void* address_to(const Tensor* t) { return t ? t->data_ptr() : nullptr; }
+
+// (residual, y, weight, gate, activation, post_norm, post_weight, scale, eps, out, residual_out)
+PyObject* residual_norm(PyObject*, PyObject* const* arg, Py_ssize_t n) {
+  if (n != 11) Py_RETURN_NONE;
+  return guarded([&]() -> PyObject* {
+    Call c;
+    Residual a;
+    const Tensor *out = c.get(arg[9], true), *ro = c.get(arg[10], true);
+    if (!a.read(c, arg) || (!a.y && ro)) Py_RETURN_NONE;
+    const at::IntArrayRef shape = a.r->sizes();
+    const auto type = (out ? out : a.y ? a.y : a.r)->scalar_type();
+    a.d.out_dtype = c.float_code(out ? out : a.y ? a.y : a.r);
+    c.dense(out, shape, type);
+    c.dense(ro, shape, a.r->scalar_type());
+    if (!c.ready()) Py_RETURN_NONE;
+    Tensor made_out, made_ro;
+    if (!out) out = &(made_out = c.empty(shape, type));
+    if (a.y && !ro) ro = &(made_ro = c.empty(shape, a.r->scalar_type()));
+    PyObject* results = tuple_of(result(arg[9], made_out),
+                                 a.y ? result(arg[10], made_ro) : Py_NewRef(arg[0]));
+    if (!results) return none();
+    return answer(results, gdr_residual_norm(a.r->data_ptr(), address(a.y), address(a.z), a.w, a.wp,
+                                             a.s, address_to(ro), out->data_ptr(), &a.d,
+                                             c.stream()));
+  });
+}
+
+// (d_out, d_residual_out, residual_out, y, weight, gate, activation, post_norm, post_weight,
+//  scale, eps, d_residual, d_y, d_gate, output_weight_grads, workspace)
+PyObject* residual_norm_bwd(PyObject*, PyObject* const* arg, Py_ssize_t n) {
+  if (n != 16) Py_RETURN_NONE;
+  return guarded([&]() -> PyObject* {
+    Call c;
+    Residual a;
+    const Tensor *go = c.get(arg[0]), *gr = c.get(arg[1], true), *dr = c.get(arg[11], true);
+    const Tensor *dy = c.get(arg[12], true), *dz = c.get(arg[13], true), *ws = c.get(arg[15], true);
+    if (!c.ok || !a.read(c, arg + 2) || (dy && !a.y) || (dz && !a.z)) Py_RETURN_NONE;
+    const bool want = truth(arg[14], c);
+    const at::IntArrayRef shape = a.r->sizes();
+    const auto rt = a.r->scalar_type();
+    a.d.out_dtype = c.float_code(go);
+    c.dense(go, shape, go->scalar_type());
+    c.dense(gr, shape, rt);
+    c.dense(dr, shape, rt);
+    if (a.y) c.dense(dy, shape, a.y->scalar_type());
+    if (a.z) c.dense(dz, shape, a.z->scalar_type());
+    if (ws) c.need(ws->scalar_type() == at::kByte && ws->is_contiguous());
+    if (!c.ready()) Py_RETURN_NONE;
+    Tensor made_dr, made_dy, made_dz, made_w, made_p, made_s, made_ws;
+    if (!dr) dr = &(made_dr = c.empty(shape, rt));
+    if (!dy && a.y) dy = &(made_dy = c.empty(shape, a.y->scalar_type()));
+    if (!dz && a.z) dz = &(made_dz = c.empty(shape, a.z->scalar_type()));
+    if (want) {
+      made_w = c.empty({a.D}, at::kFloat);
+      if (a.d.post_norm) made_p = c.empty({a.D}, at::kFloat);
+      if (a.s) made_s = c.empty({a.D}, at::kFloat);
+      if (!ws) {
+        const size_t size = gdr_residual_norm_bwd_workspace_size(&a.d);
+        if (!size) Py_RETURN_NONE;
+        ws = &(made_ws = c.empty({(int64_t)size}, at::kByte));
+      }
+    }
+    PyObject* results = tuple_of(result(arg[11], made_dr), result(arg[12], made_dy),
+                                 result(arg[13], made_dz), result(Py_None, made_w),
+                                 result(Py_None, made_p), result(Py_None, made_s));
+    if (!results) return none();
+    const auto vec = [](const Tensor& t) { return t.defined() ? t.data_ptr<float>() : nullptr; };
+    return answer(results,
+                  gdr_residual_norm_bwd(go->data_ptr(), address(gr), a.r->data_ptr(), address(a.y),
+                                        address(a.z), a.w, a.wp, a.s, dr->data_ptr(),
+                                        address_to(dy), address_to(dz), vec(made_w), vec(made_p),
+                                        vec(made_s), &a.d, want && ws ? ws->data_ptr() : nullptr,
+                                        want && ws ? ws->numel() : 0, c.stream()));
+  });
+}
+
 #define FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST(linear_scan_fwd),     FAST(linear_scan_bwd),
                          FAST(qk_norm_rope),        FAST(qk_norm_rope_bwd),
                          FAST(qk_norm_rope_append), FAST(paged_decode_attn),
+                         FAST(paged_prefix_attn),   FAST(gated_norm),
+                         FAST(gated_norm_bwd),      FAST(residual_norm),
+                         FAST(residual_norm_bwd),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_layers_host", nullptr, -1, methods,
                       nullptr,               nullptr,        nullptr, nullptr};

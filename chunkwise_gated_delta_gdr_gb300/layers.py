@@ -1,5 +1,6 @@
 """Entry points of a decoder's other layers: gated linear recurrence, q/k norm with
-rotation, paged key-value cache and its decode attention.
+rotation, paged key-value cache and its decode attention (for a batch behind a shared prompt
+too), and the norms around a layer.
 
 The same thin binding as the rest of the package: tensors' pointers, sizes and strides go
 into the C ABI (``include/gdr.h``), status codes come back as exceptions, all arithmetic
@@ -50,6 +51,20 @@ class gdr_attn_dims(ctypes.Structure):
                [("scale", _f), ("q_stride_b", _l), ("q_stride_h", _l)]
 
 
+class gdr_gated_dims(ctypes.Structure):
+    _fields_ = [(n, _i) for n in ("B", "T", "H", "D", "in_dtype", "out_dtype", "activation",
+                                  "gate_first", "weight_per_head")] + \
+               [("eps", _f)] + \
+               [(f"{n}_stride_{d}", _l) for n in ("x", "gate") for d in "bth"]
+
+
+class gdr_residual_dims(ctypes.Structure):
+    _fields_ = [(n, _i) for n in ("B", "T", "D", "residual_dtype", "y_dtype", "out_dtype",
+                                  "activation", "post_norm")] + \
+               [("eps", _f), ("scale", _f)] + \
+               [(f"{n}_stride_{d}", _l) for n in ("residual", "y", "gate") for d in "bt"]
+
+
 _bound = None
 
 
@@ -67,6 +82,12 @@ def _lib():
             "gdr_qk_norm_rope_append": [_p] * 12 + [P(gdr_qk_dims), P(gdr_paged_cache), _p],
             "gdr_paged_decode_attn": [_p] * 7 + [P(gdr_attn_dims), P(gdr_paged_cache), _p, _z,
                                                  _p],
+            "gdr_paged_prefix_attn": [_p] * 4 + [_i, _i] + [_p] * 4 + [
+                P(gdr_attn_dims), P(gdr_paged_cache), _p, _z, _p],
+            "gdr_gated_norm": [_p] * 4 + [P(gdr_gated_dims), _p],
+            "gdr_gated_norm_bwd": [_p] * 7 + [P(gdr_gated_dims), _p, _z, _p],
+            "gdr_residual_norm": [_p] * 8 + [P(gdr_residual_dims), _p],
+            "gdr_residual_norm_bwd": [_p] * 14 + [P(gdr_residual_dims), _p, _z, _p],
         }
         for name, args in sigs.items():
             fn = getattr(lib, name)
@@ -75,6 +96,9 @@ def _lib():
             "gdr_linear_scan_checkpoints_size": [P(gdr_scan_dims)],
             "gdr_qk_norm_rope_bwd_workspace_size": [P(gdr_qk_dims)],
             "gdr_paged_decode_attn_workspace_size": [P(gdr_attn_dims), P(gdr_paged_cache)],
+            "gdr_paged_prefix_attn_workspace_size": [P(gdr_attn_dims), P(gdr_paged_cache), _i, _i],
+            "gdr_gated_norm_bwd_workspace_size": [P(gdr_gated_dims)],
+            "gdr_residual_norm_bwd_workspace_size": [P(gdr_residual_dims)],
         }
         for name, args in sizes.items():
             fn = getattr(lib, name)
@@ -542,3 +566,287 @@ def paged_decode_attn(q, k_cache, v_cache, page_table, lens, *, scale: Optional[
         cache, ws, ws_bytes, raw)
     _raise(st, "gdr_paged_decode_attn")
     return out, lse
+
+
+# ------------------------------------------------------------------ attention behind a shared prompt
+def _prefix_args(prefix_table, prefix_len, device):
+    if prefix_table.dim() != 1:
+        raise ValueError("prefix_table must be [pages]")
+    if not isinstance(prefix_len, int) or prefix_len < 0:
+        raise ValueError("prefix_len must be an int, 0 or more")
+    at = _dense("prefix_table", prefix_table, prefix_table.shape, device, torch.int32)
+    pages = prefix_table.shape[0]
+    if max(pages, prefix_len) >= 1 << 31:
+        raise ValueError(f"prefix_len = {prefix_len} is out of range")
+    return at, pages, prefix_len
+
+
+def paged_prefix_attn_workspace_size(q, k_cache, prefix_table, prefix_len, page_table) -> int:
+    """Bytes of scratch that paged_prefix_attn needs for these sizes."""
+    dims, cache = _attn_dims(q, k_cache, k_cache, page_table, None, 0, GDR_F32)
+    _, pages, n = _prefix_args(prefix_table, prefix_len, q.device)
+    size = _lib().gdr_paged_prefix_attn_workspace_size(dims, cache, pages, n)
+    if size == 0:
+        raise GdrError(GDR_ERR_INVALID_ARG, "gdr_paged_prefix_attn_workspace_size")
+    return size
+
+
+def paged_prefix_attn(q, k_cache, v_cache, prefix_table, prefix_len, page_table, lens, *,
+                      scale: Optional[float] = None, out_dtype=None, out=None, lse=None,
+                      workspace=None, stream=None):
+    """paged_decode_attn for a batch whose sequences share a prompt, whose keys are read once
+    for all of them.
+
+    prefix_table int32 [pages]: the prompt's pages in order, in the same caches; prefix_len
+    (an int): its keys. Every sequence attends to them and, behind them, to its own keys:
+    page_table [B, max_pages] and lens [B] describe those alone. The rest as for
+    paged_decode_attn, without a window. A shared page out of range gives NaN everywhere.
+    """
+    if stream is None and out_dtype is None and _host is not None:
+        r = _host.paged_prefix_attn(q, k_cache, v_cache, prefix_table, prefix_len, page_table,
+                                    lens, scale, out, lse, workspace)
+        if r is not None:
+            if type(r) is int:
+                _raise(r, "gdr_paged_prefix_attn")
+            return r
+    shape, device = q.shape, q.device
+    raw = _stream(device, stream)
+    if out is None:
+        out = _empty(shape, out_dtype or q.dtype, device, stream)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError(f"out must be {out_dtype}, got {out.dtype}")
+    dims, cache = _attn_dims(q, k_cache, v_cache, page_table, scale, 0, _code("out", out))
+    prefix, pages, n = _prefix_args(prefix_table, prefix_len, device)
+    if lse is None:
+        lse = _empty(shape[:2], torch.float32, device, stream)
+    lib = _lib()
+    if workspace is None:
+        size = lib.gdr_paged_prefix_attn_workspace_size(dims, cache, pages, n)
+        workspace = _empty((max(size, 256),), torch.uint8, device, stream)
+    ws, ws_bytes = _scratch(workspace, device)
+    st = lib.gdr_paged_prefix_attn(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), prefix, pages, n,
+        page_table.data_ptr(), _dense("lens", lens, shape[:1], device, torch.int32),
+        _dense("out", out, shape, device, out.dtype), _dense("lse", lse, shape[:2], device), dims,
+        cache, ws, ws_bytes, raw)
+    _raise(st, "gdr_paged_prefix_attn")
+    return out, lse
+
+
+# ------------------------------------------------------------------ norms around a layer
+_ACT = {"none": 0, "sigmoid": 1, "silu": 2}
+
+
+def _activation(name):
+    code = _ACT.get(name)
+    if code is None:
+        raise ValueError(f"activation must be one of {', '.join(_ACT)}, got {name!r}")
+    return code
+
+
+def _gated_dims(x, gate, weight, activation, gate_first, eps, out_code):
+    if x.dim() != 4:
+        raise ValueError("x must be [B, T, H, D]")
+    B, T, H, D = x.shape
+    _view("x", x, x.shape, x.device)
+    _view("gate", gate, x.shape, x.device)
+    if gate.dtype != x.dtype:
+        raise TypeError("x and gate must have one dtype")
+    per_head = weight is not None and weight.dim() == 2
+    shape = (H, D) if per_head else (D,)
+    w = _dense("weight", weight, shape, x.device)
+    return _struct(gdr_gated_dims, B, T, H, D, _code("x", x), out_code, _activation(activation),
+                   bool(gate_first), per_head, eps, *x.stride()[:3], *gate.stride()[:3]), w, shape
+
+
+def gated_norm(x, gate, weight=None, *, activation: str = "silu", gate_first: bool = False,
+               eps: float = 1e-6, out_dtype=None, out=None, stream=None):
+    """The RMS norm of a layer's output heads with the layer's output gate, in one pass.
+
+    x, gate [B,T,H,D] (bf16 or fp32, one dtype, views allowed); weight fp32 [D], [H,D] or
+    None (ones). Returns norm(x) weight a(gate), or with ``gate_first`` norm(x a(gate))
+    weight, of out_dtype (default x's). activation a: "silu", "sigmoid" or "none" (the gate
+    itself).
+    """
+    if stream is None and out_dtype is None and _host is not None:
+        r = _host.gated_norm(x, gate, weight, _ACT.get(activation), gate_first, eps, out)
+        if r is not None:
+            if type(r) is int:
+                _raise(r, "gdr_gated_norm")
+            return r
+    device = x.device
+    raw = _stream(device, stream)
+    if out is None:
+        out = _empty(x.shape, out_dtype or x.dtype, device, stream)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError(f"out must be {out_dtype}, got {out.dtype}")
+    dims, w, _ = _gated_dims(x, gate, weight, activation, gate_first, eps, _code("out", out))
+    st = _lib().gdr_gated_norm(x.data_ptr(), gate.data_ptr(), w,
+                               _dense("out", out, x.shape, device, out.dtype), dims, raw)
+    _raise(st, "gdr_gated_norm")
+    return out
+
+
+def gated_norm_bwd(d_out, x, gate, weight=None, *, activation: str = "silu",
+                   gate_first: bool = False, eps: float = 1e-6, dx=None, d_gate=None,
+                   output_weight_grad: bool = True, workspace=None, stream=None):
+    """Gradients of gated_norm: d_out [B,T,H,D] (dense, of the output's dtype), the rest as in
+    the forward call. Returns (dx, d_gate, d_weight): dense, of x's dtype, and fp32 of
+    weight's shape, [D] without one (None with output_weight_grad=False)."""
+    if stream is None and _host is not None:
+        r = _host.gated_norm_bwd(d_out, x, gate, weight, _ACT.get(activation), gate_first, eps, dx,
+                                 d_gate, output_weight_grad, workspace)
+        if r is not None:
+            if type(r) is int:
+                _raise(r, "gdr_gated_norm_bwd")
+            return r
+    shape, device = x.shape, x.device
+    raw = _stream(device, stream)
+    dims, w, wshape = _gated_dims(x, gate, weight, activation, gate_first, eps,
+                                  _code("d_out", d_out))
+    if dx is None:
+        dx = _empty(shape, x.dtype, device, stream)
+    if d_gate is None:
+        d_gate = _empty(shape, x.dtype, device, stream)
+    dw, ws, ws_bytes = None, None, 0
+    lib = _lib()
+    if output_weight_grad:
+        dw = _empty(wshape, torch.float32, device, stream)
+        if workspace is None:
+            size = lib.gdr_gated_norm_bwd_workspace_size(dims)
+            workspace = _empty((max(size, 256),), torch.uint8, device, stream)
+        ws, ws_bytes = _scratch(workspace, device)
+    st = lib.gdr_gated_norm_bwd(
+        _dense("d_out", d_out, shape, device, d_out.dtype), x.data_ptr(), gate.data_ptr(), w,
+        _dense("dx", dx, shape, device, x.dtype), _dense("d_gate", d_gate, shape, device, x.dtype),
+        None if dw is None else dw.data_ptr(), dims, ws, ws_bytes, raw)
+    _raise(st, "gdr_gated_norm_bwd")
+    return dx, d_gate, dw
+
+
+def _residual_dims(residual, y, gate, weight, post_norm, post_weight, scale, activation, eps,
+                   out_code):
+    if residual.dim() != 3:
+        raise ValueError("residual must be [B, T, D]")
+    shape, device = residual.shape, residual.device
+    B, T, D = shape
+    _view("residual", residual, shape, device)
+    ys = gs = (0, 0)
+    ycode = GDR_F32
+    vector = isinstance(scale, torch.Tensor)
+    if y is not None:
+        _view("y", y, shape, device)
+        ys, ycode = y.stride(), _code("y", y)
+    elif gate is not None or post_norm or vector:
+        raise ValueError("gate, post_norm and a scale per channel need y")
+    if gate is not None:
+        _view("gate", gate, shape, device)
+        if gate.dtype != y.dtype:
+            raise TypeError("y and gate must have one dtype")
+        gs = gate.stride()
+    if post_weight is not None and not post_norm:
+        raise ValueError("post_weight needs post_norm")
+    rs = residual.stride()
+    dims = _struct(gdr_residual_dims, B, T, D, _code("residual", residual), ycode, out_code,
+                   _activation(activation), bool(post_norm), eps, 1.0 if vector else float(scale),
+                   rs[0], rs[1], ys[0], ys[1], gs[0], gs[1])
+    return dims, (None if y is None else y.data_ptr(), None if gate is None else gate.data_ptr(),
+                  _dense("weight", weight, (D,), device),
+                  _dense("post_weight", post_weight, (D,), device),
+                  _dense("scale", scale, (D,), device) if vector else None)
+
+
+def residual_norm(residual, y=None, weight=None, *, gate=None, activation: str = "sigmoid",
+                  post_norm: bool = False, post_weight=None, scale=1.0, eps: float = 1e-6,
+                  out_dtype=None, out=None, residual_out=None, stream=None):
+    """What lies between two layers, in one pass: residual_out = residual + scale a(gate) p, p
+    the layer's output y or, with ``post_norm``, its RMS norm times post_weight, and out =
+    RMS norm of residual_out times weight, for the next layer.
+
+    residual, y, gate [B,T,D] (bf16 or fp32, y and gate one dtype, views allowed); weight,
+    post_weight fp32 [D] or None (ones); scale a number or fp32 [D]; activation as in
+    gated_norm. Without y only the norm is taken. Returns (out of out_dtype, default y's or
+    else residual's; residual_out of residual's dtype, residual itself without y).
+    ``residual_out`` may be residual where that is dense.
+    """
+    if stream is None and out_dtype is None and _host is not None:
+        r = _host.residual_norm(residual, y, weight, gate, _ACT.get(activation), post_norm,
+                                post_weight, scale, eps, out, residual_out)
+        if r is not None:
+            if type(r) is int:
+                _raise(r, "gdr_residual_norm")
+            return r
+    shape, device = residual.shape, residual.device
+    raw = _stream(device, stream)
+    if out is None:
+        out = _empty(shape, out_dtype or (residual if y is None else y).dtype, device, stream)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError(f"out must be {out_dtype}, got {out.dtype}")
+    dims, (py, pg, pw, pp, ps) = _residual_dims(residual, y, gate, weight, post_norm, post_weight,
+                                                scale, activation, eps, _code("out", out))
+    if y is None:
+        if residual_out is not None and residual_out is not residual:
+            raise ValueError("residual_out needs y")
+        residual_out = None
+    elif residual_out is None:
+        residual_out = _empty(shape, residual.dtype, device, stream)
+    st = _lib().gdr_residual_norm(
+        residual.data_ptr(), py, pg, pw, pp, ps,
+        _dense("residual_out", residual_out, shape, device, residual.dtype),
+        _dense("out", out, shape, device, out.dtype), dims, raw)
+    _raise(st, "gdr_residual_norm")
+    return out, residual if y is None else residual_out
+
+
+def residual_norm_bwd(d_out, d_residual_out, residual_out, y=None, weight=None, *, gate=None,
+                      activation: str = "sigmoid", post_norm: bool = False, post_weight=None,
+                      scale=1.0, eps: float = 1e-6, d_residual=None, d_y=None, d_gate=None,
+                      output_weight_grads: bool = True, workspace=None, stream=None):
+    """Gradients of residual_norm: d_out and d_residual_out [B,T,D] (dense, of out's and
+    residual's dtype; d_residual_out or None), residual_out as the forward call returned it,
+    the rest as in that call. Returns (d_residual, d_y, d_gate, d_weight, d_post_weight,
+    d_scale): the first three dense, of their inputs' dtypes, the others fp32 [D]; None for
+    what the call does not have (no y, no gate, no post_norm, a number as scale), and for
+    the last three with output_weight_grads=False."""
+    if stream is None and _host is not None:
+        r = _host.residual_norm_bwd(d_out, d_residual_out, residual_out, y, weight, gate,
+                                    _ACT.get(activation), post_norm, post_weight, scale, eps,
+                                    d_residual, d_y, d_gate, output_weight_grads, workspace)
+        if r is not None:
+            if type(r) is int:
+                _raise(r, "gdr_residual_norm_bwd")
+            return r
+    shape, device = residual_out.shape, residual_out.device
+    raw = _stream(device, stream)
+    dims, (py, pg, pw, pp, ps) = _residual_dims(residual_out, y, gate, weight, post_norm,
+                                                post_weight, scale, activation, eps,
+                                                _code("d_out", d_out))
+    if y is None and d_y is not None or gate is None and d_gate is not None:
+        raise ValueError("d_y and d_gate belong to y and gate")
+    rt = residual_out.dtype
+    if d_residual is None:
+        d_residual = _empty(shape, rt, device, stream)
+    if d_y is None and y is not None:
+        d_y = _empty(shape, y.dtype, device, stream)
+    if d_gate is None and gate is not None:
+        d_gate = _empty(shape, gate.dtype, device, stream)
+    want = output_weight_grads
+    D = shape[2:]
+    vectors = [_empty(D, torch.float32, device, stream) if on else None
+               for on in (want, want and post_norm, want and ps is not None)]
+    ws, ws_bytes = None, 0
+    lib = _lib()
+    if want:
+        if workspace is None:
+            size = lib.gdr_residual_norm_bwd_workspace_size(dims)
+            workspace = _empty((max(size, 256),), torch.uint8, device, stream)
+        ws, ws_bytes = _scratch(workspace, device)
+    st = lib.gdr_residual_norm_bwd(
+        _dense("d_out", d_out, shape, device, d_out.dtype),
+        _dense("d_residual_out", d_residual_out, shape, device, rt), residual_out.data_ptr(), py,
+        pg, pw, pp, ps, _dense("d_residual", d_residual, shape, device, rt),
+        _dense("d_y", d_y, shape, device, None if d_y is None else y.dtype),
+        _dense("d_gate", d_gate, shape, device, None if d_gate is None else gate.dtype),
+        *[None if v is None else v.data_ptr() for v in vectors], dims, ws, ws_bytes, raw)
+    _raise(st, "gdr_residual_norm_bwd")
+    return (d_residual, d_y, d_gate, *vectors)

@@ -547,6 +547,149 @@ gdr_status gdr_paged_decode_attn(const void* q, const void* k_cache, const void*
 size_t gdr_paged_decode_attn_workspace_size(const gdr_attn_dims* dims,
                                             const gdr_paged_cache* cache);
 
+/*
+ * gdr_paged_prefix_attn -- gdr_paged_decode_attn for a batch whose sequences share a prompt.
+ * Every sequence's keys are the prompt's, 0 .. prefix_len - 1, and behind them its own:
+ * one softmax over both. The shared keys are read once for the whole batch, as one matrix
+ * product of all its queries, instead of once per sequence.
+ *
+ *   prefix_table  (device) int32 [prefix_pages]: the prompt's pages in order, in the same
+ *                 arrays k_cache and v_cache; NULL with prefix_pages == 0
+ *   prefix_len    keys of the prompt, 0 <= prefix_len <= prefix_pages page_size
+ *   page_table, lens  (device) the pages and the number of each sequence's own keys
+ *   dims->window  has to be 0
+ *   workspace     (device) gdr_paged_prefix_attn_workspace_size() bytes, 256-byte aligned
+ *
+ * The rest as for gdr_paged_decode_attn. A shared page outside [0, num_pages) gives NaN in
+ * every sequence, an own one or a bad length in its sequence. The result does not depend on
+ * the order in which blocks run.
+ */
+gdr_status gdr_paged_prefix_attn(const void* q, const void* k_cache, const void* v_cache,
+                                 const int32_t* prefix_table, int prefix_pages, int prefix_len,
+                                 const int32_t* page_table, const int32_t* lens, void* out,
+                                 float* lse, const gdr_attn_dims* dims,
+                                 const gdr_paged_cache* cache, void* workspace,
+                                 size_t workspace_bytes, gdr_stream_t stream);
+size_t gdr_paged_prefix_attn_workspace_size(const gdr_attn_dims* dims, const gdr_paged_cache* cache,
+                                            int prefix_pages, int prefix_len);
+
+/* Activations of a gate: a(z) = z, 1 / (1 + exp(-z)) or z / (1 + exp(-z)). */
+#define GDR_ACT_NONE 0
+#define GDR_ACT_SIGMOID 1
+#define GDR_ACT_SILU 2
+
+/*
+ * gdr_gated_norm -- the RMS norm of a recurrent layer's output heads with the layer's
+ * output gate, in one pass. For each row x of D channels and its gate row z
+ *     y = x / sqrt(mean(x^2) + eps) * weight * a(z)              (gate_first 0)
+ *     y = v / sqrt(mean(v^2) + eps) * weight,  v = x a(z)        (gate_first nonzero)
+ * All of it is fp32, rounded once to out_dtype.
+ *
+ *   x, gate   (device) [B, T, H, D] in_dtype, strides below
+ *   weight    (device) fp32 [D], [H, D] with weight_per_head, or NULL (ones)
+ *   y         (device) [B, T, H, D] out_dtype, dense
+ *
+ * D <= 16384, B T <= 2^30.
+ */
+typedef struct {
+  int B, T, H, D;
+  int in_dtype;         /* gdr_dtype of x, gate (and dx, d_gate) */
+  int out_dtype;        /* gdr_dtype of y (and d_y) */
+  int activation;       /* GDR_ACT_* */
+  int gate_first;       /* 0: the gate multiplies the normed row; nonzero: the row, before */
+  int weight_per_head;  /* 0: weight [D]; nonzero: [H, D] */
+  float eps;            /* finite, > 0 */
+  int64_t x_stride_b, x_stride_t, x_stride_h;  /* elements */
+  int64_t gate_stride_b, gate_stride_t, gate_stride_h;
+} gdr_gated_dims;
+
+gdr_status gdr_gated_norm(const void* x, const void* gate, const float* weight, void* y,
+                          const gdr_gated_dims* dims, gdr_stream_t stream);
+
+/*
+ * gdr_gated_norm_bwd -- gradients of gdr_gated_norm.
+ *
+ *   d_y         (device) [B, T, H, D] out_dtype, dense
+ *   dx, d_gate  (device) [B, T, H, D] in_dtype, dense
+ *   d_weight    (device) fp32 like weight, or NULL (not computed)
+ *   workspace   (device) gdr_gated_norm_bwd_workspace_size() bytes, 256-byte aligned; not
+ *               needed (NULL, 0) when d_weight is NULL
+ *
+ * The weight's gradient is summed in an order that depends on the sizes and alignment
+ * alone; without tokens it is zeros.
+ */
+gdr_status gdr_gated_norm_bwd(const void* d_y, const void* x, const void* gate, const float* weight,
+                              void* dx, void* d_gate, float* d_weight, const gdr_gated_dims* dims,
+                              void* workspace, size_t workspace_bytes, gdr_stream_t stream);
+size_t gdr_gated_norm_bwd_workspace_size(const gdr_gated_dims* dims);
+
+/*
+ * gdr_residual_norm -- what lies between two layers, in one pass: a layer's output y goes
+ * into the residual, and the sum is normed for the next layer. Per token
+ *     p = y, or y / sqrt(mean(y^2) + eps) * post_weight with post_norm
+ *     residual_out = residual + s a(gate) p,   out = norm(residual_out) weight
+ * with norm(x) = x / sqrt(mean(x^2) + eps), s = scale [D] or dims->scale, and without a
+ * gate a = 1. All of it is fp32, out from the sum before it is rounded to residual_dtype.
+ *
+ *   residual      (device) [B, T, D] residual_dtype, strides below
+ *   y             (device) [B, T, D] y_dtype, or NULL: out = norm(residual) weight alone
+ *   gate          (device) [B, T, D] y_dtype, or NULL
+ *   weight, post_weight  (device) fp32 [D], or NULL (ones)
+ *   scale         (device) fp32 [D], or NULL (the number dims->scale)
+ *   residual_out  (device) [B, T, D] residual_dtype, dense; NULL without y; may be residual
+ *                 itself where that is dense
+ *   out           (device) [B, T, D] out_dtype, dense
+ *
+ * Without y there is no gate, post_norm or scale [D]; post_weight only with post_norm.
+ * D <= 16384, B T <= 2^30.
+ */
+typedef struct {
+  int B, T, D;
+  int residual_dtype;   /* gdr_dtype of residual, residual_out (and their gradients) */
+  int y_dtype;          /* gdr_dtype of y, gate (and their gradients) */
+  int out_dtype;        /* gdr_dtype of out (and d_out) */
+  int activation;       /* GDR_ACT_* of the gate */
+  int post_norm;
+  float eps;            /* finite, > 0 */
+  float scale;          /* finite */
+  int64_t residual_stride_b, residual_stride_t;  /* elements */
+  int64_t y_stride_b, y_stride_t;
+  int64_t gate_stride_b, gate_stride_t;
+} gdr_residual_dims;
+
+gdr_status gdr_residual_norm(const void* residual, const void* y, const void* gate,
+                             const float* weight, const float* post_weight, const float* scale,
+                             void* residual_out, void* out, const gdr_residual_dims* dims,
+                             gdr_stream_t stream);
+
+/*
+ * gdr_residual_norm_bwd -- gradients of gdr_residual_norm, from residual_out as the forward
+ * call stored it (without y: residual), strides residual_stride_*. With g the gradient of
+ * residual_out, through the norm and from d_residual_out:
+ *     d_residual = g,  d_scale = sum g a p,  d_gate = g s p a',  and through p to d_y.
+ *
+ *   d_out           (device) [B, T, D] out_dtype, dense
+ *   d_residual_out  (device) [B, T, D] residual_dtype, dense, or NULL (zeros)
+ *   y               needed with a gate, post_norm or scale [D]; not read otherwise
+ *   d_residual      (device) [B, T, D] residual_dtype, dense
+ *   d_y             (device) [B, T, D] y_dtype, dense; may be NULL where y is not needed
+ *   d_gate          (device) [B, T, D] y_dtype, dense; NULL without a gate
+ *   d_weight, d_post_weight, d_scale  (device) fp32 [D], or NULL (not computed)
+ *   workspace       (device) gdr_residual_norm_bwd_workspace_size() bytes, 256-byte aligned;
+ *                   not needed (NULL, 0) when all three are NULL
+ *
+ * The vectors' gradients are summed in an order that depends on the sizes and alignment
+ * alone; without tokens they are zeros.
+ */
+gdr_status gdr_residual_norm_bwd(const void* d_out, const void* d_residual_out,
+                                 const void* residual_out, const void* y, const void* gate,
+                                 const float* weight, const float* post_weight, const float* scale,
+                                 void* d_residual, void* d_y, void* d_gate, float* d_weight,
+                                 float* d_post_weight, float* d_scale,
+                                 const gdr_residual_dims* dims, void* workspace,
+                                 size_t workspace_bytes, gdr_stream_t stream);
+size_t gdr_residual_norm_bwd_workspace_size(const gdr_residual_dims* dims);
+
 /* Static, human-readable name of a status code. */
 const char* gdr_status_string(gdr_status s);
 
