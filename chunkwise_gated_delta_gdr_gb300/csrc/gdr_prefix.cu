@@ -11,7 +11,10 @@
 // Partition. An item is one (key-value head, tile of rows); its keys are cut into tiles. All
 // tiles of the call, item after item, form one line that the blocks share out equally; each
 // block leaves one part per item of its stretch, and a last kernel joins the parts of a row.
+#include <type_traits>
+
 #include "gdr_prefix.cuh"
+#include "gdr_prefix_tc.cuh"
 
 namespace gdr {
 namespace ops {
@@ -200,8 +203,8 @@ __global__ void __launch_bounds__(JW * 32) prefix_join_kernel(PrefixArgs a) {
   const int b = (int)(row / a.HQ), hq = (int)(row - (long long)b * a.HQ);
   const int hk = hq / a.G, r = b * a.G + hq - hk * a.G;
   const int item = hk * a.row_tiles + r / a.rows, in = r % a.rows;
-  const int parts = parts_of(a, item);
-  const size_t first = ((size_t)item * a.max_parts) * a.rows + in;
+  const int parts = parts_of(a, item) * a.units;
+  const size_t first = (size_t)item * a.max_parts * a.units * a.rows + in;
   const float own = a.own_lse[row] * LOG2E;
   float m = own;
   for (int c = lane; c < parts; c += 32)
@@ -257,11 +260,32 @@ constexpr int kSms = 152;
 
 // How the shared keys of a call are cut up.
 struct Plan {
-  int rows, keys;                                // of a tile
+  bool tc, pair;                                 // on the tensor cores; 256 rows a tile
+  int rows, keys, units;                         // of a tile; parts of a block per item
   int row_tiles, tiles, blocks, per, max_parts;
   size_t o_bytes, ml_bytes, own_bytes, lse_bytes, decode_bytes;
   size_t bytes() const { return o_bytes + ml_bytes + own_bytes + lse_bytes + decode_bytes; }
 };
+
+// f(Config of the head dimension) on the tensor cores.
+template <typename F>
+auto with_config(int D, F f) {
+  return D == 64    ? f(tc::Config<64>())
+         : D == 80  ? f(tc::Config<80>())
+         : D == 96  ? f(tc::Config<96>())
+         : D == 128 ? f(tc::Config<128>())
+         : D == 192 ? f(tc::Config<192>())
+                    : f(tc::Config<256>());
+}
+
+// Whether types, head dimension and strides allow the tensor cores: 16-byte pieces of every
+// cache row (their bases are 16-byte aligned by contract).
+bool tc_fits(const gdr_attn_dims* d, const gdr_paged_cache* c) {
+  const int D = c->D;
+  return d->q_dtype == GDR_BF16 && c->dtype == GDR_BF16 &&
+         (D == 64 || D == 80 || D == 96 || D == 128 || D == 192 || D == 256) &&
+         c->page_stride % 8 == 0 && c->token_stride % 8 == 0 && c->head_stride % 8 == 0;
+}
 
 Plan make_plan(const gdr_attn_dims* d, const gdr_paged_cache* c, int P) {
   Plan p = {};
@@ -271,7 +295,19 @@ Plan make_plan(const gdr_attn_dims* d, const gdr_paged_cache* c, int P) {
   const long long M = (long long)d->B * G;
   p.rows = RM;
   p.keys = KT;
-  const int resident = c->D <= 64 ? 2 : 1;
+  p.units = 1;
+  int resident = c->D <= 64 ? 2 : 1;
+  p.tc = tc_fits(d, c);
+  if (p.tc)
+    with_config(c->D, [&](auto config) {
+      typedef decltype(config) F;
+      p.pair = F::U == 2 && M > 128;
+      p.rows = p.pair ? 256 : 128;
+      p.keys = F::KT;
+      p.units = F::U == 2 && !p.pair ? 2 : 1;
+      resident = 1;
+      return 0;
+    });
   p.row_tiles = (int)((M + p.rows - 1) / p.rows);
   p.tiles = (P + p.keys - 1) / p.keys;
   const long long total = (long long)p.row_tiles * c->HK * p.tiles;
@@ -280,7 +316,7 @@ Plan make_plan(const gdr_attn_dims* d, const gdr_paged_cache* c, int P) {
   p.per = (int)((total + p.blocks - 1) / p.blocks);
   p.blocks = (int)((total + p.per - 1) / p.per);
   p.max_parts = (p.tiles - 1) / p.per + 2;
-  const size_t rows = (size_t)p.row_tiles * c->HK * p.max_parts * p.rows;
+  const size_t rows = (size_t)p.row_tiles * c->HK * p.max_parts * p.units * p.rows;
   p.o_bytes = align_up(rows * c->D * sizeof(float));
   p.ml_bytes = align_up(rows * 2 * sizeof(float));
   p.own_bytes = align_up((size_t)d->B * d->HQ * c->D * sizeof(float));
@@ -303,6 +339,16 @@ gdr_status check(const gdr_attn_dims* d, const gdr_paged_cache* c, int prefix_pa
   if (((double)d->B * d->HQ / 64 + c->HK) * ((double)P / 64 + 1) > (double)(1LL << 37))
     return GDR_ERR_UNSUPPORTED;
   return GDR_OK;
+}
+
+template <int D, bool PAIR>
+gdr_status launch_tc(const PrefixArgs& a, cudaStream_t s) {
+  typedef tc::Config<D> F;
+  struct Tag;
+  if (!allow_smem<Tag>(tc::prefix_tc_kernel<D, PAIR>, F::SMEM)) return GDR_ERR_CUDA;
+  const int q_vec = a.qb % 8 == 0 && a.qh % 8 == 0 && is_aligned(a.q, 16);
+  return launch_kernel(tc::prefix_tc_kernel<D, PAIR>, dim3(a.blocks), F::THREADS, F::SMEM, s, a,
+                       q_vec);
 }
 
 template <typename T, int NJ>
@@ -378,14 +424,27 @@ gdr_status gdr_paged_prefix_attn(const void* q, const void* k_cache, const void*
   a.qh = a.HQ > 1 ? dims->q_stride_h : 0;
   a.pp = cache->page_stride; a.pt = cache->token_stride; a.ph = cache->head_stride;
 
-  const int vec = a.D % 4 == 0 && a.pp % 4 == 0 && a.pt % 4 == 0 && a.ph % 4 == 0;
-  gdr_status run = with_dtype(cache->dtype, [&](auto* t) {
-    using T = std::remove_pointer_t<decltype(t)>;
-    return a.D <= 64    ? launch_any<T, 1>(a, vec, p.blocks, s)
-           : a.D <= 128 ? launch_any<T, 2>(a, vec, p.blocks, s)
-           : a.D <= 192 ? launch_any<T, 3>(a, vec, p.blocks, s)
-                        : launch_any<T, 4>(a, vec, p.blocks, s);
-  });
+  // A poll may be suspended for about 1 us, as long as sixteen of a flag take.
+  a.polls = (long)(set_wait_limit(-1) / 16);
+  a.units = p.units;
+  gdr_status run;
+  if (p.tc) {
+    run = with_config(a.D, [&](auto config) {
+      constexpr int D = decltype(config)::D;
+      if constexpr (decltype(config)::U == 2)
+        if (p.pair) return launch_tc<D, true>(a, s);
+      return launch_tc<D, false>(a, s);
+    });
+  } else {
+    const int vec = a.D % 4 == 0 && a.pp % 4 == 0 && a.pt % 4 == 0 && a.ph % 4 == 0;
+    run = with_dtype(cache->dtype, [&](auto* t) {
+      using T = std::remove_pointer_t<decltype(t)>;
+      return a.D <= 64    ? launch_any<T, 1>(a, vec, p.blocks, s)
+             : a.D <= 128 ? launch_any<T, 2>(a, vec, p.blocks, s)
+             : a.D <= 192 ? launch_any<T, 3>(a, vec, p.blocks, s)
+                          : launch_any<T, 4>(a, vec, p.blocks, s);
+    });
+  }
   if (run != GDR_OK) return run;
   gdr_attn_dims own = *dims;
   own.out_dtype = GDR_F32;

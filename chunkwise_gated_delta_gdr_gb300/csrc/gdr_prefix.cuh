@@ -11,13 +11,14 @@ namespace ops {
 struct PrefixArgs {
   const void *q, *kc, *vc;
   const int32_t* table;           // the shared pages
-  float *part_o, *part_ml;        // [items][max_parts][rows][D], [items][max_parts][rows][2]
+  float *part_o, *part_ml;        // [items][max_parts][units][rows][D], the same [2]
   float *own_o, *own_lse;         // [B][HQ][D], [B][HQ]: of the sequences' own keys
   void* out;
   float* lse;                     // may be null
   int B, HQ, HK, D, G, M, P;      // G = HQ / HK, M = B G rows per kv head, P shared keys
   int rows, row_tiles, tiles;     // rows of a tile, tiles of M and of P
-  int blocks, per, max_parts;     // tiles of a block; parts of an item at most
+  int blocks, per, max_parts;     // tiles of a block; blocks of an item at most
+  int units;                      // parts that a block leaves per item
   int page, num_pages, out_bf16, q_bf16;
   float scale2;                   // scale log2(e)
   long polls;                     // bound of a wait
@@ -51,7 +52,7 @@ __device__ __forceinline__ Stretch stretch_of(const PrefixArgs& a, int block) {
   s.tile = (int)(first - (long long)s.item * a.tiles);
   return s;
 }
-// Place of a block's part of an item among all parts, and the parts of an item.
+// Place of a block's part of an item among all parts (units aside), and the blocks of an item.
 __device__ __forceinline__ size_t part_of(const PrefixArgs& a, int item, int block) {
   return (size_t)item * a.max_parts + (block - (int)((long long)item * a.tiles / a.per));
 }

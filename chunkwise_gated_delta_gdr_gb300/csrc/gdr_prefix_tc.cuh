@@ -1,0 +1,463 @@
+// gdr_prefix_tc.cuh -- the shared keys' part of the attention behind a shared prompt, on the
+// tensor cores (tcgen05): bf16 queries and caches.
+//
+// A step is a tile of 128 rows by KT keys: S = Q K^T into TMEM, the rows' softmax by 128 threads
+// (one row each, so that no sum or maximum crosses a thread), the weights back into TMEM in the
+// place of their scores, O += P V with P read from TMEM. One thread issues all products.
+//
+// Two units of 128 threads take steps in turn, so that one's softmax runs under the other's
+// products. With more than 128 rows per key head (PAIR) a block takes 256 rows, one half per
+// unit, and both read the same keys; with fewer the units take every other tile of keys and
+// leave a part each. Heads of 256 channels leave TMEM for one unit, with two tiles of scores.
+//
+// Weights. As in paged_decode_attn, a weight goes into the product with V as two bf16: its upper
+// bits as they are and what they leave over, rounded; 2^-15 of it is lost at most (one bf16 alone
+// would put as much error into a bf16 result as rounding that does). That makes the products
+// 3/2 of the plain count: (QK + 2 PV) = 6 rows keys D operations.
+// Per 16 keys the weights' TMEM columns are 8 of upper parts and 8 of rests, in the columns of
+// the scores they come from.
+//
+// Maximum. o and l are kept against a reference that is moved (and o rescaled in TMEM) only when
+// a row's scores pass it by more than 2^8: weights stay below 2^8, far from any limit of fp32.
+#pragma once
+
+#include "gdr_prefix.cuh"
+
+namespace gdr {
+namespace ops {
+namespace tc {
+
+using namespace ptx;
+
+template <int D_>
+struct Config {
+  static constexpr int D = D_, NB = (D + 63) / 64, C = D / 8;
+  static constexpr int U = D <= 192 ? 2 : 1;               // units: TMEM columns U D + 2 KT <= 512
+  static constexpr int KT = D <= 128 ? 128 : 64;           // keys of a tile
+  static constexpr int QTILE = NB * 128 * 128, TILE = NB * KT * 128;   // bytes
+  static constexpr int ST = D <= 64 ? 8 : 5;               // tiles of the ring, K and V in turn
+  static constexpr int SOFT = 4 * U, LOAD = 4, THREADS = 32 * (SOFT + LOAD + 1);
+  static constexpr int SMEM = U * QTILE + ST * TILE + 1024 + 256;
+  static constexpr uint32_t T_S = 0, T_O = 2 * KT;         // TMEM columns: S x 2, O x U
+  static_assert(U * D + 2 * KT <= 512 && SMEM <= 232448, "");
+};
+constexpr int LAG = 3;                                     // tiles of copies in flight, less one
+
+__device__ __forceinline__ void umma_bf16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id,
+                                             int acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"(acc));
+}
+// 32 columns of this warp's lanes, without waiting for them; tmem_take() makes them usable.
+__device__ __forceinline__ void tmem_get(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_take(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+template <int N>                                           // 16 or 32 columns
+__device__ __forceinline__ void tmem_put(uint32_t taddr, const uint32_t* r) {
+  if constexpr (N == 32)
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+        "%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+        "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+        "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+        "r"(r[30]), "r"(r[31]), "r"(taddr)
+        : "memory");
+  else
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+        "%13,%14,%15};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+        : "memory");
+}
+// 16 columns, waited for.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15}, [%16];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_put_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float ex2(float x) {            // 2^x, 2 ulp; 0 below 2^-126
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("min.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+struct Bars {
+  uint64_t kv_full[8], kv_empty[8];   // a tile of K or V: LOAD arrivals; commit of its last product
+  uint64_t s_full[2], p_full[2];      // scores: commit; weights in their place: 4 arrivals
+  uint64_t pv_done[2];                // commit of the step's product with V
+  uint64_t q_full, fin;               // an item's queries: SOFT arrivals; all products, at the end
+  uint32_t tmem, dead, bad;           // dead: a wait gave up; bad: a page out of range
+};
+
+// A wait that gives up after `polls`, or when another role has.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, long polls,
+                                         volatile uint32_t* dead) {
+  if (mbar_test(bar, parity)) return true;
+  for (long i = 0; i < polls; ++i) {
+    if (mbar_wait(bar, parity, 1)) return true;
+    if (*dead) return false;
+  }
+  *dead = 1;
+  return false;
+}
+
+// PAIR: 256 rows a block, a half per unit, every tile of keys taken by both.
+template <int D, bool PAIR>
+__global__ void __launch_bounds__(Config<D>::THREADS, 1) prefix_tc_kernel(PrefixArgs a, int q_vec) {
+  typedef Config<D> F;
+  constexpr int U = F::U, KT = F::KT, ST = F::ST, C = F::C, PER_TILE = PAIR ? 2 : 1;
+  constexpr int ROWS = PAIR ? 256 : 128;
+  static_assert(!PAIR || U == 2, "");
+  extern __shared__ char raw[];
+  char* base = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(raw) + 1023) &
+                                       ~static_cast<uintptr_t>(1023));
+  __shared__ Bars bars;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t q_at = smem_u32(base), ring = q_at + U * F::QTILE;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(&bars.kv_full[i], F::LOAD);
+      mbar_init(&bars.kv_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars.s_full[i], 1);
+      mbar_init(&bars.p_full[i], 4);
+      mbar_init(&bars.pv_done[i], 1);
+    }
+    mbar_init(&bars.q_full, F::SOFT);
+    mbar_init(&bars.fin, 1);
+    bars.dead = bars.bad = 0;
+    mbar_fence_init();
+  }
+  if (warp == F::SOFT + F::LOAD) tmem_alloc(&bars.tmem, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars.tmem;
+  volatile uint32_t* dead = &bars.dead;
+  Stretch st = stretch_of(a, blockIdx.x);
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_for(bar, parity, a.polls, dead); };
+
+  if (warp < F::SOFT) {
+    // ------------------------------------------------------------ softmax
+    const int unit = warp >> 2, row = threadIdx.x & 127;   // row = TMEM lane
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t o_at = tmem + lanes + F::T_O + unit * D;
+    bool ok = true;
+    int g = 0;                                             // steps of the block so far
+    for (; st.left > 0; ++st.item, st.tile = 0) {
+      const int hk = st.item / a.row_tiles, r0 = (st.item - hk * a.row_tiles) * ROWS;
+      const int last = min(a.tiles, st.tile + st.left), steps = (last - st.tile) * PER_TILE;
+      if (ok) {
+        for (int e = threadIdx.x; e < ROWS * C; e += 128 * U) {
+          const int r = e / C, ch = e - r * C, m = r0 + r;
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (m < a.M) {
+            const bf16* src = static_cast<const bf16*>(a.q) + q_row(a, hk, m) + ch * 8;
+            if (q_vec) {
+              v = *reinterpret_cast<const uint4*>(src);
+            } else {
+              const unsigned short* s = reinterpret_cast<const unsigned short*>(src);
+              v = make_uint4(s[0] | (uint32_t)s[1] << 16, s[2] | (uint32_t)s[3] << 16,
+                             s[4] | (uint32_t)s[5] << 16, s[6] | (uint32_t)s[7] << 16);
+            }
+          }
+          *reinterpret_cast<uint4*>(base + (r >> 7) * F::QTILE + (ch >> 3) * 16384 + (r & 127) * 128 +
+                                    (((ch ^ r) & 7) << 4)) = v;
+        }
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.q_full);
+      }
+      float m = -INFINITY, l = 0.f;
+      int prev = -1;                                       // this unit's last step
+      for (int i = 0; i < steps && ok; ++i, ++g) {
+        const int buf = g & 1;
+        // Unit of a step: its half of the rows, or whose turn it is.
+        if (U == 2 && buf != unit) continue;
+        const uint32_t s_at = tmem + lanes + F::T_S + buf * KT;
+        const int key0 = (st.tile + (PAIR ? i >> 1 : i)) * KT, live = a.P - key0;
+        ok = wait(&bars.s_full[buf], (g >> 1) & 1);
+        ok = __all_sync(~0u, ok);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t x[2][32];
+        float top = -INFINITY;
+        tmem_get(s_at, x[0]);
+#pragma unroll
+        for (int c = 0; c < KT / 32; ++c) {
+          tmem_take(x[c & 1]);
+          if (c + 1 < KT / 32) tmem_get(s_at + 32 * (c + 1), x[(c + 1) & 1]);
+          if (live >= KT) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) top = fmaxf(top, __uint_as_float(x[c & 1][k]));
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (32 * c + k < live) top = fmaxf(top, __uint_as_float(x[c & 1][k]));
+          }
+        }
+        top *= a.scale2;
+        if (__any_sync(~0u, top > m + 8.f)) {              // and from -inf
+          const float to = fmaxf(m, top), f = to > m ? ex2(m - to) : 1.f;    // 0 from -inf
+          m = to;
+          l *= f;
+          if (prev >= 0) {
+            ok = wait(&bars.pv_done[prev & 1], (prev >> 1) & 1);
+            ok = __all_sync(~0u, ok);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t o[16];
+              tmem_ld16(o_at + 16 * c, o);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+              tmem_put<16>(o_at + 16 * c, o);
+            }
+          }
+        }
+        const float ref = m == -INFINITY ? 0.f : m;
+        const float2 scale = make_float2(a.scale2, a.scale2), off = make_float2(-ref, -ref);
+        float2 sum = make_float2(0.f, 0.f);
+        tmem_get(s_at, x[0]);
+#pragma unroll
+        for (int c = 0; c < KT / 32; ++c) {
+          uint32_t* y = x[c & 1];
+          tmem_take(y);
+          if (c + 1 < KT / 32) tmem_get(s_at + 32 * (c + 1), x[(c + 1) & 1]);
+          uint32_t w[32];                                  // per 16 keys: 8 upper parts, 8 rests
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) {
+            float2 p = fma2(make_float2(__uint_as_float(y[k]), __uint_as_float(y[k + 1])), scale, off);
+            p.x = ex2(p.x);
+            p.y = ex2(p.y);
+            if (live < KT) {
+              if (32 * c + k >= live) p.x = 0.f;
+              if (32 * c + k + 1 >= live) p.y = 0.f;
+            }
+            sum = fma2(p, make_float2(1.f, 1.f), sum);
+            const uint32_t hi = __byte_perm(__float_as_uint(p.x), __float_as_uint(p.y), 0x7632);
+            const float2 rest = fma2(unpack2(hi), make_float2(-1.f, -1.f), p);
+            // Never 0 beside an upper part that is not, so that an infinite v gives what w v gives.
+            const int at = (k & 16) + ((k & 15) >> 1);
+            w[at] = hi;
+            w[at + 8] = max2(pack2(rest.x, rest.y), min2(hi, 0x00800080u));
+          }
+          tmem_put<32>(s_at + 32 * c, w);
+        }
+        l += sum.x + sum.y;
+        tmem_put_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.p_full[buf]);
+        prev = g;
+      }
+      if (ok && prev >= 0) {
+        ok = wait(&bars.pv_done[prev & 1], (prev >> 1) & 1);
+        ok = __all_sync(~0u, ok);
+        tc_fence_after();
+      }
+      // This unit's part: a row of its half of the tile, or of its share of the keys.
+      const size_t part = PAIR || U == 1
+                              ? part_of(a, st.item, blockIdx.x) * ROWS + (PAIR ? unit * 128 : 0) + row
+                              : (part_of(a, st.item, blockIdx.x) * 2 + unit) * ROWS + row;
+      const bool mine = r0 + (PAIR ? unit * 128 : 0) + row < a.M;
+      if (mine) {
+        a.part_ml[part * 2] = m;
+        a.part_ml[part * 2 + 1] = !ok || *(volatile uint32_t*)&bars.bad ? NAN : l;
+      }
+      if (ok) {
+#pragma unroll 1
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t o[16];
+          if (prev >= 0) {
+            tmem_ld16(o_at + 16 * c, o);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[k] = 0u;
+          }
+          if (mine) {
+            uint4* to = reinterpret_cast<uint4*>(a.part_o + part * D + 16 * c);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              to[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          }
+        }
+        tc_fence_before();
+      }
+      st.left -= last - st.tile;
+      // All scores of the item are in, so its queries are done with.
+      if (U == 2 && st.left > 0) asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (U == 1 && st.left > 0) asm volatile("bar.sync 1, 128;" ::: "memory");
+      ok = __all_sync(~0u, ok && !*dead);
+    }
+  } else if (warp < F::SOFT + F::LOAD) {
+    // ------------------------------------------------------------ copies
+    constexpr int RW = KT / F::LOAD;                       // rows of a warp, at most 32
+    const int w = warp - F::SOFT;
+    const bf16 *kc = static_cast<const bf16*>(a.kc), *vc = static_cast<const bf16*>(a.vc);
+    int n = 0, sent = 0;                                   // tiles issued, tiles handed over
+    bool ok = true;
+    auto hand_over = [&]() {                               // this warp's copies of tile `sent` are in
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.kv_full[sent % ST]);
+      ++sent;
+    };
+    auto find = [&](int tile) -> int64_t {                 // -1: no such key; bad pages read as none
+      const int j = tile * KT + w * RW + (lane & (RW - 1));
+      if (j >= a.P) return -1;
+      const int64_t r = prefix_row(a, j);
+      if (r < 0) bars.bad = 1;
+      return r;
+    };
+    for (; st.left > 0 && ok; ++st.item, st.tile = 0) {
+      const int hk = st.item / a.row_tiles;
+      const int last = min(a.tiles, st.tile + st.left);
+      int64_t next = find(st.tile);
+      for (int t = st.tile; t < last && ok; ++t) {
+        const int64_t off = next;
+        if (t + 1 < last) next = find(t + 1);              // looked up meanwhile
+#pragma unroll 1
+        for (int kv = 0; kv < 2 && ok; ++kv, ++n) {
+          const int slot = n % ST;
+          if (n >= ST) {
+            const uint32_t parity = (n / ST - 1) & 1;
+            if (!__all_sync(~0u, mbar_test(&bars.kv_empty[slot], parity))) {
+              // Nothing is held back while this waits.
+              cp_async_wait<0>();
+              while (sent < n) hand_over();
+              ok = __all_sync(~0u, wait(&bars.kv_empty[slot], parity));
+              if (!ok) break;
+            }
+          }
+          const bf16* src = (kv ? vc : kc) + hk * a.ph;
+          const uint32_t to = ring + slot * F::TILE;
+#pragma unroll 8
+          for (int i = 0; i < RW * C / 32; ++i) {
+            const int e = lane + 32 * i, r = e / C, ch = e - r * C, in = w * RW + r;
+            const int64_t o = __shfl_sync(~0u, off, r);
+            cp_async16(to + (ch >> 3) * (KT * 128) + in * 128 + (((ch ^ in) & 7) << 4),
+                       src + (o < 0 ? 0 : o + ch * 8), o < 0 ? 0 : 16);
+          }
+          cp_async_commit();
+          if (n - sent >= LAG) {
+            cp_async_wait<LAG>();
+            hand_over();
+          }
+        }
+      }
+      st.left -= last - st.tile;
+    }
+    cp_async_wait<0>();
+    while (sent < n) hand_over();
+  } else if (lane == 0) {
+    // ------------------------------------------------------------ products
+    constexpr uint32_t ID_QK = idesc_bf16_kk(128, KT), ID_PV = idesc_bf16(128, D, 0, 1);
+    int g0 = 0, item = 0, n0 = 0;                          // steps, items and tiles before this item
+    bool ok = true;
+    for (; st.left > 0 && ok; ++st.item, st.tile = 0, ++item) {
+      const int last = min(a.tiles, st.tile + st.left), tiles = last - st.tile;
+      const int steps = tiles * PER_TILE;
+      auto scores = [&](int i) {                           // S of step i
+        const int t = PAIR ? i >> 1 : i, n = n0 + 2 * t, slot = n % ST, g = g0 + i;
+        if (!PAIR || (i & 1) == 0) ok = ok && wait(&bars.kv_full[slot], (n / ST) & 1);
+        // The weights of two steps ago, in the same place, have been used.
+        if (g >= 2) ok = ok && wait(&bars.pv_done[g & 1], ((g >> 1) - 1) & 1);
+        if (!ok) return;
+        tc_fence_after();
+        const uint32_t q = q_at + (PAIR ? (i & 1) * F::QTILE : 0), k = ring + slot * F::TILE;
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c)
+          umma_bf16(tmem + F::T_S + (g & 1) * KT,
+                    sdesc_sw128(q + (c >> 2) * 16384 + (c & 3) * 32),
+                    sdesc_sw128(k + (c >> 2) * (KT * 128) + (c & 3) * 32), ID_QK, c > 0);
+        umma_commit(&bars.s_full[g & 1]);
+        if (!PAIR || (i & 1)) umma_commit(&bars.kv_empty[slot]);
+      };
+      ok = wait(&bars.q_full, item & 1);
+      if (ok) scores(0);
+      if (ok && steps > 1) scores(1);
+      for (int i = 0; i < steps && ok; ++i) {
+        const int t = PAIR ? i >> 1 : i, n = n0 + 2 * t + 1, slot = n % ST, g = g0 + i;
+        if (!PAIR || (i & 1) == 0) ok = ok && wait(&bars.kv_full[slot], (n / ST) & 1);
+        ok = ok && wait(&bars.p_full[g & 1], (g >> 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t p = tmem + F::T_S + (g & 1) * KT, v = ring + slot * F::TILE;
+        const uint32_t o = tmem + F::T_O + (U == 2 ? g & 1 : 0) * D;
+#pragma unroll
+        for (int part = 0; part < 2; ++part)
+#pragma unroll
+          for (int c = 0; c < KT / 16; ++c)
+            umma_bf16_ts(o, p + 16 * c + 8 * part, sdesc_sw128_lbo(v + c * 2048, KT * 128), ID_PV,
+                         i >= U || part || c);
+        umma_commit(&bars.pv_done[g & 1]);
+        if (!PAIR || (i & 1)) umma_commit(&bars.kv_empty[slot]);
+        if (i + 2 < steps) scores(i + 2);
+      }
+      g0 += steps;
+      n0 += 2 * tiles;
+      st.left -= tiles;
+    }
+    if (!ok) {                                             // nothing of this block's is left running
+      umma_commit(&bars.fin);
+      mbar_wait(&bars.fin, 0, a.polls);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == F::SOFT + F::LOAD) {
+    __syncwarp();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace tc
+}  // namespace ops
+}  // namespace gdr
