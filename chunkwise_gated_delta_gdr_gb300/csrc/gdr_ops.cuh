@@ -196,17 +196,23 @@ bool allow_smem(Fn fn, int bytes) {
 // A launch that may begin while the kernel before it in the stream still runs; the launched
 // kernel waits for that one's results itself (griddepcontrol.wait, in every block).
 template <typename Fn, typename... Args>
-gdr_status launch_behind(Fn fn, dim3 grid, int threads, cudaStream_t s, Args... args) {
+gdr_status launch_behind_smem(Fn fn, dim3 grid, int threads, size_t smem, cudaStream_t s,
+                              Args... args) {
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = at;
   cfg.numAttrs = 1;
   return status_of(cudaLaunchKernelEx(&cfg, fn, args...));
+}
+template <typename Fn, typename... Args>
+gdr_status launch_behind(Fn fn, dim3 grid, int threads, cudaStream_t s, Args... args) {
+  return launch_behind_smem(fn, grid, threads, 0, s, args...);
 }
 
 // Calls f with a null pointer of the element type that `dtype` names.

@@ -790,6 +790,7 @@ template <int V>
 __global__ void __launch_bounds__(JW * 32) paged_join_kernel(AttnArgs a) {
   constexpr int N = 256 / (32 * V);              // runs of V channels of a lane
   __shared__ float red[JW][256], sum[JW];
+  asm volatile("griddepcontrol.launch_dependents;");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int per_b = a.HK * a.groups;
   const long long total = total_tiles(a, lane), per = (total + a.blocks - 1) / a.blocks;

@@ -40,6 +40,7 @@ __global__ void __launch_bounds__(NT) prefix_any_kernel(PrefixArgs a, int vec) {
   constexpr int DP = Smem::DP, LD = Smem::LD, LS = Smem::LS;
   Smem& sm = *reinterpret_cast<Smem*>(raw);
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15, warp = tid >> 5, lane = tid & 31;
+  asm volatile("griddepcontrol.launch_dependents;");
   Stretch st = stretch_of(a, blockIdx.x);
   if (tid == 0) sm.bad = 0;
   while (st.left > 0) {
@@ -190,22 +191,28 @@ __global__ void __launch_bounds__(NT) prefix_any_kernel(PrefixArgs a, int vec) {
     st.tile = 0;
     ++st.item;
   }
+  // What comes behind this kernel also waits for the one before it, whose end nothing here needs.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ------------------------------------------------------------ joining the stretches
-// A warp per query head of a sequence: the shared keys' parts in order, then its own keys.
+// A row (a query head of a sequence) of few parts takes a warp; one of more the JW warps of a
+// block, every JW-th part each (SPLIT). A lane holds V channels in a row, N runs of them, and
+// has UN parts' loads under way. 64 sequences, 8192 shared keys, HK = 4 (16 parts a row): TIME.
 constexpr int JW = 4;
-template <int V>
+template <int V, bool SPLIT>
 __global__ void __launch_bounds__(JW * 32) prefix_join_kernel(PrefixArgs a) {
-  constexpr int N = 256 / (32 * V);
-  const int lane = threadIdx.x & 31;
-  const long long row = (long long)blockIdx.x * JW + (threadIdx.x >> 5);
-  if (row >= (long long)a.B * a.HQ) return;
+  constexpr int N = 256 / (32 * V), UN = 4, STEP = SPLIT ? JW : 1;
+  __shared__ float sum[JW], so[SPLIT ? JW : 1][256];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w0 = SPLIT ? warp : 0;
+  const long long row = SPLIT ? blockIdx.x : (long long)blockIdx.x * JW + warp;
+  if (!SPLIT && row >= (long long)a.B * a.HQ) return;
   const int b = (int)(row / a.HQ), hq = (int)(row - (long long)b * a.HQ);
   const int hk = hq / a.G, r = b * a.G + hq - hk * a.G;
   const int item = hk * a.row_tiles + r / a.rows, in = r % a.rows;
   const int parts = parts_of(a, item) * a.units;
   const size_t first = (size_t)item * a.max_parts * a.units * a.rows + in;
+  asm volatile("griddepcontrol.wait;" ::: "memory");       // the stretches are written
   const float own = a.own_lse[row] * LOG2E;
   float m = own;
   for (int c = lane; c < parts; c += 32)
@@ -213,31 +220,65 @@ __global__ void __launch_bounds__(JW * 32) prefix_join_kernel(PrefixArgs a) {
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, x));
   const float base = m == -INFINITY ? 0.f : m;
-  float l = exp2f(own - base), o[N][V];          // 0 without keys, NaN where they are bad
+  float l = w0 == 0 ? exp2f(own - base) : 0.f, o[N][V];    // 0 without keys, NaN where they are bad
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const int ch = (lane + 32 * i) * V;
-    if (ch < a.D) {
+#pragma unroll
+    for (int k = 0; k < V; ++k) o[i][k] = 0.f;
+    if (ch < a.D && w0 == 0) {
       load_f<float, V>(a.own_o + (size_t)row * a.D + ch, o[i]);
 #pragma unroll
       for (int k = 0; k < V; ++k) o[i][k] *= l;
     }
   }
-#pragma unroll 4
-  for (int c = 0; c < parts; ++c) {
-    const size_t at = first + (size_t)c * a.rows;
-    const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + at * 2);
-    const float f = exp2f(ml.x - base);
-    l = fmaf(f, ml.y, l);
+  for (int c0 = w0; c0 < parts; c0 += STEP * UN) {
+    float2 ml[UN];
+    float v[UN][N][V];
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int ch = (lane + 32 * i) * V;
-      if (ch < a.D) {
-        float v[V];
-        load_f<float, V>(a.part_o + at * a.D + ch, v);
+    for (int u = 0; u < UN; ++u) {
+      const int c = c0 + STEP * u;
+      ml[u] = make_float2(-INFINITY, 0.f);
 #pragma unroll
-        for (int k = 0; k < V; ++k) o[i][k] = fmaf(f, v[k], o[i][k]);
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int k = 0; k < V; ++k) v[u][i][k] = 0.f;
+      if (c < parts) {
+        const size_t at = first + (size_t)c * a.rows;
+        ml[u] = *reinterpret_cast<const float2*>(a.part_ml + at * 2);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const int ch = (lane + 32 * i) * V;
+          if (ch < a.D) load_f<float, V>(a.part_o + at * a.D + ch, v[u][i]);
+        }
       }
+    }
+#pragma unroll
+    for (int u = 0; u < UN; ++u) {
+      const float f = exp2f(ml[u].x - base);
+      l = fmaf(f, ml[u].y, l);
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int k = 0; k < V; ++k) o[i][k] = fmaf(f, v[u][i][k], o[i][k]);
+    }
+  }
+  if (SPLIT) {                                   // the warps' sums, in order
+    if (lane == 0) sum[warp] = l;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int k = 0; k < V; ++k) so[warp][(lane + 32 * i) * V + k] = o[i][k];
+    __syncthreads();
+    if (warp != 0) return;
+    l = sum[0];
+#pragma unroll
+    for (int w = 1; w < JW; ++w) {
+      l += sum[w];
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int k = 0; k < V; ++k) o[i][k] += so[SPLIT ? w : 0][(lane + 32 * i) * V + k];
     }
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -258,6 +299,7 @@ __global__ void __launch_bounds__(JW * 32) prefix_join_kernel(PrefixArgs a) {
 
 // ------------------------------------------------------------ host
 constexpr int kSms = 152;
+constexpr int kSplitParts = 5;   // parts of a row from which the warps of a block share them
 
 // How the shared keys of a call are cut up.
 struct Plan {
@@ -365,8 +407,8 @@ gdr_status launch_tc(const PrefixArgs& a, const gdr_paged_cache* c, cudaStream_t
     typedef tc::Config<D, TMA> F;
     struct Tag;
     if (!allow_smem<Tag>(tc::prefix_tc_kernel<D, PAIR, TMA>, F::SMEM)) return GDR_ERR_CUDA;
-    return launch_kernel(tc::prefix_tc_kernel<D, PAIR, TMA>, dim3(a.blocks), F::THREADS, F::SMEM, s,
-                         a, q_vec, k, v);
+    return launch_behind_smem(tc::prefix_tc_kernel<D, PAIR, TMA>, dim3(a.blocks), F::THREADS,
+                              F::SMEM, s, a, q_vec, k, v);
   };
   // Tensor copies where pages and tiles divide one another in runs of 8 rows (which the swizzle
   // repeats after), and the driver takes the strides (a stride of 0 is refused, for one). On 128
@@ -383,7 +425,8 @@ template <typename T, int NJ>
 gdr_status launch_any(const PrefixArgs& a, int vec, int blocks, cudaStream_t s) {
   struct Tag;
   if (!allow_smem<Tag>(prefix_any_kernel<T, NJ>, sizeof(AnySmem<NJ>))) return GDR_ERR_CUDA;
-  return launch_kernel(prefix_any_kernel<T, NJ>, dim3(blocks), NT, sizeof(AnySmem<NJ>), s, a, vec);
+  return launch_behind_smem(prefix_any_kernel<T, NJ>, dim3(blocks), NT, sizeof(AnySmem<NJ>), s, a,
+                            vec);
 }
 
 }  // namespace
@@ -452,10 +495,16 @@ gdr_status gdr_paged_prefix_attn(const void* q, const void* k_cache, const void*
   a.qh = a.HQ > 1 ? dims->q_stride_h : 0;
   a.pp = cache->page_stride; a.pt = cache->token_stride; a.ph = cache->head_stride;
 
+  // The sequences' own keys first, bound by HBM; the shared ones' blocks, bound by the tensor
+  // cores, come in where those leave an SM.
+  gdr_attn_dims own = *dims;
+  own.out_dtype = GDR_F32;
+  gdr_status run = gdr_paged_decode_attn(q, k_cache, v_cache, page_table, lens, a.own_o, a.own_lse, &own,
+                              cache, decode_ws, p.decode_bytes, stream);
+  if (run != GDR_OK) return run;
   // A poll may be suspended for about 1 us, as long as sixteen of a flag take.
   a.polls = (long)(set_wait_limit(-1) / 16);
   a.units = p.units;
-  gdr_status run;
   if (p.tc) {
     run = with_config(a.D, [&](auto config) {
       constexpr int D = decltype(config)::D;
@@ -474,14 +523,14 @@ gdr_status gdr_paged_prefix_attn(const void* q, const void* k_cache, const void*
     });
   }
   if (run != GDR_OK) return run;
-  gdr_attn_dims own = *dims;
-  own.out_dtype = GDR_F32;
-  run = gdr_paged_decode_attn(q, k_cache, v_cache, page_table, lens, a.own_o, a.own_lse, &own,
-                              cache, decode_ws, p.decode_bytes, stream);
-  if (run != GDR_OK) return run;
-  const long long rows = (long long)a.B * a.HQ;
-  return launch_kernel(a.D % 4 == 0 ? prefix_join_kernel<4> : prefix_join_kernel<1>,
-                       dim3((unsigned)((rows + JW - 1) / JW)), JW * 32, 0, s, a);
+  // The join may start while the shared keys are being worked on; it waits for their kernel
+  // itself, which ends behind the one for the sequences' own keys.
+  const unsigned rows = (unsigned)(a.B * a.HQ);
+  if ((p.max_parts - 1) * p.units >= kSplitParts)
+    return launch_behind(a.D % 4 == 0 ? prefix_join_kernel<4, true> : prefix_join_kernel<1, true>,
+                         dim3(rows), JW * 32, s, a);
+  return launch_behind(a.D % 4 == 0 ? prefix_join_kernel<4, false> : prefix_join_kernel<1, false>,
+                       dim3((rows + JW - 1) / JW), JW * 32, s, a);
 }
 
 }  // extern "C"

@@ -209,6 +209,7 @@ __global__ void __launch_bounds__(Config<D, TMA>::THREADS, 1)
   char* base = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(raw) + 1023) &
                                        ~static_cast<uintptr_t>(1023));
   __shared__ Bars bars;
+  asm volatile("griddepcontrol.launch_dependents;");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t q_at = smem_u32(base), ring = q_at + U * F::QTILE;
   if (threadIdx.x == 0) {
@@ -248,20 +249,21 @@ __global__ void __launch_bounds__(Config<D, TMA>::THREADS, 1)
       if (ok) {
         for (int e = threadIdx.x; e < ROWS * C; e += 128 * U) {
           const int r = e / C, ch = e - r * C, m = r0 + r;
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (m < a.M) {
-            const bf16* src = static_cast<const bf16*>(a.q) + q_row(a, hk, m) + ch * 8;
-            if (q_vec) {
-              v = *reinterpret_cast<const uint4*>(src);
-            } else {
-              const unsigned short* s = reinterpret_cast<const unsigned short*>(src);
+          const uint32_t to = (r >> 7) * F::QTILE + (ch >> 3) * 16384 + (r & 127) * 128 +
+                              (((ch ^ r) & 7) << 4);
+          const bf16* src = static_cast<const bf16*>(a.q) + (m < a.M ? q_row(a, hk, m) + ch * 8 : 0);
+          if (q_vec) {                                     // all of a thread's pieces under way at once
+            cp_async16(q_at + to, src, m < a.M ? 16 : 0);
+          } else {
+            const unsigned short* s = reinterpret_cast<const unsigned short*>(src);
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (m < a.M)
               v = make_uint4(s[0] | (uint32_t)s[1] << 16, s[2] | (uint32_t)s[3] << 16,
                              s[4] | (uint32_t)s[5] << 16, s[6] | (uint32_t)s[7] << 16);
-            }
+            *reinterpret_cast<uint4*>(base + to) = v;
           }
-          *reinterpret_cast<uint4*>(base + (r >> 7) * F::QTILE + (ch >> 3) * 16384 + (r & 127) * 128 +
-                                    (((ch ^ r) & 7) << 4)) = v;
         }
+        cp_async_wait_all();
         fence_async_shared();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.q_full);
@@ -548,6 +550,8 @@ __global__ void __launch_bounds__(Config<D, TMA>::THREADS, 1)
     __syncwarp();
     tmem_dealloc(tmem, 512);
   }
+  // What comes behind this kernel also waits for the one before it, whose end nothing here needs.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 }  // namespace tc
