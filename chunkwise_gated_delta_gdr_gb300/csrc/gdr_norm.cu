@@ -32,6 +32,7 @@ struct GatedArgs {
   int B, T, H, D, tokens, groups, per_head, kind, first;
   int in_bf16, out_bf16;         // out: of y and d
   int pieces, stages;
+  int flat;                      // the views' tokens are one stride apart, over batch rows too
   float eps, inv_d;
 };
 
@@ -39,10 +40,11 @@ struct GatedArgs {
 template <class S>
 __device__ __forceinline__ void sum_groups(float* acc, float* s, int tid) {
   if constexpr (S::LANES > 0) {
+    if constexpr (S::LANES < 32)
 #pragma unroll
-    for (int o = S::LANES; o < 32; o <<= 1)
+      for (int o = S::LANES; o < 32; o <<= 1)
 #pragma unroll
-      for (int j = 0; j < S::N; ++j) acc[j] += __shfl_xor_sync(~0u, acc[j], o);
+        for (int j = 0; j < S::N; ++j) acc[j] += __shfl_xor_sync(~0u, acc[j], o);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
     if (lane < S::LANES)
 #pragma unroll
@@ -54,6 +56,170 @@ __device__ __forceinline__ void sum_groups(float* acc, float* s, int tid) {
         for (int j = 0; j < S::N; ++j) acc[j] += s[(k * S::N + j) * S::LANES + tid];
     __syncthreads();
   }
+}
+
+// Rows of at most 256 channels: a group of LANES lanes per row, 8 channels a lane, UN rows at a
+// time (the group's head in UN tokens), the next ones' loads under way meanwhile. What bounds the
+// larger calls beside HBM is the number of instructions per row, so addresses step from row to
+// row and sums and products go in pairs; the copies through shared memory that wider rows take
+// cost twice the time here (2 x 8192 x 32 heads of 128 forward: 115 us so, TIME now).
+template <typename T, int LANES, bool BWD, bool FIRST>
+__global__ void __launch_bounds__(256, BWD ? 2 : 3) gated_rows_kernel(GatedArgs a) {
+  typedef Shape<LANES, 8, 1> S;
+  constexpr int TENSORS = BWD ? 3 : 2, UN = sizeof(T) == 2 ? 2 : 1;
+  constexpr int Q = 8 * sizeof(T) / 16;          // 16-byte pieces of 8 channels
+  __shared__ float sums[BWD ? 8 * 32 * 8 : 1];
+  if (BWD) asm volatile("griddepcontrol.launch_dependents;");
+  const Walk w = walk_of<LANES>(a.tokens, a.H, a.groups);
+  const int ch = w.tid * 8;
+  const bool mine = w.on && ch < a.D;
+  const T* base[TENSORS];
+  int64_t pitch[TENSORS];
+  base[0] = static_cast<const T*>(a.x.p) + w.head * a.x.h + ch;
+  base[1] = static_cast<const T*>(a.z.p) + w.head * a.z.h + ch;
+  pitch[0] = a.x.t;
+  pitch[1] = a.z.t;
+  if (BWD) {
+    base[TENSORS - 1] = static_cast<const T*>(a.d.p) + w.head * a.d.h + ch;
+    pitch[TENSORS - 1] = a.d.t;
+  }
+  struct Raw8 {
+    uint4 q[Q];
+  };
+  auto load = [&](int tok, Raw8* r) {            // zeros where there is nothing
+#pragma unroll
+    for (int k = 0; k < TENSORS; ++k) {
+#pragma unroll
+      for (int i = 0; i < Q; ++i) r[k].q[i] = make_uint4(0, 0, 0, 0);
+      if (mine && tok < a.tokens) {
+        int64_t at = tok * pitch[k];
+        if (!a.flat && k < 2) {
+          const int b = tok / a.T;
+          at = b * (k == 0 ? a.x.b : a.z.b) + (tok - b * a.T) * pitch[k];
+        }
+        const uint4* p = reinterpret_cast<const uint4*>(base[k] + at);
+#pragma unroll
+        for (int i = 0; i < Q; ++i) r[k].q[i] = __ldcs(p + i);
+      }
+    }
+  };
+  auto pairs = [](const Raw8& r, float2* f) {
+    const uint32_t* u = reinterpret_cast<const uint32_t*>(r.q);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      f[i] = sizeof(T) == 2 ? unpack2(u[i])
+                            : make_float2(__uint_as_float(u[(2 * i) % (4 * Q)]),
+                                          __uint_as_float(u[(2 * i + 1) % (4 * Q)]));
+  };
+  float2 wt[4], acc[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) wt[i] = make_float2(1.f, 1.f), acc[i] = make_float2(0.f, 0.f);
+  if (a.w && mine) {
+    float f[8];
+    load_run<float, 8>(a.w + (a.per_head ? (size_t)w.head * a.D : 0) + ch, f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) wt[i] = make_float2(f[2 * i], f[2 * i + 1]);
+  }
+  Raw8 next[UN][TENSORS];
+#pragma unroll
+  for (int u = 0; u < UN; ++u) load(w.tok + u * w.step, next[u]);
+  for (int it = 0; it < w.iters; it += UN) {
+    const int tok0 = w.tok + it * w.step;
+    Raw8 raw[UN][TENSORS];
+#pragma unroll
+    for (int u = 0; u < UN; ++u)
+#pragma unroll
+      for (int k = 0; k < TENSORS; ++k) raw[u][k] = next[u][k];
+    if (it + UN < w.iters)
+#pragma unroll
+      for (int u = 0; u < UN; ++u) load(tok0 + (UN + u) * w.step, next[u]);
+    // p, q: forward a, or x a with the gate before the norm. Backward d a and d w a' (behind);
+    // a and x a' (before).
+    float2 p[UN][4], q[BWD ? UN : 1][4];
+    float s[UN][2];
+#pragma unroll
+    for (int u = 0; u < UN; ++u) {
+      float2 x[4], z[4], d[4], ss = make_float2(0.f, 0.f), se = make_float2(0.f, 0.f);
+      pairs(raw[u][0], x);
+      pairs(raw[u][1], z);
+      if (BWD) pairs(raw[u][TENSORS - 1], d);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float2 g, slope;
+        g.x = act(z[i].x, a.kind, slope.x);
+        g.y = act(z[i].y, a.kind, slope.y);
+        const float2 v = FIRST ? mul2(x[i], g) : x[i];
+        ss = fma2(v, v, ss);
+        if (!BWD) {
+          p[u][i] = FIRST ? v : g;
+        } else if (FIRST) {
+          p[u][i] = g;
+          q[u][i] = mul2(x[i], slope);
+          se = fma2(mul2(d[i], wt[i]), v, se);
+        } else {
+          p[u][i] = mul2(d[i], g);
+          q[u][i] = mul2(mul2(d[i], wt[i]), slope);
+          se = fma2(mul2(p[u][i], wt[i]), v, se);
+        }
+      }
+      s[u][0] = ss.x + ss.y;
+      s[u][1] = se.x + se.y;
+    }
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1)
+#pragma unroll
+      for (int u = 0; u < UN; ++u) {
+        s[u][0] += __shfl_xor_sync(~0u, s[u][0], o);
+        if (BWD) s[u][1] += __shfl_xor_sync(~0u, s[u][1], o);
+      }
+#pragma unroll
+    for (int u = 0; u < UN; ++u) {
+      const int tok = tok0 + u * w.step;
+      const float r = rsqrtf(fmaf(s[u][0], a.inv_d, a.eps)), m = -s[u][1] * a.inv_d * r;
+      const float2 r2 = make_float2(r, r), m2 = make_float2(m, m);
+      float2 x[4], d[4];
+      float o[8], oz[8];
+      pairs(raw[u][0], x);
+      if (BWD) pairs(raw[u][TENSORS - 1], d);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float2 y, yz;
+        if (!BWD) {
+          y = FIRST ? mul2(mul2(p[u][i], r2), wt[i]) : mul2(mul2(mul2(x[i], r2), wt[i]), p[u][i]);
+        } else if (FIRST) {
+          const float2 un = mul2(mul2(x[i], p[u][i]), r2);
+          const float2 dv = mul2(r2, fma2(un, m2, mul2(d[i], wt[i])));
+          acc[i] = fma2(d[i], un, acc[i]);
+          y = mul2(dv, p[u][i]);
+          yz = mul2(dv, q[u][i]);
+        } else {
+          const float2 un = mul2(x[i], r2);
+          acc[i] = fma2(p[u][i], un, acc[i]);
+          y = mul2(r2, fma2(un, m2, mul2(p[u][i], wt[i])));
+          yz = mul2(un, q[u][i]);
+        }
+        o[2 * i] = y.x;
+        o[2 * i + 1] = y.y;
+        if (BWD) {
+          oz[2 * i] = yz.x;
+          oz[2 * i + 1] = yz.y;
+        }
+      }
+      if (mine && tok < a.tokens) {
+        const size_t dense = ((size_t)tok * a.H + w.head) * a.D + ch;
+        store_run<T, 8>(static_cast<T*>(BWD ? a.dx : a.y) + dense, o);
+        if (BWD) store_run<T, 8>(static_cast<T*>(a.dz) + dense, oz);
+      }
+    }
+  }
+  if (!BWD || !a.part) return;
+  float sum[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) sum[2 * i] = acc[i].x, sum[2 * i + 1] = acc[i].y;
+  if (!a.per_head) sum_groups<S>(sum, sums, w.tid);
+  if (ch >= a.D || (a.per_head ? !w.on : threadIdx.x >= LANES)) return;
+  float* to = a.part + (a.per_head ? ((size_t)w.tok * a.H + w.head) * a.D : (size_t)blockIdx.x * a.D);
+  store_run<float, 8>(to + ch, sum);
 }
 
 template <class S, bool BWD>
@@ -562,8 +728,8 @@ bool vec_view(const void* p, int dtype, int64_t b, int64_t t, int64_t h) {
 // Column sums of the parts, behind the kernel that writes them.
 gdr_status sum_parts(const float* part, float* o0, float* o1, float* o2, int rows, int cols,
                      cudaStream_t s) {
-  return launch_behind(column_sum_kernel, dim3((cols + 31) / 32, o1 || o2 ? 3 : 1), 32 * kSumRows,
-                       s, part, o0, o1, o2, rows, cols);
+  return launch_behind(column_sum_kernel, dim3((cols + kSumCols - 1) / kSumCols, o1 || o2 ? 3 : 1),
+                       kSumCols * kSumRows, s, part, o0, o1, o2, rows, cols);
 }
 gdr_status zero(float* p, size_t n, cudaStream_t s) {
   return !p || n == 0 ? GDR_OK : status_of(cudaMemsetAsync(p, 0, n * sizeof(float), s));
@@ -585,12 +751,15 @@ gdr_status check(const gdr_gated_dims* d) {
   return GDR_OK;
 }
 
-constexpr int kFwdPerSm = 1024, kBwdPerSm = 768;
+// Threads that an SM is to hold: of the kernels above, and of gated_rows_kernel.
+constexpr int kFwdPerSm = 1024, kBwdPerSm = 768, kFwdRowsPerSm = 768, kBwdRowsPerSm = 512;
 
 Plan gated_plan(const gdr_gated_dims* d, bool vec, bool bwd) {
   const int in = d->in_dtype == GDR_BF16 ? 1 : 2, out = d->out_dtype == GDR_BF16 ? 1 : 2;
   return make_plan(d->B * d->T, d->H, d->D, 2 * in + (bwd ? out : 0), vec, true,
-                   d->weight_per_head != 0, bwd ? kBwdPerSm : kFwdPerSm);
+                   d->weight_per_head != 0,
+                   vec && d->D <= 256 ? (bwd ? kBwdRowsPerSm : kFwdRowsPerSm)
+                                      : (bwd ? kBwdPerSm : kFwdPerSm));
 }
 size_t gated_bytes(const gdr_gated_dims* d, const Plan& p) {
   const size_t cols = (size_t)d->D * (d->weight_per_head ? d->H : 1);
@@ -608,6 +777,7 @@ gdr_status gated_args(GatedArgs& a, const gdr_gated_dims* d, const void* x, cons
   const int64_t b = d->B > 1, t = d->T > 1, h = d->H > 1;
   a.x = {x, b * d->x_stride_b, t * d->x_stride_t, h * d->x_stride_h};
   a.z = {gate, b * d->gate_stride_b, t * d->gate_stride_t, h * d->gate_stride_h};
+  a.flat = (a.B == 1 || (a.x.b == a.T * a.x.t && a.z.b == a.T * a.z.t)) ? 1 : 0;
   a.w = w;
   a.per_head = d->weight_per_head != 0;
   a.kind = d->activation;
@@ -626,6 +796,19 @@ gdr_status launch_gated(GatedArgs& a, const Plan& p, cudaStream_t s) {
   a.groups = p.groups;
   a.pieces = p.pieces;
   a.stages = p.stages;
+  if (p.lanes && p.v == 8 && a.in_bf16 == a.out_bf16)
+    return with_dtype(a.in_bf16 ? GDR_BF16 : GDR_F32, [&](auto* t) {
+      using T = std::remove_pointer_t<decltype(t)>;
+      auto go = [&](auto lanes) {
+        constexpr int L = decltype(lanes)::value;
+        return launch_kernel(a.first ? gated_rows_kernel<T, L, BWD, true>
+                                     : gated_rows_kernel<T, L, BWD, false>,
+                             dim3(p.blocks), p.threads, 0, s, a);
+      };
+      return p.lanes == 8    ? go(std::integral_constant<int, 8>())
+             : p.lanes == 16 ? go(std::integral_constant<int, 16>())
+                             : go(std::integral_constant<int, 32>());
+    });
   return with_shape(p, [&](auto shape) {
     using S = decltype(shape);
     struct Tag;

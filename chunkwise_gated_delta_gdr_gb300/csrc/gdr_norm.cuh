@@ -103,9 +103,17 @@ __device__ __forceinline__ void store_any(void* p, int64_t i, int is_bf16, const
 
 // act(z) and its derivative.
 enum Act { kNone = GDR_ACT_NONE, kSigmoid = GDR_ACT_SIGMOID, kSilu = GDR_ACT_SILU };
+// 1 / (1 + e^-z) by the approximate 2^x and reciprocal (2^-22 each, and the rounding of z log2(e),
+// half an ulp of it; 0 for z < -88).
+__device__ __forceinline__ float sigmoid(float z) {
+  float e, g;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(g) : "f"(1.f + e));
+  return g;
+}
 __device__ __forceinline__ float act(float z, int kind) {
   if (kind == kNone) return z;
-  const float g = __fdividef(1.f, 1.f + __expf(-z));
+  const float g = sigmoid(z);
   return kind == kSigmoid ? g : z * g;
 }
 __device__ __forceinline__ float act(float z, int kind, float& slope) {
@@ -113,7 +121,7 @@ __device__ __forceinline__ float act(float z, int kind, float& slope) {
     slope = 1.f;
     return z;
   }
-  const float g = __fdividef(1.f, 1.f + __expf(-z)), h = 1.f - g;
+  const float g = sigmoid(z), h = 1.f - g;
   slope = kind == kSigmoid ? g * h : fmaf(z * g, h, g);
   return kind == kSigmoid ? g : z * g;
 }
@@ -228,31 +236,33 @@ struct Row {
   }
 };
 
-// Column sums of part [which][rows][cols] into out<which>.
-constexpr int kSumRows = 32;
-__global__ void __launch_bounds__(32 * kSumRows) column_sum_kernel(const float* part, float* out0,
-                                                                   float* out1, float* out2,
-                                                                   int rows, int cols) {
-  __shared__ float s[kSumRows][33];
+// Column sums of part [which][rows][cols] into out<which>. A block takes 8 columns (a sector of
+// a row) and its 64 rows of threads share the parts, so that few loads follow one another.
+constexpr int kSumCols = 8, kSumRows = 64;
+__global__ void __launch_bounds__(kSumCols * kSumRows) column_sum_kernel(const float* part,
+                                                                         float* out0, float* out1,
+                                                                         float* out2, int rows,
+                                                                         int cols) {
+  __shared__ float s[kSumRows][kSumCols + 1];
   asm volatile("griddepcontrol.wait;" ::: "memory");       // the parts are written
-  const int lane = threadIdx.x & 31, r0 = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane, which = blockIdx.y;
+  const int x = threadIdx.x % kSumCols, r0 = threadIdx.x / kSumCols;
+  const int c = blockIdx.x * kSumCols + x, which = blockIdx.y;
   float* out = which == 0 ? out0 : which == 1 ? out1 : out2;
   if (!out) return;
   const float* p = part + (size_t)which * rows * cols;
   float v = 0.f;
   if (c < cols) {
-#pragma unroll 4
+#pragma unroll 8
     for (int r = r0; r < rows; r += kSumRows) v += p[(size_t)r * cols + c];
   }
-  s[r0][lane] = v;
+  s[r0][x] = v;
   __syncthreads();
-  if (r0 == 0) {
-    v = 0.f;
 #pragma unroll
-    for (int r = 0; r < kSumRows; ++r) v += s[r][lane];
-    if (c < cols) out[c] = v;
+  for (int n = kSumRows / 2; n > 0; n >>= 1) {
+    if (r0 < n) s[r0][x] += s[r0 + n][x];
+    __syncthreads();
   }
+  if (r0 == 0 && c < cols) out[c] = s[0][x];
 }
 
 }  // namespace
