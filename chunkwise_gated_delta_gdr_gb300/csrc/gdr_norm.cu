@@ -58,21 +58,24 @@ __device__ __forceinline__ void sum_groups(float* acc, float* s, int tid) {
   }
 }
 
-// Rows of at most 256 channels: a group of LANES lanes per row, 8 channels a lane, UN rows at a
-// time (the group's head in UN tokens), the next ones' loads under way meanwhile. What bounds the
-// larger calls beside HBM is the number of instructions per row, so addresses step from row to
-// row and sums and products go in pairs; the copies through shared memory that wider rows take
-// cost twice the time here (2 x 8192 x 32 heads of 128 forward: 115 us so, TIME now).
-template <typename T, int LANES, bool BWD, bool FIRST>
+// Rows of at most 512 channels: a group of LANES lanes per row, NV runs of 8 channels a lane, UN
+// rows at a time (the group's head in UN tokens), the next ones' loads under way meanwhile. What
+// bounds the larger calls beside HBM is the number of instructions per row, so addresses step
+// from row to row and sums and products go in pairs; the copies through shared memory that wider
+// rows take cost twice the time here (2 x 8192 x 32 heads of 128 forward: 115 us so, 57 now).
+template <typename T, int LANES, int NV, bool BWD, bool FIRST>
 __global__ void __launch_bounds__(256, BWD ? 2 : 3) gated_rows_kernel(GatedArgs a) {
-  typedef Shape<LANES, 8, 1> S;
-  constexpr int TENSORS = BWD ? 3 : 2, UN = sizeof(T) == 2 ? 2 : 1;
+  typedef Shape<LANES, 8, NV> S;
+  constexpr int TENSORS = BWD ? 3 : 2, UN = sizeof(T) == 2 && NV == 1 ? 2 : 1, N = 4 * NV;
   constexpr int Q = 8 * sizeof(T) / 16;          // 16-byte pieces of 8 channels
-  __shared__ float sums[BWD ? 8 * 32 * 8 : 1];
+  constexpr bool AHEAD = NV == 1 || !BWD;        // else there are no registers for the next rows
+  __shared__ float sums[BWD ? 8 * 32 * 8 * NV : 1];
   if (BWD) asm volatile("griddepcontrol.launch_dependents;");
   const Walk w = walk_of<LANES>(a.tokens, a.H, a.groups);
+  bool mine[NV];
+#pragma unroll
+  for (int c = 0; c < NV; ++c) mine[c] = w.on && (c * LANES + w.tid) * 8 < a.D;
   const int ch = w.tid * 8;
-  const bool mine = w.on && ch < a.D;
   const T* base[TENSORS];
   int64_t pitch[TENSORS];
   base[0] = static_cast<const T*>(a.x.p) + w.head * a.x.h + ch;
@@ -83,68 +86,73 @@ __global__ void __launch_bounds__(256, BWD ? 2 : 3) gated_rows_kernel(GatedArgs 
     base[TENSORS - 1] = static_cast<const T*>(a.d.p) + w.head * a.d.h + ch;
     pitch[TENSORS - 1] = a.d.t;
   }
-  struct Raw8 {
-    uint4 q[Q];
+  struct Raw {
+    uint4 q[NV * Q];
   };
-  auto load = [&](int tok, Raw8* r) {            // zeros where there is nothing
+  auto load = [&](int tok, Raw* r) {             // zeros where there is nothing
 #pragma unroll
     for (int k = 0; k < TENSORS; ++k) {
+      int64_t at = tok * pitch[k];
+      if (!a.flat && k < 2) {
+        const int b = tok / a.T;
+        at = b * (k == 0 ? a.x.b : a.z.b) + (tok - b * a.T) * pitch[k];
+      }
 #pragma unroll
-      for (int i = 0; i < Q; ++i) r[k].q[i] = make_uint4(0, 0, 0, 0);
-      if (mine && tok < a.tokens) {
-        int64_t at = tok * pitch[k];
-        if (!a.flat && k < 2) {
-          const int b = tok / a.T;
-          at = b * (k == 0 ? a.x.b : a.z.b) + (tok - b * a.T) * pitch[k];
-        }
-        const uint4* p = reinterpret_cast<const uint4*>(base[k] + at);
+      for (int c = 0; c < NV; ++c) {
+        const uint4* p = reinterpret_cast<const uint4*>(base[k] + at + c * LANES * 8);
 #pragma unroll
-        for (int i = 0; i < Q; ++i) r[k].q[i] = __ldcs(p + i);
+        for (int i = 0; i < Q; ++i)
+          r[k].q[c * Q + i] = mine[c] && tok < a.tokens ? __ldcs(p + i) : make_uint4(0, 0, 0, 0);
       }
     }
   };
-  auto pairs = [](const Raw8& r, float2* f) {
+  auto pairs = [](const Raw& r, float2* f) {
     const uint32_t* u = reinterpret_cast<const uint32_t*>(r.q);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < N; ++i)
       f[i] = sizeof(T) == 2 ? unpack2(u[i])
-                            : make_float2(__uint_as_float(u[(2 * i) % (4 * Q)]),
-                                          __uint_as_float(u[(2 * i + 1) % (4 * Q)]));
+                            : make_float2(__uint_as_float(u[(2 * i) % (4 * NV * Q)]),
+                                          __uint_as_float(u[(2 * i + 1) % (4 * NV * Q)]));
   };
-  float2 wt[4], acc[4];
+  float2 wt[N], acc[N];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) wt[i] = make_float2(1.f, 1.f), acc[i] = make_float2(0.f, 0.f);
-  if (a.w && mine) {
-    float f[8];
-    load_run<float, 8>(a.w + (a.per_head ? (size_t)w.head * a.D : 0) + ch, f);
+  for (int i = 0; i < N; ++i) wt[i] = make_float2(1.f, 1.f), acc[i] = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) wt[i] = make_float2(f[2 * i], f[2 * i + 1]);
-  }
-  Raw8 next[UN][TENSORS];
+  for (int c = 0; c < NV; ++c)
+    if (a.w && mine[c]) {
+      float f[8];
+      load_run<float, 8, true>(a.w + (a.per_head ? (size_t)w.head * a.D : 0) + ch + c * LANES * 8, f);
 #pragma unroll
-  for (int u = 0; u < UN; ++u) load(w.tok + u * w.step, next[u]);
+      for (int i = 0; i < 4; ++i) wt[4 * c + i] = make_float2(f[2 * i], f[2 * i + 1]);
+    }
+  Raw next[UN][TENSORS];
+  if (AHEAD)
+#pragma unroll
+    for (int u = 0; u < UN; ++u) load(w.tok + u * w.step, next[u]);
   for (int it = 0; it < w.iters; it += UN) {
     const int tok0 = w.tok + it * w.step;
-    Raw8 raw[UN][TENSORS];
+    Raw raw[UN][TENSORS];
 #pragma unroll
-    for (int u = 0; u < UN; ++u)
+    for (int u = 0; u < UN; ++u) {
+      if (!AHEAD) load(tok0 + u * w.step, next[u]);
 #pragma unroll
       for (int k = 0; k < TENSORS; ++k) raw[u][k] = next[u][k];
-    if (it + UN < w.iters)
+    }
+    if (AHEAD && it + UN < w.iters)
 #pragma unroll
       for (int u = 0; u < UN; ++u) load(tok0 + (UN + u) * w.step, next[u]);
     // p, q: forward a, or x a with the gate before the norm. Backward d a and d w a' (behind);
     // a and x a' (before).
-    float2 p[UN][4], q[BWD ? UN : 1][4];
+    float2 p[UN][N], q[BWD ? UN : 1][N];
     float s[UN][2];
 #pragma unroll
     for (int u = 0; u < UN; ++u) {
-      float2 x[4], z[4], d[4], ss = make_float2(0.f, 0.f), se = make_float2(0.f, 0.f);
+      float2 x[N], z[N], d[N], ss = make_float2(0.f, 0.f), se = make_float2(0.f, 0.f);
       pairs(raw[u][0], x);
       pairs(raw[u][1], z);
       if (BWD) pairs(raw[u][TENSORS - 1], d);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < N; ++i) {
         float2 g, slope;
         g.x = act(z[i].x, a.kind, slope.x);
         g.y = act(z[i].y, a.kind, slope.y);
@@ -177,51 +185,62 @@ __global__ void __launch_bounds__(256, BWD ? 2 : 3) gated_rows_kernel(GatedArgs 
       const int tok = tok0 + u * w.step;
       const float r = rsqrtf(fmaf(s[u][0], a.inv_d, a.eps)), m = -s[u][1] * a.inv_d * r;
       const float2 r2 = make_float2(r, r), m2 = make_float2(m, m);
-      float2 x[4], d[4];
-      float o[8], oz[8];
+      const size_t dense = ((size_t)tok * a.H + w.head) * a.D + ch;
+      float2 x[N], d[N];
       pairs(raw[u][0], x);
       if (BWD) pairs(raw[u][TENSORS - 1], d);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float2 y, yz;
-        if (!BWD) {
-          y = FIRST ? mul2(mul2(p[u][i], r2), wt[i]) : mul2(mul2(mul2(x[i], r2), wt[i]), p[u][i]);
-        } else if (FIRST) {
-          const float2 un = mul2(mul2(x[i], p[u][i]), r2);
-          const float2 dv = mul2(r2, fma2(un, m2, mul2(d[i], wt[i])));
-          acc[i] = fma2(d[i], un, acc[i]);
-          y = mul2(dv, p[u][i]);
-          yz = mul2(dv, q[u][i]);
-        } else {
-          const float2 un = mul2(x[i], r2);
-          acc[i] = fma2(p[u][i], un, acc[i]);
-          y = mul2(r2, fma2(un, m2, mul2(p[u][i], wt[i])));
-          yz = mul2(un, q[u][i]);
+      for (int c = 0; c < NV; ++c) {
+        float o[8], oz[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int i = 4 * c + j;
+          float2 y, yz;
+          if (!BWD) {
+            y = FIRST ? mul2(mul2(p[u][i], r2), wt[i])
+                      : mul2(mul2(mul2(x[i], r2), wt[i]), p[u][i]);
+          } else if (FIRST) {
+            const float2 un = mul2(mul2(x[i], p[u][i]), r2);
+            const float2 dv = mul2(r2, fma2(un, m2, mul2(d[i], wt[i])));
+            acc[i] = fma2(d[i], un, acc[i]);
+            y = mul2(dv, p[u][i]);
+            yz = mul2(dv, q[u][i]);
+          } else {
+            const float2 un = mul2(x[i], r2);
+            acc[i] = fma2(p[u][i], un, acc[i]);
+            y = mul2(r2, fma2(un, m2, mul2(p[u][i], wt[i])));
+            yz = mul2(un, q[u][i]);
+          }
+          o[2 * j] = y.x;
+          o[2 * j + 1] = y.y;
+          if (BWD) {
+            oz[2 * j] = yz.x;
+            oz[2 * j + 1] = yz.y;
+          }
         }
-        o[2 * i] = y.x;
-        o[2 * i + 1] = y.y;
-        if (BWD) {
-          oz[2 * i] = yz.x;
-          oz[2 * i + 1] = yz.y;
+        if (mine[c] && tok < a.tokens) {
+          store_run<T, 8>(static_cast<T*>(BWD ? a.dx : a.y) + dense + c * LANES * 8, o);
+          if (BWD) store_run<T, 8>(static_cast<T*>(a.dz) + dense + c * LANES * 8, oz);
         }
-      }
-      if (mine && tok < a.tokens) {
-        const size_t dense = ((size_t)tok * a.H + w.head) * a.D + ch;
-        store_run<T, 8>(static_cast<T*>(BWD ? a.dx : a.y) + dense, o);
-        if (BWD) store_run<T, 8>(static_cast<T*>(a.dz) + dense, oz);
       }
     }
   }
-  if (!BWD || !a.part) return;
-  float sum[8];
+  if constexpr (BWD) {
+    if (!a.part) return;
+    float sum[8 * NV];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) sum[2 * i] = acc[i].x, sum[2 * i + 1] = acc[i].y;
-  if (!a.per_head) sum_groups<S>(sum, sums, w.tid);
-  if (ch >= a.D || (a.per_head ? !w.on : threadIdx.x >= LANES)) return;
-  float* to = a.part + (a.per_head ? ((size_t)w.tok * a.H + w.head) * a.D : (size_t)blockIdx.x * a.D);
-  store_run<float, 8>(to + ch, sum);
+    for (int i = 0; i < N; ++i) sum[2 * i] = acc[i].x, sum[2 * i + 1] = acc[i].y;
+    if (!a.per_head) sum_groups<S>(sum, sums, w.tid);
+    if (a.per_head ? !w.on : threadIdx.x >= LANES) return;
+    float* to =
+        a.part + (a.per_head ? ((size_t)w.tok * a.H + w.head) * a.D : (size_t)blockIdx.x * a.D);
+#pragma unroll
+    for (int c = 0; c < NV; ++c)
+      if (ch + c * LANES * 8 < a.D) store_run<float, 8>(to + ch + c * LANES * 8, sum + 8 * c);
+  }
 }
 
+// Any other row: wider ones, a block each, and those that do not allow 16-byte accesses.
 template <class S, bool BWD>
 __global__ void __launch_bounds__(kMaxThreads) gated_kernel(GatedArgs a) {
   constexpr int V = S::V, NV = S::NV, N = S::N, TENSORS = BWD ? 3 : 2;
@@ -236,7 +255,7 @@ __global__ void __launch_bounds__(kMaxThreads) gated_kernel(GatedArgs a) {
 #pragma unroll
   for (int j = 0; j < N; ++j) acc[j] = 0.f;
 
-  Row<S> row[TENSORS];
+  Row<S, S::NV <= 4> row[TENSORS];
   auto rows_of = [&](int it) {                   // false: no such row
     const int tok = w.tok + it * w.step;
     if (!w.on || tok >= a.tokens) return false;
@@ -282,7 +301,7 @@ __global__ void __launch_bounds__(kMaxThreads) gated_kernel(GatedArgs a) {
         if (a.first || BWD) row[1].get(ahead, stage, c, i, z);
         if (BWD) {
           row[TENSORS - 1].get(ahead, stage, c, i, d);
-          if (weight) load_run<float, V>(weight + i, wt);
+          if (weight) load_run<float, V, true>(weight + i, wt);
         }
 #pragma unroll
         for (int e = 0; e < V; ++e) {
@@ -307,7 +326,7 @@ __global__ void __launch_bounds__(kMaxThreads) gated_kernel(GatedArgs a) {
       row[1].get(ahead, stage, c, i, z);
       if (BWD) row[TENSORS - 1].get(ahead, stage, c, i, d);
       if (weight) {
-        load_run<float, V>(weight + i, wt);
+        load_run<float, V, true>(weight + i, wt);
       } else {
 #pragma unroll
         for (int e = 0; e < V; ++e) wt[e] = 1.f;
@@ -372,7 +391,8 @@ __global__ void __launch_bounds__(kMaxThreads) residual_fwd_kernel(ResArgs a) {
   __shared__ Red red;
   const Walk w = walk_of<0>(a.tokens, 1, gridDim.x);
   const Ahead ahead = {places, a.pieces, a.stages};
-  Row<S> rr, ry, rz;
+  Row<S, false> rr;                              // may be the result's own memory
+  Row<S, S::NV <= 4> ry, rz;
   auto rows_of = [&](int it) {
     const int tok = w.tok + it * w.step;
     if (tok >= a.tokens) return false;
@@ -435,7 +455,7 @@ __global__ void __launch_bounds__(kMaxThreads) residual_fwd_kernel(ResArgs a) {
 #pragma unroll
         for (int e = 0; e < V; ++e) y[e] *= py;
         if (a.wp) {
-          load_run<float, V>(a.wp + i, k);
+          load_run<float, V, true>(a.wp + i, k);
 #pragma unroll
           for (int e = 0; e < V; ++e) y[e] *= k[e];
         }
@@ -445,7 +465,7 @@ __global__ void __launch_bounds__(kMaxThreads) residual_fwd_kernel(ResArgs a) {
           for (int e = 0; e < V; ++e) y[e] *= act(k[e], a.kind);
         }
         if (a.sv) {
-          load_run<float, V>(a.sv + i, k);
+          load_run<float, V, true>(a.sv + i, k);
 #pragma unroll
           for (int e = 0; e < V; ++e) x[e] = fmaf(k[e], y[e], x[e]);
         } else {
@@ -467,7 +487,7 @@ __global__ void __launch_bounds__(kMaxThreads) residual_fwd_kernel(ResArgs a) {
 #pragma unroll
       for (int e = 0; e < V; ++e) o[e] = r[c * V + e] * rho;
       if (a.w) {
-        load_run<float, V>(a.w + i, k);
+        load_run<float, V, true>(a.w + i, k);
 #pragma unroll
         for (int e = 0; e < V; ++e) o[e] *= k[e];
       }
@@ -490,7 +510,7 @@ __global__ void __launch_bounds__(kMaxThreads) residual_bwd_kernel(ResArgs a) {
   for (int k = 0; k < (FULL ? 3 : 1); ++k)
 #pragma unroll
     for (int j = 0; j < N; ++j) acc[k][j] = 0.f;
-  Row<S> rr, rd, rg, ry, rz;
+  Row<S, S::NV <= 4> rr, rd, rg, ry, rz;
   auto rows_of = [&](int it) {
     const int tok = w.tok + it * w.step;
     if (tok >= a.tokens) return false;
@@ -541,7 +561,7 @@ __global__ void __launch_bounds__(kMaxThreads) residual_bwd_kernel(ResArgs a) {
       rr.get(ahead, stage, c, i, x);
       rd.get(ahead, stage, c, i, d);
       if (a.w) {
-        load_run<float, V>(a.w + i, k);
+        load_run<float, V, true>(a.w + i, k);
 #pragma unroll
         for (int e = 0; e < V; ++e) d[e] *= k[e];
       }
@@ -574,7 +594,7 @@ __global__ void __launch_bounds__(kMaxThreads) residual_bwd_kernel(ResArgs a) {
         for (int e = 0; e < V; ++e) g[e] = 0.f;
       }
       if (a.w) {
-        load_run<float, V>(a.w + i, k);
+        load_run<float, V, true>(a.w + i, k);
       } else {
 #pragma unroll
         for (int e = 0; e < V; ++e) k[e] = 1.f;
@@ -600,13 +620,13 @@ __global__ void __launch_bounds__(kMaxThreads) residual_bwd_kernel(ResArgs a) {
 #pragma unroll
         for (int e = 0; e < V; ++e) y[e] *= py;
         if (a.wp) {
-          load_run<float, V>(a.wp + i, wp);
+          load_run<float, V, true>(a.wp + i, wp);
         } else {
 #pragma unroll
           for (int e = 0; e < V; ++e) wp[e] = 1.f;
         }
         if (a.has_z) rz.get(ahead, stage, c, i, z);
-        if (a.sv) load_run<float, V>(a.sv + i, k);
+        if (a.sv) load_run<float, V, true>(a.sv + i, k);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
           const int j = c * V + e;
@@ -671,7 +691,7 @@ struct Plan {
 template <typename F>
 auto with_block(const Plan& p, F f) {
   if (p.v == 8) return p.nv == 2 ? f(Shape<0, 8, 2>()) : f(Shape<0, 8, 4>());
-  return p.nv == 16 ? f(Shape<0, 1, 16>()) : f(Shape<0, 1, 32>());
+  return p.nv == 4 ? f(Shape<0, 1, 4>()) : p.nv == 16 ? f(Shape<0, 1, 16>()) : f(Shape<0, 1, 32>());
 }
 template <typename F>
 auto with_shape(const Plan& p, F f) {
@@ -679,7 +699,8 @@ auto with_shape(const Plan& p, F f) {
   if (p.v == 1) return f(Shape<32, 1, 8>());
   return p.lanes == 8    ? f(Shape<8, 8, 1>())
          : p.lanes == 16 ? f(Shape<16, 8, 1>())
-                         : f(Shape<32, 8, 1>());
+         : p.nv == 1     ? f(Shape<32, 8, 1>())
+                         : f(Shape<32, 8, 2>());
 }
 
 // pieces: 16-byte pieces per run of 8, over all tensors of a row. vec: whether 16-byte accesses
@@ -688,15 +709,17 @@ Plan make_plan(int tokens, int H, int D, int pieces, bool vec, bool lanes_ok, bo
                int per_sm) {
   Plan p = {};
   p.v = vec ? 8 : 1;
-  p.lanes = !lanes_ok || D > 256 ? 0 : !vec || D > 128 ? 32 : D > 64 ? 16 : 8;
+  p.lanes = !lanes_ok || D > (vec ? 512 : 256) ? 0 : !vec || D > 128 ? 32 : D > 64 ? 16 : 8;
   int per_block = 1;                             // groups of a block
   if (p.lanes) {
-    p.nv = vec ? 1 : 8;
+    p.nv = !vec ? 8 : D > 256 ? 2 : 1;
     p.threads = 256;
     per_block = p.threads / p.lanes;
   } else {
-    const int two = vec ? 16 : 16;               // elements of a thread, but for the widest rows
-    p.nv = D <= kMaxThreads * two ? (vec ? 2 : 16) : (vec ? 4 : 32);
+    // Elements of a thread: 16, 32 in the widest rows, 4 in short ones element by element (more
+    // threads then have more loads under way).
+    p.nv = vec ? (D <= kMaxThreads * 16 ? 2 : 4)
+               : D <= kMaxThreads * 4 ? 4 : D <= kMaxThreads * 16 ? 16 : 32;
     const int n = p.nv * p.v;
     p.threads = ((D + n - 1) / n + 31) / 32 * 32;
   }
@@ -751,14 +774,16 @@ gdr_status check(const gdr_gated_dims* d) {
   return GDR_OK;
 }
 
-// Threads that an SM is to hold: of the kernels above, and of gated_rows_kernel.
-constexpr int kFwdPerSm = 1024, kBwdPerSm = 768, kFwdRowsPerSm = 768, kBwdRowsPerSm = 512;
+// Threads that an SM is to hold: of the kernels above (kFullPerSm: the residual's backward with a
+// norm, gate or scale per channel, at most kBwdPerSm), and of gated_rows_kernel.
+constexpr int kFwdPerSm = 1024, kBwdPerSm = 768, kFullPerSm = 512;
+constexpr int kFwdRowsPerSm = 768, kBwdRowsPerSm = 512;
 
 Plan gated_plan(const gdr_gated_dims* d, bool vec, bool bwd) {
   const int in = d->in_dtype == GDR_BF16 ? 1 : 2, out = d->out_dtype == GDR_BF16 ? 1 : 2;
   return make_plan(d->B * d->T, d->H, d->D, 2 * in + (bwd ? out : 0), vec, true,
                    d->weight_per_head != 0,
-                   vec && d->D <= 256 ? (bwd ? kBwdRowsPerSm : kFwdRowsPerSm)
+                   vec && d->D <= 512 ? (bwd ? kBwdRowsPerSm : kFwdRowsPerSm)
                                       : (bwd ? kBwdPerSm : kFwdPerSm));
 }
 size_t gated_bytes(const gdr_gated_dims* d, const Plan& p) {
@@ -799,15 +824,16 @@ gdr_status launch_gated(GatedArgs& a, const Plan& p, cudaStream_t s) {
   if (p.lanes && p.v == 8 && a.in_bf16 == a.out_bf16)
     return with_dtype(a.in_bf16 ? GDR_BF16 : GDR_F32, [&](auto* t) {
       using T = std::remove_pointer_t<decltype(t)>;
-      auto go = [&](auto lanes) {
-        constexpr int L = decltype(lanes)::value;
-        return launch_kernel(a.first ? gated_rows_kernel<T, L, BWD, true>
-                                     : gated_rows_kernel<T, L, BWD, false>,
+      auto go = [&](auto shape) {
+        using S = decltype(shape);
+        return launch_kernel(a.first ? gated_rows_kernel<T, S::LANES, S::NV, BWD, true>
+                                     : gated_rows_kernel<T, S::LANES, S::NV, BWD, false>,
                              dim3(p.blocks), p.threads, 0, s, a);
       };
-      return p.lanes == 8    ? go(std::integral_constant<int, 8>())
-             : p.lanes == 16 ? go(std::integral_constant<int, 16>())
-                             : go(std::integral_constant<int, 32>());
+      return p.lanes == 8    ? go(Shape<8, 8, 1>())
+             : p.lanes == 16 ? go(Shape<16, 8, 1>())
+             : p.nv == 1     ? go(Shape<32, 8, 1>())
+                             : go(Shape<32, 8, 2>());
     });
   return with_shape(p, [&](auto shape) {
     using S = decltype(shape);
@@ -831,8 +857,8 @@ gdr_status check(const gdr_residual_dims* d) {
 }
 
 // pieces: of all tensors of a row (see make_plan).
-Plan residual_plan(const gdr_residual_dims* d, bool vec, int pieces, bool bwd) {
-  return make_plan(d->B * d->T, 1, d->D, pieces, vec, false, false, bwd ? kBwdPerSm : kFwdPerSm);
+Plan residual_plan(const gdr_residual_dims* d, bool vec, int pieces, int per_sm) {
+  return make_plan(d->B * d->T, 1, d->D, pieces, vec, false, false, per_sm);
 }
 
 gdr_status residual_args(ResArgs& a, const gdr_residual_dims* d, const void* r, const void* y,
@@ -956,7 +982,7 @@ gdr_status gdr_residual_norm(const void* residual, const void* y, const void* ga
   a.out = out;
   a.r_out = residual_out;
   const int re = a.r_bf16 ? 1 : 2, ye = a.y_bf16 ? 1 : 2;
-  const Plan p = residual_plan(dims, vec, re + a.has_y * ye + a.has_z * ye, false);
+  const Plan p = residual_plan(dims, vec, re + a.has_y * ye + a.has_z * ye, kFwdPerSm);
   a.pieces = p.pieces;
   a.stages = p.stages;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -971,7 +997,8 @@ gdr_status gdr_residual_norm(const void* residual, const void* y, const void* ga
 
 size_t gdr_residual_norm_bwd_workspace_size(const gdr_residual_dims* dims) {
   if (check(dims) != GDR_OK) return 0;
-  const Plan v = residual_plan(dims, true, 1, true), o = residual_plan(dims, false, 1, true);
+  const Plan v = residual_plan(dims, true, 1, kBwdPerSm);
+  const Plan o = residual_plan(dims, false, 1, kBwdPerSm);
   const size_t rows = v.rows > o.rows ? v.rows : o.rows;
   const size_t bytes = align_up(3 * rows * dims->D * sizeof(float));
   return bytes ? bytes : kAlign;
@@ -1012,7 +1039,7 @@ gdr_status gdr_residual_norm_bwd(const void* d_out, const void* d_residual_out,
   a.has_dr = d_residual_out != nullptr;
   const int re = a.r_bf16 ? 1 : 2, ye = a.y_bf16 ? 1 : 2, oe = a.out_bf16 ? 1 : 2;
   const int pieces = re * (1 + a.has_dr) + oe + (full ? ye * (1 + a.has_z) : 0);
-  const Plan p = residual_plan(dims, vec, pieces, true);
+  const Plan p = residual_plan(dims, vec, pieces, full ? kFullPerSm : kBwdPerSm);
   if (d_weight || d_post_weight || d_scale) {
     if (!workspace || workspace_bytes < gdr_residual_norm_bwd_workspace_size(dims))
       return GDR_ERR_WORKSPACE;

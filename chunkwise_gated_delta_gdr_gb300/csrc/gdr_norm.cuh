@@ -51,17 +51,20 @@ __device__ __forceinline__ void unpack(const Run<T, V>& r, float* f) {
     for (int i = 0; i < V; ++i) f[i] = __uint_as_float(r.w[i]);
   }
 }
-template <typename T, int V>
+// ONLY_READ: nothing writes this memory while the kernel runs, so the load may move before any
+// store of it.
+template <typename T, int V, bool ONLY_READ = false>
 __device__ __forceinline__ void load_run(const T* p, float* f) {
   Run<T, V> r;
   if constexpr (V == 1 && sizeof(T) == 2) {
-    r.v = *p;
+    r.v = ONLY_READ ? __ldg(p) : *p;
   } else if constexpr (V == 1) {
-    r.w[0] = __float_as_uint(*p);
+    r.w[0] = __float_as_uint(ONLY_READ ? __ldg(p) : *p);
   } else {
 #pragma unroll
     for (int i = 0; i < V * (int)sizeof(T) / 16; ++i) {
-      const uint4 u = reinterpret_cast<const uint4*>(p)[i];
+      const uint4* q = reinterpret_cast<const uint4*>(p) + i;
+      const uint4 u = ONLY_READ ? __ldg(q) : *q;
       r.w[4 * i] = u.x;
       r.w[4 * i + 1] = u.y;
       r.w[4 * i + 2] = u.z;
@@ -86,12 +89,12 @@ __device__ __forceinline__ void store_run(T* p, const float* f) {
   }
 }
 // The same with the type known at run time only.
-template <int V>
+template <int V, bool ONLY_READ>
 __device__ __forceinline__ void load_any(const void* p, int64_t i, int is_bf16, float* f) {
   if (is_bf16)
-    load_run<bf16, V>(static_cast<const bf16*>(p) + i, f);
+    load_run<bf16, V, ONLY_READ>(static_cast<const bf16*>(p) + i, f);
   else
-    load_run<float, V>(static_cast<const float*>(p) + i, f);
+    load_run<float, V, ONLY_READ>(static_cast<const float*>(p) + i, f);
 }
 template <int V>
 __device__ __forceinline__ void store_any(void* p, int64_t i, int is_bf16, const float* f) {
@@ -207,7 +210,7 @@ struct Ahead {
 
 // One tensor of a row. With S::kAhead its runs come from the thread's places in shared memory,
 // from `first` on, where fetch() had them copied; without, from global memory.
-template <class S>
+template <class S, bool ONLY_READ>
 struct Row {
   const void* p;                                 // the row's first element
   int is_bf16, first;                            // first: its first piece within a stage
@@ -231,7 +234,7 @@ struct Row {
         unpack<float, 8>(r, f);
       }
     } else {
-      load_any<S::V>(p, i, is_bf16, f);
+      load_any<S::V, ONLY_READ>(p, i, is_bf16, f);
     }
   }
 };
