@@ -261,16 +261,13 @@ __global__ void __launch_bounds__(kMaxThreads) gated_kernel(GatedArgs a) {
     if (!w.on || tok >= a.tokens) return false;
     const int b = tok / a.T, t = tok - b * a.T;
     const int per = NV * (a.in_bf16 ? 1 : 2);
-    const size_t es = a.in_bf16 ? 2 : 4, os = a.out_bf16 ? 2 : 4;
-    row[0] = {static_cast<const char*>(a.x.p) + a.x.at(b, t, w.head) * es, a.in_bf16, 0};
-    row[1] = {static_cast<const char*>(a.z.p) + a.z.at(b, t, w.head) * es, a.in_bf16, per};
-    if (BWD)
-      row[TENSORS - 1] = {static_cast<const char*>(a.d.p) + a.d.at(b, t, w.head) * os, a.out_bf16,
-                          2 * per};
+    row[0].set(a.x.p, a.x.at(b, t, w.head), a.in_bf16, 0);
+    row[1].set(a.z.p, a.z.at(b, t, w.head), a.in_bf16, per);
+    if (BWD) row[TENSORS - 1].set(a.d.p, a.d.at(b, t, w.head), a.out_bf16, 2 * per);
     return true;
   };
   auto fetch = [&](int it, int stage) {
-    if constexpr (S::kAhead) {
+    if constexpr (S::kAhead || S::kRegs) {
       if (it < w.iters && rows_of(it)) {
 #pragma unroll
         for (int c = 0; c < NV; ++c) {
@@ -280,12 +277,14 @@ __global__ void __launch_bounds__(kMaxThreads) gated_kernel(GatedArgs a) {
             for (int k = 0; k < TENSORS; ++k) row[k].fetch(ahead, stage, c, i);
         }
       }
-      ptx::cp_async_commit();
+      if constexpr (S::kAhead) ptx::cp_async_commit();
     }
   };
   for (int i = 0; i + 1 < a.stages; ++i) fetch(i, i);
   int turn = 0, stage = 0;
   for (int it = 0; it < w.iters; ++it, stage = stage + 1 == a.stages ? 0 : stage + 1) {
+#pragma unroll
+    for (int k = 0; k < TENSORS; ++k) row[k].advance();
     fetch(it + a.stages - 1, stage == 0 ? a.stages - 1 : stage - 1);
     if constexpr (S::kAhead) ahead.wait();
     const bool on = rows_of(it);
@@ -398,13 +397,13 @@ __global__ void __launch_bounds__(kMaxThreads) residual_fwd_kernel(ResArgs a) {
     if (tok >= a.tokens) return false;
     const int b = tok / a.T, t = tok - b * a.T;
     const int rp = NV * (a.r_bf16 ? 1 : 2), yp = NV * (a.y_bf16 ? 1 : 2);
-    rr = {static_cast<const char*>(a.r.p) + a.r.at(b, t, 0) * (a.r_bf16 ? 2 : 4), a.r_bf16, 0};
-    ry = {static_cast<const char*>(a.y.p) + a.y.at(b, t, 0) * (a.y_bf16 ? 2 : 4), a.y_bf16, rp};
-    rz = {static_cast<const char*>(a.z.p) + a.z.at(b, t, 0) * (a.y_bf16 ? 2 : 4), a.y_bf16, rp + yp};
+    rr.set(a.r.p, a.r.at(b, t, 0), a.r_bf16, 0);
+    ry.set(a.y.p, a.y.at(b, t, 0), a.y_bf16, rp);
+    rz.set(a.z.p, a.z.at(b, t, 0), a.y_bf16, rp + yp);
     return true;
   };
   auto fetch = [&](int it, int stage) {
-    if constexpr (S::kAhead) {
+    if constexpr (S::kAhead || S::kRegs) {
       if (it < w.iters && rows_of(it)) {
 #pragma unroll
         for (int c = 0; c < NV; ++c) {
@@ -416,12 +415,13 @@ __global__ void __launch_bounds__(kMaxThreads) residual_fwd_kernel(ResArgs a) {
           }
         }
       }
-      ptx::cp_async_commit();
+      if constexpr (S::kAhead) ptx::cp_async_commit();
     }
   };
   for (int i = 0; i + 1 < a.stages; ++i) fetch(i, i);
   int turn = 0, stage = 0;
   for (int it = 0; it < w.iters; ++it, stage = stage + 1 == a.stages ? 0 : stage + 1) {
+    rr.advance(), ry.advance(), rz.advance();
     fetch(it + a.stages - 1, stage == 0 ? a.stages - 1 : stage - 1);
     if constexpr (S::kAhead) ahead.wait();
     if (!rows_of(it)) break;                     // the whole block
@@ -516,17 +516,16 @@ __global__ void __launch_bounds__(kMaxThreads) residual_bwd_kernel(ResArgs a) {
     if (tok >= a.tokens) return false;
     const int b = tok / a.T, t = tok - b * a.T;
     const int rp = NV * (a.r_bf16 ? 1 : 2), op = NV * (a.out_bf16 ? 1 : 2);
-    const int yp = NV * (a.y_bf16 ? 1 : 2), re = a.r_bf16 ? 2 : 4, ye = a.y_bf16 ? 2 : 4;
-    rr = {static_cast<const char*>(a.r.p) + a.r.at(b, t, 0) * re, a.r_bf16, 0};
-    rd = {static_cast<const char*>(a.d.p) + a.d.at(b, t, 0) * (a.out_bf16 ? 2 : 4), a.out_bf16, rp};
-    rg = {static_cast<const char*>(a.dr.p) + a.dr.at(b, t, 0) * re, a.r_bf16, rp + op};
-    const int at = rp + op + (a.has_dr ? rp : 0);
-    ry = {static_cast<const char*>(a.y.p) + a.y.at(b, t, 0) * ye, a.y_bf16, at};
-    rz = {static_cast<const char*>(a.z.p) + a.z.at(b, t, 0) * ye, a.y_bf16, at + yp};
+    const int yp = NV * (a.y_bf16 ? 1 : 2), at = rp + op + (a.has_dr ? rp : 0);
+    rr.set(a.r.p, a.r.at(b, t, 0), a.r_bf16, 0);
+    rd.set(a.d.p, a.d.at(b, t, 0), a.out_bf16, rp);
+    rg.set(a.dr.p, a.dr.at(b, t, 0), a.r_bf16, rp + op);
+    ry.set(a.y.p, a.y.at(b, t, 0), a.y_bf16, at);
+    rz.set(a.z.p, a.z.at(b, t, 0), a.y_bf16, at + yp);
     return true;
   };
   auto fetch = [&](int it, int stage) {
-    if constexpr (S::kAhead) {
+    if constexpr (S::kAhead || S::kRegs) {
       if (it < w.iters && rows_of(it)) {
 #pragma unroll
         for (int c = 0; c < NV; ++c) {
@@ -542,12 +541,13 @@ __global__ void __launch_bounds__(kMaxThreads) residual_bwd_kernel(ResArgs a) {
           }
         }
       }
-      ptx::cp_async_commit();
+      if constexpr (S::kAhead) ptx::cp_async_commit();
     }
   };
   for (int i = 0; i + 1 < a.stages; ++i) fetch(i, i);
   int turn = 0, stage = 0;
   for (int it = 0; it < w.iters; ++it, stage = stage + 1 == a.stages ? 0 : stage + 1) {
+    rr.advance(), rd.advance(), rg.advance(), ry.advance(), rz.advance();
     fetch(it + a.stages - 1, stage == 0 ? a.stages - 1 : stage - 1);
     if constexpr (S::kAhead) ahead.wait();
     if (!rows_of(it)) break;                     // the whole block
@@ -733,7 +733,7 @@ Plan make_plan(int tokens, int H, int D, int pieces, bool vec, bool lanes_ok, bo
   p.groups = (int)(blocks * per_block / H * H);
   p.rows = per_head ? p.groups / H : p.blocks;
   p.pieces = pieces * p.nv;
-  p.stages = 1;
+  p.stages = !vec && p.nv <= 8 ? 2 : 1;          // 2: the next row in registers
   if (p.v == 8 && p.nv <= 2) {
     const int stage = p.pieces * p.threads * 16;
     const int resident = per_sm / p.threads > 1 ? per_sm / p.threads : 1;

@@ -18,8 +18,10 @@ template <int LANES_, int V_, int NV_>
 struct Shape {
   static constexpr int LANES = LANES_, V = V_, NV = NV_, N = V_ * NV_;
   // Copies ahead of time go through shared memory, 16 bytes at a time. Rows past 8192 elements
-  // (NV beyond 2 runs of 8) are loaded when they are needed.
+  // (NV beyond 2 runs of 8) are loaded when they are needed, and so are long ones element by element.
   static constexpr bool kAhead = V_ == 8 && NV_ <= 2;
+  // Short rows element by element: the next row's elements are loaded into registers.
+  static constexpr bool kRegs = V_ == 1 && NV_ <= 8;
 };
 
 // V consecutive elements as raw words.
@@ -209,17 +211,33 @@ struct Ahead {
 };
 
 // One tensor of a row. With S::kAhead its runs come from the thread's places in shared memory,
-// from `first` on, where fetch() had them copied; without, from global memory.
+// from `first` on, where fetch() had them copied; with S::kRegs from registers, where fetch() put
+// the next row's and advance() made them this one's; else from global memory.
 template <class S, bool ONLY_READ>
 struct Row {
   const void* p;                                 // the row's first element
   int is_bf16, first;                            // first: its first piece within a stage
+  float now[S::kRegs ? S::N : 1], next[S::kRegs ? S::N : 1];
+  __device__ __forceinline__ void set(const void* base, int64_t at, int bf, int piece) {
+    p = static_cast<const char*>(base) + at * (bf ? 2 : 4);
+    is_bf16 = bf;
+    first = piece;
+  }
   __device__ __forceinline__ int per_run() const { return is_bf16 ? 1 : 2; }
-  __device__ __forceinline__ void fetch(const Ahead& a, int stage, int c, int i) const {
-    const char* src = static_cast<const char*>(p) + (size_t)i * (is_bf16 ? 2 : 4);
-    const int at = first + c * per_run();
-    ptx::cp_async16(ptx::smem_u32(a.place(stage, at)), src, 16);
-    if (!is_bf16) ptx::cp_async16(ptx::smem_u32(a.place(stage, at + 1)), src + 16, 16);
+  __device__ __forceinline__ void fetch(const Ahead& a, int stage, int c, int i) {
+    if constexpr (S::kRegs) {
+      load_any<1, ONLY_READ>(p, i, is_bf16, next + c);
+    } else {
+      const char* src = static_cast<const char*>(p) + (size_t)i * (is_bf16 ? 2 : 4);
+      const int at = first + c * per_run();
+      ptx::cp_async16(ptx::smem_u32(a.place(stage, at)), src, 16);
+      if (!is_bf16) ptx::cp_async16(ptx::smem_u32(a.place(stage, at + 1)), src + 16, 16);
+    }
+  }
+  __device__ __forceinline__ void advance() {
+    if constexpr (S::kRegs)
+#pragma unroll
+      for (int j = 0; j < S::N; ++j) now[j] = next[j];
   }
   __device__ __forceinline__ void get(const Ahead& a, int stage, int c, int i, float* f) const {
     if constexpr (S::kAhead) {
@@ -233,6 +251,8 @@ struct Row {
         const Run<float, 8> r = {{u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w}};
         unpack<float, 8>(r, f);
       }
+    } else if constexpr (S::kRegs) {
+      f[0] = now[c];
     } else {
       load_any<S::V, ONLY_READ>(p, i, is_bf16, f);
     }
