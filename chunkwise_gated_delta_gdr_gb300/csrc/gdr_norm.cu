@@ -249,6 +249,7 @@ __global__ void __launch_bounds__(kMaxThreads) gated_kernel(GatedArgs a) {
   __shared__ float sums[BWD && S::LANES ? 8 * 32 * N : 1];      // at most 8 warps in such a block
   if (BWD) asm volatile("griddepcontrol.launch_dependents;");
   const Walk w = walk_of<S::LANES>(a.tokens, a.H, a.groups);
+  const int phase = S::SHIFT ? (int)((((long long)w.tok * a.H + w.head) * a.D) & 7) : 0;
   const Ahead ahead = {places, a.pieces, a.stages};
   const float* weight = a.w && a.per_head ? a.w + (size_t)w.head * a.D : a.w;
   float acc[N];
@@ -271,10 +272,10 @@ __global__ void __launch_bounds__(kMaxThreads) gated_kernel(GatedArgs a) {
       if (it < w.iters && rows_of(it)) {
 #pragma unroll
         for (int c = 0; c < NV; ++c) {
-          const int i = (c * w.threads + w.tid) * V;
+          const int i = (c * w.threads + w.tid) * V - phase;
           if (i < a.D)
 #pragma unroll
-            for (int k = 0; k < TENSORS; ++k) row[k].fetch(ahead, stage, c, i);
+            for (int k = 0; k < TENSORS; ++k) row[k].fetch(ahead, stage, c, i, a.D);
         }
       }
       if constexpr (S::kAhead) ptx::cp_async_commit();
@@ -293,14 +294,14 @@ __global__ void __launch_bounds__(kMaxThreads) gated_kernel(GatedArgs a) {
     if (on)
 #pragma unroll
       for (int c = 0; c < NV; ++c) {
-        const int i = (c * w.threads + w.tid) * V;
+        const int i = (c * w.threads + w.tid) * V - phase;
         if (i >= a.D) continue;
         float x[V], z[V], d[V], wt[V];
-        row[0].get(ahead, stage, c, i, x);
-        if (a.first || BWD) row[1].get(ahead, stage, c, i, z);
+        row[0].get(ahead, stage, c, i, a.D, x);
+        if (a.first || BWD) row[1].get(ahead, stage, c, i, a.D, z);
         if (BWD) {
-          row[TENSORS - 1].get(ahead, stage, c, i, d);
-          if (weight) load_run<float, V, true>(weight + i, wt);
+          row[TENSORS - 1].get(ahead, stage, c, i, a.D, d);
+          if (weight) load_shared<S>(weight, i, a.D, wt);
         }
 #pragma unroll
         for (int e = 0; e < V; ++e) {
@@ -318,14 +319,14 @@ __global__ void __launch_bounds__(kMaxThreads) gated_kernel(GatedArgs a) {
     const float r = rsqrtf(fmaf(s[0], a.inv_d, a.eps)), m = s[1] * a.inv_d * r;
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
-      const int i = (c * w.threads + w.tid) * V;
+      const int i = (c * w.threads + w.tid) * V - phase;
       if (i >= a.D) continue;
       float x[V], z[V], d[V], wt[V], o[V], oz[V];
-      row[0].get(ahead, stage, c, i, x);
-      row[1].get(ahead, stage, c, i, z);
-      if (BWD) row[TENSORS - 1].get(ahead, stage, c, i, d);
+      row[0].get(ahead, stage, c, i, a.D, x);
+      row[1].get(ahead, stage, c, i, a.D, z);
+      if (BWD) row[TENSORS - 1].get(ahead, stage, c, i, a.D, d);
       if (weight) {
-        load_run<float, V, true>(weight + i, wt);
+        load_shared<S>(weight, i, a.D, wt);
       } else {
 #pragma unroll
         for (int e = 0; e < V; ++e) wt[e] = 1.f;
@@ -350,22 +351,24 @@ __global__ void __launch_bounds__(kMaxThreads) gated_kernel(GatedArgs a) {
         }
       }
       if (BWD) {
-        store_any<V>(a.dx, dense + i, a.in_bf16, o);
-        store_any<V>(a.dz, dense + i, a.in_bf16, oz);
+        store_row<S>(a.dx, dense, i, a.D, a.in_bf16, o);
+        store_row<S>(a.dz, dense, i, a.D, a.in_bf16, oz);
       } else {
-        store_any<V>(a.y, dense + i, a.out_bf16, o);
+        store_row<S>(a.y, dense, i, a.D, a.out_bf16, o);
       }
     }
   }
   if (!BWD || !a.part) return;
-  // Shared weights: a row of parts per block; a head's own: one per group of that head.
-  if (!a.per_head) sum_groups<S>(acc, sums, w.tid);
-  if (a.per_head ? !w.on : (S::LANES && threadIdx.x >= S::LANES)) return;
-  float* to = a.part + (a.per_head ? ((size_t)w.tok * a.H + w.head) * a.D : (size_t)blockIdx.x * a.D);
+  // A row of parts per block; per group where its head has weights of its own, or its rows a
+  // phase.
+  const bool each = a.per_head || S::SHIFT;
+  if (!each) sum_groups<S>(acc, sums, w.tid);
+  if (each ? !w.on : (S::LANES && threadIdx.x >= S::LANES)) return;
+  float* to = a.part + (each ? ((size_t)w.tok * a.H + w.head) * a.D : (size_t)blockIdx.x * a.D);
 #pragma unroll
   for (int c = 0; c < NV; ++c) {
-    const int i = (c * w.threads + w.tid) * V;
-    if (i < a.D) store_run<float, V>(to + i, acc + c * V);
+    const int i = (c * w.threads + w.tid) * V - phase;
+    if (i < a.D) store_part<S>(to, i, a.D, acc + c * V);
   }
 }
 
@@ -389,6 +392,7 @@ __global__ void __launch_bounds__(kMaxThreads) residual_fwd_kernel(ResArgs a) {
   extern __shared__ __align__(16) char places[];
   __shared__ Red red;
   const Walk w = walk_of<0>(a.tokens, 1, gridDim.x);
+  const int phase = S::SHIFT ? (int)(((long long)w.tok * a.D) & 7) : 0;
   const Ahead ahead = {places, a.pieces, a.stages};
   Row<S, false> rr;                              // may be the result's own memory
   Row<S, S::NV <= 4> ry, rz;
@@ -407,11 +411,11 @@ __global__ void __launch_bounds__(kMaxThreads) residual_fwd_kernel(ResArgs a) {
       if (it < w.iters && rows_of(it)) {
 #pragma unroll
         for (int c = 0; c < NV; ++c) {
-          const int i = (c * w.threads + w.tid) * V;
+          const int i = (c * w.threads + w.tid) * V - phase;
           if (i < a.D) {
-            rr.fetch(ahead, stage, c, i);
-            if (a.has_y) ry.fetch(ahead, stage, c, i);
-            if (a.has_z) rz.fetch(ahead, stage, c, i);
+            rr.fetch(ahead, stage, c, i, a.D);
+            if (a.has_y) ry.fetch(ahead, stage, c, i, a.D);
+            if (a.has_z) rz.fetch(ahead, stage, c, i, a.D);
           }
         }
       }
@@ -431,10 +435,10 @@ __global__ void __launch_bounds__(kMaxThreads) residual_fwd_kernel(ResArgs a) {
       s[0] = 0.f;
 #pragma unroll
       for (int c = 0; c < NV; ++c) {
-        const int i = (c * w.threads + w.tid) * V;
+        const int i = (c * w.threads + w.tid) * V - phase;
         if (i >= a.D) continue;
         float y[V];
-        ry.get(ahead, stage, c, i, y);
+        ry.get(ahead, stage, c, i, a.D, y);
 #pragma unroll
         for (int e = 0; e < V; ++e) s[0] = fmaf(y[e], y[e], s[0]);
       }
@@ -445,34 +449,34 @@ __global__ void __launch_bounds__(kMaxThreads) residual_fwd_kernel(ResArgs a) {
     s[0] = 0.f;
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
-      const int i = (c * w.threads + w.tid) * V;
+      const int i = (c * w.threads + w.tid) * V - phase;
       if (i >= a.D) continue;
       float* x = r + c * V;
-      rr.get(ahead, stage, c, i, x);
+      rr.get(ahead, stage, c, i, a.D, x);
       if (a.has_y) {
         float y[V], k[V];
-        ry.get(ahead, stage, c, i, y);
+        ry.get(ahead, stage, c, i, a.D, y);
 #pragma unroll
         for (int e = 0; e < V; ++e) y[e] *= py;
         if (a.wp) {
-          load_run<float, V, true>(a.wp + i, k);
+          load_shared<S>(a.wp, i, a.D, k);
 #pragma unroll
           for (int e = 0; e < V; ++e) y[e] *= k[e];
         }
         if (a.has_z) {
-          rz.get(ahead, stage, c, i, k);
+          rz.get(ahead, stage, c, i, a.D, k);
 #pragma unroll
           for (int e = 0; e < V; ++e) y[e] *= act(k[e], a.kind);
         }
         if (a.sv) {
-          load_run<float, V, true>(a.sv + i, k);
+          load_shared<S>(a.sv, i, a.D, k);
 #pragma unroll
           for (int e = 0; e < V; ++e) x[e] = fmaf(k[e], y[e], x[e]);
         } else {
 #pragma unroll
           for (int e = 0; e < V; ++e) x[e] = fmaf(a.s, y[e], x[e]);
         }
-        store_any<V>(a.r_out, dense + i, a.r_bf16, x);
+        store_row<S>(a.r_out, dense, i, a.D, a.r_bf16, x);
       }
 #pragma unroll
       for (int e = 0; e < V; ++e) s[0] = fmaf(x[e], x[e], s[0]);
@@ -481,17 +485,17 @@ __global__ void __launch_bounds__(kMaxThreads) residual_fwd_kernel(ResArgs a) {
     const float rho = rsqrtf(fmaf(s[0], a.inv_d, a.eps));
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
-      const int i = (c * w.threads + w.tid) * V;
+      const int i = (c * w.threads + w.tid) * V - phase;
       if (i >= a.D) continue;
       float o[V], k[V];
 #pragma unroll
       for (int e = 0; e < V; ++e) o[e] = r[c * V + e] * rho;
       if (a.w) {
-        load_run<float, V, true>(a.w + i, k);
+        load_shared<S>(a.w, i, a.D, k);
 #pragma unroll
         for (int e = 0; e < V; ++e) o[e] *= k[e];
       }
-      store_any<V>(a.out, dense + i, a.out_bf16, o);
+      store_row<S>(a.out, dense, i, a.D, a.out_bf16, o);
     }
   }
 }
@@ -504,6 +508,7 @@ __global__ void __launch_bounds__(kMaxThreads) residual_bwd_kernel(ResArgs a) {
   __shared__ Red red;
   asm volatile("griddepcontrol.launch_dependents;");
   const Walk w = walk_of<0>(a.tokens, 1, gridDim.x);
+  const int phase = S::SHIFT ? (int)(((long long)w.tok * a.D) & 7) : 0;
   const Ahead ahead = {places, a.pieces, a.stages};
   float acc[FULL ? 3 : 1][N];
 #pragma unroll
@@ -529,14 +534,14 @@ __global__ void __launch_bounds__(kMaxThreads) residual_bwd_kernel(ResArgs a) {
       if (it < w.iters && rows_of(it)) {
 #pragma unroll
         for (int c = 0; c < NV; ++c) {
-          const int i = (c * w.threads + w.tid) * V;
+          const int i = (c * w.threads + w.tid) * V - phase;
           if (i < a.D) {
-            rr.fetch(ahead, stage, c, i);
-            rd.fetch(ahead, stage, c, i);
-            if (a.has_dr) rg.fetch(ahead, stage, c, i);
+            rr.fetch(ahead, stage, c, i, a.D);
+            rd.fetch(ahead, stage, c, i, a.D);
+            if (a.has_dr) rg.fetch(ahead, stage, c, i, a.D);
             if (FULL) {
-              ry.fetch(ahead, stage, c, i);
-              if (a.has_z) rz.fetch(ahead, stage, c, i);
+              ry.fetch(ahead, stage, c, i, a.D);
+              if (a.has_z) rz.fetch(ahead, stage, c, i, a.D);
             }
           }
         }
@@ -555,13 +560,13 @@ __global__ void __launch_bounds__(kMaxThreads) residual_bwd_kernel(ResArgs a) {
     float s[3] = {0.f, 0.f, 0.f};
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
-      const int i = (c * w.threads + w.tid) * V;
+      const int i = (c * w.threads + w.tid) * V - phase;
       if (i >= a.D) continue;
       float x[V], d[V], k[V];
-      rr.get(ahead, stage, c, i, x);
-      rd.get(ahead, stage, c, i, d);
+      rr.get(ahead, stage, c, i, a.D, x);
+      rd.get(ahead, stage, c, i, a.D, d);
       if (a.w) {
-        load_run<float, V, true>(a.w + i, k);
+        load_shared<S>(a.w, i, a.D, k);
 #pragma unroll
         for (int e = 0; e < V; ++e) d[e] *= k[e];
       }
@@ -571,7 +576,7 @@ __global__ void __launch_bounds__(kMaxThreads) residual_bwd_kernel(ResArgs a) {
         s[1] = fmaf(d[e], x[e], s[1]);
       }
       if (FULL && a.post) {
-        ry.get(ahead, stage, c, i, x);
+        ry.get(ahead, stage, c, i, a.D, x);
 #pragma unroll
         for (int e = 0; e < V; ++e) s[2] = fmaf(x[e], x[e], s[2]);
       }
@@ -582,19 +587,19 @@ __global__ void __launch_bounds__(kMaxThreads) residual_bwd_kernel(ResArgs a) {
     float dp[FULL ? N : 1], se[1] = {0.f};       // dp: dp wp behind a norm
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
-      const int i = (c * w.threads + w.tid) * V;
+      const int i = (c * w.threads + w.tid) * V - phase;
       if (i >= a.D) continue;
       float g[V], x[V], d[V], k[V];
-      rr.get(ahead, stage, c, i, x);
-      rd.get(ahead, stage, c, i, d);
+      rr.get(ahead, stage, c, i, a.D, x);
+      rd.get(ahead, stage, c, i, a.D, d);
       if (a.has_dr) {
-        rg.get(ahead, stage, c, i, g);
+        rg.get(ahead, stage, c, i, a.D, g);
       } else {
 #pragma unroll
         for (int e = 0; e < V; ++e) g[e] = 0.f;
       }
       if (a.w) {
-        load_run<float, V, true>(a.w + i, k);
+        load_shared<S>(a.w, i, a.D, k);
       } else {
 #pragma unroll
         for (int e = 0; e < V; ++e) k[e] = 1.f;
@@ -605,28 +610,28 @@ __global__ void __launch_bounds__(kMaxThreads) residual_bwd_kernel(ResArgs a) {
         acc[0][c * V + e] = fmaf(d[e], u, acc[0][c * V + e]);
         g[e] = fmaf(rho, fmaf(-u, m, d[e] * k[e]), g[e]);
       }
-      store_any<V>(a.o_dr, dense + i, a.r_bf16, g);
+      store_row<S>(a.o_dr, dense, i, a.D, a.r_bf16, g);
       if (!FULL) {
         if (a.o_dy) {
 #pragma unroll
           for (int e = 0; e < V; ++e) g[e] *= a.s;
-          store_any<V>(a.o_dy, dense + i, a.y_bf16, g);
+          store_row<S>(a.o_dy, dense, i, a.D, a.y_bf16, g);
         }
         continue;
       }
       if constexpr (FULL) {
         float y[V], z[V], wp[V];
-        ry.get(ahead, stage, c, i, y);           // uy, where y is normed
+        ry.get(ahead, stage, c, i, a.D, y);           // uy, where y is normed
 #pragma unroll
         for (int e = 0; e < V; ++e) y[e] *= py;
         if (a.wp) {
-          load_run<float, V, true>(a.wp + i, wp);
+          load_shared<S>(a.wp, i, a.D, wp);
         } else {
 #pragma unroll
           for (int e = 0; e < V; ++e) wp[e] = 1.f;
         }
-        if (a.has_z) rz.get(ahead, stage, c, i, z);
-        if (a.sv) load_run<float, V, true>(a.sv + i, k);
+        if (a.has_z) rz.get(ahead, stage, c, i, a.D, z);
+        if (a.sv) load_shared<S>(a.sv, i, a.D, k);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
           const int j = c * V + e;
@@ -640,8 +645,8 @@ __global__ void __launch_bounds__(kMaxThreads) residual_bwd_kernel(ResArgs a) {
           dp[j] = q * wp[e];
           se[0] = fmaf(dp[j], y[e], se[0]);
         }
-        if (a.has_z) store_any<V>(a.o_dz, dense + i, a.y_bf16, z);
-        if (!a.post) store_any<V>(a.o_dy, dense + i, a.y_bf16, dp + c * V);
+        if (a.has_z) store_row<S>(a.o_dz, dense, i, a.D, a.y_bf16, z);
+        if (!a.post) store_row<S>(a.o_dy, dense, i, a.D, a.y_bf16, dp + c * V);
       }
     }
     if constexpr (FULL) {
@@ -650,13 +655,13 @@ __global__ void __launch_bounds__(kMaxThreads) residual_bwd_kernel(ResArgs a) {
         const float my = se[0] * a.inv_d;
 #pragma unroll
         for (int c = 0; c < NV; ++c) {
-          const int i = (c * w.threads + w.tid) * V;
+          const int i = (c * w.threads + w.tid) * V - phase;
           if (i >= a.D) continue;
           float y[V];
-          ry.get(ahead, stage, c, i, y);
+          ry.get(ahead, stage, c, i, a.D, y);
 #pragma unroll
           for (int e = 0; e < V; ++e) y[e] = py * fmaf(-y[e] * py, my, dp[c * V + e]);
-          store_any<V>(a.o_dy, dense + i, a.y_bf16, y);
+          store_row<S>(a.o_dy, dense, i, a.D, a.y_bf16, y);
         }
       }
     }
@@ -668,8 +673,8 @@ __global__ void __launch_bounds__(kMaxThreads) residual_bwd_kernel(ResArgs a) {
     float* to = a.part + ((size_t)k * gridDim.x + blockIdx.x) * a.D;
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
-      const int i = (c * w.threads + w.tid) * V;
-      if (i < a.D) store_run<float, V>(to + i, acc[k] + c * V);
+      const int i = (c * w.threads + w.tid) * V - phase;
+      if (i < a.D) store_part<S>(to, i, a.D, acc[k] + c * V);
     }
   }
 }
@@ -684,18 +689,24 @@ constexpr int kPlainSmem = 36 * 1024;            // fits beside the static part 
 // What a call's kernel looks like: threads of a block, groups and blocks, copies ahead.
 struct Plan {
   int lanes, v, nv, threads, groups, blocks, rows;   // rows: of the parts, per weight
+  bool shift;
   int pieces, stages, smem;
 };
 
 // f(Shape) for a plan.
 template <typename F>
 auto with_block(const Plan& p, F f) {
+  if (p.shift) return f(Shape<0, 8, 2, true>());
   if (p.v == 8) return p.nv == 2 ? f(Shape<0, 8, 2>()) : f(Shape<0, 8, 4>());
   return p.nv == 4 ? f(Shape<0, 1, 4>()) : p.nv == 16 ? f(Shape<0, 1, 16>()) : f(Shape<0, 1, 32>());
 }
 template <typename F>
 auto with_shape(const Plan& p, F f) {
   if (p.lanes == 0) return with_block(p, f);
+  if (p.shift)
+    return p.lanes == 8    ? f(Shape<8, 8, 1, true>())
+           : p.lanes == 16 ? f(Shape<16, 8, 1, true>())
+                           : f(Shape<32, 8, 1, true>());
   if (p.v == 1) return f(Shape<32, 1, 8>());
   return p.lanes == 8    ? f(Shape<8, 8, 1>())
          : p.lanes == 16 ? f(Shape<16, 8, 1>())
@@ -703,16 +714,25 @@ auto with_shape(const Plan& p, F f) {
                          : f(Shape<32, 8, 2>());
 }
 
-// pieces: 16-byte pieces per run of 8, over all tensors of a row. vec: whether 16-byte accesses
-// fit. lanes_ok: whether a row may share a warp. per_sm: threads an SM is to hold.
-Plan make_plan(int tokens, int H, int D, int pieces, bool vec, bool lanes_ok, bool per_head,
+// How a call's rows lie: 16-byte accesses fit; fit but for a phase (Shape's SHIFT); or neither.
+enum Fit { kVec, kShift, kSingle };
+
+// pieces: 16-byte pieces per run of 8, over all tensors of a row. lanes_ok: whether a row may share
+// a warp. per_sm: threads an SM is to hold.
+Plan make_plan(int tokens, int H, int D, int pieces, Fit fit, bool lanes_ok, bool per_head,
                int per_sm) {
   Plan p = {};
+  p.shift = fit == kShift && D + 7 <= kMaxThreads * 16;
+  const bool vec = fit == kVec || p.shift;
   p.v = vec ? 8 : 1;
-  p.lanes = !lanes_ok || D > (vec ? 512 : 256) ? 0 : !vec || D > 128 ? 32 : D > 64 ? 16 : 8;
+  const int span = D + (p.shift ? 7 : 0);        // elements that a row's threads cover
+  p.lanes = !lanes_ok || span > (fit == kVec ? 512 : 256) ? 0
+            : !vec || span > 128                          ? 32
+            : span > 64                                   ? 16
+                                                          : 8;
   int per_block = 1;                             // groups of a block
   if (p.lanes) {
-    p.nv = !vec ? 8 : D > 256 ? 2 : 1;
+    p.nv = !vec ? 8 : span > 256 ? 2 : 1;
     p.threads = 256;
     per_block = p.threads / p.lanes;
   } else {
@@ -721,7 +741,7 @@ Plan make_plan(int tokens, int H, int D, int pieces, bool vec, bool lanes_ok, bo
     p.nv = vec ? (D <= kMaxThreads * 16 ? 2 : 4)
                : D <= kMaxThreads * 4 ? 4 : D <= kMaxThreads * 16 ? 16 : 32;
     const int n = p.nv * p.v;
-    p.threads = ((D + n - 1) / n + 31) / 32 * 32;
+    p.threads = ((span + n - 1) / n + 31) / 32 * 32;
   }
   const long long rows = (long long)tokens * H;
   long long blocks = (rows + per_block - 1) / per_block;
@@ -729,9 +749,16 @@ Plan make_plan(int tokens, int H, int D, int pieces, bool vec, bool lanes_ok, bo
   if (blocks > most) blocks = most;
   const long long least = (H + per_block - 1) / per_block;     // a group per head
   if (blocks < least) blocks = least;
+  long long groups = blocks * per_block / H * H;
+  if (p.shift && groups < rows) {                // steps of 8 tokens, for one phase per group
+    const long long unit = 8LL * H;
+    groups = groups < unit ? unit : groups / unit * unit;
+    blocks = (groups + per_block - 1) / per_block;
+  }
   p.blocks = (int)blocks;
-  p.groups = (int)(blocks * per_block / H * H);
-  p.rows = per_head ? p.groups / H : p.blocks;
+  p.groups = (int)groups;
+  // Groups of one block have phases of their own: a row of parts each.
+  p.rows = per_head ? p.groups / H : p.shift ? p.groups : p.blocks;
   p.pieces = pieces * p.nv;
   p.stages = !vec && p.nv <= 8 ? 2 : 1;          // 2: the next row in registers
   if (p.v == 8 && p.nv <= 2) {
@@ -744,9 +771,15 @@ Plan make_plan(int tokens, int H, int D, int pieces, bool vec, bool lanes_ok, bo
   return p;
 }
 
-bool vec_view(const void* p, int dtype, int64_t b, int64_t t, int64_t h) {
-  return b % 8 == 0 && t % 8 == 0 && h % 8 == 0 && is_aligned(p, 16);
+// The fit of a view [B, T, H, D] (strides of dimensions of one element: 0).
+Fit fit_of(const void* p, int B, int T, int H, int D, int64_t b, int64_t t, int64_t h) {
+  if (!is_aligned(p, 16)) return kSingle;
+  const int64_t row = D, tok = row * H, batch = tok * T;
+  if ((B > 1 && (b - batch) % 8) || (T > 1 && (t - tok) % 8) || (H > 1 && (h - row) % 8))
+    return kSingle;
+  return D % 8 ? kShift : kVec;
 }
+Fit worse(Fit a, Fit b) { return a > b ? a : b; }
 
 // Column sums of the parts, behind the kernel that writes them.
 gdr_status sum_parts(const float* part, float* o0, float* o1, float* o2, int rows, int cols,
@@ -779,11 +812,11 @@ gdr_status check(const gdr_gated_dims* d) {
 constexpr int kFwdPerSm = 1024, kBwdPerSm = 768, kFullPerSm = 512;
 constexpr int kFwdRowsPerSm = 768, kBwdRowsPerSm = 512;
 
-Plan gated_plan(const gdr_gated_dims* d, bool vec, bool bwd) {
+Plan gated_plan(const gdr_gated_dims* d, Fit fit, bool bwd) {
   const int in = d->in_dtype == GDR_BF16 ? 1 : 2, out = d->out_dtype == GDR_BF16 ? 1 : 2;
-  return make_plan(d->B * d->T, d->H, d->D, 2 * in + (bwd ? out : 0), vec, true,
+  return make_plan(d->B * d->T, d->H, d->D, 2 * in + (bwd ? out : 0), fit, true,
                    d->weight_per_head != 0,
-                   vec && d->D <= 512 ? (bwd ? kBwdRowsPerSm : kFwdRowsPerSm)
+                   fit == kVec && d->D <= 512 ? (bwd ? kBwdRowsPerSm : kFwdRowsPerSm)
                                       : (bwd ? kBwdPerSm : kFwdPerSm));
 }
 size_t gated_bytes(const gdr_gated_dims* d, const Plan& p) {
@@ -793,7 +826,7 @@ size_t gated_bytes(const gdr_gated_dims* d, const Plan& p) {
 
 // Arguments that both directions share.
 gdr_status gated_args(GatedArgs& a, const gdr_gated_dims* d, const void* x, const void* gate,
-                      const float* w, bool* vec) {
+                      const float* w, Fit* fit) {
   if (!is_aligned(x, dtype_size(d->in_dtype)) || !is_aligned(gate, dtype_size(d->in_dtype)) ||
       !is_aligned(w, 16))
     return GDR_ERR_ALIGNMENT;
@@ -811,8 +844,8 @@ gdr_status gated_args(GatedArgs& a, const gdr_gated_dims* d, const void* x, cons
   a.out_bf16 = d->out_dtype == GDR_BF16;
   a.eps = d->eps;
   a.inv_d = 1.f / d->D;
-  *vec = d->D % 8 == 0 && vec_view(x, d->in_dtype, a.x.b, a.x.t, a.x.h) &&
-         vec_view(gate, d->in_dtype, a.z.b, a.z.t, a.z.h);
+  *fit = worse(fit_of(x, a.B, a.T, a.H, a.D, a.x.b, a.x.t, a.x.h),
+               fit_of(gate, a.B, a.T, a.H, a.D, a.z.b, a.z.t, a.z.h));
   return GDR_OK;
 }
 
@@ -821,7 +854,7 @@ gdr_status launch_gated(GatedArgs& a, const Plan& p, cudaStream_t s) {
   a.groups = p.groups;
   a.pieces = p.pieces;
   a.stages = p.stages;
-  if (p.lanes && p.v == 8 && a.in_bf16 == a.out_bf16)
+  if (p.lanes && p.v == 8 && !p.shift && a.in_bf16 == a.out_bf16)
     return with_dtype(a.in_bf16 ? GDR_BF16 : GDR_F32, [&](auto* t) {
       using T = std::remove_pointer_t<decltype(t)>;
       auto go = [&](auto shape) {
@@ -857,13 +890,13 @@ gdr_status check(const gdr_residual_dims* d) {
 }
 
 // pieces: of all tensors of a row (see make_plan).
-Plan residual_plan(const gdr_residual_dims* d, bool vec, int pieces, int per_sm) {
-  return make_plan(d->B * d->T, 1, d->D, pieces, vec, false, false, per_sm);
+Plan residual_plan(const gdr_residual_dims* d, Fit fit, int pieces, int per_sm) {
+  return make_plan(d->B * d->T, 1, d->D, pieces, fit, false, false, per_sm);
 }
 
 gdr_status residual_args(ResArgs& a, const gdr_residual_dims* d, const void* r, const void* y,
                          const void* z, const float* w, const float* wp, const float* sv,
-                         bool* vec) {
+                         Fit* fit) {
   if (!is_aligned(r, dtype_size(d->residual_dtype)) || !is_aligned(y, dtype_size(d->y_dtype)) ||
       !is_aligned(z, dtype_size(d->y_dtype)) || !is_aligned(w, 16) || !is_aligned(wp, 16) ||
       !is_aligned(sv, 16))
@@ -884,9 +917,9 @@ gdr_status residual_args(ResArgs& a, const gdr_residual_dims* d, const void* r, 
   a.eps = d->eps;
   a.inv_d = 1.f / d->D;
   a.s = d->scale;
-  *vec = d->D % 8 == 0 && vec_view(r, d->residual_dtype, a.r.b, a.r.t, 0) &&
-         (!y || vec_view(y, d->y_dtype, a.y.b, a.y.t, 0)) &&
-         (!z || vec_view(z, d->y_dtype, a.z.b, a.z.t, 0));
+  *fit = kVec;
+  for (const View* v : {&a.r, &a.y, &a.z})
+    if (v->p) *fit = worse(*fit, fit_of(v->p, a.B, a.T, 1, a.D, v->b, v->t, 0));
   return GDR_OK;
 }
 // A gate, a post norm or a scale per channel act on y.
@@ -913,23 +946,25 @@ gdr_status gdr_gated_norm(const void* x, const void* gate, const float* weight, 
   const gdr_status st = check(dims);
   if (st != GDR_OK) return st;
   GatedArgs a = {};
-  bool vec = false;
-  const gdr_status ok = gated_args(a, dims, x, gate, weight, &vec);
+  Fit fit = kSingle;
+  const gdr_status ok = gated_args(a, dims, x, gate, weight, &fit);
   if (ok != GDR_OK) return ok;
   if (!is_aligned(y, 16)) return GDR_ERR_ALIGNMENT;
   if (a.tokens == 0) return GDR_OK;
   if (!x || !gate || !y) return GDR_ERR_INVALID_ARG;
   a.y = y;
-  return launch_gated<false>(a, gated_plan(dims, vec, false), reinterpret_cast<cudaStream_t>(stream));
+  return launch_gated<false>(a, gated_plan(dims, fit, false), reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t gdr_gated_norm_bwd_workspace_size(const gdr_gated_dims* dims) {
   if (check(dims) != GDR_OK) return 0;
-  // The bases' alignment is not known here: room for either kernel.
-  const size_t v = gated_bytes(dims, gated_plan(dims, true, true));
-  const size_t o = gated_bytes(dims, gated_plan(dims, false, true));
-  const size_t most = v > o ? v : o;
-  return most ? most : kAlign;
+  // The bases' alignment is not known here: room for every kernel.
+  size_t most = kAlign;
+  for (Fit fit : {dims->D % 8 ? kShift : kVec, kSingle}) {
+    const size_t n = gated_bytes(dims, gated_plan(dims, fit, true));
+    if (n > most) most = n;
+  }
+  return most;
 }
 
 gdr_status gdr_gated_norm_bwd(const void* d_y, const void* x, const void* gate, const float* weight,
@@ -938,8 +973,8 @@ gdr_status gdr_gated_norm_bwd(const void* d_y, const void* x, const void* gate, 
   const gdr_status st = check(dims);
   if (st != GDR_OK) return st;
   GatedArgs a = {};
-  bool vec = false;
-  const gdr_status ok = gated_args(a, dims, x, gate, weight, &vec);
+  Fit fit = kSingle;
+  const gdr_status ok = gated_args(a, dims, x, gate, weight, &fit);
   if (ok != GDR_OK) return ok;
   if (!is_aligned(d_y, 16) || !is_aligned(dx, 16) || !is_aligned(d_gate, 16) ||
       !is_aligned(d_weight, 16))
@@ -948,7 +983,7 @@ gdr_status gdr_gated_norm_bwd(const void* d_y, const void* x, const void* gate, 
   const int cols = dims->D * (a.per_head ? dims->H : 1);
   if (a.tokens == 0) return zero(d_weight, cols, s);
   if (!d_y || !x || !gate || !dx || !d_gate) return GDR_ERR_INVALID_ARG;
-  const Plan p = gated_plan(dims, vec, true);
+  const Plan p = gated_plan(dims, fit, true);
   if (d_weight) {
     if (!workspace || workspace_bytes < gdr_gated_norm_bwd_workspace_size(dims))
       return GDR_ERR_WORKSPACE;
@@ -971,9 +1006,9 @@ gdr_status gdr_residual_norm(const void* residual, const void* y, const void* ga
   const gdr_status st = check(dims);
   if (st != GDR_OK) return st;
   ResArgs a = {};
-  bool vec = false;
+  Fit fit = kSingle;
   const gdr_status ok =
-      residual_args(a, dims, residual, y, gate, weight, post_weight, scale, &vec);
+      residual_args(a, dims, residual, y, gate, weight, post_weight, scale, &fit);
   if (ok != GDR_OK) return ok;
   if (!is_aligned(residual_out, 16) || !is_aligned(out, 16)) return GDR_ERR_ALIGNMENT;
   if (a.tokens == 0) return GDR_OK;
@@ -982,7 +1017,7 @@ gdr_status gdr_residual_norm(const void* residual, const void* y, const void* ga
   a.out = out;
   a.r_out = residual_out;
   const int re = a.r_bf16 ? 1 : 2, ye = a.y_bf16 ? 1 : 2;
-  const Plan p = residual_plan(dims, vec, re + a.has_y * ye + a.has_z * ye, kFwdPerSm);
+  const Plan p = residual_plan(dims, fit, re + a.has_y * ye + a.has_z * ye, kFwdPerSm);
   a.pieces = p.pieces;
   a.stages = p.stages;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -997,11 +1032,13 @@ gdr_status gdr_residual_norm(const void* residual, const void* y, const void* ga
 
 size_t gdr_residual_norm_bwd_workspace_size(const gdr_residual_dims* dims) {
   if (check(dims) != GDR_OK) return 0;
-  const Plan v = residual_plan(dims, true, 1, kBwdPerSm);
-  const Plan o = residual_plan(dims, false, 1, kBwdPerSm);
-  const size_t rows = v.rows > o.rows ? v.rows : o.rows;
-  const size_t bytes = align_up(3 * rows * dims->D * sizeof(float));
-  return bytes ? bytes : kAlign;
+  size_t most = kAlign;
+  for (Fit fit : {dims->D % 8 ? kShift : kVec, kSingle}) {
+    const size_t rows = residual_plan(dims, fit, 1, kBwdPerSm).rows;
+    const size_t n = align_up(3 * rows * dims->D * sizeof(float));
+    if (n > most) most = n;
+  }
+  return most;
 }
 
 gdr_status gdr_residual_norm_bwd(const void* d_out, const void* d_residual_out,
@@ -1014,9 +1051,9 @@ gdr_status gdr_residual_norm_bwd(const void* d_out, const void* d_residual_out,
   const gdr_status st = check(dims);
   if (st != GDR_OK) return st;
   ResArgs a = {};
-  bool vec = false;
+  Fit fit = kSingle;
   const gdr_status ok =
-      residual_args(a, dims, residual_out, y, gate, weight, post_weight, scale, &vec);
+      residual_args(a, dims, residual_out, y, gate, weight, post_weight, scale, &fit);
   if (ok != GDR_OK) return ok;
   for (const void* p : {d_out, d_residual_out, static_cast<const void*>(d_residual),
                         static_cast<const void*>(d_y), static_cast<const void*>(d_gate),
@@ -1039,7 +1076,7 @@ gdr_status gdr_residual_norm_bwd(const void* d_out, const void* d_residual_out,
   a.has_dr = d_residual_out != nullptr;
   const int re = a.r_bf16 ? 1 : 2, ye = a.y_bf16 ? 1 : 2, oe = a.out_bf16 ? 1 : 2;
   const int pieces = re * (1 + a.has_dr) + oe + (full ? ye * (1 + a.has_z) : 0);
-  const Plan p = residual_plan(dims, vec, pieces, full ? kFullPerSm : kBwdPerSm);
+  const Plan p = residual_plan(dims, fit, pieces, full ? kFullPerSm : kBwdPerSm);
   if (d_weight || d_post_weight || d_scale) {
     if (!workspace || workspace_bytes < gdr_residual_norm_bwd_workspace_size(dims))
       return GDR_ERR_WORKSPACE;

@@ -457,3 +457,50 @@ def test_refusals_on_the_gpu(compiled, monkeypatch):
             call()
     gdr.gated_norm(x, x)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("rt,yt", [(F32, F32), (BF, BF), (F32, BF)])
+@pytest.mark.parametrize("D", [9, 65, 777, 1001, 3190, 6547, 8185, 8186])
+def test_residual_odd_rows(D, rt, yt):
+    """Rows that start anywhere against 16 bytes, more of them than blocks; a neighbour's NaN
+    next to a row's ends stays out of it, and rows next to a slice are left as they were."""
+    T = 1300 if D < 1000 else 700
+    r, y, z, d, dr, w, wp, s = residual_inputs(1, T, D, rt, yt, seed=12)
+    residual_check(r, y, w, z, wp, s, d, dr, "silu", True)
+    residual_check(r, y, w, d=d, dr=dr, s=0.5)
+    out, res = gdr.residual_norm(r, y, w)
+    bad = y.clone()
+    bad[0, 3::7] = float("nan")
+    keep = torch.ones(T, dtype=torch.bool, device=DEV)
+    keep[3::7] = False
+    out2, res2 = gdr.residual_norm(r, bad, w)
+    assert torch.equal(out2[0, keep], out[0, keep]) and torch.isnan(out2[0, ~keep]).all()
+    pool = torch.full((T + 2, D), 7.0, dtype=rt, device=DEV)
+    row = 16 // torch.finfo(rt).bits * 8          # a slice that starts on 16 bytes
+    mine = pool.view(-1)[8 * row:8 * row + 8 * D].view(1, 8, D)
+    gdr.residual_norm(r[:, :8], y[:, :8], w, residual_out=mine)
+    assert torch.equal(mine, res[:, :8])
+    flat = pool.view(-1)
+    assert (flat[:8 * row] == 7).all() and (flat[8 * row + 8 * D:] == 7).all()
+
+
+@pytest.mark.parametrize("weight", ["one", "head"])
+@pytest.mark.parametrize("shape", [(2, 900, 3, 9), (1, 1100, 5, 57), (3, 701, 7, 100), (2, 500, 4, 173),
+                                   (2, 700, 3, 250), (1, 900, 2, 335), (1, 30, 2, 8185)])
+def test_gated_odd_rows(shape, weight):
+    for dtype in (BF, F32):
+        x, z, w, d = gated_inputs(*shape, dtype=dtype, seed=13, weight=weight)
+        gated_check(x, z, w, d, "silu", False)
+        gated_check(x, z, w, d, "sigmoid", True)
+
+
+def test_odd_rows_of_views_with_even_steps():
+    """Views whose strides differ from the dense ones by multiples of 8 elements."""
+    gen, B, T, H, D = gen_of(14), 2, 40, 3, 77
+    for dtype in (BF, F32):
+        x = rnd(gen, B, T, H * D + 16, dtype=dtype)[..., :H * D].unflatten(-1, (H, D))
+        z = rnd(gen, B, T + 8, H * D, dtype=dtype)[:, :T].unflatten(-1, (H, D))
+        w, d = rnd(gen, H, D), rnd(gen, B, T, H, D, dtype=dtype)
+        gated_check(x, z, w, d)
+        residual_check(x[:, :, 0], z[:, :, 0], w[0].contiguous(), d=d[:, :, 0].contiguous(),
+                       dr=d[:, :, 1].contiguous())
