@@ -70,7 +70,6 @@ __global__ void __launch_bounds__(256, BWD ? 2 : 3) gated_rows_kernel(GatedArgs 
   constexpr int Q = 8 * sizeof(T) / 16;          // 16-byte pieces of 8 channels
   constexpr bool AHEAD = NV == 1 || !BWD;        // else there are no registers for the next rows
   __shared__ float sums[BWD ? 8 * 32 * 8 * NV : 1];
-  if (BWD) asm volatile("griddepcontrol.launch_dependents;");
   const Walk w = walk_of<LANES>(a.tokens, a.H, a.groups);
   bool mine[NV];
 #pragma unroll
@@ -114,6 +113,7 @@ __global__ void __launch_bounds__(256, BWD ? 2 : 3) gated_rows_kernel(GatedArgs 
                             : make_float2(__uint_as_float(u[(2 * i) % (4 * NV * Q)]),
                                           __uint_as_float(u[(2 * i + 1) % (4 * NV * Q)]));
   };
+  begin_behind();
   float2 wt[N], acc[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) wt[i] = make_float2(1.f, 1.f), acc[i] = make_float2(0.f, 0.f);
@@ -247,7 +247,6 @@ __global__ void __launch_bounds__(kMaxThreads) gated_kernel(GatedArgs a) {
   extern __shared__ __align__(16) char places[];
   __shared__ Red red;
   __shared__ float sums[BWD && S::LANES ? 8 * 32 * N : 1];      // at most 8 warps in such a block
-  if (BWD) asm volatile("griddepcontrol.launch_dependents;");
   const Walk w = walk_of<S::LANES>(a.tokens, a.H, a.groups);
   const int phase = S::SHIFT ? (int)((((long long)w.tok * a.H + w.head) * a.D) & 7) : 0;
   const Ahead ahead = {places, a.pieces, a.stages};
@@ -281,6 +280,7 @@ __global__ void __launch_bounds__(kMaxThreads) gated_kernel(GatedArgs a) {
       if constexpr (S::kAhead) ptx::cp_async_commit();
     }
   };
+  begin_behind();
   for (int i = 0; i + 1 < a.stages; ++i) fetch(i, i);
   int turn = 0, stage = 0;
   for (int it = 0; it < w.iters; ++it, stage = stage + 1 == a.stages ? 0 : stage + 1) {
@@ -422,6 +422,7 @@ __global__ void __launch_bounds__(kMaxThreads) residual_fwd_kernel(ResArgs a) {
       if constexpr (S::kAhead) ptx::cp_async_commit();
     }
   };
+  begin_behind();
   for (int i = 0; i + 1 < a.stages; ++i) fetch(i, i);
   int turn = 0, stage = 0;
   for (int it = 0; it < w.iters; ++it, stage = stage + 1 == a.stages ? 0 : stage + 1) {
@@ -439,8 +440,7 @@ __global__ void __launch_bounds__(kMaxThreads) residual_fwd_kernel(ResArgs a) {
         if (i >= a.D) continue;
         float y[V];
         ry.get(ahead, stage, c, i, a.D, y);
-#pragma unroll
-        for (int e = 0; e < V; ++e) s[0] = fmaf(y[e], y[e], s[0]);
+        s[0] += dot_run<V>(y, y);
       }
       row_sum<0, 1>(s, red, turn);
       py = rsqrtf(fmaf(s[0], a.inv_d, a.eps));
@@ -456,30 +456,26 @@ __global__ void __launch_bounds__(kMaxThreads) residual_fwd_kernel(ResArgs a) {
       if (a.has_y) {
         float y[V], k[V];
         ry.get(ahead, stage, c, i, a.D, y);
-#pragma unroll
-        for (int e = 0; e < V; ++e) y[e] *= py;
+        if (a.post) scale_run<V>(y, y, py);
         if (a.wp) {
           load_shared<S>(a.wp, i, a.D, k);
-#pragma unroll
-          for (int e = 0; e < V; ++e) y[e] *= k[e];
+          mul_run<V>(y, y, k);
         }
         if (a.has_z) {
           rz.get(ahead, stage, c, i, a.D, k);
 #pragma unroll
-          for (int e = 0; e < V; ++e) y[e] *= act(k[e], a.kind);
+          for (int e = 0; e < V; ++e) k[e] = act(k[e], a.kind);
+          mul_run<V>(y, y, k);
         }
         if (a.sv) {
           load_shared<S>(a.sv, i, a.D, k);
-#pragma unroll
-          for (int e = 0; e < V; ++e) x[e] = fmaf(k[e], y[e], x[e]);
+          fma_run<V>(x, k, y, x);
         } else {
-#pragma unroll
-          for (int e = 0; e < V; ++e) x[e] = fmaf(a.s, y[e], x[e]);
+          fma_run<V>(x, y, a.s, x);
         }
         store_row<S>(a.r_out, dense, i, a.D, a.r_bf16, x);
       }
-#pragma unroll
-      for (int e = 0; e < V; ++e) s[0] = fmaf(x[e], x[e], s[0]);
+      s[0] += dot_run<V>(x, x);
     }
     row_sum<0, 1>(s, red, turn);
     const float rho = rsqrtf(fmaf(s[0], a.inv_d, a.eps));
@@ -488,12 +484,10 @@ __global__ void __launch_bounds__(kMaxThreads) residual_fwd_kernel(ResArgs a) {
       const int i = (c * w.threads + w.tid) * V - phase;
       if (i >= a.D) continue;
       float o[V], k[V];
-#pragma unroll
-      for (int e = 0; e < V; ++e) o[e] = r[c * V + e] * rho;
+      scale_run<V>(o, r + c * V, rho);
       if (a.w) {
         load_shared<S>(a.w, i, a.D, k);
-#pragma unroll
-        for (int e = 0; e < V; ++e) o[e] *= k[e];
+        mul_run<V>(o, o, k);
       }
       store_row<S>(a.out, dense, i, a.D, a.out_bf16, o);
     }
@@ -506,7 +500,6 @@ __global__ void __launch_bounds__(kMaxThreads) residual_bwd_kernel(ResArgs a) {
   constexpr int V = S::V, NV = S::NV, N = S::N;
   extern __shared__ __align__(16) char places[];
   __shared__ Red red;
-  asm volatile("griddepcontrol.launch_dependents;");
   const Walk w = walk_of<0>(a.tokens, 1, gridDim.x);
   const int phase = S::SHIFT ? (int)(((long long)w.tok * a.D) & 7) : 0;
   const Ahead ahead = {places, a.pieces, a.stages};
@@ -549,6 +542,7 @@ __global__ void __launch_bounds__(kMaxThreads) residual_bwd_kernel(ResArgs a) {
       if constexpr (S::kAhead) ptx::cp_async_commit();
     }
   };
+  begin_behind();
   for (int i = 0; i + 1 < a.stages; ++i) fetch(i, i);
   int turn = 0, stage = 0;
   for (int it = 0; it < w.iters; ++it, stage = stage + 1 == a.stages ? 0 : stage + 1) {
@@ -567,18 +561,13 @@ __global__ void __launch_bounds__(kMaxThreads) residual_bwd_kernel(ResArgs a) {
       rd.get(ahead, stage, c, i, a.D, d);
       if (a.w) {
         load_shared<S>(a.w, i, a.D, k);
-#pragma unroll
-        for (int e = 0; e < V; ++e) d[e] *= k[e];
+        mul_run<V>(d, d, k);
       }
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        s[0] = fmaf(x[e], x[e], s[0]);
-        s[1] = fmaf(d[e], x[e], s[1]);
-      }
+      s[0] += dot_run<V>(x, x);
+      s[1] += dot_run<V>(d, x);
       if (FULL && a.post) {
         ry.get(ahead, stage, c, i, a.D, x);
-#pragma unroll
-        for (int e = 0; e < V; ++e) s[2] = fmaf(x[e], x[e], s[2]);
+        s[2] += dot_run<V>(x, x);
       }
     }
     row_sum<0, FULL ? 3 : 2>(s, red, turn);
@@ -598,55 +587,67 @@ __global__ void __launch_bounds__(kMaxThreads) residual_bwd_kernel(ResArgs a) {
 #pragma unroll
         for (int e = 0; e < V; ++e) g[e] = 0.f;
       }
+      scale_run<V>(x, x, rho);                   // u
+      fma_run<V>(acc[0] + c * V, d, x, acc[0] + c * V);
       if (a.w) {
         load_shared<S>(a.w, i, a.D, k);
-      } else {
-#pragma unroll
-        for (int e = 0; e < V; ++e) k[e] = 1.f;
+        mul_run<V>(d, d, k);
       }
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float u = x[e] * rho;
-        acc[0][c * V + e] = fmaf(d[e], u, acc[0][c * V + e]);
-        g[e] = fmaf(rho, fmaf(-u, m, d[e] * k[e]), g[e]);
-      }
+      fma_run<V>(d, x, -m, d);
+      fma_run<V>(g, d, rho, g);
       store_row<S>(a.o_dr, dense, i, a.D, a.r_bf16, g);
       if (!FULL) {
         if (a.o_dy) {
-#pragma unroll
-          for (int e = 0; e < V; ++e) g[e] *= a.s;
+          scale_run<V>(g, g, a.s);
           store_row<S>(a.o_dy, dense, i, a.D, a.y_bf16, g);
         }
         continue;
       }
       if constexpr (FULL) {
-        float y[V], z[V], wp[V];
-        ry.get(ahead, stage, c, i, a.D, y);           // uy, where y is normed
-#pragma unroll
-        for (int e = 0; e < V; ++e) y[e] *= py;
+        float y[V], z[V], p[V], q[V];
+        ry.get(ahead, stage, c, i, a.D, y);
+        if (a.post) scale_run<V>(y, y, py);      // uy
         if (a.wp) {
-          load_shared<S>(a.wp, i, a.D, wp);
+          load_shared<S>(a.wp, i, a.D, k);
+          mul_run<V>(p, y, k);
         } else {
 #pragma unroll
-          for (int e = 0; e < V; ++e) wp[e] = 1.f;
+          for (int e = 0; e < V; ++e) p[e] = y[e];
         }
-        if (a.has_z) rz.get(ahead, stage, c, i, a.D, z);
-        if (a.sv) load_shared<S>(a.sv, i, a.D, k);
+        if (a.has_z) {
+          rz.get(ahead, stage, c, i, a.D, z);
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const int j = c * V + e;
-          float slope = 0.f;
-          const float av = a.has_z ? act(z[e], a.kind, slope) : 1.f;
-          const float p = y[e] * wp[e], gs = g[e] * (a.sv ? k[e] : a.s);
-          acc[2][j] = fmaf(g[e] * av, p, acc[2][j]);
-          z[e] = gs * p * slope;
-          const float q = gs * av;
-          acc[1][j] = fmaf(q, y[e], acc[1][j]);
-          dp[j] = q * wp[e];
-          se[0] = fmaf(dp[j], y[e], se[0]);
+          for (int e = 0; e < V; ++e) q[e] = act(z[e], a.kind, z[e]);    // a, and a' in z
+          mul_run<V>(z, z, g);
+          mul_run<V>(z, z, p);
+          mul_run<V>(q, q, g);
+        } else {
+#pragma unroll
+          for (int e = 0; e < V; ++e) q[e] = g[e];
+        }
+        if (a.sv) {                              // q: g a, then g a s
+          fma_run<V>(acc[2] + c * V, q, p, acc[2] + c * V);
+          load_shared<S>(a.sv, i, a.D, p);
+          mul_run<V>(q, q, p);
+          if (a.has_z) mul_run<V>(z, z, p);
+        } else {
+          scale_run<V>(q, q, a.s);
+          if (a.has_z) scale_run<V>(z, z, a.s);
         }
         if (a.has_z) store_row<S>(a.o_dz, dense, i, a.D, a.y_bf16, z);
-        if (!a.post) store_row<S>(a.o_dy, dense, i, a.D, a.y_bf16, dp + c * V);
+        float* dq = dp + c * V;
+        if (a.post) {
+          fma_run<V>(acc[1] + c * V, q, y, acc[1] + c * V);
+          if (a.wp) {
+            mul_run<V>(dq, q, k);
+          } else {
+#pragma unroll
+            for (int e = 0; e < V; ++e) dq[e] = q[e];
+          }
+          se[0] += dot_run<V>(dq, y);
+        } else {
+          store_row<S>(a.o_dy, dense, i, a.D, a.y_bf16, q);
+        }
       }
     }
     if constexpr (FULL) {
@@ -659,8 +660,8 @@ __global__ void __launch_bounds__(kMaxThreads) residual_bwd_kernel(ResArgs a) {
           if (i >= a.D) continue;
           float y[V];
           ry.get(ahead, stage, c, i, a.D, y);
-#pragma unroll
-          for (int e = 0; e < V; ++e) y[e] = py * fmaf(-y[e] * py, my, dp[c * V + e]);
+          fma_run<V>(y, y, -py * my, dp + c * V);
+          scale_run<V>(y, y, py);
           store_row<S>(a.o_dy, dense, i, a.D, a.y_bf16, y);
         }
       }
@@ -809,7 +810,7 @@ gdr_status check(const gdr_gated_dims* d) {
 
 // Threads that an SM is to hold: of the kernels above (kFullPerSm: the residual's backward with a
 // norm, gate or scale per channel, at most kBwdPerSm), and of gated_rows_kernel.
-constexpr int kFwdPerSm = 1024, kBwdPerSm = 768, kFullPerSm = 512;
+constexpr int kFwdPerSm = 1024, kBwdPerSm = 1024, kFullPerSm = 512;
 constexpr int kFwdRowsPerSm = 768, kBwdRowsPerSm = 512;
 
 Plan gated_plan(const gdr_gated_dims* d, Fit fit, bool bwd) {
@@ -859,9 +860,9 @@ gdr_status launch_gated(GatedArgs& a, const Plan& p, cudaStream_t s) {
       using T = std::remove_pointer_t<decltype(t)>;
       auto go = [&](auto shape) {
         using S = decltype(shape);
-        return launch_kernel(a.first ? gated_rows_kernel<T, S::LANES, S::NV, BWD, true>
+        return launch_behind(a.first ? gated_rows_kernel<T, S::LANES, S::NV, BWD, true>
                                      : gated_rows_kernel<T, S::LANES, S::NV, BWD, false>,
-                             dim3(p.blocks), p.threads, 0, s, a);
+                             dim3(p.blocks), p.threads, s, a);
       };
       return p.lanes == 8    ? go(Shape<8, 8, 1>())
              : p.lanes == 16 ? go(Shape<16, 8, 1>())
@@ -873,7 +874,7 @@ gdr_status launch_gated(GatedArgs& a, const Plan& p, cudaStream_t s) {
     struct Tag;
     if (p.smem > kPlainSmem && !allow_smem<Tag>(gated_kernel<S, BWD>, kSmemPerSm))
       return GDR_ERR_CUDA;
-    return launch_kernel(gated_kernel<S, BWD>, dim3(p.blocks), p.threads, p.smem, s, a);
+    return launch_behind_smem(gated_kernel<S, BWD>, dim3(p.blocks), p.threads, p.smem, s, a);
   });
 }
 
@@ -1026,7 +1027,7 @@ gdr_status gdr_residual_norm(const void* residual, const void* y, const void* ga
     struct Tag;
     if (p.smem > kPlainSmem && !allow_smem<Tag>(residual_fwd_kernel<S>, kSmemPerSm))
       return GDR_ERR_CUDA;
-    return launch_kernel(residual_fwd_kernel<S>, dim3(p.blocks), p.threads, p.smem, s, a);
+    return launch_behind_smem(residual_fwd_kernel<S>, dim3(p.blocks), p.threads, p.smem, s, a);
   });
 }
 
@@ -1098,7 +1099,10 @@ gdr_status gdr_residual_norm_bwd(const void* d_out, const void* d_residual_out,
     auto go = [&](auto* fn, auto* tag) {
       if (p.smem > kPlainSmem && !allow_smem<std::remove_pointer_t<decltype(tag)>>(fn, kSmemPerSm))
         return GDR_ERR_CUDA;
-      return launch_kernel(fn, dim3(p.blocks), p.threads, p.smem, s, a);
+      // Blocks of a call that fills the device do not come early: their shared memory would be
+      // taken from the kernel before (training step of 2 x 8192 x 4096: TIME).
+      return p.blocks < kSms * 2 ? launch_behind_smem(fn, dim3(p.blocks), p.threads, p.smem, s, a)
+                             : launch_kernel(fn, dim3(p.blocks), p.threads, p.smem, s, a);
     };
     struct Full;
     struct Plain;

@@ -10,6 +10,13 @@ namespace gdr {
 namespace ops {
 namespace {
 
+// Every kernel here may be launched while the one before it in the stream still runs, and lets the
+// next one be: this is the point from which it touches memory (TIMES).
+__device__ __forceinline__ void begin_behind() {
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // Who holds a row, and how. LANES > 0: that many lanes of a warp (8, 16 or 32), several rows
 // per warp. LANES == 0: a whole block, whose size follows the row's. A thread holds NV runs of
 // V consecutive elements; run c of thread i starts at element (c threads + i) V. V is 8 where
@@ -112,6 +119,47 @@ __device__ __forceinline__ void store_any(void* p, int64_t i, int is_bf16, const
     store_run<float, V>(static_cast<float*>(p) + i, f);
 }
 
+// Operations on runs of V elements, in pairs where V is 8 (two fp32 operations per instruction).
+template <int V, typename F2, typename F1>
+__device__ __forceinline__ void over_run(F2 two, F1 one) {
+  if constexpr (V == 8) {
+#pragma unroll
+    for (int i = 0; i < V; i += 2) two(i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) one(i);
+  }
+}
+__device__ __forceinline__ float2 pair_at(const float* a, int i) { return make_float2(a[i], a[i + 1]); }
+__device__ __forceinline__ void put_pair(float* d, int i, float2 v) { d[i] = v.x, d[i + 1] = v.y; }
+template <int V>                                 // d = a b
+__device__ __forceinline__ void mul_run(float* d, const float* a, const float* b) {
+  over_run<V>([&](int i) { put_pair(d, i, mul2(pair_at(a, i), pair_at(b, i))); },
+              [&](int i) { d[i] = a[i] * b[i]; });
+}
+template <int V>                                 // d = s a
+__device__ __forceinline__ void scale_run(float* d, const float* a, float s) {
+  over_run<V>([&](int i) { put_pair(d, i, mul2(pair_at(a, i), make_float2(s, s))); },
+              [&](int i) { d[i] = a[i] * s; });
+}
+template <int V>                                 // d = a b + c
+__device__ __forceinline__ void fma_run(float* d, const float* a, const float* b, const float* c) {
+  over_run<V>([&](int i) { put_pair(d, i, fma2(pair_at(a, i), pair_at(b, i), pair_at(c, i))); },
+              [&](int i) { d[i] = fmaf(a[i], b[i], c[i]); });
+}
+template <int V>                                 // d = s a + c
+__device__ __forceinline__ void fma_run(float* d, const float* a, float s, const float* c) {
+  over_run<V>([&](int i) { put_pair(d, i, fma2(pair_at(a, i), make_float2(s, s), pair_at(c, i))); },
+              [&](int i) { d[i] = fmaf(a[i], s, c[i]); });
+}
+template <int V>                                 // sum of a b
+__device__ __forceinline__ float dot_run(const float* a, const float* b) {
+  float2 s = make_float2(0.f, 0.f);
+  over_run<V>([&](int i) { s = fma2(pair_at(a, i), pair_at(b, i), s); },
+              [&](int i) { s.x = fmaf(a[i], b[i], s.x); });
+  return s.x + s.y;
+}
+
 // act(z) and its derivative.
 enum Act { kNone = GDR_ACT_NONE, kSigmoid = GDR_ACT_SIGMOID, kSilu = GDR_ACT_SILU };
 // 1 / (1 + e^-z) by the approximate 2^x and reciprocal (2^-22 each, and the rounding of z log2(e),
@@ -132,7 +180,7 @@ __device__ __forceinline__ float act(float z, int kind, float& slope) {
     slope = 1.f;
     return z;
   }
-  const float g = sigmoid(z), h = 1.f - g;
+  const float g = sigmoid(z), h = 1.f - g;       // slope may be z's own variable: z is a copy
   slope = kind == kSigmoid ? g * h : fmaf(z * g, h, g);
   return kind == kSigmoid ? g : z * g;
 }
