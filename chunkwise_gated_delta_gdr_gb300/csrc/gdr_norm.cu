@@ -249,32 +249,31 @@ __global__ void __launch_bounds__(kMaxThreads) gated_kernel(GatedArgs a) {
   __shared__ float sums[BWD && S::LANES ? 8 * 32 * N : 1];      // at most 8 warps in such a block
   const Walk w = walk_of<S::LANES>(a.tokens, a.H, a.groups);
   const int phase = S::SHIFT ? (int)((((long long)w.tok * a.H + w.head) * a.D) & 7) : 0;
-  const Ahead ahead = {places, a.pieces, a.stages};
+  const Ahead ahead(places, a.pieces, a.stages);
   const float* weight = a.w && a.per_head ? a.w + (size_t)w.head * a.D : a.w;
   float acc[N];
 #pragma unroll
   for (int j = 0; j < N; ++j) acc[j] = 0.f;
 
   Row<S, S::NV <= 4> row[TENSORS];
-  auto rows_of = [&](int it) {                   // false: no such row
-    const int tok = w.tok + it * w.step;
-    if (!w.on || tok >= a.tokens) return false;
-    const int b = tok / a.T, t = tok - b * a.T;
-    const int per = NV * (a.in_bf16 ? 1 : 2);
-    row[0].set(a.x.p, a.x.at(b, t, w.head), a.in_bf16, 0);
-    row[1].set(a.z.p, a.z.at(b, t, w.head), a.in_bf16, per);
-    if (BWD) row[TENSORS - 1].set(a.d.p, a.d.at(b, t, w.head), a.out_bf16, 2 * per);
-    return true;
+  auto has = [&](int it) { return w.on && w.tok + it * w.step < a.tokens; };
+  auto locate = [&](int it) {
+    const int tok = w.tok + it * w.step, per = NV * (a.in_bf16 ? 1 : 2);
+    row[0].set(a.x.p, a.x.at(tok, a.T, a.flat, w.head), a.in_bf16, 0);
+    row[1].set(a.z.p, a.z.at(tok, a.T, a.flat, w.head), a.in_bf16, per);
+    if (BWD) row[TENSORS - 1].set(a.d.p, a.d.at(tok, a.T, 1, w.head), a.out_bf16, 2 * per);
   };
   auto fetch = [&](int it, int stage) {
     if constexpr (S::kAhead || S::kRegs) {
-      if (it < w.iters && rows_of(it)) {
+      if (has(it)) {
+        const uint32_t at = ahead.of(stage);
+        locate(it);
 #pragma unroll
         for (int c = 0; c < NV; ++c) {
           const int i = (c * w.threads + w.tid) * V - phase;
           if (i < a.D)
 #pragma unroll
-            for (int k = 0; k < TENSORS; ++k) row[k].fetch(ahead, stage, c, i, a.D);
+            for (int k = 0; k < TENSORS; ++k) row[k].fetch(ahead, at, c, i, a.D);
         }
       }
       if constexpr (S::kAhead) ptx::cp_async_commit();
@@ -288,7 +287,9 @@ __global__ void __launch_bounds__(kMaxThreads) gated_kernel(GatedArgs a) {
     for (int k = 0; k < TENSORS; ++k) row[k].advance();
     fetch(it + a.stages - 1, stage == 0 ? a.stages - 1 : stage - 1);
     if constexpr (S::kAhead) ahead.wait();
-    const bool on = rows_of(it);
+    const bool on = has(it);
+    if (!(S::kAhead || S::kRegs) && on) locate(it);
+    const uint32_t at = ahead.of(stage);
     const size_t dense = ((size_t)(w.tok + it * w.step) * a.H + w.head) * a.D;
     float s[2] = {0.f, 0.f};
     if (on)
@@ -297,10 +298,10 @@ __global__ void __launch_bounds__(kMaxThreads) gated_kernel(GatedArgs a) {
         const int i = (c * w.threads + w.tid) * V - phase;
         if (i >= a.D) continue;
         float x[V], z[V], d[V], wt[V];
-        row[0].get(ahead, stage, c, i, a.D, x);
-        if (a.first || BWD) row[1].get(ahead, stage, c, i, a.D, z);
+        row[0].get(ahead, at, c, i, a.D, x);
+        if (a.first || BWD) row[1].get(ahead, at, c, i, a.D, z);
         if (BWD) {
-          row[TENSORS - 1].get(ahead, stage, c, i, a.D, d);
+          row[TENSORS - 1].get(ahead, at, c, i, a.D, d);
           if (weight) load_shared<S>(weight, i, a.D, wt);
         }
 #pragma unroll
@@ -322,9 +323,9 @@ __global__ void __launch_bounds__(kMaxThreads) gated_kernel(GatedArgs a) {
       const int i = (c * w.threads + w.tid) * V - phase;
       if (i >= a.D) continue;
       float x[V], z[V], d[V], wt[V], o[V], oz[V];
-      row[0].get(ahead, stage, c, i, a.D, x);
-      row[1].get(ahead, stage, c, i, a.D, z);
-      if (BWD) row[TENSORS - 1].get(ahead, stage, c, i, a.D, d);
+      row[0].get(ahead, at, c, i, a.D, x);
+      row[1].get(ahead, at, c, i, a.D, z);
+      if (BWD) row[TENSORS - 1].get(ahead, at, c, i, a.D, d);
       if (weight) {
         load_shared<S>(weight, i, a.D, wt);
       } else {
@@ -383,39 +384,50 @@ struct ResArgs {
   int r_bf16, y_bf16, out_bf16;  // y_bf16: of y and z; out_bf16: of out and d
   int has_y, has_z, has_dr;
   int pieces, stages;
+  int flat;                      // the views' tokens are one stride apart, over batch rows too
   float eps, inv_d, s;
 };
 
-template <class S>
+// The types of a call (residual; y and gate; out): the usual ones known when the kernel is
+// compiled, the others from its arguments.
+enum { kAnyTypes, kAllBf16, kF32Residual, kAllF32 };
+template <int TY>
+struct Types {
+  __device__ static constexpr int r(const ResArgs& a) { return TY == kAnyTypes ? a.r_bf16 : TY == kAllBf16; }
+  __device__ static constexpr int y(const ResArgs& a) { return TY == kAnyTypes ? a.y_bf16 : TY != kAllF32; }
+  __device__ static constexpr int out(const ResArgs& a) { return TY == kAnyTypes ? a.out_bf16 : TY != kAllF32; }
+};
+
+template <class S, int TY>
 __global__ void __launch_bounds__(kMaxThreads) residual_fwd_kernel(ResArgs a) {
   constexpr int V = S::V, NV = S::NV, N = S::N;
   extern __shared__ __align__(16) char places[];
   __shared__ Red red;
   const Walk w = walk_of<0>(a.tokens, 1, gridDim.x);
   const int phase = S::SHIFT ? (int)(((long long)w.tok * a.D) & 7) : 0;
-  const Ahead ahead = {places, a.pieces, a.stages};
+  const Ahead ahead(places, a.pieces, a.stages);
   Row<S, false> rr;                              // may be the result's own memory
   Row<S, S::NV <= 4> ry, rz;
-  auto rows_of = [&](int it) {
-    const int tok = w.tok + it * w.step;
-    if (tok >= a.tokens) return false;
-    const int b = tok / a.T, t = tok - b * a.T;
-    const int rp = NV * (a.r_bf16 ? 1 : 2), yp = NV * (a.y_bf16 ? 1 : 2);
-    rr.set(a.r.p, a.r.at(b, t, 0), a.r_bf16, 0);
-    ry.set(a.y.p, a.y.at(b, t, 0), a.y_bf16, rp);
-    rz.set(a.z.p, a.z.at(b, t, 0), a.y_bf16, rp + yp);
-    return true;
+  const int r_bf16 = Types<TY>::r(a), y_bf16 = Types<TY>::y(a), out_bf16 = Types<TY>::out(a);
+  auto has = [&](int it) { return w.tok + it * w.step < a.tokens; };
+  auto locate = [&](int it) {
+    const int tok = w.tok + it * w.step, rp = NV * (r_bf16 ? 1 : 2), yp = NV * (y_bf16 ? 1 : 2);
+    rr.set(a.r.p, a.r.at(tok, a.T, a.flat, 0), r_bf16, 0);
+    ry.set(a.y.p, a.y.at(tok, a.T, a.flat, 0), y_bf16, rp);
+    rz.set(a.z.p, a.z.at(tok, a.T, a.flat, 0), y_bf16, rp + yp);
   };
   auto fetch = [&](int it, int stage) {
     if constexpr (S::kAhead || S::kRegs) {
-      if (it < w.iters && rows_of(it)) {
+      if (has(it)) {
+        const uint32_t at = ahead.of(stage);
+        locate(it);
 #pragma unroll
         for (int c = 0; c < NV; ++c) {
           const int i = (c * w.threads + w.tid) * V - phase;
           if (i < a.D) {
-            rr.fetch(ahead, stage, c, i, a.D);
-            if (a.has_y) ry.fetch(ahead, stage, c, i, a.D);
-            if (a.has_z) rz.fetch(ahead, stage, c, i, a.D);
+            rr.fetch(ahead, at, c, i, a.D);
+            if (a.has_y) ry.fetch(ahead, at, c, i, a.D);
+            if (a.has_z) rz.fetch(ahead, at, c, i, a.D);
           }
         }
       }
@@ -429,7 +441,9 @@ __global__ void __launch_bounds__(kMaxThreads) residual_fwd_kernel(ResArgs a) {
     rr.advance(), ry.advance(), rz.advance();
     fetch(it + a.stages - 1, stage == 0 ? a.stages - 1 : stage - 1);
     if constexpr (S::kAhead) ahead.wait();
-    if (!rows_of(it)) break;                     // the whole block
+    if (!has(it)) break;                         // the whole block
+    if (!(S::kAhead || S::kRegs)) locate(it);
+    const uint32_t at = ahead.of(stage);
     const size_t dense = (size_t)(w.tok + it * w.step) * a.D;
     float py = 1.f, s[1];
     if (a.post) {
@@ -439,7 +453,7 @@ __global__ void __launch_bounds__(kMaxThreads) residual_fwd_kernel(ResArgs a) {
         const int i = (c * w.threads + w.tid) * V - phase;
         if (i >= a.D) continue;
         float y[V];
-        ry.get(ahead, stage, c, i, a.D, y);
+        ry.get(ahead, at, c, i, a.D, y);
         s[0] += dot_run<V>(y, y);
       }
       row_sum<0, 1>(s, red, turn);
@@ -452,17 +466,17 @@ __global__ void __launch_bounds__(kMaxThreads) residual_fwd_kernel(ResArgs a) {
       const int i = (c * w.threads + w.tid) * V - phase;
       if (i >= a.D) continue;
       float* x = r + c * V;
-      rr.get(ahead, stage, c, i, a.D, x);
+      rr.get(ahead, at, c, i, a.D, x);
       if (a.has_y) {
         float y[V], k[V];
-        ry.get(ahead, stage, c, i, a.D, y);
+        ry.get(ahead, at, c, i, a.D, y);
         if (a.post) scale_run<V>(y, y, py);
         if (a.wp) {
           load_shared<S>(a.wp, i, a.D, k);
           mul_run<V>(y, y, k);
         }
         if (a.has_z) {
-          rz.get(ahead, stage, c, i, a.D, k);
+          rz.get(ahead, at, c, i, a.D, k);
 #pragma unroll
           for (int e = 0; e < V; ++e) k[e] = act(k[e], a.kind);
           mul_run<V>(y, y, k);
@@ -473,7 +487,7 @@ __global__ void __launch_bounds__(kMaxThreads) residual_fwd_kernel(ResArgs a) {
         } else {
           fma_run<V>(x, y, a.s, x);
         }
-        store_row<S>(a.r_out, dense, i, a.D, a.r_bf16, x);
+        store_row<S>(a.r_out, dense, i, a.D, r_bf16, x);
       }
       s[0] += dot_run<V>(x, x);
     }
@@ -489,52 +503,53 @@ __global__ void __launch_bounds__(kMaxThreads) residual_fwd_kernel(ResArgs a) {
         load_shared<S>(a.w, i, a.D, k);
         mul_run<V>(o, o, k);
       }
-      store_row<S>(a.out, dense, i, a.D, a.out_bf16, o);
+      store_row<S>(a.out, dense, i, a.D, out_bf16, o);
     }
   }
 }
 
 // FULL: y goes through a norm, a gate or a scale per channel; without, dy = s g.
-template <class S, bool FULL>
+template <class S, int TY, bool FULL>
 __global__ void __launch_bounds__(kMaxThreads) residual_bwd_kernel(ResArgs a) {
   constexpr int V = S::V, NV = S::NV, N = S::N;
   extern __shared__ __align__(16) char places[];
   __shared__ Red red;
   const Walk w = walk_of<0>(a.tokens, 1, gridDim.x);
   const int phase = S::SHIFT ? (int)(((long long)w.tok * a.D) & 7) : 0;
-  const Ahead ahead = {places, a.pieces, a.stages};
+  const Ahead ahead(places, a.pieces, a.stages);
   float acc[FULL ? 3 : 1][N];
 #pragma unroll
   for (int k = 0; k < (FULL ? 3 : 1); ++k)
 #pragma unroll
     for (int j = 0; j < N; ++j) acc[k][j] = 0.f;
   Row<S, S::NV <= 4> rr, rd, rg, ry, rz;
-  auto rows_of = [&](int it) {
+  const int r_bf16 = Types<TY>::r(a), y_bf16 = Types<TY>::y(a), out_bf16 = Types<TY>::out(a);
+  auto has = [&](int it) { return w.tok + it * w.step < a.tokens; };
+  auto locate = [&](int it) {
     const int tok = w.tok + it * w.step;
-    if (tok >= a.tokens) return false;
-    const int b = tok / a.T, t = tok - b * a.T;
-    const int rp = NV * (a.r_bf16 ? 1 : 2), op = NV * (a.out_bf16 ? 1 : 2);
-    const int yp = NV * (a.y_bf16 ? 1 : 2), at = rp + op + (a.has_dr ? rp : 0);
-    rr.set(a.r.p, a.r.at(b, t, 0), a.r_bf16, 0);
-    rd.set(a.d.p, a.d.at(b, t, 0), a.out_bf16, rp);
-    rg.set(a.dr.p, a.dr.at(b, t, 0), a.r_bf16, rp + op);
-    ry.set(a.y.p, a.y.at(b, t, 0), a.y_bf16, at);
-    rz.set(a.z.p, a.z.at(b, t, 0), a.y_bf16, at + yp);
-    return true;
+    const int rp = NV * (r_bf16 ? 1 : 2), op = NV * (out_bf16 ? 1 : 2);
+    const int yp = NV * (y_bf16 ? 1 : 2), at = rp + op + (a.has_dr ? rp : 0);
+    rr.set(a.r.p, a.r.at(tok, a.T, a.flat, 0), r_bf16, 0);
+    rd.set(a.d.p, a.d.at(tok, a.T, 1, 0), out_bf16, rp);
+    rg.set(a.dr.p, a.dr.at(tok, a.T, 1, 0), r_bf16, rp + op);
+    ry.set(a.y.p, a.y.at(tok, a.T, a.flat, 0), y_bf16, at);
+    rz.set(a.z.p, a.z.at(tok, a.T, a.flat, 0), y_bf16, at + yp);
   };
   auto fetch = [&](int it, int stage) {
     if constexpr (S::kAhead || S::kRegs) {
-      if (it < w.iters && rows_of(it)) {
+      if (has(it)) {
+        const uint32_t at = ahead.of(stage);
+        locate(it);
 #pragma unroll
         for (int c = 0; c < NV; ++c) {
           const int i = (c * w.threads + w.tid) * V - phase;
           if (i < a.D) {
-            rr.fetch(ahead, stage, c, i, a.D);
-            rd.fetch(ahead, stage, c, i, a.D);
-            if (a.has_dr) rg.fetch(ahead, stage, c, i, a.D);
+            rr.fetch(ahead, at, c, i, a.D);
+            rd.fetch(ahead, at, c, i, a.D);
+            if (a.has_dr) rg.fetch(ahead, at, c, i, a.D);
             if (FULL) {
-              ry.fetch(ahead, stage, c, i, a.D);
-              if (a.has_z) rz.fetch(ahead, stage, c, i, a.D);
+              ry.fetch(ahead, at, c, i, a.D);
+              if (a.has_z) rz.fetch(ahead, at, c, i, a.D);
             }
           }
         }
@@ -549,7 +564,9 @@ __global__ void __launch_bounds__(kMaxThreads) residual_bwd_kernel(ResArgs a) {
     rr.advance(), rd.advance(), rg.advance(), ry.advance(), rz.advance();
     fetch(it + a.stages - 1, stage == 0 ? a.stages - 1 : stage - 1);
     if constexpr (S::kAhead) ahead.wait();
-    if (!rows_of(it)) break;                     // the whole block
+    if (!has(it)) break;                         // the whole block
+    if (!(S::kAhead || S::kRegs)) locate(it);
+    const uint32_t at = ahead.of(stage);
     const size_t dense = (size_t)(w.tok + it * w.step) * a.D;
     float s[3] = {0.f, 0.f, 0.f};
 #pragma unroll
@@ -557,8 +574,8 @@ __global__ void __launch_bounds__(kMaxThreads) residual_bwd_kernel(ResArgs a) {
       const int i = (c * w.threads + w.tid) * V - phase;
       if (i >= a.D) continue;
       float x[V], d[V], k[V];
-      rr.get(ahead, stage, c, i, a.D, x);
-      rd.get(ahead, stage, c, i, a.D, d);
+      rr.get(ahead, at, c, i, a.D, x);
+      rd.get(ahead, at, c, i, a.D, d);
       if (a.w) {
         load_shared<S>(a.w, i, a.D, k);
         mul_run<V>(d, d, k);
@@ -566,7 +583,7 @@ __global__ void __launch_bounds__(kMaxThreads) residual_bwd_kernel(ResArgs a) {
       s[0] += dot_run<V>(x, x);
       s[1] += dot_run<V>(d, x);
       if (FULL && a.post) {
-        ry.get(ahead, stage, c, i, a.D, x);
+        ry.get(ahead, at, c, i, a.D, x);
         s[2] += dot_run<V>(x, x);
       }
     }
@@ -579,10 +596,10 @@ __global__ void __launch_bounds__(kMaxThreads) residual_bwd_kernel(ResArgs a) {
       const int i = (c * w.threads + w.tid) * V - phase;
       if (i >= a.D) continue;
       float g[V], x[V], d[V], k[V];
-      rr.get(ahead, stage, c, i, a.D, x);
-      rd.get(ahead, stage, c, i, a.D, d);
+      rr.get(ahead, at, c, i, a.D, x);
+      rd.get(ahead, at, c, i, a.D, d);
       if (a.has_dr) {
-        rg.get(ahead, stage, c, i, a.D, g);
+        rg.get(ahead, at, c, i, a.D, g);
       } else {
 #pragma unroll
         for (int e = 0; e < V; ++e) g[e] = 0.f;
@@ -595,17 +612,17 @@ __global__ void __launch_bounds__(kMaxThreads) residual_bwd_kernel(ResArgs a) {
       }
       fma_run<V>(d, x, -m, d);
       fma_run<V>(g, d, rho, g);
-      store_row<S>(a.o_dr, dense, i, a.D, a.r_bf16, g);
+      store_row<S>(a.o_dr, dense, i, a.D, r_bf16, g);
       if (!FULL) {
         if (a.o_dy) {
           scale_run<V>(g, g, a.s);
-          store_row<S>(a.o_dy, dense, i, a.D, a.y_bf16, g);
+          store_row<S>(a.o_dy, dense, i, a.D, y_bf16, g);
         }
         continue;
       }
       if constexpr (FULL) {
         float y[V], z[V], p[V], q[V];
-        ry.get(ahead, stage, c, i, a.D, y);
+        ry.get(ahead, at, c, i, a.D, y);
         if (a.post) scale_run<V>(y, y, py);      // uy
         if (a.wp) {
           load_shared<S>(a.wp, i, a.D, k);
@@ -615,7 +632,7 @@ __global__ void __launch_bounds__(kMaxThreads) residual_bwd_kernel(ResArgs a) {
           for (int e = 0; e < V; ++e) p[e] = y[e];
         }
         if (a.has_z) {
-          rz.get(ahead, stage, c, i, a.D, z);
+          rz.get(ahead, at, c, i, a.D, z);
 #pragma unroll
           for (int e = 0; e < V; ++e) q[e] = act(z[e], a.kind, z[e]);    // a, and a' in z
           mul_run<V>(z, z, g);
@@ -634,7 +651,7 @@ __global__ void __launch_bounds__(kMaxThreads) residual_bwd_kernel(ResArgs a) {
           scale_run<V>(q, q, a.s);
           if (a.has_z) scale_run<V>(z, z, a.s);
         }
-        if (a.has_z) store_row<S>(a.o_dz, dense, i, a.D, a.y_bf16, z);
+        if (a.has_z) store_row<S>(a.o_dz, dense, i, a.D, y_bf16, z);
         float* dq = dp + c * V;
         if (a.post) {
           fma_run<V>(acc[1] + c * V, q, y, acc[1] + c * V);
@@ -646,7 +663,7 @@ __global__ void __launch_bounds__(kMaxThreads) residual_bwd_kernel(ResArgs a) {
           }
           se[0] += dot_run<V>(dq, y);
         } else {
-          store_row<S>(a.o_dy, dense, i, a.D, a.y_bf16, q);
+          store_row<S>(a.o_dy, dense, i, a.D, y_bf16, q);
         }
       }
     }
@@ -659,10 +676,10 @@ __global__ void __launch_bounds__(kMaxThreads) residual_bwd_kernel(ResArgs a) {
           const int i = (c * w.threads + w.tid) * V - phase;
           if (i >= a.D) continue;
           float y[V];
-          ry.get(ahead, stage, c, i, a.D, y);
+          ry.get(ahead, at, c, i, a.D, y);
           fma_run<V>(y, y, -py * my, dp + c * V);
           scale_run<V>(y, y, py);
-          store_row<S>(a.o_dy, dense, i, a.D, a.y_bf16, y);
+          store_row<S>(a.o_dy, dense, i, a.D, y_bf16, y);
         }
       }
     }
@@ -918,10 +935,25 @@ gdr_status residual_args(ResArgs& a, const gdr_residual_dims* d, const void* r, 
   a.eps = d->eps;
   a.inv_d = 1.f / d->D;
   a.s = d->scale;
+  a.flat = 1;
+  for (const View* v : {&a.r, &a.y, &a.z})
+    if (v->p && a.B > 1 && v->b != a.T * v->t) a.flat = 0;
   *fit = kVec;
   for (const View* v : {&a.r, &a.y, &a.z})
     if (v->p) *fit = worse(*fit, fit_of(v->p, a.B, a.T, 1, a.D, v->b, v->t, 0));
   return GDR_OK;
+}
+// f(the call's types) for the rows that go through shared memory; the others look at run time.
+template <class S, typename F>
+auto with_types(const ResArgs& a, F f) {
+  if constexpr (S::kAhead) {
+    const int y = a.has_y || a.o_dy ? a.y_bf16 : a.out_bf16; // neither: any type of it
+    if (y == a.out_bf16 && a.r_bf16 && y) return f(std::integral_constant<int, kAllBf16>());
+    if (y == a.out_bf16 && !a.r_bf16)
+      return y ? f(std::integral_constant<int, kF32Residual>())
+               : f(std::integral_constant<int, kAllF32>());
+  }
+  return f(std::integral_constant<int, kAnyTypes>());
 }
 // A gate, a post norm or a scale per channel act on y.
 bool needs_y(const gdr_residual_dims* d, const void* z, const float* wp, const float* sv) {
@@ -1024,10 +1056,14 @@ gdr_status gdr_residual_norm(const void* residual, const void* y, const void* ga
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return with_block(p, [&](auto shape) {
     using S = decltype(shape);
-    struct Tag;
-    if (p.smem > kPlainSmem && !allow_smem<Tag>(residual_fwd_kernel<S>, kSmemPerSm))
-      return GDR_ERR_CUDA;
-    return launch_behind_smem(residual_fwd_kernel<S>, dim3(p.blocks), p.threads, p.smem, s, a);
+    return with_types<S>(a, [&](auto types) {
+      constexpr int TY = decltype(types)::value;
+      struct Tag;
+      if (p.smem > kPlainSmem && !allow_smem<Tag>(residual_fwd_kernel<S, TY>, kSmemPerSm))
+        return GDR_ERR_CUDA;
+      return launch_behind_smem(residual_fwd_kernel<S, TY>, dim3(p.blocks), p.threads, p.smem, s,
+                                a);
+    });
   });
 }
 
@@ -1100,14 +1136,17 @@ gdr_status gdr_residual_norm_bwd(const void* d_out, const void* d_residual_out,
       if (p.smem > kPlainSmem && !allow_smem<std::remove_pointer_t<decltype(tag)>>(fn, kSmemPerSm))
         return GDR_ERR_CUDA;
       // Blocks of a call that fills the device do not come early: their shared memory would be
-      // taken from the kernel before (training step of 2 x 8192 x 4096: TIME).
+      // taken from the kernel before (training step of 2 x 8192 x 4096: 231 us so, 220 us not).
       return p.blocks < kSms * 2 ? launch_behind_smem(fn, dim3(p.blocks), p.threads, p.smem, s, a)
-                             : launch_kernel(fn, dim3(p.blocks), p.threads, p.smem, s, a);
+                                 : launch_kernel(fn, dim3(p.blocks), p.threads, p.smem, s, a);
     };
-    struct Full;
-    struct Plain;
-    return full ? go(residual_bwd_kernel<S, true>, static_cast<Full*>(nullptr))
-                : go(residual_bwd_kernel<S, false>, static_cast<Plain*>(nullptr));
+    return with_types<S>(a, [&](auto types) {
+      constexpr int TY = decltype(types)::value;
+      struct Full;
+      struct Plain;
+      return full ? go(residual_bwd_kernel<S, TY, true>, static_cast<Full*>(nullptr))
+                  : go(residual_bwd_kernel<S, TY, false>, static_cast<Plain*>(nullptr));
+    });
   });
   if (run != GDR_OK || !a.part) return run;
   return sum_parts(a.part, d_weight, d_post_weight, d_scale, p.rows, dims->D, s);

@@ -243,17 +243,33 @@ __device__ __forceinline__ Walk walk_of(int tokens, int H, int groups) {
 struct View {
   const void* p;
   int64_t b, t, h;
-  __device__ int64_t at(int bi, int ti, int head) const { return bi * b + ti * t + head * h; }
+  // Of token `tok` of all batch rows; flat: those are one token stride apart, too.
+  __device__ __forceinline__ int64_t at(int tok, int T, int flat, int head) const {
+    if (flat) return tok * t + head * h;
+    const int bi = tok / T;
+    return bi * b + (tok - bi * T) * t + head * h;
+  }
 };
+__device__ __forceinline__ uint4 shared16(uint32_t at) {
+  uint4 u;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+               : "r"(at)
+               : "memory");
+  return u;
+}
 
 // A group's copies ahead of time: every thread's own pieces of 16 bytes, in its own places of
 // shared memory, so that no barrier is needed between a copy and its use.
 struct Ahead {
-  char* base;                                    // [stages][pieces][threads of the block] x 16 bytes
+  uint32_t base, pitch;                          // of this thread; from piece to piece
   int pieces, stages;
-  __device__ __forceinline__ char* place(int stage, int piece) const {
-    return base + ((size_t)(stage * pieces + piece) * blockDim.x + threadIdx.x) * 16;
-  }
+  __device__ __forceinline__ Ahead(const char* places, int pieces_, int stages_)
+      : base(ptx::smem_u32(places) + threadIdx.x * 16),
+        pitch(blockDim.x * 16),
+        pieces(pieces_),
+        stages(stages_) {}
+  __device__ __forceinline__ uint32_t of(int stage) const { return base + stage * pieces * pitch; }
   __device__ __forceinline__ void wait() const {
     if (stages == 3)
       ptx::cp_async_wait<2>();
@@ -279,19 +295,19 @@ struct Row {
   }
   __device__ __forceinline__ int per_run() const { return is_bf16 ? 1 : 2; }
   // D: the row's length.
-  __device__ __forceinline__ void fetch(const Ahead& a, int stage, int c, int i, int D) {
+  __device__ __forceinline__ void fetch(const Ahead& a, uint32_t places, int c, int i, int D) {
     if constexpr (S::kRegs) {
       load_any<1, ONLY_READ>(p, i, is_bf16, next + c);
     } else {
-      const int es = is_bf16 ? 2 : 4, at = first + c * per_run();
+      const int es = is_bf16 ? 2 : 4;
+      const uint32_t at = places + (first + c * per_run()) * a.pitch;
       const char* src = static_cast<const char*>(p) + (int64_t)i * es;
       int left = 16 * per_run();                 // bytes of the run
       if (S::SHIFT) left = min(left, (D - i) * es);        // nothing behind the row is read
-      ptx::cp_async16(ptx::smem_u32(a.place(stage, at)), src, min(left, 16));
+      ptx::cp_async16(at, src, min(left, 16));
       if (!is_bf16) {
         const bool more = left > 16;
-        ptx::cp_async16(ptx::smem_u32(a.place(stage, at + 1)), more ? src + 16 : src,
-                        more ? left - 16 : 0);
+        ptx::cp_async16(at + a.pitch, more ? src + 16 : src, more ? left - 16 : 0);
       }
     }
   }
@@ -300,16 +316,16 @@ struct Row {
 #pragma unroll
       for (int j = 0; j < S::N; ++j) now[j] = next[j];
   }
-  __device__ __forceinline__ void get(const Ahead& a, int stage, int c, int i, int D,
+  __device__ __forceinline__ void get(const Ahead& a, uint32_t places, int c, int i, int D,
                                       float* f) const {
     if constexpr (S::kAhead) {
-      const int at = first + c * per_run();
-      const uint4 u = *reinterpret_cast<const uint4*>(a.place(stage, at));
+      const uint32_t at = places + (first + c * per_run()) * a.pitch;
+      const uint4 u = shared16(at);
       if (is_bf16) {
         const Run<bf16, 8> r = {{u.x, u.y, u.z, u.w}};
         unpack<bf16, 8>(r, f);
       } else {
-        const uint4 v = *reinterpret_cast<const uint4*>(a.place(stage, at + 1));
+        const uint4 v = shared16(at + a.pitch);
         const Run<float, 8> r = {{u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w}};
         unpack<float, 8>(r, f);
       }
