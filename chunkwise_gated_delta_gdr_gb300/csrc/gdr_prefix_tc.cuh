@@ -44,6 +44,7 @@ struct Config {
   static_assert(U * D + 2 * KT <= 512 && SMEM <= 232448, "");
 };
 constexpr int LAG = 3;                                     // tiles of copies in flight, less one
+constexpr long kDrainPolls = 1L << 20;                     // of the last waits; about a second
 
 __device__ __forceinline__ void umma_bf16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id,
                                              int acc) {
@@ -184,7 +185,9 @@ struct Bars {
   uint32_t tmem, dead, bad;           // dead: a wait gave up; bad: a page out of range
 };
 
-// A wait that gives up after `polls`, or when another role has.
+// A wait that gives up after `polls`, or when another role has: then every role runs to its end,
+// the block's remaining parts get a sum of NaN, and copies and products under way are waited for,
+// again with a limit.
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, long polls,
                                          volatile uint32_t* dead) {
   if (mbar_test(bar, parity)) return true;
@@ -405,9 +408,8 @@ __global__ void __launch_bounds__(Config<D, TMA>::THREADS, 1)
       }
       st.left -= last - st.tile;
     }
-    if (!ok)                                               // no copy outlives the block
-      for (int k = max(0, n - ST); k < n; ++k)
-        mbar_wait(&bars.kv_full[k % ST], (k / ST) & 1, a.polls);
+    for (int k = max(0, n - ST); k < n; ++k)               // no copy outlives the block
+      mbar_wait(&bars.kv_full[k % ST], (k / ST) & 1, kDrainPolls);
   } else if (!TMA && warp < F::SOFT + F::LOAD) {
     // ------------------------------------------------------------ copies, row by row
     // Warp w takes every third row from w on (a fourth warp would leave the softmax 128 registers
@@ -538,10 +540,8 @@ __global__ void __launch_bounds__(Config<D, TMA>::THREADS, 1)
       n0 += 2 * tiles;
       st.left -= tiles;
     }
-    if (!ok) {                                             // nothing of this block's is left running
-      umma_commit(&bars.fin);
-      mbar_wait(&bars.fin, 0, a.polls);
-    }
+    umma_commit(&bars.fin);                                // and no product
+    mbar_wait(&bars.fin, 0, kDrainPolls);
   }
   tc_fence_before();
   __syncthreads();

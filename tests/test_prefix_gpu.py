@@ -350,3 +350,28 @@ def test_refusals_on_the_gpu(compiled, monkeypatch):
     with pytest.raises(TypeError):
         call(s, out=torch.empty_like(s["q"]), out_dtype=F32)
     check(s)
+
+
+@pytest.mark.parametrize("D,B,HQ,HK,P,page", [(128, 64, 16, 4, 5000, 64), (128, 3, 4, 2, 5000, 64),
+                                              (64, 200, 2, 2, 900, 17), (256, 40, 8, 2, 3001, 128)])
+def test_waits_that_give_up(D, B, HQ, HK, P, page):
+    """With few polls allowed the kernel's waits give up: every result is NaN or has its right
+    bits, the launch ends by itself, and calls with the usual bound are as ever."""
+    s = make(B, HQ, HK, D, P, [(7 * b) % 40 for b in range(B)], page=page, seed=19)
+    want = call(s)
+    old = gdr.set_flag_wait_limit(-1)
+    for polls in (0, 0, 16, 32, 128, 1024):      # a sixteenth of them per wait
+        gdr.set_flag_wait_limit(polls)
+        try:
+            got = call(s, out=torch.full_like(s["q"], 7),
+                       lse=torch.full((B, HQ), 7.0, device=DEV))
+            torch.cuda.synchronize()
+        finally:
+            gdr.set_flag_wait_limit(old)
+        for a, b in zip(got, want):
+            there = ~torch.isnan(a)
+            assert torch.equal(a[there], b[there]), polls
+        if polls == 0:                           # a tile needs a microsecond
+            assert torch.isnan(got[0]).any() and torch.isnan(got[1]).any()
+    for a, b in zip(call(s), want):
+        assert torch.equal(a, b)
