@@ -22,16 +22,118 @@ namespace ops {
 namespace {
 
 // ------------------------------------------------------------ fp32 arithmetic, any type
-// 64 rows x 64 keys a step: scores as 4 x 4 per thread from shared memory, then the rows'
-// softmax by four lanes each, then 4 rows x (D / 16) channels per thread of the product with V.
+// Up to 64 rows x 64 keys a step: scores as NI x 4 per thread from shared memory, then the rows'
+// softmax by four lanes each, then NI rows x (D / 16) channels per thread of the product with V,
+// NI = 1, 2 or 4 as there are rows. fp32 caches with 16-byte rows are copied asynchronously: the
+// next tile's K while this one's weights and P V are computed, its V while the next scores are.
+// 5 sequences behind 2999 keys, HK = 3, D = 64: a block has one tile, and the call is the chain
+// page - row - scores - sums - join (20 us; with a page looked up per row 20.4). Long prompts are
+// bound by the reads of q and k from shared memory.
 constexpr int RM = 64, KT = 64, NT = 256;
 template <int NJ>                                // channels in runs of 64: D <= 64 NJ
 struct AnySmem {
   static constexpr int DP = NJ * 64, LD = DP + 4, LS = KT + 4;
   float q[RM * LD], k[KT * LD], v[KT * LD], s[RM * LS];
   float factor[RM];
+  int64_t row[2][KT];                            // where the keys of a tile start; -1: none
   int bad;
 };
+
+// A tile of K or V into shared memory: asynchronously (to be waited for) or at once.
+template <typename T, int NJ>
+__device__ __forceinline__ void any_tile(const PrefixArgs& a, float* to, const T* cache,
+                                         const int64_t* row, int vec) {
+  constexpr int DP = NJ * 64, LD = DP + 4, PER = DP / 4;
+#pragma unroll 4
+  for (int e = threadIdx.x; e < KT * PER; e += NT) {
+    const int r = e / PER, d = 4 * (e - r * PER);
+    const int64_t at = row[r];
+    if (sizeof(T) == 4 && vec) {
+      const bool there = at >= 0 && d < a.D;
+      ptx::cp_async16(ptx::smem_u32(to + r * LD + d), cache + (there ? at + d : 0), there ? 16 : 0);
+      continue;
+    }
+    float f[4] = {0.f, 0.f, 0.f, 0.f};
+    if (at >= 0 && d < a.D) {
+      if (vec) {
+        load_f<T, 4>(cache + at + d, f);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (d + i < a.D) f[i] = static_cast<float>(cache[at + d + i]);
+      }
+    }
+    *reinterpret_cast<float4*>(to + r * LD + d) = make_float4(f[0], f[1], f[2], f[3]);
+  }
+}
+
+// Scores of rows ty + 16 i, keys tx + 16 j; keys from `live` on get -inf.
+template <int NJ, int NI>
+__device__ __forceinline__ void any_scores(AnySmem<NJ>& sm, int live) {
+  constexpr int LD = AnySmem<NJ>::LD, LS = AnySmem<NJ>::LS;
+  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+  float2 acc[NI][4];
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = make_float2(0.f, 0.f);
+#pragma unroll 4
+  for (int d = 0; d < NJ * 64; d += 4) {
+    float4 qv[NI], kv[4];
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+      qv[i] = *reinterpret_cast<const float4*>(&sm.q[(ty + 16 * i) * LD + d]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      kv[j] = *reinterpret_cast<const float4*>(&sm.k[(tx + 16 * j) * LD + d]);
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        acc[i][j] = fma2(make_float2(qv[i].x, qv[i].y), make_float2(kv[j].x, kv[j].y), acc[i][j]);
+        acc[i][j] = fma2(make_float2(qv[i].z, qv[i].w), make_float2(kv[j].z, kv[j].w), acc[i][j]);
+      }
+  }
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      sm.s[(ty + 16 * i) * LS + tx + 16 * j] =
+          tx + 16 * j < live ? acc[i][j].x + acc[i][j].y : -INFINITY;
+}
+
+// o = factor o + P V for rows ty + 16 i, channels 64 j + 4 tx ..
+template <int NJ, int NI>
+__device__ __forceinline__ void any_values(const AnySmem<NJ>& sm, float (*o)[NJ * 4]) {
+  constexpr int LD = AnySmem<NJ>::LD, LS = AnySmem<NJ>::LS;
+  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const float f = sm.factor[ty + 16 * i];
+#pragma unroll
+    for (int j = 0; j < NJ * 4; ++j) o[i][j] *= f;
+  }
+#pragma unroll 2
+  for (int k = 0; k < KT; k += 4) {
+    float4 p[NI];
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+      p[i] = *reinterpret_cast<const float4*>(&sm.s[(ty + 16 * i) * LS + k]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        const float4 v = *reinterpret_cast<const float4*>(&sm.v[(k + e) * LD + 64 * j + 4 * tx]);
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          const float w = e == 0 ? p[i].x : e == 1 ? p[i].y : e == 2 ? p[i].z : p[i].w;
+          float2* oo = reinterpret_cast<float2*>(&o[i][4 * j]);
+          oo[0] = fma2(make_float2(w, w), make_float2(v.x, v.y), oo[0]);
+          oo[1] = fma2(make_float2(w, w), make_float2(v.z, v.w), oo[1]);
+        }
+      }
+  }
+}
 
 template <typename T, int NJ>
 __global__ void __launch_bounds__(NT) prefix_any_kernel(PrefixArgs a, int vec) {
@@ -39,89 +141,62 @@ __global__ void __launch_bounds__(NT) prefix_any_kernel(PrefixArgs a, int vec) {
   typedef AnySmem<NJ> Smem;
   constexpr int DP = Smem::DP, LD = Smem::LD, LS = Smem::LS;
   Smem& sm = *reinterpret_cast<Smem*>(raw);
-  const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
   asm volatile("griddepcontrol.launch_dependents;");
   Stretch st = stretch_of(a, blockIdx.x);
   if (tid == 0) sm.bad = 0;
+  // The keys of tile t, each looked up by one thread.
+  auto find = [&](int t) {
+    if (tid < KT) {
+      const int j = t * KT + tid;
+      const int64_t r = j < a.P ? prefix_row(a, j) : -1;
+      if (j < a.P && r < 0) sm.bad = 1;
+      sm.row[t & 1][tid] = r;
+    }
+  };
   while (st.left > 0) {
     const int hk = st.item / a.row_tiles, r0 = (st.item - hk * a.row_tiles) * RM;
+    const int last = min(a.tiles, st.tile + st.left), rows = min(RM, a.M - r0);
+    const T* kc = static_cast<const T*>(a.kc) + hk * a.ph;
+    const T* vc = static_cast<const T*>(a.vc) + hk * a.ph;
     __syncthreads();                             // the last item's tiles are done with
-    for (int r = warp; r < RM; r += NT / 32) {
-      const int m = r0 + r;
-      const int64_t at = m < a.M ? q_row(a, hk, m) : 0;
-      for (int d = lane; d < DP; d += 32) {
-        float v = 0.f;
-        if (m < a.M && d < a.D)
-          v = a.scale2 * (a.q_bf16 ? __bfloat162float(static_cast<const bf16*>(a.q)[at + d])
-                                   : static_cast<const float*>(a.q)[at + d]);
-        sm.q[r * LD + d] = v;
+    find(st.tile);
+#pragma unroll 4
+    for (int e = tid; e < RM * DP; e += NT) {
+      const int r = e / DP, d = e - r * DP, m = r0 + r;
+      float v = 0.f;
+      if (m < a.M && d < a.D) {
+        const int64_t at = q_row(a, hk, m) + d;
+        v = a.scale2 * (a.q_bf16 ? __bfloat162float(static_cast<const bf16*>(a.q)[at])
+                                 : static_cast<const float*>(a.q)[at]);
       }
+      sm.q[r * LD + d] = v;
     }
     float o[4][NJ * 4], m = -INFINITY, l = 0.f;  // m, l: of row tid / 4
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < NJ * 4; ++j) o[i][j] = 0.f;
-    const int last = min(a.tiles, st.tile + st.left);
-    const T* kc = static_cast<const T*>(a.kc) + hk * a.ph;
-    const T* vc = static_cast<const T*>(a.vc) + hk * a.ph;
+    __syncthreads();
+    any_tile<T, NJ>(a, sm.k, kc, sm.row[st.tile & 1], vec);
+    ptx::cp_async_commit();
+    any_tile<T, NJ>(a, sm.v, vc, sm.row[st.tile & 1], vec);
+    ptx::cp_async_commit();
     for (int t = st.tile; t < last; ++t) {
-      for (int r = warp; r < KT; r += NT / 32) {
-        const int j = t * KT + r;
-        const int64_t row = j < a.P ? prefix_row(a, j) : 0;
-        const bool live = j < a.P && row >= 0;
-        if (j < a.P && row < 0) sm.bad = 1;
-        for (int d = 4 * lane; d < DP; d += 128) {
-          float kv[4], vv[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) kv[e] = vv[e] = 0.f;
-          if (live && vec) {
-            if (d < a.D) {
-              load_f<T, 4>(kc + row + d, kv);
-              load_f<T, 4>(vc + row + d, vv);
-            }
-          } else if (live) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (d + e < a.D) {
-                kv[e] = static_cast<float>(kc[row + d + e]);
-                vv[e] = static_cast<float>(vc[row + d + e]);
-              }
-          }
-          *reinterpret_cast<float4*>(&sm.k[r * LD + d]) = make_float4(kv[0], kv[1], kv[2], kv[3]);
-          *reinterpret_cast<float4*>(&sm.v[r * LD + d]) = make_float4(vv[0], vv[1], vv[2], vv[3]);
-        }
-      }
+      const bool more = t + 1 < last;
+      if (more) find(t + 1);
+      ptx::cp_async_wait<1>();                   // K of this tile
       __syncthreads();
-      float2 acc[4][4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = make_float2(0.f, 0.f);
-#pragma unroll 4
-      for (int d = 0; d < DP; d += 4) {
-        float4 qv[4], kv[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          qv[i] = *reinterpret_cast<const float4*>(&sm.q[(ty + 16 * i) * LD + d]);
-          kv[i] = *reinterpret_cast<const float4*>(&sm.k[(tx + 16 * i) * LD + d]);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            acc[i][j] = fma2(make_float2(qv[i].x, qv[i].y), make_float2(kv[j].x, kv[j].y), acc[i][j]);
-            acc[i][j] = fma2(make_float2(qv[i].z, qv[i].w), make_float2(kv[j].z, kv[j].w), acc[i][j]);
-          }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          sm.s[(ty + 16 * i) * LS + tx + 16 * j] =
-              t * KT + tx + 16 * j < a.P ? acc[i][j].x + acc[i][j].y : -INFINITY;
+      if (rows <= 16)
+        any_scores<NJ, 1>(sm, a.P - t * KT);
+      else if (rows <= 32)
+        any_scores<NJ, 2>(sm, a.P - t * KT);
+      else
+        any_scores<NJ, 4>(sm, a.P - t * KT);
       __syncthreads();
-      {                                          // four lanes per row, every fourth key each
+      if (more) any_tile<T, NJ>(a, sm.k, kc, sm.row[(t + 1) & 1], vec);
+      ptx::cp_async_commit();
+      if (tid >> 2 < (rows + 15) / 16 * 16) {    // four lanes per row, every fourth key each
         float* row = sm.s + (tid >> 2) * LS + (tid & 3);
         float top = m;
 #pragma unroll
@@ -141,34 +216,17 @@ __global__ void __launch_bounds__(NT) prefix_any_kernel(PrefixArgs a, int vec) {
         l = fmaf(l, f, sum);                     // of this lane's keys; the four meet at the end
         if ((tid & 3) == 0) sm.factor[tid >> 2] = f;
       }
+      ptx::cp_async_wait<1>();                   // V of this tile
       __syncthreads();
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float f = sm.factor[ty + 16 * i];
-#pragma unroll
-        for (int j = 0; j < NJ * 4; ++j) o[i][j] *= f;
-      }
-#pragma unroll 2
-      for (int k = 0; k < KT; k += 4) {
-        float4 p[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          p[i] = *reinterpret_cast<const float4*>(&sm.s[(ty + 16 * i) * LS + k]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-#pragma unroll
-          for (int j = 0; j < NJ; ++j) {
-            const float4 v = *reinterpret_cast<const float4*>(&sm.v[(k + e) * LD + 64 * j + 4 * tx]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float w = e == 0 ? p[i].x : e == 1 ? p[i].y : e == 2 ? p[i].z : p[i].w;
-              float2* oo = reinterpret_cast<float2*>(&o[i][4 * j]);
-              oo[0] = fma2(make_float2(w, w), make_float2(v.x, v.y), oo[0]);
-              oo[1] = fma2(make_float2(w, w), make_float2(v.z, v.w), oo[1]);
-            }
-          }
-      }
+      if (rows <= 16)
+        any_values<NJ, 1>(sm, o);
+      else if (rows <= 32)
+        any_values<NJ, 2>(sm, o);
+      else
+        any_values<NJ, 4>(sm, o);
       __syncthreads();
+      if (more) any_tile<T, NJ>(a, sm.v, vc, sm.row[(t + 1) & 1], vec);
+      ptx::cp_async_commit();
     }
     l += __shfl_xor_sync(~0u, l, 1);
     l += __shfl_xor_sync(~0u, l, 2);
@@ -179,14 +237,21 @@ __global__ void __launch_bounds__(NT) prefix_any_kernel(PrefixArgs a, int vec) {
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (r0 + ty + 16 * i < a.M)
+      if (ty + 16 * i < rows)
 #pragma unroll
-        for (int j = 0; j < NJ; ++j)
+        for (int j = 0; j < NJ; ++j) {
+          const int d = 64 * j + 4 * tx;
+          float* to = a.part_o + (part + ty + 16 * i) * a.D + d;
+          if (a.D % 4 == 0) {
+            if (d < a.D)
+              *reinterpret_cast<float4*>(to) =
+                  make_float4(o[i][4 * j], o[i][4 * j + 1], o[i][4 * j + 2], o[i][4 * j + 3]);
+          } else {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int d = 64 * j + 4 * tx + e;
-            if (d < a.D) a.part_o[(part + ty + 16 * i) * a.D + d] = o[i][4 * j + e];
+            for (int e = 0; e < 4; ++e)
+              if (d + e < a.D) to[e] = o[i][4 * j + e];
           }
+        }
     st.left -= last - st.tile;
     st.tile = 0;
     ++st.item;
@@ -198,7 +263,8 @@ __global__ void __launch_bounds__(NT) prefix_any_kernel(PrefixArgs a, int vec) {
 // ------------------------------------------------------------ joining the stretches
 // A row (a query head of a sequence) of few parts takes a warp; one of more the JW warps of a
 // block, every JW-th part each (SPLIT). A lane holds V channels in a row, N runs of them, and
-// has UN parts' loads under way. 64 sequences, 8192 shared keys, HK = 4 (16 parts a row): TIME.
+// has UN parts' loads under way. 64 sequences, 8192 shared keys, HK = 4
+// (16 parts a row), the whole call: 47 us, 55 with one warp for all parts of a row.
 constexpr int JW = 4;
 template <int V, bool SPLIT>
 __global__ void __launch_bounds__(JW * 32) prefix_join_kernel(PrefixArgs a) {

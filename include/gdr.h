@@ -562,7 +562,8 @@ size_t gdr_paged_decode_attn_workspace_size(const gdr_attn_dims* dims,
  *
  * The rest as for gdr_paged_decode_attn. A shared page outside [0, num_pages) gives NaN in
  * every sequence, an own one or a bad length in its sequence. The result does not depend on
- * the order in which blocks run.
+ * the order in which blocks run. Waits inside a block are bounded (gdr_set_flag_wait_limit);
+ * where one gives up, the rows it would have reached are NaN: what is finite is right.
  */
 gdr_status gdr_paged_prefix_attn(const void* q, const void* k_cache, const void* v_cache,
                                  const int32_t* prefix_table, int prefix_pages, int prefix_len,
