@@ -601,6 +601,8 @@ def paged_prefix_attn(q, k_cache, v_cache, prefix_table, prefix_len, page_table,
     (an int): its keys. Every sequence attends to them and, behind them, to its own keys:
     page_table [B, max_pages] and lens [B] describe those alone. The rest as for
     paged_decode_attn, without a window. A shared page out of range gives NaN everywhere.
+    qk_norm_rope_append stores by position: for a prompt of whole pages it takes the tables
+    [prompt's pages | own pages].
     """
     if stream is None and out_dtype is None and _host is not None:
         r = _host.paged_prefix_attn(q, k_cache, v_cache, prefix_table, prefix_len, page_table,

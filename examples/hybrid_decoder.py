@@ -11,6 +11,11 @@ projections are torch matrix products. Shows how the entry points fit together:
   decode    recurrent_fwd, linear_scan_fwd on one token with the state in place,
             qk_norm_rope_append, paged_decode_attn
   training  linear_scan_fwd / _bwd and qk_norm_rope / _bwd as autograd functions
+
+NormedDecoder is the same stack with an output gate behind the delta rule (gated_norm) and its
+adds and norms in one call between two layers (residual_norm); generate_shared() decodes a batch
+behind one prompt, whose states are computed and whose keys are stored and read once
+(paged_prefix_attn). GatedNorm and ResidualNorm are their autograd functions.
 """
 from __future__ import annotations
 
@@ -127,7 +132,131 @@ class HybridDecoder:
         return torch.cat(tokens, 1), torch.cat(seen, 1)
 
 
+# ------------------------------------------------------------------ gate, norms, shared prompt
+class SharedCache:
+    """What decoding behind a shared prompt carries: the prompt's whole pages once, and for
+    every sequence its states and its own pages in the same arrays."""
+
+    def __init__(self, prompt, batch, longest, device):
+        self.shared = prompt // PAGE * PAGE          # tokens of whole pages
+        first, own = self.shared // PAGE, -(-longest // PAGE)
+        order = torch.randperm(first + batch * own, device=device).int()
+        self.prefix, self.table = order[:first].clone(), order[first:].view(batch, own)
+        # New keys are stored by their position in the sequence: prompt's pages, then its own.
+        self.whole = torch.cat([self.prefix.repeat(batch, 1), self.table], 1).contiguous()
+        shape = (first + batch * own, PAGE, HK, DIM)
+        self.k = torch.zeros(shape, dtype=torch.bfloat16, device=device)
+        self.v = torch.zeros_like(self.k)
+        self.delta = torch.zeros(batch, DELTA_HEADS, DELTA_DIM, DELTA_DIM, device=device)
+        self.scan = torch.zeros(batch, WIDTH, device=device)
+        self.length = self.shared
+
+    def prompt(self):
+        """A cache of one sequence that fills the prompt's pages."""
+        one = Cache.__new__(Cache)
+        one.delta, one.scan = torch.zeros_like(self.delta[:1]), torch.zeros_like(self.scan[:1])
+        one.table, one.k, one.v, one.length = self.prefix[None], self.k, self.v, 0
+        return one
+
+
+class NormedDecoder(HybridDecoder):
+    def __init__(self, device, seed=0, longest=512):
+        super().__init__(device, seed, longest)
+        gen = torch.Generator(device=device).manual_seed(seed + 1)
+        heads = DELTA_HEADS * DELTA_DIM
+        self.gate_in = (torch.randn(WIDTH, heads, generator=gen, device=device)
+                        / math.sqrt(WIDTH)).to(torch.bfloat16)
+        self.gate_weight = torch.ones(DELTA_DIM, device=device)
+        self.norms = [torch.ones(WIDTH, device=device) for _ in range(4)]
+
+    def delta(self, x, cache):
+        B, T, _ = x.shape
+        q, k, v = (x @ self.delta_in).view(B, T, 3, DELTA_HEADS, DELTA_DIM).unbind(2)
+        gates = (x @ self.delta_gate).float().view(B, T, 2, DELTA_HEADS)
+        g = nnf.logsigmoid(gates[:, :, 0] + 2.0).contiguous()
+        beta = torch.sigmoid(gates[:, :, 1]).contiguous()
+        q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
+        if T == 1:
+            o = gdr.recurrent_fwd(q, k, v, g, beta, cache.delta)
+        else:
+            o, _ = gdr.chunk_fwd(q, k, v, g, beta, cache.delta, final_state=cache.delta)
+        z = (x @ self.gate_in).view(B, T, DELTA_HEADS, DELTA_DIM)
+        o = gdr.gated_norm(o.view(z.shape), z, self.gate_weight)
+        return o.view(B, T, -1) @ self.delta_out
+
+    def attention(self, x, cache):
+        if not isinstance(cache, SharedCache):
+            return super().attention(x, cache)
+        B, T, _ = x.shape
+        qkv = (x @ self.attn_in).view(B, T, HQ + 2 * HK, DIM)
+        pos = (cache.length + torch.arange(T, device=x.device, dtype=torch.int32)).repeat(B, 1)
+        q = gdr.qk_norm_rope_append(qkv[:, :, :HQ], qkv[:, :, HQ:HQ + HK], qkv[:, :, HQ + HK:],
+                                    self.q_weight, self.k_weight, self.cos, self.sin, pos,
+                                    cache.k, cache.v, cache.whole)
+        table = cache.table.repeat_interleave(T, 0) if T > 1 else cache.table
+        o, _ = gdr.paged_prefix_attn(q.view(B * T, HQ, DIM), cache.k, cache.v, cache.prefix,
+                                     cache.shared, table, (pos + 1 - cache.shared).view(-1))
+        return o.view(B, T, -1) @ self.attn_out
+
+    def forward(self, tokens, cache):
+        residual = self.embed[tokens].float()        # kept in 32 bits
+        x, _ = gdr.residual_norm(residual, None, self.norms[0], out_dtype=torch.bfloat16)
+        for layer, weight in zip((self.delta, self.scan, self.attention), self.norms[1:]):
+            x, residual = gdr.residual_norm(residual, layer(x, cache), weight,
+                                            residual_out=residual)
+        cache.length += tokens.shape[1]
+        return x @ self.head
+
+    def generate_shared(self, prompt, tails, steps):
+        """Greedy, for a batch behind one prompt: prompt [P], tails [B, n] the rest of each
+        sequence; (tokens [B, steps], logits of every step [B, steps, VOCAB])."""
+        B, n = tails.shape
+        cache = SharedCache(len(prompt), B, len(prompt) % PAGE + n + steps, self.device)
+        if cache.shared:
+            once = cache.prompt()
+            self.forward(prompt[None, :cache.shared], once)
+            cache.delta.copy_(once.delta.expand_as(cache.delta))
+            cache.scan.copy_(once.scan.expand_as(cache.scan))
+        rest = torch.cat([prompt[cache.shared:].expand(B, -1), tails], 1)
+        logits = self.forward(rest, cache)[:, -1:]
+        tokens, seen = [], []
+        for i in range(steps):
+            seen.append(logits)
+            tokens.append(logits.argmax(-1))
+            if i + 1 < steps:
+                logits = self.forward(tokens[-1], cache)
+        return torch.cat(tokens, 1), torch.cat(seen, 1)
+
+
 # ------------------------------------------------------------------ training
+class GatedNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, gate, weight):
+        ctx.save_for_backward(x, gate, weight)
+        return gdr.gated_norm(x, gate, weight)
+
+    @staticmethod
+    def backward(ctx, d):
+        return gdr.gated_norm_bwd(d.contiguous(), *ctx.saved_tensors)
+
+
+class ResidualNorm(torch.autograd.Function):
+    """(out, residual + scale y) with a scale per channel."""
+
+    @staticmethod
+    def forward(ctx, residual, y, weight, scale):
+        out, residual = gdr.residual_norm(residual, y, weight, scale=scale)
+        ctx.save_for_backward(residual, y, weight, scale)
+        return out, residual
+
+    @staticmethod
+    def backward(ctx, d, d_residual):
+        residual, y, weight, scale = ctx.saved_tensors
+        dr, dy, _, dw, _, ds = gdr.residual_norm_bwd(d.contiguous(), d_residual.contiguous(),
+                                                     residual, y, weight, scale=scale)
+        return dr, dy, dw, ds
+
+
 class LinearScan(torch.autograd.Function):
     """h = linear_scan(x, g) with the input gated, from a zero state."""
 
@@ -194,5 +323,7 @@ if __name__ == "__main__":
     prompt = torch.randint(0, VOCAB, (3, 100), generator=torch.Generator().manual_seed(1)).to(dev)
     out, _ = model.generate(prompt, 16)
     print("generated:", out.tolist())
+    out, _ = NormedDecoder(dev).generate_shared(prompt[0], prompt[:, :7], 16)
+    print("behind one prompt:", out.tolist())
     losses = train(dev)
     print(f"training loss {losses[0]:.4f} -> {losses[-1]:.4f} in {len(losses)} steps")
