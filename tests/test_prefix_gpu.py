@@ -375,3 +375,23 @@ def test_waits_that_give_up(D, B, HQ, HK, P, page):
             assert torch.isnan(got[0]).any() and torch.isnan(got[1]).any()
     for a, b in zip(call(s), want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype,D", [(BF, 128), (F32, 64), (BF, 40)])
+def test_prompt_in_an_empty_cache(dtype, D):
+    """A cache without pages has no page that a prompt could name: NaN, and nothing is read."""
+    s = make(3, 4, 2, D, 40, [0, 0, 0], dtype=dtype, seed=20)
+    s["kc"], s["vc"] = s["kc"][:0], s["vc"][:0]
+    o, lse = call(s)
+    assert torch.isnan(o).all() and torch.isnan(lse).all()
+
+
+@pytest.mark.parametrize("page", [16, 64])
+def test_broadcast_heads(page):
+    """Key heads that are one head (a stride of 0 between them)."""
+    s = make(9, 8, 1, 128, 300, [5, 0, 30, 64, 1, 2, 3, 4, 5], page=page, seed=21)
+    want = call(s)
+    s["kc"], s["vc"] = (t.expand(-1, -1, 4, -1) for t in (s["kc"], s["vc"]))
+    ref, _, size = reference(s)
+    o, _ = check(s)
+    assert ((o.double() - want[0].double()).abs() <= 2 * (2.0 ** -8 * ref.abs() + 1e-4 * size)).all()
