@@ -66,6 +66,37 @@ __device__ __forceinline__ void sum_groups(float* acc, float* s, int tid) {
   }
 }
 
+// A block's part of a weight gradient: its group's sums, or those of its groups added in order,
+// element by element (groups of SHIFT have phases of their own).
+constexpr int kBlockSum = 2048;                  // groups x elements of a block at most
+template <class S>
+__device__ __forceinline__ void block_part(const float* acc, float* s, float* to, const Walk& w,
+                                           int phase, int D) {
+  if constexpr (S::LANES == 0) {
+#pragma unroll
+    for (int c = 0; c < S::NV; ++c) {
+      const int i = (c * w.threads + w.tid) * S::V - phase;
+      if (i < D) store_part<S>(to, i, D, acc + c * S::V);
+    }
+  } else {
+    const int groups = blockDim.x / S::LANES;
+    __syncthreads();                             // the last sum's readers are done
+#pragma unroll
+    for (int c = 0; c < S::NV; ++c)
+#pragma unroll
+      for (int e = 0; e < S::V; ++e) {
+        const int i = (c * w.threads + w.tid) * S::V - phase + e;
+        if (i >= 0 && i < D) s[threadIdx.x / S::LANES * D + i] = acc[c * S::V + e];
+      }
+    __syncthreads();
+    for (int i = threadIdx.x; i < D; i += blockDim.x) {
+      float v = 0.f;
+      for (int g = 0; g < groups; ++g) v += s[g * D + i];
+      to[i] = v;
+    }
+  }
+}
+
 // Rows of at most 512 channels: a group of LANES lanes per row, NV runs of 8 channels a lane, UN
 // rows at a time (the group's head in UN tokens), the next ones' loads under way meanwhile. What
 // bounds the larger calls beside HBM is the number of instructions per row, so addresses step
@@ -254,7 +285,7 @@ __global__ void __launch_bounds__(kMaxThreads) gated_kernel(GatedArgs a) {
   constexpr int V = S::V, NV = S::NV, N = S::N, TENSORS = BWD ? 3 : 2;
   extern __shared__ __align__(16) char places[];
   __shared__ Red red;
-  __shared__ float sums[BWD && S::LANES ? 8 * 32 * N : 1];      // at most 8 warps in such a block
+  __shared__ float sums[BWD && S::LANES ? kBlockSum : 1];
   const Walk w = walk_of<S::LANES>(a.tokens, a.H, a.groups);
   const int phase = S::SHIFT ? (int)((((long long)w.tok * a.H + w.head) * a.D) & 7) : 0;
   const Ahead ahead(places, a.pieces, a.stages);
@@ -367,17 +398,19 @@ __global__ void __launch_bounds__(kMaxThreads) gated_kernel(GatedArgs a) {
       }
     }
   }
-  if (!BWD || !a.part) return;
-  // A row of parts per block; per group where its head has weights of its own, or its rows a
-  // phase.
-  const bool each = a.per_head || S::SHIFT;
-  if (!each) sum_groups<S>(acc, sums, w.tid);
-  if (each ? !w.on : (S::LANES && threadIdx.x >= S::LANES)) return;
-  float* to = a.part + (each ? ((size_t)w.tok * a.H + w.head) * a.D : (size_t)blockIdx.x * a.D);
+  if constexpr (BWD) {
+    if (!a.part) return;
+    // A row of parts per block; per group where its head has weights of its own.
+    if (!a.per_head) {
+      block_part<S>(acc, sums, a.part + (size_t)blockIdx.x * a.D, w, phase, a.D);
+    } else if (w.on) {
+      float* to = a.part + ((size_t)w.tok * a.H + w.head) * a.D;
 #pragma unroll
-  for (int c = 0; c < NV; ++c) {
-    const int i = (c * w.threads + w.tid) * V - phase;
-    if (i < a.D) store_part<S>(to, i, a.D, acc + c * V);
+      for (int c = 0; c < NV; ++c) {
+        const int i = (c * w.threads + w.tid) * V - phase;
+        if (i < a.D) store_part<S>(to, i, a.D, acc + c * V);
+      }
+    }
   }
 }
 
@@ -391,7 +424,7 @@ struct ResArgs {
   int B, T, D, tokens, kind, post, want_p, want_s;
   int r_bf16, y_bf16, out_bf16;  // y_bf16: of y and z; out_bf16: of out and d
   int has_y, has_z, has_dr;
-  int pieces, stages;
+  int pieces, stages, groups;
   int flat;                      // the views' tokens are one stride apart, over batch rows too
   float eps, inv_d, s;
 };
@@ -406,18 +439,19 @@ struct Types {
   __device__ static constexpr int out(const ResArgs& a) { return TY == kAnyTypes ? a.out_bf16 : TY != kAllF32; }
 };
 
+// (With 16 elements a thread, 64 registers: an SM holds the kFwdPerSm threads that the plan counts on.)
 template <class S, int TY>
-__global__ void __launch_bounds__(kMaxThreads) residual_fwd_kernel(ResArgs a) {
+__global__ void __launch_bounds__(kMaxThreads, S::N <= 16 ? 2 : 1) residual_fwd_kernel(ResArgs a) {
   constexpr int V = S::V, NV = S::NV, N = S::N;
   extern __shared__ __align__(16) char places[];
   __shared__ Red red;
-  const Walk w = walk_of<0>(a.tokens, 1, gridDim.x);
+  const Walk w = walk_of<S::LANES>(a.tokens, 1, a.groups);
   const int phase = S::SHIFT ? (int)(((long long)w.tok * a.D) & 7) : 0;
   const Ahead ahead(places, a.pieces, a.stages);
   Row<S, false> rr;                              // may be the result's own memory
   Row<S, S::NV <= 4> ry, rz;
   const int r_bf16 = Types<TY>::r(a), y_bf16 = Types<TY>::y(a), out_bf16 = Types<TY>::out(a);
-  auto has = [&](int it) { return w.tok + it * w.step < a.tokens; };
+  auto has = [&](int it) { return (S::LANES == 0 || w.on) && w.tok + it * w.step < a.tokens; };
   auto locate = [&](int it) {
     const int tok = w.tok + it * w.step, rp = NV * (r_bf16 ? 1 : 2), yp = NV * (y_bf16 ? 1 : 2);
     rr.set(a.r.p, a.r.at(tok, a.T, a.flat, 0), r_bf16, 0);
@@ -449,7 +483,8 @@ __global__ void __launch_bounds__(kMaxThreads) residual_fwd_kernel(ResArgs a) {
     rr.advance(), ry.advance(), rz.advance();
     fetch(it + a.stages - 1, stage == 0 ? a.stages - 1 : stage - 1);
     if constexpr (S::kAhead) ahead.wait();
-    if (!has(it)) break;                         // the whole block
+    const bool on = S::LANES == 0 || has(it);
+    if (S::LANES == 0 && !has(it)) break;        // the whole block
     if (!(S::kAhead || S::kRegs)) locate(it);
     const uint32_t at = ahead.of(stage);
     const size_t dense = (size_t)(w.tok + it * w.step) * a.D;
@@ -459,12 +494,12 @@ __global__ void __launch_bounds__(kMaxThreads) residual_fwd_kernel(ResArgs a) {
 #pragma unroll
       for (int c = 0; c < NV; ++c) {
         const int i = (c * w.threads + w.tid) * V - phase;
-        if (i >= a.D) continue;
+        if (!on || i >= a.D) continue;
         float y[V];
         ry.get(ahead, at, c, i, a.D, y);
         s[0] += dot_run<V>(y, y);
       }
-      row_sum<0, 1>(s, red, turn);
+      row_sum<S::LANES, 1>(s, red, turn);
       py = rsqrtf(fmaf(s[0], a.inv_d, a.eps));
     }
     float r[N];
@@ -472,7 +507,7 @@ __global__ void __launch_bounds__(kMaxThreads) residual_fwd_kernel(ResArgs a) {
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
       const int i = (c * w.threads + w.tid) * V - phase;
-      if (i >= a.D) continue;
+      if (!on || i >= a.D) continue;
       float* x = r + c * V;
       rr.get(ahead, at, c, i, a.D, x);
       if (a.has_y) {
@@ -499,12 +534,12 @@ __global__ void __launch_bounds__(kMaxThreads) residual_fwd_kernel(ResArgs a) {
       }
       s[0] += dot_run<V>(x, x);
     }
-    row_sum<0, 1>(s, red, turn);
+    row_sum<S::LANES, 1>(s, red, turn);
     const float rho = rsqrtf(fmaf(s[0], a.inv_d, a.eps));
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
       const int i = (c * w.threads + w.tid) * V - phase;
-      if (i >= a.D) continue;
+      if (!on || i >= a.D) continue;
       float o[V], k[V];
       scale_run<V>(o, r + c * V, rho);
       if (a.w) {
@@ -518,11 +553,11 @@ __global__ void __launch_bounds__(kMaxThreads) residual_fwd_kernel(ResArgs a) {
 
 // FULL: y goes through a norm, a gate or a scale per channel; without, dy = s g.
 template <class S, int TY, bool FULL>
-__global__ void __launch_bounds__(kMaxThreads) residual_bwd_kernel(ResArgs a) {
+__global__ void __launch_bounds__(kMaxThreads, S::N <= 16 && !FULL ? 2 : 1) residual_bwd_kernel(ResArgs a) {
   constexpr int V = S::V, NV = S::NV, N = S::N;
   extern __shared__ __align__(16) char places[];
   __shared__ Red red;
-  const Walk w = walk_of<0>(a.tokens, 1, gridDim.x);
+  const Walk w = walk_of<S::LANES>(a.tokens, 1, a.groups);
   const int phase = S::SHIFT ? (int)(((long long)w.tok * a.D) & 7) : 0;
   const Ahead ahead(places, a.pieces, a.stages);
   float acc[FULL ? 3 : 1][N];
@@ -532,7 +567,7 @@ __global__ void __launch_bounds__(kMaxThreads) residual_bwd_kernel(ResArgs a) {
     for (int j = 0; j < N; ++j) acc[k][j] = 0.f;
   Row<S, S::NV <= 4> rr, rd, rg, ry, rz;
   const int r_bf16 = Types<TY>::r(a), y_bf16 = Types<TY>::y(a), out_bf16 = Types<TY>::out(a);
-  auto has = [&](int it) { return w.tok + it * w.step < a.tokens; };
+  auto has = [&](int it) { return (S::LANES == 0 || w.on) && w.tok + it * w.step < a.tokens; };
   auto locate = [&](int it) {
     const int tok = w.tok + it * w.step;
     const int rp = NV * (r_bf16 ? 1 : 2), op = NV * (out_bf16 ? 1 : 2);
@@ -572,7 +607,8 @@ __global__ void __launch_bounds__(kMaxThreads) residual_bwd_kernel(ResArgs a) {
     rr.advance(), rd.advance(), rg.advance(), ry.advance(), rz.advance();
     fetch(it + a.stages - 1, stage == 0 ? a.stages - 1 : stage - 1);
     if constexpr (S::kAhead) ahead.wait();
-    if (!has(it)) break;                         // the whole block
+    const bool on = S::LANES == 0 || has(it);
+    if (S::LANES == 0 && !has(it)) break;        // the whole block
     if (!(S::kAhead || S::kRegs)) locate(it);
     const uint32_t at = ahead.of(stage);
     const size_t dense = (size_t)(w.tok + it * w.step) * a.D;
@@ -580,7 +616,7 @@ __global__ void __launch_bounds__(kMaxThreads) residual_bwd_kernel(ResArgs a) {
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
       const int i = (c * w.threads + w.tid) * V - phase;
-      if (i >= a.D) continue;
+      if (!on || i >= a.D) continue;
       float x[V], d[V], k[V];
       rr.get(ahead, at, c, i, a.D, x);
       rd.get(ahead, at, c, i, a.D, d);
@@ -595,14 +631,14 @@ __global__ void __launch_bounds__(kMaxThreads) residual_bwd_kernel(ResArgs a) {
         s[2] += dot_run<V>(x, x);
       }
     }
-    row_sum<0, FULL ? 3 : 2>(s, red, turn);
+    row_sum<S::LANES, FULL ? 3 : 2>(s, red, turn);
     const float rho = rsqrtf(fmaf(s[0], a.inv_d, a.eps)), m = s[1] * a.inv_d * rho;
     const float py = FULL && a.post ? rsqrtf(fmaf(s[2], a.inv_d, a.eps)) : 1.f;
     float dp[FULL ? N : 1], se[1] = {0.f};       // dp: dp wp behind a norm
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
       const int i = (c * w.threads + w.tid) * V - phase;
-      if (i >= a.D) continue;
+      if (!on || i >= a.D) continue;
       float g[V], x[V], d[V], k[V];
       rr.get(ahead, at, c, i, a.D, x);
       rd.get(ahead, at, c, i, a.D, d);
@@ -677,12 +713,12 @@ __global__ void __launch_bounds__(kMaxThreads) residual_bwd_kernel(ResArgs a) {
     }
     if constexpr (FULL) {
       if (a.post) {
-        row_sum<0, 1>(se, red, turn);
+        row_sum<S::LANES, 1>(se, red, turn);
         const float my = se[0] * a.inv_d;
 #pragma unroll
         for (int c = 0; c < NV; ++c) {
           const int i = (c * w.threads + w.tid) * V - phase;
-          if (i >= a.D) continue;
+          if (!on || i >= a.D) continue;
           float y[V];
           ry.get(ahead, at, c, i, a.D, y);
           fma_run<V>(y, y, -py * my, dp + c * V);
@@ -693,15 +729,11 @@ __global__ void __launch_bounds__(kMaxThreads) residual_bwd_kernel(ResArgs a) {
     }
   }
   if (!a.part) return;
+  __shared__ float sums[S::LANES ? kBlockSum : 1];
 #pragma unroll
   for (int k = 0; k < (FULL ? 3 : 1); ++k) {
     if ((k == 1 && !a.want_p) || (k == 2 && !a.want_s)) continue;
-    float* to = a.part + ((size_t)k * gridDim.x + blockIdx.x) * a.D;
-#pragma unroll
-    for (int c = 0; c < NV; ++c) {
-      const int i = (c * w.threads + w.tid) * V - phase;
-      if (i < a.D) store_part<S>(to, i, a.D, acc[k] + c * V);
-    }
+    block_part<S>(acc[k], sums, a.part + ((size_t)k * gridDim.x + blockIdx.x) * a.D, w, phase, a.D);
   }
 }
 
@@ -743,16 +775,16 @@ auto with_shape(const Plan& p, F f) {
 // How a call's rows lie: 16-byte accesses fit; fit but for a phase (Shape's SHIFT); or neither.
 enum Fit { kVec, kShift, kSingle };
 
-// pieces: 16-byte pieces per run of 8, over all tensors of a row. lanes_ok: whether a row may share
-// a warp. per_sm: threads an SM is to hold.
-Plan make_plan(int tokens, int H, int D, int pieces, Fit fit, bool lanes_ok, bool per_head,
+// pieces: 16-byte pieces per run of 8, over all tensors of a row. widest: elements of a row
+// that shares a warp, at most (256 where rows have a phase or no alignment). per_sm: threads an SM is to hold.
+Plan make_plan(int tokens, int H, int D, int pieces, Fit fit, int widest, bool per_head,
                int per_sm) {
   Plan p = {};
   p.shift = fit == kShift && D + 7 <= kMaxThreads * 16;
   const bool vec = fit == kVec || p.shift;
   p.v = vec ? 8 : 1;
   const int span = D + (p.shift ? 7 : 0);        // elements that a row's threads cover
-  p.lanes = !lanes_ok || span > (fit == kVec ? 512 : 256) ? 0
+  p.lanes = span > (fit == kVec ? widest : 256) ? 0
             : !vec || span > 128                          ? 32
             : span > 64                                   ? 16
                                                           : 8;
@@ -783,8 +815,7 @@ Plan make_plan(int tokens, int H, int D, int pieces, Fit fit, bool lanes_ok, boo
   }
   p.blocks = (int)blocks;
   p.groups = (int)groups;
-  // Groups of one block have phases of their own: a row of parts each.
-  p.rows = per_head ? p.groups / H : p.shift ? p.groups : p.blocks;
+  p.rows = per_head ? p.groups / H : p.blocks;
   p.pieces = pieces * p.nv;
   p.stages = !vec && p.nv <= 8 ? 2 : 1;          // 2: the next row in registers
   if (p.v == 8 && p.nv <= 2) {
@@ -840,7 +871,7 @@ constexpr int kFwdRowsPerSm = 768, kBwdRowsPerSm = 512;
 
 Plan gated_plan(const gdr_gated_dims* d, Fit fit, bool bwd) {
   const int in = d->in_dtype == GDR_BF16 ? 1 : 2, out = d->out_dtype == GDR_BF16 ? 1 : 2;
-  return make_plan(d->B * d->T, d->H, d->D, 2 * in + (bwd ? out : 0), fit, true,
+  return make_plan(d->B * d->T, d->H, d->D, 2 * in + (bwd ? out : 0), fit, 512,
                    d->weight_per_head != 0,
                    fit == kVec && d->D <= 512 ? (bwd ? kBwdRowsPerSm : kFwdRowsPerSm)
                                       : (bwd ? kBwdPerSm : kFwdPerSm));
@@ -917,7 +948,7 @@ gdr_status check(const gdr_residual_dims* d) {
 
 // pieces: of all tensors of a row (see make_plan).
 Plan residual_plan(const gdr_residual_dims* d, Fit fit, int pieces, int per_sm) {
-  return make_plan(d->B * d->T, 1, d->D, pieces, fit, false, false, per_sm);
+  return make_plan(d->B * d->T, 1, d->D, pieces, fit, 256, false, per_sm);
 }
 
 gdr_status residual_args(ResArgs& a, const gdr_residual_dims* d, const void* r, const void* y,
@@ -954,7 +985,7 @@ gdr_status residual_args(ResArgs& a, const gdr_residual_dims* d, const void* r, 
 // f(the call's types) for the rows that go through shared memory; the others look at run time.
 template <class S, typename F>
 auto with_types(const ResArgs& a, F f) {
-  if constexpr (S::kAhead) {
+  if constexpr (S::kAhead && S::LANES == 0) {
     const int y = a.has_y || a.o_dy ? a.y_bf16 : a.out_bf16; // neither: any type of it
     if (y == a.out_bf16 && a.r_bf16 && y) return f(std::integral_constant<int, kAllBf16>());
     if (y == a.out_bf16 && !a.r_bf16)
@@ -1061,8 +1092,9 @@ gdr_status gdr_residual_norm(const void* residual, const void* y, const void* ga
   const Plan p = residual_plan(dims, fit, re + a.has_y * ye + a.has_z * ye, kFwdPerSm);
   a.pieces = p.pieces;
   a.stages = p.stages;
+  a.groups = p.groups;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return with_block(p, [&](auto shape) {
+  return with_shape(p, [&](auto shape) {
     using S = decltype(shape);
     return with_types<S>(a, [&](auto types) {
       constexpr int TY = decltype(types)::value;
@@ -1138,13 +1170,15 @@ gdr_status gdr_residual_norm_bwd(const void* d_out, const void* d_residual_out,
   a.o_dz = d_gate;
   a.pieces = p.pieces;
   a.stages = p.stages;
-  const gdr_status run = with_block(p, [&](auto shape) {
+  a.groups = p.groups;
+  const gdr_status run = with_shape(p, [&](auto shape) {
     using S = decltype(shape);
     auto go = [&](auto* fn, auto* tag) {
       if (p.smem > kPlainSmem && !allow_smem<std::remove_pointer_t<decltype(tag)>>(fn, kSmemPerSm))
         return GDR_ERR_CUDA;
       // Blocks of a call that fills the device do not come early: their shared memory would be
-      // taken from the kernel before (training step of 2 x 8192 x 4096: 231 us so, 220 us not).
+      // taken from the kernel before (training step of 4096 x 1536 with norm, gate and scale: 74.9 us
+      // so, 70.7 not).
       return p.blocks < kSms * 2 ? launch_behind_smem(fn, dim3(p.blocks), p.threads, p.smem, s, a)
                                  : launch_kernel(fn, dim3(p.blocks), p.threads, p.smem, s, a);
     };

@@ -504,3 +504,15 @@ def test_odd_rows_of_views_with_even_steps():
         gated_check(x, z, w, d)
         residual_check(x[:, :, 0], z[:, :, 0], w[0].contiguous(), d=d[:, :, 0].contiguous(),
                        dr=d[:, :, 1].contiguous())
+
+
+@pytest.mark.parametrize("D", [5, 8, 57, 58, 64, 72, 100, 128, 200, 249, 250, 256, 264])
+@pytest.mark.parametrize("rt,yt", [(F32, BF), (F32, F32)])
+def test_residual_short_rows(D, rt, yt):
+    """Several rows per warp: more of them than groups, and too few for one block."""
+    for T in (3, 20011 if D < 100 else 9001):
+        r, y, z, d, dr, w, wp, s = residual_inputs(1, T, D, rt, yt, seed=15)
+        residual_check(r, y, w, z, wp, s, d, dr, "silu", True)
+        residual_check(r, y, w, d=d, dr=dr, s=0.5)
+    wide = torch.cat([r, r], -1)                 # rows that are not aligned at all
+    residual_check(wide[..., 1:D + 1], y, w, d=d, dr=dr)
