@@ -220,10 +220,6 @@ __global__ void __launch_bounds__(Config<D, TMA>::THREADS, 1)
   asm volatile("griddepcontrol.launch_dependents;");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t q_at = smem_u32(base), ring = q_at + U * F::QTILE;
-  if (TMA && threadIdx.x == 32 * F::SOFT) {
-    asm volatile("prefetch.tensormap [%0];" ::"l"(&k_map) : "memory");
-    asm volatile("prefetch.tensormap [%0];" ::"l"(&v_map) : "memory");
-  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < ST; ++i) {
       mbar_init(&bars.kv_full[i], F::LOAD);
