@@ -758,7 +758,8 @@ auto with_block(const Plan& p, F f) {
   if (p.v == 8) return p.nv == 2 ? f(Shape<0, 8, 2>()) : f(Shape<0, 8, 4>());
   return p.nv == 4 ? f(Shape<0, 1, 4>()) : p.nv == 16 ? f(Shape<0, 1, 16>()) : f(Shape<0, 1, 32>());
 }
-template <typename F>
+// TWO: whether rows of more than 256 elements share a warp.
+template <bool TWO, typename F>
 auto with_shape(const Plan& p, F f) {
   if (p.lanes == 0) return with_block(p, f);
   if (p.shift)
@@ -766,10 +767,11 @@ auto with_shape(const Plan& p, F f) {
            : p.lanes == 16 ? f(Shape<16, 8, 1, true>())
                            : f(Shape<32, 8, 1, true>());
   if (p.v == 1) return f(Shape<32, 1, 8>());
+  if constexpr (TWO)
+    if (p.nv == 2) return f(Shape<32, 8, 2>());
   return p.lanes == 8    ? f(Shape<8, 8, 1>())
          : p.lanes == 16 ? f(Shape<16, 8, 1>())
-         : p.nv == 1     ? f(Shape<32, 8, 1>())
-                         : f(Shape<32, 8, 2>());
+                         : f(Shape<32, 8, 1>());
 }
 
 // How a call's rows lie: 16-byte accesses fit; fit but for a phase (Shape's SHIFT); or neither.
@@ -859,7 +861,8 @@ gdr_status check(const gdr_gated_dims* d) {
   for (int64_t s : {d->x_stride_b, d->x_stride_t, d->x_stride_h, d->gate_stride_b,
                     d->gate_stride_t, d->gate_stride_h})
     if (s < 0) return GDR_ERR_INVALID_ARG;
-  if (d->D > kWidest || (long long)d->B * d->T > (1LL << 30) || d->H > (1 << 20))
+  if (d->D > kWidest || (long long)d->B * d->T > (1LL << 30) || d->H > (1 << 20) ||
+      (long long)d->H * d->D > (1LL << 30))
     return GDR_ERR_UNSUPPORTED;
   return GDR_OK;
 }
@@ -892,6 +895,7 @@ gdr_status gated_args(GatedArgs& a, const gdr_gated_dims* d, const void* x, cons
   const int64_t b = d->B > 1, t = d->T > 1, h = d->H > 1;
   a.x = {x, b * d->x_stride_b, t * d->x_stride_t, h * d->x_stride_h};
   a.z = {gate, b * d->gate_stride_b, t * d->gate_stride_t, h * d->gate_stride_h};
+  if (a.T == 1) a.x.t = a.x.b, a.z.t = a.z.b;      // tokens are batch rows
   a.flat = (a.B == 1 || (a.x.b == a.T * a.x.t && a.z.b == a.T * a.z.t)) ? 1 : 0;
   a.w = w;
   a.per_head = d->weight_per_head != 0;
@@ -925,7 +929,7 @@ gdr_status launch_gated(GatedArgs& a, const Plan& p, cudaStream_t s) {
              : p.nv == 1     ? go(Shape<32, 8, 1>())
                              : go(Shape<32, 8, 2>());
     });
-  return with_shape(p, [&](auto shape) {
+  return with_shape<true>(p, [&](auto shape) {
     using S = decltype(shape);
     struct Tag;
     if (p.smem > kPlainSmem && !allow_smem<Tag>(gated_kernel<S, BWD>, kSmemPerSm))
@@ -974,6 +978,7 @@ gdr_status residual_args(ResArgs& a, const gdr_residual_dims* d, const void* r, 
   a.eps = d->eps;
   a.inv_d = 1.f / d->D;
   a.s = d->scale;
+  if (a.T == 1) a.r.t = a.r.b, a.y.t = a.y.b, a.z.t = a.z.b;   // tokens are batch rows
   a.flat = 1;
   for (const View* v : {&a.r, &a.y, &a.z})
     if (v->p && a.B > 1 && v->b != a.T * v->t) a.flat = 0;
@@ -1094,7 +1099,7 @@ gdr_status gdr_residual_norm(const void* residual, const void* y, const void* ga
   a.stages = p.stages;
   a.groups = p.groups;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return with_shape(p, [&](auto shape) {
+  return with_shape<false>(p, [&](auto shape) {
     using S = decltype(shape);
     return with_types<S>(a, [&](auto types) {
       constexpr int TY = decltype(types)::value;
@@ -1171,7 +1176,7 @@ gdr_status gdr_residual_norm_bwd(const void* d_out, const void* d_residual_out,
   a.pieces = p.pieces;
   a.stages = p.stages;
   a.groups = p.groups;
-  const gdr_status run = with_shape(p, [&](auto shape) {
+  const gdr_status run = with_shape<false>(p, [&](auto shape) {
     using S = decltype(shape);
     auto go = [&](auto* fn, auto* tag) {
       if (p.smem > kPlainSmem && !allow_smem<std::remove_pointer_t<decltype(tag)>>(fn, kSmemPerSm))

@@ -590,7 +590,7 @@ size_t gdr_paged_prefix_attn_workspace_size(const gdr_attn_dims* dims, const gdr
  *   weight    (device) fp32 [D], [H, D] with weight_per_head, or NULL (ones)
  *   y         (device) [B, T, H, D] out_dtype, dense
  *
- * D <= 16384, B T <= 2^30.
+ * D <= 16384, H D <= 2^30, B T <= 2^30.
  */
 typedef struct {
   int B, T, H, D;

@@ -516,3 +516,25 @@ def test_residual_short_rows(D, rt, yt):
         residual_check(r, y, w, d=d, dr=dr, s=0.5)
     wide = torch.cat([r, r], -1)                 # rows that are not aligned at all
     residual_check(wide[..., 1:D + 1], y, w, d=d, dr=dr)
+
+
+@pytest.mark.parametrize("dtype,out", [(BF, F32), (F32, BF)])
+@pytest.mark.parametrize("D", [24, 100, 200, 333, 400])
+def test_gated_other_output_type_of_short_rows(D, dtype, out):
+    x, z, w, d = gated_inputs(2, 300, 3, D, dtype=dtype, seed=16)
+    y = gdr.gated_norm(x, z, w, out_dtype=out)
+    got = (y, *gdr.gated_norm_bwd(d.to(out), x, z, w))
+    for g, r, s in zip(got, *gated_ref(x, z, w, d.to(out), "silu", False)):
+        check(g, r, s)
+
+
+def test_single_tokens_of_a_batch():
+    """T = 1 with batch rows any stride apart, and with one row for all of them."""
+    gen, B, H, D = gen_of(17), 300, 2, 72
+    for dtype in (BF, F32):
+        x = rnd(gen, B, 5, H, D, dtype=dtype)[:, 2:3]
+        z = rnd(gen, 1, 1, H, D, dtype=dtype).expand(B, 1, H, D)
+        w, d = rnd(gen, D), rnd(gen, B, 1, H, D, dtype=dtype)
+        gated_check(x, z, w, d)
+        residual_check(x[:, :, 0], z[:, :, 1], w, d=d[:, :, 0].contiguous(),
+                       dr=d[:, :, 1].contiguous())

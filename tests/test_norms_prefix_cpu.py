@@ -46,7 +46,7 @@ def gated_bwd(mod, d, dy=A, x=A, z=A, w=A, dx=A, dz=A, dw=A, ws=A, n=1 << 40):
     (dict(activation=-1), INV), (dict(eps=0.0), INV), (dict(eps=-1.0), INV),
     (dict(eps=math.nan), INV), (dict(eps=math.inf), INV), (dict(x_stride_t=-1), INV),
     (dict(gate_stride_h=-1), INV), (dict(D=16385), UNS), (dict(B=1 << 16, T=1 << 16), UNS),
-    (dict(H=1 << 21), UNS)])
+    (dict(H=1 << 21), UNS), (dict(H=1 << 20, D=2048), UNS)])
 def test_gated_sizes(layers, kw, want):
     d = gated_dims(layers, **kw)
     assert gated(layers, d) == want and gated_bwd(layers, d) == want

@@ -395,3 +395,26 @@ def test_broadcast_heads(page):
     ref, _, size = reference(s)
     o, _ = check(s)
     assert ((o.double() - want[0].double()).abs() <= 2 * (2.0 ** -8 * ref.abs() + 1e-4 * size)).all()
+
+
+def test_two_calls_at_once():
+    """Calls on two streams that run side by side, each with its own inputs and scratch."""
+    cases = [make(64, 16, 4, 128, 4000, [(7 * b) % 90 for b in range(64)], page=64, seed=22),
+             make(9, 8, 2, 128, 6000, [(5 * b) % 40 for b in range(9)], page=17, seed=23)]
+    want = [call(s) for s in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        got = []
+        for s, stream in zip(cases, streams):
+            with torch.cuda.stream(stream):
+                x = s["q"].unsqueeze(1)
+                y = gdr.gated_norm(x, x)
+                got.append((call(s), y, gdr.residual_norm(y.flatten(2), x.flatten(2))[0]))
+        torch.cuda.synchronize()
+        for s, w, (g, y, r) in zip(cases, want, got):
+            assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
+            x = s["q"].unsqueeze(1)
+            again = gdr.gated_norm(x, x)
+            assert torch.equal(y, again)
+            assert torch.equal(r, gdr.residual_norm(again.flatten(2), x.flatten(2))[0])
