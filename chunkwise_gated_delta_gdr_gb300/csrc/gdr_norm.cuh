@@ -1,6 +1,6 @@
-// gdr_norm.cuh -- what the norm kernels around a layer share: rows of a norm held in the
-// registers of a group of lanes or of a block, their copies ahead of time, sums over a row,
-// gate activations, and the column sums of the weights' gradients.
+// gdr_norm.cuh -- what gdr_gated.cu and gdr_residual.cu share: rows of a norm held by a group of
+// lanes or by a block, their copies ahead of time, sums over a row, gate activations, the weights'
+// gradients, and the plan of a launch.
 #pragma once
 
 #include "gdr_ops.cuh"
@@ -18,6 +18,8 @@ __device__ __forceinline__ void begin_behind() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+constexpr int kMaxThreads = 512;
+
 // Who holds a row, and how. LANES > 0: that many lanes of a warp (8, 16 or 32), several rows
 // per warp. LANES == 0: a whole block, whose size follows the row's. A thread holds NV runs of
 // V consecutive elements; run c of thread i starts at element (c threads + i) V. V is 8 where
@@ -31,6 +33,8 @@ template <int LANES_, int V_, int NV_, bool SHIFT_ = false>
 struct Shape {
   static constexpr int LANES = LANES_, V = V_, NV = NV_, N = V_ * NV_;
   static constexpr bool SHIFT = SHIFT_;
+  // Elements that the groups of a block of 256 threads hold.
+  static constexpr int kSums = LANES_ ? 256 * N : 1;
   // Copies ahead of time go through shared memory, 16 bytes at a time. Rows past 8192 elements
   // (NV beyond 2 runs of 8) are loaded when they are needed, and so are long ones element by element.
   static constexpr bool kAhead = V_ == 8 && NV_ <= 2;
@@ -404,6 +408,156 @@ __global__ void __launch_bounds__(kSumCols * kSumRows) column_sum_kernel(const f
   }
   if (r0 == 0 && c < cols) out[c] = s[0][x];
 }
+
+// A block's part of a weight gradient: its group's sums, or those of its groups added in order,
+// element by element (groups of SHIFT have phases of their own); s: S::kSums floats.
+template <class S>
+__device__ __forceinline__ void block_part(const float* acc, float* s, float* to, const Walk& w,
+                                           int phase, int D) {
+  if constexpr (S::LANES == 0) {
+#pragma unroll
+    for (int c = 0; c < S::NV; ++c) {
+      const int i = (c * w.threads + w.tid) * S::V - phase;
+      if (i < D) store_part<S>(to, i, D, acc + c * S::V);
+    }
+  } else {
+    const int groups = blockDim.x / S::LANES;
+    __syncthreads();                             // the last sum's readers are done
+#pragma unroll
+    for (int c = 0; c < S::NV; ++c)
+#pragma unroll
+      for (int e = 0; e < S::V; ++e) {
+        const int i = (c * w.threads + w.tid) * S::V - phase + e;
+        if (i >= 0 && i < D) s[threadIdx.x / S::LANES * D + i] = acc[c * S::V + e];
+      }
+    __syncthreads();
+    for (int i = threadIdx.x; i < D; i += blockDim.x) {
+      float v = 0.f;
+      for (int g = 0; g < groups; ++g) v += s[g * D + i];
+      to[i] = v;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ host
+constexpr int kSms = 152;
+constexpr int kWidest = 16384;                   // elements of a row at most
+constexpr int kSmemPerSm = 200 * 1024;           // of copies ahead, an SM and a block at most
+constexpr int kPlainSmem = 24 * 1024;            // fits beside the static part without being asked for
+
+// What a call's kernel looks like: threads of a block, groups and blocks, copies ahead.
+struct Plan {
+  int lanes, v, nv, threads, groups, blocks, rows;   // rows: of the parts, per weight
+  bool shift;
+  int pieces, stages, smem;
+};
+
+// f(Shape) for a plan.
+template <typename F>
+auto with_block(const Plan& p, F f) {
+  if (p.shift) return f(Shape<0, 8, 2, true>());
+  if (p.v == 8) return p.nv == 2 ? f(Shape<0, 8, 2>()) : f(Shape<0, 8, 4>());
+  return p.nv == 4 ? f(Shape<0, 1, 4>()) : p.nv == 16 ? f(Shape<0, 1, 16>()) : f(Shape<0, 1, 32>());
+}
+// TWO: whether rows of more than 256 elements share a warp.
+template <bool TWO, typename F>
+auto with_shape(const Plan& p, F f) {
+  if (p.lanes == 0) return with_block(p, f);
+  if (p.shift)
+    return p.lanes == 8    ? f(Shape<8, 8, 1, true>())
+           : p.lanes == 16 ? f(Shape<16, 8, 1, true>())
+                           : f(Shape<32, 8, 1, true>());
+  if (p.v == 1) return f(Shape<32, 1, 8>());
+  if constexpr (TWO)
+    if (p.nv == 2) return f(Shape<32, 8, 2>());
+  return p.lanes == 8    ? f(Shape<8, 8, 1>())
+         : p.lanes == 16 ? f(Shape<16, 8, 1>())
+                         : f(Shape<32, 8, 1>());
+}
+
+// How a call's rows lie: 16-byte accesses fit; fit but for a phase (Shape's SHIFT); or neither.
+enum Fit { kVec, kShift, kSingle };
+
+// pieces: 16-byte pieces per run of 8, over all tensors of a row. widest: elements of a row
+// that shares a warp, at most (256 where rows have a phase or no alignment). per_sm: threads an SM is to hold.
+Plan make_plan(int tokens, int H, int D, int pieces, Fit fit, int widest, bool per_head,
+               int per_sm) {
+  Plan p = {};
+  p.shift = fit == kShift && D + 7 <= kMaxThreads * 16;
+  const bool vec = fit == kVec || p.shift;
+  p.v = vec ? 8 : 1;
+  const int span = D + (p.shift ? 7 : 0);        // elements that a row's threads cover
+  p.lanes = span > (fit == kVec ? widest : 256) ? 0
+            : !vec || span > 128                          ? 32
+            : span > 64                                   ? 16
+                                                          : 8;
+  int per_block = 1;                             // groups of a block
+  if (p.lanes) {
+    p.nv = !vec ? 8 : span > 256 ? 2 : 1;
+    p.threads = 256;
+    per_block = p.threads / p.lanes;
+  } else {
+    // Elements of a thread: 16, 32 in the widest rows, 4 in short ones element by element (more
+    // threads then have more loads under way).
+    p.nv = vec ? (D <= kMaxThreads * 16 ? 2 : 4)
+               : D <= kMaxThreads * 4 ? 4 : D <= kMaxThreads * 16 ? 16 : 32;
+    const int n = p.nv * p.v;
+    p.threads = ((span + n - 1) / n + 31) / 32 * 32;
+  }
+  const long long rows = (long long)tokens * H;
+  long long blocks = (rows + per_block - 1) / per_block;
+  const long long most = (long long)kSms * (per_sm / p.threads > 1 ? per_sm / p.threads : 1);
+  if (blocks > most) blocks = most;
+  const long long least = (H + per_block - 1) / per_block;     // a group per head
+  if (blocks < least) blocks = least;
+  long long groups = blocks * per_block / H * H;
+  if (p.shift && groups < rows) {                // steps of 8 tokens, for one phase per group
+    const long long unit = 8LL * H;
+    groups = groups < unit ? unit : groups / unit * unit;
+    blocks = (groups + per_block - 1) / per_block;
+  }
+  p.blocks = (int)blocks;
+  p.groups = (int)groups;
+  p.rows = per_head ? p.groups / H : p.blocks;
+  p.pieces = pieces * p.nv;
+  p.stages = !vec && p.nv <= 8 ? 2 : 1;          // 2: the next row in registers
+  if (p.v == 8 && p.nv <= 2) {
+    const int stage = p.pieces * p.threads * 16;
+    const int resident = per_sm / p.threads > 1 ? per_sm / p.threads : 1;
+    p.stages = 3;
+    while (p.stages > 1 && (long long)p.stages * stage * resident > kSmemPerSm) --p.stages;
+    p.smem = p.stages * stage;
+  }
+  return p;
+}
+
+// The fit of a view [B, T, H, D] (strides of dimensions of one element: 0).
+Fit fit_of(const void* p, int B, int T, int H, int D, int64_t b, int64_t t, int64_t h) {
+  if (!is_aligned(p, 16)) return kSingle;
+  const int64_t row = D, tok = row * H, batch = tok * T;
+  if ((B > 1 && (b - batch) % 8) || (T > 1 && (t - tok) % 8) || (H > 1 && (h - row) % 8))
+    return kSingle;
+  return D % 8 ? kShift : kVec;
+}
+Fit worse(Fit a, Fit b) { return a > b ? a : b; }
+
+// Column sums of the parts, behind the kernel that writes them.
+gdr_status sum_parts(const float* part, float* o0, float* o1, float* o2, int rows, int cols,
+                     cudaStream_t s) {
+  return launch_behind(column_sum_kernel, dim3((cols + kSumCols - 1) / kSumCols, o1 || o2 ? 3 : 1),
+                       kSumCols * kSumRows, s, part, o0, o1, o2, rows, cols);
+}
+gdr_status zero(float* p, size_t n, cudaStream_t s) {
+  return !p || n == 0 ? GDR_OK : status_of(cudaMemsetAsync(p, 0, n * sizeof(float), s));
+}
+
+bool bad_eps(float e) { return !(isfinite(e) && e > 0.f); }
+bool bad_act(int k) { return k != GDR_ACT_NONE && k != GDR_ACT_SIGMOID && k != GDR_ACT_SILU; }
+
+// Threads that an SM is to hold: of the kernels above (kFullPerSm: the residual's backward with a
+// norm, gate or scale per channel, at most kBwdPerSm), and of gated_rows_kernel.
+constexpr int kFwdPerSm = 1024, kBwdPerSm = 1024, kFullPerSm = 512;
+constexpr int kFwdRowsPerSm = 768, kBwdRowsPerSm = 512;
 
 }  // namespace
 }  // namespace ops
