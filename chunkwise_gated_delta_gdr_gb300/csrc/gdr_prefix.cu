@@ -15,9 +15,9 @@
 // Measured on one GB300, bf16, D = 128, a call among others:
 //   128 sequences behind 65000 keys, 32 / 16 heads, 0 .. 1024 own keys: 271 us (own keys 98, their
 //     join 8, shared keys 145 with the tensor cores 70 % busy, join 10-20; the bytes alone 160)
-//   64 behind 8192, 32 / 4 heads, 0 .. 512 own keys: 42 us (16, 22 and 8-14, in part at once)
-//   4 behind 200, 16 / 16 heads: 12.3 us
-// fp32, 5 behind 2999, 6 / 3 heads, D = 64: 16.5 us.
+//   64 behind 8192, 32 / 4 heads, 0 .. 512 own keys: 40 us (16, 22 and 8-14, in part at once)
+//   4 behind 200, 16 / 16 heads: 10.8 us
+// fp32, 5 behind 2999, 6 / 3 heads, D = 64: 14.8 us.
 #include <type_traits>
 
 #include "gdr_prefix.cuh"
@@ -34,7 +34,7 @@ namespace {
 // NI = 1, 2 or 4 as there are rows. fp32 caches with 16-byte rows are copied asynchronously: the
 // next tile's K while this one's weights and P V are computed, its V while the next scores are.
 // 5 sequences behind 2999 keys, HK = 3, D = 64: a block has one tile, and the call is the chain
-// page - row - scores - sums - join (16.5 us; 20.4 with a page looked up per row, one row after
+// page - row - scores - sums - join (14.8 us; 4 more with a page looked up per row, one row after
 // the other). Long prompts are bound by the reads of q and k from shared memory.
 constexpr int RM = 64, KT = 64, NT = 256;
 template <int NJ>                                // channels in runs of 64: D <= 64 NJ
