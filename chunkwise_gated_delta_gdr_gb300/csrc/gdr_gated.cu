@@ -10,8 +10,9 @@
 // chain load - sum over the row - store of one row below. Measured on one GB300, bf16, a pass
 // among others (a plain copy: 6.70 TB/s):
 //   2 x 8192 x 32 heads of 128: 62.7 us, 6.4 TB/s; 64 decode tokens x 16 heads 2.5 us
-//   training step, 4096 x 12 heads of 128: 24.9 us (forward 9, backward 15, weights' sums 5 with
-//   cold caches); 2 x 4096 x 4 groups of 512, gate first, weights per group 54.9 us
+//   training step, 4096 x 12 heads of 128: 24.1 us (forward 9, backward 14, weights' sums 5 with
+//   cold caches); 2 x 4096 x 4 groups of 512, gate first, weights per group 50.9 us; whole rows,
+//   8192 x 1536 55 us, 4096 x 4096 69 us, 36288 rows of 173 58 us
 #include "gdr_norm.cuh"
 
 namespace gdr {
@@ -145,11 +146,19 @@ __global__ void __launch_bounds__(256, BWD ? 2 : 3) gated_rows_kernel(GatedArgs 
       pairs(raw[u][0], x);
       pairs(raw[u][1], z);
       if (BWD) pairs(raw[u][TENSORS - 1], d);
+      float zs[2 * N], gs[2 * N], as[2 * N], sl[2 * N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) put_pair(zs, 2 * i, z[i]);
+#pragma unroll
+      for (int c = 0; c < 2 * N; c += 8) {
+        gate_sigma<8>(gs + c, zs + c, a.kind);
+        gate_open<8>(as + c, gs + c, zs + c, a.kind);
+        if (BWD) gate_slope<8>(sl + c, gs + c, zs + c, a.kind);
+      }
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        float2 g, slope;
-        g.x = act(z[i].x, a.kind, slope.x);
-        g.y = act(z[i].y, a.kind, slope.y);
+        const float2 g = pair_at(as, 2 * i);
+        const float2 slope = BWD ? pair_at(sl, 2 * i) : g;
         const float2 v = FIRST ? mul2(x[i], g) : x[i];
         ss = fma2(v, v, ss);
         if (!BWD) {
@@ -235,14 +244,19 @@ __global__ void __launch_bounds__(256, BWD ? 2 : 3) gated_rows_kernel(GatedArgs 
 }
 
 // Any other row: wider ones, a block each, and those that do not allow 16-byte accesses.
-template <class S, bool BWD>
-__global__ void __launch_bounds__(kMaxThreads) gated_kernel(GatedArgs a) {
+// TY: the types of a call, where they are the usual ones.
+enum { kAnyTypes, kAllBf16, kAllF32 };
+template <class S, int TY, bool BWD>
+__global__ void __launch_bounds__(kMaxThreads, !BWD && S::N <= 16 && !S::SHIFT ? 2 : 1)
+    gated_kernel(GatedArgs a) {
   constexpr int V = S::V, NV = S::NV, N = S::N, TENSORS = BWD ? 3 : 2;
   extern __shared__ __align__(16) char places[];
   __shared__ Red red;
   __shared__ float sums[BWD ? S::kSums : 1];
   const Walk w = walk_of<S::LANES>(a.tokens, a.H, a.groups);
   const int phase = S::SHIFT ? (int)((((long long)w.tok * a.H + w.head) * a.D) & 7) : 0;
+  const int in_bf16 = TY == kAnyTypes ? a.in_bf16 : TY == kAllBf16;
+  const int out_bf16 = TY == kAnyTypes ? a.out_bf16 : TY == kAllBf16;
   const Ahead ahead(places, a.pieces, a.stages);
   const float* weight = a.w && a.per_head ? a.w + (size_t)w.head * a.D : a.w;
   float acc[N];
@@ -252,10 +266,10 @@ __global__ void __launch_bounds__(kMaxThreads) gated_kernel(GatedArgs a) {
   Row<S, S::NV <= 4> row[TENSORS];
   auto has = [&](int it) { return w.on && w.tok + it * w.step < a.tokens; };
   auto locate = [&](int it) {
-    const int tok = w.tok + it * w.step, per = NV * (a.in_bf16 ? 1 : 2);
-    row[0].set(a.x.p, a.x.at(tok, a.T, a.flat, w.head), a.in_bf16, 0);
-    row[1].set(a.z.p, a.z.at(tok, a.T, a.flat, w.head), a.in_bf16, per);
-    if (BWD) row[TENSORS - 1].set(a.d.p, a.d.at(tok, a.T, 1, w.head), a.out_bf16, 2 * per);
+    const int tok = w.tok + it * w.step, per = NV * (in_bf16 ? 1 : 2);
+    row[0].set(a.x.p, a.x.at(tok, a.T, a.flat, w.head), in_bf16, 0);
+    row[1].set(a.z.p, a.z.at(tok, a.T, a.flat, w.head), in_bf16, per);
+    if (BWD) row[TENSORS - 1].set(a.d.p, a.d.at(tok, a.T, 1, w.head), out_bf16, 2 * per);
   };
   auto fetch = [&](int it, int stage) {
     if constexpr (S::kAhead || S::kRegs) {
@@ -285,28 +299,30 @@ __global__ void __launch_bounds__(kMaxThreads) gated_kernel(GatedArgs a) {
     if (!(S::kAhead || S::kRegs) && on) locate(it);
     const uint32_t at = ahead.of(stage);
     const size_t dense = ((size_t)(w.tok + it * w.step) * a.H + w.head) * a.D;
-    float s[2] = {0.f, 0.f};
+    float s[2] = {0.f, 0.f}, g[N];               // g: the gates' sigmoids
     if (on)
 #pragma unroll
       for (int c = 0; c < NV; ++c) {
         const int i = (c * w.threads + w.tid) * V - phase;
         if (i >= a.D) continue;
-        float x[V], z[V], d[V], wt[V];
+        float x[V], z[V], t[V];
         row[0].get(ahead, at, c, i, a.D, x);
-        if (a.first || BWD) row[1].get(ahead, at, c, i, a.D, z);
-        if (BWD) {
-          row[TENSORS - 1].get(ahead, at, c, i, a.D, d);
-          if (weight) load_shared<S>(weight, i, a.D, wt);
+        if (a.first || BWD) {
+          row[1].get(ahead, at, c, i, a.D, z);
+          gate_sigma<V>(g + c * V, z, a.kind);
+          gate_open<V>(t, g + c * V, z, a.kind);
         }
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float g = a.first || BWD ? act(z[e], a.kind) : 1.f;
-          const float v = a.first ? x[e] * g : x[e];
-          s[0] = fmaf(v, v, s[0]);
-          if (BWD) {
-            const float dc = a.first ? d[e] : d[e] * g;
-            s[1] = fmaf(weight ? dc * wt[e] : dc, v, s[1]);
+        if (a.first) mul_run<V>(x, x, t);
+        s[0] += dot_run<V>(x, x);
+        if (BWD) {
+          float d[V];
+          row[TENSORS - 1].get(ahead, at, c, i, a.D, d);
+          if (!a.first) mul_run<V>(d, d, t);
+          if (weight) {
+            load_shared<S>(weight, i, a.D, t);
+            mul_run<V>(d, d, t);
           }
+          s[1] += dot_run<V>(d, x);
         }
       }
     row_sum<S::LANES, BWD ? 2 : 1>(s, red, turn);
@@ -316,40 +332,49 @@ __global__ void __launch_bounds__(kMaxThreads) gated_kernel(GatedArgs a) {
     for (int c = 0; c < NV; ++c) {
       const int i = (c * w.threads + w.tid) * V - phase;
       if (i >= a.D) continue;
-      float x[V], z[V], d[V], wt[V], o[V], oz[V];
+      float *gc = g + c * V, x[V], z[V], t[V], u[V], wt[V];
       row[0].get(ahead, at, c, i, a.D, x);
       row[1].get(ahead, at, c, i, a.D, z);
-      if (BWD) row[TENSORS - 1].get(ahead, at, c, i, a.D, d);
-      if (weight) {
-        load_shared<S>(weight, i, a.D, wt);
+      if (!BWD && !a.first) gate_sigma<V>(gc, z, a.kind);
+      gate_open<V>(t, gc, z, a.kind);            // a
+      if (weight) load_shared<S>(weight, i, a.D, wt);
+      if (a.first) {
+        mul_run<V>(u, x, t);
+        scale_run<V>(u, u, r);
       } else {
-#pragma unroll
-        for (int e = 0; e < V; ++e) wt[e] = 1.f;
+        scale_run<V>(u, x, r);
       }
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        float slope;
-        const float g = act(z[e], a.kind, slope);
-        const float u = (a.first ? x[e] * g : x[e]) * r;
-        if (!BWD) {
-          o[e] = a.first ? u * wt[e] : u * wt[e] * g;
-        } else if (a.first) {
-          const float dv = r * fmaf(-u, m, d[e] * wt[e]);
-          acc[c * V + e] = fmaf(d[e], u, acc[c * V + e]);
-          o[e] = dv * g;
-          oz[e] = dv * x[e] * slope;
+      if constexpr (!BWD) {
+        if (weight) mul_run<V>(u, u, wt);
+        if (!a.first) mul_run<V>(u, u, t);
+        store_row<S>(a.y, dense, i, a.D, out_bf16, u);
+      } else {
+        float d[V], q[V];
+        row[TENSORS - 1].get(ahead, at, c, i, a.D, d);
+        gate_slope<V>(z, gc, z, a.kind);         // a'
+        if (a.first) {
+          fma_run<V>(acc + c * V, d, u, acc + c * V);
+          if (weight) mul_run<V>(d, d, wt);
+          fma_run<V>(q, u, -m, d);
+          scale_run<V>(q, q, r);                 // dv
+          mul_run<V>(t, t, q);                   // dx
+          mul_run<V>(z, z, x);
+          mul_run<V>(z, z, q);                   // dz
+          store_row<S>(a.dx, dense, i, a.D, in_bf16, t);
         } else {
-          const float dg = d[e] * g;
-          acc[c * V + e] = fmaf(dg, u, acc[c * V + e]);
-          o[e] = r * fmaf(-u, m, dg * wt[e]);
-          oz[e] = d[e] * u * wt[e] * slope;
+          mul_run<V>(q, d, t);
+          fma_run<V>(acc + c * V, q, u, acc + c * V);
+          if (weight) {
+            mul_run<V>(q, q, wt);
+            mul_run<V>(d, d, wt);
+          }
+          fma_run<V>(q, u, -m, q);
+          scale_run<V>(q, q, r);                 // dx
+          mul_run<V>(z, z, u);
+          mul_run<V>(z, z, d);                   // dz
+          store_row<S>(a.dx, dense, i, a.D, in_bf16, q);
         }
-      }
-      if (BWD) {
-        store_row<S>(a.dx, dense, i, a.D, a.in_bf16, o);
-        store_row<S>(a.dz, dense, i, a.D, a.in_bf16, oz);
-      } else {
-        store_row<S>(a.y, dense, i, a.D, a.out_bf16, o);
+        store_row<S>(a.dz, dense, i, a.D, in_bf16, z);
       }
     }
   }
@@ -386,10 +411,12 @@ gdr_status check(const gdr_gated_dims* d) {
 
 Plan gated_plan(const gdr_gated_dims* d, Fit fit, bool bwd) {
   const int in = d->in_dtype == GDR_BF16 ? 1 : 2, out = d->out_dtype == GDR_BF16 ? 1 : 2;
+  const int per_sm = fit == kVec && d->D <= 512 ? (bwd ? kBwdRowsPerSm : kFwdRowsPerSm)
+                     : bwd                      ? kGatedBwdPerSm
+                     : fit == kShift            ? kGatedShiftPerSm
+                                                : kFwdPerSm;
   return make_plan(d->B * d->T, d->H, d->D, 2 * in + (bwd ? out : 0), fit, 512,
-                   d->weight_per_head != 0,
-                   fit == kVec && d->D <= 512 ? (bwd ? kBwdRowsPerSm : kFwdRowsPerSm)
-                                      : (bwd ? kBwdPerSm : kFwdPerSm));
+                   d->weight_per_head != 0, per_sm);
 }
 size_t gated_bytes(const gdr_gated_dims* d, const Plan& p) {
   const size_t cols = (size_t)d->D * (d->weight_per_head ? d->H : 1);
@@ -443,10 +470,18 @@ gdr_status launch_gated(GatedArgs& a, const Plan& p, cudaStream_t s) {
     });
   return with_shape<true>(p, [&](auto shape) {
     using S = decltype(shape);
-    struct Tag;
-    if (p.smem > kPlainSmem && !allow_smem<Tag>(gated_kernel<S, BWD>, kSmemPerSm))
-      return GDR_ERR_CUDA;
-    return launch_behind_smem(gated_kernel<S, BWD>, dim3(p.blocks), p.threads, p.smem, s, a);
+    auto go = [&](auto types) {
+      constexpr int TY = decltype(types)::value;
+      struct Tag;
+      if (p.smem > kPlainSmem && !allow_smem<Tag>(gated_kernel<S, TY, BWD>, kSmemPerSm))
+        return GDR_ERR_CUDA;
+      return launch_behind_smem(gated_kernel<S, TY, BWD>, dim3(p.blocks), p.threads, p.smem, s, a);
+    };
+    if constexpr (S::kAhead && (S::LANES == 0 || S::SHIFT))
+      if (a.in_bf16 == a.out_bf16)
+        return a.in_bf16 ? go(std::integral_constant<int, kAllBf16>())
+                         : go(std::integral_constant<int, kAllF32>());
+    return go(std::integral_constant<int, kAnyTypes>());
   });
 }
 

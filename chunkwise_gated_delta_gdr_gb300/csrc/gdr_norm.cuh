@@ -165,29 +165,43 @@ __device__ __forceinline__ float dot_run(const float* a, const float* b) {
   return s.x + s.y;
 }
 
-// act(z) and its derivative.
+// The gate a(z) = g zz and its slope g (zz (1 - g) + c): g = 1 / (1 + e^-z) or 1 without an
+// activation, zz = z or, for the sigmoid, 1, and c = 1, 0 likewise.
 enum Act { kNone = GDR_ACT_NONE, kSigmoid = GDR_ACT_SIGMOID, kSilu = GDR_ACT_SILU };
-// 1 / (1 + e^-z) by the approximate 2^x and reciprocal (2^-22 each, and the rounding of z log2(e),
-// half an ulp of it; 0 for z < -88).
+// By the approximate 2^x and reciprocal (2^-22 each, and the rounding of z log2(e), half an ulp
+// of it); 0 for z < -88.
 __device__ __forceinline__ float sigmoid(float z) {
   float e, g;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(g) : "f"(1.f + e));
   return g;
 }
-__device__ __forceinline__ float act(float z, int kind) {
-  if (kind == kNone) return z;
-  const float g = sigmoid(z);
-  return kind == kSigmoid ? g : z * g;
+template <int V>
+__device__ __forceinline__ void gate_sigma(float* g, const float* z, int kind) {
+#pragma unroll
+  for (int e = 0; e < V; ++e) g[e] = kind == kNone ? 1.f : sigmoid(z[e]);
 }
-__device__ __forceinline__ float act(float z, int kind, float& slope) {
-  if (kind == kNone) {
-    slope = 1.f;
-    return z;
+template <int V>
+__device__ __forceinline__ void gate_open(float* a, const float* g, const float* z, int kind) {
+  if (kind == kSigmoid) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) a[e] = g[e];
+  } else {
+    mul_run<V>(a, g, z);
   }
-  const float g = sigmoid(z), h = 1.f - g;       // slope may be z's own variable: z is a copy
-  slope = kind == kSigmoid ? g * h : fmaf(z * g, h, g);
-  return kind == kSigmoid ? g : z * g;
+}
+template <int V>                                 // s may be z
+__device__ __forceinline__ void gate_slope(float* s, const float* g, const float* z, int kind) {
+  over_run<V>(
+      [&](int i) {
+        const float2 gp = pair_at(g, i), one = make_float2(1.f, 1.f);
+        const float2 h = fma2(gp, make_float2(-1.f, -1.f), one);
+        put_pair(s, i, mul2(gp, kind == kSigmoid ? h : fma2(pair_at(z, i), h, one)));
+      },
+      [&](int i) {
+        const float h = 1.f - g[i];
+        s[i] = g[i] * (kind == kSigmoid ? h : fmaf(z[i], h, 1.f));
+      });
 }
 
 // Sums of K values over a row's threads, known to all of them. A block's sums meet in `red`
@@ -478,8 +492,9 @@ auto with_shape(const Plan& p, F f) {
 // How a call's rows lie: 16-byte accesses fit; fit but for a phase (Shape's SHIFT); or neither.
 enum Fit { kVec, kShift, kSingle };
 
-// pieces: 16-byte pieces per run of 8, over all tensors of a row. widest: elements of a row
-// that shares a warp, at most (256 where rows have a phase or no alignment). per_sm: threads an SM is to hold.
+// pieces: 16-byte pieces per run of 8, over all tensors of a row. widest: elements of a row that
+// shares a warp, at most (256 where rows have a phase or no alignment). per_sm: threads an SM is
+// to hold.
 Plan make_plan(int tokens, int H, int D, int pieces, Fit fit, int widest, bool per_head,
                int per_sm) {
   Plan p = {};
@@ -488,9 +503,9 @@ Plan make_plan(int tokens, int H, int D, int pieces, Fit fit, int widest, bool p
   p.v = vec ? 8 : 1;
   const int span = D + (p.shift ? 7 : 0);        // elements that a row's threads cover
   p.lanes = span > (fit == kVec ? widest : 256) ? 0
-            : !vec || span > 128                          ? 32
-            : span > 64                                   ? 16
-                                                          : 8;
+            : !vec || span > 128                ? 32
+            : span > 64                         ? 16
+                                                : 8;
   int per_block = 1;                             // groups of a block
   if (p.lanes) {
     p.nv = !vec ? 8 : span > 256 ? 2 : 1;
@@ -499,8 +514,10 @@ Plan make_plan(int tokens, int H, int D, int pieces, Fit fit, int widest, bool p
   } else {
     // Elements of a thread: 16, 32 in the widest rows, 4 in short ones element by element (more
     // threads then have more loads under way).
-    p.nv = vec ? (D <= kMaxThreads * 16 ? 2 : 4)
-               : D <= kMaxThreads * 4 ? 4 : D <= kMaxThreads * 16 ? 16 : 32;
+    p.nv = vec                     ? (D <= kMaxThreads * 16 ? 2 : 4)
+           : D <= kMaxThreads * 4  ? 4
+           : D <= kMaxThreads * 16 ? 16
+                                   : 32;
     const int n = p.nv * p.v;
     p.threads = ((span + n - 1) / n + 31) / 32 * 32;
   }
@@ -554,9 +571,11 @@ gdr_status zero(float* p, size_t n, cudaStream_t s) {
 bool bad_eps(float e) { return !(isfinite(e) && e > 0.f); }
 bool bad_act(int k) { return k != GDR_ACT_NONE && k != GDR_ACT_SIGMOID && k != GDR_ACT_SILU; }
 
-// Threads that an SM is to hold: of the kernels above (kFullPerSm: the residual's backward with a
-// norm, gate or scale per channel, at most kBwdPerSm), and of gated_rows_kernel.
+// Threads that an SM is to hold, as their registers allow: forward; the residual's backward, and
+// with a norm, gate or scale per channel (at most the former); the gated norm forward with a phase,
+// and backward; gated_rows_kernel, forward and backward.
 constexpr int kFwdPerSm = 1024, kBwdPerSm = 1024, kFullPerSm = 512;
+constexpr int kGatedShiftPerSm = 640, kGatedBwdPerSm = 512;
 constexpr int kFwdRowsPerSm = 768, kBwdRowsPerSm = 512;
 
 }  // namespace

@@ -124,8 +124,9 @@ __global__ void __launch_bounds__(kMaxThreads, S::N <= 16 ? 2 : 1) residual_fwd_
         }
         if (a.has_z) {
           rz.get(ahead, at, c, i, a.D, k);
-#pragma unroll
-          for (int e = 0; e < V; ++e) k[e] = act(k[e], a.kind);
+          float g[V];
+          gate_sigma<V>(g, k, a.kind);
+          gate_open<V>(k, g, k, a.kind);
           mul_run<V>(y, y, k);
         }
         if (a.sv) {
@@ -281,8 +282,10 @@ __global__ void __launch_bounds__(kMaxThreads, S::N <= 16 && !FULL ? 2 : 1) resi
         }
         if (a.has_z) {
           rz.get(ahead, at, c, i, a.D, z);
-#pragma unroll
-          for (int e = 0; e < V; ++e) q[e] = act(z[e], a.kind, z[e]);    // a, and a' in z
+          float sg[V];
+          gate_sigma<V>(sg, z, a.kind);
+          gate_open<V>(q, sg, z, a.kind);        // a
+          gate_slope<V>(z, sg, z, a.kind);       // a'
           mul_run<V>(z, z, g);
           mul_run<V>(z, z, p);
           mul_run<V>(q, q, g);
