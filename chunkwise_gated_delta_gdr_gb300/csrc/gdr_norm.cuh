@@ -166,7 +166,8 @@ __device__ __forceinline__ float dot_run(const float* a, const float* b) {
 }
 
 // The gate a(z) = g zz and its slope g (zz (1 - g) + c): g = 1 / (1 + e^-z) or 1 without an
-// activation, zz = z or, for the sigmoid, 1, and c = 1, 0 likewise.
+// activation, zz = z or, for the sigmoid, 1, and c = 1, 0 likewise. (Without an activation the
+// slope is 1 outright: the formula would make NaN of an infinite z.)
 enum Act { kNone = GDR_ACT_NONE, kSigmoid = GDR_ACT_SIGMOID, kSilu = GDR_ACT_SILU };
 // By the approximate 2^x and reciprocal (2^-22 each, and the rounding of z log2(e), half an ulp
 // of it); 0 for z < -88.
@@ -192,6 +193,11 @@ __device__ __forceinline__ void gate_open(float* a, const float* g, const float*
 }
 template <int V>                                 // s may be z
 __device__ __forceinline__ void gate_slope(float* s, const float* g, const float* z, int kind) {
+  if (kind == kNone) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) s[e] = 1.f;
+    return;
+  }
   over_run<V>(
       [&](int i) {
         const float2 gp = pair_at(g, i), one = make_float2(1.f, 1.f);

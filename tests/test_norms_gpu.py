@@ -538,3 +538,19 @@ def test_single_tokens_of_a_batch():
         gated_check(x, z, w, d)
         residual_check(x[:, :, 0], z[:, :, 1], w, d=d[:, :, 0].contiguous(),
                        dr=d[:, :, 1].contiguous())
+
+
+@pytest.mark.parametrize("D", [64, 513, 1024])
+def test_infinite_gate_without_activation(D):
+    """Its slope is 1, so its gradient d u w does not depend on it: with one row's gates infinite
+    every row's is what it is with finite ones, bit by bit."""
+    x, z, w, d = gated_inputs(1, 3, 2, D, seed=60)
+    _, want, _ = gdr.gated_norm_bwd(d, x, z, w, activation="none")
+    z[0, 1, 1] = float("inf")
+    _, got, _ = gdr.gated_norm_bwd(d, x, z, w, activation="none")
+    assert torch.equal(got, want)
+    r, y, z, d, dr, w, _, _ = residual_inputs(1, 3, D, seed=61)
+    kw = dict(activation="none", scale=0.5)
+    want = gdr.residual_norm_bwd(d, dr, r, y, w, gate=z, **kw)[2]
+    z[0, 1] = float("-inf")
+    assert torch.equal(gdr.residual_norm_bwd(d, dr, r, y, w, gate=z, **kw)[2], want)
