@@ -564,6 +564,7 @@ size_t gdr_paged_decode_attn_workspace_size(const gdr_attn_dims* dims,
  * every sequence, an own one or a bad length in its sequence. The result does not depend on
  * the order in which blocks run. Waits inside a block are bounded (gdr_set_flag_wait_limit);
  * where one gives up, the rows it would have reached are NaN: what is finite is right.
+ * prefix_len <= 2^30, HQ <= 2^20, B HQ <= 2^30.
  */
 gdr_status gdr_paged_prefix_attn(const void* q, const void* k_cache, const void* v_cache,
                                  const int32_t* prefix_table, int prefix_pages, int prefix_len,
@@ -590,7 +591,7 @@ size_t gdr_paged_prefix_attn_workspace_size(const gdr_attn_dims* dims, const gdr
  *   weight    (device) fp32 [D], [H, D] with weight_per_head, or NULL (ones)
  *   y         (device) [B, T, H, D] out_dtype, dense
  *
- * D <= 16384, H D <= 2^30, B T <= 2^30.
+ * D <= 16384, H <= 2^20, H D <= 2^30, B T <= 2^30.
  */
 typedef struct {
   int B, T, H, D;
