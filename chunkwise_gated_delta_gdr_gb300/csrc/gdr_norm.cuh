@@ -193,20 +193,16 @@ __device__ __forceinline__ void gate_open(float* a, const float* g, const float*
 }
 template <int V>                                 // s may be z
 __device__ __forceinline__ void gate_slope(float* s, const float* g, const float* z, int kind) {
-  if (kind == kNone) {
-#pragma unroll
-    for (int e = 0; e < V; ++e) s[e] = 1.f;
-    return;
-  }
   over_run<V>(
       [&](int i) {
         const float2 gp = pair_at(g, i), one = make_float2(1.f, 1.f);
         const float2 h = fma2(gp, make_float2(-1.f, -1.f), one);
-        put_pair(s, i, mul2(gp, kind == kSigmoid ? h : fma2(pair_at(z, i), h, one)));
+        const float2 zh = fma2(pair_at(z, i), h, one);
+        put_pair(s, i, kind == kNone ? one : mul2(gp, kind == kSigmoid ? h : zh));
       },
       [&](int i) {
         const float h = 1.f - g[i];
-        s[i] = g[i] * (kind == kSigmoid ? h : fmaf(z[i], h, 1.f));
+        s[i] = kind == kNone ? 1.f : g[i] * (kind == kSigmoid ? h : fmaf(z[i], h, 1.f));
       });
 }
 
