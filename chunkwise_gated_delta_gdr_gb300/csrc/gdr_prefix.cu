@@ -13,11 +13,11 @@
 // block leaves one part per item of its stretch, and a last kernel joins the parts of a row.
 //
 // Measured on one GB300, bf16, D = 128, a call among others:
-//   128 sequences behind 65000 keys, 32 / 16 heads, 0 .. 1024 own keys: 271 us (own keys 98, their
-//     join 8, shared keys 145 with the tensor cores 70 % busy, join 10-20; the bytes alone 160)
-//   64 behind 8192, 32 / 4 heads, 0 .. 512 own keys: 40 us (16, 22 and 8-14, in part at once)
-//   4 behind 200, 16 / 16 heads: 10.8 us
-// fp32, 5 behind 2999, 6 / 3 heads, D = 64: 14.8 us.
+//   128 sequences behind 65000 keys, 32 / 16 heads, 0 .. 1024 own keys: 266 us (own keys 98, their
+//     join 8, shared keys 145 with the tensor cores 70 % busy, join 10-15; the bytes alone 160)
+//   64 behind 8192, 32 / 4 heads, 0 .. 512 own keys: 39 us (16, 22 and 7-13, in part at once)
+//   4 behind 200, 16 / 16 heads: 10.1 us
+// fp32, 5 behind 2999, 6 / 3 heads, D = 64: 14.0 us.
 #include <type_traits>
 
 #include "gdr_prefix.cuh"
@@ -34,8 +34,10 @@ namespace {
 // NI = 1, 2 or 4 as there are rows. fp32 caches with 16-byte rows are copied asynchronously: the
 // next tile's K while this one's weights and P V are computed, its V while the next scores are.
 // 5 sequences behind 2999 keys, HK = 3, D = 64: a block has one tile, and the call is the chain
-// page - row - scores - sums - join (14.8 us; 4 more with a page looked up per row, one row after
-// the other). Long prompts are bound by the reads of q and k from shared memory.
+// page - row - scores - sums - join (14.0 us; 4 more with a page looked up per row, one row after
+// the other). Queries come four channels at a time, up to eight of a thread's loads under way at
+// once: 139 sequences behind 2 keys, 4 heads of 256, 26 us, 42 channel by channel. Long prompts
+// are bound by the reads of q and k from shared memory.
 constexpr int RM = 64, KT = 64, NT = 256;
 template <int NJ>                                // channels in runs of 64: D <= 64 NJ
 struct AnySmem {
@@ -74,9 +76,40 @@ __device__ __forceinline__ void any_tile(const PrefixArgs& a, float* to, const T
   }
 }
 
+// The first n rows of an item's queries, likewise (zeros where there are none).
+template <typename T, int NJ>
+__device__ __forceinline__ void any_queries(const PrefixArgs& a, float* to, int hk, int r0, int n,
+                                            int q_vec) {
+  constexpr int DP = NJ * 64, LD = DP + 4, PER = DP / 4;
+#pragma unroll 8
+  for (int e = threadIdx.x; e < n * PER; e += NT) {
+    const int r = e / PER, d = 4 * (e - r * PER), m = r0 + r;
+    const bool there = m < a.M && d < a.D;
+    const int64_t at = there ? q_row(a, hk, m) + d : 0;
+    if (!a.q_bf16 && q_vec) {
+      ptx::cp_async16(ptx::smem_u32(to + r * LD + d), static_cast<const float*>(a.q) + at,
+                      there ? 16 : 0);
+      continue;
+    }
+    float f[4] = {0.f, 0.f, 0.f, 0.f};
+    if (there) {
+      if (q_vec) {
+        load_f<bf16, 4>(static_cast<const bf16*>(a.q) + at, f);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (d + i < a.D)
+            f[i] = a.q_bf16 ? __bfloat162float(static_cast<const bf16*>(a.q)[at + i])
+                            : static_cast<const float*>(a.q)[at + i];
+      }
+    }
+    *reinterpret_cast<float4*>(to + r * LD + d) = make_float4(f[0], f[1], f[2], f[3]);
+  }
+}
+
 // Scores of rows ty + 16 i, keys tx + 16 j; keys from `live` on get -inf.
 template <int NJ, int NI>
-__device__ __forceinline__ void any_scores(AnySmem<NJ>& sm, int live) {
+__device__ __forceinline__ void any_scores(AnySmem<NJ>& sm, int live, float scale2) {
   constexpr int LD = AnySmem<NJ>::LD, LS = AnySmem<NJ>::LS;
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   float2 acc[NI][4];
@@ -106,7 +139,7 @@ __device__ __forceinline__ void any_scores(AnySmem<NJ>& sm, int live) {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       sm.s[(ty + 16 * i) * LS + tx + 16 * j] =
-          tx + 16 * j < live ? acc[i][j].x + acc[i][j].y : -INFINITY;
+          tx + 16 * j < live ? scale2 * (acc[i][j].x + acc[i][j].y) : -INFINITY;
 }
 
 // o = factor o + P V for rows ty + 16 i, channels 64 j + 4 tx ..
@@ -143,10 +176,10 @@ __device__ __forceinline__ void any_values(const AnySmem<NJ>& sm, float (*o)[NJ 
 }
 
 template <typename T, int NJ>
-__global__ void __launch_bounds__(NT) prefix_any_kernel(PrefixArgs a, int vec) {
+__global__ void __launch_bounds__(NT) prefix_any_kernel(PrefixArgs a, int vec, int q_vec) {
   extern __shared__ __align__(16) char raw[];
   typedef AnySmem<NJ> Smem;
-  constexpr int DP = Smem::DP, LD = Smem::LD, LS = Smem::LS;
+  constexpr int LS = Smem::LS;
   Smem& sm = *reinterpret_cast<Smem*>(raw);
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
   asm volatile("griddepcontrol.launch_dependents;");
@@ -168,17 +201,7 @@ __global__ void __launch_bounds__(NT) prefix_any_kernel(PrefixArgs a, int vec) {
     const T* vc = static_cast<const T*>(a.vc) + hk * a.ph;
     __syncthreads();                             // the last item's tiles are done with
     find(st.tile);
-#pragma unroll 4
-    for (int e = tid; e < RM * DP; e += NT) {
-      const int r = e / DP, d = e - r * DP, m = r0 + r;
-      float v = 0.f;
-      if (m < a.M && d < a.D) {
-        const int64_t at = q_row(a, hk, m) + d;
-        v = a.scale2 * (a.q_bf16 ? __bfloat162float(static_cast<const bf16*>(a.q)[at])
-                                 : static_cast<const float*>(a.q)[at]);
-      }
-      sm.q[r * LD + d] = v;
-    }
+    any_queries<T, NJ>(a, sm.q, hk, r0, rows <= 16 ? 16 : rows <= 32 ? 32 : RM, q_vec);
     float o[4][NJ * 4], m = -INFINITY, l = 0.f;  // m, l: of row tid / 4
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -195,11 +218,11 @@ __global__ void __launch_bounds__(NT) prefix_any_kernel(PrefixArgs a, int vec) {
       ptx::cp_async_wait<1>();                   // K of this tile
       __syncthreads();
       if (rows <= 16)
-        any_scores<NJ, 1>(sm, a.P - t * KT);
+        any_scores<NJ, 1>(sm, a.P - t * KT, a.scale2);
       else if (rows <= 32)
-        any_scores<NJ, 2>(sm, a.P - t * KT);
+        any_scores<NJ, 2>(sm, a.P - t * KT, a.scale2);
       else
-        any_scores<NJ, 4>(sm, a.P - t * KT);
+        any_scores<NJ, 4>(sm, a.P - t * KT, a.scale2);
       __syncthreads();
       if (more) any_tile<T, NJ>(a, sm.k, kc, sm.row[(t + 1) & 1], vec);
       ptx::cp_async_commit();
@@ -270,7 +293,8 @@ __global__ void __launch_bounds__(NT) prefix_any_kernel(PrefixArgs a, int vec) {
 // ------------------------------------------------------------ joining the stretches
 // A row (a query head of a sequence) of few parts takes a warp; one of more the JW warps of a
 // block, every JW-th part each (SPLIT). A lane holds V channels in a row, N runs of them, and
-// has UN parts' loads under way. 64 sequences, 8192 shared keys, HK = 4
+// has UN parts' loads under way, the first of them before the maximum is known (140 sequences of
+// 256 heads of 256 channels behind 9 keys: 146 -> 140 us a call). 64 sequences, 8192 shared keys, HK = 4
 // (16 parts a row), the whole call: 47 us, 55 with one warp for all parts of a row.
 constexpr int JW = 4;
 template <int V, bool SPLIT>
@@ -286,28 +310,9 @@ __global__ void __launch_bounds__(JW * 32) prefix_join_kernel(PrefixArgs a) {
   const int parts = parts_of(a, item) * a.units;
   const size_t first = (size_t)item * a.max_parts * a.units * a.rows + in;
   asm volatile("griddepcontrol.wait;" ::: "memory");       // the stretches are written
-  const float own = a.own_lse[row] * LOG2E;
-  float m = own;
-  for (int c = lane; c < parts; c += 32)
-    m = fmaxf(m, a.part_ml[(first + (size_t)c * a.rows) * 2]);
-#pragma unroll
-  for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, x));
-  const float base = m == -INFINITY ? 0.f : m;
-  float l = w0 == 0 ? exp2f(own - base) : 0.f, o[N][V];    // 0 without keys, NaN where they are bad
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int ch = (lane + 32 * i) * V;
-#pragma unroll
-    for (int k = 0; k < V; ++k) o[i][k] = 0.f;
-    if (ch < a.D && w0 == 0) {
-      load_f<float, V>(a.own_o + (size_t)row * a.D + ch, o[i]);
-#pragma unroll
-      for (int k = 0; k < V; ++k) o[i][k] *= l;
-    }
-  }
-  for (int c0 = w0; c0 < parts; c0 += STEP * UN) {
-    float2 ml[UN];
-    float v[UN][N][V];
+  float2 ml[UN];
+  float v[UN][N][V], o[N][V];
+  auto load = [&](int c0) {
 #pragma unroll
     for (int u = 0; u < UN; ++u) {
       const int c = c0 + STEP * u;
@@ -326,6 +331,29 @@ __global__ void __launch_bounds__(JW * 32) prefix_join_kernel(PrefixArgs a) {
         }
       }
     }
+  };
+  // All of the first loads under way before the first is waited for.
+  const float own = a.own_lse[row] * LOG2E;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int ch = (lane + 32 * i) * V;
+#pragma unroll
+    for (int k = 0; k < V; ++k) o[i][k] = 0.f;
+    if (ch < a.D && w0 == 0) load_f<float, V>(a.own_o + (size_t)row * a.D + ch, o[i]);
+  }
+  load(w0);
+  float m = own;
+  for (int c = lane; c < parts; c += 32)
+    m = fmaxf(m, a.part_ml[(first + (size_t)c * a.rows) * 2]);
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, x));
+  const float base = m == -INFINITY ? 0.f : m;
+  float l = w0 == 0 ? exp2f(own - base) : 0.f;   // 0 without keys, NaN where they are bad
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int k = 0; k < V; ++k) o[i][k] *= l;
+  for (int c0 = w0; c0 < parts;) {
 #pragma unroll
     for (int u = 0; u < UN; ++u) {
       const float f = exp2f(ml[u].x - base);
@@ -335,6 +363,8 @@ __global__ void __launch_bounds__(JW * 32) prefix_join_kernel(PrefixArgs a) {
 #pragma unroll
         for (int k = 0; k < V; ++k) o[i][k] = fmaf(f, v[u][i][k], o[i][k]);
     }
+    c0 += STEP * UN;
+    if (c0 < parts) load(c0);
   }
   if (SPLIT) {                                   // the warps' sums, in order
     if (lane == 0) sum[warp] = l;
@@ -496,10 +526,12 @@ gdr_status launch_tc(const PrefixArgs& a, const gdr_paged_cache* c, cudaStream_t
 
 template <typename T, int NJ>
 gdr_status launch_any(const PrefixArgs& a, int vec, int blocks, cudaStream_t s) {
+  const int q_vec = a.D % 4 == 0 && a.qb % 4 == 0 && a.qh % 4 == 0 &&
+                    is_aligned(a.q, a.q_bf16 ? 8 : 16);
   struct Tag;
   if (!allow_smem<Tag>(prefix_any_kernel<T, NJ>, sizeof(AnySmem<NJ>))) return GDR_ERR_CUDA;
   return launch_behind_smem(prefix_any_kernel<T, NJ>, dim3(blocks), NT, sizeof(AnySmem<NJ>), s, a,
-                            vec);
+                            vec, q_vec);
 }
 
 }  // namespace
