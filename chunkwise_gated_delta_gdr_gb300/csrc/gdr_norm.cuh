@@ -116,6 +116,20 @@ __device__ __forceinline__ void load_any(const void* p, int64_t i, int is_bf16, 
   else
     load_run<float, V, ONLY_READ>(static_cast<const float*>(p) + i, f);
 }
+// One element as it lies in memory, and its value. Nothing here waits for the load: with the
+// conversion beside it, in one of two branches, every load waited for the one before.
+template <bool ONLY_READ>
+__device__ __forceinline__ uint32_t load_raw(const void* p, int64_t i, int is_bf16) {
+  if (is_bf16) {
+    const unsigned short* q = static_cast<const unsigned short*>(p) + i;
+    return ONLY_READ ? __ldg(q) : *q;
+  }
+  const uint32_t* q = static_cast<const uint32_t*>(p) + i;
+  return ONLY_READ ? __ldg(q) : *q;
+}
+__device__ __forceinline__ float raw_value(uint32_t raw, int is_bf16) {
+  return __uint_as_float(is_bf16 ? raw << 16 : raw);
+}
 template <int V>
 __device__ __forceinline__ void store_any(void* p, int64_t i, int is_bf16, const float* f) {
   if (is_bf16)
@@ -308,7 +322,7 @@ template <class S, bool ONLY_READ>
 struct Row {
   const void* p;                                 // the row's first element
   int is_bf16, first;                            // first: its first piece within a stage
-  float now[S::kRegs ? S::N : 1], next[S::kRegs ? S::N : 1];
+  uint32_t now[S::kRegs ? S::N : 1], next[S::kRegs ? S::N : 1];
   __device__ __forceinline__ void set(const void* base, int64_t at, int bf, int piece) {
     p = static_cast<const char*>(base) + at * (bf ? 2 : 4);
     is_bf16 = bf;
@@ -318,7 +332,7 @@ struct Row {
   // D: the row's length.
   __device__ __forceinline__ void fetch(const Ahead& a, uint32_t places, int c, int i, int D) {
     if constexpr (S::kRegs) {
-      load_any<1, ONLY_READ>(p, i, is_bf16, next + c);
+      next[c] = load_raw<ONLY_READ>(p, i, is_bf16);
     } else {
       const int es = is_bf16 ? 2 : 4;
       const uint32_t at = places + (first + c * per_run()) * a.pitch;
@@ -356,7 +370,7 @@ struct Row {
           if (i + e < 0 || i + e >= D) f[e] = 0.f;
       }
     } else if constexpr (S::kRegs) {
-      f[0] = now[c];
+      f[0] = raw_value(now[c], is_bf16);
     } else {
       load_any<S::V, ONLY_READ>(p, i, is_bf16, f);
     }
