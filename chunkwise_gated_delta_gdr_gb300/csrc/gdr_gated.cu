@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(256, BWD ? 2 : 3) gated_rows_kernel(GatedArgs 
 // TY: the types of a call, where they are the usual ones.
 enum { kAnyTypes, kAllBf16, kAllF32 };
 template <class S, int TY, bool BWD>
-__global__ void __launch_bounds__(kMaxThreads, !BWD && S::N <= 16 && !S::SHIFT ? 2 : 1)
+__global__ void __launch_bounds__(kMaxThreads, !BWD && S::N <= 16 && !S::SHIFT && !S::kGroups ? 2 : 1)
     gated_kernel(GatedArgs a) {
   constexpr int V = S::V, NV = S::NV, N = S::N, TENSORS = BWD ? 3 : 2;
   extern __shared__ __align__(16) char places[];
@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kMaxThreads, !BWD && S::N <= 16 && !S::SHIFT ?
 #pragma unroll
   for (int j = 0; j < N; ++j) acc[j] = 0.f;
 
-  Row<S, S::NV <= 4> row[TENSORS];
+  Row<S, true> row[TENSORS];
   auto has = [&](int it) { return w.on && w.tok + it * w.step < a.tokens; };
   auto locate = [&](int it) {
     const int tok = w.tok + it * w.step, per = NV * (in_bf16 ? 1 : 2);
@@ -303,6 +303,9 @@ __global__ void __launch_bounds__(kMaxThreads, !BWD && S::N <= 16 && !S::SHIFT ?
     if (on)
 #pragma unroll
       for (int c = 0; c < NV; ++c) {
+        group_at<S>(w, c, a.D, row[0]);
+        if (a.first || BWD) group_at<S>(w, c, a.D, row[1]);
+        if (BWD) group_at<S>(w, c, a.D, row[TENSORS - 1]);
         const int i = (c * w.threads + w.tid) * V - phase;
         if (i >= a.D) continue;
         float x[V], z[V], t[V];
@@ -330,6 +333,8 @@ __global__ void __launch_bounds__(kMaxThreads, !BWD && S::N <= 16 && !S::SHIFT ?
     const float r = rsqrtf(fmaf(s[0], a.inv_d, a.eps)), m = s[1] * a.inv_d * r;
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
+      group_at<S>(w, c, a.D, row[0], row[1]);
+      if (BWD) group_at<S>(w, c, a.D, row[TENSORS - 1]);
       const int i = (c * w.threads + w.tid) * V - phase;
       if (i >= a.D) continue;
       float *gc = g + c * V, x[V], z[V], t[V], u[V], wt[V];

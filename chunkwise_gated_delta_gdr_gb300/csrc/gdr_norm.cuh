@@ -35,11 +35,15 @@ struct Shape {
   static constexpr bool SHIFT = SHIFT_;
   // Elements that the groups of a block of 256 threads hold.
   static constexpr int kSums = LANES_ ? 256 * N : 1;
-  // Copies ahead of time go through shared memory, 16 bytes at a time. Rows past 8192 elements
-  // (NV beyond 2 runs of 8) are loaded when they are needed, and so are long ones element by element.
+  // Copies ahead of time go through shared memory, 16 bytes at a time.
   static constexpr bool kAhead = V_ == 8 && NV_ <= 2;
   // Short rows element by element: the next row's elements are loaded into registers.
   static constexpr bool kRegs = V_ == 1 && NV_ <= 8;
+  // Rows past 8192 elements, and long ones element by element, are loaded when they are needed,
+  // kGroup runs at a time (3006 rows of 9000 with norm, gate and scale, training step: 582 us run by
+  // run, 472 so).
+  static constexpr bool kGroups = !kAhead && !kRegs;
+  static constexpr int kGroup = V_ == 1 ? 8 : 2;
 };
 
 // V consecutive elements as raw words.
@@ -108,14 +112,6 @@ __device__ __forceinline__ void store_run(T* p, const float* f) {
     reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
   }
 }
-// The same with the type known at run time only.
-template <int V, bool ONLY_READ>
-__device__ __forceinline__ void load_any(const void* p, int64_t i, int is_bf16, float* f) {
-  if (is_bf16)
-    load_run<bf16, V, ONLY_READ>(static_cast<const bf16*>(p) + i, f);
-  else
-    load_run<float, V, ONLY_READ>(static_cast<const float*>(p) + i, f);
-}
 // One element as it lies in memory, and its value. Nothing here waits for the load: with the
 // conversion beside it, in one of two branches, every load waited for the one before.
 template <bool ONLY_READ>
@@ -130,6 +126,7 @@ __device__ __forceinline__ uint32_t load_raw(const void* p, int64_t i, int is_bf
 __device__ __forceinline__ float raw_value(uint32_t raw, int is_bf16) {
   return __uint_as_float(is_bf16 ? raw << 16 : raw);
 }
+// A run into memory whose type is known at run time only.
 template <int V>
 __device__ __forceinline__ void store_any(void* p, int64_t i, int is_bf16, const float* f) {
   if (is_bf16)
@@ -317,12 +314,12 @@ struct Ahead {
 
 // One tensor of a row. With S::kAhead its runs come from the thread's places in shared memory,
 // from `first` on, where fetch() had them copied; with S::kRegs from registers, where fetch() put
-// the next row's and advance() made them this one's; else from global memory.
+// the next row's and advance() made them this one's; else group() brings them.
 template <class S, bool ONLY_READ>
 struct Row {
   const void* p;                                 // the row's first element
   int is_bf16, first;                            // first: its first piece within a stage
-  uint32_t now[S::kRegs ? S::N : 1], next[S::kRegs ? S::N : 1];
+  uint32_t now[S::kRegs ? S::N : S::kGroups ? S::kGroup * S::V : 1], next[S::kRegs ? S::N : 1];
   __device__ __forceinline__ void set(const void* base, int64_t at, int bf, int piece) {
     p = static_cast<const char*>(base) + at * (bf ? 2 : 4);
     is_bf16 = bf;
@@ -351,6 +348,34 @@ struct Row {
 #pragma unroll
       for (int j = 0; j < S::N; ++j) now[j] = next[j];
   }
+  // Runs c .. c + kGroup - 1, all under way at once: zeros behind the row.
+  __device__ __forceinline__ void group(const Walk& w, int c, int D) {
+    if constexpr (S::kGroups) {
+      auto bring = [&](auto* t) {
+        using T = std::remove_pointer_t<decltype(t)>;
+#pragma unroll
+        for (int j = 0; j < S::kGroup; ++j) {
+          const int i = ((c + j) * w.threads + w.tid) * S::V;
+          uint32_t* to = now + j * S::V;
+          if constexpr (S::V == 1) {
+            to[0] = i < D ? load_raw<ONLY_READ>(p, i, sizeof(T) == 2) : 0u;
+          } else {
+            const uint4* q = reinterpret_cast<const uint4*>(static_cast<const T*>(p) + i);
+#pragma unroll
+            for (int k = 0; k < S::V * (int)sizeof(T) / 16; ++k) {
+              uint4 u = make_uint4(0, 0, 0, 0);
+              if (i < D) u = ONLY_READ ? __ldg(q + k) : q[k];
+              to[4 * k] = u.x, to[4 * k + 1] = u.y, to[4 * k + 2] = u.z, to[4 * k + 3] = u.w;
+            }
+          }
+        }
+      };
+      if (is_bf16)
+        bring(static_cast<bf16*>(nullptr));
+      else
+        bring(static_cast<float*>(nullptr));
+    }
+  }
   __device__ __forceinline__ void get(const Ahead& a, uint32_t places, int c, int i, int D,
                                       float* f) const {
     if constexpr (S::kAhead) {
@@ -371,13 +396,21 @@ struct Row {
       }
     } else if constexpr (S::kRegs) {
       f[0] = raw_value(now[c], is_bf16);
+    } else if constexpr (S::V == 1) {
+      f[0] = raw_value(now[c % S::kGroup], is_bf16);
     } else {
-      load_any<S::V, ONLY_READ>(p, i, is_bf16, f);
+      const uint32_t* u = now + c % S::kGroup * S::V;
+      if (is_bf16) {
+        const Run<bf16, 8> r = {{u[0], u[1], u[2], u[3]}};
+        unpack<bf16, 8>(r, f);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(u[e]);
+      }
     }
   }
 };
-
-// A run's elements of a vector [D] that all rows share (0 outside it), and a run into a row.
+// A run's elements of a vector [D] that all rows share (0 outside it).
 template <class S>
 __device__ __forceinline__ void load_shared(const float* w, int i, int D, float* f) {
   if constexpr (S::SHIFT) {
@@ -387,6 +420,14 @@ __device__ __forceinline__ void load_shared(const float* w, int i, int D, float*
     load_run<float, S::V, true>(w + i, f);
   }
 }
+// The next group of a row's tensors, where run c is its first.
+template <class S, typename... Rows>
+__device__ __forceinline__ void group_at(const Walk& w, int c, int D, Rows&... rows) {
+  if constexpr (S::kGroups)
+    if (c % S::kGroup == 0) (rows.group(w, c, D), ...);
+}
+
+// A run into a row.
 template <class S>
 __device__ __forceinline__ void store_row(void* p, size_t row, int i, int D, int is_bf16,
                                           const float* f) {
@@ -473,6 +514,7 @@ __device__ __forceinline__ void block_part(const float* acc, float* s, float* to
 constexpr int kSms = 152;
 constexpr int kWidest = 16384;                   // elements of a row at most
 constexpr int kSmemPerSm = 200 * 1024;           // of copies ahead, an SM and a block at most
+constexpr int kGroupsPerSm = 512;                // threads, of rows in groups of elements
 constexpr int kPlainSmem = 24 * 1024;            // fits beside the static part without being asked for
 
 // What a call's kernel looks like: threads of a block, groups and blocks, copies ahead.
@@ -487,7 +529,10 @@ template <typename F>
 auto with_block(const Plan& p, F f) {
   if (p.shift) return f(Shape<0, 8, 2, true>());
   if (p.v == 8) return p.nv == 2 ? f(Shape<0, 8, 2>()) : f(Shape<0, 8, 4>());
-  return p.nv == 4 ? f(Shape<0, 1, 4>()) : p.nv == 16 ? f(Shape<0, 1, 16>()) : f(Shape<0, 1, 32>());
+  return p.nv == 4    ? f(Shape<0, 1, 4>())
+         : p.nv == 8  ? f(Shape<0, 1, 8>())
+         : p.nv == 16 ? f(Shape<0, 1, 16>())
+                      : f(Shape<0, 1, 32>());
 }
 // TWO: whether rows of more than 256 elements share a warp.
 template <bool TWO, typename F>
@@ -528,15 +573,18 @@ Plan make_plan(int tokens, int H, int D, int pieces, Fit fit, int widest, bool p
     p.threads = 256;
     per_block = p.threads / p.lanes;
   } else {
-    // Elements of a thread: 16, 32 in the widest rows, 4 in short ones element by element (more
-    // threads then have more loads under way).
+    // Elements of a thread: 16, 32 in the widest rows; element by element as few as 512 threads
+    // allow (more threads have more loads under way: 1776 rows of 4075 with a gate from an odd
+    // slice, training step, 124 us with 16 a thread, 70 with 8).
     p.nv = vec                     ? (D <= kMaxThreads * 16 ? 2 : 4)
            : D <= kMaxThreads * 4  ? 4
+           : D <= kMaxThreads * 8  ? 8
            : D <= kMaxThreads * 16 ? 16
                                    : 32;
     const int n = p.nv * p.v;
     p.threads = ((span + n - 1) / n + 31) / 32 * 32;
   }
+  if (p.lanes == 0 && !vec && p.nv > 8 && per_sm > kGroupsPerSm) per_sm = kGroupsPerSm;
   const long long rows = (long long)tokens * H;
   long long blocks = (rows + per_block - 1) / per_block;
   const long long most = (long long)kSms * (per_sm / p.threads > 1 ? per_sm / p.threads : 1);

@@ -45,7 +45,7 @@ struct Types {
 
 // (With 16 elements a thread, 64 registers: an SM holds the kFwdPerSm threads that the plan counts on.)
 template <class S, int TY>
-__global__ void __launch_bounds__(kMaxThreads, S::N <= 16 ? 2 : 1) residual_fwd_kernel(ResArgs a) {
+__global__ void __launch_bounds__(kMaxThreads, S::N <= 16 && !S::kGroups ? 2 : 1) residual_fwd_kernel(ResArgs a) {
   constexpr int V = S::V, NV = S::NV, N = S::N;
   extern __shared__ __align__(16) char places[];
   __shared__ Red red;
@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(kMaxThreads, S::N <= 16 ? 2 : 1) residual_fwd_
   const int phase = S::SHIFT ? (int)(((long long)w.tok * a.D) & 7) : 0;
   const Ahead ahead(places, a.pieces, a.stages);
   Row<S, false> rr;                              // may be the result's own memory
-  Row<S, S::NV <= 4> ry, rz;
+  Row<S, true> ry, rz;
   const int r_bf16 = Types<TY>::r(a), y_bf16 = Types<TY>::y(a), out_bf16 = Types<TY>::out(a);
   auto has = [&](int it) { return (S::LANES == 0 || w.on) && w.tok + it * w.step < a.tokens; };
   auto locate = [&](int it) {
@@ -97,6 +97,7 @@ __global__ void __launch_bounds__(kMaxThreads, S::N <= 16 ? 2 : 1) residual_fwd_
       s[0] = 0.f;
 #pragma unroll
       for (int c = 0; c < NV; ++c) {
+        group_at<S>(w, c, a.D, ry);
         const int i = (c * w.threads + w.tid) * V - phase;
         if (!on || i >= a.D) continue;
         float y[V];
@@ -110,6 +111,9 @@ __global__ void __launch_bounds__(kMaxThreads, S::N <= 16 ? 2 : 1) residual_fwd_
     s[0] = 0.f;
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
+      group_at<S>(w, c, a.D, rr);
+      if (a.has_y) group_at<S>(w, c, a.D, ry);
+      if (a.has_z) group_at<S>(w, c, a.D, rz);
       const int i = (c * w.threads + w.tid) * V - phase;
       if (!on || i >= a.D) continue;
       float* x = r + c * V;
@@ -158,7 +162,7 @@ __global__ void __launch_bounds__(kMaxThreads, S::N <= 16 ? 2 : 1) residual_fwd_
 
 // FULL: y goes through a norm, a gate or a scale per channel; without, dy = s g.
 template <class S, int TY, bool FULL>
-__global__ void __launch_bounds__(kMaxThreads, S::N <= 16 && !FULL ? 2 : 1) residual_bwd_kernel(ResArgs a) {
+__global__ void __launch_bounds__(kMaxThreads, S::N <= 16 && !S::kGroups && !FULL ? 2 : 1) residual_bwd_kernel(ResArgs a) {
   constexpr int V = S::V, NV = S::NV, N = S::N;
   extern __shared__ __align__(16) char places[];
   __shared__ Red red;
@@ -170,7 +174,7 @@ __global__ void __launch_bounds__(kMaxThreads, S::N <= 16 && !FULL ? 2 : 1) resi
   for (int k = 0; k < (FULL ? 3 : 1); ++k)
 #pragma unroll
     for (int j = 0; j < N; ++j) acc[k][j] = 0.f;
-  Row<S, S::NV <= 4> rr, rd, rg, ry, rz;
+  Row<S, true> rr, rd, rg, ry, rz;
   const int r_bf16 = Types<TY>::r(a), y_bf16 = Types<TY>::y(a), out_bf16 = Types<TY>::out(a);
   auto has = [&](int it) { return (S::LANES == 0 || w.on) && w.tok + it * w.step < a.tokens; };
   auto locate = [&](int it) {
@@ -220,6 +224,8 @@ __global__ void __launch_bounds__(kMaxThreads, S::N <= 16 && !FULL ? 2 : 1) resi
     float s[3] = {0.f, 0.f, 0.f};
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
+      group_at<S>(w, c, a.D, rr, rd);
+      if (FULL && a.post) group_at<S>(w, c, a.D, ry);
       const int i = (c * w.threads + w.tid) * V - phase;
       if (!on || i >= a.D) continue;
       float x[V], d[V], k[V];
@@ -242,6 +248,10 @@ __global__ void __launch_bounds__(kMaxThreads, S::N <= 16 && !FULL ? 2 : 1) resi
     float dp[FULL ? N : 1], se[1] = {0.f};       // dp: dp wp behind a norm
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
+      group_at<S>(w, c, a.D, rr, rd);
+      if (a.has_dr) group_at<S>(w, c, a.D, rg);
+      if (FULL) group_at<S>(w, c, a.D, ry);
+      if (FULL && a.has_z) group_at<S>(w, c, a.D, rz);
       const int i = (c * w.threads + w.tid) * V - phase;
       if (!on || i >= a.D) continue;
       float g[V], x[V], d[V], k[V];
@@ -324,6 +334,7 @@ __global__ void __launch_bounds__(kMaxThreads, S::N <= 16 && !FULL ? 2 : 1) resi
         const float my = se[0] * a.inv_d;
 #pragma unroll
         for (int c = 0; c < NV; ++c) {
+          group_at<S>(w, c, a.D, ry);
           const int i = (c * w.threads + w.tid) * V - phase;
           if (!on || i >= a.D) continue;
           float y[V];
