@@ -554,3 +554,18 @@ def test_infinite_gate_without_activation(D):
     want = gdr.residual_norm_bwd(d, dr, r, y, w, gate=z, **kw)[2]
     z[0, 1] = float("-inf")
     assert torch.equal(gdr.residual_norm_bwd(d, dr, r, y, w, gate=z, **kw)[2], want)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("D", [301, 2047, 2049, 4075, 4097, 8191, 9000])
+def test_long_rows_from_anywhere(D, dtype):
+    """Slices that start one element behind a boundary: no row is aligned."""
+    gen, B, T, H = gen_of(70), 2, 5, 2
+    x, z, w, d = gated_inputs(B, T, H, D, dtype=dtype, seed=71, weight="head")
+    wide = rnd(gen, B, T, 2 * H * D + 3, dtype=dtype)
+    gated_check(x, wide[..., 1:1 + H * D].unflatten(-1, (H, D)), w, d, "silu", False)
+    gated_check(wide[..., 1 + H * D:1 + 2 * H * D].unflatten(-1, (H, D)), z, w, d, "sigmoid", True)
+    r, y, _, d, dr, w, wp, s = residual_inputs(B, T, D, rt=F32, yt=dtype, seed=72)
+    gate = wide[..., 1:1 + D]
+    residual_check(r, y, w, gate, wp, s, d, dr, "silu", True)
+    residual_check(r, wide[..., 1:1 + D], w, d=d, dr=dr)
