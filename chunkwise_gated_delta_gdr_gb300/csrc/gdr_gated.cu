@@ -10,8 +10,8 @@
 // chain load - sum over the row - store of one row below. Measured on one GB300, bf16, a pass
 // among others (a plain copy: 6.70 TB/s):
 //   2 x 8192 x 32 heads of 128: 62.7 us, 6.4 TB/s; 64 decode tokens x 16 heads 2.5 us
-//   training step, 4096 x 12 heads of 128: 24.1 us (forward 9, backward 14, weights' sums 5 with
-//   cold caches); 2 x 4096 x 4 groups of 512, gate first, weights per group 50.9 us; whole rows,
+//   training step, 4096 x 12 heads of 128: 24.3 us (forward 9, backward 14, weights' sums 5 with
+//   cold caches); 2 x 4096 x 4 groups of 512, gate first, weights per group 51.4 us; whole rows,
 //   8192 x 1536 55 us, 4096 x 4096 69 us, 36288 rows of 173 58 us
 #include "gdr_norm.cuh"
 
