@@ -436,7 +436,8 @@ bool tc_fits(const gdr_attn_dims* d, const gdr_paged_cache* c) {
 Plan make_plan(const gdr_attn_dims* d, const gdr_paged_cache* c, int P) {
   Plan p = {};
   p.decode_bytes = gdr_paged_decode_attn_workspace_size(d, c);
-  if (P == 0) return p;                          // no shared keys: paged_decode_attn's own work
+  // No shared keys: paged_decode_attn's own work; no sequences: nothing to cut up.
+  if (P == 0 || d->B == 0) return p;
   const int G = d->HQ / c->HK;
   const long long M = (long long)d->B * G;
   p.rows = RM;

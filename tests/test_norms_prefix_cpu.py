@@ -184,6 +184,24 @@ def test_prefix_pointers(layers):
     assert prefix(layers, attn_dims(layers, B=0), c, q=None) == OK
 
 
+@pytest.mark.parametrize("dtype,D", [(1, 128), (1, 256), (1, 40), (0, 128)])
+def test_scratch_of_no_tokens(layers, dtype, D):
+    """The binding asks for the scratch's size before the call: an empty batch has one, too,
+    whichever kernels its sizes and types would take."""
+    lib = layers._lib()
+    c = cache_dims(layers, dtype=dtype, D=D, page_stride=32 * D, token_stride=2 * D, head_stride=D)
+    for n in (0, 1, 70, 80):
+        d = attn_dims(layers, B=0, q_dtype=dtype)
+        assert lib.gdr_paged_prefix_attn_workspace_size(d, c, 5, n) > 0
+        assert prefix(layers, d, c, n=n, q=None) == OK
+    for kw in (dict(B=0), dict(T=0), dict(B=0, T=0)):
+        for D in (D, D + 1, 5000):
+            d = gated_dims(layers, in_dtype=dtype, D=D, **kw)
+            assert lib.gdr_gated_norm_bwd_workspace_size(d) > 0
+            d = residual_dims(layers, residual_dtype=dtype, D=D, **kw)
+            assert lib.gdr_residual_norm_bwd_workspace_size(d) > 0
+
+
 # ------------------------------------------------------------------ the binding
 def test_binding_refuses_host_tensors(layers):
     x = torch.zeros(1, 4, 2, 8)
