@@ -193,8 +193,25 @@ bool allow_smem(Fn fn, int bytes) {
   return true;
 }
 
-// A launch that may begin while the kernel before it in the stream still runs; the launched
-// kernel waits for that one's results itself (griddepcontrol.wait, in every block).
+// Kernels that overlap their neighbours in the stream. What the kernel before wrote may be read, and
+// what it still reads may be written, only behind wait_for_before(); that one waited for the kernel
+// before it, so everything earlier in the stream is done, too. No kernel launched so touches memory
+// ahead of its own wait, not even what an earlier kernel is known to have finished: nothing promises
+// that a grid sees that without one. let_next_begin() lets the next kernel's blocks come in; they wait
+// themselves.
+__device__ __forceinline__ void wait_for_before() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void let_next_begin() {
+  asm volatile("griddepcontrol.launch_dependents;");
+}
+__device__ __forceinline__ void begin_behind() {
+  let_next_begin();
+  wait_for_before();
+}
+
+// A launch that may begin while the kernel before it in the stream still runs; every block of the
+// launched kernel waits for that one's results itself (wait_for_before).
 template <typename Fn, typename... Args>
 gdr_status launch_behind_smem(Fn fn, dim3 grid, int threads, size_t smem, cudaStream_t s,
                               Args... args) {

@@ -19,8 +19,8 @@
 // tensor rate at 8 queries a head. Bound by HBM from some 100 MB on, by the chain length -
 // page - row - sums below. Measured on one GB300, bf16, D = 128, kv heads of the cache HK:
 //   1 x 65000 keys, HK = 16, 2 queries a head: 90-92 us, 5.8-6.0 TB/s (a plain copy: 6.78 TB/s)
-//   64 sequences of 0 .. 8192 keys, HK = 4, 8 queries a head: 97-101 us, 79-82 % of the copy rate
-//   4 x 200 keys, HK = 16: 7.0 us a call (8.2 when it starts after the kernel before has ended)
+//   64 sequences of 0 .. 8192 keys, HK = 4, 8 queries a head: 104-106 us, 75-77 % of the copy rate
+//   4 x 200 keys, HK = 16: 7.1 us a call (8.2 when it starts after the kernel before has ended)
 // 16 x 8000 keys, HK = 8, D = 128: 4 queries a head 92 us, 5.7 TB/s; 16 97 us; 32 182 us, since the
 // cache is read once per group of 16.
 // fp32, 16 x 8000 keys, HK = 8: D = 256 309 us, 6.8 TB/s; D = 64 92 us, 5.7; D = 128 with 4
@@ -57,13 +57,6 @@ struct AttnArgs {
   int64_t qb, qh, pp, pt, ph;
   long long cap;                  // max_pages * page
 };
-
-// Starts while the kernel before still runs; from here on that one is done, and what is launched
-// behind may start: it finds the inputs of this call ready.
-__device__ __forceinline__ void begin_behind() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;");
-}
 
 // Keys of sequence b: [lo, n), and whether its length is valid.
 struct Span {
@@ -786,18 +779,18 @@ __global__ void __launch_bounds__(Core::NW * 32, Core::OCC) paged_ring_kernel(At
 }
 
 // ------------------------------------------------------------ items cut by block boundaries
-// Launched behind the kernel above; each block finds its item before it waits for that kernel,
-// so that what is left after it is two rounds of loads. It costs 4 us at 64 sequences and 6 at
-// one of 65000 keys (16 items of 19 or 20 parts), most of it the second kernel's start. Block (x, y): heads y hb
-// and on of item x, or, with more items than blocks, of the item that the boundary after
-// stretch x is the first to cut. The JW warps share a head's parts (hb < JW) or take every
-// JW-th head; a lane has V channels in a row at a time.
+// Launched behind the kernel above and waits for it before it reads the lengths, too: they may come
+// from the kernel before that one. (64 sequences of 0 .. 8192 keys: 104-106 us a call; 97-101 were
+// measured with the items looked up ahead of the wait, on other draws of the lengths.) Block (x, y):
+// heads y hb and on of item x, or, with more items than blocks, of the item that the boundary after
+// stretch x is the first to cut. The JW warps share a head's parts (hb < JW) or take every JW-th
+// head; a lane has V channels in a row at a time.
 constexpr int JW = 4;
 template <int V>
 __global__ void __launch_bounds__(JW * 32) paged_join_kernel(AttnArgs a) {
   constexpr int N = 256 / (32 * V);              // runs of V channels of a lane
   __shared__ float red[JW][256], sum[JW];
-  asm volatile("griddepcontrol.launch_dependents;");       // what comes behind waits for this one
+  begin_behind();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int per_b = a.HK * a.groups;
   const long long total = total_tiles(a, lane), per = (total + a.blocks - 1) / a.blocks;
@@ -827,7 +820,6 @@ __global__ void __launch_bounds__(JW * 32) paged_join_kernel(AttnArgs a) {
   const int parts = mine ? (int)((first + p.s.tiles() - 1) / per - c0) + 1 : 0;
   const int hk = p.item / a.groups, g0 = (p.item - hk * a.groups) * a.GH;
   const int heads = min(a.GH, a.G - g0), h0 = blockIdx.y * a.hb, h1 = min(heads, h0 + a.hb);
-  asm volatile("griddepcontrol.wait;" ::: "memory");       // the parts are written
   if (parts < 2) return;
   const int share = a.hb < JW ? JW / a.hb : 1;             // warps per head
   const int w0 = warp % share;

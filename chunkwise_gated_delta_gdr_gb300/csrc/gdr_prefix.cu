@@ -13,11 +13,16 @@
 // block leaves one part per item of its stretch, and a last kernel joins the parts of a row.
 //
 // Measured on one GB300, bf16, D = 128, a call among others:
-//   128 sequences behind 65000 keys, 32 / 16 heads, 0 .. 1024 own keys: 266 us (own keys 98, their
-//     join 8, shared keys 145 with the tensor cores 70 % busy, join 10-15; the bytes alone 160)
-//   64 behind 8192, 32 / 4 heads, 0 .. 512 own keys: 39 us (16, 22 and 7-13, in part at once)
-//   4 behind 200, 16 / 16 heads: 10.1 us
-// fp32, 5 behind 2999, 6 / 3 heads, D = 64: 14.0 us.
+//   128 sequences behind 65000 keys, 32 / 16 heads, 0 .. 1024 own keys: 264-267 us (own keys 98,
+//     their join 8, shared keys 145 with the tensor cores 70 % busy, join 10-15; the bytes alone 160)
+//   64 behind 8192, 32 / 4 heads, 0 .. 512 own keys: 41 us (16, 22 and 7-13)
+//   4 behind 200, 16 / 16 heads: 12.7 us
+// fp32, 5 behind 2999, 6 / 3 heads, D = 64: 17.6 us.
+//
+// The kernels start behind one another and each waits for the one before. That the shared keys'
+// kernel would find the call's inputs ready without a wait, since the own keys' one waited for them
+// before it let the next one start, is true of the device and promised nowhere; it was worth 2 us on
+// 64 behind 8192, 2.6 and 3.6 on the two short ones.
 #include <type_traits>
 
 #include "gdr_prefix.cuh"
@@ -34,7 +39,7 @@ namespace {
 // NI = 1, 2 or 4 as there are rows. fp32 caches with 16-byte rows are copied asynchronously: the
 // next tile's K while this one's weights and P V are computed, its V while the next scores are.
 // 5 sequences behind 2999 keys, HK = 3, D = 64: a block has one tile, and the call is the chain
-// page - row - scores - sums - join (14.0 us; 4 more with a page looked up per row, one row after
+// page - row - scores - sums - join (17.6 us; 4 more with a page looked up per row, one row after
 // the other). Queries come four channels at a time, up to eight of a thread's loads under way at
 // once: 139 sequences behind 2 keys, 4 heads of 256, 26 us, 42 channel by channel. Long prompts
 // are bound by the reads of q and k from shared memory.
@@ -182,9 +187,10 @@ __global__ void __launch_bounds__(NT) prefix_any_kernel(PrefixArgs a, int vec, i
   constexpr int LS = Smem::LS;
   Smem& sm = *reinterpret_cast<Smem*>(raw);
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
-  asm volatile("griddepcontrol.launch_dependents;");
+  let_next_begin();
   Stretch st = stretch_of(a, blockIdx.x);
   if (tid == 0) sm.bad = 0;
+  wait_for_before();
   // The keys of tile t, each looked up by one thread.
   auto find = [&](int t) {
     if (tid < KT) {
@@ -286,8 +292,6 @@ __global__ void __launch_bounds__(NT) prefix_any_kernel(PrefixArgs a, int vec, i
     st.tile = 0;
     ++st.item;
   }
-  // What comes behind this kernel also waits for the one before it, whose end nothing here needs.
-  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ------------------------------------------------------------ joining the stretches
@@ -309,7 +313,7 @@ __global__ void __launch_bounds__(JW * 32) prefix_join_kernel(PrefixArgs a) {
   const int item = hk * a.row_tiles + r / a.rows, in = r % a.rows;
   const int parts = parts_of(a, item) * a.units;
   const size_t first = (size_t)item * a.max_parts * a.units * a.rows + in;
-  asm volatile("griddepcontrol.wait;" ::: "memory");       // the stretches are written
+  wait_for_before();                             // the stretches are written
   float2 ml[UN];
   float v[UN][N][V], o[N][V];
   auto load = [&](int c0) {

@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(Config<D, TMA>::THREADS, 1)
   char* base = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(raw) + 1023) &
                                        ~static_cast<uintptr_t>(1023));
   __shared__ Bars bars;
-  asm volatile("griddepcontrol.launch_dependents;");
+  let_next_begin();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t q_at = smem_u32(base), ring = q_at + U * F::QTILE;
   if (threadIdx.x == 0) {
@@ -242,6 +242,7 @@ __global__ void __launch_bounds__(Config<D, TMA>::THREADS, 1)
   const uint32_t tmem = bars.tmem;
   volatile uint32_t* dead = &bars.dead;
   Stretch st = stretch_of(a, blockIdx.x);
+  wait_for_before();                                       // nothing above touches global memory
   auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_for(bar, parity, a.polls, dead); };
 
   if (warp < F::SOFT) {
@@ -555,8 +556,6 @@ __global__ void __launch_bounds__(Config<D, TMA>::THREADS, 1)
     __syncwarp();
     tmem_dealloc(tmem, 512);
   }
-  // What comes behind this kernel also waits for the one before it, whose end nothing here needs.
-  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 }  // namespace tc

@@ -68,7 +68,7 @@ constexpr int GW = 8;                            // warps per block
 template <typename I, typename O, int MODE>
 __global__ void __launch_bounds__(GW * 32) qk_any_kernel(QkArgs a) {
   constexpr int J = 8;                           // channels per lane: D <= 256
-  if (MODE == kBwd) asm volatile("griddepcontrol.launch_dependents;");
+  if (MODE == kBwd) let_next_begin();
   __shared__ float row[GW][256];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = a.R >> 1;
   const int per = a.HQ + a.HK + (MODE == kAppend ? a.HK : 0);
@@ -238,7 +238,7 @@ constexpr int resident(int mode) { return mode == kBwd ? 4 : 6; }
 template <typename I, typename O, int MODE, bool kNeighbours, int GL>
 __global__ void __launch_bounds__(VT, resident(MODE)) qk_vec_kernel(QkArgs a, VecPlan v) {
   constexpr bool bwd = MODE == kBwd;
-  if (bwd) asm volatile("griddepcontrol.launch_dependents;");
+  if (bwd) let_next_begin();
   constexpr int K = bwd ? 1 : 2, DEPTH = 4;      // rows at work; steps of as many under way
   constexpr int XROW = 2 * VT * 4, DROW = bwd ? 2 * VT * 4 : 0;   // elements of a row of the block
   __shared__ __align__(16) I stage_x[DEPTH * K * XROW];
@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(SX * SR) qk_weight_kernel(const float* part, i
                                                             float* dwq, float* dwk) {
   __shared__ float red[SR][SX];
   const int x = threadIdx.x % SX, y = threadIdx.x / SX, col = blockIdx.x * SX + x;
-  asm volatile("griddepcontrol.wait;" ::: "memory");       // the sums are written
+  wait_for_before();                             // the sums are written
   float s = 0.f;
   if (col < 2 * D) {
 #pragma unroll 10

@@ -418,3 +418,95 @@ def test_two_calls_at_once():
             again = gdr.gated_norm(x, x)
             assert torch.equal(y, again)
             assert torch.equal(r, gdr.residual_norm(again.flatten(2), x.flatten(2))[0])
+
+
+@pytest.mark.parametrize("dtype,D,page,P", [(BF, 128, 64, 3000), (BF, 64, 17, 700), (F32, 64, 16, 900),
+                                            (BF, 40, 16, 300), (BF, 128, 16, 0)])
+def test_inputs_written_just_before(dtype, D, page, P):
+    """Queries, keys, tables and lengths that the kernels right before write, one of which lets
+    the next one begin at once, in a queue that the device is behind with: the bits of the same
+    calls waited for one by one. With own keys of several blocks, whose parts are joined, too."""
+    B, HQ, HK, n = 20, 8, 2, 6
+    s = make(B, HQ, HK, D, P, [(131 * b) % 2000 for b in range(B)], page=page, dtype=dtype, seed=24)
+    gen = torch.Generator().manual_seed(25)
+    q = rnd(gen, n, B, 1, HQ, D, dtype=dtype)
+    z = rnd(gen, n, B, 1, HQ, D, dtype=dtype)
+    k, v = (rnd(gen, n, B, 1, HK, D, dtype=dtype) for _ in range(2))
+    lens = torch.stack([torch.randperm(B, generator=gen).to(DEV) for _ in range(n)])
+    lens, tables = s["lens"].clone()[lens], s["table"][lens]
+    kc, vc = s["kc"].clone(), s["vc"].clone()
+    # The table of the sequence that a length came from; each sequence's last key is new.
+    held = [dict(s, kc=kc.clone(), vc=vc.clone(), table=s["table"].clone(), lens=s["lens"].clone())
+            for _ in range(n)]
+    busy = rnd(gen, 1, 1 << 14, 8, 128)
+
+    def step(i, wait):
+        h = held[i]
+        h["kc"].copy_(kc), h["vc"].copy_(vc)
+        h["table"].copy_(tables[i]), h["lens"].copy_(lens[i])
+        pos = (h["lens"] - 1)[:, None].contiguous()
+        gdr.qk_norm_rope_append(q[i], k[i], v[i], None, None, None, None, pos, h["kc"], h["vc"],
+                                h["table"])
+        h["q"] = gdr.gated_norm(q[i], z[i])[:, 0]
+        if wait:
+            torch.cuda.synchronize()
+        out = [call(h), gdr.paged_decode_attn(h["q"], h["kc"], h["vc"], h["table"], h["lens"])]
+        if wait:
+            torch.cuda.synchronize()
+        return [t for pair in out for t in pair]
+
+    want = [[t.clone() for t in step(i, True)] for i in range(n)]
+    for _ in range(3):
+        for h in held:                           # nothing of the last round is left to be found
+            h["kc"].zero_(), h["vc"].zero_(), h["lens"].zero_(), h["table"].fill_(-1)
+        torch.cuda.synchronize()
+        gdr.gated_norm(busy, busy)
+        got = [step(i, False) for i in range(n)]
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            for x, y in zip(a, b):
+                assert torch.equal(x, y)
+
+
+def test_capture_behind_copies_and_another_stream():
+    """Calls captured behind a copy, a fill and another stream's kernel, as a program's first
+    kernels are; the replays take what those leave."""
+    s = make(9, 8, 2, 128, 1000, [(131 * b) % 900 for b in range(9)], page=64, seed=26)
+    source, x = s["q"].clone(), torch.zeros(9, 1, 8, 128, dtype=BF, device=DEV)
+    side = torch.cuda.Stream()
+    state = torch.zeros(9, 1024, dtype=F32, device=DEV)
+
+    def run():
+        main = torch.cuda.current_stream()
+        x.zero_()
+        y = gdr.gated_norm(x, x, activation="sigmoid")               # behind a fill
+        s["q"].copy_(source)
+        a = call(s)                                                  # behind a copy
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            g = a[0].unsqueeze(1) * 2
+        state.add_(1)
+        main.wait_stream(side)
+        z = gdr.gated_norm(g, g)                                     # behind both streams
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            w = gdr.residual_norm(state.view(9, 1, 1024), z.flatten(2))
+        main.wait_stream(side)
+        b = gdr.paged_decode_attn(z[:, 0], s["kc"], s["vc"], s["table"], s["lens"])
+        return [y, *a, z, *w, *b]
+
+    run()
+    state.zero_()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = run()
+    gen = torch.Generator().manual_seed(27)
+    for _ in range(3):
+        source.copy_(rnd(gen, *source.shape))
+        before = state.clone()
+        graph.replay()
+        got = [t.clone() for t in held]
+        state.copy_(before)
+        for a, b in zip(got, run()):
+            assert torch.equal(a, b)
