@@ -134,12 +134,12 @@ class HybridDecoder:
 
 # ------------------------------------------------------------------ gate, norms, shared prompt
 class SharedCache:
-    """What decoding behind a shared prompt carries: the prompt's whole pages once, and for
-    every sequence its states and its own pages in the same arrays."""
+    """What decoding behind a shared prompt carries: the prompt's whole pages once (`shared` tokens),
+    and for every sequence its states and pages for `longest` tokens of its own in the same arrays."""
 
-    def __init__(self, prompt, batch, longest, device):
-        self.shared = prompt // PAGE * PAGE          # tokens of whole pages
-        first, own = self.shared // PAGE, -(-longest // PAGE)
+    def __init__(self, shared, batch, longest, device):
+        self.shared = shared
+        first, own = shared // PAGE, -(-longest // PAGE)
         order = torch.randperm(first + batch * own, device=device).int()
         self.prefix, self.table = order[:first].clone(), order[first:].view(batch, own)
         # New keys are stored by their position in the sequence: prompt's pages, then its own.
@@ -211,7 +211,12 @@ class NormedDecoder(HybridDecoder):
         """Greedy, for a batch behind one prompt: prompt [P], tails [B, n] the rest of each
         sequence; (tokens [B, steps], logits of every step [B, steps, VOCAB])."""
         B, n = tails.shape
-        cache = SharedCache(len(prompt), B, len(prompt) % PAGE + n + steps, self.device)
+        if len(prompt) + n == 0:
+            raise ValueError("prompt and tails are empty: there is nothing to continue")
+        # Whole pages. Without tails the prompt's last token is each sequence's own: the first new
+        # token needs its logits.
+        shared = (len(prompt) - (n == 0)) // PAGE * PAGE
+        cache = SharedCache(shared, B, len(prompt) - shared + n + steps, self.device)
         if cache.shared:
             once = cache.prompt()
             self.forward(prompt[None, :cache.shared], once)

@@ -110,3 +110,23 @@ def test_gradients_through_gate_norms_and_scan(example):
         run(*exact, plain_join, plain_scan, lambda o, z, w: norm(o) * w * nnf.silu(z)), exact)
     for g, e in zip(got, want):
         assert (g.double() - e).abs().max() <= 5e-4 * e.abs().max()
+
+
+@pytest.mark.parametrize("prompt", [1, 16, 32, 33, 47])
+def test_several_continuations_of_one_prompt(example, prompt):
+    """No tails: every sequence begins with the prompt's own next token, whole pages or not.
+    The bound as above."""
+    dev, batch, steps = torch.device("cuda:0"), 3, 4
+    model = example.NormedDecoder(dev)
+    gen = torch.Generator().manual_seed(prompt)
+    first = torch.randint(0, example.VOCAB, (prompt,), generator=gen).to(dev)
+    tails = torch.empty(batch, 0, dtype=torch.long, device=dev)
+    out, logits = model.generate_shared(first, tails, steps)
+    assert out.shape == (batch, steps) and logits.shape == (batch, steps, example.VOCAB)
+    whole = torch.cat([first.expand(batch, -1), out[:, :-1]], 1)
+    again = model.forward(whole, example.Cache(batch, whole.shape[1], dev))[:, prompt - 1:]
+    rms = again.float().pow(2).mean().sqrt()
+    assert torch.isfinite(logits).all()
+    assert (logits.float() - again.float()).pow(2).mean().sqrt() <= 3e-2 * rms
+    with pytest.raises(ValueError, match="nothing to continue"):
+        model.generate_shared(first[:0], tails, steps)
