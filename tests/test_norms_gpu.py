@@ -569,3 +569,30 @@ def test_long_rows_from_anywhere(D, dtype):
     gate = wide[..., 1:1 + D]
     residual_check(r, y, w, gate, wp, s, d, dr, "silu", True)
     residual_check(r, wide[..., 1:1 + D], w, d=d, dr=dr)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("D", [40, 64, 513, 1024, 4096])
+def test_infinite_gate_before_the_norm(D, dtype):
+    """An infinite gate without activation makes its row's root mean square infinite: that channel
+    is inf / inf, the row's others are 0, its gradients are NaN; every other row, and the weights'
+    gradients of the other channels, have the bits that they have without it."""
+    x, z, w, d = gated_inputs(2, 3, 2, D, dtype=dtype, seed=62)
+    x[1, 1, 0, 7] = 2.0
+    kw = dict(activation="none", gate_first=True)
+    without = d.clone()
+    without[1, 1, 0] = 0
+    y = gdr.gated_norm(x, z, w, **kw)
+    dx, dz, _ = gdr.gated_norm_bwd(d, x, z, w, **kw)
+    dw = gdr.gated_norm_bwd(without, x, z, w, **kw)[2]
+    z[1, 1, 0, 7] = float("inf")
+    y2 = gdr.gated_norm(x, z, w, **kw)
+    dx2, dz2, dw2 = gdr.gated_norm_bwd(d, x, z, w, **kw)
+    keep = torch.ones(2, 3, 2, dtype=torch.bool, device=DEV)
+    keep[1, 1, 0] = False
+    for a, b in ((y, y2), (dx, dx2), (dz, dz2)):
+        assert torch.equal(a[keep], b[keep])
+    others = torch.arange(D, device=DEV) != 7
+    assert torch.isnan(y2[1, 1, 0, 7]) and (y2[1, 1, 0][others] == 0).all()
+    assert torch.isnan(dx2[1, 1, 0]).all() and torch.isnan(dz2[1, 1, 0]).all()
+    assert torch.isnan(dw2[7]) and torch.equal(dw2[others], dw[others])

@@ -510,3 +510,26 @@ def test_capture_behind_copies_and_another_stream():
         state.copy_(before)
         for a, b in zip(got, run()):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("ot", [BF, F32])
+@pytest.mark.parametrize("dtype,D", [(BF, 128), (BF, 256), (F32, 64), (BF, 40)])
+def test_keys_shut_out_to_the_rounding(dtype, D, ot):
+    """Keys whose score is -inf in part of the prompt, in all of it and everywhere: rows with a key
+    left are the rounding of a value within the bound, as everywhere, and so is their lse."""
+    s = make(3, 2, 1, D, 300, [0, 10, 33], dtype=dtype, seed=28)
+    s["q"][..., 0] = 1.0
+    full = s["kc"].clone()
+    page, at = s["kc"].shape[1], torch.arange(300, device=DEV)
+    rows = s["prefix"].long()[at // page]
+    for part in (at < 200, at >= 70, at % 3 != 1, at >= 0):
+        s["kc"] = full.clone()
+        s["kc"][rows[part], (at % page)[part], :, 0] = -math.inf
+        o, lse = call(s, out_dtype=ot)
+        ref, rlse, size = reference(s)
+        live = torch.isfinite(rlse)
+        assert (o[~live] == 0).all() and (lse[~live] == -math.inf).all()
+        tol = 4e-5 + (2.0 ** -15 if dtype == BF and D != 40 else 0)
+        lo, hi = ((ref + k * tol * size).to(ot).double()[live] for k in (-1, 1))
+        assert ((o.double()[live] <= hi) & (o.double()[live] >= lo)).all()
+        assert ((lse.double() - rlse)[live].abs() <= 4e-5 + 4e-7 * rlse[live].abs()).all()
