@@ -596,3 +596,51 @@ def test_infinite_gate_before_the_norm(D, dtype):
     assert torch.isnan(y2[1, 1, 0, 7]) and (y2[1, 1, 0][others] == 0).all()
     assert torch.isnan(dx2[1, 1, 0]).all() and torch.isnan(dz2[1, 1, 0]).all()
     assert torch.isnan(dw2[7]) and torch.equal(dw2[others], dw[others])
+
+
+def _many(rows, D, seed):
+    """rows x D elements, more than 2^31, bf16; the last ones are compared."""
+    gen = torch.Generator(device=DEV).manual_seed(seed)
+    return torch.randn(rows, D, generator=gen, dtype=BF, device=DEV)
+
+
+@pytest.mark.parametrize("H,D,offset", [(8, 128, 0), (2, 1000, 0), (3, 1001, 0), (2, 700, 1)])
+def test_gated_offsets_beyond_32_bits(H, D, offset):
+    """Tensors of more than 2^31 elements: rows at the end have the bits that they have in a call
+    of their own, and the weights' gradient, from those rows alone, is the same sum."""
+    T, n = (1 << 31) // (H * D) + 40, 9
+    x, z = (_many(T, H * D + offset, seed)[:, offset:].view(1, T, H, D) for seed in (1, 2))
+    w = 1 + 0.2 * rnd(gen_of(3), D)
+    d = torch.zeros(1, T, H, D, dtype=BF, device=DEV)
+    d[:, -n:] = rnd(gen_of(4), 1, n, H, D, dtype=BF)
+    small = [t[:, -n:].clone() for t in (x, z, d)]
+    assert torch.equal(gdr.gated_norm(x, z, w)[:, -n:], gdr.gated_norm(*small[:2], w))
+    dx, dz, dw = gdr.gated_norm_bwd(d, x, z, w)
+    assert not dx[:, :-n].any() and not dz[:, :-n].any()
+    for g, e in zip((dx, dz), gdr.gated_norm_bwd(small[2], *small[:2], w)):
+        assert torch.equal(g[:, -n:], e)
+    (_, _, _, ref), sizes = gated_ref(*small[:2], w, small[2], "silu", False)
+    check(dw, ref, sizes[3])
+
+
+@pytest.mark.parametrize("D,offset", [(4096, 0), (4099, 0), (200, 0), (4096, 1)])
+def test_residual_offsets_beyond_32_bits(D, offset):
+    """The same for the residual's add and norm, in place where it is dense."""
+    T, n = (1 << 31) // D + 40, 9
+    r, y = (_many(T, D + offset, seed)[:, offset:].view(1, T, D) for seed in (5, 6))
+    w, s = (1 + 0.2 * rnd(gen_of(seed), D) for seed in (7, 8))
+    small = [t[:, -n:].clone() for t in (r, y)]
+    want, stored = gdr.residual_norm(*small, w, scale=s, out_dtype=BF)
+    out, res = gdr.residual_norm(r, y, w, scale=s, out_dtype=BF, residual_out=None if offset else r)
+    assert torch.equal(out[:, -n:], want) and torch.equal(res[:, -n:], stored)
+    out.zero_()
+    d = out
+    d[:, -n:] = rnd(gen_of(9), 1, n, D, dtype=BF)
+    dr, dy, _, dw, _, ds = gdr.residual_norm_bwd(d, None, res, y, w, scale=s)
+    assert not dr[:, :-n].any() and not dy[:, :-n].any()
+    dn = d[:, -n:].clone()
+    e = gdr.residual_norm_bwd(dn, None, stored, small[1], w, scale=s)
+    assert torch.equal(dr[:, -n:], e[0]) and torch.equal(dy[:, -n:], e[1])
+    ref = residual_ref(*small, w, None, None, s, dn, None, "sigmoid", False, stored)
+    check(dw, *ref["dw"])
+    check(ds, *ref["ds"])
