@@ -41,8 +41,9 @@ namespace {
 // 5 sequences behind 2999 keys, HK = 3, D = 64: a block has one tile, and the call is the chain
 // page - row - scores - sums - join (17.6 us; 4 more with a page looked up per row, one row after
 // the other). Queries come four channels at a time, up to eight of a thread's loads under way at
-// once: 139 sequences behind 2 keys, 4 heads of 256, 26 us, 42 channel by channel. Long prompts
-// are bound by the reads of q and k from shared memory.
+// once: 139 sequences behind 2 keys, 4 heads of 256, 32 us (channel by channel 42, and 26 so, when the
+// kernel did not wait for the one before). Long prompts are bound by the reads of q and k from shared
+// memory: 16 sequences behind 32768 keys, 32 / 8 heads of 128, 244 us where the bytes take 43.
 constexpr int RM = 64, KT = 64, NT = 256;
 template <int NJ>                                // channels in runs of 64: D <= 64 NJ
 struct AnySmem {
@@ -298,8 +299,7 @@ __global__ void __launch_bounds__(NT) prefix_any_kernel(PrefixArgs a, int vec, i
 // A row (a query head of a sequence) of few parts takes a warp; one of more the JW warps of a
 // block, every JW-th part each (SPLIT). A lane holds V channels in a row, N runs of them, and
 // has UN parts' loads under way, the first of them before the maximum is known (140 sequences of
-// 256 heads of 256 channels behind 9 keys: 146 -> 140 us a call). 64 sequences, 8192 shared keys, HK = 4
-// (16 parts a row), the whole call: 47 us, 55 with one warp for all parts of a row.
+// 256 heads of 256 channels behind 9 keys: 146 -> 140 us a call).
 constexpr int JW = 4;
 template <int V, bool SPLIT>
 __global__ void __launch_bounds__(JW * 32) prefix_join_kernel(PrefixArgs a) {
@@ -406,7 +406,11 @@ __global__ void __launch_bounds__(JW * 32) prefix_join_kernel(PrefixArgs a) {
 
 // ------------------------------------------------------------ host
 constexpr int kSms = 152;
-constexpr int kSplitParts = 5;   // parts of a row from which the warps of a block share them
+// Parts of a row from which the warps of a block share them. The whole call, shared and not: 8
+// sequences behind 4096 keys, 16 query heads (16 parts) 15.7 and 17.9 us, 64 (4 parts) 30.5 and 32.2;
+// 64 behind 8192, 32 heads (16 parts) 32.4 and 31.6, 128 heads (5 parts) 87 and 75, 192 (4 parts) 115
+// and 95. It pays where rows are few, which this border does not ask.
+constexpr int kSplitParts = 5;
 
 // How the shared keys of a call are cut up.
 struct Plan {

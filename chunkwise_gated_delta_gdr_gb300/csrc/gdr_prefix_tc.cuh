@@ -20,7 +20,8 @@
 // What bounds it: the chain S - softmax - P V of two units. A step is 1536 cycles of products by
 // count and takes 2200 (65000 keys, 256 rows per key head): Q K^T reads both operands from shared
 // memory at its limit while the copies write there, and each of the two waits of a step between
-// products costs some 200. The softmax is 1600 cycles of the other unit's time.
+// products costs some 200. The softmax is 1600 cycles of the other unit's time, some of it spills: the
+// 168 registers that 9 or 10 warps share equally do not quite hold a row's 128 scores.
 //
 // Maximum. o and l are kept against a reference that is moved (and o rescaled in TMEM) only when
 // a row's scores pass it by more than 2^8: weights stay below 2^8, far from any limit of fp32.
@@ -418,8 +419,8 @@ __global__ void __launch_bounds__(Config<D, TMA>::THREADS, 1)
       mbar_wait(&bars.kv_full[k % ST], (k / ST) & 1, kDrainPolls);
   } else if (!TMA && warp < F::SOFT + F::LOAD) {
     // ------------------------------------------------------------ copies, row by row
-    // Warp w takes every third row from w on (a fourth warp would leave the softmax 128 registers
-    // instead of 168, and its scores would not fit).
+    // Warp w takes every third row from w on. (A fourth warp would leave the softmax 128 registers
+    // instead of 168; with these, tiles of 128 keys spill 80 to 142 bytes, those of 64 keys nothing.)
     constexpr int RW = (KT + F::LOAD - 1) / F::LOAD, NO = (RW + 31) / 32;   // rows of a warp, a lane
     const int w = warp - F::SOFT;
     const bf16 *kc = static_cast<const bf16*>(a.kc), *vc = static_cast<const bf16*>(a.vc);

@@ -11,8 +11,11 @@
 // among others (a plain copy: 6.70 TB/s):
 //   training step, 2 x 8192 x 4096: 196 us, 6.2 TB/s (forward 77, backward 104)
 //   training step, 4096 x 1536, residual in 32 bits, y normed, gated and scaled per channel: 71 us
-//   (22, 41, 8: 2.7 and 5.4 rows a block, whose loads, sums and stores fall together)
-//   training step, 3 x 1021 x 777 in 32 bits: 49 us; 64 decode tokens x 2048 channels: 3.3 us
+//   (22, 41, 8: 2.7 and 5.4 rows a block with one stage of copies, no row ahead: two would take 210
+//   KB of an SM for its five blocks)
+//   training step, 3 x 1021 x 777 in 32 bits, likewise without a row ahead: 50 us
+//   training step, 2 x 8192 x 4096, residual in 32 bits 396 us, all in 32 bits 567: 4.7 and 4.3 TB/s
+//   64 decode tokens x 2048 channels: 3.3 us
 #include "gdr_norm.cuh"
 
 namespace gdr {
@@ -542,8 +545,10 @@ gdr_status gdr_residual_norm_bwd(const void* d_out, const void* d_residual_out,
       if (p.smem > kPlainSmem && !allow_smem<std::remove_pointer_t<decltype(tag)>>(fn, kSmemPerSm))
         return GDR_ERR_CUDA;
       // Blocks of a call that fills the device do not come early: their shared memory would be
-      // taken from the kernel before (training step of 4096 x 1536 with norm, gate and scale: 74.9 us
-      // so, 70.7 not).
+      // taken from the kernel before. Training steps, early and not: with norm, gate and scale 1000 x
+      // 1536 27.7 and 28.8 us, 4096 x 1536 71.8 and 70.1, 16384 x 1536 229 and 218, 8192 x 4096 326 and
+      // 312; without, 600 x 4096 in bf16 17.0 and 18.8, 16384 x 4096 195 and 197, in 32 bits 3063 x 777
+      // 36.7 and 33.0, 4096 x 2048 63.6 and 59.5.
       return p.blocks < kSms * 2 ? launch_behind_smem(fn, dim3(p.blocks), p.threads, p.smem, s, a)
                                  : launch_kernel(fn, dim3(p.blocks), p.threads, p.smem, s, a);
     };

@@ -5,7 +5,9 @@ too), and the norms around a layer.
 The same thin binding as the rest of the package: tensors' pointers, sizes and strides go
 into the C ABI (``include/gdr.h``), status codes come back as exceptions, all arithmetic
 runs in the CUDA kernels. Inputs may be views (any batch, token and head stride, the last
-dimension dense); outputs are dense.
+dimension dense); outputs are dense. What has to be dense (outputs, gradients of outputs, weights,
+scales, tables of angles, lse) starts on a 16-byte boundary, as tensors of their own do; a dense part
+of another tensor that does not is refused.
 """
 from __future__ import annotations
 
